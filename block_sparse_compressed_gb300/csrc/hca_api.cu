@@ -114,6 +114,8 @@ const char *hca_status_string(int s) {
     case HCA_ERR_UNSUPPORTED: return "HCA_ERR_UNSUPPORTED: no kernel for this dtype/D combination";
     case HCA_ERR_CUDA: return "HCA_ERR_CUDA: a CUDA call or launch failed";
     case HCA_ERR_TIMEOUT: return "HCA_ERR_TIMEOUT: an on-device wait gave up";
+    case HCA_ERR_CAPACITY: return "HCA_ERR_CAPACITY: the cache plan needs more blocks or slots than there are";
+    case HCA_ERR_CACHE: return "HCA_ERR_CACHE: a length, block id, slot or scale of the cache is out of range";
     default: return "HCA_ERR_UNKNOWN";
   }
 }
@@ -422,6 +424,120 @@ int hca_local_attn_bwd(const void *q, const void *kv, const int32_t *seg, const 
   void *dckv = static_cast<char *>(workspace) + need;  // [B, 1, D], discarded
   return hca_attn_bwd(q, kv, kv, seg, out, lse, dout, dq, dkv, dckv, B, H, S, D, W, m, scale, dtype, workspace,
                       need, stream);
+}
+
+// ---------------------------------------------------------------------------
+// serving
+// ---------------------------------------------------------------------------
+static bool block_size_ok(int bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
+
+// The status word of a call that has nothing to do.
+static int empty_call(void *workspace, void *stream) {
+  return cuda_status(cudaMemsetAsync(workspace, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream)));
+}
+
+size_t hca_cache_plan_workspace_size(void) { return kHeaderBytes; }
+
+int hca_cache_plan(const int32_t *held, const int32_t *added, int32_t *table, const int32_t *free_blocks,
+                   const int32_t *free_in, int32_t *free_out, int32_t *start, int32_t *slots, int R, int cols, int bs,
+                   int m, int nblocks, int nfree, int nslots, void *workspace, size_t workspace_bytes, void *stream) {
+  if (R < 0 || R > (1 << 24) || cols < 1 || cols > (1 << 26) || nblocks < 0 || nfree < 0 || nslots < 0 ||
+      nslots > (1 << 30))
+    return HCA_ERR_SHAPE;
+  if (!block_size_ok(bs) || m < 1) return HCA_ERR_ARG;
+  if ((long long)nblocks * bs > 0x7fffffffll) return HCA_ERR_SHAPE;
+  if (!free_in || !free_out || !start) return HCA_ERR_NULL;
+  if (R > 0 && (!held || !added || !table)) return HCA_ERR_NULL;
+  if ((nslots > 0 && !slots) || (nfree > 0 && !free_blocks)) return HCA_ERR_NULL;
+  int rc = check_ws(workspace, workspace_bytes, kHeaderBytes);
+  if (rc != HCA_OK) return rc;
+  if (take_launch_failure()) return HCA_ERR_CUDA;
+  CachePlanArgs a;
+  a.held = held; a.added = added; a.free_blocks = free_blocks; a.free_in = free_in;
+  a.table = table; a.free_out = free_out; a.start = start; a.slots = slots;
+  a.status = static_cast<int32_t *>(workspace);
+  a.R = R; a.cols = cols; a.bs = bs; a.m = m; a.nblocks = nblocks; a.nfree = nfree; a.nslots = nslots;
+  return cuda_status(cache_plan(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t hca_cache_append_workspace_size(int nblocks) {
+  if (nblocks < 0) return 0;
+  return kHeaderBytes + align_up((size_t)nblocks * sizeof(int32_t));
+}
+
+int hca_cache_append(const void *x, const int32_t *slots, void *pool, float *scale, int N, int D, int bs, int nblocks,
+                     int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+  if (dtype != HCA_BF16 && dtype != HCA_F32) return HCA_ERR_DTYPE;
+  if (N < 0 || N > (1 << 30) || D < 1 || D > kMaxD || nblocks < 0) return HCA_ERR_SHAPE;
+  if (!block_size_ok(bs)) return HCA_ERR_ARG;
+  if ((long long)nblocks * bs > 0x7fffffffll) return HCA_ERR_SHAPE;
+  if (D % 16 != 0) return HCA_ERR_ALIGN;
+  if (N > 0 && (!x || !slots)) return HCA_ERR_NULL;
+  if (nblocks > 0 && (!pool || !scale)) return HCA_ERR_NULL;
+  if (!aligned16(x) || !aligned16(pool)) return HCA_ERR_ALIGN;
+  int rc = check_ws(workspace, workspace_bytes, hca_cache_append_workspace_size(nblocks));
+  if (rc != HCA_OK) return rc;
+  if (take_launch_failure()) return HCA_ERR_CUDA;
+  if (N == 0) return empty_call(workspace, stream);
+  CacheAppendArgs a;
+  a.x = x; a.slots = slots; a.pool = static_cast<uint8_t *>(pool); a.scale = scale;
+  a.status = static_cast<int32_t *>(workspace);
+  a.owner = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + kHeaderBytes);
+  a.N = N; a.D = D; a.bs = bs; a.nblocks = nblocks; a.dtype = dtype;
+  return cuda_status(cache_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+static int cache_attn_shape(int N, int R, int H, int D, int dtype) {
+  if (dtype != HCA_BF16 && dtype != HCA_F32) return HCA_ERR_DTYPE;
+  if (N < 0 || R < 0 || H < 1 || D < 1 || D > kMaxD || N > (1 << 30) || R > (1 << 24) || H > (1 << 14) ||
+      (double)N * H > (double)(1 << 30))
+    return HCA_ERR_SHAPE;
+  if (D % 16 != 0) return HCA_ERR_ALIGN;
+  if (dtype == HCA_BF16 && D != 64 && D != 128) return HCA_ERR_UNSUPPORTED;
+  return HCA_OK;
+}
+
+size_t hca_cache_attn_workspace_size(int N, int R, int H, int D, int dtype) {
+  if (cache_attn_shape(N, R, H, D, dtype) != HCA_OK) return 0;
+  return cache_attn_ws_bytes(N, R, H, D, dtype);
+}
+
+int hca_cache_attn(const void *q, const int32_t *start, const int32_t *held, const void *raw_pool,
+                   const float *raw_scale, const int32_t *raw_table, int raw_blocks, int raw_cols,
+                   const void *comp_pool, const float *comp_scale, const int32_t *comp_table, int comp_blocks,
+                   int comp_cols, void *out, float *lse, int N, int R, int H, int D, int W, int m, int bs, float scale,
+                   int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+  int rc = cache_attn_shape(N, R, H, D, dtype);
+  if (rc != HCA_OK) return rc;
+  if (!std::isfinite(scale) || W < 1 || m < 1 || !block_size_ok(bs)) return HCA_ERR_ARG;
+  if (raw_blocks < 0 || raw_cols < 1 || (long long)raw_blocks * bs > 0x7fffffffll) return HCA_ERR_SHAPE;
+  if (comp_table && (comp_blocks < 0 || comp_cols < 1 || (long long)comp_blocks * bs > 0x7fffffffll)) return HCA_ERR_SHAPE;
+  const bool empty = N == 0 || R == 0;
+  if (!empty) {
+    if (!q || !start || !held || !out || !lse || !raw_table) return HCA_ERR_NULL;
+    if (raw_blocks > 0 && (!raw_pool || !raw_scale)) return HCA_ERR_NULL;
+    if (comp_table && comp_blocks > 0 && (!comp_pool || !comp_scale)) return HCA_ERR_NULL;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(raw_pool) || !aligned16(comp_pool))
+      return HCA_ERR_ALIGN;
+  }
+  rc = check_ws(workspace, workspace_bytes, cache_attn_ws_bytes(N, R, H, D, dtype));
+  if (rc != HCA_OK) return rc;
+  if (take_launch_failure()) return HCA_ERR_CUDA;
+  if (empty) return empty_call(workspace, stream);
+  CacheAttnArgs a;
+  a.q = q; a.start = start; a.held = held;
+  a.raw = CacheSet{static_cast<const uint8_t *>(raw_pool), raw_scale, raw_table, raw_blocks, raw_cols};
+  a.comp = comp_table
+               ? CacheSet{static_cast<const uint8_t *>(comp_pool), comp_scale, comp_table, comp_blocks, comp_cols}
+               : CacheSet{nullptr, nullptr, nullptr, 0, 0};
+  a.out = out; a.lse = lse;
+  a.N = N; a.R = R; a.H = H; a.D = D;
+  a.W = W < (1 << 30) ? W : 1 << 30;  // no position lies further back
+  a.m = m; a.bs = bs; a.scale = scale; a.dtype = dtype;
+  a.ws = workspace;
+  a.wait_ns = wait_limit_ns();
+  a.stall = dtype == HCA_BF16 ? take_stall_mask() & HCA_STALL_FWD : 0;
+  return cuda_status(cache_attn(a, static_cast<cudaStream_t>(stream)));
 }
 
 int hca_visible_pairs(const int32_t *seg, int B, int S, int W, int m, int64_t *raw_pairs, int64_t *comp_pairs,

@@ -11,7 +11,8 @@ namespace hca {
 // kernels the optional profiler distinguishes (hca_profile_read ids)
 enum KernelId {
   kKPrep = 0, kKFwdTc, kKBwdDq, kKBwdDkv, kKBwdReduce, kKSimtFwd, kKSimtBwd, kKVisibility, kKCompress,
-  kKIndexScore, kKIndexTopk, kKCsaUnion, kKCsaDckv, kNumKernels
+  kKIndexScore, kKIndexTopk, kKCsaUnion, kKCsaDckv, kKCachePlan, kKCacheAppend, kKCacheSched, kKCacheAttn,
+  kKCacheSimt, kKCacheCombine, kNumKernels
 };
 
 // Brackets the launches issued during its lifetime with CUDA events on `st`
@@ -120,6 +121,49 @@ cudaError_t csa_build_union(const int32_t *sel, const int32_t *sstart, int B, in
 size_t csa_dckv_acc_bytes(int B, int Sc);
 struct BwdArgs;
 cudaError_t csa_dckv(const BwdArgs &a, const CsaUnion &u, const float *rowstat, float *acc, cudaStream_t st);
+
+// Serving (hca_cache.cu): block tables and slot maps, writes into the 8-bit cache
+struct CachePlanArgs {
+  const int32_t *held, *added, *free_blocks, *free_in;
+  int32_t *table, *free_out, *start, *slots;
+  int32_t *status;
+  int R, cols, bs, m, nblocks, nfree, nslots;
+};
+cudaError_t cache_plan(const CachePlanArgs &a, cudaStream_t st);
+struct CacheAppendArgs {
+  const void *x;
+  const int32_t *slots;
+  uint8_t *pool;
+  float *scale;
+  int32_t *owner;  // workspace [nblocks]
+  int32_t *status;
+  int N, D, bs, nblocks, dtype;
+};
+cudaError_t cache_append(const CacheAppendArgs &a, cudaStream_t st);
+
+// Attention over the cache (hca_cache_attn.cu: schedule, fp32 kernel, combine;
+// hca_cache_attn_tc.cu: the tensor-core kernel)
+struct CacheSet {
+  const uint8_t *pool;   // [nblocks][bs][D] e4m3
+  const float *scale;    // [nblocks]
+  const int32_t *table;  // [R][cols]
+  int nblocks, cols;
+};
+struct CacheAttnArgs {
+  const void *q;
+  const int32_t *start, *held;
+  CacheSet raw, comp;  // comp.table NULL: no compressed set
+  void *out;
+  float *lse;
+  int N, R, H, D, W, m, bs;
+  float scale;
+  int dtype;
+  void *ws;
+  uint64_t wait_ns;
+  int stall;
+};
+size_t cache_attn_ws_bytes(int N, int R, int H, int D, int dtype);
+cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st);
 
 // tensor-core (tcgen05) path
 bool tc_fwd_supported(int H, int D, int dtype);

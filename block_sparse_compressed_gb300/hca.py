@@ -31,7 +31,9 @@ EXPORTS = ("hca_status_string", "hca_version", "hca_workspace_size", "hca_query_
            "hca_profile_read", "hca_num_kernels", "hca_kernel_name", "hca_attn_fwd_noalloc",
            "hca_local_workspace_size", "hca_local_attn_fwd", "hca_local_attn_bwd", "hca_test_inject",
            "hca_compress_fwd", "hca_compress_workspace_size", "hca_compress_bwd", "hca_indexer_workspace_size",
-           "hca_indexer_topk", "hca_csa_workspace_size", "hca_csa_attn_fwd", "hca_csa_attn_bwd")
+           "hca_indexer_topk", "hca_csa_workspace_size", "hca_csa_attn_fwd", "hca_csa_attn_bwd",
+           "hca_cache_plan_workspace_size", "hca_cache_plan", "hca_cache_append_workspace_size", "hca_cache_append",
+           "hca_cache_attn_workspace_size", "hca_cache_attn")
 
 # failure-path test hooks (hca_test_inject)
 INJECT_RESET, INJECT_LAUNCH_FAILURE, INJECT_STALL, INJECT_WAIT_LIMIT_NS, INJECT_CSA_UNION = 0, 1, 2, 3, 4
@@ -105,6 +107,18 @@ def load(path: str = LIB_PATH):
             lib.hca_csa_attn_fwd.restype = I
             lib.hca_csa_attn_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, P, Z, P]
             lib.hca_csa_attn_bwd.restype = I
+            lib.hca_cache_plan_workspace_size.argtypes = []
+            lib.hca_cache_plan_workspace_size.restype = Z
+            lib.hca_cache_plan.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, Z, P]
+            lib.hca_cache_plan.restype = I
+            lib.hca_cache_append_workspace_size.argtypes = [I]
+            lib.hca_cache_append_workspace_size.restype = Z
+            lib.hca_cache_append.argtypes = [P, P, P, P, I, I, I, I, I, P, Z, P]
+            lib.hca_cache_append.restype = I
+            lib.hca_cache_attn_workspace_size.argtypes = [I, I, I, I, I]
+            lib.hca_cache_attn_workspace_size.restype = Z
+            lib.hca_cache_attn.argtypes = [P, P, P, P, P, P, I, I, P, P, P, I, I, P, P, I, I, I, I, I, I, I, F, I, P, Z, P]
+            lib.hca_cache_attn.restype = I
             _lib = lib
     return _lib
 
@@ -498,3 +512,123 @@ def hca_csa_attn_bwd(q, kv, ckv, seg, sel, out, lse, dout, W: int, m: int, scale
     if check:
         _check(hca_workspace_status(ws), "hca_csa_attn_bwd (device)")
     return dq, dkv, dckv
+
+
+# ---------------------------------------------------------------------------
+# serving: plan, append and attend over a paged 8-bit cache
+# ---------------------------------------------------------------------------
+def hca_cache_plan(held: torch.Tensor, added: torch.Tensor, table: torch.Tensor, free_blocks: torch.Tensor,
+                   free_count: torch.Tensor, nblocks: int, bs: int, nslots: int, m: int = 1,
+                   start: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                   free_left: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, check: bool = False):
+    """Block tables and slot maps of a serving step (include/hca.h,
+    hca_cache_plan): held[R], added[R], table[R,cols] (updated in place),
+    free_blocks[nfree], free_count[1], all int32.  Returns (start[R+1],
+    slots[nslots], free_left[1]); free_left may be free_count itself."""
+    lib = load()
+    dev = held.device
+    if held.dim() != 1 or table.dim() != 2 or free_blocks.dim() != 1:
+        raise ValueError("held must be [R], table [R,cols] and free_blocks [nfree]")
+    R, cols = held.shape[0], table.shape[1]
+    _need(held, "held", (R,), torch.int32, dev)
+    _need(added, "added", (R,), torch.int32, dev)
+    _need(table, "table", (R, cols), torch.int32, dev)
+    _need(free_blocks, "free_blocks", free_blocks.shape, torch.int32, dev)
+    _need(free_count, "free_count", (1,), torch.int32, dev)
+    start = torch.empty(R + 1, dtype=torch.int32, device=dev) if start is None else start
+    slots = torch.empty(nslots, dtype=torch.int32, device=dev) if slots is None else slots
+    free_left = torch.empty(1, dtype=torch.int32, device=dev) if free_left is None else free_left
+    _need(start, "start", (R + 1,), torch.int32, dev)
+    _need(slots, "slots", (nslots,), torch.int32, dev)
+    _need(free_left, "free_left", (1,), torch.int32, dev)
+    if ws is None:
+        ws = torch.empty(lib.hca_cache_plan_workspace_size(), dtype=torch.uint8, device=dev)
+    with _on(dev):
+        rc = lib.hca_cache_plan(_ptr(held), _ptr(added), _ptr(table), _ptr(free_blocks), _ptr(free_count),
+                                _ptr(free_left), _ptr(start), _ptr(slots), R, cols, bs, m, nblocks,
+                                free_blocks.shape[0], nslots, _ptr(ws), ws.numel(), _stream(dev))
+    _check(rc, "hca_cache_plan")
+    if check:
+        _check(hca_workspace_status(ws), "hca_cache_plan (device)")
+    return start, slots, free_left
+
+
+def _cache_pool(pool: torch.Tensor, scale: torch.Tensor, name: str, device):
+    if pool.dim() != 3:
+        raise ValueError(f"{name} pool must be [nblocks,bs,D]")
+    _need(pool, f"{name} pool", pool.shape, torch.float8_e4m3fn, device)
+    _need(scale, f"{name} scale", (pool.shape[0],), torch.float32, device)
+    return pool.shape
+
+
+def hca_cache_append(x: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor, scale: torch.Tensor,
+                     ws: Optional[torch.Tensor] = None, check: bool = False) -> None:
+    """Rows x[N,D] (bf16 or fp32) into slots[N] (int32, -1: nowhere) of the
+    cache pool[nblocks,bs,D] (float8_e4m3fn) with scale[nblocks] (fp32), both
+    updated in place (include/hca.h, hca_cache_append)."""
+    lib = load()
+    dev = x.device
+    nblocks, bs, D = _cache_pool(pool, scale, "cache", dev)
+    _need(x, "x", (x.shape[0], D), x.dtype, dev)
+    dt = _dtype_code(x)
+    N = x.shape[0]
+    _need(slots, "slots", (N,), torch.int32, dev)
+    if ws is None:
+        ws = torch.empty(lib.hca_cache_append_workspace_size(nblocks), dtype=torch.uint8, device=dev)
+    with _on(dev):
+        rc = lib.hca_cache_append(_ptr(x), _ptr(slots), _ptr(pool), _ptr(scale), N, D, bs, nblocks, dt, _ptr(ws),
+                                  ws.numel(), _stream(dev))
+    _check(rc, "hca_cache_append")
+    if check:
+        _check(hca_workspace_status(ws), "hca_cache_append (device)")
+
+
+def hca_cache_attn(q: torch.Tensor, start: torch.Tensor, held: torch.Tensor, raw, comp, W: int, m: int, scale: float,
+                   out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                   ws: Optional[torch.Tensor] = None, check: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+    """HCA attention of packed query tokens q[N,H,D] over the cache
+    (include/hca.h, hca_cache_attn): request r's tokens are rows
+    start[r]..start[r+1]-1 at positions held[r]...  raw and comp are
+    (pool, scale, table[R,cols]); comp may be None.  Returns (out[N,H,D],
+    lse[N,H] fp32)."""
+    lib = load()
+    dev = q.device
+    if q.dim() != 3 or held.dim() != 1:
+        raise ValueError("q must be [N,H,D] and held [R]")
+    N, H, D = q.shape
+    R = held.shape[0]
+    dt = _dtype_code(q)
+    _need(q, "q", (N, H, D), q.dtype, dev)
+    _need(held, "held", (R,), torch.int32, dev)
+    _need(start, "start", (R + 1,), torch.int32, dev)
+    args = []
+    bs = raw[0].shape[1] if raw[0].dim() == 3 else 0
+    for name, cache in (("raw", raw), ("comp", comp)):
+        if cache is None:
+            args += [None, None, None, 0, 0]
+            continue
+        pool, sc, table = cache
+        nblocks, b, d = _cache_pool(pool, sc, name, dev)
+        if (b, d) != (bs, D):
+            raise ValueError(f"{name} pool has blocks of {b} rows of {d}, expected {bs} rows of {D}")
+        if table.dim() != 2:
+            raise ValueError(f"{name} table must be [R,cols]")
+        _need(table, f"{name} table", (R, table.shape[1]), torch.int32, dev)
+        args += [_ptr(pool), _ptr(sc), _ptr(table), nblocks, table.shape[1]]
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty(N, H, dtype=torch.float32, device=dev) if lse is None else lse
+    _need(out, "out", (N, H, D), q.dtype, dev)
+    _need(lse, "lse", (N, H), torch.float32, dev)
+    if ws is None:
+        n = lib.hca_cache_attn_workspace_size(N, R, H, D, dt)
+        if n == 0:
+            raise HCAError(8, "hca_cache_attn_workspace_size")
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    with _on(dev):
+        rc = lib.hca_cache_attn(_ptr(q), _ptr(start), _ptr(held), *args, _ptr(out), _ptr(lse), N, R, H, D, min(W, 1 << 30),
+                                m, bs,
+                                float(scale), dt, _ptr(ws), ws.numel(), _stream(dev))
+    _check(rc, "hca_cache_attn")
+    if check:
+        _check(hca_workspace_status(ws), "hca_cache_attn (device)")
+    return out, lse

@@ -74,7 +74,11 @@ typedef enum {
   HCA_ERR_UNSUPPORTED = 8, /* no kernel for this dtype / D combination (bf16
                               runs on tensor cores only, for D = 64 or 128)  */
   HCA_ERR_CUDA = 9,        /* a CUDA runtime call or launch failed             */
-  HCA_ERR_TIMEOUT = 10     /* a bounded on-device wait gave up                 */
+  HCA_ERR_TIMEOUT = 10,    /* a bounded on-device wait gave up                 */
+  HCA_ERR_CAPACITY = 11,   /* a cache plan needs more blocks or slots than
+                              there are (device-side check)                  */
+  HCA_ERR_CACHE = 12       /* a length, block id, slot or scale of the cache is
+                              out of range (device-side check)               */
 } hca_status;
 
 typedef enum { HCA_BF16 = 0, HCA_F32 = 1 } hca_dtype;
@@ -260,6 +264,93 @@ HCA_API size_t hca_indexer_workspace_size(int B, int S, int m);
 HCA_API int hca_indexer_topk(const void *qi, const void *ki, const float *w, const int32_t *seg,
                              int32_t *sel, float *scores, int B, int S, int Hi, int Di, int m, int k,
                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- Serving: HCA over a paged 8-bit cache -------------------------------
+ *
+ * The pages define the training path only; these calls are this library's own
+ * form of the same attention for serving, one token or several at a time.
+ * A serving step of a batch of requests is
+ *   hca_cache_plan     blocks and slots for the raw rows that the step adds
+ *                      (m = 1), and for its completed compressed entries (m);
+ *   hca_cache_append   the kv rows and the compressed entries into them;
+ *   hca_cache_attn     the step's query tokens over the cache.
+ *
+ * The cache.  A pool holds nblocks blocks of bs rows of D e4m3 values
+ * ([nblocks,bs,D], one shared kv head) and one fp32 scale per block
+ * ([nblocks]); a row's value is scale * e4m3.  Raw rows and compressed entries
+ * may share a pool or have one each.  bs is 16, 32, 64 or 128 and nblocks * bs
+ * < 2^31.  Entry e of request r is row e mod bs of block table[r][(e / bs) mod
+ * cols]; a table that is narrower than a request needs is a ring that keeps
+ * its last blocks, which is how raw rows behind the window are given up:
+ * ceil((W - 1 + t) / bs) + 1 columns do for steps of up to t tokens.
+ * A request's entries are floor(L / m) for L tokens: its raw rows for m = 1,
+ * its completed compression windows otherwise.  Positions stay below 2^30.
+ *
+ * All lengths, tables and slots are device int32 arrays, so that a step can be
+ * captured into a CUDA graph once and replayed with the lengths it finds.  The
+ * values in them are checked on the device: an out-of-range one is never used
+ * as an index, and hca_workspace_status says HCA_ERR_CACHE (each call states
+ * what happens to its outputs). */
+
+/* Block tables and slot maps.  Request r holds held[r] tokens and gets
+ * added[r] >= 0 more; it adds entries [held / m, (held + added) / m).
+ *   table [R,cols]   in/out: blocks of the columns that were empty are filled
+ *                    in, requests in order, from the end of the free list
+ *   free_blocks [nfree], free_in [1]  free block ids, of which the first
+ *                    free_in[0] are valid
+ *   free_out [1]     how many are left (may be free_in itself)
+ *   start [R+1]      first new entry of each request, start[R] their number
+ *   slots [nslots]   slot block * bs + row of every new entry; -1 for an entry
+ *                    that a later one of the same step overwrites in a ring
+ *                    and for all places behind the last entry
+ * A plan that needs more blocks or slots than there are (HCA_ERR_CAPACITY), or
+ * a length out of range (HCA_ERR_CACHE), changes nothing: start is all 0, slots
+ * all -1, free_out is free_in, and the table stays.  A block id outside
+ * [0, nblocks) gives slots of -1 (HCA_ERR_CACHE). */
+HCA_API size_t hca_cache_plan_workspace_size(void);
+HCA_API int hca_cache_plan(const int32_t *held, const int32_t *added, int32_t *table, const int32_t *free_blocks,
+                           const int32_t *free_in, int32_t *free_out, int32_t *start, int32_t *slots, int R, int cols,
+                           int bs, int m, int nblocks, int nfree, int nslots, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/* Rows into the cache: row t of x ([N,D], bf16 or fp32, D a multiple of 16 up
+ * to 256) goes to slots[t] (-1: nowhere).  Rows of one block are adjacent in x
+ * in ascending slots.  A block whose row 0 is written starts afresh, with the
+ * smallest power of two s >= 2^-96 for which no finite new value exceeds 448 s
+ * as its scale; otherwise its scale becomes the larger of its own and that one,
+ * and its rows in front of the new ones are brought to it (rounded to nearest
+ * even; only values that become subnormal in e4m3 can change).  New values are
+ * x / s rounded to nearest even; infinities and NaN are stored as NaN.  Rows
+ * behind the new ones keep their bytes.  A slot >= nblocks * bs is skipped, a
+ * scale that is not positive and finite is replaced, and of several runs of
+ * rows for one block only one is written; all three are HCA_ERR_CACHE.
+ * Workspace: hca_cache_append_workspace_size(nblocks). */
+HCA_API size_t hca_cache_append_workspace_size(int nblocks);
+HCA_API int hca_cache_append(const void *x, const int32_t *slots, void *pool, float *scale, int N, int D, int bs,
+                             int nblocks, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* HCA attention over the cache.  q, out [N,H,D] (dtype), lse [N,H] fp32: the
+ * query tokens of all requests packed, request r's being rows start[r] ..
+ * start[r+1] - 1 (start[0] = 0, start[R] <= N) at positions held[r], held[r] +
+ * 1, ...; the cache holds the rows of all of them already.  A token at position
+ * i attends to its request's raw rows t with i - W < t <= i and to its
+ * compressed entries j with (j + 1) m <= i + 1 under one softmax; entries and
+ * raw rows are key and value at once.  comp_table NULL: no compressed set (local
+ * sliding attention; full causal attention with W beyond the length).  Rows of
+ * out and lse from start[R] on are left as they are.  Cache rows that no token
+ * sees may hold anything.
+ * bf16: D = 64 or 128 (HCA_ERR_UNSUPPORTED otherwise); fp32: D a multiple of 16
+ * up to 256.  Lengths out of range, a raw table too narrow for a token's window
+ * or a compressed table too narrow for the entries make all N rows of out and
+ * lse NaN; a block id out of range makes the tokens that see the block NaN; both
+ * are HCA_ERR_CACHE.  A given input gives the same bits every time.  Workspace:
+ * hca_cache_attn_workspace_size bytes (0: unsupported sizes). */
+HCA_API size_t hca_cache_attn_workspace_size(int N, int R, int H, int D, int dtype);
+HCA_API int hca_cache_attn(const void *q, const int32_t *start, const int32_t *held, const void *raw_pool,
+                           const float *raw_scale, const int32_t *raw_table, int raw_blocks, int raw_cols,
+                           const void *comp_pool, const float *comp_scale, const int32_t *comp_table, int comp_blocks,
+                           int comp_cols, void *out, float *lse, int N, int R, int H, int D, int W, int m, int bs,
+                           float scale, int dtype, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Failure-path test hooks.  "Add HCA Static Compilation for Splash Attention
  * [Deepseek v4]" (Description, validation-guard bullet) wants unsupported or
