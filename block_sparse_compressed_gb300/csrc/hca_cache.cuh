@@ -39,6 +39,12 @@ __device__ __forceinline__ float2 f32x2_from_e4m3x2(uint32_t b2) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
+// not 0 where one of 16 e4m3 bytes is NaN (0x7f or 0xff)
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t nan_bytes(const uint4 &v) {
+  return nan_bytes(v.x) | nan_bytes(v.y) | nan_bytes(v.z) | nan_bytes(v.w);
+}
+
 // Exponent k of the smallest power of two with amax <= 448 * 2^k (448 = 1.75
 // * 2^8, the largest e4m3 value); amax is finite and not negative.
 __device__ __forceinline__ int scale_exponent(float amax) {

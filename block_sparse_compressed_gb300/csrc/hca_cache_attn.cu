@@ -14,6 +14,8 @@
 // from each part's (O, reference exponent, sum).
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "hca_cache_attn.cuh"
 #include "tc_tiles.cuh"
 
@@ -99,19 +101,19 @@ __global__ void __launch_bounds__(kSchedThreads) hca_cache_sched_kernel(const At
 // ---------------------------------------------------------------------------
 // helpers of the fp32 kernel
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Every output of a call whose schedule was refused is NaN.
+// Every output of a call that failed on the device is NaN.
 template <typename T>
 __device__ __forceinline__ void poison(const AttnParams &p) {
   const size_t n = (size_t)p.N * p.H;
   const float nan = __int_as_float(0x7fc00000);
-  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n * p.D; i += (size_t)gridDim.x * blockDim.x)
+  const size_t at = ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x;
+  const size_t step = (size_t)gridDim.y * gridDim.x * blockDim.x;
+  for (size_t i = at; i < n * p.D; i += step)
     put(static_cast<T *>(p.out) + i, nan);
-  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x)
+  for (size_t i = at; i < n; i += step)
     p.lse[i] = nan;
 }
 
@@ -156,14 +158,13 @@ __device__ __forceinline__ PageRef page_ref(const AttnParams &p, const Pages &pg
   return x;
 }
 
-template <typename T>
 __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const AttnParams p) {
   extern __shared__ uint8_t keys[];  // [128][D + 4] bytes: a row's words fall into different banks
   __shared__ SimtShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long ntiles = p.hdr->ntiles;
   if (ntiles < 0) {
-    poison<T>(p);
+    poison<float>(p);
     return;
   }
   const long long quota = cta_quota(ntiles, p.grid, kMinTiles);
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
     for (int i = tid; i < p.D * kSimtCols; i += kSimtThreads) {
       const int c = i / p.D, d = i % p.D;
       float v = 0.f;
-      if (c < nreal) v = to_f32(static_cast<const T *>(p.q)[((size_t)(g.row0 + c / p.HS) * p.H + h0 + c % p.HS) * p.D + d]);
+      if (c < nreal) v = static_cast<const float *>(p.q)[((size_t)(g.row0 + c / p.HS) * p.H + h0 + c % p.HS) * p.D + d];
       sh.q[d][c] = v;
     }
     if (tid < kSimtCols) {
@@ -262,8 +263,15 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         if (lane == 0) sh.red[warp][c] = sum;
       }
-      if (cb <= ca) {
-        // its values meet a probability of 0: no NaN may
+      bool clear = cb <= ca;
+      if (!clear && cb - ca < g.npos * p.HS) {
+        uint32_t nan = 0;
+        for (int u = 0; u < upr; ++u) nan |= nan_bytes(*reinterpret_cast<const uint32_t *>(keys + tid * pitch + 4 * u));
+        clear = nan != 0;
+      }
+      if (clear) {
+        // its values meet a probability of 0, where 0 * NaN is not 0; a column
+        // that sees a NaN has one for a probability
         for (int u = 0; u < upr; ++u) *reinterpret_cast<uint32_t *>(keys + tid * pitch + 4 * u) = 0;
       }
       __syncthreads();
@@ -307,7 +315,7 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
       for (int c = 0; c < kSimtCols; ++c) {
         if (c >= nreal) continue;
         if (seg.whole)
-          put(static_cast<T *>(p.out) + ((size_t)(g.row0 + c / p.HS) * p.H + h0 + c % p.HS) * p.D + d, o[x2][c] / sh.l[c]);
+          static_cast<float *>(p.out)[((size_t)(g.row0 + c / p.HS) * p.H + h0 + c % p.HS) * p.D + d] = o[x2][c] / sh.l[c];
         else
           p.part_o[((size_t)seg.slot * kSimtCols + c) * p.D + d] = o[x2][c];
       }
@@ -334,6 +342,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps) hca_cache_combine_kernel(c
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long ntiles = p.hdr->ntiles;
   if (ntiles <= 0) return;
+  if (p.hdr->status == HCA_ERR_TIMEOUT) {
+    poison<T>(p);
+    return;
+  }
   const long long quota = cta_quota(ntiles, p.grid, kMinTiles);
   const long long border = quota * (blockIdx.x + 1);
   if (border >= ntiles) return;
@@ -394,7 +406,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) hca_cache_combine_kernel(c
 // Columns of a group for H heads: enough for one position's slice of heads, and
 // for as many positions as the average request brings.  More columns share a
 // key tile between more rows; unused ones cost tensor and exponential work.
-bool on_tensor_cores(int dtype) { return false; }
+bool on_tensor_cores(int dtype) { return dtype == HCA_BF16; }
 
 int pick_columns(int N, int R, int H, int dtype) {
   if (!on_tensor_cores(dtype)) return kSimtCols;
@@ -460,18 +472,21 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
   p.scale = a.scale; p.wait_ns = a.wait_ns; p.stall = a.stall;
   const int sms = tc::sm_count();
   if (sms <= 0) return cudaErrorNoDevice;
-  p.grid = min(4 * sms, max_ctas(l.NQ, on_tensor_cores(a.dtype)));
+  const bool tcs = on_tensor_cores(a.dtype);
+  p.grid = std::min((tcs ? tc_cache_ctas(l.NQ) : 4) * sms, max_ctas(l.NQ, tcs));
   {
     ProfScope prof(kKCacheSched, st);
     hca_cache_sched_kernel<<<1, kSchedThreads, 0, st>>>(p);
   }
-  {
-    void (*kern)(const AttnParams) = a.dtype == HCA_F32 ? hca_cache_simt_kernel<float> : hca_cache_simt_kernel<__nv_bfloat16>;
-    static tc::SmemAttrOnce attr[2];
-    cudaError_t e = attr[a.dtype == HCA_F32].ensure(reinterpret_cast<const void *>(kern), kTileKeys * (256 + 4));
+  if (tcs) {
+    const cudaError_t e = tc_cache_attn(p, st);
+    if (e != cudaSuccess) return e;
+  } else {
+    static tc::SmemAttrOnce attr;
+    const cudaError_t e = attr.ensure(reinterpret_cast<const void *>(hca_cache_simt_kernel), kTileKeys * (256 + 4));
     if (e != cudaSuccess) return e;
     ProfScope prof(kKCacheSimt, st);
-    kern<<<p.grid, kSimtThreads, kTileKeys * (a.D + 4), st>>>(p);
+    hca_cache_simt_kernel<<<p.grid, kSimtThreads, kTileKeys * (a.D + 4), st>>>(p);
   }
   {
     ProfScope prof(kKCacheCombine, st);

@@ -54,5 +54,9 @@ __device__ __forceinline__ Segment segment_of(const Group &g, long long c0, long
   return s;
 }
 
+// tensor-core kernel (hca_cache_attn_tc.cu)
+int tc_cache_ctas(int NQ);  // CTAs per SM
+cudaError_t tc_cache_attn(const AttnParams &p, cudaStream_t st);
+
 }  // namespace cache
 }  // namespace hca

@@ -368,6 +368,23 @@ def test_nan_in_one_query_row_stays_there(dtype):
     assert err.max() < 0.05
 
 
+@pytest.mark.parametrize("dtype,H,D", [(BF16, 16, 64), (BF16, 64, 128), (F32, 4, 64)])
+def test_nan_in_a_row_reaches_only_the_tokens_that_see_it(dtype, H, D):
+    # four tokens in one step; the third one's own row and the entry that it
+    # completes hold NaN, the row at the window's far end of the first too
+    held, added, W, m, bs = [77], [4], 30, 8, 16
+    q, start, h, raw, c = attn_case(held, added, H, D, W, m, bs, dtype, 2, ring=False)
+    clean = tuple(t.clone() for t in raw), tuple(t.clone() for t in c)
+    for cache, e in ((raw, 79), (raw, 48), (c, 9)):
+        cache[0].view(torch.uint8)[int(cache[2][0, e // bs]), e % bs, 5] = 0xFF
+    out, lse = hca.hca_cache_attn(q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), W, m, scale_of(D), check=True)
+    want, wl = hca.hca_cache_attn(q.to(DEV), start.to(DEV), h.to(DEV), dev(clean[0]), dev(clean[1]), W, m, scale_of(D))
+    # row 48 is in the window of token 77 only, row 79 and entry 9 are seen from token 79 on
+    for t in (0, 2, 3):
+        assert bool(torch.isnan(out[t]).all()) and bool(torch.isnan(lse[t]).all())
+    assert torch.equal(out[1], want[1]) and torch.equal(lse[1], wl[1])
+
+
 def _status_case(dtype=BF16):
     held, added, H, D, W, m, bs = [500, 300, 40], [1, 1, 2], 16, 64, 64, 4, 16
     q, start, h, raw, c = attn_case(held, added, H, D, W, m, bs, dtype, 2)
