@@ -106,10 +106,29 @@ struct __align__(16) Group {
   int slice;        // head slice
 };
 
-struct SchedHeader {      // at the start of the workspace
+// A CTA's piece of a group.
+struct __align__(16) Segment {
+  int r, row0, pos0, npos;
+  int j0, j1;       // tiles of the group
+  int slot;         // partial result slot, -1: the group is all here
+  int slice_last;   // 2 * head slice + (the CTA's last segment)
+  __device__ __forceinline__ int slice() const { return slice_last >> 1; }
+  __device__ __forceinline__ bool last() const { return slice_last & 1; }
+};
+
+// What the combine kernel has to join at the border behind CTA c, written by
+// that CTA: a group that begins in its range and ends behind it.
+struct __align__(16) Border {
+  int row;      // row of column 0 in out and lse, columns are rows in order
+  int columns;  // 0: nothing to join
+  int parts;
+  int slot;     // of the first part; the others have slot 2 (c + i)
+};
+
+struct SchedHeader {  // at the start of the workspace
   int32_t status;
   int32_t ngroups;
-  long long ntiles;
+  long long ntiles;   // -1: refused, the attention fills its outputs with NaN
 };
 
 struct Pages {

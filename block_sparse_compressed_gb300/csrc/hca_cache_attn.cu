@@ -32,20 +32,12 @@ constexpr int kSchedThreads = 1024;
 __global__ void __launch_bounds__(kSchedThreads) hca_cache_sched_kernel(const AttnParams p) {
   __shared__ long long tmp[33];
   const int tid = threadIdx.x;
-  const int bs = 1 << p.log_bs;
-  // chunks of P positions of every request, and the checks of the lengths
-  bool ok = p.start[0] == 0;
+  bool ok = true;
   long long chunks = 0;
   for (int r0 = 0; r0 < p.R; r0 += kSchedThreads) {
     const int r = r0 + tid;
     long long n = 0;
-    if (r < p.R) {
-      const long long s0 = p.start[r], s1 = p.start[r + 1], h = p.held[r];
-      const long long T = s1 - s0;
-      const bool good = T >= 0 && s0 >= 0 && s1 <= p.N && h >= 0 && h + T <= kMaxPos;
-      ok = ok && good;
-      if (good) n = (T + p.P - 1) / p.P;
-    }
+    if (r < p.R) ok = request_chunks(p, r, n) && ok;
     long long all;
     const long long before = block_scan(n, tmp, all);
     if (r < p.R) p.gbase[r] = (int)(chunks + before);
@@ -54,9 +46,7 @@ __global__ void __launch_bounds__(kSchedThreads) hca_cache_sched_kernel(const At
   if (tid == 0) p.gbase[p.R] = (int)chunks;
   ok = __syncthreads_and(ok);
   if (!ok) chunks = 0;
-  // groups: a chunk's tiles, and its place in the line
   long long line = 0;
-  bool fits = true;
   for (long long c0 = 0; c0 < chunks; c0 += kSchedThreads) {
     const long long c = c0 + tid;
     Group g;
@@ -67,17 +57,7 @@ __global__ void __launch_bounds__(kSchedThreads) hca_cache_sched_kernel(const At
         const int mid = (lo + hi) >> 1;
         if (p.gbase[mid] <= c) lo = mid; else hi = mid;
       }
-      const int first = ((int)c - p.gbase[lo]) * p.P;
-      const int T = p.start[lo + 1] - p.start[lo];
-      const int h = p.held[lo];
-      g.r = lo;
-      g.row0 = p.start[lo] + first;
-      g.pos0 = h + first;
-      g.npos = min(p.P, T - first);
-      const Pages pg = group_pages(g.pos0, g.npos, p.W, p.m, p.log_bs, p.comp.table != nullptr);
-      g.ntiles = (int)(((long long)(pg.nraw + pg.ncomp) * bs + kTileKeys - 1) / kTileKeys);
-      // the raw table keeps the last cols pages of the request's tokens
-      fits = fits && ((h + T - 1) >> p.log_bs) - pg.rp0 < p.raw.cols && pg.ncomp <= p.comp.cols;
+      ok = chunk_group(p, lo, (int)c - p.gbase[lo], g) && ok;
     }
     long long all;
     const long long before = block_scan(g.ntiles, tmp, all);
@@ -90,11 +70,10 @@ __global__ void __launch_bounds__(kSchedThreads) hca_cache_sched_kernel(const At
     }
     line += all;
   }
-  fits = __syncthreads_and(fits);
+  ok = __syncthreads_and(ok);
   if (tid == 0) {
-    p.hdr->status = ok && fits ? HCA_OK : HCA_ERR_CACHE;
     p.hdr->ngroups = (int)(chunks * p.slices);
-    p.hdr->ntiles = ok && fits ? line * p.slices : -1;  // -1: the attention fills its outputs with NaN
+    p.hdr->ntiles = ok ? line * p.slices : -1;
   }
 }
 
@@ -103,6 +82,13 @@ __global__ void __launch_bounds__(kSchedThreads) hca_cache_sched_kernel(const At
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ void put4(float *p, const float4 &v, float f) {
+  *reinterpret_cast<float4 *>(p) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+}
+__device__ __forceinline__ void put4(__nv_bfloat16 *p, const float4 &v, float f) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(tc::pack_bf16x2(v.x * f, v.y * f), tc::pack_bf16x2(v.z * f, v.w * f));
+}
 
 // Every output of a call that failed on the device is NaN.
 template <typename T>
@@ -128,73 +114,51 @@ struct SimtShared {
   float pr[kTileKeys][kSimtCols];     // probabilities times the block's scale
   float red[4][kSimtCols];
   float m[kSimtCols], f[kSimtCols], l[kSimtCols];
-  Segment seg;
-  Group g;
+  const uint8_t *rows[8];             // the tile's pages (NULL: none or a bad block id)
+  float scale[8];
+  int key0[8], kind[8];               // kind 0 raw, 1 compressed, 2 no page
+  int first;
 };
-
-// A page of the group: its rows in memory (NULL: none or a bad block id), its
-// first key, its scale.
-struct PageRef {
-  const uint8_t *rows;
-  float scale;
-  long long key0;
-  bool comp, there;
-};
-__device__ __forceinline__ PageRef page_ref(const AttnParams &p, const Pages &pg, int r, int v) {
-  PageRef x;
-  x.rows = nullptr;
-  x.there = v < pg.nraw + pg.ncomp;
-  x.comp = v >= pg.nraw;
-  x.scale = __int_as_float(0x7fc00000);
-  x.key0 = 0;
-  if (!x.there) return x;
-  const CacheSet &s = x.comp ? p.comp : p.raw;
-  const int page = x.comp ? v - pg.nraw : pg.rp0 + v;
-  x.key0 = (long long)page << p.log_bs;
-  const int id = s.table[(size_t)r * s.cols + page % s.cols];
-  if (id < 0 || id >= s.nblocks) return x;
-  x.rows = s.pool + ((size_t)id << p.log_bs) * p.D;
-  x.scale = s.scale[id];
-  return x;
-}
 
 __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const AttnParams p) {
   extern __shared__ uint8_t keys[];  // [128][D + 4] bytes: a row's words fall into different banks
   __shared__ SimtShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long ntiles = p.hdr->ntiles;
+  if (tid == 0) {
+    p.err[blockIdx.x] = ntiles < 0 ? HCA_ERR_CACHE : HCA_OK;
+    p.border[blockIdx.x] = Border{0, 0, 0, 0};
+  }
   if (ntiles < 0) {
     poison<float>(p);
     return;
   }
-  const long long quota = cta_quota(ntiles, p.grid, kMinTiles);
+  const long long quota = cta_quota(ntiles, p.grid, p.min_tiles);
   const long long c0 = quota * blockIdx.x, c1 = min(c0 + quota, ntiles);
   if (c0 >= c1) return;
   if (warp == 0) {
     const int g = find_group(p.groups, p.hdr->ngroups, c0);
-    if (lane == 0) p.first[blockIdx.x] = g;
-    if (lane == 0) sh.red[0][0] = __int_as_float(g);
+    if (lane == 0) sh.first = g;
   }
   __syncthreads();
-  int gi = __float_as_int(sh.red[0][0]);
-  const int pitch = p.D + 4;
+  int gi = sh.first;
+  const int pitch = p.D + 4, upr = p.D / 4, ppt = kTileKeys >> p.log_bs, off = tid & ((1 << p.log_bs) - 1);
   // output threads: dimension d, keys k0, k0 + kstep, ...
   int dpad = 16;
   while (dpad < p.D && dpad < kSimtThreads) dpad *= 2;
   const int kstep = kSimtThreads / dpad, kfirst = tid / dpad;
-  for (long long at = c0; at < c1; ++gi) {
+  for (bool last = false; !last; ++gi) {
     __syncthreads();
     const Group g = p.groups[gi];
     const Segment seg = segment_of(g, c0, c1, blockIdx.x);
-    at = g.tile0 + seg.j1;
-    const int nreal = real_columns(p, g);
+    last = seg.last();
+    if (last && tid == 0) p.border[blockIdx.x] = border_of(p, g, c0, c1, quota, blockIdx.x);
+    const int nreal = real_columns(p, g.npos, g.slice);
+    const size_t row0 = (size_t)g.row0 * p.H + g.slice * p.HS;  // columns are rows of q and out in order
     const Pages pg = group_pages(g.pos0, g.npos, p.W, p.m, p.log_bs, p.comp.table != nullptr);
-    const int h0 = g.slice * p.HS;
     for (int i = tid; i < p.D * kSimtCols; i += kSimtThreads) {
       const int c = i / p.D, d = i % p.D;
-      float v = 0.f;
-      if (c < nreal) v = static_cast<const float *>(p.q)[((size_t)(g.row0 + c / p.HS) * p.H + h0 + c % p.HS) * p.D + d];
-      sh.q[d][c] = v;
+      sh.q[d][c] = c < nreal ? static_cast<const float *>(p.q)[row0 * p.D + i] : 0.f;
     }
     if (tid < kSimtCols) {
       sh.m[tid] = -INFINITY;
@@ -208,21 +172,39 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
     const float sl2 = p.scale * 1.4426950408889634f;
     for (int j = seg.j0; j < seg.j1; ++j) {
       __syncthreads();
+      if (tid < ppt) {
+        const int v = j * ppt + tid;
+        sh.rows[tid] = nullptr;
+        sh.scale[tid] = __int_as_float(0x7fc00000);
+        sh.kind[tid] = 2;
+        if (v < pg.nraw + pg.ncomp) {
+          const bool comp = v >= pg.nraw;
+          const CacheSet &s = comp ? p.comp : p.raw;
+          const int page = comp ? v - pg.nraw : pg.rp0 + v;
+          sh.kind[tid] = comp;
+          sh.key0[tid] = page << p.log_bs;
+          const int id = s.table[(size_t)g.r * s.cols + page % s.cols];
+          if (id >= 0 && id < s.nblocks) {
+            sh.rows[tid] = s.pool + ((size_t)id << p.log_bs) * p.D;
+            sh.scale[tid] = s.scale[id];
+          } else {
+            p.err[blockIdx.x] = HCA_ERR_CACHE;
+          }
+        }
+      }
+      __syncthreads();
       // stage the tile's rows
-      const int upr = p.D / 4;
-      const int ppt = kTileKeys >> p.log_bs;
       for (int i = tid; i < kTileKeys * upr; i += kSimtThreads) {
         const int row = i / upr, u = i % upr;
-        const PageRef x = page_ref(p, pg, g.r, j * ppt + (row >> p.log_bs));
+        const uint8_t *rows = sh.rows[row >> p.log_bs];
         uint32_t w = 0;
-        if (x.rows) w = reinterpret_cast<const uint32_t *>(x.rows + (size_t)(row & ((1 << p.log_bs) - 1)) * p.D)[u];
+        if (rows) w = reinterpret_cast<const uint32_t *>(rows + (size_t)(row & ((1 << p.log_bs) - 1)) * p.D)[u];
         *reinterpret_cast<uint32_t *>(keys + row * pitch + 4 * u) = w;
       }
-      const PageRef x = page_ref(p, pg, g.r, j * ppt + (tid >> p.log_bs));
+      const int kind = sh.kind[tid >> p.log_bs];
+      const float sk = sh.scale[tid >> p.log_bs];
       int ca = 0, cb = 0;
-      if (x.there) key_columns(x.comp, x.key0 + (tid & ((1 << p.log_bs) - 1)), g.pos0, g.npos, p.HS, p.W, p.m, ca, cb);
-      const float sk = x.scale;
-      if (!x.rows && x.there && cb > ca) p.hdr->status = HCA_ERR_CACHE;
+      if (kind < 2) key_columns(kind == 1, (long long)sh.key0[tid >> p.log_bs] + off, g.pos0, g.npos, p.HS, p.W, p.m, ca, cb);
       __syncthreads();
       float s[kSimtCols];
 #pragma unroll
@@ -242,7 +224,7 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
         s[c] = c >= ca && c < cb ? s[c] * (sl2 * sk) : -INFINITY;
         float mx = s[c];
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
         if (lane == 0) sh.red[warp][c] = mx;
       }
       __syncthreads();
@@ -260,7 +242,7 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
         sh.pr[tid][c] = e == 0.f ? 0.f : e * sk;
         float sum = e;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         if (lane == 0) sh.red[warp][c] = sum;
       }
       bool clear = cb <= ca;
@@ -277,6 +259,7 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
       __syncthreads();
       if (tid < kSimtCols)
         sh.l[tid] = sh.l[tid] * sh.f[tid] + ((sh.red[0][tid] + sh.red[1][tid]) + (sh.red[2][tid] + sh.red[3][tid]));
+#pragma unroll
       for (int x2 = 0; x2 < 2; ++x2) {
         const int d = tid % dpad + x2 * kSimtThreads;
         if (d >= p.D) break;
@@ -289,10 +272,7 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
           for (int c = 0; c < kSimtCols; ++c) acc[c] = fmaf(sh.pr[k][c], v, acc[c]);
         }
 #pragma unroll
-        for (int c = 0; c < kSimtCols; ++c) {
-          if (x2 == 0) o[0][c] = fmaf(o[0][c], sh.f[c], acc[c]);
-          else o[1][c] = fmaf(o[1][c], sh.f[c], acc[c]);
-        }
+        for (int c = 0; c < kSimtCols; ++c) o[x2][c] = fmaf(o[x2][c], sh.f[c], acc[c]);
       }
     }
     __syncthreads();
@@ -314,93 +294,99 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
 #pragma unroll
       for (int c = 0; c < kSimtCols; ++c) {
         if (c >= nreal) continue;
-        if (seg.whole)
-          static_cast<float *>(p.out)[((size_t)(g.row0 + c / p.HS) * p.H + h0 + c % p.HS) * p.D + d] = o[x2][c] / sh.l[c];
-        else
-          p.part_o[((size_t)seg.slot * kSimtCols + c) * p.D + d] = o[x2][c];
+        if (seg.slot < 0) static_cast<float *>(p.out)[(row0 + c) * p.D + d] = o[x2][c] / sh.l[c];
+        else p.part_o[((size_t)seg.slot * kSimtCols + c) * p.D + d] = o[x2][c];
       }
     }
     if (tid < nreal) {
-      if (seg.whole)
-        p.lse[(size_t)(g.row0 + tid / p.HS) * p.H + h0 + tid % p.HS] = (sh.m[tid] + log2f(sh.l[tid])) * 0.69314718055994531f;
-      else
-        p.part_ml[(size_t)seg.slot * kSimtCols + tid] = make_float2(sh.m[tid], sh.l[tid]);
+      if (seg.slot < 0) p.lse[row0 + tid] = (sh.m[tid] + log2f(sh.l[tid])) * 0.69314718055994531f;
+      else p.part_ml[(size_t)seg.slot * kSimtCols + tid] = make_float2(sh.m[tid], sh.l[tid]);
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// combine: out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i over a group's parts
+// combine: out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i over a group's parts,
+// and the call's status from its CTAs'
 // ---------------------------------------------------------------------------
-constexpr int kCombineWarps = 4;
+constexpr int kCombineWarps = 8;
 
-// Block (c, y): the group that crosses the border between CTAs c and c + 1 and
-// no earlier border; columns y, y + gridDim.y, ...
+// Block (c, y): the group that begins in CTA c's range and ends behind it,
+// columns [y, y + 1) * kCombineWarps / wpc.  wpc warps share a column's parts:
+// one where groups have a few parts each, more where one has many (few rows over
+// a long cache), as a warp keeps only a few rows in flight.
 template <typename T>
-__global__ void __launch_bounds__(32 * kCombineWarps) hca_cache_combine_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(32 * kCombineWarps) hca_cache_combine_kernel(const AttnParams p, int wpc) {
   __shared__ float4 acc[kCombineWarps][64];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long ntiles = p.hdr->ntiles;
-  if (ntiles <= 0) return;
-  if (p.hdr->status == HCA_ERR_TIMEOUT) {
+  const Border g = p.border[blockIdx.x];
+  int worst = HCA_OK;
+  for (int i = tid; i < p.grid; i += blockDim.x) worst = max(worst, p.err[i] == HCA_ERR_TIMEOUT ? 1000 : p.err[i]);
+  const bool late = __syncthreads_or(worst == 1000);
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    const bool bad = __syncthreads_or(worst != HCA_OK);
+    if (tid == 0) p.hdr->status = late ? HCA_ERR_TIMEOUT : bad ? HCA_ERR_CACHE : HCA_OK;
+  }
+  if (late) {
     poison<T>(p);
     return;
   }
-  const long long quota = cta_quota(ntiles, p.grid, kMinTiles);
-  const long long border = quota * (blockIdx.x + 1);
-  if (border >= ntiles) return;
-  const Group g = p.groups[p.first[blockIdx.x + 1]];
-  if (g.tile0 >= border || g.tile0 < border - quota) return;  // does not cross, or crosses an earlier border
-  const int cta0 = blockIdx.x;
-  const int n = (int)((g.tile0 + g.ntiles - 1) / quota) - cta0 + 1;
-  // the first part's slot is 0 only where the group begins with its CTA's range
-  auto slot = [&](int i) { return (size_t)(2 * (cta0 + i) + (i == 0 && g.tile0 != quota * cta0 ? 1 : 0)); };
-  const int nreal = real_columns(p, g), h0 = g.slice * p.HS;
+  const int c = blockIdx.y * (kCombineWarps / wpc) + warp / wpc, sub = warp % wpc;
+  const bool mine = c < g.columns;
+  if (wpc == 1 && !mine) return;
+  const int n = mine ? g.parts : 0;
+  auto slot = [&](int i) { return (size_t)(i == 0 ? g.slot : 2 * (blockIdx.x + i)); };
+  float M = -INFINITY, L = 0.f;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_ml[slot(i) * p.NQ + c].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const int v4 = p.D / 4;  // float4 of a row, at most 64
-  for (int c = blockIdx.y; c < nreal; c += gridDim.y) {
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_ml[slot(i) * p.NQ + c].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f;
-    for (int i = lane; i < n; i += 32) {
-      const float2 ml = p.part_ml[slot(i) * p.NQ + c];
-      if (ml.y != 0.f) L += exp2f(ml.x - M) * ml.y;
+  float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float w = 0.f;
+    if (i0 + lane < n) {
+      const float2 ml = p.part_ml[slot(i0 + lane) * p.NQ + c];
+      if (ml.y != 0.f) {  // 0: a part in which the column saw no key
+        w = exp2f(ml.x - M);
+        L += w * ml.y;
+      }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int i = warp; i < n; i += kCombineWarps) {
-      const float2 ml = p.part_ml[slot(i) * p.NQ + c];
-      const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - M);
-      const float4 *o = reinterpret_cast<const float4 *>(p.part_o + (slot(i) * p.NQ + c) * p.D);
+    const int k1 = min(32, n - i0);
+#pragma unroll 4
+    for (int k = sub; k < k1; k += wpc) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const float4 *o = reinterpret_cast<const float4 *>(p.part_o + (slot(i0 + k) * p.NQ + c) * p.D);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        if (lane + 32 * x < v4 && w != 0.f) {
+        if (lane + 32 * x < v4 && wk != 0.f) {
           const float4 v = o[lane + 32 * x];
-          s[x].x = fmaf(w, v.x, s[x].x); s[x].y = fmaf(w, v.y, s[x].y);
-          s[x].z = fmaf(w, v.z, s[x].z); s[x].w = fmaf(w, v.w, s[x].w);
+          s[x].x = fmaf(wk, v.x, s[x].x); s[x].y = fmaf(wk, v.y, s[x].y);
+          s[x].z = fmaf(wk, v.z, s[x].z); s[x].w = fmaf(wk, v.w, s[x].w);
         }
       }
     }
-    __syncthreads();
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (wpc > 1) {
     acc[warp][lane] = s[0];
     acc[warp][32 + lane] = s[1];
     __syncthreads();
-    const size_t row = (size_t)(g.row0 + c / p.HS) * p.H + h0 + c % p.HS;
-    if (tid < v4) {
-      float4 t = acc[0][tid];
+    if (!mine || sub != 0) return;
+    for (int w = 1; w < wpc; ++w) {
 #pragma unroll
-      for (int w = 1; w < kCombineWarps; ++w) {
-        const float4 u = acc[w][tid];
-        t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+      for (int x = 0; x < 2; ++x) {
+        const float4 u = acc[warp + w][lane + 32 * x];
+        s[x].x += u.x; s[x].y += u.y; s[x].z += u.z; s[x].w += u.w;
       }
-      const float inv = 1.f / L;
-      T *o = static_cast<T *>(p.out) + row * p.D + 4 * tid;
-      put(o, t.x * inv); put(o + 1, t.y * inv); put(o + 2, t.z * inv); put(o + 3, t.w * inv);
     }
-    if (tid == 0) p.lse[row] = (M + log2f(L)) * 0.69314718055994531f;
   }
+  const float inv = 1.f / L;
+  const size_t row = (size_t)g.row + c;
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    if (lane + 32 * x < v4) put4(static_cast<T *>(p.out) + row * p.D + 4 * (lane + 32 * x), s[x], inv);
+  if (lane == 0) p.lse[row] = (M + log2f(L)) * 0.69314718055994531f;
 }
 
 // Columns of a group for H heads: enough for one position's slice of heads, and
@@ -419,7 +405,8 @@ int pick_columns(int N, int R, int H, int dtype) {
 struct Layout {
   int NQ, HS, slices, P;
   size_t gmax;
-  size_t off_gbase, off_groups, off_first, off_ml, off_o, bytes;
+  size_t off_gbase, off_groups, off_err, off_border, off_ml, off_o, bytes;
+  int ctas;  // at most
 };
 
 Layout layout_of(int N, int R, int H, int D, int dtype) {
@@ -429,15 +416,19 @@ Layout layout_of(int N, int R, int H, int D, int dtype) {
   l.slices = (H + most - 1) / most;
   l.HS = (H + l.slices - 1) / l.slices;
   l.P = l.slices == 1 ? l.NQ / l.HS : 1;
-  l.gmax = ((size_t)N / l.P + R) * l.slices;
-  const size_t slots = 2 * (size_t)max_ctas(l.NQ, on_tensor_cores(dtype));
+  // a request's last chunk may be short, and a chunk has at least one token
+  l.gmax = std::min((size_t)N / l.P + R, (size_t)N) * l.slices;
+  l.ctas = max_ctas(l.NQ, on_tensor_cores(dtype));
+  const size_t slots = 2 * (size_t)l.ctas;
   size_t at = kHeaderBytes;
   l.off_gbase = at;
   at += align_up(((size_t)R + 1) * sizeof(int32_t));
   l.off_groups = at;
   at += align_up(l.gmax * sizeof(Group));
-  l.off_first = at;
-  at += align_up(slots * sizeof(int32_t));
+  l.off_err = at;
+  at += align_up(l.ctas * sizeof(int32_t));
+  l.off_border = at;
+  at += align_up(l.ctas * sizeof(Border));
   l.off_ml = at;
   at += align_up(slots * l.NQ * sizeof(float2));
   l.off_o = at;
@@ -464,7 +455,8 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
   p.hdr = reinterpret_cast<SchedHeader *>(ws);
   p.gbase = reinterpret_cast<int32_t *>(ws + l.off_gbase);
   p.groups = reinterpret_cast<Group *>(ws + l.off_groups);
-  p.first = reinterpret_cast<int32_t *>(ws + l.off_first);
+  p.err = reinterpret_cast<int32_t *>(ws + l.off_err);
+  p.border = reinterpret_cast<Border *>(ws + l.off_border);
   p.part_ml = reinterpret_cast<float2 *>(ws + l.off_ml);
   p.part_o = reinterpret_cast<float *>(ws + l.off_o);
   p.N = a.N; p.R = a.R; p.H = a.H; p.D = a.D; p.W = a.W; p.m = a.m; p.log_bs = log2_int(a.bs);
@@ -473,8 +465,11 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
   const int sms = tc::sm_count();
   if (sms <= 0) return cudaErrorNoDevice;
   const bool tcs = on_tensor_cores(a.dtype);
-  p.grid = std::min((tcs ? tc_cache_ctas(l.NQ) : 4) * sms, max_ctas(l.NQ, tcs));
-  {
+  p.grid = std::min((tcs ? tc_cache_ctas(l.NQ) : 4) * sms, l.ctas);
+  p.min_tiles = tcs ? 2 : 1;
+  const int threads = tcs ? tc_cache_threads(l.NQ) : 0;
+  p.in_cta = l.slices == 1 && a.R <= threads && l.gmax <= (size_t)threads;
+  if (!p.in_cta) {
     ProfScope prof(kKCacheSched, st);
     hca_cache_sched_kernel<<<1, kSchedThreads, 0, st>>>(p);
   }
@@ -490,9 +485,12 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
   }
   {
     ProfScope prof(kKCacheCombine, st);
-    const dim3 grid(p.grid - 1, min(p.NQ, 8));
-    if (a.dtype == HCA_F32) hca_cache_combine_kernel<float><<<grid, 32 * kCombineWarps, 0, st>>>(p);
-    else hca_cache_combine_kernel<__nv_bfloat16><<<grid, 32 * kCombineWarps, 0, st>>>(p);
+    // parts of a group, if the groups were alike: 4 for each warp of a column
+    const size_t parts = p.grid / std::max<size_t>(1, l.gmax);
+    const int wpc = parts >= 32 ? 8 : parts >= 16 ? 4 : parts >= 8 ? 2 : 1;
+    const dim3 grid(p.grid, (std::min(p.NQ, p.P * p.HS) * wpc + kCombineWarps - 1) / kCombineWarps);
+    if (a.dtype == HCA_F32) hca_cache_combine_kernel<float><<<grid, 32 * kCombineWarps, 0, st>>>(p, wpc);
+    else hca_cache_combine_kernel<__nv_bfloat16><<<grid, 32 * kCombineWarps, 0, st>>>(p, wpc);
   }
   return cudaGetLastError();
 }

@@ -48,11 +48,16 @@ constexpr float kTopLog2 = 8.f;   // larger ones move the reference (e4m3 ends a
 
 template <int NQ, int D>
 struct Cfg {
-  static constexpr int WG = NQ == 128 ? 2 : 1;         // softmax warpgroups, CW columns each
+  static constexpr int WG = NQ == 128 ? 2 : 1;    // softmax warpgroups, CW columns each
   static constexpr int CW = NQ / WG;
-  static constexpr int kSoft = 128 * WG;               // softmax threads
-  static constexpr int kThreads = kSoft + 64;          // and a TMA and an MMA warp
-  static constexpr int kCtas = NQ == 128 ? 1 : 2;      // CTAs per SM
+  static constexpr int kSoft = 128 * WG;          // softmax threads
+  static constexpr int kThreads = kSoft + 128;    // and the warpgroup of the TMA and the MMA warp
+  static constexpr int kCtas = NQ == 128 ? 1 : 2; // CTAs per SM
+  // Registers.  A softmax thread holds CW scores and CW sums, more than an even
+  // share of the SM's registers allows: the other warpgroup gives up some of its.
+  static constexpr int kRegsSoft = NQ == 128 ? 216 : 192, kRegsIssue = 64;
+  static constexpr int kRegsLaunch = NQ == 128 ? 168 : 128;
+  static_assert(kSoft * kRegsSoft + 128 * kRegsIssue <= kThreads * kRegsLaunch, "register split must fit the launch");
   static constexpr int kStageBytes = kTileKeys * D;
   static constexpr int kStages = (NQ == 128 ? 6 : 3) * (128 / D);
   static constexpr int kQBytes = 2 * NQ * D;           // q_hi | q_lo
@@ -64,10 +69,11 @@ struct Cfg {
   static constexpr int kTmem = 4 * NQ;                 // S twice, O_hi, O_lo
 };
 
+// A page of a tile.
+enum PageKind { kRaw = 0, kComp = 1, kNoPage = 2, kAllSeen = 3 };  // kAllSeen: every column sees every key
 struct __align__(16) PageMeta {
-  int key0;     // first key of the page
-  int kind;     // 0 raw, 1 compressed, 2 no page
-  float scale, log2_scale;
+  int key0_kind;  // first key (a multiple of 16) + kind
+  float scale, log2_scale, inv_scale;
 };
 
 template <int NQ, int D>
@@ -82,6 +88,11 @@ struct Shared {
   float delta[NQ], fac[NQ], inv[NQ];
   int unset[NQ];
   float amax[4 * C::WG];
+  // the CTA's pieces of groups, in order (more than there is room for: read
+  // from the schedule kernel's groups)
+  Segment seg[C::kThreads];
+  int gbase[C::kThreads];
+  long long scan[33];
   uint32_t tmem_base;
   int abort, first;
 };
@@ -123,27 +134,30 @@ __device__ __forceinline__ void load_cols(uint32_t addr, uint32_t (&r)[N]) {
   tmem_wait_ld();
 }
 
-__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
+__device__ __forceinline__ void st_shared(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
 
-// Two values to two e4m3 numbers each: hi = e4m3(v), lo = e4m3((v - hi) * f).
+// Four values to two e4m3 numbers each: hi = e4m3(v), lo = e4m3((v - hi) * f).
 // fp16 holds v to 11 bits, hi and the difference exactly.
-__device__ __forceinline__ void split2(uint32_t h2, uint32_t f2, uint32_t &hi, uint32_t &lo) {
-  hi = e4m3x2_from_f16x2(h2);
-  lo = e4m3x2_from_f16x2(hmul2(hsub2(h2, f16x2_from_e4m3x2(hi)), f2));
+__device__ __forceinline__ void split4(float v0, float v1, float v2, float v3, uint32_t f2, uint32_t &hi, uint32_t &lo) {
+  asm("{\n\t.reg .b32 a, b, c, d;\n\t.reg .b16 x, y;\n\t"
+      "cvt.rn.f16x2.f32 a, %3, %2;\n\t"
+      "cvt.rn.f16x2.f32 b, %5, %4;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 x, a;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 y, b;\n\t"
+      "mov.b32 %0, {x, y};\n\t"
+      "cvt.rn.f16x2.e4m3x2 c, x;\n\t"
+      "cvt.rn.f16x2.e4m3x2 d, y;\n\t"
+      "sub.rn.f16x2 a, a, c;\n\t"
+      "sub.rn.f16x2 b, b, d;\n\t"
+      "mul.rn.f16x2 a, a, %6;\n\t"
+      "mul.rn.f16x2 b, b, %6;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 x, a;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 y, b;\n\t"
+      "mov.b32 %1, {x, y};\n\t}"
+      : "=&r"(hi), "=r"(lo)
+      : "f"(v0), "f"(v1), "f"(v2), "f"(v3), "r"(f2));
 }
 
 template <int NQ, int D>
@@ -157,7 +171,7 @@ __global__ void __launch_bounds__(Cfg<NQ, D>::kThreads, Cfg<NQ, D>::kCtas)
   __shared__ Shared<NQ, D> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int *abort_flag = &sh.abort;
-  int32_t *status = &p.hdr->status;
+  int32_t *status = &p.err[blockIdx.x];
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -176,23 +190,79 @@ __global__ void __launch_bounds__(Cfg<NQ, D>::kThreads, Cfg<NQ, D>::kCtas)
     sh.abort = 0;
     fence_mbar_init();
   }
-  const long long ntiles = p.hdr->ntiles;
-  const long long quota = cta_quota(ntiles, p.grid, kMinTiles);
-  const long long c0 = quota * blockIdx.x, c1 = min(c0 + quota, ntiles);
-  const bool busy = c0 < c1;
-  if (warp == 0) {
+  if (warp == C::kSoft / 32 + 2) {
     tmem_alloc(&sh.tmem_base, C::kTmem);
     tmem_relinquish();
   }
-  if (warp == C::kSoft / 32 && busy) {
-    const int g = find_group(p.groups, p.hdr->ngroups, c0);
-    if (lane == 0) sh.first = p.first[blockIdx.x] = g;
+  // the CTA's range of the line, and its pieces of groups
+  long long ntiles, quota, c0, c1;
+  if (p.in_cta) {
+    // one thread per request, then one per group
+    long long n = 0, all;
+    bool ok = true;
+    if (tid < p.R) ok = request_chunks(p, tid, n);
+    const long long before = block_scan(n, sh.scan, all);
+    if (tid < p.R) sh.gbase[tid] = (int)before;
+    ok = __syncthreads_and(ok);
+    Group g;
+    g.ntiles = 0;
+    const bool mine = ok && tid < all;
+    if (mine) {
+      int lo = 0, hi = p.R;  // gbase[lo] <= tid < gbase[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sh.gbase[mid] <= tid) lo = mid; else hi = mid;
+      }
+      ok = chunk_group(p, lo, tid - sh.gbase[lo], g);
+    }
+    g.tile0 = block_scan(g.ntiles, sh.scan, ntiles);
+    if (!__syncthreads_and(ok)) ntiles = -1;
+    quota = cta_quota(ntiles, p.grid, p.min_tiles);
+    c0 = quota * blockIdx.x;
+    c1 = min(c0 + quota, ntiles);
+    const bool in = mine && g.tile0 < c1 && g.tile0 + g.ntiles > c0;
+    if (in && g.tile0 <= c0) sh.first = tid;
+    __syncthreads();
+    if (in) {
+      const Segment x = segment_of(g, c0, c1, blockIdx.x);
+      sh.seg[tid - sh.first] = x;
+      if (x.last()) p.border[blockIdx.x] = border_of(p, g, c0, c1, quota, blockIdx.x);
+    }
+  } else {
+    ntiles = p.hdr->ntiles;
+    quota = cta_quota(ntiles, p.grid, p.min_tiles);
+    c0 = quota * blockIdx.x;
+    c1 = min(c0 + quota, ntiles);
+    if (c0 < c1) {
+      const int ng = p.hdr->ngroups;
+      if (warp == 0) {
+        const int g = find_group(p.groups, ng, c0);
+        if (lane == 0) sh.first = g;
+      } else if (warp == 1) {
+        const int g = find_group(p.groups, ng, c1 - 1);
+        if (lane == 0) p.border[blockIdx.x] = border_of(p, p.groups[g], c0, c1, quota, blockIdx.x);
+      }
+      __syncthreads();
+      const int gi = sh.first + tid;
+      if (gi < ng) {
+        const Group g = p.groups[gi];
+        if (g.tile0 < c1) sh.seg[tid] = segment_of(g, c0, c1, blockIdx.x);
+      }
+    }
   }
+  const bool busy = c0 < c1;
+  if (tid == 0) {
+    p.err[blockIdx.x] = ntiles < 0 ? HCA_ERR_CACHE : HCA_OK;
+    if (!busy) p.border[blockIdx.x] = Border{0, 0, 0, 0};
+  }
+  auto segment = [&](int k) { return k < C::kThreads ? sh.seg[k] : segment_of(p.groups[sh.first + k], c0, c1, blockIdx.x); };
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
 
+  if (warp >= C::kSoft / 32) {
+  setmaxnreg_dec<C::kRegsIssue>();
   if (warp == C::kSoft / 32) {
     // -------------------------------------------------------------- TMA
     if (busy) {
@@ -205,57 +275,56 @@ __global__ void __launch_bounds__(Cfg<NQ, D>::kThreads, Cfg<NQ, D>::kCtas)
       const int page_bytes = D << p.log_bs;
       uint32_t n = 0, issued = 0;  // tiles; bit s: stage s loaded, bit 16 + s: parity of its last load
       bool ok = true;
-      int gi = sh.first;
-      Group g = p.groups[gi];
-      for (long long at = c0; ok && at < c1;) {
-        const Segment seg = segment_of(g, c0, c1, blockIdx.x);
-        at = g.tile0 + seg.j1;
+      for (int k = 0; ok; ++k) {
+        const Segment g = segment(k);
         const Pages pg = group_pages(g.pos0, g.npos, p.W, p.m, p.log_bs, p.comp.table != nullptr);
-        Group gn = g;
-        if (at < c1) gn = p.groups[gi + 1];
-        for (int jb = seg.j0; ok && jb < seg.j1; jb += batch) {
+        for (int jb = g.j0; ok && jb < g.j1; jb += batch) {
           const int v = jb * ppt + lane;
-          PageMeta pm = {0, 2, 0.f, 0.f};
+          PageMeta pm = {kNoPage, 1.f, 0.f, 0.f};
           int id = -1;
-          bool good = false;
-          if (v < pg.nraw + pg.ncomp && v < seg.j1 * ppt) {
-            const bool comp = v >= pg.nraw;
+          bool good = false, comp = false;
+          if (v < pg.nraw + pg.ncomp && v < g.j1 * ppt) {
+            comp = v >= pg.nraw;
             const CacheSet &cs = comp ? p.comp : p.raw;
             const int page = comp ? v - pg.nraw : pg.rp0 + v;
             id = cs.table[(size_t)g.r * cs.cols + page % cs.cols];
-            pm.kind = comp;
-            pm.key0 = page << p.log_bs;
+            const int key0 = page << p.log_bs;
+            const long long end = (long long)key0 + (1 << p.log_bs);
+            const bool all = comp ? end * p.m <= g.pos0 + 1 : end <= (long long)g.pos0 + 1 && key0 > g.pos0 + g.npos - 1 - p.W;
+            pm.key0_kind = key0 + (all ? kAllSeen : comp ? kComp : kRaw);
             pm.scale = __int_as_float(0x7fc00000);
             good = id >= 0 && id < cs.nblocks;
             if (good) pm.scale = cs.scale[id];
             else atomicExch(status, HCA_ERR_CACHE);
           }
           const uint32_t have = __ballot_sync(0xffffffffu, good);
-          const int jn = min(batch, seg.j1 - jb);
-          for (int k = 0; k < jn; ++k, ++n) {
+          const int jn = min(batch, g.j1 - jb);
+          for (int t = 0; t < jn; ++t, ++n) {
             const int st = n % C::kStages;
             if (n >= (uint32_t)C::kStages)
               ok = wait_warp(&sh.kv_empty[st], ((n / C::kStages) - 1) & 1, abort_flag, status, p.wait_ns);
             if (!ok) break;
-            const uint32_t mine = (have >> (k * ppt)) & ((1u << ppt) - 1u);
+            const uint32_t mine = (have >> (t * ppt)) & ((1u << ppt) - 1u);
             if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[st], __popc(mine) * page_bytes);
             issued = (issued | (1u << st)) & ~(1u << (16 + st));
             issued |= ((n / C::kStages) & 1u) << (16 + st);
             __syncwarp();
-            if (lane / ppt == k) {
+            if (lane / ppt == t) {
               const int slot = lane % ppt;
               uint8_t *dst = smem + st * C::kStageBytes + slot * page_bytes;
-              if (good && pm.kind) tma_load_2d(&map_comp, &sh.kv_full[st], dst, 0, id << p.log_bs);
+              if (good && comp) tma_load_2d(&map_comp, &sh.kv_full[st], dst, 0, id << p.log_bs);
               else if (good) tma_load_2d(&map_raw, &sh.kv_full[st], dst, 0, id << p.log_bs);
-              pm.log2_scale = log2f(pm.scale);
+              if (pm.key0_kind != kNoPage) {
+                pm.log2_scale = log2f(pm.scale);
+                pm.inv_scale = 1.f / pm.scale;
+              }
               sh.meta[st][slot] = pm;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.kv_full[st]);
           }
         }
-        g = gn;
-        ++gi;
+        if (g.last()) break;
       }
       if (!ok && lane == 0) {
         volatile int never = 0;
@@ -266,6 +335,9 @@ __global__ void __launch_bounds__(Cfg<NQ, D>::kThreads, Cfg<NQ, D>::kCtas)
     }
   } else if (warp == C::kSoft / 32 + 1) {
     // -------------------------------------------------------------- MMA
+    // S of tile n + 1 is issued before O of tile n, so that it is there when the
+    // softmax of tile n ends.  Products run in the order of issue: S of tile n
+    // complete means O of tile n - 2 complete, whose P buffer tile n takes.
     if (busy) {
       const uint32_t kv0 = smem_u32(smem), q0 = smem_u32(smem + C::kOffQ), p0 = smem_u32(smem + C::kOffP);
       uint64_t dk, dv, dq;
@@ -309,12 +381,8 @@ __global__ void __launch_bounds__(Cfg<NQ, D>::kThreads, Cfg<NQ, D>::kCtas)
         __syncwarp();
         return true;
       };
-      int gi = sh.first;
-      Group g = p.groups[gi];
-      for (long long at = c0; ok && at < c1; ++nseg) {
-        const Segment seg = segment_of(g, c0, c1, blockIdx.x);
-        at = g.tile0 + seg.j1;
-        if (at < c1) g = p.groups[++gi];
+      for (; ok; ++nseg) {
+        const Segment seg = segment(nseg);
         for (int j = seg.j0; ok && j < seg.j1; ++j, ++n) {
           const bool first = j == seg.j0;
           // a group's q is written after the last softmax of the group before
@@ -340,6 +408,7 @@ __global__ void __launch_bounds__(Cfg<NQ, D>::kThreads, Cfg<NQ, D>::kCtas)
           if (!first) ok = issue_pv(n - 1, prev_first);
           prev_first = first;
         }
+        if (seg.last()) break;
       }
       if (ok && n > 0) ok = issue_pv(n - 1, prev_first);
       if (!ok && issued) {
@@ -350,7 +419,10 @@ __global__ void __launch_bounds__(Cfg<NQ, D>::kThreads, Cfg<NQ, D>::kCtas)
         __syncwarp();
       }
     }
-  } else if (ntiles < 0) {
+  }
+  } else {
+  setmaxnreg_inc<C::kRegsSoft>();
+  if (ntiles < 0) {
     // the schedule was refused
     const size_t rows = (size_t)p.N * p.H;
     const uint4 nan4 = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
@@ -365,14 +437,14 @@ __global__ void __launch_bounds__(Cfg<NQ, D>::kThreads, Cfg<NQ, D>::kCtas)
     const int wg = warp >> 2, r = tid & 127;  // warpgroup; key of a tile, dimension of O
     const int col0 = wg * CW;
     const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t bar_wg = 1 + wg, bar_all = 3;
+    const uint32_t bar_wg = 1 + wg, bar_all = 1 + C::WG;
     auto wait = [&](uint64_t *bar, uint32_t parity) { (void)wait_warp(bar, parity, abort_flag, status, p.wait_ns); };
 
     // q of a group into shared memory; returns log2(e) * scale / (its factor)
-    auto load_q = [&](const Group &g) {
+    auto load_q = [&](const Segment &g) {
       constexpr int kUnits = NQ * D / 16 / C::kSoft;  // 16 values each
-      const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)g.row0 * p.H + g.slice * p.HS) * D;
-      const int nreal = real_columns(p, g);
+      const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)g.row0 * p.H + g.slice() * p.HS) * D;
+      const int nreal = real_columns(p, g.npos, g.slice());
       uint4 u[kUnits > 0 ? kUnits : 1][2];
       constexpr int kAll = NQ * D / 16;
       float amax = 0.f;
@@ -408,23 +480,16 @@ __global__ void __launch_bounds__(Cfg<NQ, D>::kThreads, Cfg<NQ, D>::kCtas)
         const uint32_t w[8] = {u[k][0].x, u[k][0].y, u[k][0].z, u[k][0].w, u[k][1].x, u[k][1].y, u[k][1].z, u[k][1].w};
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float a = __uint_as_float(w[e] << 16), b = __uint_as_float(w[e] & 0xffff0000u);
-          // an infinity becomes NaN, not 448
-          const uint32_t h2 = f16x2_rn(fmaf(a, 0.f, a * inv), fmaf(b, 0.f, b * inv));
-          uint32_t h, l;
-          split2(h2, 0x3c003c00u, h, l);  // factor 1: one accumulator for both
-          if (e & 1) {
-            hi[e >> 1] |= h << 16;
-            lo[e >> 1] |= l << 16;
-          } else {
-            hi[e >> 1] = h;
-            lo[e >> 1] = l;
-          }
+        for (int e = 0; e < 4; ++e) {
+          float v[4] = {__uint_as_float(w[2 * e] << 16), __uint_as_float(w[2 * e] & 0xffff0000u),
+                        __uint_as_float(w[2 * e + 1] << 16), __uint_as_float(w[2 * e + 1] & 0xffff0000u)};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) v[x] = fmaf(v[x], 0.f, v[x] * inv);  // an infinity becomes NaN, not 448
+          split4(v[0], v[1], v[2], v[3], 0x3c003c00u, hi[e], lo[e]);        // factor 1: one accumulator for both
         }
         const int off = D == 128 ? c * 128 + ((ch ^ (c & 7)) << 4) : c * 64 + ((ch ^ ((c >> 1) & 3)) << 4);
-        *reinterpret_cast<uint4 *>(smem + C::kOffQ + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4 *>(smem + C::kOffQ + NQ * D + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        st_shared(smem_u32(smem) + C::kOffQ + off, hi);
+        st_shared(smem_u32(smem) + C::kOffQ + NQ * D + off, lo);
       }
       fence_async_smem();
       mbar_arrive(&sh.q_full);
@@ -432,31 +497,29 @@ __global__ void __launch_bounds__(Cfg<NQ, D>::kThreads, Cfg<NQ, D>::kCtas)
     };
 
     uint32_t n = 0;
-    int gi = sh.first;
-    Group g = p.groups[gi];
-    float cs = load_q(g);
-    for (long long at = c0; at < c1;) {
-      const Segment seg = segment_of(g, c0, c1, blockIdx.x);
-      at = g.tile0 + seg.j1;
-      Group gn = g;
-      if (at < c1) gn = p.groups[++gi];
-      const int nfull = g.npos * p.HS, nreal = real_columns(p, g);
+    float cs = load_q(segment(0));
+    for (int k = 0;; ++k) {
+      const Segment g = segment(k);
+      const int nreal = real_columns(p, g.npos, g.slice());
       float l[CW];
 #pragma unroll
       for (int c = 0; c < CW; ++c) l[c] = 0.f;
       bool unset = true;  // some column has seen no key yet
-      for (int j = seg.j0; j < seg.j1; ++j, ++n) {
-        const bool first = j == seg.j0;
+      for (int j = g.j0; j < g.j1; ++j, ++n) {
+        const bool first = j == g.j0;
         const uint32_t st = n % C::kStages, b = n & 1;
         wait(&sh.kv_full[st], (n / C::kStages) & 1);  // for the pages' data; the MMA warp has waited for the rows
         const PageMeta pm = sh.meta[st][r >> p.log_bs];
-        int ca = 0, cb = 0;
-        if (pm.kind < 2)
-          key_columns(pm.kind == 1, (long long)pm.key0 + (r & ((1 << p.log_bs) - 1)), g.pos0, g.npos, p.HS, p.W, p.m, ca, cb);
+        const int kind = pm.key0_kind & 3;
+        int ca = 0, cb = kind == kAllSeen ? NQ : 0;
+        if (kind < kNoPage) {
+          key_columns(kind == kComp, (long long)(pm.key0_kind & ~3) + (r & ((1 << p.log_bs) - 1)), g.pos0, g.npos, p.HS, p.W,
+                      p.m, ca, cb);
+          if (ca == 0 && cb == g.npos * p.HS) cb = NQ;  // columns that stand for nothing do no harm
+        }
         const bool none = cb <= ca;
-        if (ca == 0 && cb == nfull) cb = NQ;  // columns that stand for nothing do no harm
         const bool full = __all_sync(0xffffffffu, ca == 0 && cb == NQ);
-        const float ck = cs * pm.scale, inv_s = 1.f / pm.scale;
+        const float ck = cs * pm.scale;
         wait(&sh.s_full[b], (n >> 1) & 1);
         tc_fence_after();
         uint32_t t[CW];
@@ -551,37 +614,28 @@ __global__ void __launch_bounds__(Cfg<NQ, D>::kThreads, Cfg<NQ, D>::kCtas)
           }
         }
         // probabilities, the row sums, and two e4m3 numbers for each
-        if (n >= 2) wait(&sh.pv_done[b], ((n >> 1) - 1) & 1);  // P's buffer is free
-        uint8_t *prow = smem + C::kOffP + b * C::kPBytes + r * 128;
-        const uint64_t inv2 = f32x2(__float_as_uint(inv_s), __float_as_uint(inv_s));
+        const uint32_t prow = smem_u32(smem) + C::kOffP + b * C::kPBytes + r * 128;
+        const uint64_t inv2 = f32x2(__float_as_uint(pm.inv_scale), __float_as_uint(pm.inv_scale));
 #pragma unroll
         for (int c = 0; c < CW; c += 16) {
           uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int y = 0; y < 16; y += 2) {
-            const float e0 = ex2_approx(__uint_as_float(t[c + y])), e1 = ex2_approx(__uint_as_float(t[c + y + 1]));
-            uint64_t l2 = f32x2(__float_as_uint(l[c + y]), __float_as_uint(l[c + y + 1]));
-            // a masked key's scale may be anything
-            l2 = none ? l2 : ffma2(f32x2(__float_as_uint(e0), __float_as_uint(e1)), inv2, l2);
-            f32x2_split(l2, l[c + y], l[c + y + 1]);
-            uint32_t h, lw;
-            split2(f16x2_rn(e0, e1), 0x50005000u, h, lw);  // 2^5
-            if (y & 2) {
-              hi[y >> 2] |= h << 16;
-              lo[y >> 2] |= lw << 16;
-            } else {
-              hi[y >> 2] = h;
-              lo[y >> 2] = lw;
+          for (int y = 0; y < 16; y += 4) {
+            float e[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) e[x] = ex2_approx(__uint_as_float(t[c + y + x]));
+#pragma unroll
+            for (int x = 0; x < 4; x += 2) {
+              const uint64_t l2 = f32x2(__float_as_uint(l[c + y + x]), __float_as_uint(l[c + y + x + 1]));
+              f32x2_split(ffma2(f32x2(__float_as_uint(e[x]), __float_as_uint(e[x + 1])), inv2, l2), l[c + y + x],
+                          l[c + y + x + 1]);
             }
+            split4(e[0], e[1], e[2], e[3], 0x50005000u, hi[y >> 2], lo[y >> 2]);  // 2^5
           }
           const int ch = (col0 + c) >> 4;
-          if constexpr (NQ == 128) {
-            *reinterpret_cast<uint4 *>(prow + ((ch ^ (r & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(prow + C::kPHalf + ((ch ^ (r & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          } else {
-            *reinterpret_cast<uint4 *>(prow + ((ch ^ (r & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(prow + (((NQ / 16 + ch) ^ (r & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
+          constexpr int kLo = NQ == 128 ? 0 : NQ / 16;  // P_lo's first 16-byte chunk
+          st_shared(prow + ((ch ^ (r & 7)) << 4), hi);
+          st_shared(prow + C::kPHalf + (((kLo + ch) ^ (r & 7)) << 4), lo);
         }
         if (wg == 0 && !full) {
           uint4 *row = reinterpret_cast<uint4 *>(smem + st * C::kStageBytes + r * D);
@@ -604,7 +658,7 @@ __global__ void __launch_bounds__(Cfg<NQ, D>::kThreads, Cfg<NQ, D>::kCtas)
       }
       // the next group's q: every product with this one's has been made
       const float nref = r < CW ? sh.nref[col0 + r] : 0.f;
-      if (at < c1) cs = load_q(gn);
+      if (!g.last()) cs = load_q(segment(k + 1));
       // sums over the keys
       if constexpr (CW >= 32) {
 #pragma unroll
@@ -614,16 +668,17 @@ __global__ void __launch_bounds__(Cfg<NQ, D>::kThreads, Cfg<NQ, D>::kCtas)
         if (lane < CW) sh.lred[warp][lane] = s;
       }
       named_bar_sync(bar_wg, 128);
-      const size_t row0 = (size_t)g.row0 * p.H + g.slice * p.HS;  // row of column 0: columns are rows of q and out in order
+      const bool whole = g.slot < 0;
+      const size_t row0 = (size_t)g.row0 * p.H + g.slice() * p.HS;  // row of column 0: columns are rows of q and out in order
       if (r < CW) {
         const int w0 = 4 * wg, c = col0 + r;
         float s = (sh.lred[w0][r] + sh.lred[w0 + 1][r]) + (sh.lred[w0 + 2][r] + sh.lred[w0 + 3][r]);
         if (*abort_flag) s = __int_as_float(0x7fc00000);
         if (c < nreal) {
-          if (seg.whole) p.lse[row0 + c] = (log2f(s) - nref) * 0.69314718055994531f;
-          else p.part_ml[(size_t)seg.slot * NQ + c] = make_float2(-nref, s);
+          if (whole) p.lse[row0 + c] = (log2f(s) - nref) * 0.69314718055994531f;
+          else p.part_ml[(size_t)g.slot * NQ + c] = make_float2(-nref, s);
         }
-        sh.inv[c] = seg.whole ? 1.f / s : 1.f;
+        sh.inv[c] = whole ? 1.f / s : 1.f;
       }
       named_bar_sync(bar_wg, 128);
       wait(&sh.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
@@ -640,20 +695,21 @@ __global__ void __launch_bounds__(Cfg<NQ, D>::kThreads, Cfg<NQ, D>::kCtas)
             const int cc = col0 + c + y;
             const float o = fmaf(__uint_as_float(lo[y]), 1.f / 32.f, __uint_as_float(hi[y])) * sh.inv[cc];
             if (cc < nreal) {
-              if (seg.whole) static_cast<__nv_bfloat16 *>(p.out)[(row0 + cc) * D + r] = __float2bfloat16_rn(o);
-              else p.part_o[((size_t)seg.slot * NQ + cc) * D + r] = o;
+              if (whole) static_cast<__nv_bfloat16 *>(p.out)[(row0 + cc) * D + r] = __float2bfloat16_rn(o);
+              else p.part_o[((size_t)g.slot * NQ + cc) * D + r] = o;
             }
           }
         }
       }
       tc_fence_before();
-      g = gn;
+      if (g.last()) break;
     }
+  }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == C::kSoft / 32 + 2) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmem);
   }
@@ -688,6 +744,10 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &raw, const CUtensorMa
 namespace cache {
 
 int tc_cache_ctas(int NQ) { return NQ == 128 ? 1 : 2; }
+int tc_cache_threads(int NQ) {
+  return NQ == 16 ? Cfg<16, 128>::kThreads : NQ == 32 ? Cfg<32, 128>::kThreads : NQ == 64 ? Cfg<64, 128>::kThreads
+                                                                                       : Cfg<128, 128>::kThreads;
+}
 
 cudaError_t tc_cache_attn(const AttnParams &p, cudaStream_t st) {
   CUtensorMap raw, comp;

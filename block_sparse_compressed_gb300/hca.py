@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional, Tuple
@@ -516,7 +517,46 @@ def hca_csa_attn_bwd(q, kv, ckv, seg, sel, out, lse, dout, W: int, m: int, scale
 
 # ---------------------------------------------------------------------------
 # serving: plan, append and attend over a paged 8-bit cache
+#
+# A decode step's kernels take a few microseconds each, so what these calls do
+# in Python counts: no context manager unless the tensors' device is not the
+# current one, sizes of workspaces remembered, pointers passed as plain ints.
 # ---------------------------------------------------------------------------
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _enqueue(dev: torch.device, f, *args) -> int:
+    """f(*args, stream) on the device's current stream."""
+    if dev.type == "cuda" and _raw_stream is not None and dev.index == torch.cuda.current_device():
+        return f(*args, _raw_stream(dev.index))
+    with _on(dev):
+        return f(*args, _stream(dev))
+
+
+def _fits(t: torch.Tensor, name: str, shape, dtype, device) -> int:
+    """The pointer of a tensor that is as it has to be (as _need)."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _need(t, name, shape, dtype, device)
+    return t.data_ptr()
+
+
+_I32, _F32, _E4M3 = torch.int32, torch.float32, torch.float8_e4m3fn
+_PLAN_WS = 256
+
+
+@functools.lru_cache(maxsize=4096)
+def _append_ws_bytes(nblocks: int) -> int:
+    return load().hca_cache_append_workspace_size(nblocks)
+
+
+@functools.lru_cache(maxsize=4096)
+def _attn_ws_bytes(N: int, R: int, H: int, D: int, dt: int) -> int:
+    n = load().hca_cache_attn_workspace_size(N, R, H, D, dt)
+    if n == 0:
+        raise HCAError(8, "hca_cache_attn_workspace_size")
+    return n
+
+
 def hca_cache_plan(held: torch.Tensor, added: torch.Tensor, table: torch.Tensor, free_blocks: torch.Tensor,
                    free_count: torch.Tensor, nblocks: int, bs: int, nslots: int, m: int = 1,
                    start: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
@@ -525,40 +565,26 @@ def hca_cache_plan(held: torch.Tensor, added: torch.Tensor, table: torch.Tensor,
     hca_cache_plan): held[R], added[R], table[R,cols] (updated in place),
     free_blocks[nfree], free_count[1], all int32.  Returns (start[R+1],
     slots[nslots], free_left[1]); free_left may be free_count itself."""
-    lib = load()
+    lib = _lib or load()
     dev = held.device
     if held.dim() != 1 or table.dim() != 2 or free_blocks.dim() != 1:
         raise ValueError("held must be [R], table [R,cols] and free_blocks [nfree]")
-    R, cols = held.shape[0], table.shape[1]
-    _need(held, "held", (R,), torch.int32, dev)
-    _need(added, "added", (R,), torch.int32, dev)
-    _need(table, "table", (R, cols), torch.int32, dev)
-    _need(free_blocks, "free_blocks", free_blocks.shape, torch.int32, dev)
-    _need(free_count, "free_count", (1,), torch.int32, dev)
-    start = torch.empty(R + 1, dtype=torch.int32, device=dev) if start is None else start
-    slots = torch.empty(nslots, dtype=torch.int32, device=dev) if slots is None else slots
-    free_left = torch.empty(1, dtype=torch.int32, device=dev) if free_left is None else free_left
-    _need(start, "start", (R + 1,), torch.int32, dev)
-    _need(slots, "slots", (nslots,), torch.int32, dev)
-    _need(free_left, "free_left", (1,), torch.int32, dev)
-    if ws is None:
-        ws = torch.empty(lib.hca_cache_plan_workspace_size(), dtype=torch.uint8, device=dev)
-    with _on(dev):
-        rc = lib.hca_cache_plan(_ptr(held), _ptr(added), _ptr(table), _ptr(free_blocks), _ptr(free_count),
-                                _ptr(free_left), _ptr(start), _ptr(slots), R, cols, bs, m, nblocks,
-                                free_blocks.shape[0], nslots, _ptr(ws), ws.numel(), _stream(dev))
-    _check(rc, "hca_cache_plan")
+    R, cols = table.shape
+    nfree = free_blocks.shape[0]
+    start = torch.empty(R + 1, dtype=_I32, device=dev) if start is None else start
+    slots = torch.empty(nslots, dtype=_I32, device=dev) if slots is None else slots
+    free_left = torch.empty(1, dtype=_I32, device=dev) if free_left is None else free_left
+    ws = torch.empty(_PLAN_WS, dtype=torch.uint8, device=dev) if ws is None else ws
+    rc = _enqueue(dev, lib.hca_cache_plan, _fits(held, "held", (R,), _I32, dev), _fits(added, "added", (R,), _I32, dev),
+                  _fits(table, "table", (R, cols), _I32, dev), _fits(free_blocks, "free_blocks", (nfree,), _I32, dev),
+                  _fits(free_count, "free_count", (1,), _I32, dev), _fits(free_left, "free_left", (1,), _I32, dev),
+                  _fits(start, "start", (R + 1,), _I32, dev), _fits(slots, "slots", (nslots,), _I32, dev), R, cols, bs, m,
+                  nblocks, nfree, nslots, ws.data_ptr(), ws.numel())
+    if rc != 0:
+        _check(rc, "hca_cache_plan")
     if check:
         _check(hca_workspace_status(ws), "hca_cache_plan (device)")
     return start, slots, free_left
-
-
-def _cache_pool(pool: torch.Tensor, scale: torch.Tensor, name: str, device):
-    if pool.dim() != 3:
-        raise ValueError(f"{name} pool must be [nblocks,bs,D]")
-    _need(pool, f"{name} pool", pool.shape, torch.float8_e4m3fn, device)
-    _need(scale, f"{name} scale", (pool.shape[0],), torch.float32, device)
-    return pool.shape
 
 
 def hca_cache_append(x: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor, scale: torch.Tensor,
@@ -566,21 +592,32 @@ def hca_cache_append(x: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor, s
     """Rows x[N,D] (bf16 or fp32) into slots[N] (int32, -1: nowhere) of the
     cache pool[nblocks,bs,D] (float8_e4m3fn) with scale[nblocks] (fp32), both
     updated in place (include/hca.h, hca_cache_append)."""
-    lib = load()
+    lib = _lib or load()
     dev = x.device
-    nblocks, bs, D = _cache_pool(pool, scale, "cache", dev)
-    _need(x, "x", (x.shape[0], D), x.dtype, dev)
+    if x.dim() != 2 or pool.dim() != 3:
+        raise ValueError("x must be [N,D] and pool [nblocks,bs,D]")
     dt = _dtype_code(x)
+    nblocks, bs, D = pool.shape
     N = x.shape[0]
-    _need(slots, "slots", (N,), torch.int32, dev)
-    if ws is None:
-        ws = torch.empty(lib.hca_cache_append_workspace_size(nblocks), dtype=torch.uint8, device=dev)
-    with _on(dev):
-        rc = lib.hca_cache_append(_ptr(x), _ptr(slots), _ptr(pool), _ptr(scale), N, D, bs, nblocks, dt, _ptr(ws),
-                                  ws.numel(), _stream(dev))
-    _check(rc, "hca_cache_append")
+    ws = torch.empty(_append_ws_bytes(nblocks), dtype=torch.uint8, device=dev) if ws is None else ws
+    rc = _enqueue(dev, lib.hca_cache_append, _fits(x, "x", (N, D), x.dtype, dev), _fits(slots, "slots", (N,), _I32, dev),
+                  _fits(pool, "pool", (nblocks, bs, D), _E4M3, dev), _fits(scale, "scale", (nblocks,), _F32, dev), N, D,
+                  bs, nblocks, dt, ws.data_ptr(), ws.numel())
+    if rc != 0:
+        _check(rc, "hca_cache_append")
     if check:
         _check(hca_workspace_status(ws), "hca_cache_append (device)")
+
+
+def _cache_args(name: str, cache, R: int, bs: int, D: int, dev):
+    if cache is None:
+        return None, None, None, 0, 0
+    pool, scale, table = cache
+    if pool.dim() != 3 or table.dim() != 2:
+        raise ValueError(f"{name} must be (pool[nblocks,bs,D], scale[nblocks], table[R,cols])")
+    nblocks, cols = pool.shape[0], table.shape[1]
+    return (_fits(pool, f"{name} pool", (nblocks, bs, D), _E4M3, dev), _fits(scale, f"{name} scale", (nblocks,), _F32, dev),
+            _fits(table, f"{name} table", (R, cols), _I32, dev), nblocks, cols)
 
 
 def hca_cache_attn(q: torch.Tensor, start: torch.Tensor, held: torch.Tensor, raw, comp, W: int, m: int, scale: float,
@@ -591,44 +628,23 @@ def hca_cache_attn(q: torch.Tensor, start: torch.Tensor, held: torch.Tensor, raw
     start[r]..start[r+1]-1 at positions held[r]...  raw and comp are
     (pool, scale, table[R,cols]); comp may be None.  Returns (out[N,H,D],
     lse[N,H] fp32)."""
-    lib = load()
+    lib = _lib or load()
     dev = q.device
-    if q.dim() != 3 or held.dim() != 1:
-        raise ValueError("q must be [N,H,D] and held [R]")
+    if q.dim() != 3 or held.dim() != 1 or raw[0].dim() != 3:
+        raise ValueError("q must be [N,H,D], held [R] and the raw pool [nblocks,bs,D]")
     N, H, D = q.shape
-    R = held.shape[0]
+    R, bs = held.shape[0], raw[0].shape[1]
     dt = _dtype_code(q)
-    _need(q, "q", (N, H, D), q.dtype, dev)
-    _need(held, "held", (R,), torch.int32, dev)
-    _need(start, "start", (R + 1,), torch.int32, dev)
-    args = []
-    bs = raw[0].shape[1] if raw[0].dim() == 3 else 0
-    for name, cache in (("raw", raw), ("comp", comp)):
-        if cache is None:
-            args += [None, None, None, 0, 0]
-            continue
-        pool, sc, table = cache
-        nblocks, b, d = _cache_pool(pool, sc, name, dev)
-        if (b, d) != (bs, D):
-            raise ValueError(f"{name} pool has blocks of {b} rows of {d}, expected {bs} rows of {D}")
-        if table.dim() != 2:
-            raise ValueError(f"{name} table must be [R,cols]")
-        _need(table, f"{name} table", (R, table.shape[1]), torch.int32, dev)
-        args += [_ptr(pool), _ptr(sc), _ptr(table), nblocks, table.shape[1]]
+    args = (*_cache_args("raw", raw, R, bs, D, dev), *_cache_args("comp", comp, R, bs, D, dev))
     out = torch.empty_like(q) if out is None else out
-    lse = torch.empty(N, H, dtype=torch.float32, device=dev) if lse is None else lse
-    _need(out, "out", (N, H, D), q.dtype, dev)
-    _need(lse, "lse", (N, H), torch.float32, dev)
-    if ws is None:
-        n = lib.hca_cache_attn_workspace_size(N, R, H, D, dt)
-        if n == 0:
-            raise HCAError(8, "hca_cache_attn_workspace_size")
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    with _on(dev):
-        rc = lib.hca_cache_attn(_ptr(q), _ptr(start), _ptr(held), *args, _ptr(out), _ptr(lse), N, R, H, D, min(W, 1 << 30),
-                                m, bs,
-                                float(scale), dt, _ptr(ws), ws.numel(), _stream(dev))
-    _check(rc, "hca_cache_attn")
+    lse = torch.empty((N, H), dtype=_F32, device=dev) if lse is None else lse
+    ws = torch.empty(_attn_ws_bytes(N, R, H, D, dt), dtype=torch.uint8, device=dev) if ws is None else ws
+    rc = _enqueue(dev, lib.hca_cache_attn, _fits(q, "q", (N, H, D), q.dtype, dev), _fits(start, "start", (R + 1,), _I32, dev),
+                  _fits(held, "held", (R,), _I32, dev), *args, _fits(out, "out", (N, H, D), q.dtype, dev),
+                  _fits(lse, "lse", (N, H), _F32, dev), N, R, H, D, min(W, 1 << 30), m, bs, scale, dt, ws.data_ptr(),
+                  ws.numel())
+    if rc != 0:
+        _check(rc, "hca_cache_attn")
     if check:
         _check(hca_workspace_status(ws), "hca_cache_attn (device)")
     return out, lse
