@@ -114,7 +114,7 @@ struct SimtShared {
   float pr[kTileKeys][kSimtCols];     // probabilities times the block's scale
   float red[4][kSimtCols];
   float m[kSimtCols], f[kSimtCols], l[kSimtCols];
-  const uint8_t *rows[8];             // the tile's pages (NULL: none or a bad block id)
+  const uint8_t *rows[8];             // the tile's pages (NULL: none, or a bad block id or scale)
   float scale[8];
   int key0[8], kind[8];               // kind 0 raw, 1 compressed, 2 no page
   int first;
@@ -184,9 +184,10 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
           sh.kind[tid] = comp;
           sh.key0[tid] = page << p.log_bs;
           const int id = s.table[(size_t)g.r * s.cols + page % s.cols];
-          if (id >= 0 && id < s.nblocks) {
+          const float sc = id >= 0 && id < s.nblocks ? s.scale[id] : 0.f;
+          if (sc > 0.f && sc < INFINITY) {
             sh.rows[tid] = s.pool + ((size_t)id << p.log_bs) * p.D;
-            sh.scale[tid] = s.scale[id];
+            sh.scale[tid] = sc;
           } else {
             p.err[blockIdx.x] = HCA_ERR_CACHE;
           }
@@ -309,21 +310,36 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
 // combine: out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i over a group's parts,
 // and the call's status from its CTAs'
 // ---------------------------------------------------------------------------
-constexpr int kCombineWarps = 8;
+constexpr int kCombineWarps = 8, kCombineThreads = 32 * kCombineWarps;
+constexpr int kMaxBorders = 640;
 
-// Block (c, y): the group that begins in CTA c's range and ends behind it,
-// columns [y, y + 1) * kCombineWarps / wpc.  wpc warps share a column's parts:
-// one where groups have a few parts each, more where one has many (few rows over
-// a long cache), as a warp keeps only a few rows in flight.
+// Warps that share a column's parts: one where a group has a few, more where it
+// has many (few rows over a long cache), as a warp keeps only a few rows in
+// flight.
+__device__ __forceinline__ int warps_per_column(int parts) { return parts >= 32 ? 8 : parts >= 16 ? 4 : parts >= 8 ? 2 : 1; }
+
+// The joins are listed by every block (the borders' records are a few hundred),
+// an item is kCombineWarps / warps_per_column columns of one of them.
 template <typename T>
-__global__ void __launch_bounds__(32 * kCombineWarps) hca_cache_combine_kernel(const AttnParams p, int wpc) {
+__global__ void __launch_bounds__(kCombineThreads) hca_cache_combine_kernel(const AttnParams p) {
   __shared__ float4 acc[kCombineWarps][64];
+  __shared__ int before[kMaxBorders + 1];
+  __shared__ long long tmp[33];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Border g = p.border[blockIdx.x];
-  int worst = HCA_OK;
-  for (int i = tid; i < p.grid; i += blockDim.x) worst = max(worst, p.err[i] == HCA_ERR_TIMEOUT ? 1000 : p.err[i]);
+  const int per = (p.grid + kCombineThreads - 1) / kCombineThreads, i0 = tid * per, i1 = min(i0 + per, p.grid);
+  int worst = HCA_OK, items = 0;
+  for (int i = i0; i < i1; ++i) {
+    const Border g = p.border[i];
+    const int e = p.err[i];
+    before[i] = items;
+    if (g.columns > 0) items += (g.columns * warps_per_column(g.parts) + kCombineWarps - 1) / kCombineWarps;
+    worst = max(worst, e == HCA_ERR_TIMEOUT ? 1000 : e);
+  }
+  long long total;
+  const int base = (int)block_scan(items, tmp, total);
+  for (int i = i0; i < i1; ++i) before[i] += base;
   const bool late = __syncthreads_or(worst == 1000);
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
+  if (blockIdx.x == 0) {
     const bool bad = __syncthreads_or(worst != HCA_OK);
     if (tid == 0) p.hdr->status = late ? HCA_ERR_TIMEOUT : bad ? HCA_ERR_CACHE : HCA_OK;
   }
@@ -331,62 +347,71 @@ __global__ void __launch_bounds__(32 * kCombineWarps) hca_cache_combine_kernel(c
     poison<T>(p);
     return;
   }
-  const int c = blockIdx.y * (kCombineWarps / wpc) + warp / wpc, sub = warp % wpc;
-  const bool mine = c < g.columns;
-  if (wpc == 1 && !mine) return;
-  const int n = mine ? g.parts : 0;
-  auto slot = [&](int i) { return (size_t)(i == 0 ? g.slot : 2 * (blockIdx.x + i)); };
-  float M = -INFINITY, L = 0.f;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_ml[slot(i) * p.NQ + c].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const int v4 = p.D / 4;  // float4 of a row, at most 64
-  float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float w = 0.f;
-    if (i0 + lane < n) {
-      const float2 ml = p.part_ml[slot(i0 + lane) * p.NQ + c];
-      if (ml.y != 0.f) {  // 0: a part in which the column saw no key
-        w = exp2f(ml.x - M);
-        L += w * ml.y;
-      }
+  for (int item = blockIdx.x; item < total; item += gridDim.x) {
+    int lo = 0, hi = p.grid;  // before[lo] <= item < before[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] <= item) lo = mid; else hi = mid;
     }
-    const int k1 = min(32, n - i0);
-#pragma unroll 4
-    for (int k = sub; k < k1; k += wpc) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      const float4 *o = reinterpret_cast<const float4 *>(p.part_o + (slot(i0 + k) * p.NQ + c) * p.D);
+    const Border g = p.border[lo];
+    const int wpc = warps_per_column(g.parts);
+    const int c = (item - before[lo]) * (kCombineWarps / wpc) + warp / wpc, sub = warp % wpc;
+    const int n = c < g.columns ? g.parts : 0;
+    auto slot = [&](int i) { return (size_t)(i == 0 ? g.slot : 2 * (lo + i)); };
+    float M = -INFINITY, L = 0.f;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_ml[slot(i) * p.NQ + c].x);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (lane + 32 * x < v4 && wk != 0.f) {
-          const float4 v = o[lane + 32 * x];
-          s[x].x = fmaf(wk, v.x, s[x].x); s[x].y = fmaf(wk, v.y, s[x].y);
-          s[x].z = fmaf(wk, v.z, s[x].z); s[x].w = fmaf(wk, v.w, s[x].w);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int b = 0; b < n; b += 32) {
+      float w = 0.f;
+      if (b + lane < n) {
+        const float2 ml = p.part_ml[slot(b + lane) * p.NQ + c];
+        if (ml.y != 0.f) {  // 0: a part in which the column saw no key
+          w = exp2f(ml.x - M);
+          L += w * ml.y;
+        }
+      }
+      const int k1 = min(32, n - b);
+#pragma unroll 4
+      for (int k = sub; k < k1; k += wpc) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const float4 *o = reinterpret_cast<const float4 *>(p.part_o + (slot(b + k) * p.NQ + c) * p.D);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (lane + 32 * x < v4 && wk != 0.f) {
+            const float4 v = o[lane + 32 * x];
+            s[x].x = fmaf(wk, v.x, s[x].x); s[x].y = fmaf(wk, v.y, s[x].y);
+            s[x].z = fmaf(wk, v.z, s[x].z); s[x].w = fmaf(wk, v.w, s[x].w);
+          }
         }
       }
     }
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  if (wpc > 1) {
-    acc[warp][lane] = s[0];
-    acc[warp][32 + lane] = s[1];
-    __syncthreads();
-    if (!mine || sub != 0) return;
-    for (int w = 1; w < wpc; ++w) {
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (wpc > 1) {  // the same for the whole block
+      __syncthreads();
+      acc[warp][lane] = s[0];
+      acc[warp][32 + lane] = s[1];
+      __syncthreads();
+      for (int w = 1; sub == 0 && w < wpc; ++w) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float4 u = acc[warp + w][lane + 32 * x];
-        s[x].x += u.x; s[x].y += u.y; s[x].z += u.z; s[x].w += u.w;
+        for (int x = 0; x < 2; ++x) {
+          const float4 u = acc[warp + w][lane + 32 * x];
+          s[x].x += u.x; s[x].y += u.y; s[x].z += u.z; s[x].w += u.w;
+        }
       }
     }
-  }
-  const float inv = 1.f / L;
-  const size_t row = (size_t)g.row + c;
+    if (n > 0 && sub == 0) {
+      const float inv = 1.f / L;
+      const size_t row = (size_t)g.row + c;
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
-    if (lane + 32 * x < v4) put4(static_cast<T *>(p.out) + row * p.D + 4 * (lane + 32 * x), s[x], inv);
-  if (lane == 0) p.lse[row] = (M + log2f(L)) * 0.69314718055994531f;
+      for (int x = 0; x < 2; ++x)
+        if (lane + 32 * x < v4) put4(static_cast<T *>(p.out) + row * p.D + 4 * (lane + 32 * x), s[x], inv);
+      if (lane == 0) p.lse[row] = (M + log2f(L)) * 0.69314718055994531f;
+    }
+  }
 }
 
 // Columns of a group for H heads: enough for one position's slice of heads, and
@@ -399,7 +424,7 @@ int pick_columns(int N, int R, int H, int dtype) {
   const int slices = (H + 127) / 128, HS = (H + slices - 1) / slices;
   const int T = R > 0 ? (N + R - 1) / R : 1;
   const long long want = (long long)HS * T;
-  return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
+  return want <= 32 ? 32 : want <= 64 ? 64 : 128;
 }
 
 struct Layout {
@@ -418,7 +443,7 @@ Layout layout_of(int N, int R, int H, int D, int dtype) {
   l.P = l.slices == 1 ? l.NQ / l.HS : 1;
   // a request's last chunk may be short, and a chunk has at least one token
   l.gmax = std::min((size_t)N / l.P + R, (size_t)N) * l.slices;
-  l.ctas = max_ctas(l.NQ, on_tensor_cores(dtype));
+  l.ctas = max_ctas(on_tensor_cores(dtype));
   const size_t slots = 2 * (size_t)l.ctas;
   size_t at = kHeaderBytes;
   l.off_gbase = at;
@@ -465,9 +490,9 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
   const int sms = tc::sm_count();
   if (sms <= 0) return cudaErrorNoDevice;
   const bool tcs = on_tensor_cores(a.dtype);
-  p.grid = std::min((tcs ? tc_cache_ctas(l.NQ) : 4) * sms, l.ctas);
+  p.grid = std::min((tcs ? tc_cache_ctas() : 4) * sms, l.ctas);
   p.min_tiles = tcs ? 2 : 1;
-  const int threads = tcs ? tc_cache_threads(l.NQ) : 0;
+  const int threads = tcs ? tc_cache_threads() : 0;
   p.in_cta = l.slices == 1 && a.R <= threads && l.gmax <= (size_t)threads;
   if (!p.in_cta) {
     ProfScope prof(kKCacheSched, st);
@@ -485,12 +510,8 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
   }
   {
     ProfScope prof(kKCacheCombine, st);
-    // parts of a group, if the groups were alike: 4 for each warp of a column
-    const size_t parts = p.grid / std::max<size_t>(1, l.gmax);
-    const int wpc = parts >= 32 ? 8 : parts >= 16 ? 4 : parts >= 8 ? 2 : 1;
-    const dim3 grid(p.grid, (std::min(p.NQ, p.P * p.HS) * wpc + kCombineWarps - 1) / kCombineWarps);
-    if (a.dtype == HCA_F32) hca_cache_combine_kernel<float><<<grid, 32 * kCombineWarps, 0, st>>>(p, wpc);
-    else hca_cache_combine_kernel<__nv_bfloat16><<<grid, 32 * kCombineWarps, 0, st>>>(p, wpc);
+    if (a.dtype == HCA_F32) hca_cache_combine_kernel<float><<<2 * sms, kCombineThreads, 0, st>>>(p);
+    else hca_cache_combine_kernel<__nv_bfloat16><<<2 * sms, kCombineThreads, 0, st>>>(p);
   }
   return cudaGetLastError();
 }

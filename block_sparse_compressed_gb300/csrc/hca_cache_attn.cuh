@@ -7,7 +7,7 @@ namespace hca {
 namespace cache {
 
 // CTAs of a launch, at most (the workspace holds two partial results for each)
-inline int max_ctas(int NQ, bool tensor_cores) { return !tensor_cores ? 640 : NQ == 128 ? 160 : 320; }
+inline int max_ctas(bool tensor_cores) { return tensor_cores ? 320 : 640; }
 constexpr int kSimtCols = 16;   // columns of an fp32 group
 
 struct AttnParams {
@@ -89,8 +89,8 @@ __device__ __forceinline__ bool chunk_group(const AttnParams &p, int r, int k, G
 }
 
 // tensor-core kernel (hca_cache_attn_tc.cu)
-int tc_cache_ctas(int NQ);     // CTAs per SM
-int tc_cache_threads(int NQ);  // threads of a CTA
+int tc_cache_ctas();     // CTAs per SM
+int tc_cache_threads();  // threads of a CTA
 cudaError_t tc_cache_attn(const AttnParams &p, cudaStream_t st);
 
 }  // namespace cache

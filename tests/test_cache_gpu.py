@@ -435,6 +435,18 @@ def test_a_bad_block_id_is_reported(dtype, bad):
     assert call()[0] == 0
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bad", [0.0, -1.0, float("inf"), float("nan")])
+def test_a_bad_scale_is_reported(dtype, bad):
+    call, start, h, raw, c = _status_case(dtype)
+    good = call()
+    scale = c[1].clone()
+    scale[int(c[2][0, 3])] = bad
+    st, out, lse = call(c=(c[0], scale, c[2]))
+    assert st == E_CACHE and bool(torch.isnan(out[0]).all()) and bool(torch.isnan(lse[0]).all())
+    assert torch.equal(out[1:], good[1][1:]) and torch.equal(lse[1:], good[2][1:])
+
+
 def test_attention_without_tokens():
     q, start, h, raw, c = attn_case([5, 9], [0, 0], 16, 64, 32, 4, 16, BF16, 2)
     out, lse = hca.hca_cache_attn(q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), 32, 4, 0.1, check=True)
