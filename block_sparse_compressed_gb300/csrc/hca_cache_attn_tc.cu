@@ -48,7 +48,7 @@ constexpr int kThreads = 3 * kWG;  // softmax | converter | page and MMA warp
 // Registers: 2 CTAs of 384 threads leave 80 each; the softmax holds 64 scores.
 constexpr int kRegsSoft = 136, kRegsConv = 64, kRegsIssue = 40;
 static_assert(kRegsSoft + kRegsConv + kRegsIssue <= 3 * 80, "register split must fit the launch");
-constexpr int kTmem = 256;      // S (P takes its first half) | O
+constexpr int kTmem = 256;      // S of keys 0 .. 63 | S of keys 64 .. 127 (P takes the first half of each) | O
 constexpr uint32_t kColO = 128;
 
 template <int NQ, int D>
@@ -77,10 +77,11 @@ template <int NQ, int D>
 struct Shared {
   uint64_t meta_full[kMetaStages], meta_empty[kMetaStages];
   uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t q_full, s_full, p_full[2], pv_done[2], drain, never;
+  uint64_t q_full, s_full[2], p_full[2], pv_done[2], drain, never;
   PageMeta meta[kMetaStages][8];
   uint32_t nan_keys[kMetaStages][4];  // keys whose rows hold a NaN that not everybody sees
   int nan_any[kMetaStages];
+  int all_seen[kMetaStages];          // bit h: every row sees every key of half h
   float amax[4];
   // the CTA's pieces of groups, in order (more than there is room for: read
   // from the schedule kernel's groups)
@@ -134,8 +135,8 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       mbar_init(&sh.kv_empty[s], 1);
     }
     mbar_init(&sh.q_full, C::kActive);
-    mbar_init(&sh.s_full, 1);
     for (int h = 0; h < 2; ++h) {
+      mbar_init(&sh.s_full[h], 1);
       mbar_init(&sh.p_full[h], C::kActive);
       mbar_init(&sh.pv_done[h], 1);
     }
@@ -252,6 +253,8 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
               atomicExch(status, HCA_ERR_CACHE);
             }
           }
+          const uint32_t seen = __ballot_sync(0xffffffffu, pm.kind == kAllSeen);
+          const uint32_t half = (1u << (ppt > 1 ? ppt / 2 : 1)) - 1u;  // pages of a half (one page has both)
           const int jn = min(batch, g.j1 - jb);
           for (int t = 0; t < jn; ++t, ++n) {
             const int ms = n % kMetaStages;
@@ -265,7 +268,11 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
               sh.meta[ms][lane % ppt] = pm;
             }
             if (lane < 4) sh.nan_keys[ms][lane] = 0;
-            if (lane == 0) sh.nan_any[ms] = 0;
+            if (lane == 0) {
+              const uint32_t a = seen >> (t * ppt), b = ppt > 1 ? a >> (ppt / 2) : a;
+              sh.nan_any[ms] = 0;
+              sh.all_seen[ms] = ((a & half) == half ? 1 : 0) | ((b & half) == half ? 2 : 0);
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.meta_full[ms]);
           }
@@ -274,37 +281,47 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       }
     } else if (warp == 9 && busy) {
       // ------------------------------------------------------------ MMA
-      // One thread's products run in order, so S of tile n + 1 may be issued
-      // right behind the O product of tile n that reads P from S's columns.
+      // Half-block (n, h) is keys 64 h .. 64 h + 63 of tile n.  S of (n + 1, h)
+      // is issued right behind the O product of (n, h), which reads P from the
+      // same columns: one thread's products run in order, and while the softmax
+      // works on one half the other's scores are made.
       const uint32_t kv0 = smem_u32(smem), q0 = smem_u32(smem + C::kOffQ);
       const uint64_t dk = smem_desc_sw128(kv0, 16, 1024);        // K view of stage 0
       const uint64_t dv = smem_desc_sw128(kv0, kHalfTile, 1024);  // V view of stage 0
       const uint64_t dq = smem_desc_sw128(NQ <= 64 ? q0 - base * 128 : q0, 16, 1024);
-      const uint32_t id_s = idesc_f16_f32(128, 128, false, false), id_o = idesc_f16_f32(128, D, false, true);
+      const uint32_t id_s = idesc_f16_f32(128, 64, false, false), id_o = idesc_f16_f32(128, D, false, true);
       uint32_t n = 0, nseg = 0;
       bool ok = true, issued = false;
       if (p.stall) {
         injected_stall(&sh.never, abort_flag, status, p.wait_ns);
         ok = false;
       }
+      auto issue_s = [&](uint32_t n, int h) {
+        const uint64_t b = dk + desc_bytes((n % kStages) * C::kStageBytes + h * 8192);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + h * 64, dq + desc_bytes((kk >> 2) * C::kQHalf + (kk & 3) * 32), b + kmaj_step(kk), id_s, kk > 0);
+          mma_commit(&sh.s_full[h]);
+        }
+        __syncwarp();
+        issued = true;
+      };
       for (; ok; ++nseg) {
         const Segment seg = segment(nseg);
         for (int j = seg.j0; ok && j < seg.j1; ++j, ++n) {
           const uint32_t st = n % kStages;
-          if (j == seg.j0) ok = wait_warp(&sh.q_full, nseg & 1, abort_flag, status, p.wait_ns);
-          if (ok) ok = wait_warp(&sh.kv_full[st], (n / kStages) & 1, abort_flag, status, p.wait_ns);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t b = dk + desc_bytes(st * C::kStageBytes);
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_ss(tmem, dq + desc_bytes((kk >> 2) * C::kQHalf + (kk & 3) * 32), b + kmaj_step(kk), id_s, kk > 0);
-            mma_commit(&sh.s_full);
+          if (j == seg.j0) {
+            // a group's q is written after the last softmax of the group before
+            ok = wait_warp(&sh.q_full, nseg & 1, abort_flag, status, p.wait_ns) &&
+                 wait_warp(&sh.kv_full[st], (n / kStages) & 1, abort_flag, status, p.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(n, 0);
+            issue_s(n, 1);
           }
-          __syncwarp();
-          issued = true;
           const uint64_t bv = dv + desc_bytes(st * C::kStageBytes);
+          const bool more = j + 1 < seg.j1;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             ok = wait_warp(&sh.p_full[h], n & 1, abort_flag, status, p.wait_ns);
@@ -313,11 +330,17 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             if (elect_one()) {
 #pragma unroll
               for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                mma_ts(tmem + kColO, tmem + kk * 8, bv + mnmaj_step(kk), id_o, j > seg.j0 || kk > 0);
+                mma_ts(tmem + kColO, tmem + h * 64 + (kk & 3) * 8, bv + mnmaj_step(kk), id_o, j > seg.j0 || kk > 0);
               mma_commit(&sh.pv_done[h]);
               if (h == 1) mma_commit(&sh.kv_empty[st]);
             }
             __syncwarp();
+            if (more) {
+              if (h == 0) ok = wait_warp(&sh.kv_full[(n + 1) % kStages], ((n + 1) / kStages) & 1, abort_flag, status, p.wait_ns);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(n + 1, h);
+            }
           }
         }
         if (seg.last()) break;
@@ -359,27 +382,27 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       ok = load(0);
       for (int k = 0; ok; ++k) {
         const Segment g = segment(k);
+        // keys that some row and that every row sees
+        const int last = g.pos0 + g.npos - 1, raw_any = g.pos0 - p.W + 1, raw_all = last - p.W + 1;
+        const int ent_any = (last + 1) / p.m, ent_all = (g.pos0 + 1) / p.m;
         for (int j = g.j0; ok && j < g.j1; ++j, ++n) {
           const int ms = n % kMetaStages, st = n % kStages;
-          bool plain = true;
-          for (int pgi = 0; pgi < ppt; ++pgi) plain = plain && sh.meta[ms][pgi].kind == kAllSeen;
-          if (!plain) {
+          if (sh.all_seen[ms] != 3) {
             // rows that nobody sees, or some only
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
               const int row = row0 + i * kRowStep;
               const PageMeta &pm = sh.meta[ms][row >> p.log_bs];
-              const int kind = pm.kind;
-              int ca = 0, cb = kind == kAllSeen ? g.npos : 0;
-              if (kind < kNoPage) key_columns(kind == kComp, (long long)pm.key0 + (row & bs_mask), g.pos0, g.npos, 1, p.W, p.m, ca, cb);
-              const bool some = cb > ca && cb - ca < g.npos;
-              bool nan = some && nan_bytes(raw[i]) != 0;
-              if (kind < kNoPage && !pm.rows) nan = true;  // a bad block id
+              const int kind = pm.kind, key = pm.key0 + (row & bs_mask);
+              const bool seen = kind == kAllSeen || (kind == kRaw && key >= raw_any && key <= last) || (kind == kComp && key < ent_any);
+              const bool all = kind == kAllSeen || (kind == kRaw && key >= raw_all && key <= g.pos0) || (kind == kComp && key < ent_all);
+              bool nan = kind < kNoPage && !pm.rows;  // a bad block id
+              if (__any_sync(0xffffffffu, seen && !all)) nan = nan || (seen && !all && nan_bytes(raw[i]) != 0);
               // a row's pieces are in kPer neighbouring lanes
               const uint32_t grp = ((1u << kPer) - 1u) << (lane & ~(kPer - 1));
               nan = (__ballot_sync(0xffffffffu, nan) & grp) != 0;
-              if (cb <= ca || nan) raw[i] = make_uint4(0, 0, 0, 0);
-              if (nan && cb > ca && ch == 0) {
+              if (!seen || nan) raw[i] = make_uint4(0, 0, 0, 0);
+              if (nan && seen && ch == 0) {
                 atomicOr(&sh.nan_keys[ms][row >> 5], 1u << (row & 31));
                 sh.nan_any[ms] = 1;
               }
@@ -497,36 +520,34 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           const int ms = n % kMetaStages;
           const PageMeta *meta = sh.meta[ms];
           (void)wait(&sh.kv_full[n % kStages], (n / kStages) & 1);  // for the pages' data and the converter's notes
-          (void)wait(&sh.s_full, n & 1);
-          tc_fence_after();
           const bool odd_rows = sh.nan_any[ms] != 0;
+          const int all_seen = sh.all_seen[ms];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            (void)wait(&sh.s_full[h], n & 1);
+            tc_fence_after();
             uint32_t sv[64];
             tmem_ld32(lane_addr + h * 64, *reinterpret_cast<uint32_t(*)[32]>(sv));
             tmem_ld32(lane_addr + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
             // visible columns of this half
             uint64_t vis = ~0ull;
-            bool plain = true;
-            {
+            if (!((all_seen >> h) & 1)) {
+              vis = 0;
               const int per_half = p.log_bs == 7 ? 1 : 64 >> p.log_bs, p0 = p.log_bs == 7 ? 0 : h * per_half;
-              for (int x = 0; x < per_half; ++x) plain = plain && meta[p0 + x].kind == kAllSeen;
-              if (!plain) {
-                vis = 0;
-                for (int x = 0; x < per_half; ++x) {
-                  const int kind = meta[p0 + x].kind;
-                  const int first = p.log_bs == 7 ? h * 64 : 0, cnt = min(1 << p.log_bs, 64), at = x << p.log_bs;
-                  const int key = meta[p0 + x].key0 + first;  // key of column `at`
-                  // of columns [at, at + cnt): those with a visible key
-                  int a = 0, b = kind == kAllSeen ? cnt : 0;
-                  if (kind == kRaw) {
-                    a = max(raw_lo - key, 0);
-                    b = min(pos - key + 1, cnt);
-                  } else if (kind == kComp) {
-                    b = min(entries - key, cnt);
-                  }
-                  if (b > a) vis |= (b - a >= 64 ? ~0ull : ((1ull << (b - a)) - 1ull)) << (at + a);
+              const int skip = p.log_bs == 7 ? h * 64 : 0, cnt = min(1 << p.log_bs, 64);
+#pragma unroll 1
+              for (int x = 0; x < per_half; ++x) {
+                const int kind = meta[p0 + x].kind, at = x << p.log_bs;
+                const int key = meta[p0 + x].key0 + skip;  // key of column `at`
+                // of columns [at, at + cnt): those with a visible key
+                int a = 0, b = kind == kAllSeen ? cnt : 0;
+                if (kind == kRaw) {
+                  a = max(raw_lo - key, 0);
+                  b = min(pos - key + 1, cnt);
+                } else if (kind == kComp) {
+                  b = min(entries - key, cnt);
                 }
+                if (b > a) vis |= (b - a >= 64 ? ~0ull : ((1ull << (b - a)) - 1ull)) << (at + a);
               }
             }
             if (odd_rows) {
@@ -534,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
               if (bad & vis) l_run = __int_as_float(0x7fc00000);
             }
             tmem_wait_ld();
-            if (!__all_sync(0xffffffffu, vis == ~0ull)) {
+            if (!((all_seen >> h) & 1)) {
 #pragma unroll
               for (int c = 0; c < 64; ++c)
                 if (!((vis >> c) & 1)) sv[c] = 0xff800000u;
@@ -605,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
                 f32x2_split(fadd2(acc[0], acc[1]), a, b);
                 l_run = fmaf(a + b, meta[pgi[c4]].inv_scale, l_run);
               }
-              tmem_st16(lane_addr + h * 32 + c2 * 16, pk);
+              tmem_st16(lane_addr + h * 64 + c2 * 16, pk);
             }
             tmem_wait_st();
             tc_fence_before();
