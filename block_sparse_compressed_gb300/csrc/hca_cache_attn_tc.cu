@@ -2,8 +2,7 @@
 // (tcgen05 + TMEM), bf16 queries, D = 64 or 128.
 //
 // A CTA takes a range of the line of tiles (hca_cache.cuh).  A tile is 128 keys
-// of one group, a group up to NQ (position, head) rows of a request; they fill
-// the M = 128 rows of the products from `base` on:
+// of one group, a group NQ (position, head) rows of a request:
 //   S [128 x 128 keys]  = Q [128 x D] K^T       kind::f16, Q and K from shared memory
 //   O [128 x D]        += P [128 x 128 keys] K   kind::f16, P from tensor memory
 // With the rows in the lanes of tensor memory a softmax thread owns a row: its
@@ -11,6 +10,11 @@
 // threads.  (Keys in the lanes instead waste none of the M dimension on a single
 // token's 64 heads and can use the e4m3 rows as they are, but every maximum then
 // crosses 128 threads: 4,200 cycles a tile were measured, half of them there.)
+//
+// The products take 128 rows whatever NQ is, so a group of NQ = 64 (32) rows has
+// them in the lanes twice (four times), and each copy sees its own half
+// (quarter) of a tile's keys: P is zero for the others.  The copies are so many
+// independent streams of the online softmax, joined when the group ends.
 //
 // The cache's e4m3 values become fp16 on the way to shared memory, exactly, once
 // for both products and all rows: converter warps load pages of global memory
@@ -43,6 +47,7 @@ namespace {
 constexpr float kRaiseLog2 = 8.f;
 constexpr int kMetaStages = 4;  // tiles whose pages are looked up ahead
 constexpr int kStages = 2;      // fp16 tiles
+constexpr int kMaxSegs = 64;    // pieces of groups listed in shared memory
 constexpr int kWG = 128;
 constexpr int kThreads = 3 * kWG;  // softmax | converter | page and MMA warp
 // Registers: 2 CTAs of 384 threads leave 80 each; the softmax holds 64 scores.
@@ -53,15 +58,12 @@ constexpr uint32_t kColO = 128;
 
 template <int NQ, int D>
 struct Cfg {
-  static constexpr int kRowsQ = NQ <= 64 ? 64 : 128;       // rows of Q in shared memory
-  static constexpr int kHalves = D / 64;                   // 128-byte columns blocks of an fp16 row
-  static constexpr int kQHalf = kRowsQ * 128;
+  static constexpr int kCopies = 128 / NQ;                 // of a row in the lanes
+  static constexpr int kSpan = kCopies == 1 ? 64 : NQ;     // keys that a thread takes at a time: 64, 64, 32
+  static constexpr int kHalves = D / 64;                   // 128-byte column blocks of an fp16 row
   static constexpr int kStageBytes = kHalves * kHalfTile;  // fp16 tile of 128 keys
-  // With 64 rows of Q, the other 64 rows of its operand are whatever lies in
-  // front or behind: their results are not read.
   static constexpr int kOffQ = kStages * kStageBytes;
-  static constexpr int kSmem = kOffQ + kHalves * kQHalf + (NQ <= 64 ? 8192 : 0) + 1024;
-  static constexpr int kActive = NQ <= 32 ? 32 : NQ;       // softmax threads with a row
+  static constexpr int kSmem = kOffQ + kHalves * kHalfTile + 1024;
 };
 
 enum PageKind { kRaw = 0, kComp = 1, kNoPage = 2, kAllSeen = 3 };  // kAllSeen: every row sees every key
@@ -78,15 +80,18 @@ struct Shared {
   uint64_t meta_full[kMetaStages], meta_empty[kMetaStages];
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t q_full, s_full[2], p_full[2], pv_done[2], drain, never;
+  uint64_t scale_full[kMetaStages];
   PageMeta meta[kMetaStages][8];
   uint32_t nan_keys[kMetaStages][4];  // keys whose rows hold a NaN that not everybody sees
   int nan_any[kMetaStages];
   int all_seen[kMetaStages];          // bit h: every row sees every key of half h
   float amax[4];
-  // the CTA's pieces of groups, in order (more than there is room for: read
-  // from the schedule kernel's groups)
-  Segment seg[kThreads];
+  // the CTA's pieces of groups, in order; what there is no room for is in the
+  // workspace's groups
+  Segment seg[kMaxSegs];
   int gbase[kThreads];
+  float2 ml[kWG];                                // copies: reference and sum of every lane
+  float join[NQ < 128 ? (128 - NQ) * 17 : 1];    // copies: 16 columns of O of all lanes but the first copy's
   long long scan[33];
   uint32_t tmem_base;
   int abort, first;
@@ -128,16 +133,17 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
   if (tid == 0) {
     for (int s = 0; s < kMetaStages; ++s) {
       mbar_init(&sh.meta_full[s], 1);
-      mbar_init(&sh.meta_empty[s], C::kActive);  // the softmax is the last to read a tile's pages
+      mbar_init(&sh.scale_full[s], 1);
+      mbar_init(&sh.meta_empty[s], kWG);  // the softmax is the last to read a tile's pages
     }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sh.kv_full[s], kWG);
       mbar_init(&sh.kv_empty[s], 1);
     }
-    mbar_init(&sh.q_full, C::kActive);
+    mbar_init(&sh.q_full, kWG);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&sh.s_full[h], 1);
-      mbar_init(&sh.p_full[h], C::kActive);
+      mbar_init(&sh.p_full[h], kWG);
       mbar_init(&sh.pv_done[h], 1);
     }
     mbar_init(&sh.drain, 1);
@@ -152,35 +158,44 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
   // the CTA's range of the line, and its pieces of groups
   long long ntiles, quota, c0, c1;
   if (p.in_cta) {
-    // one thread per request, then one per group
+    // one thread per request; where some bring more than one group, one per group
     long long n = 0, all;
     bool ok = true;
     if (tid < p.R) ok = request_chunks(p, tid, n);
-    const long long before = block_scan(n, sh.scan, all);
-    if (tid < p.R) sh.gbase[tid] = (int)before;
-    ok = __syncthreads_and(ok);
     Group g;
     g.ntiles = 0;
-    const bool mine = ok && tid < all;
-    if (mine) {
-      int lo = 0, hi = p.R;  // gbase[lo] <= tid < gbase[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sh.gbase[mid] <= tid) lo = mid; else hi = mid;
+    bool mine = n == 1;
+    if (!__syncthreads_or(n > 1)) {
+      if (mine && ok) ok = chunk_group(p, tid, 0, g);
+    } else {
+      const long long before = block_scan(n, sh.scan, all);
+      if (tid < p.R) sh.gbase[tid] = (int)before;
+      ok = __syncthreads_and(ok);
+      mine = ok && tid < all;
+      if (mine) {
+        int lo = 0, hi = p.R;  // gbase[lo] <= tid < gbase[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (sh.gbase[mid] <= tid) lo = mid; else hi = mid;
+        }
+        ok = chunk_group(p, lo, tid - sh.gbase[lo], g);
       }
-      ok = chunk_group(p, lo, tid - sh.gbase[lo], g);
     }
-    g.tile0 = block_scan(g.ntiles, sh.scan, ntiles);
-    if (!__syncthreads_and(ok)) ntiles = -1;
+    // tiles before this group, and (in the upper bits) groups before it
+    const long long at = block_scan((mine ? g.ntiles : 0) | (mine ? 1ll << 44 : 0), sh.scan, all);
+    g.tile0 = at & ((1ll << 44) - 1);
+    const int index = (int)(at >> 44);
+    ntiles = __syncthreads_and(ok) ? all & ((1ll << 44) - 1) : -1;
     quota = cta_quota(ntiles, p.grid, p.min_tiles);
     c0 = quota * blockIdx.x;
     c1 = min(c0 + quota, ntiles);
     const bool in = mine && g.tile0 < c1 && g.tile0 + g.ntiles > c0;
-    if (in && g.tile0 <= c0) sh.first = tid;
+    if (in && g.tile0 <= c0) sh.first = index;
     __syncthreads();
     if (in) {
       const Segment x = segment_of(g, c0, c1, blockIdx.x);
-      sh.seg[tid - sh.first] = x;
+      if (index - sh.first < kMaxSegs) sh.seg[index - sh.first] = x;
+      else p.groups[index] = g;
       if (x.last()) p.border[blockIdx.x] = border_of(p, g, c0, c1, quota, blockIdx.x);
     }
   } else {
@@ -199,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       }
       __syncthreads();
       const int gi = sh.first + tid;
-      if (gi < ng) {
+      if (tid < kMaxSegs && gi < ng) {
         const Group g = p.groups[gi];
         if (g.tile0 < c1) sh.seg[tid] = segment_of(g, c0, c1, blockIdx.x);
       }
@@ -210,17 +225,12 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
     p.err[blockIdx.x] = ntiles < 0 ? HCA_ERR_CACHE : HCA_OK;
     if (!busy) p.border[blockIdx.x] = Border{0, 0, 0, 0};
   }
-  auto segment = [&](int k) { return k < kThreads ? sh.seg[k] : segment_of(p.groups[sh.first + k], c0, c1, blockIdx.x); };
+  auto segment = [&](int k) { return k < kMaxSegs ? sh.seg[k] : segment_of(p.groups[sh.first + k], c0, c1, blockIdx.x); };
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
   const int ppt = kTileKeys >> p.log_bs;  // pages per tile: a power of two, 1 .. 8
-  // The rows' place in the 128 lanes: the warp that may read a lane is fixed, so
-  // the two CTAs of an SM work in different lanes and their softmax warps on
-  // different schedulers where the rows leave room.
-  const int base = NQ == 128 ? 0 : NQ == 64 ? 64 * (2 * blockIdx.x >= gridDim.x) : 64 * (2 * blockIdx.x >= gridDim.x) + 32 * (blockIdx.x & 1);
-
   if (warp >= 8) {
     setmaxnreg_dec<kRegsIssue>();
     if (warp == 8 && busy) {
@@ -244,10 +254,9 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             const long long end = (long long)pm.key0 + (1 << p.log_bs);
             const bool all = comp ? end * p.m <= g.pos0 + 1 : end <= (long long)g.pos0 + 1 && pm.key0 > g.pos0 + g.npos - 1 - p.W;
             pm.kind = all ? kAllSeen : comp ? kComp : kRaw;
-            const float sc = id >= 0 && id < cs.nblocks ? cs.scale[id] : 0.f;
-            if (sc > 0.f && sc < INFINITY) {
+            if (id >= 0 && id < cs.nblocks) {
               pm.rows = cs.pool + (size_t)id * page_bytes;
-              pm.scale = sc;
+              pm.scale = cs.scale[id];
             } else {
               pm.kind = comp ? kComp : kRaw;  // every key of it is noted as NaN
               atomicExch(status, HCA_ERR_CACHE);
@@ -261,11 +270,13 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             if (n >= (uint32_t)kMetaStages)
               ok = wait_warp(&sh.meta_empty[ms], ((n / kMetaStages) - 1) & 1, abort_flag, status, p.wait_ns);
             if (!ok) break;
-            if (lane / ppt == t) {
+            const bool here = lane / ppt == t;
+            PageMeta &to = sh.meta[ms][lane % ppt];
+            if (here) {
               if (pm.rows) prefetch_l2(pm.rows, page_bytes);
-              pm.log2_scale = log2f(pm.scale);
-              pm.inv_scale = 1.f / pm.scale;
-              sh.meta[ms][lane % ppt] = pm;
+              to.rows = pm.rows;
+              to.key0 = pm.key0;
+              to.kind = pm.kind;
             }
             if (lane < 4) sh.nan_keys[ms][lane] = 0;
             if (lane == 0) {
@@ -275,21 +286,44 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.meta_full[ms]);
+            // the scales are needed later than the rows
+            if (here) {
+              if (!(pm.scale > 0.f && pm.scale < INFINITY)) {
+                pm.scale = 1.f;
+                atomicExch(status, HCA_ERR_CACHE);
+                for (int r = (lane % ppt) << p.log_bs, i = 0; i < 1 << p.log_bs; ++i, ++r)
+                  atomicOr(&sh.nan_keys[ms][r >> 5], 1u << (r & 31));
+                sh.nan_any[ms] = 1;
+              }
+              to.scale = pm.scale;
+              to.log2_scale = log2f(pm.scale);
+              to.inv_scale = 1.f / pm.scale;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.scale_full[ms]);
           }
+        }
+        if (!g.last() && lane == 0) {
+          // the next group's rows of q
+          const Segment gn = segment(k + 1);
+          prefetch_l2(static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)gn.row0 * p.H + gn.slice() * p.HS) * D,
+                      real_columns(p, gn.npos, gn.slice()) * D * 2);
         }
         if (g.last()) break;
       }
     } else if (warp == 9 && busy) {
       // ------------------------------------------------------------ MMA
-      // Half-block (n, h) is keys 64 h .. 64 h + 63 of tile n.  S of (n + 1, h)
-      // is issued right behind the O product of (n, h), which reads P from the
-      // same columns: one thread's products run in order, and while the softmax
-      // works on one half the other's scores are made.
+      // One thread's products run in order, so the S product that overwrites P is
+      // issued right behind the O product that reads it.  Without copies a tile
+      // goes in two halves of 64 keys, S of (n + 1, h) behind O of (n, h), so that
+      // the scores of one half are made while the softmax works on the other.
+      // With copies every thread works on its keys of the whole tile at once.
       const uint32_t kv0 = smem_u32(smem), q0 = smem_u32(smem + C::kOffQ);
       const uint64_t dk = smem_desc_sw128(kv0, 16, 1024);        // K view of stage 0
       const uint64_t dv = smem_desc_sw128(kv0, kHalfTile, 1024);  // V view of stage 0
-      const uint64_t dq = smem_desc_sw128(NQ <= 64 ? q0 - base * 128 : q0, 16, 1024);
-      const uint32_t id_s = idesc_f16_f32(128, 64, false, false), id_o = idesc_f16_f32(128, D, false, true);
+      const uint64_t dq = smem_desc_sw128(q0, 16, 1024);
+      constexpr int kParts = C::kCopies == 1 ? 2 : 1;  // of a tile
+      const uint32_t id_s = idesc_f16_f32(128, 128 / kParts, false, false), id_o = idesc_f16_f32(128, D, false, true);
       uint32_t n = 0, nseg = 0;
       bool ok = true, issued = false;
       if (p.stall) {
@@ -301,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + h * 64, dq + desc_bytes((kk >> 2) * C::kQHalf + (kk & 3) * 32), b + kmaj_step(kk), id_s, kk > 0);
+            mma_ss(tmem + h * 64, dq + kmaj_step(kk), b + kmaj_step(kk), id_s, kk > 0);
           mma_commit(&sh.s_full[h]);
         }
         __syncwarp();
@@ -317,22 +351,23 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
                  wait_warp(&sh.kv_full[st], (n / kStages) & 1, abort_flag, status, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
-            issue_s(n, 0);
-            issue_s(n, 1);
+            for (int h = 0; h < kParts; ++h) issue_s(n, h);
           }
           const uint64_t bv = dv + desc_bytes(st * C::kStageBytes);
           const bool more = j + 1 < seg.j1;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < kParts; ++h) {
             ok = wait_warp(&sh.p_full[h], n & 1, abort_flag, status, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-              for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                mma_ts(tmem + kColO, tmem + h * 64 + (kk & 3) * 8, bv + mnmaj_step(kk), id_o, j > seg.j0 || kk > 0);
+              for (int k1 = 0; k1 < 8 / kParts; ++k1) {
+                const int kk = h * 4 + k1;
+                mma_ts(tmem + kColO, tmem + h * 64 + k1 * 8, bv + mnmaj_step(kk), id_o, j > seg.j0 || kk > 0);
+              }
               mma_commit(&sh.pv_done[h]);
-              if (h == 1) mma_commit(&sh.kv_empty[st]);
+              if (h == kParts - 1) mma_commit(&sh.kv_empty[st]);
             }
             __syncwarp();
             if (more) {
@@ -438,7 +473,6 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
     }
   } else {
     setmaxnreg_inc<kRegsSoft>();
-    const int row = tid - base;  // row of the group
     if (ntiles < 0) {
       // the schedule was refused
       const size_t rows = (size_t)p.N * p.H;
@@ -447,60 +481,62 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         reinterpret_cast<uint4 *>(p.out)[i] = nan4;
       for (size_t i = (size_t)blockIdx.x * kWG + tid; i < rows; i += (size_t)gridDim.x * kWG)
         p.lse[i] = __int_as_float(0x7fc00000);
-    } else if (busy && row >= 0 && row < C::kActive) {
+    } else if (busy) {
       // ------------------------------------------------------------ softmax
-      // Rows beyond the group's repeat row 0 of Q's memory or a zero row: their
-      // results are not written.
+      // Rows beyond the group's are zero in Q: their results are not written.
+      constexpr int kSpan = C::kSpan;
+      const int row = tid % NQ, copy = tid / NQ;  // row of the group
       const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
-      const int w0 = base >> 5;
       auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, abort_flag, status, p.wait_ns); };
 
       // q of a group into shared memory; returns log2(e) * |scale| / (its factor)
       auto load_q = [&](const Segment &g) {
-        constexpr int kUnits = C::kRowsQ * D / 16;  // 16 values each; rows >= nreal are zero
-        constexpr int kMine = kUnits / C::kActive;
+        constexpr int kUnits = NQ * D / 16;  // 16 values each
+        constexpr int kMine = (kUnits + kWG - 1) / kWG;
         const int nreal = real_columns(p, g.npos, g.slice());
         const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
                                                           ((size_t)g.row0 * p.H + g.slice() * p.HS) * D);
-        float amax = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < kMine; ++k) {
-          const int i = row + k * C::kActive;
-          if (i / (D / 16) < nreal) {
-            const uint4 u0 = q[2 * i], u1 = q[2 * i + 1];
-            const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+        uint4 u[kMine][2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float a = fabsf(__uint_as_float(w[e] << 16)), b = fabsf(__uint_as_float(w[e] & 0xffff0000u));
-              if (a < INFINITY) amax = fmaxf(amax, a);
-              if (b < INFINITY) amax = fmaxf(amax, b);
-            }
+        for (int k = 0; k < kMine; ++k) {
+          const int i = tid + k * kWG;
+          u[k][0] = u[k][1] = make_uint4(0, 0, 0, 0);
+          if (i / (D / 16) < nreal) u[k][0] = q[2 * i], u[k][1] = q[2 * i + 1];
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) {
+          const uint32_t w[8] = {u[k][0].x, u[k][0].y, u[k][0].z, u[k][0].w, u[k][1].x, u[k][1].y, u[k][1].z, u[k][1].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float a = fabsf(__uint_as_float(w[e] << 16)), b = fabsf(__uint_as_float(w[e] & 0xffff0000u));
+            if (a < INFINITY) amax = fmaxf(amax, a);
+            if (b < INFINITY) amax = fmaxf(amax, b);
           }
         }
         const int wm = __reduce_max_sync(0xffffffffu, __float_as_int(amax));
         if (lane == 0) sh.amax[warp] = __int_as_float(wm);
-        if (C::kActive > 32) named_bar_sync(1, C::kActive);
-        else __syncwarp();
-        amax = sh.amax[w0];
-#pragma unroll
-        for (int w = 1; w < C::kActive / 32; ++w) amax = fmaxf(amax, sh.amax[w0 + w]);
+        named_bar_sync(1, kWG);
+        amax = fmaxf(fmaxf(sh.amax[0], sh.amax[1]), fmaxf(sh.amax[2], sh.amax[3]));
         // the largest |q| becomes 224 .. 448; a negative scale goes into q's sign
         const float s = exp2_int(scale_exponent(amax)), inv = p.scale < 0.f ? -1.f / s : p.scale > 0.f ? 1.f / s : 0.f;
         const uint32_t dst = smem_u32(smem) + C::kOffQ;
-#pragma unroll 2
+#pragma unroll
         for (int k = 0; k < kMine; ++k) {
-          const int i = row + k * C::kActive, c = i / (D / 16), ch = i % (D / 16);
-          uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-          if (c < nreal) u0 = q[2 * i], u1 = q[2 * i + 1];
-          const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+          const int i = tid + k * kWG, c = i / (D / 16), ch = i % (D / 16);
+          if (kUnits % kWG != 0 && c >= NQ) break;
+          const uint32_t w[8] = {u[k][0].x, u[k][0].y, u[k][0].z, u[k][0].w, u[k][1].x, u[k][1].y, u[k][1].z, u[k][1].w};
           uint32_t f[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             f[e] = f16x2_rn(__uint_as_float(w[e] << 16) * inv, __uint_as_float(w[e] & 0xffff0000u) * inv);
-          const uint32_t at = dst + (ch >> 2) * C::kQHalf + c * 128;
           const int c2 = 2 * (ch & 3), x = c & 7;
-          st_shared(at + ((c2 ^ x) << 4), f[0], f[1], f[2], f[3]);
-          st_shared(at + (((c2 + 1) ^ x) << 4), f[4], f[5], f[6], f[7]);
+#pragma unroll
+          for (int y = 0; y < C::kCopies; ++y) {
+            const uint32_t at = dst + (ch >> 2) * kHalfTile + (c + y * NQ) * 128;
+            st_shared(at + ((c2 ^ x) << 4), f[0], f[1], f[2], f[3]);
+            st_shared(at + (((c2 + 1) ^ x) << 4), f[4], f[5], f[6], f[7]);
+          }
         }
         fence_async_smem();
         mbar_arrive(&sh.q_full);
@@ -519,26 +555,29 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         for (int j = g.j0; j < g.j1; ++j, ++n) {
           const int ms = n % kMetaStages;
           const PageMeta *meta = sh.meta[ms];
+          (void)wait(&sh.scale_full[ms], (n / kMetaStages) & 1);
           (void)wait(&sh.kv_full[n % kStages], (n / kStages) & 1);  // for the pages' data and the converter's notes
           const bool odd_rows = sh.nan_any[ms] != 0;
           const int all_seen = sh.all_seen[ms];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < (C::kCopies == 1 ? 2 : 1); ++h) {
             (void)wait(&sh.s_full[h], n & 1);
             tc_fence_after();
-            uint32_t sv[64];
-            tmem_ld32(lane_addr + h * 64, *reinterpret_cast<uint32_t(*)[32]>(sv));
-            tmem_ld32(lane_addr + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
-            // visible columns of this half
+            const int k0 = C::kCopies == 1 ? h * 64 : copy * kSpan;  // first of the thread's keys, uniform in a warp
+            uint32_t sv[kSpan];
+#pragma unroll
+            for (int c = 0; c < kSpan; c += 32) tmem_ld32(lane_addr + k0 + c, *reinterpret_cast<uint32_t(*)[32]>(sv + c));
+            // which of them the row sees
+            const bool plain = (all_seen >> (k0 >> 6)) & 1;
             uint64_t vis = ~0ull;
-            if (!((all_seen >> h) & 1)) {
+            if (!plain) {
               vis = 0;
-              const int per_half = p.log_bs == 7 ? 1 : 64 >> p.log_bs, p0 = p.log_bs == 7 ? 0 : h * per_half;
-              const int skip = p.log_bs == 7 ? h * 64 : 0, cnt = min(1 << p.log_bs, 64);
+              const int bs = 1 << p.log_bs;
 #pragma unroll 1
-              for (int x = 0; x < per_half; ++x) {
-                const int kind = meta[p0 + x].kind, at = x << p.log_bs;
-                const int key = meta[p0 + x].key0 + skip;  // key of column `at`
+              for (int at = 0; at < kSpan; at += bs) {
+                const PageMeta &pm = meta[(k0 + at) >> p.log_bs];
+                const int skip = (k0 + at) & (bs - 1), cnt = min(bs, kSpan);
+                const int kind = pm.kind, key = pm.key0 + skip;  // key of column `at`
                 // of columns [at, at + cnt): those with a visible key
                 int a = 0, b = kind == kAllSeen ? cnt : 0;
                 if (kind == kRaw) {
@@ -551,21 +590,29 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
               }
             }
             if (odd_rows) {
-              const uint64_t bad = (uint64_t)sh.nan_keys[ms][2 * h] | (uint64_t)sh.nan_keys[ms][2 * h + 1] << 32;
+              const uint64_t bad = kSpan == 64 ? (uint64_t)sh.nan_keys[ms][k0 >> 5] | (uint64_t)sh.nan_keys[ms][(k0 >> 5) + 1] << 32
+                                               : (uint64_t)sh.nan_keys[ms][k0 >> 5];
               if (bad & vis) l_run = __int_as_float(0x7fc00000);
             }
             tmem_wait_ld();
-            if (!((all_seen >> h) & 1)) {
+            if (!plain) {
 #pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (!((vis >> c) & 1)) sv[c] = 0xff800000u;
+              for (int c = 0; c < kSpan; c += 32) {
+                const uint32_t v = (uint32_t)(vis >> c);
+                if (!__all_sync(0xffffffffu, v == 0xffffffffu)) {
+#pragma unroll
+                  for (int y = 0; y < 32; ++y)
+                    if (!((v >> y) & 1)) sv[c + y] = 0xff800000u;
+                }
+              }
             }
             // 16 columns at a time have one block scale
-            float ck[4], lb[4], mx = -INFINITY;
-            int pgi[4];
+            constexpr int kGroups = kSpan / 16;
+            float ck[kGroups], lb[kGroups], mx = -INFINITY;
+            int pgi[kGroups];
 #pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4) {
-              pgi[c4] = (h * 64 + c4 * 16) >> p.log_bs;
+            for (int c4 = 0; c4 < kGroups; ++c4) {
+              pgi[c4] = (k0 + c4 * 16) >> p.log_bs;
               ck[c4] = fmaxf(meta[pgi[c4]].scale * cs, FLT_MIN);  // positive: a masked score stays -inf
               lb[c4] = meta[pgi[c4]].log2_scale;
               float m0 = -INFINITY, m1 = -INFINITY;
@@ -590,9 +637,9 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             }
             const float m_use = m_run == -INFINITY ? 0.f : m_run;
             if (__any_sync(0xffffffffu, raise)) {
-              // O holds the sum up to the half before this one once that is done
-              const int ph = h ^ 1;
-              (void)wait(&sh.pv_done[ph], (h ? n : n - 1) & 1);
+              // O holds the sum up to the keys before these once that is done
+              constexpr int kLast = C::kCopies == 1 ? 1 : 0;
+              (void)wait(&sh.pv_done[h ? 0 : kLast], (h ? n : n - 1) & 1);
               tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < D; c += 16) {
@@ -604,8 +651,11 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
                 tmem_st16(lane_addr + kColO + c, o);
               }
             }
+            // P over the columns of S: those of half h, or (copies) the first 64,
+            // with zeros for the other copies' keys
+            const uint32_t pcol = lane_addr + (C::kCopies == 1 ? h * 64 : copy * (kSpan / 2));
 #pragma unroll
-            for (int c2 = 0; c2 < 2; ++c2) {
+            for (int c2 = 0; c2 < kSpan / 32; ++c2) {
               uint32_t pk[16];
 #pragma unroll
               for (int c1 = 0; c1 < 2; ++c1) {
@@ -626,7 +676,17 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
                 f32x2_split(fadd2(acc[0], acc[1]), a, b);
                 l_run = fmaf(a + b, meta[pgi[c4]].inv_scale, l_run);
               }
-              tmem_st16(lane_addr + h * 64 + c2 * 16, pk);
+              tmem_st16(pcol + c2 * 16, pk);
+            }
+            if constexpr (C::kCopies > 1) {
+              uint32_t zero[16];
+#pragma unroll
+              for (int y = 0; y < 16; ++y) zero[y] = 0;
+#pragma unroll
+              for (int y = 1; y < C::kCopies; ++y)
+#pragma unroll
+                for (int c = 0; c < kSpan / 2; c += 16)
+                  tmem_st16(lane_addr + (copy + y) % C::kCopies * (kSpan / 2) + c, zero);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -637,37 +697,66 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         // the next group's q: every product with this one's has been made
         if (!g.last()) cs = load_q(segment(k + 1));
         if (*abort_flag) l_run = __int_as_float(0x7fc00000);
-        const bool whole = g.slot < 0;
+        const bool whole = g.slot < 0, write = row < nreal && copy == 0;
         const size_t orow = (size_t)g.row0 * p.H + g.slice() * p.HS + row;  // rows of the group are rows of q and out in order
-        const bool write = row < nreal;
+        float weight = 1.f;
+        if constexpr (C::kCopies > 1) {
+          // the copies' common reference and sum
+          sh.ml[tid] = make_float2(m_run, l_run);
+          named_bar_sync(1, kWG);
+          float M = -INFINITY, L = 0.f;
+#pragma unroll
+          for (int y = 0; y < C::kCopies; ++y) M = fmaxf(M, sh.ml[row + y * NQ].x);
+#pragma unroll
+          for (int y = 0; y < C::kCopies; ++y) {
+            const float2 v = sh.ml[row + y * NQ];
+            const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
+            L += v.y != 0.f ? f * v.y : 0.f;  // NaN stays
+            if (y == copy) weight = f;
+          }
+          if (l_run != l_run) L = l_run;
+          m_run = M;
+          l_run = L;
+        }
         if (write) {
           if (whole) p.lse[orow] = (m_run + log2f(l_run)) * 0.69314718055994531f;
           else p.part_ml[(size_t)g.slot * NQ + row] = make_float2(m_run, l_run);
         }
-        const float inv = whole ? 1.f / l_run : 1.f;
-        (void)wait(&sh.pv_done[1], (n - 1) & 1);
+        const float inv = weight * (whole ? 1.f / l_run : 1.f);
+        (void)wait(&sh.pv_done[C::kCopies == 1 ? 1 : 0], (n - 1) & 1);
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(lane_addr + kColO + c, o);
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(lane_addr + kColO + c, o);
           tmem_wait_ld();
+          float v[16];
+#pragma unroll
+          for (int y = 0; y < 16; ++y) v[y] = __uint_as_float(o[y]) * inv;
+          if constexpr (C::kCopies > 1) {
+            if (copy > 0) {
+#pragma unroll
+              for (int y = 0; y < 16; ++y) sh.join[(tid - NQ) * 17 + y] = v[y];
+            }
+            named_bar_sync(1, kWG);
+            if (copy == 0) {
+#pragma unroll
+              for (int x = 1; x < C::kCopies; ++x)
+#pragma unroll
+                for (int y = 0; y < 16; ++y) v[y] += sh.join[(row + (x - 1) * NQ) * 17 + y];
+            }
+            named_bar_sync(1, kWG);
+          }
           if (write && whole) {
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + orow * D + c);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              uint32_t w[4];
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                w[x] = pack_bf16x2(__uint_as_float(o[8 * y + 2 * x]) * inv, __uint_as_float(o[8 * y + 2 * x + 1]) * inv);
-              dst[y] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int y = 0; y < 2; ++y)
+              dst[y] = make_uint4(pack_bf16x2(v[8 * y], v[8 * y + 1]), pack_bf16x2(v[8 * y + 2], v[8 * y + 3]),
+                                  pack_bf16x2(v[8 * y + 4], v[8 * y + 5]), pack_bf16x2(v[8 * y + 6], v[8 * y + 7]));
           } else if (write) {
             float4 *dst = reinterpret_cast<float4 *>(p.part_o + ((size_t)g.slot * NQ + row) * D + c);
 #pragma unroll
-            for (int y = 0; y < 8; ++y)
-              dst[y] = make_float4(__uint_as_float(o[4 * y]), __uint_as_float(o[4 * y + 1]), __uint_as_float(o[4 * y + 2]),
-                                   __uint_as_float(o[4 * y + 3]));
+            for (int y = 0; y < 4; ++y) dst[y] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
           }
         }
         tc_fence_before();
