@@ -141,9 +141,11 @@ __device__ __forceinline__ Pages group_pages(int pos0, int npos, int W, int m, i
   return g;
 }
 
-// tiles per CTA
+// tiles per CTA (the 64-bit division is several times the 32-bit one)
 __device__ __forceinline__ long long cta_quota(long long ntiles, int grid, int min_tiles) {
-  const long long q = (ntiles + grid - 1) / grid;
+  if (ntiles <= 0) return min_tiles;
+  const unsigned long long n = (unsigned long long)ntiles + grid - 1;
+  const long long q = n >> 32 ? (long long)(n / grid) : (long long)((uint32_t)n / (uint32_t)grid);
   return q > min_tiles ? q : min_tiles;
 }
 

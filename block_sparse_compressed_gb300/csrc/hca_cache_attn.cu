@@ -510,8 +510,8 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
   }
   {
     ProfScope prof(kKCacheCombine, st);
-    if (a.dtype == HCA_F32) hca_cache_combine_kernel<float><<<2 * sms, kCombineThreads, 0, st>>>(p);
-    else hca_cache_combine_kernel<__nv_bfloat16><<<2 * sms, kCombineThreads, 0, st>>>(p);
+    if (a.dtype == HCA_F32) hca_cache_combine_kernel<float><<<4 * sms, kCombineThreads, 0, st>>>(p);
+    else hca_cache_combine_kernel<__nv_bfloat16><<<4 * sms, kCombineThreads, 0, st>>>(p);
   }
   return cudaGetLastError();
 }

@@ -11,26 +11,30 @@
 // token's 64 heads and can use the e4m3 rows as they are, but every maximum then
 // crosses 128 threads: 4,200 cycles a tile were measured, half of them there.)
 //
+// A tile goes in two halves of 64 keys: while the softmax works on one, the
+// tensor cores add the other's part of O and make its next scores.
+//
 // The products take 128 rows whatever NQ is, so a group of NQ = 64 (32) rows has
 // them in the lanes twice (four times), and each copy sees its own half
-// (quarter) of a tile's keys: P is zero for the others.  The copies are so many
+// (quarter) of a half's keys: P is zero for the others.  The copies are so many
 // independent streams of the online softmax, joined when the group ends.
 //
 // The cache's e4m3 values become fp16 on the way to shared memory, exactly, once
 // for both products and all rows: converter warps load pages of global memory
 // into registers, a tile ahead of the one that they store, behind L2 prefetches
-// that the page warp issues two tiles ahead.  A key's block scale s multiplies
-// one number, its score; P is p * s, and the row's sum divides by s again.  q is
-// scaled by a power of two for the whole tile, so its 8 bits survive in fp16;
-// p * s is rounded to fp16 (11 bits; 2^-25 of the row's reference where tiny).
+// that the page warp issues up to four tiles ahead.  A key's block scale s
+// multiplies one number, its score; P is p * s, and the row's sum divides by s
+// again.  A row of q is scaled by a power of two, so its 8 bits survive in fp16
+// (what is below 2^-32 of its largest value is lost); p * s is rounded to fp16
+// (11 bits; 2^-25 of the row's reference where tiny).
 //
 // The reference exponent of a row is its largest score so far, raised only when
 // beaten by 2^8 (fp16 has room for 2^15), so O is rarely rescaled.
 //
 // A row of the cache that some query row does not see may hold anything, and
-// 0 * NaN is not 0: the converter stores zeros for keys that nobody sees and for
-// keys that hold a NaN and are seen by some only, and notes the latter in a bit
-// mask, by which the softmax gives a NaN to whoever sees them.
+// 0 * NaN is not 0: of the pages that not every row sees whole, the converter
+// stores zeros for keys with a NaN and notes them in a bit mask, by which the
+// softmax gives a NaN to whoever sees them.
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -49,17 +53,18 @@ constexpr int kMetaStages = 4;  // tiles whose pages are looked up ahead
 constexpr int kStages = 2;      // fp16 tiles
 constexpr int kMaxSegs = 64;    // pieces of groups listed in shared memory
 constexpr int kWG = 128;
-constexpr int kThreads = 3 * kWG;  // softmax | converter | page and MMA warp
-// Registers: 2 CTAs of 384 threads leave 80 each; the softmax holds 64 scores.
-constexpr int kRegsSoft = 136, kRegsConv = 64, kRegsIssue = 40;
-static_assert(kRegsSoft + kRegsConv + kRegsIssue <= 3 * 80, "register split must fit the launch");
+constexpr int kThreads = 3 * kWG;  // softmax | converter | page warp, MMA warp, two q warps
 constexpr int kTmem = 256;      // S of keys 0 .. 63 | S of keys 64 .. 127 (P takes the first half of each) | O
 constexpr uint32_t kColO = 128;
 
 template <int NQ, int D>
 struct Cfg {
   static constexpr int kCopies = 128 / NQ;                 // of a row in the lanes
-  static constexpr int kSpan = kCopies == 1 ? 64 : NQ;     // keys that a thread takes at a time: 64, 64, 32
+  // Registers: 2 CTAs of 384 threads leave 80 each; a softmax thread holds kSpan scores.
+  static constexpr int kRegsSoft = kCopies == 1 ? 128 : 112, kRegsConv = 64, kRegsIssue = kCopies == 1 ? 48 : 64;
+  static_assert(kRegsSoft + kRegsConv + kRegsIssue <= 3 * 80, "register split must fit the launch");
+  static constexpr int kSpan = 64 / kCopies;               // keys of a half that a thread takes: 64, 32, 16
+  static constexpr int kJoin = kCopies == 2 ? 32 : 16;     // columns of O joined at a time
   static constexpr int kHalves = D / 64;                   // 128-byte column blocks of an fp16 row
   static constexpr int kStageBytes = kHalves * kHalfTile;  // fp16 tile of 128 keys
   static constexpr int kOffQ = kStages * kStageBytes;
@@ -79,20 +84,21 @@ template <int NQ, int D>
 struct Shared {
   uint64_t meta_full[kMetaStages], meta_empty[kMetaStages];
   uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t q_full, s_full[2], p_full[2], pv_done[2], drain, never;
+  uint64_t q_full, q_free, s_full[2], p_full[2], pv_done[2], drain, never;
   uint64_t scale_full[kMetaStages];
   PageMeta meta[kMetaStages][8];
   uint32_t nan_keys[kMetaStages][4];  // keys whose rows hold a NaN that not everybody sees
   int nan_any[kMetaStages];
   int all_seen[kMetaStages];          // bit h: every row sees every key of half h
-  float amax[4];
+  float q_factor[2][NQ];                         // log2(e) |scale| / (a row's factor), of two groups in turn
   // the CTA's pieces of groups, in order; what there is no room for is in the
   // workspace's groups
   Segment seg[kMaxSegs];
   int gbase[kThreads];
   float2 ml[kWG];                                // copies: reference and sum of every lane
-  float join[NQ < 128 ? (128 - NQ) * 17 : 1];    // copies: 16 columns of O of all lanes but the first copy's
+  float join[NQ < 128 ? (128 - NQ) * (Cfg<NQ, D>::kJoin + 1) : 1];  // copies: columns of O of all lanes but the first copy's
   long long scan[33];
+  int2 sums[2][kThreads / 32];                   // tiles and groups of each warp
   uint32_t tmem_base;
   int abort, first;
 };
@@ -105,6 +111,14 @@ __device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
 __device__ __forceinline__ void st_shared(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+__device__ __forceinline__ void ld_shared(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
+}
+// 16 bytes of which the first n come from p and the others are 0
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *p, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ uint4 ld_global_16(const uint8_t *p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
@@ -118,6 +132,11 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &a, uint32_t 
   asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
       : "=r"(a), "=r"(b)
       : "r"(w));
+}
+
+__device__ __forceinline__ bool wait_idle(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status,
+                                          uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, mbar_wait_idle(bar, parity, abort, status, limit_ns));
 }
 
 template <int NQ, int D>
@@ -140,7 +159,8 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       mbar_init(&sh.kv_full[s], kWG);
       mbar_init(&sh.kv_empty[s], 1);
     }
-    mbar_init(&sh.q_full, kWG);
+    mbar_init(&sh.q_full, 64);
+    mbar_init(&sh.q_free, kWG);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&sh.s_full[h], 1);
       mbar_init(&sh.p_full[h], kWG);
@@ -157,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
   }
   // the CTA's range of the line, and its pieces of groups
   long long ntiles, quota, c0, c1;
+  bool busy;
   if (p.in_cta) {
     // one thread per request; where some bring more than one group, one per group
     long long n = 0, all;
@@ -168,8 +189,8 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
     if (!__syncthreads_or(n > 1)) {
       if (mine && ok) ok = chunk_group(p, tid, 0, g);
     } else {
-      const long long before = block_scan(n, sh.scan, all);
-      if (tid < p.R) sh.gbase[tid] = (int)before;
+      const long long chunks = block_scan(n, sh.scan, all);
+      if (tid < p.R) sh.gbase[tid] = (int)chunks;
       ok = __syncthreads_and(ok);
       mine = ok && tid < all;
       if (mine) {
@@ -181,19 +202,62 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         ok = chunk_group(p, lo, tid - sh.gbase[lo], g);
       }
     }
-    // tiles before this group, and (in the upper bits) groups before it
-    const long long at = block_scan((mine ? g.ntiles : 0) | (mine ? 1ll << 44 : 0), sh.scan, all);
-    g.tile0 = at & ((1ll << 44) - 1);
-    const int index = (int)(at >> 44);
-    ntiles = __syncthreads_and(ok) ? all & ((1ll << 44) - 1) : -1;
-    quota = cta_quota(ntiles, p.grid, p.min_tiles);
-    c0 = quota * blockIdx.x;
-    c1 = min(c0 + quota, ntiles);
-    const bool in = mine && g.tile0 < c1 && g.tile0 + g.ntiles > c0;
-    if (in && g.tile0 <= c0) sh.first = index;
-    __syncthreads();
+    // Tiles and groups before this one: within the warp, then over the warps in
+    // front.  A warp's groups have less than 2^31 tiles (2^25 each at most).
+    auto scan_tiles = [&](int v, int2 *sums, long long &total, int &groups, int &index) {
+      int x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const uint32_t b = __ballot_sync(0xffffffffu, mine);
+      if (lane == 31) sums[warp] = make_int2(x, __popc(b));
+      __syncthreads();
+      long long before = 0;
+      total = 0;
+      groups = 0;
+      index = __popc(b & ((1u << lane) - 1u));
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        const int2 s = sums[w];
+        if (w < warp) before += s.x, index += s.y;
+        total += s.x;
+        groups += s.y;
+      }
+      return before + x - v;
+    };
+    ok = __syncthreads_and(ok);
+    int ngroups, index;
+    const long long before = scan_tiles(mine ? g.ntiles : 0, sh.sums[0], ntiles, ngroups, index);
+    if (!ok) ntiles = -1;
+    // Ranges that no group's border cuts give a CTA tiles of one group only and
+    // save it a second one's beginning and end, about two tiles' time each;
+    // ceil(tiles / quota) of them for each group fit the grid with a larger quota.
+    const long long cut = cta_quota(ntiles, p.grid, p.min_tiles);
+    const long long own = cta_quota(ntiles, max(p.grid - ngroups, 1), p.min_tiles);
+    const bool whole_groups = ngroups < p.grid && own <= cut + 2;
+    bool in;
+    if (whole_groups) {
+      quota = own;
+      const int q32 = (int)quota;  // a group's share of the tiles fits
+      g.tile0 = quota * scan_tiles(mine ? (g.ntiles + q32 - 1) / q32 : 0, sh.sums[1], all, ngroups, index);
+      c0 = quota * blockIdx.x;
+      c1 = c0 + quota;
+      in = mine && ntiles > 0 && g.tile0 <= c0 && c0 < g.tile0 + g.ntiles;
+      if (in) sh.first = index;
+    } else {
+      g.tile0 = before;
+      quota = cut;
+      c0 = quota * blockIdx.x;
+      c1 = min(c0 + quota, ntiles);
+      in = mine && g.tile0 < c1 && g.tile0 + g.ntiles > c0;
+      if (in && g.tile0 <= c0) sh.first = index;
+    }
+    busy = __syncthreads_or(in);
     if (in) {
-      const Segment x = segment_of(g, c0, c1, blockIdx.x);
+      Segment x = segment_of(g, c0, c1, blockIdx.x);
+      if (whole_groups) x.slice_last |= 1;
       if (index - sh.first < kMaxSegs) sh.seg[index - sh.first] = x;
       else p.groups[index] = g;
       if (x.last()) p.border[blockIdx.x] = border_of(p, g, c0, c1, quota, blockIdx.x);
@@ -203,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
     quota = cta_quota(ntiles, p.grid, p.min_tiles);
     c0 = quota * blockIdx.x;
     c1 = min(c0 + quota, ntiles);
-    if (c0 < c1) {
+    busy = c0 < c1;
+    if (busy) {
       const int ng = p.hdr->ngroups;
       if (warp == 0) {
         const int g = find_group(p.groups, ng, c0);
@@ -220,7 +285,6 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       }
     }
   }
-  const bool busy = c0 < c1;
   if (tid == 0) {
     p.err[blockIdx.x] = ntiles < 0 ? HCA_ERR_CACHE : HCA_OK;
     if (!busy) p.border[blockIdx.x] = Border{0, 0, 0, 0};
@@ -232,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
   const uint32_t tmem = sh.tmem_base;
   const int ppt = kTileKeys >> p.log_bs;  // pages per tile: a power of two, 1 .. 8
   if (warp >= 8) {
-    setmaxnreg_dec<kRegsIssue>();
+    setmaxnreg_dec<C::kRegsIssue>();
     if (warp == 8 && busy) {
       // ------------------------------------------------------------ pages
       const int batch = 32 / ppt;  // tiles whose pages the warp's lanes look up at once
@@ -245,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         for (int jb = g.j0; ok && jb < g.j1; jb += batch) {
           const int v = jb * ppt + lane;
           PageMeta pm = {nullptr, 0, kNoPage, 1.f, 0.f, 1.f, 0};
+          bool bad = false;  // block id out of range
           if (v < pg.nraw + pg.ncomp && v < g.j1 * ppt) {
             const bool comp = v >= pg.nraw;
             const CacheSet &cs = comp ? p.comp : p.raw;
@@ -258,8 +323,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
               pm.rows = cs.pool + (size_t)id * page_bytes;
               pm.scale = cs.scale[id];
             } else {
-              pm.kind = comp ? kComp : kRaw;  // every key of it is noted as NaN
-              atomicExch(status, HCA_ERR_CACHE);
+              bad = true;  // every key of it is noted as NaN
             }
           }
           const uint32_t seen = __ballot_sync(0xffffffffu, pm.kind == kAllSeen);
@@ -268,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           for (int t = 0; t < jn; ++t, ++n) {
             const int ms = n % kMetaStages;
             if (n >= (uint32_t)kMetaStages)
-              ok = wait_warp(&sh.meta_empty[ms], ((n / kMetaStages) - 1) & 1, abort_flag, status, p.wait_ns);
+              ok = wait_idle(&sh.meta_empty[ms], ((n / kMetaStages) - 1) & 1, abort_flag, status, p.wait_ns);
             if (!ok) break;
             const bool here = lane / ppt == t;
             PageMeta &to = sh.meta[ms][lane % ppt];
@@ -288,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             if (lane == 0) mbar_arrive(&sh.meta_full[ms]);
             // the scales are needed later than the rows
             if (here) {
-              if (!(pm.scale > 0.f && pm.scale < INFINITY)) {
+              if (bad || !(pm.scale > 0.f && pm.scale < INFINITY)) {
                 pm.scale = 1.f;
                 atomicExch(status, HCA_ERR_CACHE);
                 for (int r = (lane % ppt) << p.log_bs, i = 0; i < 1 << p.log_bs; ++i, ++r)
@@ -313,17 +377,13 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       }
     } else if (warp == 9 && busy) {
       // ------------------------------------------------------------ MMA
-      // One thread's products run in order, so the S product that overwrites P is
-      // issued right behind the O product that reads it.  Without copies a tile
-      // goes in two halves of 64 keys, S of (n + 1, h) behind O of (n, h), so that
-      // the scores of one half are made while the softmax works on the other.
-      // With copies every thread works on its keys of the whole tile at once.
+      // One thread's products run in order: S of half (n + 1, h) is issued right
+      // behind the O product of (n, h), whose P it overwrites.
       const uint32_t kv0 = smem_u32(smem), q0 = smem_u32(smem + C::kOffQ);
       const uint64_t dk = smem_desc_sw128(kv0, 16, 1024);        // K view of stage 0
       const uint64_t dv = smem_desc_sw128(kv0, kHalfTile, 1024);  // V view of stage 0
       const uint64_t dq = smem_desc_sw128(q0, 16, 1024);
-      constexpr int kParts = C::kCopies == 1 ? 2 : 1;  // of a tile
-      const uint32_t id_s = idesc_f16_f32(128, 128 / kParts, false, false), id_o = idesc_f16_f32(128, D, false, true);
+      const uint32_t id_s = idesc_f16_f32(128, 64, false, false), id_o = idesc_f16_f32(128, D, false, true);
       uint32_t n = 0, nseg = 0;
       bool ok = true, issued = false;
       if (p.stall) {
@@ -347,31 +407,32 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           const uint32_t st = n % kStages;
           if (j == seg.j0) {
             // a group's q is written after the last softmax of the group before
-            ok = wait_warp(&sh.q_full, nseg & 1, abort_flag, status, p.wait_ns) &&
-                 wait_warp(&sh.kv_full[st], (n / kStages) & 1, abort_flag, status, p.wait_ns);
+            ok = wait_idle(&sh.q_full, nseg & 1, abort_flag, status, p.wait_ns) &&
+                 wait_idle(&sh.kv_full[st], (n / kStages) & 1, abort_flag, status, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
-            for (int h = 0; h < kParts; ++h) issue_s(n, h);
+            issue_s(n, 0);
+            issue_s(n, 1);
           }
           const uint64_t bv = dv + desc_bytes(st * C::kStageBytes);
           const bool more = j + 1 < seg.j1;
 #pragma unroll
-          for (int h = 0; h < kParts; ++h) {
-            ok = wait_warp(&sh.p_full[h], n & 1, abort_flag, status, p.wait_ns);
+          for (int h = 0; h < 2; ++h) {
+            ok = wait_idle(&sh.p_full[h], n & 1, abort_flag, status, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-              for (int k1 = 0; k1 < 8 / kParts; ++k1) {
+              for (int k1 = 0; k1 < 4; ++k1) {
                 const int kk = h * 4 + k1;
                 mma_ts(tmem + kColO, tmem + h * 64 + k1 * 8, bv + mnmaj_step(kk), id_o, j > seg.j0 || kk > 0);
               }
               mma_commit(&sh.pv_done[h]);
-              if (h == kParts - 1) mma_commit(&sh.kv_empty[st]);
+              if (h == 1) mma_commit(&sh.kv_empty[st]);
             }
             __syncwarp();
             if (more) {
-              if (h == 0) ok = wait_warp(&sh.kv_full[(n + 1) % kStages], ((n + 1) / kStages) & 1, abort_flag, status, p.wait_ns);
+              if (h == 0) ok = wait_idle(&sh.kv_full[(n + 1) % kStages], ((n + 1) / kStages) & 1, abort_flag, status, p.wait_ns);
               if (!ok) break;
               tc_fence_after();
               issue_s(n + 1, h);
@@ -388,8 +449,69 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         __syncwarp();
       }
     }
+    else if (warp >= 10 && busy) {
+      // ------------------------------------------------------------ q
+      // A group's q into shared memory once every product with the last one's
+      // has been made: copied as it is (asynchronously, all rows in flight), then
+      // each thread turns the pieces that it copied into fp16 in their place.
+      // D / 8 neighbouring lanes have a row's 16-byte pieces, so its largest
+      // value is a few shuffles away.
+      constexpr int kLanes = D / 8, kRows = 64 / kLanes;  // lanes of a row, rows at a time
+      const int t64 = tid - 320, ch = t64 % kLanes, c0q = t64 / kLanes;
+      const uint32_t dst = smem_u32(smem) + C::kOffQ + (ch >> 3) * kHalfTile;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const Segment g = segment(k);
+        const int nreal = real_columns(p, g.npos, g.slice());
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)g.row0 * p.H + g.slice() * p.HS) * D + ch * 8;
+#pragma unroll 4
+        for (int c = c0q; c < NQ; c += kRows)  // rows beyond the group's are zero
+          cp_async_16(dst + c * 128 + (((ch & 7) ^ (c & 7)) << 4), c < nreal ? q + (size_t)c * D : q, c < nreal ? 16 : 0);
+        cp_async_wait();
+        // four rows at a time, step by step, so that their latencies overlap
+        constexpr int kBatch = NQ / kRows < 4 ? NQ / kRows : 4;
+        for (int c = c0q; c < NQ; c += kBatch * kRows) {
+          uint32_t w[kBatch][4];
+          float amax[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) ld_shared(dst + (c + i * kRows) * 128 + (((ch & 7) ^ ((c + i * kRows) & 7)) << 4), w[i]);
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            amax[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float a = fabsf(__uint_as_float(w[i][e] << 16)), b = fabsf(__uint_as_float(w[i][e] & 0xffff0000u));
+              if (a < INFINITY) amax[i] = fmaxf(amax[i], a);
+              if (b < INFINITY) amax[i] = fmaxf(amax[i], b);
+            }
+          }
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], o));
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            // the largest |q| becomes 224 .. 448; a negative scale goes into q's sign
+            const int ex = scale_exponent(amax[i]), ci = c + i * kRows;
+            const float inv = p.scale < 0.f ? -exp2_int(-ex) : p.scale > 0.f ? exp2_int(-ex) : 0.f;
+            if (ch == 0) sh.q_factor[k & 1][ci] = exp2_int(ex) * fabsf(p.scale) * 1.4426950408889634f;
+            uint32_t f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              f[e] = f16x2_rn(__uint_as_float(w[i][e] << 16) * inv, __uint_as_float(w[i][e] & 0xffff0000u) * inv);
+#pragma unroll
+            for (int y = 0; y < C::kCopies; ++y)
+              st_shared(dst + (ci + y * NQ) * 128 + (((ch & 7) ^ (ci & 7)) << 4), f[0], f[1], f[2], f[3]);
+          }
+        }
+        fence_async_smem();
+        mbar_arrive(&sh.q_full);
+        if (g.last()) break;
+        ok = wait_idle(&sh.q_free, k & 1, abort_flag, status, p.wait_ns);
+      }
+    }
   } else if (warp >= 4) {
-    setmaxnreg_dec<kRegsConv>();
+    setmaxnreg_dec<C::kRegsConv>();
     if (busy) {
       // ------------------------------------------------------------ converter
       // Thread c takes 16-byte pieces (16 values) c, c + 128, ... of a tile: 16
@@ -405,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       // loads of tile n's rows, once its pages are known
       auto load = [&](uint32_t n) {
         const int ms = n % kMetaStages;
-        if (!wait_warp(&sh.meta_full[ms], (n / kMetaStages) & 1, abort_flag, status, p.wait_ns)) return false;
+        if (!wait_idle(&sh.meta_full[ms], (n / kMetaStages) & 1, abort_flag, status, p.wait_ns)) return false;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int row = row0 + i * kRowStep;
@@ -417,34 +539,33 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       ok = load(0);
       for (int k = 0; ok; ++k) {
         const Segment g = segment(k);
-        // keys that some row and that every row sees
-        const int last = g.pos0 + g.npos - 1, raw_any = g.pos0 - p.W + 1, raw_all = last - p.W + 1;
-        const int ent_any = (last + 1) / p.m, ent_all = (g.pos0 + 1) / p.m;
         for (int j = g.j0; ok && j < g.j1; ++j, ++n) {
           const int ms = n % kMetaStages, st = n % kStages;
+          uint32_t nans = 0;
           if (sh.all_seen[ms] != 3) {
-            // rows that nobody sees, or some only
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) nans |= nan_bytes(raw[i]);
+          }
+          if (__any_sync(0xffffffffu, nans != 0)) {
+            // NaN in a row that not every row of the group sees
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
               const int row = row0 + i * kRowStep;
-              const PageMeta &pm = sh.meta[ms][row >> p.log_bs];
-              const int kind = pm.kind, key = pm.key0 + (row & bs_mask);
-              const bool seen = kind == kAllSeen || (kind == kRaw && key >= raw_any && key <= last) || (kind == kComp && key < ent_any);
-              const bool all = kind == kAllSeen || (kind == kRaw && key >= raw_all && key <= g.pos0) || (kind == kComp && key < ent_all);
-              bool nan = kind < kNoPage && !pm.rows;  // a bad block id
-              if (__any_sync(0xffffffffu, seen && !all)) nan = nan || (seen && !all && nan_bytes(raw[i]) != 0);
               // a row's pieces are in kPer neighbouring lanes
               const uint32_t grp = ((1u << kPer) - 1u) << (lane & ~(kPer - 1));
-              nan = (__ballot_sync(0xffffffffu, nan) & grp) != 0;
-              if (!seen || nan) raw[i] = make_uint4(0, 0, 0, 0);
-              if (nan && seen && ch == 0) {
-                atomicOr(&sh.nan_keys[ms][row >> 5], 1u << (row & 31));
-                sh.nan_any[ms] = 1;
+              const bool nan = (__ballot_sync(0xffffffffu, nan_bytes(raw[i]) != 0) & grp) != 0;
+              const PageMeta &pm = sh.meta[ms][row >> p.log_bs];
+              if (nan && pm.kind != kAllSeen) {
+                raw[i] = make_uint4(0, 0, 0, 0);
+                if (ch == 0) {
+                  atomicOr(&sh.nan_keys[ms][row >> 5], 1u << (row & 31));
+                  sh.nan_any[ms] = 1;
+                }
               }
             }
           }
           if (n >= (uint32_t)kStages)
-            ok = wait_warp(&sh.kv_empty[st], ((n / kStages) - 1) & 1, abort_flag, status, p.wait_ns);
+            ok = wait_idle(&sh.kv_empty[st], ((n / kStages) - 1) & 1, abort_flag, status, p.wait_ns);
           if (!ok) break;
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
@@ -472,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       }
     }
   } else {
-    setmaxnreg_inc<kRegsSoft>();
+    setmaxnreg_inc<C::kRegsSoft>();
     if (ntiles < 0) {
       // the schedule was refused
       const size_t rows = (size_t)p.N * p.H;
@@ -487,64 +608,9 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       constexpr int kSpan = C::kSpan;
       const int row = tid % NQ, copy = tid / NQ;  // row of the group
       const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
-      auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, abort_flag, status, p.wait_ns); };
-
-      // q of a group into shared memory; returns log2(e) * |scale| / (its factor)
-      auto load_q = [&](const Segment &g) {
-        constexpr int kUnits = NQ * D / 16;  // 16 values each
-        constexpr int kMine = (kUnits + kWG - 1) / kWG;
-        const int nreal = real_columns(p, g.npos, g.slice());
-        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
-                                                          ((size_t)g.row0 * p.H + g.slice() * p.HS) * D);
-        uint4 u[kMine][2];
-#pragma unroll
-        for (int k = 0; k < kMine; ++k) {
-          const int i = tid + k * kWG;
-          u[k][0] = u[k][1] = make_uint4(0, 0, 0, 0);
-          if (i / (D / 16) < nreal) u[k][0] = q[2 * i], u[k][1] = q[2 * i + 1];
-        }
-        float amax = 0.f;
-#pragma unroll
-        for (int k = 0; k < kMine; ++k) {
-          const uint32_t w[8] = {u[k][0].x, u[k][0].y, u[k][0].z, u[k][0].w, u[k][1].x, u[k][1].y, u[k][1].z, u[k][1].w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float a = fabsf(__uint_as_float(w[e] << 16)), b = fabsf(__uint_as_float(w[e] & 0xffff0000u));
-            if (a < INFINITY) amax = fmaxf(amax, a);
-            if (b < INFINITY) amax = fmaxf(amax, b);
-          }
-        }
-        const int wm = __reduce_max_sync(0xffffffffu, __float_as_int(amax));
-        if (lane == 0) sh.amax[warp] = __int_as_float(wm);
-        named_bar_sync(1, kWG);
-        amax = fmaxf(fmaxf(sh.amax[0], sh.amax[1]), fmaxf(sh.amax[2], sh.amax[3]));
-        // the largest |q| becomes 224 .. 448; a negative scale goes into q's sign
-        const float s = exp2_int(scale_exponent(amax)), inv = p.scale < 0.f ? -1.f / s : p.scale > 0.f ? 1.f / s : 0.f;
-        const uint32_t dst = smem_u32(smem) + C::kOffQ;
-#pragma unroll
-        for (int k = 0; k < kMine; ++k) {
-          const int i = tid + k * kWG, c = i / (D / 16), ch = i % (D / 16);
-          if (kUnits % kWG != 0 && c >= NQ) break;
-          const uint32_t w[8] = {u[k][0].x, u[k][0].y, u[k][0].z, u[k][0].w, u[k][1].x, u[k][1].y, u[k][1].z, u[k][1].w};
-          uint32_t f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            f[e] = f16x2_rn(__uint_as_float(w[e] << 16) * inv, __uint_as_float(w[e] & 0xffff0000u) * inv);
-          const int c2 = 2 * (ch & 3), x = c & 7;
-#pragma unroll
-          for (int y = 0; y < C::kCopies; ++y) {
-            const uint32_t at = dst + (ch >> 2) * kHalfTile + (c + y * NQ) * 128;
-            st_shared(at + ((c2 ^ x) << 4), f[0], f[1], f[2], f[3]);
-            st_shared(at + (((c2 + 1) ^ x) << 4), f[4], f[5], f[6], f[7]);
-          }
-        }
-        fence_async_smem();
-        mbar_arrive(&sh.q_full);
-        return s * fabsf(p.scale) * 1.4426950408889634f;
-      };
+      auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_idle(bar, parity, abort_flag, status, p.wait_ns); };
 
       uint32_t n = 0;
-      float cs = load_q(segment(0));
       for (int k = 0;; ++k) {
         const Segment g = segment(k);
         const int nreal = real_columns(p, g.npos, g.slice());
@@ -552,6 +618,8 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         // what the row sees: raw keys [raw_lo, pos], entries [0, entries)
         const int raw_lo = pos - p.W + 1, entries = (pos + 1) / p.m;
         float m_run = -INFINITY, l_run = 0.f;
+        (void)wait(&sh.q_full, k & 1);
+        const float cs = sh.q_factor[k & 1][row];
         for (int j = g.j0; j < g.j1; ++j, ++n) {
           const int ms = n % kMetaStages;
           const PageMeta *meta = sh.meta[ms];
@@ -560,15 +628,19 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           const bool odd_rows = sh.nan_any[ms] != 0;
           const int all_seen = sh.all_seen[ms];
 #pragma unroll
-          for (int h = 0; h < (C::kCopies == 1 ? 2 : 1); ++h) {
+          for (int h = 0; h < 2; ++h) {
             (void)wait(&sh.s_full[h], n & 1);
             tc_fence_after();
-            const int k0 = C::kCopies == 1 ? h * 64 : copy * kSpan;  // first of the thread's keys, uniform in a warp
+            const int k0 = h * 64 + copy * kSpan;  // first of the thread's keys, uniform in a warp
             uint32_t sv[kSpan];
+            if constexpr (kSpan == 16) {
+              tmem_ld16(lane_addr + k0, sv);
+            } else {
 #pragma unroll
-            for (int c = 0; c < kSpan; c += 32) tmem_ld32(lane_addr + k0 + c, *reinterpret_cast<uint32_t(*)[32]>(sv + c));
+              for (int c = 0; c < kSpan; c += 32) tmem_ld32(lane_addr + k0 + c, *reinterpret_cast<uint32_t(*)[32]>(sv + c));
+            }
             // which of them the row sees
-            const bool plain = (all_seen >> (k0 >> 6)) & 1;
+            const bool plain = (all_seen >> h) & 1;
             uint64_t vis = ~0ull;
             if (!plain) {
               vis = 0;
@@ -590,18 +662,21 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
               }
             }
             if (odd_rows) {
-              const uint64_t bad = kSpan == 64 ? (uint64_t)sh.nan_keys[ms][k0 >> 5] | (uint64_t)sh.nan_keys[ms][(k0 >> 5) + 1] << 32
-                                               : (uint64_t)sh.nan_keys[ms][k0 >> 5];
+              uint64_t bad = sh.nan_keys[ms][k0 >> 5] >> (k0 & 31);
+              if (kSpan == 64) bad |= (uint64_t)sh.nan_keys[ms][(k0 >> 5) + 1] << 32;
+              if constexpr (kSpan < 64) bad &= (1ull << kSpan) - 1;
               if (bad & vis) l_run = __int_as_float(0x7fc00000);
             }
             tmem_wait_ld();
             if (!plain) {
+              constexpr int kStep = kSpan < 32 ? kSpan : 32;
+              constexpr uint32_t kAll = kStep == 32 ? 0xffffffffu : (1u << kStep) - 1u;
 #pragma unroll
-              for (int c = 0; c < kSpan; c += 32) {
-                const uint32_t v = (uint32_t)(vis >> c);
-                if (!__all_sync(0xffffffffu, v == 0xffffffffu)) {
+              for (int c = 0; c < kSpan; c += kStep) {
+                const uint32_t v = (uint32_t)(vis >> c) & kAll;
+                if (!__all_sync(0xffffffffu, v == kAll)) {
 #pragma unroll
-                  for (int y = 0; y < 32; ++y)
+                  for (int y = 0; y < kStep; ++y)
                     if (!((v >> y) & 1)) sv[c + y] = 0xff800000u;
                 }
               }
@@ -638,8 +713,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             const float m_use = m_run == -INFINITY ? 0.f : m_run;
             if (__any_sync(0xffffffffu, raise)) {
               // O holds the sum up to the keys before these once that is done
-              constexpr int kLast = C::kCopies == 1 ? 1 : 0;
-              (void)wait(&sh.pv_done[h ? 0 : kLast], (h ? n : n - 1) & 1);
+              (void)wait(&sh.pv_done[h ^ 1], (h ? n : n - 1) & 1);
               tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < D; c += 16) {
@@ -651,42 +725,42 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
                 tmem_st16(lane_addr + kColO + c, o);
               }
             }
-            // P over the columns of S: those of half h, or (copies) the first 64,
-            // with zeros for the other copies' keys
-            const uint32_t pcol = lane_addr + (C::kCopies == 1 ? h * 64 : copy * (kSpan / 2));
+            // P over the first columns of the half's S, with zeros for the other
+            // copies' keys
+            const uint32_t pcol = lane_addr + h * 64;
+            uint32_t pk[kSpan / 2];
 #pragma unroll
-            for (int c2 = 0; c2 < kSpan / 32; ++c2) {
-              uint32_t pk[16];
+            for (int c4 = 0; c4 < kGroups; ++c4) {
+              const float nm = lb[c4] - m_use;
+              const uint64_t ck2 = f32x2(__float_as_uint(ck[c4]), __float_as_uint(ck[c4]));
+              const uint64_t nm2 = f32x2(__float_as_uint(nm), __float_as_uint(nm));
+              uint64_t acc[2] = {0, 0};
 #pragma unroll
-              for (int c1 = 0; c1 < 2; ++c1) {
-                const int c4 = 2 * c2 + c1;
-                const float nm = lb[c4] - m_use;
-                const uint64_t ck2 = f32x2(__float_as_uint(ck[c4]), __float_as_uint(ck[c4]));
-                const uint64_t nm2 = f32x2(__float_as_uint(nm), __float_as_uint(nm));
-                uint64_t acc[2] = {0, 0};
-#pragma unroll
-                for (int y = 0; y < 16; y += 2) {
-                  float t0, t1;
-                  f32x2_split(ffma2(f32x2(sv[c4 * 16 + y], sv[c4 * 16 + y + 1]), ck2, nm2), t0, t1);
-                  const float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
-                  acc[(y >> 1) & 1] = fadd2(acc[(y >> 1) & 1], f32x2(__float_as_uint(e0), __float_as_uint(e1)));
-                  pk[c1 * 8 + (y >> 1)] = f16x2_rn(e0, e1);
-                }
-                float a, b;
-                f32x2_split(fadd2(acc[0], acc[1]), a, b);
-                l_run = fmaf(a + b, meta[pgi[c4]].inv_scale, l_run);
+              for (int y = 0; y < 16; y += 2) {
+                float t0, t1;
+                f32x2_split(ffma2(f32x2(sv[c4 * 16 + y], sv[c4 * 16 + y + 1]), ck2, nm2), t0, t1);
+                const float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
+                acc[(y >> 1) & 1] = fadd2(acc[(y >> 1) & 1], f32x2(__float_as_uint(e0), __float_as_uint(e1)));
+                pk[c4 * 8 + (y >> 1)] = f16x2_rn(e0, e1);
               }
-              tmem_st16(pcol + c2 * 16, pk);
+              float a, b;
+              f32x2_split(fadd2(acc[0], acc[1]), a, b);
+              l_run = fmaf(a + b, meta[pgi[c4]].inv_scale, l_run);
+              if (kSpan > 16 && (c4 & 1)) tmem_st16(pcol + copy * (kSpan / 2) + (c4 - 1) * 8, *reinterpret_cast<uint32_t(*)[16]>(&pk[(c4 - 1) * 8]));
             }
-            if constexpr (C::kCopies > 1) {
+            if constexpr (kSpan == 16) tmem_st8(pcol + copy * 8, pk);
+            if constexpr (C::kCopies == 2) {
               uint32_t zero[16];
 #pragma unroll
               for (int y = 0; y < 16; ++y) zero[y] = 0;
+              tmem_st16(pcol + (copy ^ 1) * 16, zero);
+            }
+            if constexpr (C::kCopies == 4) {
+              uint32_t zero[8];
 #pragma unroll
-              for (int y = 1; y < C::kCopies; ++y)
+              for (int y = 0; y < 8; ++y) zero[y] = 0;
 #pragma unroll
-                for (int c = 0; c < kSpan / 2; c += 16)
-                  tmem_st16(lane_addr + (copy + y) % C::kCopies * (kSpan / 2) + c, zero);
+              for (int y = 1; y < 4; ++y) tmem_st8(pcol + ((copy + y) & 3) * 8, zero);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -694,8 +768,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           }
           mbar_arrive(&sh.meta_empty[ms]);
         }
-        // the next group's q: every product with this one's has been made
-        if (!g.last()) cs = load_q(segment(k + 1));
+        mbar_arrive(&sh.q_free);  // every score of the group has been read
         if (*abort_flag) l_run = __int_as_float(0x7fc00000);
         const bool whole = g.slot < 0, write = row < nreal && copy == 0;
         const size_t orow = (size_t)g.row0 * p.H + g.slice() * p.HS + row;  // rows of the group are rows of q and out in order
@@ -723,40 +796,42 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           else p.part_ml[(size_t)g.slot * NQ + row] = make_float2(m_run, l_run);
         }
         const float inv = weight * (whole ? 1.f / l_run : 1.f);
-        (void)wait(&sh.pv_done[C::kCopies == 1 ? 1 : 0], (n - 1) & 1);
+        (void)wait(&sh.pv_done[1], (n - 1) & 1);
         tc_fence_after();
+        constexpr int kJoin = C::kJoin;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          uint32_t o[16];
-          tmem_ld16(lane_addr + kColO + c, o);
-          tmem_wait_ld();
-          float v[16];
+        for (int c = 0; c < D; c += kJoin) {
+          uint32_t o[kJoin];
 #pragma unroll
-          for (int y = 0; y < 16; ++y) v[y] = __uint_as_float(o[y]) * inv;
+          for (int x = 0; x < kJoin; x += 16) tmem_ld16(lane_addr + kColO + c + x, *reinterpret_cast<uint32_t(*)[16]>(&o[x]));
+          tmem_wait_ld();
+          float v[kJoin];
+#pragma unroll
+          for (int y = 0; y < kJoin; ++y) v[y] = __uint_as_float(o[y]) * inv;
           if constexpr (C::kCopies > 1) {
             if (copy > 0) {
 #pragma unroll
-              for (int y = 0; y < 16; ++y) sh.join[(tid - NQ) * 17 + y] = v[y];
+              for (int y = 0; y < kJoin; ++y) sh.join[(tid - NQ) * (kJoin + 1) + y] = v[y];
             }
             named_bar_sync(1, kWG);
             if (copy == 0) {
 #pragma unroll
               for (int x = 1; x < C::kCopies; ++x)
 #pragma unroll
-                for (int y = 0; y < 16; ++y) v[y] += sh.join[(row + (x - 1) * NQ) * 17 + y];
+                for (int y = 0; y < kJoin; ++y) v[y] += sh.join[(row + (x - 1) * NQ) * (kJoin + 1) + y];
             }
             named_bar_sync(1, kWG);
           }
           if (write && whole) {
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + orow * D + c);
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
+            for (int y = 0; y < kJoin / 8; ++y)
               dst[y] = make_uint4(pack_bf16x2(v[8 * y], v[8 * y + 1]), pack_bf16x2(v[8 * y + 2], v[8 * y + 3]),
                                   pack_bf16x2(v[8 * y + 4], v[8 * y + 5]), pack_bf16x2(v[8 * y + 6], v[8 * y + 7]));
           } else if (write) {
             float4 *dst = reinterpret_cast<float4 *>(p.part_o + ((size_t)g.slot * NQ + row) * D + c);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) dst[y] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+            for (int y = 0; y < kJoin / 4; ++y) dst[y] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
           }
         }
         tc_fence_before();
