@@ -436,7 +436,7 @@ static int empty_call(void *workspace, void *stream) {
   return cuda_status(cudaMemsetAsync(workspace, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream)));
 }
 
-size_t hca_cache_plan_workspace_size(void) { return kHeaderBytes; }
+size_t hca_cache_plan_workspace_size(int R) { return R < 0 || R > (1 << 24) ? 0 : cache_plan_ws_bytes(R); }
 
 int hca_cache_plan(const int32_t *held, const int32_t *added, int32_t *table, const int32_t *free_blocks,
                    const int32_t *free_in, int32_t *free_out, int32_t *start, int32_t *slots, int R, int cols, int bs,
@@ -449,15 +449,14 @@ int hca_cache_plan(const int32_t *held, const int32_t *added, int32_t *table, co
   if (!free_in || !free_out || !start) return HCA_ERR_NULL;
   if (R > 0 && (!held || !added || !table)) return HCA_ERR_NULL;
   if ((nslots > 0 && !slots) || (nfree > 0 && !free_blocks)) return HCA_ERR_NULL;
-  int rc = check_ws(workspace, workspace_bytes, kHeaderBytes);
+  int rc = check_ws(workspace, workspace_bytes, cache_plan_ws_bytes(R));
   if (rc != HCA_OK) return rc;
   if (take_launch_failure()) return HCA_ERR_CUDA;
   CachePlanArgs a;
   a.held = held; a.added = added; a.free_blocks = free_blocks; a.free_in = free_in;
   a.table = table; a.free_out = free_out; a.start = start; a.slots = slots;
-  a.status = static_cast<int32_t *>(workspace);
   a.R = R; a.cols = cols; a.bs = bs; a.m = m; a.nblocks = nblocks; a.nfree = nfree; a.nslots = nslots;
-  return cuda_status(cache_plan(a, static_cast<cudaStream_t>(stream)));
+  return cuda_status(cache_plan(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 size_t hca_cache_append_workspace_size(int nblocks) {

@@ -5,10 +5,12 @@
 // [E(held), E(held + added)).  Entry e lies in table column (e / bs) mod cols
 // at row e mod bs; the blocks of columns that were empty come from the end of
 // the free list, in the order of the requests.  Two exclusive sums over the
-// requests (entries, blocks) say everything: one CTA computes them, then the
-// slots follow from a search in the first.  A few hundred integers in, one
-// integer out for each entry: bound by latency for a decode step, by the slot
-// writes for long prompts.
+// requests (entries, blocks) say everything: one CTA computes them, and every
+// slot and every new table entry follows from a search in them and the free list
+// alone, so they are written in any order, by that CTA for a decode step or by
+// as many as there are SMs for prompts.  A few hundred integers in, one integer
+// out for each entry: bound by latency for a decode step, by the slot writes for
+// long prompts.
 //
 // Append.  A run is a maximal stretch of rows with consecutive slots in one
 // block.  Its block's scale s is a power of two, so an e4m3 value never changes
@@ -17,6 +19,8 @@
 // contiguous in x and in the pool, so a run is one flat conversion of n * D
 // values after one maximum over them.
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "hca_cache.cuh"
 
@@ -33,114 +37,146 @@ constexpr int kPlanOneCta = 4096;  // slots that the planning CTA itself writes
 
 struct PlanItem {
   long long entries;
-  int n0, n1;  // blocks held before and after
+  int e0, n0, n1;  // entries held; blocks held before and after
   int ok;
 };
 
 __device__ __forceinline__ PlanItem plan_item(const CachePlanArgs &a, int r) {
-  PlanItem t = {0, 0, 0, 1};
+  PlanItem t = {0, 0, 0, 0, 1};
   if (r >= a.R) return t;
   const long long h = a.held[r], d = a.added[r];
   if (h < 0 || d < 0 || h + d > kMaxPos) {
     t.ok = 0;
     return t;
   }
-  const int e0 = (int)h / a.m, e1 = (int)(h + d) / a.m;
-  t.entries = e1 - e0;
-  t.n0 = min((e0 + a.bs - 1) / a.bs, a.cols);
-  t.n1 = min((e1 + a.bs - 1) / a.bs, a.cols);
+  const int e1 = (int)(h + d) / a.m;
+  t.e0 = (int)h / a.m;
+  t.entries = e1 - t.e0;
+  t.n0 = min((t.e0 + a.bs - 1) >> a.log_bs, a.cols);
+  t.n1 = min((e1 + a.bs - 1) >> a.log_bs, a.cols);
   return t;
 }
 
-// Slots [i0, i1) of the plan, by the threads of this block.
-__device__ __forceinline__ void fill_slots(const CachePlanArgs &a, const int32_t *start, int i0, int i1) {
-  const int total = start[a.R];
-  for (int i = i0 + threadIdx.x; i < i1; i += blockDim.x) {
-    int slot = -1;
-    if (i < total) {
-      int lo = 0, hi = a.R;  // start[lo] <= i < start[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid] <= i) lo = mid; else hi = mid;
+// Largest r with before[r] <= i, of r in [lo, hi).
+__device__ __forceinline__ int find_request(const int32_t *before, int lo, int hi, int i) {
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (before[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Part `part` of `parts` of the slots and of the new table entries, by the
+// threads of this block.  start, taken [R + 1]: entries and blocks in front of
+// each request; avail: free blocks before the plan.
+__device__ __forceinline__ void plan_fill(const CachePlanArgs &a, const int32_t *start, const int32_t *taken, int avail,
+                                          int part, int parts) {
+  const int total = start[a.R], blocks = taken[a.R];
+  const int per = (a.nslots + parts - 1) / parts, i0 = part * per, i1 = min(i0 + per, a.nslots);
+  if (i0 < i1) {
+    // the requests of this part
+    const int r0 = i0 < total ? find_request(start, 0, a.R, i0) : 0;
+    const int r1 = i0 < total ? find_request(start, r0, a.R, min(i1, total) - 1) + 1 : 0;
+    for (int i = i0 + threadIdx.x; i < i1; i += blockDim.x) {
+      int slot = -1;
+      if (i < total) {
+        const int r = find_request(start, r0, r1, i);
+        const PlanItem t = plan_item(a, r);
+        const int e = t.e0 + i - start[r], last = t.e0 + (int)t.entries - 1;
+        const int page = e >> a.log_bs;
+        if ((last >> a.log_bs) - page < a.cols) {  // else a later new entry takes the row
+          const int col = page < a.cols ? page : page % a.cols;
+          const int id = col < t.n0 ? a.table[(size_t)r * a.cols + col] : a.free_blocks[avail - 1 - taken[r] - (col - t.n0)];
+          if (id >= 0 && id < a.nblocks) slot = (id << a.log_bs) + (e & (a.bs - 1));
+          else atomicExch(a.status, HCA_ERR_CACHE);
+        }
       }
-      const int e0 = a.held[lo] / a.m, e1 = (a.held[lo] + a.added[lo]) / a.m;
-      const int e = e0 + i - start[lo];
-      const int page = e / a.bs;
-      if ((e1 - 1) / a.bs - page < a.cols) {  // else a later new entry takes the row
-        const int id = a.table[(size_t)lo * a.cols + page % a.cols];
-        if (id >= 0 && id < a.nblocks) slot = id * a.bs + e % a.bs;
-        else atomicExch(a.status, HCA_ERR_CACHE);
-      }
+      a.slots[i] = slot;
     }
-    a.slots[i] = slot;
+  }
+  const int bper = (blocks + parts - 1) / parts, k1 = min((part + 1) * bper, blocks);
+  for (int k = part * bper + threadIdx.x; k < k1; k += blockDim.x) {
+    const int r = find_request(taken, 0, a.R, k);
+    a.table[(size_t)r * a.cols + plan_item(a, r).n0 + k - taken[r]] = a.free_blocks[avail - 1 - k];
   }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) hca_cache_plan_kernel(const CachePlanArgs a) {
   __shared__ long long tmp[33];
+  __shared__ int32_t near[2][kPlanThreads + 1];  // start and taken of up to 1024 requests
   const int tid = threadIdx.x;
   const int avail = *a.free_in;
+  const int nt = blockDim.x;
+  const bool few = a.R <= nt;
   // totals first: a plan that does not fit changes nothing
   long long entries = 0, blocks = 0;
   bool ok = avail >= 0 && avail <= a.nfree;
-  for (int r = tid; r < a.R; r += kPlanThreads) {
-    const PlanItem t = plan_item(a, r);
+  PlanItem t = {0, 0, 0, 0, 1};
+  for (int r = tid; r < a.R; r += nt) {
+    t = plan_item(a, r);
     ok = ok && t.ok;
     entries += t.entries;
     blocks += t.n1 - t.n0;
   }
   long long all_entries, all_blocks;
-  block_scan(entries, tmp, all_entries);
-  block_scan(blocks, tmp, all_blocks);
+  long long s = block_scan(entries, tmp, all_entries), k = block_scan(blocks, tmp, all_blocks);
   const bool valid = __syncthreads_and(ok);
-  const bool fits = all_entries <= a.nslots && all_blocks <= avail;
-  if (tid == 0) *a.status = !valid ? HCA_ERR_CACHE : fits ? HCA_OK : HCA_ERR_CAPACITY;
-  const bool go = valid && fits;
-  long long at = 0, taken = 0;
-  for (int r0 = 0; r0 < a.R; r0 += kPlanThreads) {
-    const int r = r0 + tid;
-    PlanItem t = {0, 0, 0, 1};
-    if (go) t = plan_item(a, r);
-    long long n, nb;
-    const long long s = at + block_scan(t.entries, tmp, n);
-    const long long k0 = taken + block_scan(t.n1 - t.n0, tmp, nb);
-    if (r < a.R) {
-      a.start[r] = (int)s;
-      for (int j = t.n0; j < t.n1; ++j) {
-        const int id = a.free_blocks[avail - 1 - (int)k0 - (j - t.n0)];
-        a.table[(size_t)r * a.cols + j] = id;
-      }
-    }
-    at += n;
-    taken += nb;
-  }
+  const bool go = valid && all_entries <= a.nslots && all_blocks <= avail;
   if (tid == 0) {
-    a.start[a.R] = (int)at;
-    *a.free_out = avail - (int)taken;
+    *a.status = go ? HCA_OK : valid ? HCA_ERR_CAPACITY : HCA_ERR_CACHE;
+    *a.free_out = go ? avail - (int)all_blocks : avail;
+    *a.avail = avail;
+    a.start[a.R] = near[0][few ? a.R : 0] = go ? (int)all_entries : 0;
+    a.taken[a.R] = near[1][few ? a.R : 0] = go ? (int)all_blocks : 0;
+  }
+  if (few) {
+    // one request a thread: its sums are at hand
+    if (tid < a.R) {
+      a.start[tid] = near[0][tid] = go ? (int)s : 0;
+      a.taken[tid] = near[1][tid] = go ? (int)k : 0;
+    }
+  } else {
+    long long at = 0, took = 0;
+    for (int r0 = 0; r0 < a.R; r0 += nt) {
+      const int r = r0 + tid;
+      PlanItem x = {0, 0, 0, 0, 1};
+      if (go) x = plan_item(a, r);
+      long long n, nb;
+      s = at + block_scan(x.entries, tmp, n);
+      k = took + block_scan(x.n1 - x.n0, tmp, nb);
+      if (r < a.R) {
+        a.start[r] = (int)s;
+        a.taken[r] = (int)k;
+      }
+      at += n;
+      took += nb;
+    }
   }
   __syncthreads();
-  if (a.nslots <= kPlanOneCta) fill_slots(a, a.start, 0, a.nslots);
+  if (a.nslots <= kPlanOneCta) plan_fill(a, few ? near[0] : a.start, few ? near[1] : a.taken, avail, 0, 1);
 }
 
-constexpr int kSlotThreads = 256, kSlotsPerCta = 2048;
+constexpr int kFillThreads = 256, kSlotsPerCta = 1024;
 
-__global__ void __launch_bounds__(kSlotThreads) hca_cache_slots_kernel(const CachePlanArgs a) {
-  const int i0 = blockIdx.x * kSlotsPerCta;
-  fill_slots(a, a.start, i0, min(i0 + kSlotsPerCta, a.nslots));
+__global__ void __launch_bounds__(kFillThreads) hca_cache_fill_kernel(const CachePlanArgs a) {
+  plan_fill(a, a.start, a.taken, *a.avail, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------------------
 // append
 // ---------------------------------------------------------------------------
-constexpr int kAppendThreads = 256;
-constexpr int kRowsPerCta = 8;
+// Up to this many rows (a decode step's) one cluster of CTAs does it all: a run
+// looks through all slots for others of its block.  For more the blocks are
+// claimed by a kernel in front (measured: 2 us more for 64 rows).
+constexpr int kAppendLook = 256;
+constexpr int kSmallCtas = 8, kSmallThreads = 512, kSmallWarps = kSmallCtas * kSmallThreads / 32;
 
 // Row t begins a run: its slot is not the one behind row t - 1's, or it is the
 // first of a block.
 __device__ __forceinline__ bool begins_run(const CacheAppendArgs &a, int t) {
   const int s = a.slots[t];
   if (s < 0 || s >= a.nblocks * a.bs) return false;
-  return t == 0 || s % a.bs == 0 || a.slots[t - 1] != s - 1;
+  return t == 0 || (s & (a.bs - 1)) == 0 || a.slots[t - 1] != s - 1;
 }
 
 // Every run writes its first row's index into its block's owner word.  A run
@@ -149,7 +185,7 @@ __device__ __forceinline__ bool begins_run(const CacheAppendArgs &a, int t) {
 __global__ void hca_cache_claim_kernel(const CacheAppendArgs a) {
   const int t = blockIdx.x * blockDim.x + threadIdx.x;
   if (t == 0) *a.status = HCA_OK;
-  if (t < a.N && begins_run(a, t)) a.owner[a.slots[t] / a.bs] = t;
+  if (t < a.N && begins_run(a, t)) a.owner[a.slots[t] >> a.log_bs] = t;
 }
 
 template <typename T>
@@ -181,11 +217,57 @@ __device__ __forceinline__ uint4 pack16(const float (&v)[16]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One run by one warp.
-template <typename T>
-__device__ __forceinline__ void append_run(const CacheAppendArgs &a, int t, int lane) {
+// Largest magnitude of the finite ones.
+__device__ __forceinline__ float finite_max(const float (&v)[16]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float f = fabsf(v[i]);
+    if (f < INFINITY) m = fmaxf(m, f);
+  }
+  return m;
+}
+
+__device__ __forceinline__ uint4 quantise16(float (&v)[16], float inv) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = fmaf(v[i], 0.f, v[i] * inv);  // an infinity becomes NaN, not 448
+  return pack16(v);
+}
+
+// The scale of block blk with new values up to amax from row off on; the rows in
+// front of them are brought to it by `nthreads` threads.
+__device__ __forceinline__ float settle_scale(const CacheAppendArgs &a, int blk, int off, float amax, int tid, int nthreads,
+                                              int &err) {
+  const float s = exp2_int(scale_exponent(amax));
+  if (off == 0) return s;
+  const float old = a.scale[blk];
+  if (!(old > 0.f && old < INFINITY)) {
+    err = HCA_ERR_CACHE;
+    return s;
+  }
+  if (old >= s) return old;
+  const float f = old / s;
+  uint4 *rows = reinterpret_cast<uint4 *>(a.pool + (size_t)blk * a.bs * a.D);
+  for (int u = tid; u < off * a.D / 16; u += nthreads) {
+    const uint4 w = rows[u];
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 p = f32x2_from_e4m3x2((in[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+      v[2 * i] = p.x * f;
+      v[2 * i + 1] = p.y * f;
+    }
+    rows[u] = pack16(v);
+  }
+  return s;
+}
+
+// The run that begins at row t, by one warp; returns an error status.
+template <typename T, bool kClaimed>
+__device__ __forceinline__ int append_run(const CacheAppendArgs &a, int t, int lane) {
   const int slot = a.slots[t];
-  const int blk = slot / a.bs, off = slot % a.bs;
+  const int blk = slot >> a.log_bs, off = slot & (a.bs - 1);
   // length of the run: up to the block's end
   int n = 1;
   const int most = min(a.bs - off, a.N - t);
@@ -197,91 +279,188 @@ __device__ __forceinline__ void append_run(const CacheAppendArgs &a, int t, int 
     n += k;
     if (k < 32) break;
   }
-  if (a.owner[blk] != t) {
-    if (lane == 0) atomicExch(a.status, HCA_ERR_CACHE);
-    return;
+  int err = HCA_OK;
+  if constexpr (kClaimed) {
+    if (a.owner[blk] != t) return HCA_ERR_CACHE;
+  } else {
+    // another run of the block: the first one of them all is written
+    bool before = false, behind = false;
+    for (int u = lane; u < a.N; u += 32) {
+      const bool same = a.slots[u] >> a.log_bs == blk;
+      before = before || (same && u < t);
+      behind = behind || (same && u >= t + n);
+    }
+    if (__any_sync(0xffffffffu, before || behind)) err = HCA_ERR_CACHE;
+    if (__any_sync(0xffffffffu, before)) return err;
   }
   const T *x = static_cast<const T *>(a.x) + (size_t)t * a.D;
   uint8_t *dst = a.pool + (size_t)slot * a.D;
   const int units = n * a.D / 16;
   float amax = 0.f;
+#pragma unroll 4
   for (int u = lane; u < units; u += 32) {
     float v[16];
     load16(x + (size_t)u * 16, v);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float f = fabsf(v[i]);
-      if (f < INFINITY) amax = fmaxf(amax, f);
-    }
+    amax = fmaxf(amax, finite_max(v));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  float s = exp2_int(scale_exponent(amax));
-  if (off > 0) {
-    const float old = a.scale[blk];
-    if (!(old > 0.f && old < INFINITY)) {
-      if (lane == 0) atomicExch(a.status, HCA_ERR_CACHE);
-    } else if (old < s) {
-      // the block's earlier rows to the larger scale
-      const float f = old / s;
-      uint4 *rows = reinterpret_cast<uint4 *>(a.pool + (size_t)blk * a.bs * a.D);
-      for (int u = lane; u < off * a.D / 16; u += 32) {
-        const uint4 w = rows[u];
-        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 p = f32x2_from_e4m3x2((in[i >> 1] >> (16 * (i & 1))) & 0xffffu);
-          v[2 * i] = p.x * f;
-          v[2 * i + 1] = p.y * f;
-        }
-        rows[u] = pack16(v);
-      }
-    } else {
-      s = old;
-    }
-  }
+  const float s = settle_scale(a, blk, off, amax, lane, 32, err);
   __syncwarp();
   if (lane == 0) a.scale[blk] = s;
   const float inv = 1.f / s;
+#pragma unroll 4
   for (int u = lane; u < units; u += 32) {
     float v[16];
     load16(x + (size_t)u * 16, v);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = fmaf(v[i], 0.f, v[i] * inv);  // an infinity becomes NaN, not 448
-    *reinterpret_cast<uint4 *>(dst + (size_t)u * 16) = pack16(v);
+    *reinterpret_cast<uint4 *>(dst + (size_t)u * 16) = quantise16(v, inv);
   }
+  return err;
+}
+
+// A CTA takes the runs that begin in `rows` consecutive rows: long ones all
+// threads together, so that a block's rows are in flight at once, short ones a
+// warp each.
+constexpr int kChunkThreads = 128, kChunkRows = 64, kLongRun = 8;
+constexpr int kWindow = kChunkRows + 128;  // rows looked at: the last run may go on for a block
+
+template <typename T>
+__global__ void __launch_bounds__(kChunkThreads) hca_cache_append_kernel(const CacheAppendArgs a, int rows) {
+  __shared__ int slot_of[kWindow + 1];       // slots of rows t0 - 1, t0, ...
+  __shared__ uint32_t breaks[kWindow / 32];  // rows that are not behind the one in front
+  __shared__ int lead[kChunkRows], nlead;
+  __shared__ float red[kChunkThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int t0 = blockIdx.x * rows, cnt = min(rows, a.N - t0), limit = a.nblocks * a.bs;
+  for (int i = tid; i <= kWindow; i += kChunkThreads) {
+    const int t = t0 - 1 + i;
+    slot_of[i] = t >= 0 && t < a.N ? a.slots[t] : -2;
+  }
+  if (tid == 0) nlead = 0;
+  __syncthreads();
+  int err = HCA_OK;
+  for (int i = tid; i < kWindow; i += kChunkThreads) {
+    const int s = slot_of[i + 1];
+    const bool brk = s < 0 || (s & (a.bs - 1)) == 0 || slot_of[i] != s - 1;
+    const uint32_t b = __ballot_sync(0xffffffffu, brk);
+    if (lane == 0) breaks[i >> 5] = b;
+    if (i < cnt && s >= limit) err = HCA_ERR_CACHE;
+    // the order of the list does not matter
+    if (i < cnt && brk && s >= 0 && s < limit) lead[atomicAdd(&nlead, 1)] = i;
+  }
+  __syncthreads();
+  auto length = [&](int i) {
+    int w = (i + 1) >> 5;
+    uint32_t b = w < kWindow / 32 ? breaks[w] & (0xffffffffu << ((i + 1) & 31)) : 0;
+    while (!b && ++w < kWindow / 32) b = breaks[w];
+    return (b ? 32 * w + __ffs(b) - 1 : kWindow) - i;
+  };
+  for (int j = 0; j < nlead; ++j) {
+    const int i = lead[j], n = length(i);
+    if (n < kLongRun) continue;
+    const int t = t0 + i, slot = slot_of[i + 1], blk = slot >> a.log_bs, off = slot & (a.bs - 1);
+    if (a.owner[blk] != t) {
+      err = HCA_ERR_CACHE;
+      continue;
+    }
+    const T *x = static_cast<const T *>(a.x) + (size_t)t * a.D;
+    uint8_t *dst = a.pool + (size_t)slot * a.D;
+    const int units = n * a.D / 16;
+    constexpr int kHold = 4;  // units of 16 values that a thread keeps
+    float v[kHold][16];
+    float amax = 0.f;
+    for (int u0 = 0; u0 < units; u0 += kHold * kChunkThreads) {
+#pragma unroll
+      for (int k = 0; k < kHold; ++k) {
+        const int u = u0 + k * kChunkThreads + tid;
+        if (u < units) load16(x + (size_t)u * 16, v[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kHold; ++k)
+        if (u0 + k * kChunkThreads + tid < units) amax = fmaxf(amax, finite_max(v[k]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    __syncthreads();
+    if (lane == 0) red[warp] = amax;
+    __syncthreads();
+    amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const float s = settle_scale(a, blk, off, amax, tid, kChunkThreads, err);
+    __syncthreads();  // every thread has read the old scale
+    if (tid == 0) a.scale[blk] = s;
+    const float inv = 1.f / s;
+    for (int u0 = 0; u0 < units; u0 += kHold * kChunkThreads) {
+#pragma unroll
+      for (int k = 0; k < kHold; ++k) {
+        const int u = u0 + k * kChunkThreads + tid;
+        if (u < units) {
+          if (units > kHold * kChunkThreads) load16(x + (size_t)u * 16, v[k]);  // else it is still there
+          *reinterpret_cast<uint4 *>(dst + (size_t)u * 16) = quantise16(v[k], inv);
+        }
+      }
+    }
+  }
+  for (int j = warp; j < nlead; j += kChunkThreads / 32)
+    if (length(lead[j]) < kLongRun) err = max(err, append_run<T, true>(a, t0 + lead[j], lane));
+  if (__any_sync(0xffffffffu, err != HCA_OK) && lane == 0) atomicExch(a.status, HCA_ERR_CACHE);
+}
+
+template <typename T, bool kClaimed>
+__device__ __forceinline__ int append_row(const CacheAppendArgs &a, int t, int lane) {
+  if (a.slots[t] >= a.nblocks * a.bs) return HCA_ERR_CACHE;
+  return begins_run(a, t) ? append_run<T, kClaimed>(a, t, lane) : HCA_OK;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kAppendThreads) hca_cache_append_kernel(const CacheAppendArgs a) {
-  const int t = blockIdx.x * kRowsPerCta + (threadIdx.x >> 5);
-  if (t >= a.N) return;
+__global__ void __cluster_dims__(kSmallCtas, 1, 1) __launch_bounds__(kSmallThreads)
+    hca_cache_append_small_kernel(const CacheAppendArgs a) {
   const int lane = threadIdx.x & 31;
-  const int s = a.slots[t];
-  if (s >= a.nblocks * a.bs) {
-    if (lane == 0) atomicExch(a.status, HCA_ERR_CACHE);
-    return;
-  }
-  if (begins_run(a, t)) append_run<T>(a, t, lane);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = HCA_OK;
+  int err = HCA_OK;
+  for (int t = (threadIdx.x >> 5) * kSmallCtas + blockIdx.x; t < a.N; t += kSmallWarps)
+    err = max(err, append_row<T, false>(a, t, lane));
+  // the status has been reset before anybody raises it
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (err != HCA_OK && lane == 0) atomicExch(a.status, err);
 }
 
 }  // namespace
 
-cudaError_t cache_plan(const CachePlanArgs &a, cudaStream_t st) {
+size_t cache_plan_ws_bytes(int R) { return kHeaderBytes + align_up(((size_t)R + 1) * sizeof(int32_t)); }
+
+cudaError_t cache_plan(const CachePlanArgs &args, void *ws, cudaStream_t st) {
+  CachePlanArgs a = args;
+  a.status = static_cast<int32_t *>(ws);
+  a.avail = a.status + 1;
+  a.taken = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + kHeaderBytes);
+  a.log_bs = 0;
+  while ((1 << a.log_bs) < a.bs) ++a.log_bs;
   ProfScope prof(kKCachePlan, st);
-  hca_cache_plan_kernel<<<1, kPlanThreads, 0, st>>>(a);
+  // a thread for each request, and for the slots that this CTA writes
+  const int want = std::max(a.R, a.nslots <= kPlanOneCta ? a.nslots : 0);
+  hca_cache_plan_kernel<<<1, std::min(std::max((want + 31) / 32 * 32, 32), kPlanThreads), 0, st>>>(a);
   if (a.nslots > kPlanOneCta)
-    hca_cache_slots_kernel<<<(a.nslots + kSlotsPerCta - 1) / kSlotsPerCta, kSlotThreads, 0, st>>>(a);
+    hca_cache_fill_kernel<<<(a.nslots + kSlotsPerCta - 1) / kSlotsPerCta, kFillThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t cache_append(const CacheAppendArgs &a, cudaStream_t st) {
+cudaError_t cache_append(const CacheAppendArgs &args, cudaStream_t st) {
+  CacheAppendArgs a = args;
+  a.log_bs = 0;
+  while ((1 << a.log_bs) < a.bs) ++a.log_bs;
+  const bool f32 = a.dtype == HCA_F32;
   ProfScope prof(kKCacheAppend, st);
+  if (a.N <= kAppendLook) {
+    if (f32) hca_cache_append_small_kernel<float><<<kSmallCtas, kSmallThreads, 0, st>>>(a);
+    else hca_cache_append_small_kernel<__nv_bfloat16><<<kSmallCtas, kSmallThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
   hca_cache_claim_kernel<<<(a.N + 255) / 256, 256, 0, st>>>(a);
-  const int grid = (a.N + kRowsPerCta - 1) / kRowsPerCta;
-  if (a.dtype == HCA_F32) hca_cache_append_kernel<float><<<grid, kAppendThreads, 0, st>>>(a);
-  else hca_cache_append_kernel<__nv_bfloat16><<<grid, kAppendThreads, 0, st>>>(a);
+  // enough CTAs for every SM, but no more than one for each block of a long prompt
+  const int rows = std::min(std::max(a.N / 1024, 4), kChunkRows);
+  const int grid = (a.N + rows - 1) / rows;
+  if (f32) hca_cache_append_kernel<float><<<grid, kChunkThreads, 0, st>>>(a, rows);
+  else hca_cache_append_kernel<__nv_bfloat16><<<grid, kChunkThreads, 0, st>>>(a, rows);
   return cudaGetLastError();
 }
 

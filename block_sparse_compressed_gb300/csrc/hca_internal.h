@@ -126,10 +126,13 @@ cudaError_t csa_dckv(const BwdArgs &a, const CsaUnion &u, const float *rowstat, 
 struct CachePlanArgs {
   const int32_t *held, *added, *free_blocks, *free_in;
   int32_t *table, *free_out, *start, *slots;
-  int32_t *status;
   int R, cols, bs, m, nblocks, nfree, nslots;
+  // set by cache_plan
+  int32_t *status, *avail, *taken;  // workspace: status, free blocks before, [R + 1] blocks in front of each request
+  int log_bs;
 };
-cudaError_t cache_plan(const CachePlanArgs &a, cudaStream_t st);
+size_t cache_plan_ws_bytes(int R);
+cudaError_t cache_plan(const CachePlanArgs &a, void *ws, cudaStream_t st);
 struct CacheAppendArgs {
   const void *x;
   const int32_t *slots;
@@ -138,6 +141,7 @@ struct CacheAppendArgs {
   int32_t *owner;  // workspace [nblocks]
   int32_t *status;
   int N, D, bs, nblocks, dtype;
+  int log_bs;      // set by cache_append
 };
 cudaError_t cache_append(const CacheAppendArgs &a, cudaStream_t st);
 

@@ -108,7 +108,7 @@ def load(path: str = LIB_PATH):
             lib.hca_csa_attn_fwd.restype = I
             lib.hca_csa_attn_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, P, Z, P]
             lib.hca_csa_attn_bwd.restype = I
-            lib.hca_cache_plan_workspace_size.argtypes = []
+            lib.hca_cache_plan_workspace_size.argtypes = [I]
             lib.hca_cache_plan_workspace_size.restype = Z
             lib.hca_cache_plan.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, Z, P]
             lib.hca_cache_plan.restype = I
@@ -541,7 +541,11 @@ def _fits(t: torch.Tensor, name: str, shape, dtype, device) -> int:
 
 
 _I32, _F32, _E4M3 = torch.int32, torch.float32, torch.float8_e4m3fn
-_PLAN_WS = 256
+
+
+@functools.lru_cache(maxsize=4096)
+def _plan_ws_bytes(R: int) -> int:
+    return load().hca_cache_plan_workspace_size(R)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -574,7 +578,7 @@ def hca_cache_plan(held: torch.Tensor, added: torch.Tensor, table: torch.Tensor,
     start = torch.empty(R + 1, dtype=_I32, device=dev) if start is None else start
     slots = torch.empty(nslots, dtype=_I32, device=dev) if slots is None else slots
     free_left = torch.empty(1, dtype=_I32, device=dev) if free_left is None else free_left
-    ws = torch.empty(_PLAN_WS, dtype=torch.uint8, device=dev) if ws is None else ws
+    ws = torch.empty(_plan_ws_bytes(R), dtype=torch.uint8, device=dev) if ws is None else ws
     rc = _enqueue(dev, lib.hca_cache_plan, _fits(held, "held", (R,), _I32, dev), _fits(added, "added", (R,), _I32, dev),
                   _fits(table, "table", (R, cols), _I32, dev), _fits(free_blocks, "free_blocks", (nfree,), _I32, dev),
                   _fits(free_count, "free_count", (1,), _I32, dev), _fits(free_left, "free_left", (1,), _I32, dev),

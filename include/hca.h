@@ -306,8 +306,9 @@ HCA_API int hca_indexer_topk(const void *qi, const void *ki, const float *w, con
  * A plan that needs more blocks or slots than there are (HCA_ERR_CAPACITY), or
  * a length out of range (HCA_ERR_CACHE), changes nothing: start is all 0, slots
  * all -1, free_out is free_in, and the table stays.  A block id outside
- * [0, nblocks) gives slots of -1 (HCA_ERR_CACHE). */
-HCA_API size_t hca_cache_plan_workspace_size(void);
+ * [0, nblocks) gives slots of -1 (HCA_ERR_CACHE).  Workspace:
+ * hca_cache_plan_workspace_size(R) bytes. */
+HCA_API size_t hca_cache_plan_workspace_size(int R);
 HCA_API int hca_cache_plan(const int32_t *held, const int32_t *added, int32_t *table, const int32_t *free_blocks,
                            const int32_t *free_in, int32_t *free_out, int32_t *start, int32_t *slots, int R, int cols,
                            int bs, int m, int nblocks, int nfree, int nslots, void *workspace, size_t workspace_bytes,

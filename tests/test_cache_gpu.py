@@ -101,7 +101,7 @@ def test_plan_that_does_not_fit_changes_nothing(what, status, big):
         count = nfree + 1
     if what == "long":
         held[1] = (1 << 30) - 50
-    ws = torch.empty(256, dtype=torch.uint8, device=DEV)
+    ws = torch.empty(hca.load().hca_cache_plan_workspace_size(R), dtype=torch.uint8, device=DEV)
     start, slots, left = hca.hca_cache_plan(i32(held), i32(added), table, i32(list(range(nfree))), i32([count]), nfree, bs,
                                             nslots, ws=ws)
     assert hca.hca_workspace_status(ws) == status
@@ -111,7 +111,7 @@ def test_plan_that_does_not_fit_changes_nothing(what, status, big):
 
 def test_plan_gives_no_slot_for_a_bad_block():
     table = torch.full((2, 3), -1, dtype=torch.int32, device=DEV)
-    ws = torch.empty(256, dtype=torch.uint8, device=DEV)
+    ws = torch.empty(512, dtype=torch.uint8, device=DEV)
     _, slots, _ = hca.hca_cache_plan(i32([0, 0]), i32([20, 3]), table, i32([1, 99, 0]), i32([3]), 8, 16, 23, ws=ws)
     assert hca.hca_workspace_status(ws) == E_CACHE
     assert slots.tolist() == [0 * 16 + k for k in range(16)] + [-1] * 4 + [16, 17, 18]
@@ -155,9 +155,10 @@ def test_append_matches_oracle(D, bs, dtype):
     assert torch.equal(again.view(torch.uint8), p.view(torch.uint8)) and torch.equal(s, s2)
 
 
-def test_append_many_rows():
+@pytest.mark.parametrize("N", [1500, 20011, 70001])
+def test_append_many_rows(N):
     # a long prompt: blocks in random order, whole and cut ones
-    N, D, bs, nblocks = 20011, 128, 64, 400
+    D, bs, nblocks = 128, 64, N // 64 + 90
     perm = np.random.default_rng(1).permutation(nblocks)
     slots = [int(perm[(k + 37) // bs]) * bs + (k + 37) % bs for k in range(N)]
     x, _, pool, scale = _append_inputs(N, D, bs, BF16, 9, [], nblocks)
@@ -190,6 +191,24 @@ def test_append_values_at_the_edges(dtype):
     np.testing.assert_array_equal(s.cpu().double().numpy(), ws)
     np.testing.assert_array_equal(values(p), want)
     assert ws[0] == 1.0 and ws[1] == (1.0 if dtype == BF16 else 2.0) and ws[5] == 2.0 ** -96
+
+
+@pytest.mark.parametrize("N", [255, 256, 257, 1025])
+def test_append_single_rows(N):
+    # a decode step: every row a run of its own, in a block that holds others
+    D, bs, nblocks = 64, 16, N + 3
+    perm = np.random.default_rng(N).permutation(nblocks)
+    slots = [int(perm[k]) * bs + (5 * k) % bs for k in range(N)]
+    x, _, pool, scale = _append_inputs(N, D, bs, BF16, N, [], nblocks)
+    want, ws = OC.append(x.float().double().numpy(), slots, values(pool), scale.double().numpy())
+    p, s = pool.to(DEV), scale.to(DEV)
+    hca.hca_cache_append(x.to(DEV), i32(slots), p, s, check=True)
+    np.testing.assert_array_equal(s.cpu().double().numpy(), ws)
+    np.testing.assert_array_equal(values(p), want)
+    # one slot again at the end: reported, whichever way the rows are taken
+    ws = torch.empty(hca.load().hca_cache_append_workspace_size(nblocks), dtype=torch.uint8, device=DEV)
+    hca.hca_cache_append(x.to(DEV), i32(slots[:-1] + [slots[0]]), p, s, ws=ws)
+    assert hca.hca_workspace_status(ws) == E_CACHE
 
 
 def test_append_touches_nothing_else():

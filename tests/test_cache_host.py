@@ -25,7 +25,7 @@ def test_status_strings(lib):
 
 def _plan(lib, **kw):
     a = dict(held=16, added=16, table=16, free=16, fin=16, fout=16, start=16, slots=16, R=4, cols=2, bs=16, m=1, nblocks=8,
-             nfree=8, nslots=10, ws=256, wsb=256)
+             nfree=8, nslots=10, ws=256, wsb=512)
     a.update(kw)
     return lib.hca_cache_plan(*[P(a[k]) for k in ("held", "added", "table", "free", "fin", "fout", "start", "slots")],
                               a["R"], a["cols"], a["bs"], a["m"], a["nblocks"], a["nfree"], a["nslots"], P(a["ws"]),
@@ -37,7 +37,7 @@ def _plan(lib, **kw):
     (dict(nblocks=1 << 28), E_SHAPE), (dict(bs=24), E_ARG), (dict(bs=256), E_ARG), (dict(m=0), E_ARG),
     (dict(held=None), E_NULL), (dict(added=None), E_NULL), (dict(table=None), E_NULL), (dict(free=None), E_NULL),
     (dict(fin=None), E_NULL), (dict(fout=None), E_NULL), (dict(start=None), E_NULL), (dict(slots=None), E_NULL),
-    (dict(ws=None), E_WS), (dict(ws=128), E_WS), (dict(wsb=255), E_WS),
+    (dict(ws=None), E_WS), (dict(ws=128), E_WS), (dict(wsb=256), E_WS),
 ])
 def test_plan_refusals(lib, kw, want):
     assert _plan(lib, **kw) == want
@@ -90,9 +90,9 @@ def test_workspace_sizes(lib):
     assert f(64, 64, 64, 128, 0) > 0 and f(64, 64, 64, 96, 0) == 0 and f(64, 64, 64, 96, 1) > 0
     assert f(64, 64, 0, 128, 0) == 0 and f(64, 64, 64, 128, 5) == 0 and f(-1, 64, 64, 128, 0) == 0
     # grows with the tokens, not with the cache
-    assert f(65536, 4, 64, 128, 0) < f(4, 4, 64, 128, 0) + 65536 * 128
+    assert f(65536, 4, 64, 128, 0) < f(256, 4, 64, 128, 0) + 65536 * 128
     assert lib.hca_cache_append_workspace_size(1000) >= 4000 and lib.hca_cache_append_workspace_size(-1) == 0
-    assert lib.hca_cache_plan_workspace_size() >= 4
+    assert lib.hca_cache_plan_workspace_size(1000) >= 4000 and lib.hca_cache_plan_workspace_size(-1) == 0
 
 
 def test_binding_checks_tensors():
