@@ -326,6 +326,7 @@ __global__ void __launch_bounds__(kCombineThreads) hca_cache_combine_kernel(cons
   __shared__ int before[kMaxBorders + 1];
   __shared__ long long tmp[33];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  tc::pdl_wait();
   const int per = (p.grid + kCombineThreads - 1) / kCombineThreads, i0 = tid * per, i1 = min(i0 + per, p.grid);
   int worst = HCA_OK, items = 0;
   for (int i = i0; i < i1; ++i) {
@@ -510,8 +511,19 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
   }
   {
     ProfScope prof(kKCacheCombine, st);
-    if (a.dtype == HCA_F32) hca_cache_combine_kernel<float><<<4 * sms, kCombineThreads, 0, st>>>(p);
-    else hca_cache_combine_kernel<__nv_bfloat16><<<4 * sms, kCombineThreads, 0, st>>>(p);
+    // its blocks are set up while the attention's last CTAs run
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(4 * sms);
+    cfg.blockDim = dim3(kCombineThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = a.dtype == HCA_F32 ? cudaLaunchKernelEx(&cfg, hca_cache_combine_kernel<float>, p)
+                                             : cudaLaunchKernelEx(&cfg, hca_cache_combine_kernel<__nv_bfloat16>, p);
+    if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();
 }

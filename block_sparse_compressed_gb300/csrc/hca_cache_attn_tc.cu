@@ -38,6 +38,7 @@
 #include <cuda_bf16.h>
 
 #include <cfloat>
+#include <type_traits>
 
 #include "hca_cache_attn.cuh"
 #include "tc_tiles.cuh"
@@ -114,6 +115,11 @@ __device__ __forceinline__ void st_shared(uint32_t addr, uint32_t a, uint32_t b,
 __device__ __forceinline__ void ld_shared(uint32_t addr, uint32_t (&v)[4]) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
 }
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // 16 bytes of which the first n come from p and the others are 0
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *p, uint32_t n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
@@ -159,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       mbar_init(&sh.kv_full[s], kWG);
       mbar_init(&sh.kv_empty[s], 1);
     }
-    mbar_init(&sh.q_full, 64);
+    mbar_init(&sh.q_full, 64 + kWG);
     mbar_init(&sh.q_free, kWG);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&sh.s_full[h], 1);
@@ -186,13 +192,13 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
     Group g;
     g.ntiles = 0;
     bool mine = n == 1;
-    if (!__syncthreads_or(n > 1)) {
-      if (mine && ok) ok = chunk_group(p, tid, 0, g);
-    } else {
+    if (mine) ok = chunk_group(p, tid, 0, g);
+    if (__syncthreads_or(n > 1)) {
       const long long chunks = block_scan(n, sh.scan, all);
       if (tid < p.R) sh.gbase[tid] = (int)chunks;
       ok = __syncthreads_and(ok);
       mine = ok && tid < all;
+      g.ntiles = 0;
       if (mine) {
         int lo = 0, hi = p.R;  // gbase[lo] <= tid < gbase[hi]
         while (hi - lo > 1) {
@@ -227,10 +233,9 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       }
       return before + x - v;
     };
-    ok = __syncthreads_and(ok);
     int ngroups, index;
     const long long before = scan_tiles(mine ? g.ntiles : 0, sh.sums[0], ntiles, ngroups, index);
-    if (!ok) ntiles = -1;
+    if (!__syncthreads_and(ok)) ntiles = -1;
     // Ranges that no group's border cuts give a CTA tiles of one group only and
     // save it a second one's beginning and end, about two tiles' time each;
     // ceil(tiles / quota) of them for each group fit the grid with a larger quota.
@@ -289,12 +294,61 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
     p.err[blockIdx.x] = ntiles < 0 ? HCA_ERR_CACHE : HCA_OK;
     if (!busy) p.border[blockIdx.x] = Border{0, 0, 0, 0};
   }
+  pdl_launch_dependents();  // the combine kernel waits for this one's end by itself
   auto segment = [&](int k) { return k < kMaxSegs ? sh.seg[k] : segment_of(p.groups[sh.first + k], c0, c1, blockIdx.x); };
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
   const int ppt = kTileKeys >> p.log_bs;  // pages per tile: a power of two, 1 .. 8
+  // Half of the rows of a group's q into shared memory, by `threads` threads: copied
+  // as they are (asynchronously, all in flight), then each thread turns the
+  // pieces that it copied into fp16 in their place.  D / 8 neighbouring lanes
+  // have a row's 16-byte pieces, so its largest value is a few shuffles away.
+  auto load_q = [&](const Segment &g, int k, int t, auto threads, int half) {
+    constexpr int kLanes = D / 8, step = decltype(threads)::value / kLanes;  // rows at a time
+    static_assert((NQ / 2) % step == 0, "rows divide evenly");
+    const int ch = t % kLanes, r0 = half * (NQ / 2), r1 = r0 + NQ / 2;
+    const int nreal = real_columns(p, g.npos, g.slice());
+    const uint32_t dst = smem_u32(smem) + C::kOffQ + (ch >> 3) * kHalfTile;
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)g.row0 * p.H + g.slice() * p.HS) * D + ch * 8;
+#pragma unroll 4
+    for (int c = r0 + t / kLanes; c < r1; c += step)  // rows beyond the group's are zero
+      cp_async_16(dst + c * 128 + (((ch & 7) ^ (c & 7)) << 4), c < nreal ? q + (size_t)c * D : q, c < nreal ? 16 : 0);
+    cp_async_wait();
+    // four rows at a time, step by step, so that their latencies overlap
+    constexpr int kBatch = NQ / 2 / step < 4 ? NQ / 2 / step : 4;
+    for (int c = r0 + t / kLanes; c < r1; c += kBatch * step) {
+      uint32_t w[kBatch][4], amax[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) ld_shared(dst + (c + i * step) * 128 + (((ch & 7) ^ ((c + i * step) & 7)) << 4), w[i]);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        amax[i] = bf16x2_max(bf16x2_max(w[i][0] & 0x7fff7fffu, w[i][1] & 0x7fff7fffu),
+                             bf16x2_max(w[i][2] & 0x7fff7fffu, w[i][3] & 0x7fff7fffu));
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) amax[i] = bf16x2_max(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], o));
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        // the largest |q| becomes 224 .. 448; a negative scale goes into q's sign
+        // (of a row with an infinity nothing but NaN comes, whatever the factor)
+        const int ex = scale_exponent(__uint_as_float(max(amax[i] & 0xffffu, amax[i] >> 16) << 16)), ci = c + i * step;
+        const float inv = p.scale < 0.f ? -exp2_int(-ex) : p.scale > 0.f ? exp2_int(-ex) : 0.f;
+        if (ch == 0) sh.q_factor[k & 1][ci] = exp2_int(ex) * fabsf(p.scale) * 1.4426950408889634f;
+        uint32_t f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          f[e] = f16x2_rn(__uint_as_float(w[i][e] << 16) * inv, __uint_as_float(w[i][e] & 0xffff0000u) * inv);
+#pragma unroll
+        for (int y = 0; y < C::kCopies; ++y)
+          st_shared(dst + (ci + y * NQ) * 128 + (((ch & 7) ^ (ci & 7)) << 4), f[0], f[1], f[2], f[3]);
+      }
+    }
+    fence_async_smem();
+  };
+
   if (warp >= 8) {
     setmaxnreg_dec<C::kRegsIssue>();
     if (warp == 8 && busy) {
@@ -451,63 +505,12 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
     }
     else if (warp >= 10 && busy) {
       // ------------------------------------------------------------ q
-      // A group's q into shared memory once every product with the last one's
-      // has been made: copied as it is (asynchronously, all rows in flight), then
-      // each thread turns the pieces that it copied into fp16 in their place.
-      // D / 8 neighbouring lanes have a row's 16-byte pieces, so its largest
-      // value is a few shuffles away.
-      constexpr int kLanes = D / 8, kRows = 64 / kLanes;  // lanes of a row, rows at a time
-      const int t64 = tid - 320, ch = t64 % kLanes, c0q = t64 / kLanes;
-      const uint32_t dst = smem_u32(smem) + C::kOffQ + (ch >> 3) * kHalfTile;
-      bool ok = true;
-      for (int k = 0; ok; ++k) {
+      for (int k = 0;; ++k) {
         const Segment g = segment(k);
-        const int nreal = real_columns(p, g.npos, g.slice());
-        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)g.row0 * p.H + g.slice() * p.HS) * D + ch * 8;
-#pragma unroll 4
-        for (int c = c0q; c < NQ; c += kRows)  // rows beyond the group's are zero
-          cp_async_16(dst + c * 128 + (((ch & 7) ^ (c & 7)) << 4), c < nreal ? q + (size_t)c * D : q, c < nreal ? 16 : 0);
-        cp_async_wait();
-        // four rows at a time, step by step, so that their latencies overlap
-        constexpr int kBatch = NQ / kRows < 4 ? NQ / kRows : 4;
-        for (int c = c0q; c < NQ; c += kBatch * kRows) {
-          uint32_t w[kBatch][4];
-          float amax[kBatch];
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) ld_shared(dst + (c + i * kRows) * 128 + (((ch & 7) ^ ((c + i * kRows) & 7)) << 4), w[i]);
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            amax[i] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float a = fabsf(__uint_as_float(w[i][e] << 16)), b = fabsf(__uint_as_float(w[i][e] & 0xffff0000u));
-              if (a < INFINITY) amax[i] = fmaxf(amax[i], a);
-              if (b < INFINITY) amax[i] = fmaxf(amax[i], b);
-            }
-          }
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], o));
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            // the largest |q| becomes 224 .. 448; a negative scale goes into q's sign
-            const int ex = scale_exponent(amax[i]), ci = c + i * kRows;
-            const float inv = p.scale < 0.f ? -exp2_int(-ex) : p.scale > 0.f ? exp2_int(-ex) : 0.f;
-            if (ch == 0) sh.q_factor[k & 1][ci] = exp2_int(ex) * fabsf(p.scale) * 1.4426950408889634f;
-            uint32_t f[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              f[e] = f16x2_rn(__uint_as_float(w[i][e] << 16) * inv, __uint_as_float(w[i][e] & 0xffff0000u) * inv);
-#pragma unroll
-            for (int y = 0; y < C::kCopies; ++y)
-              st_shared(dst + (ci + y * NQ) * 128 + (((ch & 7) ^ (ci & 7)) << 4), f[0], f[1], f[2], f[3]);
-          }
-        }
-        fence_async_smem();
+        load_q(g, k, tid - 320, std::integral_constant<int, 64>(), 0);
         mbar_arrive(&sh.q_full);
         if (g.last()) break;
-        ok = wait_idle(&sh.q_free, k & 1, abort_flag, status, p.wait_ns);
+        if (!wait_idle(&sh.q_free, k & 1, abort_flag, status, p.wait_ns)) break;
       }
     }
   } else if (warp >= 4) {
@@ -613,6 +616,9 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       uint32_t n = 0;
       for (int k = 0;; ++k) {
         const Segment g = segment(k);
+        if (k > 0) (void)wait(&sh.q_free, (k - 1) & 1);
+        load_q(g, k, tid, std::integral_constant<int, kWG>(), 1);
+        mbar_arrive(&sh.q_full);
         const int nreal = real_columns(p, g.npos, g.slice());
         const int pos = g.pos0 + (row < nreal ? row / p.HS : 0);
         // what the row sees: raw keys [raw_lo, pos], entries [0, entries)
