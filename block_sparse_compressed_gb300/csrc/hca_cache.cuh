@@ -93,12 +93,13 @@ __device__ __forceinline__ long long block_scan(long long v, long long *tmp, lon
 // reference exponent and its sum) in each CTA it touches, joined by the combine
 // kernel.
 struct __align__(16) Group {
-  long long tile0;  // first tile in the line
+  int tile0;        // first tile in the line
   int ntiles;
   int r;            // request
   int row0;         // row of the first position in q / out
   int pos0, npos;   // first position, positions
   int slice;        // head slice
+  int pad;
 };
 
 // A CTA's piece of a group.
@@ -120,10 +121,13 @@ struct __align__(16) Border {
   int slot;     // of the first part; the others have slot 2 (c + i)
 };
 
+// The line has less than 2^31 tiles, or the call is refused.
+constexpr long long kMaxTiles = 0x7fff0000ll;
+
 struct SchedHeader {  // at the start of the workspace
   int32_t status;
   int32_t ngroups;
-  long long ntiles;   // -1: refused, the attention fills its outputs with NaN
+  int32_t ntiles;     // -1: refused, the attention fills its outputs with NaN
 };
 
 struct Pages {
@@ -137,21 +141,18 @@ __device__ __forceinline__ Pages group_pages(int pos0, int npos, int W, int m, i
   g.rp0 = max(0, pos0 - W + 1) >> log_bs;
   g.nraw = (last >> log_bs) - g.rp0 + 1;
   const int ent = comp ? (last + 1) / m : 0;
-  g.ncomp = (int)(((long long)ent + (1 << log_bs) - 1) >> log_bs);
+  g.ncomp = (ent + (1 << log_bs) - 1) >> log_bs;
   return g;
 }
 
-// tiles per CTA (the 64-bit division is several times the 32-bit one)
-__device__ __forceinline__ long long cta_quota(long long ntiles, int grid, int min_tiles) {
-  if (ntiles <= 0) return min_tiles;
-  const unsigned long long n = (unsigned long long)ntiles + grid - 1;
-  const long long q = n >> 32 ? (long long)(n / grid) : (long long)((uint32_t)n / (uint32_t)grid);
-  return q > min_tiles ? q : min_tiles;
+// tiles per CTA
+__device__ __forceinline__ int cta_quota(int ntiles, int grid, int min_tiles) {
+  return max((int)(((uint32_t)max(ntiles, 0) + grid - 1) / (uint32_t)grid), min_tiles);
 }
 
 // Index of the group that holds tile t (all lanes of a warp call it): a search
 // that narrows 32-fold a step, since each step is one dependent load.
-__device__ __forceinline__ int find_group(const Group *groups, int n, long long t) {
+__device__ __forceinline__ int find_group(const Group *groups, int n, int t) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = n;  // groups[lo].tile0 <= t, hi is past the answer
   while (hi - lo > 1) {

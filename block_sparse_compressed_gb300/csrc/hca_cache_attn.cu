@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kSchedThreads) hca_cache_sched_kernel(const At
   long long chunks = 0;
   for (int r0 = 0; r0 < p.R; r0 += kSchedThreads) {
     const int r = r0 + tid;
-    long long n = 0;
+    int n = 0;
     if (r < p.R) ok = request_chunks(p, r, n) && ok;
     long long all;
     const long long before = block_scan(n, tmp, all);
@@ -64,16 +64,16 @@ __global__ void __launch_bounds__(kSchedThreads) hca_cache_sched_kernel(const At
     if (c < chunks) {
       for (int s = 0; s < p.slices; ++s) {
         g.slice = s;
-        g.tile0 = (line + before) * p.slices + (long long)s * g.ntiles;
+        g.tile0 = (int)((line + before) * p.slices + (long long)s * g.ntiles);  // of use if all of it fits
         p.groups[c * p.slices + s] = g;
       }
     }
     line += all;
   }
-  ok = __syncthreads_and(ok);
+  ok = __syncthreads_and(ok) && line * p.slices < kMaxTiles;
   if (tid == 0) {
     p.hdr->ngroups = (int)(chunks * p.slices);
-    p.hdr->ntiles = ok ? line * p.slices : -1;
+    p.hdr->ntiles = ok ? (int)(line * p.slices) : -1;
   }
 }
 
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
   extern __shared__ uint8_t keys[];  // [128][D + 4] bytes: a row's words fall into different banks
   __shared__ SimtShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long ntiles = p.hdr->ntiles;
+  const int ntiles = p.hdr->ntiles;
   if (tid == 0) {
     p.err[blockIdx.x] = ntiles < 0 ? HCA_ERR_CACHE : HCA_OK;
     p.border[blockIdx.x] = Border{0, 0, 0, 0};
@@ -133,9 +133,9 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
     poison<float>(p);
     return;
   }
-  const long long quota = cta_quota(ntiles, p.grid, p.min_tiles);
-  const long long c0 = quota * blockIdx.x, c1 = min(c0 + quota, ntiles);
-  if (c0 >= c1) return;
+  const int quota = cta_quota(ntiles, p.grid, p.min_tiles);
+  if (blockIdx.x >= (ntiles + quota - 1) / quota) return;
+  const int c0 = quota * blockIdx.x, c1 = min(c0 + quota, ntiles);
   if (warp == 0) {
     const int g = find_group(p.groups, p.hdr->ngroups, c0);
     if (lane == 0) sh.first = g;
@@ -487,7 +487,7 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
   p.part_o = reinterpret_cast<float *>(ws + l.off_o);
   p.N = a.N; p.R = a.R; p.H = a.H; p.D = a.D; p.W = a.W; p.m = a.m; p.log_bs = log2_int(a.bs);
   p.HS = l.HS; p.slices = l.slices; p.P = l.P; p.NQ = l.NQ;
-  p.scale = a.scale; p.wait_ns = a.wait_ns; p.stall = a.stall;
+  p.scale = a.scale; p.wait_ns = std::min<uint64_t>(a.wait_ns, 4000000000u); p.stall = a.stall;
   const int sms = tc::sm_count();
   if (sms <= 0) return cudaErrorNoDevice;
   const bool tcs = on_tensor_cores(a.dtype);

@@ -40,12 +40,12 @@ __device__ __forceinline__ int real_columns(const AttnParams &p, int npos, int s
 }
 
 // Tiles [c0, c1) of the line and what of group g lies in them.
-__device__ __forceinline__ Segment segment_of(const Group &g, long long c0, long long c1, int cta) {
+__device__ __forceinline__ Segment segment_of(const Group &g, int c0, int c1, int cta) {
   Segment s;
-  const long long a = g.tile0 > c0 ? g.tile0 : c0, end = g.tile0 + g.ntiles, b = end < c1 ? end : c1;
+  const int a = max(g.tile0, c0), b = min(g.tile0 + g.ntiles, c1);
   s.r = g.r; s.row0 = g.row0; s.pos0 = g.pos0; s.npos = g.npos;
-  s.j0 = (int)(a - g.tile0);
-  s.j1 = (int)(b - g.tile0);
+  s.j0 = a - g.tile0;
+  s.j1 = b - g.tile0;
   // the group that enters the CTA's range from before it takes slot 0
   s.slot = s.j0 == 0 && s.j1 == g.ntiles ? -1 : 2 * cta + (a == c0 ? 0 : 1);
   s.slice_last = 2 * g.slice + (b == c1 ? 1 : 0);
@@ -53,24 +53,23 @@ __device__ __forceinline__ Segment segment_of(const Group &g, long long c0, long
 }
 
 // The join at the end of this CTA's range, if its last group begins in it.
-__device__ __forceinline__ Border border_of(const AttnParams &p, const Group &g, long long c0, long long c1,
-                                            long long quota, int cta) {
+__device__ __forceinline__ Border border_of(const AttnParams &p, const Group &g, int c0, int c1, int quota, int cta) {
   Border x = {0, 0, 0, 0};
-  const long long end = g.tile0 + g.ntiles;
+  const int end = g.tile0 + g.ntiles;
   if (g.tile0 >= c0 && end > c1) {
     x.row = g.row0 * p.H + g.slice * p.HS;
     x.columns = real_columns(p, g.npos, g.slice);
-    x.parts = (int)((end - 1) / quota) - cta + 1;
+    x.parts = (end - 1) / quota - cta + 1;
     x.slot = 2 * cta + (g.tile0 == c0 ? 0 : 1);
   }
   return x;
 }
 
 // Chunks (groups before slicing) of request r; false: lengths out of range.
-__device__ __forceinline__ bool request_chunks(const AttnParams &p, int r, long long &n) {
-  const long long s0 = p.start[r], s1 = p.start[r + 1], h = p.held[r], T = s1 - s0;
-  const bool ok = T >= 0 && s0 >= 0 && s1 <= p.N && h >= 0 && h + T <= kMaxPos && (r > 0 || s0 == 0);
-  n = ok ? (T + p.P - 1) / p.P : 0;
+__device__ __forceinline__ bool request_chunks(const AttnParams &p, int r, int &n) {
+  const int s0 = p.start[r], s1 = p.start[r + 1], h = p.held[r];
+  const bool ok = s0 >= 0 && s1 >= s0 && s1 <= p.N && h >= 0 && h <= kMaxPos - (s1 - s0) && (r > 0 || s0 == 0);
+  n = ok ? (s1 - s0 + p.P - 1) / p.P : 0;
   return ok;
 }
 
@@ -83,7 +82,7 @@ __device__ __forceinline__ bool chunk_group(const AttnParams &p, int r, int k, G
   g.npos = min(p.P, T - first);
   g.slice = 0;
   const Pages pg = group_pages(g.pos0, g.npos, p.W, p.m, p.log_bs, p.comp.table != nullptr);
-  g.ntiles = (int)((((long long)(pg.nraw + pg.ncomp) << p.log_bs) + kTileKeys - 1) / kTileKeys);
+  g.ntiles = (int)((((uint32_t)(pg.nraw + pg.ncomp) << p.log_bs) + kTileKeys - 1) / kTileKeys);
   // the raw table keeps the last cols pages of the request's tokens
   return ((h + T - 1) >> p.log_bs) - pg.rp0 < p.raw.cols && pg.ncomp <= p.comp.cols;
 }

@@ -54,7 +54,7 @@ constexpr int kMetaStages = 4;  // tiles whose pages are looked up ahead
 constexpr int kStages = 2;      // fp16 tiles
 constexpr int kMaxSegs = 64;    // pieces of groups listed in shared memory
 constexpr int kWG = 128;
-constexpr int kThreads = 3 * kWG;  // softmax | converter | page warp, MMA warp, two q warps
+constexpr int kThreads = 3 * kWG;  // softmax | converter | page and MMA warp
 constexpr int kTmem = 256;      // S of keys 0 .. 63 | S of keys 64 .. 127 (P takes the first half of each) | O
 constexpr uint32_t kColO = 128;
 
@@ -85,13 +85,13 @@ template <int NQ, int D>
 struct Shared {
   uint64_t meta_full[kMetaStages], meta_empty[kMetaStages];
   uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t q_full, q_free, s_full[2], p_full[2], pv_done[2], drain, never;
+  uint64_t q_full, s_full[2], p_full[2], pv_done[2], drain, never;
   uint64_t scale_full[kMetaStages];
   PageMeta meta[kMetaStages][8];
   uint32_t nan_keys[kMetaStages][4];  // keys whose rows hold a NaN that not everybody sees
   int nan_any[kMetaStages];
   int all_seen[kMetaStages];          // bit h: every row sees every key of half h
-  float q_factor[2][NQ];                         // log2(e) |scale| / (a row's factor), of two groups in turn
+  float q_factor[NQ];                            // log2(e) |scale| / (a row's factor)
   // the CTA's pieces of groups, in order; what there is no room for is in the
   // workspace's groups
   Segment seg[kMaxSegs];
@@ -140,11 +140,6 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &a, uint32_t 
       : "r"(w));
 }
 
-__device__ __forceinline__ bool wait_idle(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status,
-                                          uint64_t limit_ns) {
-  return __all_sync(0xffffffffu, mbar_wait_idle(bar, parity, abort, status, limit_ns));
-}
-
 template <int NQ, int D>
 __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnParams p) {
   using C = Cfg<NQ, D>;
@@ -165,8 +160,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       mbar_init(&sh.kv_full[s], kWG);
       mbar_init(&sh.kv_empty[s], 1);
     }
-    mbar_init(&sh.q_full, 64 + kWG);
-    mbar_init(&sh.q_free, kWG);
+    mbar_init(&sh.q_full, kWG);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&sh.s_full[h], 1);
       mbar_init(&sh.p_full[h], kWG);
@@ -182,37 +176,38 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
     tmem_relinquish();
   }
   // the CTA's range of the line, and its pieces of groups
-  long long ntiles, quota, c0, c1;
-  bool busy;
+  int ntiles, quota, c0 = 0, c1 = 0;
+  bool busy = false;
   if (p.in_cta) {
     // one thread per request; where some bring more than one group, one per group
-    long long n = 0, all;
+    int n = 0, r = tid, k = 0;
     bool ok = true;
     if (tid < p.R) ok = request_chunks(p, tid, n);
-    Group g;
-    g.ntiles = 0;
     bool mine = n == 1;
-    if (mine) ok = chunk_group(p, tid, 0, g);
     if (__syncthreads_or(n > 1)) {
+      long long all;
       const long long chunks = block_scan(n, sh.scan, all);
       if (tid < p.R) sh.gbase[tid] = (int)chunks;
-      ok = __syncthreads_and(ok);
-      mine = ok && tid < all;
-      g.ntiles = 0;
-      if (mine) {
-        int lo = 0, hi = p.R;  // gbase[lo] <= tid < gbase[hi]
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (sh.gbase[mid] <= tid) lo = mid; else hi = mid;
-        }
-        ok = chunk_group(p, lo, tid - sh.gbase[lo], g);
+      __syncthreads();
+      mine = tid < all;
+      int hi = p.R;  // gbase[r] <= tid < gbase[hi]
+      for (r = 0; hi - r > 1;) {
+        const int mid = (r + hi) >> 1;
+        if (sh.gbase[mid] <= tid) r = mid; else hi = mid;
       }
+      k = tid - sh.gbase[r];
     }
+    ok = __syncthreads_and(ok);
+    Group g;
+    g.ntiles = 0;
+    mine = mine && ok;
+    if (mine) ok = chunk_group(p, r, k, g);
     // Tiles and groups before this one: within the warp, then over the warps in
     // front.  A warp's groups have less than 2^31 tiles (2^25 each at most).
-    auto scan_tiles = [&](int v, int2 *sums, long long &total, int &groups, int &index) {
+    int ngroups, index;
+    auto scan_tiles = [&](int v, int2 *sums, long long &total) {
       int x = v;
-#pragma unroll
+#pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
@@ -220,45 +215,36 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       const uint32_t b = __ballot_sync(0xffffffffu, mine);
       if (lane == 31) sums[warp] = make_int2(x, __popc(b));
       __syncthreads();
-      long long before = 0;
+      int before = x - v;
       total = 0;
-      groups = 0;
+      ngroups = 0;
       index = __popc(b & ((1u << lane) - 1u));
-#pragma unroll
+#pragma unroll 1
       for (int w = 0; w < kThreads / 32; ++w) {
         const int2 s = sums[w];
         if (w < warp) before += s.x, index += s.y;
         total += s.x;
-        groups += s.y;
+        ngroups += s.y;
       }
-      return before + x - v;
+      return before;
     };
-    int ngroups, index;
-    const long long before = scan_tiles(mine ? g.ntiles : 0, sh.sums[0], ntiles, ngroups, index);
-    if (!__syncthreads_and(ok)) ntiles = -1;
+    long long total;
+    g.tile0 = scan_tiles(mine ? g.ntiles : 0, sh.sums[0], total);
+    ntiles = __syncthreads_and(ok) && total < kMaxTiles ? (int)total : -1;
     // Ranges that no group's border cuts give a CTA tiles of one group only and
     // save it a second one's beginning and end, about two tiles' time each;
     // ceil(tiles / quota) of them for each group fit the grid with a larger quota.
-    const long long cut = cta_quota(ntiles, p.grid, p.min_tiles);
-    const long long own = cta_quota(ntiles, max(p.grid - ngroups, 1), p.min_tiles);
-    const bool whole_groups = ngroups < p.grid && own <= cut + 2;
-    bool in;
+    quota = cta_quota(ntiles, p.grid, p.min_tiles);
+    const int own = cta_quota(ntiles, max(p.grid - ngroups, 1), p.min_tiles);
+    const bool whole_groups = ngroups < p.grid && own <= quota + 2;
     if (whole_groups) {
       quota = own;
-      const int q32 = (int)quota;  // a group's share of the tiles fits
-      g.tile0 = quota * scan_tiles(mine ? (g.ntiles + q32 - 1) / q32 : 0, sh.sums[1], all, ngroups, index);
-      c0 = quota * blockIdx.x;
-      c1 = c0 + quota;
-      in = mine && ntiles > 0 && g.tile0 <= c0 && c0 < g.tile0 + g.ntiles;
-      if (in) sh.first = index;
-    } else {
-      g.tile0 = before;
-      quota = cut;
-      c0 = quota * blockIdx.x;
-      c1 = min(c0 + quota, ntiles);
-      in = mine && g.tile0 < c1 && g.tile0 + g.ntiles > c0;
-      if (in && g.tile0 <= c0) sh.first = index;
+      g.tile0 = quota * scan_tiles(mine ? (g.ntiles + quota - 1) / quota : 0, sh.sums[1], total);
     }
+    c0 = quota * blockIdx.x;
+    c1 = whole_groups ? c0 + quota : min(c0 + quota, ntiles);
+    const bool in = mine && ntiles > 0 && g.tile0 < c1 && g.tile0 + g.ntiles > c0;
+    if (in && g.tile0 <= c0) sh.first = index;
     busy = __syncthreads_or(in);
     if (in) {
       Segment x = segment_of(g, c0, c1, blockIdx.x);
@@ -270,17 +256,15 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
   } else {
     ntiles = p.hdr->ntiles;
     quota = cta_quota(ntiles, p.grid, p.min_tiles);
-    c0 = quota * blockIdx.x;
-    c1 = min(c0 + quota, ntiles);
-    busy = c0 < c1;
+    busy = ntiles > 0 && blockIdx.x <= (ntiles - 1) / quota;
     if (busy) {
+      c0 = quota * blockIdx.x;
+      c1 = min(c0 + quota, ntiles);
       const int ng = p.hdr->ngroups;
-      if (warp == 0) {
-        const int g = find_group(p.groups, ng, c0);
-        if (lane == 0) sh.first = g;
-      } else if (warp == 1) {
-        const int g = find_group(p.groups, ng, c1 - 1);
-        if (lane == 0) p.border[blockIdx.x] = border_of(p, p.groups[g], c0, c1, quota, blockIdx.x);
+      if (warp < 2) {
+        const int g = find_group(p.groups, ng, warp ? c1 - 1 : c0);
+        if (warp == 0 && lane == 0) sh.first = g;
+        if (warp == 1 && lane == 0) p.border[blockIdx.x] = border_of(p, p.groups[g], c0, c1, quota, blockIdx.x);
       }
       __syncthreads();
       const int gi = sh.first + tid;
@@ -294,6 +278,10 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
     p.err[blockIdx.x] = ntiles < 0 ? HCA_ERR_CACHE : HCA_OK;
     if (!busy) p.border[blockIdx.x] = Border{0, 0, 0, 0};
   }
+  const uint32_t limit_ns = (uint32_t)p.wait_ns;
+  auto wait_bar = [&](uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_idle(bar, parity, abort_flag, limit_ns));
+  };
   pdl_launch_dependents();  // the combine kernel waits for this one's end by itself
   auto segment = [&](int k) { return k < kMaxSegs ? sh.seg[k] : segment_of(p.groups[sh.first + k], c0, c1, blockIdx.x); };
   tc_fence_before();
@@ -301,54 +289,6 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
   const int ppt = kTileKeys >> p.log_bs;  // pages per tile: a power of two, 1 .. 8
-  // Half of the rows of a group's q into shared memory, by `threads` threads: copied
-  // as they are (asynchronously, all in flight), then each thread turns the
-  // pieces that it copied into fp16 in their place.  D / 8 neighbouring lanes
-  // have a row's 16-byte pieces, so its largest value is a few shuffles away.
-  auto load_q = [&](const Segment &g, int k, int t, auto threads, int half) {
-    constexpr int kLanes = D / 8, step = decltype(threads)::value / kLanes;  // rows at a time
-    static_assert((NQ / 2) % step == 0, "rows divide evenly");
-    const int ch = t % kLanes, r0 = half * (NQ / 2), r1 = r0 + NQ / 2;
-    const int nreal = real_columns(p, g.npos, g.slice());
-    const uint32_t dst = smem_u32(smem) + C::kOffQ + (ch >> 3) * kHalfTile;
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)g.row0 * p.H + g.slice() * p.HS) * D + ch * 8;
-#pragma unroll 4
-    for (int c = r0 + t / kLanes; c < r1; c += step)  // rows beyond the group's are zero
-      cp_async_16(dst + c * 128 + (((ch & 7) ^ (c & 7)) << 4), c < nreal ? q + (size_t)c * D : q, c < nreal ? 16 : 0);
-    cp_async_wait();
-    // four rows at a time, step by step, so that their latencies overlap
-    constexpr int kBatch = NQ / 2 / step < 4 ? NQ / 2 / step : 4;
-    for (int c = r0 + t / kLanes; c < r1; c += kBatch * step) {
-      uint32_t w[kBatch][4], amax[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) ld_shared(dst + (c + i * step) * 128 + (((ch & 7) ^ ((c + i * step) & 7)) << 4), w[i]);
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        amax[i] = bf16x2_max(bf16x2_max(w[i][0] & 0x7fff7fffu, w[i][1] & 0x7fff7fffu),
-                             bf16x2_max(w[i][2] & 0x7fff7fffu, w[i][3] & 0x7fff7fffu));
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) amax[i] = bf16x2_max(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], o));
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        // the largest |q| becomes 224 .. 448; a negative scale goes into q's sign
-        // (of a row with an infinity nothing but NaN comes, whatever the factor)
-        const int ex = scale_exponent(__uint_as_float(max(amax[i] & 0xffffu, amax[i] >> 16) << 16)), ci = c + i * step;
-        const float inv = p.scale < 0.f ? -exp2_int(-ex) : p.scale > 0.f ? exp2_int(-ex) : 0.f;
-        if (ch == 0) sh.q_factor[k & 1][ci] = exp2_int(ex) * fabsf(p.scale) * 1.4426950408889634f;
-        uint32_t f[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          f[e] = f16x2_rn(__uint_as_float(w[i][e] << 16) * inv, __uint_as_float(w[i][e] & 0xffff0000u) * inv);
-#pragma unroll
-        for (int y = 0; y < C::kCopies; ++y)
-          st_shared(dst + (ci + y * NQ) * 128 + (((ch & 7) ^ (ci & 7)) << 4), f[0], f[1], f[2], f[3]);
-      }
-    }
-    fence_async_smem();
-  };
-
   if (warp >= 8) {
     setmaxnreg_dec<C::kRegsIssue>();
     if (warp == 8 && busy) {
@@ -386,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           for (int t = 0; t < jn; ++t, ++n) {
             const int ms = n % kMetaStages;
             if (n >= (uint32_t)kMetaStages)
-              ok = wait_idle(&sh.meta_empty[ms], ((n / kMetaStages) - 1) & 1, abort_flag, status, p.wait_ns);
+              ok = wait_bar(&sh.meta_empty[ms], ((n / kMetaStages) - 1) & 1);
             if (!ok) break;
             const bool here = lane / ppt == t;
             PageMeta &to = sh.meta[ms][lane % ppt];
@@ -461,18 +401,18 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           const uint32_t st = n % kStages;
           if (j == seg.j0) {
             // a group's q is written after the last softmax of the group before
-            ok = wait_idle(&sh.q_full, nseg & 1, abort_flag, status, p.wait_ns) &&
-                 wait_idle(&sh.kv_full[st], (n / kStages) & 1, abort_flag, status, p.wait_ns);
+            ok = wait_bar(&sh.q_full, nseg & 1) &&
+                 wait_bar(&sh.kv_full[st], (n / kStages) & 1);
             if (!ok) break;
             tc_fence_after();
-            issue_s(n, 0);
-            issue_s(n, 1);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) issue_s(n, h);
           }
           const uint64_t bv = dv + desc_bytes(st * C::kStageBytes);
           const bool more = j + 1 < seg.j1;
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
-            ok = wait_idle(&sh.p_full[h], n & 1, abort_flag, status, p.wait_ns);
+            ok = wait_bar(&sh.p_full[h], n & 1);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
@@ -486,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             }
             __syncwarp();
             if (more) {
-              if (h == 0) ok = wait_idle(&sh.kv_full[(n + 1) % kStages], ((n + 1) / kStages) & 1, abort_flag, status, p.wait_ns);
+              if (h == 0) ok = wait_bar(&sh.kv_full[(n + 1) % kStages], ((n + 1) / kStages) & 1);
               if (!ok) break;
               tc_fence_after();
               issue_s(n + 1, h);
@@ -503,25 +443,19 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         __syncwarp();
       }
     }
-    else if (warp >= 10 && busy) {
-      // ------------------------------------------------------------ q
-      for (int k = 0;; ++k) {
-        const Segment g = segment(k);
-        load_q(g, k, tid - 320, std::integral_constant<int, 64>(), 0);
-        mbar_arrive(&sh.q_full);
-        if (g.last()) break;
-        if (!wait_idle(&sh.q_free, k & 1, abort_flag, status, p.wait_ns)) break;
-      }
-    }
   } else if (warp >= 4) {
     setmaxnreg_dec<C::kRegsConv>();
     if (busy) {
       // ------------------------------------------------------------ converter
-      // Thread c takes 16-byte pieces (16 values) c, c + 128, ... of a tile: 16
-      // rows apart for D = 128, 32 for D = 64.
-      constexpr int kPer = D / 16;                   // pieces of a row = pieces of a thread (128 rows x kPer / 128)
-      const int ct = tid - kWG, ch = ct % kPer, row0 = ct / kPer;
+      // A thread takes 16-byte pieces (16 values) of rows kRowStep apart.  Of 8
+      // neighbouring lanes 4 have pieces of one row and 4 those of the next, of
+      // the same 64 columns, so that what they store falls into different banks.
+      constexpr int kPer = D / 16;  // pieces of a row = pieces of a thread (128 rows x kPer / 128)
       constexpr int kRowStep = kWG / kPer;
+      const int ct = tid - kWG;
+      const int ch = D == 128 ? (ct & 3) | ((ct >> 1) & 4) : ct & 3;
+      const int row0 = D == 128 ? ((ct >> 2) & 1) | ((ct >> 3) & ~1) : ct >> 2;
+      const uint32_t row_lanes = D == 128 ? 0x0f0fu << (lane & 20) : 0xfu << (lane & 28);  // of the thread's row
       const uint32_t out0 = smem_u32(smem);
       const int bs_mask = (1 << p.log_bs) - 1;
       uint32_t n = 0;
@@ -530,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       // loads of tile n's rows, once its pages are known
       auto load = [&](uint32_t n) {
         const int ms = n % kMetaStages;
-        if (!wait_idle(&sh.meta_full[ms], (n / kMetaStages) & 1, abort_flag, status, p.wait_ns)) return false;
+        if (!wait_bar(&sh.meta_full[ms], (n / kMetaStages) & 1)) return false;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int row = row0 + i * kRowStep;
@@ -554,9 +488,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
               const int row = row0 + i * kRowStep;
-              // a row's pieces are in kPer neighbouring lanes
-              const uint32_t grp = ((1u << kPer) - 1u) << (lane & ~(kPer - 1));
-              const bool nan = (__ballot_sync(0xffffffffu, nan_bytes(raw[i]) != 0) & grp) != 0;
+              const bool nan = (__ballot_sync(0xffffffffu, nan_bytes(raw[i]) != 0) & row_lanes) != 0;
               const PageMeta &pm = sh.meta[ms][row >> p.log_bs];
               if (nan && pm.kind != kAllSeen) {
                 raw[i] = make_uint4(0, 0, 0, 0);
@@ -568,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             }
           }
           if (n >= (uint32_t)kStages)
-            ok = wait_idle(&sh.kv_empty[st], ((n / kStages) - 1) & 1, abort_flag, status, p.wait_ns);
+            ok = wait_bar(&sh.kv_empty[st], ((n / kStages) - 1) & 1);
           if (!ok) break;
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
@@ -578,15 +510,10 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             e4m3x4_to_f16(raw[i].y, f[2], f[3]);
             e4m3x4_to_f16(raw[i].z, f[4], f[5]);
             e4m3x4_to_f16(raw[i].w, f[6], f[7]);
-            // 32 bytes: chunks 2 ch and 2 ch + 1 of the row; of a row's 8 lanes
-            // (D = 128) the upper four store their second one first, into the
-            // banks that the lower four leave
             const uint32_t at = out0 + st * C::kStageBytes + (ch >> 2) * kHalfTile + row * 128;
             const int c2 = 2 * (ch & 3), x = row & 7;
-            const bool odd = D == 128 && ch >= 4;
-            const uint32_t a0 = at + (((c2 + odd) ^ x) << 4), a1 = at + (((c2 + !odd) ^ x) << 4);
-            st_shared(a0, odd ? f[4] : f[0], odd ? f[5] : f[1], odd ? f[6] : f[2], odd ? f[7] : f[3]);
-            st_shared(a1, odd ? f[0] : f[4], odd ? f[1] : f[5], odd ? f[2] : f[6], odd ? f[3] : f[7]);
+            st_shared(at + ((c2 ^ x) << 4), f[0], f[1], f[2], f[3]);
+            st_shared(at + (((c2 + 1) ^ x) << 4), f[4], f[5], f[6], f[7]);
           }
           fence_async_smem();
           mbar_arrive(&sh.kv_full[st]);
@@ -611,31 +538,76 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       constexpr int kSpan = C::kSpan;
       const int row = tid % NQ, copy = tid / NQ;  // row of the group
       const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
-      auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_idle(bar, parity, abort_flag, status, p.wait_ns); };
-
+      
       uint32_t n = 0;
       for (int k = 0;; ++k) {
         const Segment g = segment(k);
-        if (k > 0) (void)wait(&sh.q_free, (k - 1) & 1);
-        load_q(g, k, tid, std::integral_constant<int, kWG>(), 1);
+        // q into shared memory (every product with the last group's has been
+        // made): copied as it is, asynchronously, then each thread turns the
+        // pieces that it copied into fp16 in their place.  D / 8 neighbouring
+        // lanes have a row's 16-byte pieces, so its largest value is a few
+        // shuffles away.
+        {
+          constexpr int kLanes = D / 8, step = kWG / kLanes;  // rows at a time
+          const int ch = tid % kLanes, c0q = tid / kLanes, nq = real_columns(p, g.npos, g.slice());
+          const uint32_t dst = smem_u32(smem) + C::kOffQ + (ch >> 3) * kHalfTile;
+          const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)g.row0 * p.H + g.slice() * p.HS) * D + ch * 8;
+#pragma unroll 1
+          for (int c = c0q; c < NQ; c += step)  // rows beyond the group's are zero
+            cp_async_16(dst + c * 128 + (((ch & 7) ^ (c & 7)) << 4), c < nq ? q + (size_t)c * D : q, c < nq ? 16 : 0);
+          cp_async_wait();
+          constexpr int kBatch = 2;  // rows whose latencies overlap
+          static_assert(NQ % (kBatch * step) == 0, "rows divide evenly");
+#pragma unroll 1
+          for (int c = c0q; c < NQ; c += kBatch * step) {
+            uint32_t w[kBatch][4], amax[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+              ld_shared(dst + (c + i * step) * 128 + (((ch & 7) ^ ((c + i * step) & 7)) << 4), w[i]);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+              amax[i] = bf16x2_max(bf16x2_max(w[i][0] & 0x7fff7fffu, w[i][1] & 0x7fff7fffu),
+                                   bf16x2_max(w[i][2] & 0x7fff7fffu, w[i][3] & 0x7fff7fffu));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) amax[i] = bf16x2_max(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], o));
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              // the largest |q| becomes 224 .. 448; a negative scale goes into q's sign
+              // (of a row with an infinity nothing but NaN comes, whatever the factor)
+              const int ex = scale_exponent(__uint_as_float(max(amax[i] & 0xffffu, amax[i] >> 16) << 16)), ci = c + i * step;
+              const float inv = p.scale < 0.f ? -exp2_int(-ex) : p.scale > 0.f ? exp2_int(-ex) : 0.f;
+              if (ch == 0) sh.q_factor[ci] = exp2_int(ex) * fabsf(p.scale) * 1.4426950408889634f;
+              uint32_t f[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                f[e] = f16x2_rn(__uint_as_float(w[i][e] << 16) * inv, __uint_as_float(w[i][e] & 0xffff0000u) * inv);
+#pragma unroll
+              for (int y = 0; y < C::kCopies; ++y)
+                st_shared(dst + (ci + y * NQ) * 128 + (((ch & 7) ^ (ci & 7)) << 4), f[0], f[1], f[2], f[3]);
+            }
+          }
+          fence_async_smem();
+        }
         mbar_arrive(&sh.q_full);
         const int nreal = real_columns(p, g.npos, g.slice());
         const int pos = g.pos0 + (row < nreal ? row / p.HS : 0);
         // what the row sees: raw keys [raw_lo, pos], entries [0, entries)
         const int raw_lo = pos - p.W + 1, entries = (pos + 1) / p.m;
         float m_run = -INFINITY, l_run = 0.f;
-        (void)wait(&sh.q_full, k & 1);
-        const float cs = sh.q_factor[k & 1][row];
+        (void)wait_bar(&sh.q_full, k & 1);
+        const float cs = sh.q_factor[row];
         for (int j = g.j0; j < g.j1; ++j, ++n) {
           const int ms = n % kMetaStages;
           const PageMeta *meta = sh.meta[ms];
-          (void)wait(&sh.scale_full[ms], (n / kMetaStages) & 1);
-          (void)wait(&sh.kv_full[n % kStages], (n / kStages) & 1);  // for the pages' data and the converter's notes
+          (void)wait_bar(&sh.scale_full[ms], (n / kMetaStages) & 1);
+          (void)wait_bar(&sh.kv_full[n % kStages], (n / kStages) & 1);  // for the pages' data and the converter's notes
           const bool odd_rows = sh.nan_any[ms] != 0;
           const int all_seen = sh.all_seen[ms];
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
-            (void)wait(&sh.s_full[h], n & 1);
+            (void)wait_bar(&sh.s_full[h], n & 1);
             tc_fence_after();
             const int k0 = h * 64 + copy * kSpan;  // first of the thread's keys, uniform in a warp
             uint32_t sv[kSpan];
@@ -719,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             const float m_use = m_run == -INFINITY ? 0.f : m_run;
             if (__any_sync(0xffffffffu, raise)) {
               // O holds the sum up to the keys before these once that is done
-              (void)wait(&sh.pv_done[h ^ 1], (h ? n : n - 1) & 1);
+              (void)wait_bar(&sh.pv_done[h ^ 1], (h ? n : n - 1) & 1);
               tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < D; c += 16) {
@@ -774,7 +746,6 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           }
           mbar_arrive(&sh.meta_empty[ms]);
         }
-        mbar_arrive(&sh.q_free);  // every score of the group has been read
         if (*abort_flag) l_run = __int_as_float(0x7fc00000);
         const bool whole = g.slot < 0, write = row < nreal && copy == 0;
         const size_t orow = (size_t)g.row0 * p.H + g.slice() * p.HS + row;  // rows of the group are rows of q and out in order
@@ -802,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           else p.part_ml[(size_t)g.slot * NQ + row] = make_float2(m_run, l_run);
         }
         const float inv = weight * (whole ? 1.f / l_run : 1.f);
-        (void)wait(&sh.pv_done[1], (n - 1) & 1);
+        (void)wait_bar(&sh.pv_done[1], (n - 1) & 1);
         tc_fence_after();
         constexpr int kJoin = C::kJoin;
 #pragma unroll 1
@@ -848,6 +819,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
 
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && sh.abort) atomicExch(status, HCA_ERR_TIMEOUT);
   if (warp == 10) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmem);

@@ -94,34 +94,32 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
   }
 }
 
-// The same for warps that often wait long beside warps that work: try_wait is
-// told to suspend the thread for up to kIdleNs, so it leaves its issue slots to
-// the others (polling, a dozen waiting warps of an SM took most of them).
+// The same for kernels of many roles, where a wait has to be short code (their
+// instructions come from far when the roles do not fit the instruction cache):
+// nothing is recorded but *abort.  try_wait may suspend the thread for kIdleNs.
 constexpr uint32_t kIdleNs = 2000;
 
-__device__ __forceinline__ bool mbar_try_wait_idle(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(kIdleNs)
-      : "memory");
-  return ok != 0;
+__device__ __forceinline__ uint32_t globaltimer_lo_ns() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
 }
 
-__device__ __forceinline__ bool mbar_wait_idle(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status,
-                                               uint64_t limit_ns) {
-  const uint32_t a = smem_u32(bar);
-  if (mbar_try_wait_idle(a, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t limit_ns) {
+  const uint32_t a = smem_u32(bar), t0 = globaltimer_lo_ns();
   for (;;) {
-    if (mbar_try_wait_idle(a, parity)) return true;
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(parity), "r"(kIdleNs)
+        : "memory");
+    if (ok) return true;
     if (*abort) return false;
-    if (globaltimer_ns() - t0 > limit_ns) {
+    if (globaltimer_lo_ns() - t0 > limit_ns) {
       *abort = 1;
-      atomicExch(status, 10 /* HCA_ERR_TIMEOUT */);
       return false;
     }
   }
