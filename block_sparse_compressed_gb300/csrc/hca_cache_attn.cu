@@ -313,41 +313,102 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
 constexpr int kCombineWarps = 8, kCombineThreads = 32 * kCombineWarps;
 constexpr int kMaxBorders = 640;
 
-// Warps that share a column's parts: one where a group has a few, more where it
-// has many (few rows over a long cache), as a warp keeps only a few rows in
-// flight.
+// The call's status from its CTAs' ones, written by the grid's first block; true
+// if a wait gave up: the outputs become NaN.
+template <typename T>
+__device__ __forceinline__ bool settle_status(const AttnParams &p) {
+  int worst = HCA_OK;
+  for (int i = threadIdx.x; i < p.grid; i += kCombineThreads) worst = max(worst, p.err[i] == HCA_ERR_TIMEOUT ? 1000 : p.err[i]);
+  const bool late = __syncthreads_or(worst == 1000);
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    const bool bad = __syncthreads_or(worst != HCA_OK);
+    if (threadIdx.x == 0) p.hdr->status = late ? HCA_ERR_TIMEOUT : bad ? HCA_ERR_CACHE : HCA_OK;
+  }
+  if (late) poison<T>(p);
+  return late;
+}
+
+// Many groups: block (c, y) joins 32 columns of the group that begins in CTA c's
+// range and ends behind it.  8 lanes have a column, kX float4 of it each, so that
+// a warp's loads of 4 columns are in flight together.
+template <typename T, int kX>
+__global__ void __launch_bounds__(kCombineThreads, 4) hca_cache_combine_kernel(const AttnParams p) {
+  tc::pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l8 = lane & 7;
+  const Border g = p.border[blockIdx.x];
+  if (settle_status<T>(p) || g.columns <= (int)blockIdx.y * 4 * kCombineWarps) return;
+  const int c = (blockIdx.y * kCombineWarps + warp) * 4 + (lane >> 3);
+  const bool mine = c < g.columns;
+  const int n = g.parts, v4 = p.D / 4;
+  auto slot = [&](int i) { return (size_t)(i == 0 ? g.slot : 2 * ((int)blockIdx.x + i)) * p.NQ + c; };
+  float M = -INFINITY, L = 0.f;
+  for (int i = l8; mine && i < n; i += 8) M = fmaxf(M, p.part_ml[slot(i)].x);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float4 acc[kX];
+#pragma unroll
+  for (int x = 0; x < kX; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int b = 0; b < n; b += 8) {
+    float w = 0.f;
+    if (mine && b + l8 < n) {
+      const float2 ml = p.part_ml[slot(b + l8)];
+      if (ml.y != 0.f) {  // 0: a part in which the column saw no key
+        w = exp2f(ml.x - M);
+        L += w * ml.y;
+      }
+    }
+    const int k1 = min(8, n - b);
+#pragma unroll 2
+    for (int k = 0; k < k1; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, (lane & 24) | k);
+      const float4 *o = reinterpret_cast<const float4 *>(p.part_o + slot(b + k) * p.D);
+      if (mine && wk != 0.f) {
+#pragma unroll
+        for (int x = 0; x < kX; ++x) {
+          if (l8 + 8 * x < v4) {
+            const float4 v = o[l8 + 8 * x];
+            acc[x].x = fmaf(wk, v.x, acc[x].x); acc[x].y = fmaf(wk, v.y, acc[x].y);
+            acc[x].z = fmaf(wk, v.z, acc[x].z); acc[x].w = fmaf(wk, v.w, acc[x].w);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (!mine) return;
+  const float inv = 1.f / L;
+  const size_t row = (size_t)g.row + c;
+#pragma unroll
+  for (int x = 0; x < kX; ++x)
+    if (l8 + 8 * x < v4) put4(static_cast<T *>(p.out) + row * p.D + 4 * (l8 + 8 * x), acc[x], inv);
+  if (l8 == 0) p.lse[row] = (M + log2f(L)) * 0.69314718055994531f;
+}
+
+// Few groups (few rows over long caches): a group has many parts, so several
+// warps share a column's; the joins are listed by every block, as their places
+// among the borders are not known, and dealt out column by column.
 __device__ __forceinline__ int warps_per_column(int parts) { return parts >= 32 ? 8 : parts >= 16 ? 4 : parts >= 8 ? 2 : 1; }
 
-// The joins are listed by every block (the borders' records are a few hundred),
-// an item is kCombineWarps / warps_per_column columns of one of them.
 template <typename T>
-__global__ void __launch_bounds__(kCombineThreads) hca_cache_combine_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kCombineThreads) hca_cache_combine_few_kernel(const AttnParams p) {
   __shared__ float4 acc[kCombineWarps][64];
   __shared__ int before[kMaxBorders + 1];
   __shared__ long long tmp[33];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   tc::pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (settle_status<T>(p)) return;
   const int per = (p.grid + kCombineThreads - 1) / kCombineThreads, i0 = tid * per, i1 = min(i0 + per, p.grid);
-  int worst = HCA_OK, items = 0;
+  int items = 0;
   for (int i = i0; i < i1; ++i) {
     const Border g = p.border[i];
-    const int e = p.err[i];
     before[i] = items;
     if (g.columns > 0) items += (g.columns * warps_per_column(g.parts) + kCombineWarps - 1) / kCombineWarps;
-    worst = max(worst, e == HCA_ERR_TIMEOUT ? 1000 : e);
   }
   long long total;
   const int base = (int)block_scan(items, tmp, total);
   for (int i = i0; i < i1; ++i) before[i] += base;
-  const bool late = __syncthreads_or(worst == 1000);
-  if (blockIdx.x == 0) {
-    const bool bad = __syncthreads_or(worst != HCA_OK);
-    if (tid == 0) p.hdr->status = late ? HCA_ERR_TIMEOUT : bad ? HCA_ERR_CACHE : HCA_OK;
-  }
-  if (late) {
-    poison<T>(p);
-    return;
-  }
+  __syncthreads();
   const int v4 = p.D / 4;  // float4 of a row, at most 64
   for (int item = blockIdx.x; item < total; item += gridDim.x) {
     int lo = 0, hi = p.grid;  // before[lo] <= item < before[hi]
@@ -369,7 +430,7 @@ __global__ void __launch_bounds__(kCombineThreads) hca_cache_combine_kernel(cons
       float w = 0.f;
       if (b + lane < n) {
         const float2 ml = p.part_ml[slot(b + lane) * p.NQ + c];
-        if (ml.y != 0.f) {  // 0: a part in which the column saw no key
+        if (ml.y != 0.f) {
           w = exp2f(ml.x - M);
           L += w * ml.y;
         }
@@ -391,17 +452,15 @@ __global__ void __launch_bounds__(kCombineThreads) hca_cache_combine_kernel(cons
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (wpc > 1) {  // the same for the whole block
-      __syncthreads();
-      acc[warp][lane] = s[0];
-      acc[warp][32 + lane] = s[1];
-      __syncthreads();
-      for (int w = 1; sub == 0 && w < wpc; ++w) {
+    __syncthreads();
+    acc[warp][lane] = s[0];
+    acc[warp][32 + lane] = s[1];
+    __syncthreads();
+    for (int w = 1; sub == 0 && w < wpc; ++w) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float4 u = acc[warp + w][lane + 32 * x];
-          s[x].x += u.x; s[x].y += u.y; s[x].z += u.z; s[x].w += u.w;
-        }
+      for (int x = 0; x < 2; ++x) {
+        const float4 u = acc[warp + w][lane + 32 * x];
+        s[x].x += u.x; s[x].y += u.y; s[x].z += u.z; s[x].w += u.w;
       }
     }
     if (n > 0 && sub == 0) {
@@ -413,6 +472,26 @@ __global__ void __launch_bounds__(kCombineThreads) hca_cache_combine_kernel(cons
       if (lane == 0) p.lse[row] = (M + log2f(L)) * 0.69314718055994531f;
     }
   }
+}
+
+template <typename T>
+cudaError_t combine(const AttnParams &p, int gmax, int sms, cudaStream_t st) {
+  // few groups: fewer than leave each 16 CTAs
+  const bool few = (long long)gmax * 16 <= p.grid;
+  // its blocks are set up while the attention's last CTAs run
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = few ? dim3(4 * sms) : dim3(p.grid, (p.P * p.HS + 4 * kCombineWarps - 1) / (4 * kCombineWarps));
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  ProfScope prof(kKCacheCombine, st);
+  if (few) return cudaLaunchKernelEx(&cfg, hca_cache_combine_few_kernel<T>, p);
+  return p.D <= 128 ? cudaLaunchKernelEx(&cfg, hca_cache_combine_kernel<T, 4>, p)
+                    : cudaLaunchKernelEx(&cfg, hca_cache_combine_kernel<T, 8>, p);
 }
 
 // Columns of a group for H heads: enough for one position's slice of heads, and
@@ -509,22 +588,9 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
     ProfScope prof(kKCacheSimt, st);
     hca_cache_simt_kernel<<<p.grid, kSimtThreads, kTileKeys * (a.D + 4), st>>>(p);
   }
-  {
-    ProfScope prof(kKCacheCombine, st);
-    // its blocks are set up while the attention's last CTAs run
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(4 * sms);
-    cfg.blockDim = dim3(kCombineThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = a.dtype == HCA_F32 ? cudaLaunchKernelEx(&cfg, hca_cache_combine_kernel<float>, p)
-                                             : cudaLaunchKernelEx(&cfg, hca_cache_combine_kernel<__nv_bfloat16>, p);
-    if (e != cudaSuccess) return e;
-  }
+  const int gmax = (int)std::min<size_t>(l.gmax, 1 << 20);
+  const cudaError_t e = tcs ? combine<__nv_bfloat16>(p, gmax, sms, st) : combine<float>(p, gmax, sms, st);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 

@@ -21,7 +21,7 @@
 //
 // The cache's e4m3 values become fp16 on the way to shared memory, exactly, once
 // for both products and all rows: converter warps load pages of global memory
-// into registers, a tile ahead of the one that they store, behind L2 prefetches
+// into registers as soon as they have stored a tile, behind L2 prefetches
 // that the page warp issues up to four tiles ahead.  A key's block scale s
 // multiplies one number, its score; P is p * s, and the row's sum divides by s
 // again.  A row of q is scaled by a power of two, so its 8 bits survive in fp16
@@ -98,12 +98,16 @@ struct Shared {
   int gbase[kThreads];
   float2 ml[kWG];                                // copies: reference and sum of every lane
   float join[NQ < 128 ? (128 - NQ) * (Cfg<NQ, D>::kJoin + 1) : 1];  // copies: columns of O of all lanes but the first copy's
-  long long scan[33];
   int2 sums[2][kThreads / 32];                   // tiles and groups of each warp
   uint32_t tmem_base;
   int abort, first;
 };
 
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -140,6 +144,35 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &a, uint32_t 
       : "r"(w));
 }
 
+// Sum of v over the threads in front of this one, total and number of those
+// that count; a warp's v sum up to less than 2^31 (a group has 2^25 tiles at
+// most).
+static __device__ __noinline__ int scan_tiles(int v, bool counts, int2 *sums, long long &total, int &ncounts, int &index) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  const uint32_t b = __ballot_sync(0xffffffffu, counts);
+  if (lane == 31) sums[warp] = make_int2(x, __popc(b));
+  __syncthreads();
+  int before = x - v, n = 0, idx = __popc(b & ((1u << lane) - 1u));
+  long long all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const int2 s = sums[w];
+    if (w < warp) before += s.x, idx += s.y;
+    all += s.x;
+    n += s.y;
+  }
+  total = all;
+  ncounts = n;
+  index = idx;
+  return before;
+}
+
 template <int NQ, int D>
 __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnParams p) {
   using C = Cfg<NQ, D>;
@@ -151,11 +184,13 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
   int32_t *status = &p.err[blockIdx.x];
 
   if (tid == 0) {
+#pragma unroll 1
     for (int s = 0; s < kMetaStages; ++s) {
       mbar_init(&sh.meta_full[s], 1);
       mbar_init(&sh.scale_full[s], 1);
       mbar_init(&sh.meta_empty[s], kWG);  // the softmax is the last to read a tile's pages
     }
+#pragma unroll 1
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sh.kv_full[s], kWG);
       mbar_init(&sh.kv_empty[s], 1);
@@ -186,11 +221,13 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
     bool mine = n == 1;
     if (__syncthreads_or(n > 1)) {
       long long all;
-      const long long chunks = block_scan(n, sh.scan, all);
-      if (tid < p.R) sh.gbase[tid] = (int)chunks;
+      int unused;
+      const int chunks = scan_tiles(n, false, sh.sums[1], all, unused, unused);
+      if (tid < p.R) sh.gbase[tid] = chunks;
       __syncthreads();
       mine = tid < all;
       int hi = p.R;  // gbase[r] <= tid < gbase[hi]
+#pragma unroll 1
       for (r = 0; hi - r > 1;) {
         const int mid = (r + hi) >> 1;
         if (sh.gbase[mid] <= tid) r = mid; else hi = mid;
@@ -202,34 +239,9 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
     g.ntiles = 0;
     mine = mine && ok;
     if (mine) ok = chunk_group(p, r, k, g);
-    // Tiles and groups before this one: within the warp, then over the warps in
-    // front.  A warp's groups have less than 2^31 tiles (2^25 each at most).
     int ngroups, index;
-    auto scan_tiles = [&](int v, int2 *sums, long long &total) {
-      int x = v;
-#pragma unroll 1
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      const uint32_t b = __ballot_sync(0xffffffffu, mine);
-      if (lane == 31) sums[warp] = make_int2(x, __popc(b));
-      __syncthreads();
-      int before = x - v;
-      total = 0;
-      ngroups = 0;
-      index = __popc(b & ((1u << lane) - 1u));
-#pragma unroll 1
-      for (int w = 0; w < kThreads / 32; ++w) {
-        const int2 s = sums[w];
-        if (w < warp) before += s.x, index += s.y;
-        total += s.x;
-        ngroups += s.y;
-      }
-      return before;
-    };
     long long total;
-    g.tile0 = scan_tiles(mine ? g.ntiles : 0, sh.sums[0], total);
+    g.tile0 = scan_tiles(mine ? g.ntiles : 0, mine, sh.sums[0], total, ngroups, index);
     ntiles = __syncthreads_and(ok) && total < kMaxTiles ? (int)total : -1;
     // Ranges that no group's border cuts give a CTA tiles of one group only and
     // save it a second one's beginning and end, about two tiles' time each;
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
     const bool whole_groups = ngroups < p.grid && own <= quota + 2;
     if (whole_groups) {
       quota = own;
-      g.tile0 = quota * scan_tiles(mine ? (g.ntiles + quota - 1) / quota : 0, sh.sums[1], total);
+      g.tile0 = quota * scan_tiles(mine ? (g.ntiles + quota - 1) / quota : 0, mine, sh.sums[1], total, ngroups, index);
     }
     c0 = quota * blockIdx.x;
     c1 = whole_groups ? c0 + quota : min(c0 + quota, ntiles);
@@ -297,9 +309,11 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       const uint32_t page_bytes = D << p.log_bs;
       uint32_t n = 0;
       bool ok = true;
+#pragma unroll 1
       for (int k = 0; ok; ++k) {
         const Segment g = segment(k);
         const Pages pg = group_pages(g.pos0, g.npos, p.W, p.m, p.log_bs, p.comp.table != nullptr);
+#pragma unroll 1
         for (int jb = g.j0; ok && jb < g.j1; jb += batch) {
           const int v = jb * ppt + lane;
           PageMeta pm = {nullptr, 0, kNoPage, 1.f, 0.f, 1.f, 0};
@@ -323,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           const uint32_t seen = __ballot_sync(0xffffffffu, pm.kind == kAllSeen);
           const uint32_t half = (1u << (ppt > 1 ? ppt / 2 : 1)) - 1u;  // pages of a half (one page has both)
           const int jn = min(batch, g.j1 - jb);
+#pragma unroll 1
           for (int t = 0; t < jn; ++t, ++n) {
             const int ms = n % kMetaStages;
             if (n >= (uint32_t)kMetaStages)
@@ -349,13 +364,15 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
               if (bad || !(pm.scale > 0.f && pm.scale < INFINITY)) {
                 pm.scale = 1.f;
                 atomicExch(status, HCA_ERR_CACHE);
+#pragma unroll 1
                 for (int r = (lane % ppt) << p.log_bs, i = 0; i < 1 << p.log_bs; ++i, ++r)
                   atomicOr(&sh.nan_keys[ms][r >> 5], 1u << (r & 31));
                 sh.nan_any[ms] = 1;
               }
               to.scale = pm.scale;
-              to.log2_scale = log2f(pm.scale);
-              to.inv_scale = 1.f / pm.scale;
+              // powers of two, for which both are exact
+              to.log2_scale = lg2_approx(pm.scale);
+              to.inv_scale = ex2_approx(-to.log2_scale);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.scale_full[ms]);
@@ -384,55 +401,47 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         injected_stall(&sh.never, abort_flag, status, p.wait_ns);
         ok = false;
       }
-      auto issue_s = [&](uint32_t n, int h) {
-        const uint64_t b = dk + desc_bytes((n % kStages) * C::kStageBytes + h * 8192);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + h * 64, dq + kmaj_step(kk), b + kmaj_step(kk), id_s, kk > 0);
-          mma_commit(&sh.s_full[h]);
-        }
-        __syncwarp();
-        issued = true;
-      };
+#pragma unroll 1
       for (; ok; ++nseg) {
         const Segment seg = segment(nseg);
-        for (int j = seg.j0; ok && j < seg.j1; ++j, ++n) {
-          const uint32_t st = n % kStages;
-          if (j == seg.j0) {
-            // a group's q is written after the last softmax of the group before
-            ok = wait_bar(&sh.q_full, nseg & 1) &&
-                 wait_bar(&sh.kv_full[st], (n / kStages) & 1);
+        const int halves = 2 * (seg.j1 - seg.j0);
+#pragma unroll 1
+        for (int u = 0; ok && u < halves + 2; ++u) {
+          const int h = u & 1;
+          if (u >= 2) {
+            // O of half u - 2
+            const uint32_t t = n + (u >> 1) - 1, st = t % kStages;
+            ok = wait_bar(&sh.p_full[h], t & 1);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) issue_s(n, h);
-          }
-          const uint64_t bv = dv + desc_bytes(st * C::kStageBytes);
-          const bool more = j + 1 < seg.j1;
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            ok = wait_bar(&sh.p_full[h], n & 1);
-            if (!ok) break;
-            tc_fence_after();
+            const uint64_t bv = dv + desc_bytes(st * C::kStageBytes + h * 8192);
+            const uint32_t pa = tmem + h * 64, more = u > 2;
             if (elect_one()) {
 #pragma unroll
-              for (int k1 = 0; k1 < 4; ++k1) {
-                const int kk = h * 4 + k1;
-                mma_ts(tmem + kColO, tmem + h * 64 + k1 * 8, bv + mnmaj_step(kk), id_o, j > seg.j0 || kk > 0);
-              }
+              for (int kk = 0; kk < 4; ++kk) mma_ts(tmem + kColO, pa + kk * 8, bv + mnmaj_step(kk), id_o, more || kk > 0);
               mma_commit(&sh.pv_done[h]);
               if (h == 1) mma_commit(&sh.kv_empty[st]);
             }
             __syncwarp();
-            if (more) {
-              if (h == 0) ok = wait_bar(&sh.kv_full[(n + 1) % kStages], ((n + 1) / kStages) & 1);
-              if (!ok) break;
-              tc_fence_after();
-              issue_s(n + 1, h);
+          }
+          if (u < halves) {
+            // S of half u (a group's q is written after the softmax of the group before)
+            const uint32_t t = n + (u >> 1), st = t % kStages;
+            if (u == 0) ok = wait_bar(&sh.q_full, nseg & 1);
+            if (h == 0 && ok) ok = wait_bar(&sh.kv_full[st], (t / kStages) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t b = dk + desc_bytes(st * C::kStageBytes + h * 8192);
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) mma_ss(tmem + h * 64, dq + kmaj_step(kk), b + kmaj_step(kk), id_s, kk > 0);
+              mma_commit(&sh.s_full[h]);
             }
+            __syncwarp();
+            issued = true;
           }
         }
+        n += halves / 2;
         if (seg.last()) break;
       }
       if (!ok && issued) {
@@ -473,11 +482,14 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         }
         return true;
       };
-      ok = load(0);
+#pragma unroll 1
       for (int k = 0; ok; ++k) {
         const Segment g = segment(k);
+#pragma unroll 1
         for (int j = g.j0; ok && j < g.j1; ++j, ++n) {
           const int ms = n % kMetaStages, st = n % kStages;
+          ok = load(n);
+          if (!ok) break;
           uint32_t nans = 0;
           if (sh.all_seen[ms] != 3) {
 #pragma unroll
@@ -517,7 +529,6 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           }
           fence_async_smem();
           mbar_arrive(&sh.kv_full[st]);
-          if (j + 1 < g.j1 || !g.last()) ok = load(n + 1);
         }
         if (g.last()) break;
       }
@@ -528,8 +539,10 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       // the schedule was refused
       const size_t rows = (size_t)p.N * p.H;
       const uint4 nan4 = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+#pragma unroll 1
       for (size_t i = (size_t)blockIdx.x * kWG + tid; i < rows * (D / 8); i += (size_t)gridDim.x * kWG)
         reinterpret_cast<uint4 *>(p.out)[i] = nan4;
+#pragma unroll 1
       for (size_t i = (size_t)blockIdx.x * kWG + tid; i < rows; i += (size_t)gridDim.x * kWG)
         p.lse[i] = __int_as_float(0x7fc00000);
     } else if (busy) {
@@ -540,6 +553,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
       
       uint32_t n = 0;
+#pragma unroll 1
       for (int k = 0;; ++k) {
         const Segment g = segment(k);
         // q into shared memory (every product with the last group's has been
@@ -598,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         float m_run = -INFINITY, l_run = 0.f;
         (void)wait_bar(&sh.q_full, k & 1);
         const float cs = sh.q_factor[row];
+#pragma unroll 1
         for (int j = g.j0; j < g.j1; ++j, ++n) {
           const int ms = n % kMetaStages;
           const PageMeta *meta = sh.meta[ms];
