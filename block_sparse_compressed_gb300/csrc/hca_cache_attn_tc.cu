@@ -65,7 +65,6 @@ struct Cfg {
   static constexpr int kRegsSoft = kCopies == 1 ? 128 : 112, kRegsConv = 64, kRegsIssue = kCopies == 1 ? 48 : 64;
   static_assert(kRegsSoft + kRegsConv + kRegsIssue <= 3 * 80, "register split must fit the launch");
   static constexpr int kSpan = 64 / kCopies;               // keys of a half that a thread takes: 64, 32, 16
-  static constexpr int kJoin = kCopies == 2 ? 32 : 16;     // columns of O joined at a time
   static constexpr int kHalves = D / 64;                   // 128-byte column blocks of an fp16 row
   static constexpr int kStageBytes = kHalves * kHalfTile;  // fp16 tile of 128 keys
   static constexpr int kOffQ = kStages * kStageBytes;
@@ -83,6 +82,7 @@ struct __align__(16) PageMeta {
 
 template <int NQ, int D>
 struct Shared {
+  uint4 join[kWG * 4];  // O on its way out: 64 bytes of each lane's row
   uint64_t meta_full[kMetaStages], meta_empty[kMetaStages];
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t q_full, s_full[2], p_full[2], pv_done[2], drain, never;
@@ -97,7 +97,6 @@ struct Shared {
   Segment seg[kMaxSegs];
   int gbase[kThreads];
   float2 ml[kWG];                                // copies: reference and sum of every lane
-  float join[NQ < 128 ? (128 - NQ) * (Cfg<NQ, D>::kJoin + 1) : 1];  // copies: columns of O of all lanes but the first copy's
   int2 sums[2][kThreads / 32];                   // tiles and groups of each warp
   uint32_t tmem_base;
   int abort, first;
@@ -551,24 +550,30 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       constexpr int kSpan = C::kSpan;
       const int row = tid % NQ, copy = tid / NQ;  // row of the group
       const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
-      
+      // q of a group into shared memory: D / 8 neighbouring lanes copy a row's
+      // 16-byte pieces as they are, asynchronously; rows beyond the group's are
+      // zero.  Each thread turns its own pieces into fp16 in their place.
+      constexpr int kLanes = D / 8, step = kWG / kLanes;  // rows at a time
+      const int ch = tid % kLanes, c0q = tid / kLanes;
+      const uint32_t dst = smem_u32(smem) + C::kOffQ + (ch >> 3) * kHalfTile;
+      auto copy_q = [&](const Segment &g) {
+        const int nq = real_columns(p, g.npos, g.slice());
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)g.row0 * p.H + g.slice() * p.HS) * D + ch * 8;
+#pragma unroll 1
+        for (int c = c0q; c < NQ; c += step)
+          cp_async_16(dst + c * 128 + (((ch & 7) ^ (c & 7)) << 4), c < nq ? q + (size_t)c * D : q, c < nq ? 16 : 0);
+      };
+      Segment g = segment(0);
+      copy_q(g);
       uint32_t n = 0;
+      float m_run = 0.f, l_run = 0.f;
+      bool last = false;
+      // A pass makes a group's q ready, so that the tensor cores have its first
+      // scores to make, ends the group before and then goes through the tiles.
 #pragma unroll 1
       for (int k = 0;; ++k) {
-        const Segment g = segment(k);
-        // q into shared memory (every product with the last group's has been
-        // made): copied as it is, asynchronously, then each thread turns the
-        // pieces that it copied into fp16 in their place.  D / 8 neighbouring
-        // lanes have a row's 16-byte pieces, so its largest value is a few
-        // shuffles away.
-        {
-          constexpr int kLanes = D / 8, step = kWG / kLanes;  // rows at a time
-          const int ch = tid % kLanes, c0q = tid / kLanes, nq = real_columns(p, g.npos, g.slice());
-          const uint32_t dst = smem_u32(smem) + C::kOffQ + (ch >> 3) * kHalfTile;
-          const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)g.row0 * p.H + g.slice() * p.HS) * D + ch * 8;
-#pragma unroll 1
-          for (int c = c0q; c < NQ; c += step)  // rows beyond the group's are zero
-            cp_async_16(dst + c * 128 + (((ch & 7) ^ (c & 7)) << 4), c < nq ? q + (size_t)c * D : q, c < nq ? 16 : 0);
+        if (!last) g = segment(k);
+        if (!last) {
           cp_async_wait();
           constexpr int kBatch = 2;  // rows whose latencies overlap
           static_assert(NQ % (kBatch * step) == 0, "rows divide evenly");
@@ -603,13 +608,106 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             }
           }
           fence_async_smem();
+          mbar_arrive(&sh.q_full);
         }
-        mbar_arrive(&sh.q_full);
+        if (k > 0) {
+          const Segment e = segment(k - 1);  // the group that ends
+          const int nreal = real_columns(p, e.npos, e.slice());
+          if (*abort_flag) l_run = __int_as_float(0x7fc00000);
+          const bool whole = e.slot < 0;
+          const size_t orow = (size_t)e.row0 * p.H + e.slice() * p.HS;  // rows of the group are rows of q and out in order
+          float weight = 1.f;
+          if constexpr (C::kCopies > 1) {
+            // the copies' common reference and sum
+            sh.ml[tid] = make_float2(m_run, l_run);
+            named_bar_sync(1, kWG);
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int y = 0; y < C::kCopies; ++y) M = fmaxf(M, sh.ml[row + y * NQ].x);
+#pragma unroll
+            for (int y = 0; y < C::kCopies; ++y) {
+              const float2 v = sh.ml[row + y * NQ];
+              const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
+              L += v.y != 0.f ? f * v.y : 0.f;  // NaN stays
+              if (y == copy) weight = f;
+            }
+            if (l_run != l_run) L = l_run;
+            m_run = M;
+            l_run = L;
+          }
+          if (row < nreal && copy == 0) {
+            if (whole) p.lse[orow + row] = (m_run + log2f(l_run)) * 0.69314718055994531f;
+            else p.part_ml[(size_t)e.slot * NQ + row] = make_float2(m_run, l_run);
+          }
+          const float inv = weight * (whole ? 1.f / l_run : 1.f);
+          (void)wait_bar(&sh.pv_done[1], (n - 1) & 1);
+          tc_fence_after();
+          // O leaves through shared memory, 64 bytes of a row at a time, so that
+          // four lanes write a row's: a store to 32 rows takes 32 cycles.
+          uint8_t *to = whole ? static_cast<uint8_t *>(p.out) + orow * D * 2 : reinterpret_cast<uint8_t *>(p.part_o + (size_t)e.slot * NQ * D);
+          const int row_bytes = whole ? D * 2 : D * 4, piece = lane & 3;
+          const uint32_t join = smem_u32(sh.join);
+          const uint32_t mine = join + tid * 64, swz = (tid >> 1) & 3;
+          const bool packed = C::kCopies == 1 && whole;  // staged as bf16 already: 32 columns
+          const int rounds = packed ? D / 32 : D / 16;
+#pragma unroll 1
+          for (int c = 0; c < rounds; ++c) {
+            uint32_t o[16];
+            if (packed) {
+              uint32_t x[32];
+              tmem_ld32(lane_addr + kColO + c * 32, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[y] = pack_bf16x2(__uint_as_float(x[2 * y]) * inv, __uint_as_float(x[2 * y + 1]) * inv);
+            } else {
+              tmem_ld16(lane_addr + kColO + c * 16, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * inv);
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) st_shared(mine + ((y ^ swz) << 4), o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+            if constexpr (C::kCopies == 1) {
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = warp * 32 + i * 8 + (lane >> 2);
+                uint32_t v[4];
+                ld_shared(join + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4), v);
+                if (r < nreal) *reinterpret_cast<uint4 *>(to + (size_t)r * row_bytes + c * 64 + piece * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+              }
+              __syncwarp();
+            } else {
+              named_bar_sync(1, kWG);
+#pragma unroll
+              for (int i = 0; i < NQ / 32; ++i) {
+                const int r = i * 32 + (tid >> 2);
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int x = 0; x < C::kCopies; ++x) {
+                  uint32_t v[4];
+                  ld_shared(join + (r + x * NQ) * 64 + ((piece ^ ((r >> 1) & 3)) << 4), v);
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) sum[y] += __uint_as_float(v[y]);
+                }
+                uint8_t *at = to + (size_t)r * row_bytes;
+                if (r < nreal) {
+                  if (whole) *reinterpret_cast<uint2 *>(at + c * 32 + piece * 8) = make_uint2(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]));
+                  else *reinterpret_cast<float4 *>(at + c * 64 + piece * 16) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+                }
+              }
+              named_bar_sync(1, kWG);
+            }
+          }
+          tc_fence_before();
+        }
+        if (last) break;
         const int nreal = real_columns(p, g.npos, g.slice());
         const int pos = g.pos0 + (row < nreal ? row / p.HS : 0);
         // what the row sees: raw keys [raw_lo, pos], entries [0, entries)
         const int raw_lo = pos - p.W + 1, entries = (pos + 1) / p.m;
-        float m_run = -INFINITY, l_run = 0.f;
+        m_run = -INFINITY;
+        l_run = 0.f;
         (void)wait_bar(&sh.q_full, k & 1);
         const float cs = sh.q_factor[row];
 #pragma unroll 1
@@ -624,6 +722,8 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           for (int h = 0; h < 2; ++h) {
             (void)wait_bar(&sh.s_full[h], n & 1);
             tc_fence_after();
+            // the group's last scores are made: the next one's q may come
+            if (h == 1 && j == g.j1 - 1 && !g.last()) copy_q(segment(k + 1));
             const int k0 = h * 64 + copy * kSpan;  // first of the thread's keys, uniform in a warp
             uint32_t sv[kSpan];
             if constexpr (kSpan == 16) {
@@ -761,73 +861,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           }
           mbar_arrive(&sh.meta_empty[ms]);
         }
-        if (*abort_flag) l_run = __int_as_float(0x7fc00000);
-        const bool whole = g.slot < 0, write = row < nreal && copy == 0;
-        const size_t orow = (size_t)g.row0 * p.H + g.slice() * p.HS + row;  // rows of the group are rows of q and out in order
-        float weight = 1.f;
-        if constexpr (C::kCopies > 1) {
-          // the copies' common reference and sum
-          sh.ml[tid] = make_float2(m_run, l_run);
-          named_bar_sync(1, kWG);
-          float M = -INFINITY, L = 0.f;
-#pragma unroll
-          for (int y = 0; y < C::kCopies; ++y) M = fmaxf(M, sh.ml[row + y * NQ].x);
-#pragma unroll
-          for (int y = 0; y < C::kCopies; ++y) {
-            const float2 v = sh.ml[row + y * NQ];
-            const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
-            L += v.y != 0.f ? f * v.y : 0.f;  // NaN stays
-            if (y == copy) weight = f;
-          }
-          if (l_run != l_run) L = l_run;
-          m_run = M;
-          l_run = L;
-        }
-        if (write) {
-          if (whole) p.lse[orow] = (m_run + log2f(l_run)) * 0.69314718055994531f;
-          else p.part_ml[(size_t)g.slot * NQ + row] = make_float2(m_run, l_run);
-        }
-        const float inv = weight * (whole ? 1.f / l_run : 1.f);
-        (void)wait_bar(&sh.pv_done[1], (n - 1) & 1);
-        tc_fence_after();
-        constexpr int kJoin = C::kJoin;
-#pragma unroll 1
-        for (int c = 0; c < D; c += kJoin) {
-          uint32_t o[kJoin];
-#pragma unroll
-          for (int x = 0; x < kJoin; x += 16) tmem_ld16(lane_addr + kColO + c + x, *reinterpret_cast<uint32_t(*)[16]>(&o[x]));
-          tmem_wait_ld();
-          float v[kJoin];
-#pragma unroll
-          for (int y = 0; y < kJoin; ++y) v[y] = __uint_as_float(o[y]) * inv;
-          if constexpr (C::kCopies > 1) {
-            if (copy > 0) {
-#pragma unroll
-              for (int y = 0; y < kJoin; ++y) sh.join[(tid - NQ) * (kJoin + 1) + y] = v[y];
-            }
-            named_bar_sync(1, kWG);
-            if (copy == 0) {
-#pragma unroll
-              for (int x = 1; x < C::kCopies; ++x)
-#pragma unroll
-                for (int y = 0; y < kJoin; ++y) v[y] += sh.join[(row + (x - 1) * NQ) * (kJoin + 1) + y];
-            }
-            named_bar_sync(1, kWG);
-          }
-          if (write && whole) {
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + orow * D + c);
-#pragma unroll
-            for (int y = 0; y < kJoin / 8; ++y)
-              dst[y] = make_uint4(pack_bf16x2(v[8 * y], v[8 * y + 1]), pack_bf16x2(v[8 * y + 2], v[8 * y + 3]),
-                                  pack_bf16x2(v[8 * y + 4], v[8 * y + 5]), pack_bf16x2(v[8 * y + 6], v[8 * y + 7]));
-          } else if (write) {
-            float4 *dst = reinterpret_cast<float4 *>(p.part_o + ((size_t)g.slot * NQ + row) * D + c);
-#pragma unroll
-            for (int y = 0; y < kJoin / 4; ++y) dst[y] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
-          }
-        }
-        tc_fence_before();
-        if (g.last()) break;
+        last = g.last();
       }
     }
   }
