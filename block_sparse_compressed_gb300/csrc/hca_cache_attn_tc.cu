@@ -38,6 +38,7 @@
 #include <cuda_bf16.h>
 
 #include <cfloat>
+#include <climits>
 #include <type_traits>
 
 #include "hca_cache_attn.cuh"
@@ -91,7 +92,6 @@ struct Shared {
   uint32_t nan_keys[kMetaStages][4];  // keys whose rows hold a NaN that not everybody sees
   int nan_any[kMetaStages];
   int all_seen[kMetaStages];          // bit h: every row sees every key of half h
-  float q_factor[NQ];                            // log2(e) |scale| / (a row's factor)
   // the CTA's pieces of groups, in order; what there is no room for is in the
   // workspace's groups
   Segment seg[kMaxSegs];
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
       // q of a group into shared memory: D / 8 neighbouring lanes copy a row's
       // 16-byte pieces as they are, asynchronously; rows beyond the group's are
-      // zero.  Each thread turns its own pieces into fp16 in their place.
+      // zero.
       constexpr int kLanes = D / 8, step = kWG / kLanes;  // rows at a time
       const int ch = tid % kLanes, c0q = tid / kLanes;
       const uint32_t dst = smem_u32(smem) + C::kOffQ + (ch >> 3) * kHalfTile;
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       Segment g = segment(0);
       copy_q(g);
       uint32_t n = 0;
-      float m_run = 0.f, l_run = 0.f;
+      float m_run = 0.f, l_run = 0.f, cs = 0.f;
       bool last = false;
       // A pass makes a group's q ready, so that the tensor cores have its first
       // scores to make, ends the group before and then goes through the tiles.
@@ -574,38 +574,41 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       for (int k = 0;; ++k) {
         if (!last) g = segment(k);
         if (!last) {
+          // bf16 -> fp16 with a factor for each row, by the row's thread (its
+          // copies share the work): the largest |q| becomes 224 .. 448; a
+          // negative scale goes into q's sign (of a row with an infinity nothing
+          // but NaN comes, whatever the factor)
           cp_async_wait();
-          constexpr int kBatch = 2;  // rows whose latencies overlap
-          static_assert(NQ % (kBatch * step) == 0, "rows divide evenly");
-#pragma unroll 1
-          for (int c = c0q; c < NQ; c += kBatch * step) {
-            uint32_t w[kBatch][4], amax[kBatch];
+          named_bar_sync(1, kWG);
+          const uint32_t qrow = smem_u32(smem) + C::kOffQ + row * 128;
+          auto piece_at = [&](int c) { return qrow + (c >> 3) * kHalfTile + (((c & 7) ^ (row & 7)) << 4); };
+          uint32_t amax = 0;
+#pragma unroll 4
+          for (int c = 0; c < kLanes; ++c) {
+            uint32_t w[4];
+            ld_shared(piece_at(c), w);
+            amax = bf16x2_max(amax, bf16x2_max(bf16x2_max(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                               bf16x2_max(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu)));
+          }
+          const int ex = scale_exponent(__uint_as_float(max(amax & 0xffffu, amax >> 16) << 16));
+          const float inv = p.scale < 0.f ? -exp2_int(-ex) : p.scale > 0.f ? exp2_int(-ex) : 0.f;
+          cs = exp2_int(ex) * fabsf(p.scale) * 1.4426950408889634f;
+          if constexpr (C::kCopies > 1) named_bar_sync(1, kWG);
+          const uint64_t inv2 = f32x2(__float_as_uint(inv), __float_as_uint(inv));
+          constexpr int kOwn = kLanes / C::kCopies;  // pieces of each copy
+#pragma unroll(kOwn < 4 ? kOwn : 4)
+          for (int i = 0; i < kOwn; ++i) {
+            const uint32_t at = piece_at(copy * kOwn + i);
+            uint32_t w[4], f[4];
+            ld_shared(at, w);
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-              ld_shared(dst + (c + i * step) * 128 + (((ch & 7) ^ ((c + i * step) & 7)) << 4), w[i]);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-              amax[i] = bf16x2_max(bf16x2_max(w[i][0] & 0x7fff7fffu, w[i][1] & 0x7fff7fffu),
-                                   bf16x2_max(w[i][2] & 0x7fff7fffu, w[i][3] & 0x7fff7fffu));
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1)
-#pragma unroll
-              for (int i = 0; i < kBatch; ++i) amax[i] = bf16x2_max(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], o));
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              // the largest |q| becomes 224 .. 448; a negative scale goes into q's sign
-              // (of a row with an infinity nothing but NaN comes, whatever the factor)
-              const int ex = scale_exponent(__uint_as_float(max(amax[i] & 0xffffu, amax[i] >> 16) << 16)), ci = c + i * step;
-              const float inv = p.scale < 0.f ? -exp2_int(-ex) : p.scale > 0.f ? exp2_int(-ex) : 0.f;
-              if (ch == 0) sh.q_factor[ci] = exp2_int(ex) * fabsf(p.scale) * 1.4426950408889634f;
-              uint32_t f[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                f[e] = f16x2_rn(__uint_as_float(w[i][e] << 16) * inv, __uint_as_float(w[i][e] & 0xffff0000u) * inv);
-#pragma unroll
-              for (int y = 0; y < C::kCopies; ++y)
-                st_shared(dst + (ci + y * NQ) * 128 + (((ch & 7) ^ (ci & 7)) << 4), f[0], f[1], f[2], f[3]);
+            for (int e = 0; e < 4; ++e) {
+              float lo, hi;
+              f32x2_split(fmul2(f32x2(w[e] << 16, w[e] & 0xffff0000u), inv2), lo, hi);
+              f[e] = f16x2_rn(lo, hi);
             }
+#pragma unroll
+            for (int y = 0; y < C::kCopies; ++y) st_shared(at + y * NQ * 128, f[0], f[1], f[2], f[3]);
           }
           fence_async_smem();
           mbar_arrive(&sh.q_full);
@@ -708,8 +711,6 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         const int raw_lo = pos - p.W + 1, entries = (pos + 1) / p.m;
         m_run = -INFINITY;
         l_run = 0.f;
-        (void)wait_bar(&sh.q_full, k & 1);
-        const float cs = sh.q_factor[row];
 #pragma unroll 1
         for (int j = g.j0; j < g.j1; ++j, ++n) {
           const int ms = n % kMetaStages;
