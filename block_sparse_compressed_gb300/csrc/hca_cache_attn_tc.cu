@@ -52,7 +52,8 @@ namespace {
 
 constexpr float kRaiseLog2 = 8.f;
 constexpr int kMetaStages = 4;  // tiles whose pages are looked up ahead
-constexpr int kStages = 2;      // fp16 tiles
+constexpr int kStages = 2;      // fp16 tiles; filled and released by halves
+constexpr int kHalfStages = 2 * kStages;
 constexpr int kMaxSegs = 64;    // pieces of groups listed in shared memory
 constexpr int kWG = 128;
 constexpr int kThreads = 3 * kWG;  // softmax | converter | page and MMA warp
@@ -69,7 +70,11 @@ struct Cfg {
   static constexpr int kHalves = D / 64;                   // 128-byte column blocks of an fp16 row
   static constexpr int kStageBytes = kHalves * kHalfTile;  // fp16 tile of 128 keys
   static constexpr int kOffQ = kStages * kStageBytes;
-  static constexpr int kSmem = kOffQ + kHalves * kHalfTile + 1024;
+  // e4m3 rows as they are in the cache: of 128 bytes in the columns 64 .. 127 of
+  // their fp16 rows, of 64 bytes behind q
+  static constexpr int kOffRaw = D == 128 ? kHalfTile : kOffQ + kHalves * kHalfTile;
+  static constexpr int kRawStride = D == 128 ? kStageBytes : kTileKeys * D;
+  static constexpr int kSmem = kOffQ + kHalves * kHalfTile + (D == 128 ? 0 : kStages * kRawStride) + 1024;
 };
 
 enum PageKind { kRaw = 0, kComp = 1, kNoPage = 2, kAllSeen = 3 };  // kAllSeen: every row sees every key
@@ -85,13 +90,14 @@ template <int NQ, int D>
 struct Shared {
   uint4 join[kWG * 4];  // O on its way out: 64 bytes of each lane's row
   uint64_t meta_full[kMetaStages], meta_empty[kMetaStages];
-  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t raw_full[kHalfStages], kv_full[kHalfStages], kv_empty[kHalfStages];
   uint64_t q_full, s_full[2], p_full[2], pv_done[2], drain, never;
   uint64_t scale_full[kMetaStages];
   PageMeta meta[kMetaStages][8];
   uint32_t nan_keys[kMetaStages][4];  // keys whose rows hold a NaN that not everybody sees
   int nan_any[kMetaStages];
   int all_seen[kMetaStages];          // bit h: every row sees every key of half h
+  uint32_t valid[kMetaStages];        // bit i: there is a page i
   // the CTA's pieces of groups, in order; what there is no room for is in the
   // workspace's groups
   Segment seg[kMaxSegs];
@@ -128,10 +134,10 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *p, uint32_
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-__device__ __forceinline__ uint4 ld_global_16(const uint8_t *p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+               "r"(smem_u32(bar))
+               : "memory");
 }
 __device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
@@ -190,7 +196,8 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       mbar_init(&sh.meta_empty[s], kWG);  // the softmax is the last to read a tile's pages
     }
 #pragma unroll 1
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kHalfStages; ++s) {
+      mbar_init(&sh.raw_full[s], 1);
       mbar_init(&sh.kv_full[s], kWG);
       mbar_init(&sh.kv_empty[s], 1);
     }
@@ -333,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
               bad = true;  // every key of it is noted as NaN
             }
           }
-          const uint32_t seen = __ballot_sync(0xffffffffu, pm.kind == kAllSeen);
+          const uint32_t seen = __ballot_sync(0xffffffffu, pm.kind == kAllSeen), valid = __ballot_sync(0xffffffffu, pm.rows != nullptr);
           const uint32_t half = (1u << (ppt > 1 ? ppt / 2 : 1)) - 1u;  // pages of a half (one page has both)
           const int jn = min(batch, g.j1 - jb);
 #pragma unroll 1
@@ -354,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             if (lane == 0) {
               const uint32_t a = seen >> (t * ppt), b = ppt > 1 ? a >> (ppt / 2) : a;
               sh.nan_any[ms] = 0;
+              sh.valid[ms] = (valid >> (t * ppt)) & ((1u << ppt) - 1u);
               sh.all_seen[ms] = ((a & half) == half ? 1 : 0) | ((b & half) == half ? 2 : 0);
             }
             __syncwarp();
@@ -419,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk) mma_ts(tmem + kColO, pa + kk * 8, bv + mnmaj_step(kk), id_o, more || kk > 0);
               mma_commit(&sh.pv_done[h]);
-              if (h == 1) mma_commit(&sh.kv_empty[st]);
+              mma_commit(&sh.kv_empty[2 * st + h]);
             }
             __syncwarp();
           }
@@ -427,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             // S of half u (a group's q is written after the softmax of the group before)
             const uint32_t t = n + (u >> 1), st = t % kStages;
             if (u == 0) ok = wait_bar(&sh.q_full, nseg & 1);
-            if (h == 0 && ok) ok = wait_bar(&sh.kv_full[st], (t / kStages) & 1);
+            if (ok) ok = wait_bar(&sh.kv_full[2 * st + h], (t / kStages) & 1);
             if (!ok) break;
             tc_fence_after();
             const uint64_t b = dk + desc_bytes(st * C::kStageBytes + h * 8192);
@@ -451,80 +459,110 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         __syncwarp();
       }
     }
+    else if (warp == 11 && busy) {
+      // ------------------------------------------------------------ copies
+      const bool split = p.log_bs == 7;  // a page has both halves
+      const uint32_t bytes = split ? 64 * D : D << p.log_bs, per_half = split ? 1 : ppt / 2;
+      const uint32_t to = smem_u32(smem) + C::kOffRaw + lane * bytes;
+      uint32_t n = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int k = 0; ok; ++k) {
+        const Segment g = segment(k);
+        const uint32_t end = n + 2 * (g.j1 - g.j0);
+#pragma unroll 1
+        for (; n < end; ++n) {
+          const int ms = (n >> 1) % kMetaStages, st = n % kHalfStages, h = n & 1;
+          if (h == 0) ok = wait_bar(&sh.meta_full[ms], ((n >> 1) / kMetaStages) & 1);
+          if (ok && n >= (uint32_t)kHalfStages) ok = wait_bar(&sh.kv_empty[st], ((n / kHalfStages) - 1) & 1);
+          if (!ok) break;
+          const uint32_t valid = split ? sh.valid[ms] : sh.valid[ms] >> (h * per_half) & ((1u << per_half) - 1u);
+          if (lane == 0) mbar_arrive_expect_tx(&sh.raw_full[st], __popc(valid) * bytes);
+          __syncwarp();
+          if ((valid >> lane) & 1)
+            bulk_load(to + (st >> 1) * C::kRawStride + h * 64 * D, split ? sh.meta[ms][0].rows + h * 64 * D : sh.meta[ms][h * per_half + lane].rows,
+                      bytes, &sh.raw_full[st]);
+          __syncwarp();
+        }
+        if (g.last()) break;
+      }
+      // copies in flight end in any case; none may outlive the CTA
+      volatile int never = 0;
+#pragma unroll 1
+      for (uint32_t t = n > (uint32_t)kHalfStages ? n - kHalfStages : 0; t < n; ++t)
+        if (lane == 0) mbar_wait(&sh.raw_full[t % kHalfStages], (t / kHalfStages) & 1, &never, status, 100000000ull);
+      __syncwarp();
+    }
   } else if (warp >= 4) {
     setmaxnreg_dec<C::kRegsConv>();
     if (busy) {
       // ------------------------------------------------------------ converter
       // A thread takes 16-byte pieces (16 values) of rows kRowStep apart.  Of 8
-      // neighbouring lanes 4 have pieces of one row and 4 those of the next, of
-      // the same 64 columns, so that what they store falls into different banks.
-      constexpr int kPer = D / 16;  // pieces of a row = pieces of a thread (128 rows x kPer / 128)
-      constexpr int kRowStep = kWG / kPer;
+      // neighbouring lanes 4 have pieces of one row and 4 of the next, with
+      // columns 0 .. 63 of the one and 64 .. 127 of the other, so that what they
+      // load and what they store falls into different banks.
+      constexpr int kRowStep = kWG * 16 / D, kPer = 64 / kRowStep;  // of a half
+      constexpr int kBatch = 2;     // pieces under way at a time
       const int ct = tid - kWG;
-      const int ch = D == 128 ? (ct & 3) | ((ct >> 1) & 4) : ct & 3;
+      const int ch = D == 128 ? (ct & 3) | (((ct >> 2) ^ (ct >> 3)) & 1) << 2 : ct & 3;
       const int row0 = D == 128 ? ((ct >> 2) & 1) | ((ct >> 3) & ~1) : ct >> 2;
       const uint32_t row_lanes = D == 128 ? 0x0f0fu << (lane & 20) : 0xfu << (lane & 28);  // of the thread's row
-      const uint32_t out0 = smem_u32(smem);
-      const int bs_mask = (1 << p.log_bs) - 1;
+      const uint32_t from0 = smem_u32(smem) + C::kOffRaw + row0 * D + ch * 16;
+      const uint32_t to0 = smem_u32(smem) + (ch >> 2) * kHalfTile + row0 * 128;
+      const uint32_t swz0 = (((2 * (ch & 3)) ^ (row0 & 7)) << 4);  // the other piece's differs in one bit
+      static_assert(kRowStep % 8 == 0, "a thread's rows have one swizzle");
       uint32_t n = 0;
       bool ok = true;
-      uint4 raw[kPer];
-      // loads of tile n's rows, once its pages are known
-      auto load = [&](uint32_t n) {
-        const int ms = n % kMetaStages;
-        if (!wait_bar(&sh.meta_full[ms], (n / kMetaStages) & 1)) return false;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int row = row0 + i * kRowStep;
-          const uint8_t *rows = sh.meta[ms][row >> p.log_bs].rows;
-          raw[i] = rows ? ld_global_16(rows + (row & bs_mask) * D + ch * 16) : make_uint4(0, 0, 0, 0);
-        }
-        return true;
-      };
 #pragma unroll 1
       for (int k = 0; ok; ++k) {
         const Segment g = segment(k);
+        const uint32_t end = n + 2 * (g.j1 - g.j0);
 #pragma unroll 1
-        for (int j = g.j0; ok && j < g.j1; ++j, ++n) {
-          const int ms = n % kMetaStages, st = n % kStages;
-          ok = load(n);
+        for (; n < end; ++n) {
+          const int ms = (n >> 1) % kMetaStages, st = n % kHalfStages, h = n & 1;
+          ok = wait_bar(&sh.raw_full[st], (n / kHalfStages) & 1);
           if (!ok) break;
-          uint32_t nans = 0;
-          if (sh.all_seen[ms] != 3) {
+          const uint32_t valid = sh.valid[ms];
+          const bool look = !((sh.all_seen[ms] >> h) & 1);
+          const uint32_t from = from0 + (st >> 1) * C::kRawStride + h * 64 * D, to = to0 + (st >> 1) * C::kStageBytes + h * 8192;
+#pragma unroll 1
+          for (int i0 = 0; i0 < kPer; i0 += kBatch) {
+            uint32_t raw[kBatch][4];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) nans |= nan_bytes(raw[i]);
-          }
-          if (__any_sync(0xffffffffu, nans != 0)) {
-            // NaN in a row that not every row of the group sees
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-              const int row = row0 + i * kRowStep;
-              const bool nan = (__ballot_sync(0xffffffffu, nan_bytes(raw[i]) != 0) & row_lanes) != 0;
-              const PageMeta &pm = sh.meta[ms][row >> p.log_bs];
-              if (nan && pm.kind != kAllSeen) {
-                raw[i] = make_uint4(0, 0, 0, 0);
-                if (ch == 0) {
-                  atomicOr(&sh.nan_keys[ms][row >> 5], 1u << (row & 31));
-                  sh.nan_any[ms] = 1;
+            for (int i = 0; i < kBatch; ++i) {
+              const int row = h * 64 + row0 + (i0 + i) * kRowStep;
+              ld_shared(from + (i0 + i) * kRowStep * D, raw[i]);
+              if (!((valid >> (row >> p.log_bs)) & 1)) raw[i][0] = raw[i][1] = raw[i][2] = raw[i][3] = 0;
+            }
+            if (look) {
+#pragma unroll 1
+              for (int i = 0; i < kBatch; ++i) {
+                const uint4 v = i ? make_uint4(raw[1][0], raw[1][1], raw[1][2], raw[1][3]) : make_uint4(raw[0][0], raw[0][1], raw[0][2], raw[0][3]);
+                const uint32_t nan = __ballot_sync(0xffffffffu, nan_bytes(v) != 0);
+                if (nan) {
+                  // NaN in a row that not every row of the group sees
+                  const int row = h * 64 + row0 + (i0 + i) * kRowStep;
+                  if ((nan & row_lanes) && sh.meta[ms][row >> p.log_bs].kind != kAllSeen) {
+                    if (i) raw[1][0] = raw[1][1] = raw[1][2] = raw[1][3] = 0;
+                    else raw[0][0] = raw[0][1] = raw[0][2] = raw[0][3] = 0;
+                    if (ch == 0) {
+                      atomicOr(&sh.nan_keys[ms][row >> 5], 1u << (row & 31));
+                      sh.nan_any[ms] = 1;
+                    }
+                  }
                 }
               }
             }
-          }
-          if (n >= (uint32_t)kStages)
-            ok = wait_bar(&sh.kv_empty[st], ((n / kStages) - 1) & 1);
-          if (!ok) break;
+            __syncwarp();  // rows of 128 bytes are overwritten; all their pieces are a warp's
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int row = row0 + i * kRowStep;
-            uint32_t f[8];
-            e4m3x4_to_f16(raw[i].x, f[0], f[1]);
-            e4m3x4_to_f16(raw[i].y, f[2], f[3]);
-            e4m3x4_to_f16(raw[i].z, f[4], f[5]);
-            e4m3x4_to_f16(raw[i].w, f[6], f[7]);
-            const uint32_t at = out0 + st * C::kStageBytes + (ch >> 2) * kHalfTile + row * 128;
-            const int c2 = 2 * (ch & 3), x = row & 7;
-            st_shared(at + ((c2 ^ x) << 4), f[0], f[1], f[2], f[3]);
-            st_shared(at + (((c2 + 1) ^ x) << 4), f[4], f[5], f[6], f[7]);
+            for (int i = 0; i < kBatch; ++i) {
+              uint32_t f[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) e4m3x4_to_f16(raw[i][e], f[2 * e], f[2 * e + 1]);
+              const uint32_t at = to + (i0 + i) * kRowStep * 128;
+              st_shared(at + swz0, f[0], f[1], f[2], f[3]);
+              st_shared(at + (swz0 ^ 16), f[4], f[5], f[6], f[7]);
+            }
           }
           fence_async_smem();
           mbar_arrive(&sh.kv_full[st]);
@@ -716,8 +754,6 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           const int ms = n % kMetaStages;
           const PageMeta *meta = sh.meta[ms];
           (void)wait_bar(&sh.scale_full[ms], (n / kMetaStages) & 1);
-          (void)wait_bar(&sh.kv_full[n % kStages], (n / kStages) & 1);  // for the pages' data and the converter's notes
-          const bool odd_rows = sh.nan_any[ms] != 0;
           const int all_seen = sh.all_seen[ms];
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
@@ -735,6 +771,8 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             }
             // which of them the row sees
             const bool plain = (all_seen >> h) & 1;
+            if (!plain) (void)wait_bar(&sh.kv_full[(2 * n + h) % kHalfStages], (n / kStages) & 1);  // for the converter's notes
+            const bool odd_rows = sh.nan_any[ms] != 0;
             uint64_t vis = ~0ull;
             if (!plain) {
               vis = 0;
