@@ -4,7 +4,9 @@ Each ``csrc/*.cu`` translation unit is compiled to an object in parallel,
 then linked into ``block_sparse_compressed_gb300/libhca.so`` with the CUDA
 runtime linked statically (the driver API is reached at run time through
 ``cudaGetDriverEntryPoint``, so the library loads on a machine without a
-GPU).  Usage: ``python -m block_sparse_compressed_gb300.build [--force]``.
+GPU).  ``csrc/hca_py.cpp``, the serving calls without their Python, becomes
+``_hca_py.so`` with the host compiler and torch's headers.  Usage: ``python -m
+block_sparse_compressed_gb300.build [--force]``.
 """
 from __future__ import annotations
 
@@ -13,11 +15,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhca.so")
+PY_LIB = os.path.join(HERE, "_hca_py.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xcompiler", "-fvisibility=hidden"]
@@ -47,6 +51,18 @@ def _stale(target, inputs) -> bool:
     return any(os.path.getmtime(p) > t for p in inputs)
 
 
+def _py_command(target: str):
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(a for i in inc for a in ("-isystem", i)),
+            os.path.join(CSRC, "hca_py.cpp"), "-o", target, "-L" + os.path.join(root, "lib"), "-ltorch_python",
+            "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -61,6 +77,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             cmd = [nvcc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", s, "-o", o]
             jobs.append(cmd)
 
+    # the module belongs to the torch that it was compiled with
+    import torch
+    stamp = os.path.join(BUILD, "hca_py.torch")
+    known = open(stamp).read() if os.path.exists(stamp) else ""
+    py_src = [os.path.join(CSRC, "hca_py.cpp"), os.path.join(os.path.dirname(HERE), "include", "hca.h")]
+    py_tmp = PY_LIB + f".tmp{os.getpid()}"
+    py_stale = force or known != torch.__version__ or _stale(PY_LIB, py_src)
+    if py_stale:
+        jobs.insert(0, _py_command(py_tmp))
+    kernels = len(jobs) - py_stale
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -69,9 +96,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         for cmd, r in ex.map(run, jobs):
             if verbose or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-            if r.returncode != 0:
+            if r.returncode != 0 and "-o" in cmd and cmd[cmd.index("-o") + 1] == py_tmp:
+                # no headers of Python or torch: the calls work without it, through ctypes
+                sys.stderr.write("_hca_py.so was not built: the serving calls cost 10 to 20 us more each\n")
+            elif r.returncode != 0:
                 raise RuntimeError(f"nvcc failed on {cmd[-3]}")
-    if force or jobs or _stale(LIB, objs):
+    if py_stale and os.path.exists(py_tmp):
+        os.replace(py_tmp, PY_LIB)
+        with open(stamp, "w") as f:
+            f.write(torch.__version__)
+    elif py_stale and os.path.exists(PY_LIB):
+        os.remove(PY_LIB)  # of another torch or another source
+    if force or kernels or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"]
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -26,6 +26,7 @@ _DTYPES = {torch.bfloat16: HCA_BF16, torch.float32: HCA_F32}
 
 _lock = threading.Lock()
 _lib = None
+_py = None  # the serving calls' short way (csrc/hca_py.cpp)
 
 EXPORTS = ("hca_status_string", "hca_version", "hca_workspace_size", "hca_query_tile_positions", "hca_attn_fwd",
            "hca_attn_bwd", "hca_visible_pairs", "hca_tile_map", "hca_workspace_status", "hca_profile_enable",
@@ -48,7 +49,7 @@ class HCAError(RuntimeError):
 
 def load(path: str = LIB_PATH):
     """Load libhca.so and declare the C signatures (no CUDA call is made)."""
-    global _lib
+    global _lib, _py
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -120,6 +121,14 @@ def load(path: str = LIB_PATH):
             lib.hca_cache_attn_workspace_size.restype = Z
             lib.hca_cache_attn.argtypes = [P, P, P, P, P, P, I, I, P, P, P, I, I, P, P, I, I, I, I, I, I, I, F, I, P, Z, P]
             lib.hca_cache_attn.restype = I
+            try:
+                from . import _hca_py as py
+                py.bind(*(ctypes.cast(getattr(lib, f), P).value for f in (
+                    "hca_cache_plan_workspace_size", "hca_cache_plan", "hca_cache_append_workspace_size",
+                    "hca_cache_append", "hca_cache_attn_workspace_size", "hca_cache_attn")))
+                _py = py
+            except ImportError:  # not built: no headers of Python or torch
+                pass
             _lib = lib
     return _lib
 
@@ -519,8 +528,9 @@ def hca_csa_attn_bwd(q, kv, ckv, seg, sel, out, lse, dout, W: int, m: int, scale
 # serving: plan, append and attend over a paged 8-bit cache
 #
 # A decode step's kernels take a few microseconds each, so what these calls do
-# in Python counts: no context manager unless the tensors' device is not the
-# current one, sizes of workspaces remembered, pointers passed as plain ints.
+# in Python counts.  An ordinary one goes through _hca_py (its tensors fit and
+# are on the current device); what that declines is checked, refused or done
+# here.
 # ---------------------------------------------------------------------------
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -531,6 +541,15 @@ def _enqueue(dev: torch.device, f, *args) -> int:
         return f(*args, _raw_stream(dev.index))
     with _on(dev):
         return f(*args, _stream(dev))
+
+
+def _made(r, name: str, check: bool):
+    """The answer of a call that _hca_py has made: its results and workspace, or the status."""
+    if type(r) is int:
+        _check(r, name)
+    elif check:
+        _check(hca_workspace_status(r[-1]), name + " (device)")
+    return r
 
 
 def _fits(t: torch.Tensor, name: str, shape, dtype, device) -> int:
@@ -570,6 +589,10 @@ def hca_cache_plan(held: torch.Tensor, added: torch.Tensor, table: torch.Tensor,
     free_blocks[nfree], free_count[1], all int32.  Returns (start[R+1],
     slots[nslots], free_left[1]); free_left may be free_count itself."""
     lib = _lib or load()
+    r = _py and _py.cache_plan(held, added, table, free_blocks, free_count, nblocks, bs, nslots, m, start, slots,
+                               free_left, ws)
+    if r is not None:
+        return _made(r, "hca_cache_plan", check)[:3]
     dev = held.device
     if held.dim() != 1 or table.dim() != 2 or free_blocks.dim() != 1:
         raise ValueError("held must be [R], table [R,cols] and free_blocks [nfree]")
@@ -597,6 +620,10 @@ def hca_cache_append(x: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor, s
     cache pool[nblocks,bs,D] (float8_e4m3fn) with scale[nblocks] (fp32), both
     updated in place (include/hca.h, hca_cache_append)."""
     lib = _lib or load()
+    r = _py and _py.cache_append(x, slots, pool, scale, ws)
+    if r is not None:
+        _made(r, "hca_cache_append", check)
+        return
     dev = x.device
     if x.dim() != 2 or pool.dim() != 3:
         raise ValueError("x must be [N,D] and pool [nblocks,bs,D]")
@@ -633,6 +660,9 @@ def hca_cache_attn(q: torch.Tensor, start: torch.Tensor, held: torch.Tensor, raw
     (pool, scale, table[R,cols]); comp may be None.  Returns (out[N,H,D],
     lse[N,H] fp32)."""
     lib = _lib or load()
+    r = _py and _py.cache_attn(q, start, held, raw, comp, W, m, scale, out, lse, ws)
+    if r is not None:
+        return _made(r, "hca_cache_attn", check)[:2]
     dev = q.device
     if q.dim() != 3 or held.dim() != 1 or raw[0].dim() != 3:
         raise ValueError("q must be [N,H,D], held [R] and the raw pool [nblocks,bs,D]")
