@@ -71,27 +71,27 @@ def bounds(q, ref, nkeys, scale, dtype):
 
     Scores.  fp32 sums of D products, each rounding (or a truncation, on the
     tensor cores) at most 2^-23 of the sum of magnitudes: D 2^-23 scale spread.
-    bf16: q goes in as two e4m3 numbers of one power-of-two scale that puts the
-    group's largest |q| at 224 .. 448, exact but for what falls below 2^-10, so
-    off by at most 2^-10 / 224 max|q| an element: scale max|q| D max|k| 2^-17.
+    bf16: q goes in as fp16 with a power-of-two factor that puts a row's largest
+    |q| at 224 .. 448, exact (8 bits) but for what falls below 2^-14, off by at
+    most 2^-25 / 224 max|q| an element: scale max|q| D max|k| 2^-32.
     The exponent itself is a few roundings of the score in base 2: 8 2^-24 |s|.
     A probability is off by that, relatively; so is lse, absolutely, plus the
     sum's roundings.
 
-    Output.  bf16: p as two e4m3 numbers is off by 2^-8 (2^-4 of 2^-4), by 2^-11
-    for its way through fp16, and by 2^-20 of the largest where it is tiny, once
-    a key; the result is rounded by 2^-8.  fp32: nkeys roundings of 2^-24."""
+    Output.  bf16: p as fp16 is off by 2^-11, or by 2^-25 of the largest where it
+    is tiny, once a key: 2^-20 for values that differ by up to 2^5; the result is
+    rounded by 2^-8.  fp32: nkeys roundings of 2^-24."""
     out, lse, mass, spread = ref
     D = q.shape[2]
     e = D * 2.0 ** -23 * abs(scale) * spread + 8 * 2.0 ** -24 * (np.abs(lse) + abs(scale) * spread)
     if dtype == torch.bfloat16:
         qmax = float(q.float().abs().max())
         kmax = 448.0 * 2.0 ** -6 * 2  # largest key of make_cache
-        e = e + abs(scale) * qmax * D * kmax * 2.0 ** -17 * 2.0 ** -2  # |k| averages under a quarter of its largest
+        e = e + abs(scale) * qmax * D * kmax * 2.0 ** -32
     lse_tol = e + 2.0 ** -22 * (np.abs(lse) + 1.0)
     p = 2 * e + 2.0 ** -20
     if dtype == torch.bfloat16:
-        p = p + 2.0 ** -8 + 2.0 ** -11 + nkeys * 2.0 ** -20
+        p = p + 2.0 ** -11 + nkeys * 2.0 ** -20
         out_tol = 2.0 ** -8 * np.abs(out) + p[..., None] * 2 * mass
     else:
         out_tol = 2.0 ** -22 * np.abs(out) + (p + nkeys * 2.0 ** -24)[..., None] * 2 * mass

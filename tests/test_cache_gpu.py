@@ -673,3 +673,149 @@ def test_two_streams_at_once():
     for k, (out, lse) in enumerate(got):
         want = cases[k % len(cases)][1]
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+# ---------------------------------------------------------------------------
+# the binding, failures, shapes of the schedule
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_both_ways_of_the_binding_give_the_same(dtype, monkeypatch):
+    hca.load()
+    short = hca._py
+    if short is None:
+        pytest.skip("built without the headers of Python or torch")
+    R, H, D, W, m, bs = 5, 8, 64, 40, 8, 16
+    held, added = [70, 0, 12, 333, 5], [1, 9, 0, 2, 40]
+    q, start, h, raw, c = attn_case(held, added, H, D, W, m, bs, dtype, 3)
+    rows = torch.randn(sum(added), D, generator=torch.Generator().manual_seed(1)).to(dtype).to(DEV)
+    seen = []
+
+    class Spy:
+        def __getattr__(self, name):
+            def call(*a):
+                r = getattr(short, name)(*a)
+                seen.append(r is not None)
+                return r
+            return call
+
+    results = []
+    for py in (Spy(), None):
+        monkeypatch.setattr(hca, "_py", py)
+        table = torch.full((R, 40), -1, dtype=torch.int32, device=DEV)
+        for r, n in enumerate(held):
+            for k in range(-(-n // bs)):
+                table[r, k] = 25 * r + k
+        plan = hca.hca_cache_plan(i32(held), i32(added), table, i32(list(range(125, 160))), i32([35]), 160, bs, sum(added), check=True)
+        pool, scale = torch.zeros(160, bs, D, device=DEV).to(E4M3), torch.ones(160, device=DEV)
+        hca.hca_cache_append(rows, plan[1], pool, scale, check=True)
+        attn = hca.hca_cache_attn(q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), W, m, scale_of(D), check=True)
+        bare = hca.hca_cache_attn(q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), None, W, m, scale_of(D), check=True)
+        results.append([*plan, table, pool.view(torch.uint8), scale, *attn, *bare])
+    assert seen == [True] * 4
+    assert len(results[0]) == len(results[1])
+    for a, b in zip(*results):
+        assert a.dtype == b.dtype and torch.equal(a, b)
+
+
+def test_results_go_into_the_callers_tensors():
+    q, start, h, raw, c = attn_case([70, 9], [1, 2], 8, 64, 40, 8, 16, BF16, 3)
+    args = (q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), 40, 8, scale_of(64))
+    want = hca.hca_cache_attn(*args)
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    ws = torch.empty(hca.load().hca_cache_attn_workspace_size(3, 2, 8, 64, 0), dtype=torch.uint8, device=DEV)
+    got = hca.hca_cache_attn(*args, out=out, lse=lse, ws=ws, check=True)
+    assert got[0] is out and got[1] is lse and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    with pytest.raises(hca.HCAError):
+        hca.hca_cache_attn(*args, ws=ws[:-1])
+    with pytest.raises(ValueError):
+        hca.hca_cache_attn(*args, out=out[:2])
+    with pytest.raises(TypeError):
+        hca.hca_cache_attn(*args, lse=lse.double())
+    with pytest.raises(ValueError):
+        hca.hca_cache_attn(args[0], args[1].cpu(), *args[2:])
+    with pytest.raises(ValueError):
+        hca.hca_cache_attn(args[0].transpose(0, 1).contiguous().transpose(0, 1), *args[1:])
+    with pytest.raises(hca.HCAError):
+        hca.hca_cache_attn(*args[:5], 0, *args[6:])
+    with pytest.raises(hca.HCAError):
+        hca.hca_cache_attn(*args[:7], float("nan"))
+
+
+@pytest.mark.parametrize("H,D,T", [(64, 128, 1), (16, 64, 2), (200, 64, 1)])
+def test_a_stalled_attention_times_out(H, D, T):
+    # the tensor-core warp waits for what never comes: every wait ends, the status
+    # says so and no stale number is left; the next call works
+    held = [3000, 17, 260]
+    q, start, h, raw, c = attn_case(held, [T] * 3, H, D, 64, 4, 16, BF16, 2)
+    args = (q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), 64, 4, scale_of(D))
+    want = hca.hca_cache_attn(*args, check=True)
+    hca.hca_test_inject(hca.INJECT_WAIT_LIMIT_NS, 30_000_000)
+    hca.hca_test_inject(hca.INJECT_STALL, 1)
+    try:
+        ws = torch.empty(hca.load().hca_cache_attn_workspace_size(3 * T, 3, H, D, 0), dtype=torch.uint8, device=DEV)
+        out, lse = hca.hca_cache_attn(*args, ws=ws)
+        assert hca.hca_workspace_status(ws) == 10
+        assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
+    finally:
+        hca.hca_test_inject(hca.INJECT_RESET, 0)
+    got = hca.hca_cache_attn(*args, check=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_a_failed_launch_is_reported():
+    q, start, h, raw, c = attn_case([70, 9], [1, 2], 8, 64, 40, 8, 16, BF16, 3)
+    args = (q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), 40, 8, scale_of(64))
+    for call in (lambda: hca.hca_cache_attn(*args),
+                 lambda: hca.hca_cache_append(q[:, 0].contiguous().to(DEV), i32([-1, -1, -1]), *dev(c)[:2]),
+                 lambda: hca.hca_cache_plan(i32([1]), i32([1]), i32([[0, -1]]), i32([1, 2]), i32([2]), 3, 16, 1)):
+        hca.hca_test_inject(hca.INJECT_LAUNCH_FAILURE, 1)
+        try:
+            with pytest.raises(hca.HCAError):
+                call()
+        finally:
+            hca.hca_test_inject(hca.INJECT_RESET, 0)
+        call()
+
+
+@pytest.mark.parametrize("dtype,H,D", [(BF16, 64, 128), (BF16, 1, 64), (F32, 2, 64)])
+def test_more_requests_than_threads(dtype, H, D):
+    held = [(k * 37) % 300 for k in range(401)]
+    q, start, h, raw, c = attn_case(held, [1] * 401, H, D, 48, 8, 16, dtype, 6)
+    got = hca.hca_cache_attn(q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), 48, 8, scale_of(D), check=True)
+    check_attn(got, q, start, h, raw, c, 48, 8, scale_of(D), dtype)
+
+
+def test_more_groups_for_a_block_than_it_lists():
+    # one tile a request, more than 64 requests to a block of 304
+    R, H, D, W, m, bs = 21000, 1, 64, 8, 4, 16
+    held = [k % 5 for k in range(R)]
+    q, start, h, raw, c = attn_case(held, [1] * R, H, D, W, m, bs, BF16, 6)
+    got = hca.hca_cache_attn(q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), W, m, scale_of(D), check=True)
+    check_attn(got, q, start, h, raw, c, W, m, scale_of(D), BF16)
+
+
+@pytest.mark.parametrize("dtype,H,D,T", [(BF16, 64, 128, 1), (BF16, 200, 128, 1), (BF16, 16, 64, 3), (BF16, 128, 64, 2), (F32, 4, 64, 1)])
+def test_one_long_request_in_many_parts(dtype, H, D, T):
+    held = [9001, 20]
+    q, start, h, raw, c = attn_case(held, [T, 1], H, D, 300, 2, 32, dtype, 8)
+    got = hca.hca_cache_attn(q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), 300, 2, scale_of(D), check=True)
+    check_attn(got, q, start, h, raw, c, 300, 2, scale_of(D), dtype)
+
+
+def test_two_graphs_share_a_workspace():
+    cases = [attn_case(held, [1] * len(held), 16, 64, 64, 4, 16, BF16, 5) for held in ([900, 3, 77], [12, 2500, 40])]
+    ws = torch.empty(hca.load().hca_cache_attn_workspace_size(3, 3, 16, 64, 0), dtype=torch.uint8, device=DEV)
+    graphs, outs, wants = [], [], []
+    for q, start, h, raw, c in cases:
+        args = (q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), 64, 4, scale_of(64))
+        wants.append(hca.hca_cache_attn(*args, check=True))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(hca.hca_cache_attn(*args, ws=ws))
+        graphs.append((g, args))
+    for k in (0, 1, 1, 0, 1, 0, 0):
+        for t in outs[k]:
+            t.fill_(7)
+        graphs[k][0].replay()
+        assert torch.equal(outs[k][0], wants[k][0]) and torch.equal(outs[k][1], wants[k][1])
+    assert hca.hca_workspace_status(ws) == 0
