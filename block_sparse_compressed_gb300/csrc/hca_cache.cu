@@ -23,6 +23,7 @@
 #include <algorithm>
 
 #include "hca_cache.cuh"
+#include "tc_ptx.cuh"
 
 namespace hca {
 using namespace cache;
@@ -105,6 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads) hca_cache_plan_kernel(const Cach
   __shared__ long long tmp[33];
   __shared__ int32_t near[2][kPlanThreads + 1];  // start and taken of up to 1024 requests
   const int tid = threadIdx.x;
+  tc::pdl_launch_dependents();  // the fill kernel waits for this one's end by itself
   const int avail = *a.free_in;
   const int nt = blockDim.x;
   const bool few = a.R <= nt;
@@ -159,6 +161,7 @@ __global__ void __launch_bounds__(kPlanThreads) hca_cache_plan_kernel(const Cach
 constexpr int kFillThreads = 256, kSlotsPerCta = 1024;
 
 __global__ void __launch_bounds__(kFillThreads) hca_cache_fill_kernel(const CachePlanArgs a) {
+  tc::pdl_wait();
   plan_fill(a, a.start, a.taken, *a.avail, blockIdx.x, gridDim.x);
 }
 
@@ -184,6 +187,7 @@ __device__ __forceinline__ bool begins_run(const CacheAppendArgs &a, int t) {
 // a slot twice) is reported and left out: it would race with the other.
 __global__ void hca_cache_claim_kernel(const CacheAppendArgs a) {
   const int t = blockIdx.x * blockDim.x + threadIdx.x;
+  tc::pdl_launch_dependents();  // the rows' kernel waits for this one's end by itself
   if (t == 0) *a.status = HCA_OK;
   if (t < a.N && begins_run(a, t)) a.owner[a.slots[t] >> a.log_bs] = t;
 }
@@ -348,6 +352,7 @@ __global__ void __launch_bounds__(kChunkThreads) hca_cache_append_kernel(const C
     // the order of the list does not matter
     if (i < cnt && brk && s >= 0 && s < limit) lead[atomicAdd(&nlead, 1)] = i;
   }
+  tc::pdl_wait();  // for the owners
   __syncthreads();
   auto length = [&](int i) {
     int w = (i + 1) >> 5;
@@ -440,7 +445,7 @@ cudaError_t cache_plan(const CachePlanArgs &args, void *ws, cudaStream_t st) {
   const int want = std::max(a.R, a.nslots <= kPlanOneCta ? a.nslots : 0);
   hca_cache_plan_kernel<<<1, std::min(std::max((want + 31) / 32 * 32, 32), kPlanThreads), 0, st>>>(a);
   if (a.nslots > kPlanOneCta)
-    hca_cache_fill_kernel<<<(a.nslots + kSlotsPerCta - 1) / kSlotsPerCta, kFillThreads, 0, st>>>(a);
+    return launch_behind(hca_cache_fill_kernel, dim3((a.nslots + kSlotsPerCta - 1) / kSlotsPerCta), kFillThreads, 0, st, a);
   return cudaGetLastError();
 }
 
@@ -459,9 +464,8 @@ cudaError_t cache_append(const CacheAppendArgs &args, cudaStream_t st) {
   // enough CTAs for every SM, but no more than one for each block of a long prompt
   const int rows = std::min(std::max(a.N / 1024, 4), kChunkRows);
   const int grid = (a.N + rows - 1) / rows;
-  if (f32) hca_cache_append_kernel<float><<<grid, kChunkThreads, 0, st>>>(a, rows);
-  else hca_cache_append_kernel<__nv_bfloat16><<<grid, kChunkThreads, 0, st>>>(a, rows);
-  return cudaGetLastError();
+  return f32 ? launch_behind(hca_cache_append_kernel<float>, dim3(grid), kChunkThreads, 0, st, a, rows)
+             : launch_behind(hca_cache_append_kernel<__nv_bfloat16>, dim3(grid), kChunkThreads, 0, st, a, rows);
 }
 
 }  // namespace hca

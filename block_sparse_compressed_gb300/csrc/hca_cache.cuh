@@ -15,6 +15,23 @@ constexpr int kMaxPos = 1 << 30;      // positions stay below this
 constexpr int kMinScaleExp = -96;     // smallest block scale 2^-96 (a block of zeros)
 constexpr int kTileKeys = 128;        // keys of an attention tile
 
+// Launches a kernel that is set up while the one in front of it on the stream
+// still runs, and calls tc::pdl_wait before it reads what that one wrote.
+template <typename K, typename... A>
+inline cudaError_t launch_behind(K *kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---------------------------------------------------------------------------
 // e4m3
 // ---------------------------------------------------------------------------

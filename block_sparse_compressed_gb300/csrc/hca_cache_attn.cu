@@ -32,6 +32,7 @@ constexpr int kSchedThreads = 1024;
 __global__ void __launch_bounds__(kSchedThreads) hca_cache_sched_kernel(const AttnParams p) {
   __shared__ long long tmp[33];
   const int tid = threadIdx.x;
+  tc::pdl_launch_dependents();  // the attention kernel waits for this one's end by itself
   bool ok = true;
   long long chunks = 0;
   for (int r0 = 0; r0 < p.R; r0 += kSchedThreads) {
@@ -109,21 +110,25 @@ __device__ __forceinline__ void poison(const AttnParams &p) {
 // ---------------------------------------------------------------------------
 constexpr int kSimtThreads = 128;
 
+template <int kCols>
 struct SimtShared {
-  float q[256][kSimtCols];            // [d][c]
-  float pr[kTileKeys][kSimtCols];     // probabilities times the block's scale
-  float red[4][kSimtCols];
-  float m[kSimtCols], f[kSimtCols], l[kSimtCols];
+  float q[256][kCols];                // [d][c]
+  float pr[kTileKeys][kCols];         // probabilities times the block's scale
+  float red[4][kCols];
+  float m[kCols], f[kCols], l[kCols];
   const uint8_t *rows[8];             // the tile's pages (NULL: none, or a bad block id or scale)
   float scale[8];
   int key0[8], kind[8];               // kind 0 raw, 1 compressed, 2 no page
   int first;
 };
 
+template <int kCols>
 __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const AttnParams p) {
   extern __shared__ uint8_t keys[];  // [128][D + 4] bytes: a row's words fall into different banks
-  __shared__ SimtShared sh;
+  __shared__ SimtShared<kCols> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  tc::pdl_wait();
+  tc::pdl_launch_dependents();
   const int ntiles = p.hdr->ntiles;
   if (tid == 0) {
     p.err[blockIdx.x] = ntiles < 0 ? HCA_ERR_CACHE : HCA_OK;
@@ -156,19 +161,20 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
     const int nreal = real_columns(p, g.npos, g.slice);
     const size_t row0 = (size_t)g.row0 * p.H + g.slice * p.HS;  // columns are rows of q and out in order
     const Pages pg = group_pages(g.pos0, g.npos, p.W, p.m, p.log_bs, p.comp.table != nullptr);
-    for (int i = tid; i < p.D * kSimtCols; i += kSimtThreads) {
+#pragma unroll 4
+    for (int i = tid; i < p.D * kCols; i += kSimtThreads) {
       const int c = i / p.D, d = i % p.D;
       sh.q[d][c] = c < nreal ? static_cast<const float *>(p.q)[row0 * p.D + i] : 0.f;
     }
-    if (tid < kSimtCols) {
+    if (tid < kCols) {
       sh.m[tid] = -INFINITY;
       sh.l[tid] = 0.f;
     }
-    float o[2][kSimtCols];
+    float o[2][kCols];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int c = 0; c < kSimtCols; ++c) o[x][c] = 0.f;
+      for (int c = 0; c < kCols; ++c) o[x][c] = 0.f;
     const float sl2 = p.scale * 1.4426950408889634f;
     for (int j = seg.j0; j < seg.j1; ++j) {
       __syncthreads();
@@ -194,22 +200,36 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
         }
       }
       __syncthreads();
-      // stage the tile's rows
-      for (int i = tid; i < kTileKeys * upr; i += kSimtThreads) {
-        const int row = i / upr, u = i % upr;
-        const uint8_t *rows = sh.rows[row >> p.log_bs];
-        uint32_t w = 0;
-        if (rows) w = reinterpret_cast<const uint32_t *>(rows + (size_t)(row & ((1 << p.log_bs) - 1)) * p.D)[u];
-        *reinterpret_cast<uint32_t *>(keys + row * pitch + 4 * u) = w;
+      // stage the tile's rows, 16 bytes at a time and 4 loads in flight
+      const int u16 = p.D / 16, units = kTileKeys * u16;
+      for (int i0 = tid; i0 < units; i0 += 4 * kSimtThreads) {
+        uint4 w[4];
+        int row[4], u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = i0 + k * kSimtThreads;
+          row[k] = i / u16;
+          u[k] = i - row[k] * u16;
+          const uint8_t *rows = i < units ? sh.rows[row[k] >> p.log_bs] : nullptr;
+          w[k] = make_uint4(0, 0, 0, 0);
+          if (rows) w[k] = reinterpret_cast<const uint4 *>(rows + (size_t)(row[k] & ((1 << p.log_bs) - 1)) * p.D)[u[k]];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (i0 + k * kSimtThreads >= units) break;
+          uint32_t *to = reinterpret_cast<uint32_t *>(keys + row[k] * pitch + 16 * u[k]);
+          to[0] = w[k].x; to[1] = w[k].y; to[2] = w[k].z; to[3] = w[k].w;
+        }
       }
       const int kind = sh.kind[tid >> p.log_bs];
       const float sk = sh.scale[tid >> p.log_bs];
       int ca = 0, cb = 0;
       if (kind < 2) key_columns(kind == 1, (long long)sh.key0[tid >> p.log_bs] + off, g.pos0, g.npos, p.HS, p.W, p.m, ca, cb);
       __syncthreads();
-      float s[kSimtCols];
+      float s[kCols];
 #pragma unroll
-      for (int c = 0; c < kSimtCols; ++c) s[c] = 0.f;
+      for (int c = 0; c < kCols; ++c) s[c] = 0.f;
+#pragma unroll 2
       for (int u = 0; u < upr; ++u) {
         const uint32_t w = *reinterpret_cast<const uint32_t *>(keys + tid * pitch + 4 * u);
         const float2 a = f32x2_from_e4m3x2(w & 0xffffu), b = f32x2_from_e4m3x2(w >> 16);
@@ -217,10 +237,10 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int c = 0; c < kSimtCols; ++c) s[c] = fmaf(kk[e], sh.q[4 * u + e][c], s[c]);
+          for (int c = 0; c < kCols; ++c) s[c] = fmaf(kk[e], sh.q[4 * u + e][c], s[c]);
       }
 #pragma unroll
-      for (int c = 0; c < kSimtCols; ++c) {
+      for (int c = 0; c < kCols; ++c) {
         // a masked key's row may hold anything, NaN among it
         s[c] = c >= ca && c < cb ? s[c] * (sl2 * sk) : -INFINITY;
         float mx = s[c];
@@ -229,7 +249,7 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
         if (lane == 0) sh.red[warp][c] = mx;
       }
       __syncthreads();
-      if (tid < kSimtCols) {
+      if (tid < kCols) {
         const float mx = fmaxf(fmaxf(sh.red[0][tid], sh.red[1][tid]), fmaxf(sh.red[2][tid], sh.red[3][tid]));
         const float mo = sh.m[tid], mn = fmaxf(mo, mx);
         sh.f[tid] = mn == -INFINITY ? 1.f : exp2f(mo - mn);
@@ -237,7 +257,7 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
       }
       __syncthreads();
 #pragma unroll
-      for (int c = 0; c < kSimtCols; ++c) {
+      for (int c = 0; c < kCols; ++c) {
         const float mn = sh.m[c];
         const float e = s[c] == -INFINITY ? 0.f : exp2f(s[c] - mn);
         sh.pr[tid][c] = e == 0.f ? 0.f : e * sk;
@@ -258,50 +278,51 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
         for (int u = 0; u < upr; ++u) *reinterpret_cast<uint32_t *>(keys + tid * pitch + 4 * u) = 0;
       }
       __syncthreads();
-      if (tid < kSimtCols)
+      if (tid < kCols)
         sh.l[tid] = sh.l[tid] * sh.f[tid] + ((sh.red[0][tid] + sh.red[1][tid]) + (sh.red[2][tid] + sh.red[3][tid]));
 #pragma unroll
       for (int x2 = 0; x2 < 2; ++x2) {
         const int d = tid % dpad + x2 * kSimtThreads;
         if (d >= p.D) break;
-        float acc[kSimtCols];
+        float acc[kCols];
 #pragma unroll
-        for (int c = 0; c < kSimtCols; ++c) acc[c] = 0.f;
+        for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+#pragma unroll 8
         for (int k = kfirst; k < kTileKeys; k += kstep) {
           const float v = f32x2_from_e4m3x2(keys[k * pitch + d]).x;
 #pragma unroll
-          for (int c = 0; c < kSimtCols; ++c) acc[c] = fmaf(sh.pr[k][c], v, acc[c]);
+          for (int c = 0; c < kCols; ++c) acc[c] = fmaf(sh.pr[k][c], v, acc[c]);
         }
 #pragma unroll
-        for (int c = 0; c < kSimtCols; ++c) o[x2][c] = fmaf(o[x2][c], sh.f[c], acc[c]);
+        for (int c = 0; c < kCols; ++c) o[x2][c] = fmaf(o[x2][c], sh.f[c], acc[c]);
       }
     }
     __syncthreads();
     // join the key subsets of a dimension (D < 128), then write
-    float *join = &sh.pr[0][0];  // [kstep][dpad][16] = 128 * 16
+    float *join = &sh.pr[0][0];  // [kstep][dpad][kCols]
     if (kstep > 1) {
 #pragma unroll
-      for (int c = 0; c < kSimtCols; ++c) join[tid * kSimtCols + c] = o[0][c];
+      for (int c = 0; c < kCols; ++c) join[tid * kCols + c] = o[0][c];
       __syncthreads();
       if (kfirst == 0)
         for (int k = 1; k < kstep; ++k)
 #pragma unroll
-          for (int c = 0; c < kSimtCols; ++c) o[0][c] += join[(k * dpad + tid) * kSimtCols + c];
+          for (int c = 0; c < kCols; ++c) o[0][c] += join[(k * dpad + tid) * kCols + c];
     }
 #pragma unroll
     for (int x2 = 0; x2 < 2; ++x2) {
       const int d = tid % dpad + x2 * kSimtThreads;
       if (d >= p.D || (kstep > 1 && kfirst > 0)) continue;
 #pragma unroll
-      for (int c = 0; c < kSimtCols; ++c) {
+      for (int c = 0; c < kCols; ++c) {
         if (c >= nreal) continue;
         if (seg.slot < 0) static_cast<float *>(p.out)[(row0 + c) * p.D + d] = o[x2][c] / sh.l[c];
-        else p.part_o[((size_t)seg.slot * kSimtCols + c) * p.D + d] = o[x2][c];
+        else p.part_o[((size_t)seg.slot * kCols + c) * p.D + d] = o[x2][c];
       }
     }
     if (tid < nreal) {
       if (seg.slot < 0) p.lse[row0 + tid] = (sh.m[tid] + log2f(sh.l[tid])) * 0.69314718055994531f;
-      else p.part_ml[(size_t)seg.slot * kSimtCols + tid] = make_float2(sh.m[tid], sh.l[tid]);
+      else p.part_ml[(size_t)seg.slot * kCols + tid] = make_float2(sh.m[tid], sh.l[tid]);
     }
   }
 }
@@ -474,24 +495,25 @@ __global__ void __launch_bounds__(kCombineThreads) hca_cache_combine_few_kernel(
   }
 }
 
+template <int kCols>
+cudaError_t simt(const AttnParams &p, cudaStream_t st) {
+  static tc::SmemAttrOnce attr;
+  const cudaError_t e = attr.ensure(reinterpret_cast<const void *>(hca_cache_simt_kernel<kCols>), kTileKeys * (256 + 4));
+  if (e != cudaSuccess) return e;
+  ProfScope prof(kKCacheSimt, st);
+  return launch_behind(hca_cache_simt_kernel<kCols>, dim3(p.grid), kSimtThreads, kTileKeys * (p.D + 4), st, p);
+}
+
 template <typename T>
 cudaError_t combine(const AttnParams &p, int gmax, int sms, cudaStream_t st) {
   // few groups: fewer than leave each 16 CTAs
   const bool few = (long long)gmax * 16 <= p.grid;
-  // its blocks are set up while the attention's last CTAs run
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = few ? dim3(4 * sms) : dim3(p.grid, (p.P * p.HS + 4 * kCombineWarps - 1) / (4 * kCombineWarps));
-  cfg.blockDim = dim3(kCombineThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  const dim3 grid = few ? dim3(4 * sms) : dim3(p.grid, (p.P * p.HS + 4 * kCombineWarps - 1) / (4 * kCombineWarps));
   ProfScope prof(kKCacheCombine, st);
-  if (few) return cudaLaunchKernelEx(&cfg, hca_cache_combine_few_kernel<T>, p);
-  return p.D <= 128 ? cudaLaunchKernelEx(&cfg, hca_cache_combine_kernel<T, 4>, p)
-                    : cudaLaunchKernelEx(&cfg, hca_cache_combine_kernel<T, 8>, p);
+  // its blocks are set up while the attention's last CTAs run
+  if (few) return launch_behind(hca_cache_combine_few_kernel<T>, grid, kCombineThreads, 0, st, p);
+  return p.D <= 128 ? launch_behind(hca_cache_combine_kernel<T, 4>, grid, kCombineThreads, 0, st, p)
+                    : launch_behind(hca_cache_combine_kernel<T, 8>, grid, kCombineThreads, 0, st, p);
 }
 
 // Columns of a group for H heads: enough for one position's slice of heads, and
@@ -500,10 +522,11 @@ cudaError_t combine(const AttnParams &p, int gmax, int sms, cudaStream_t st) {
 bool on_tensor_cores(int dtype) { return dtype == HCA_BF16; }
 
 int pick_columns(int N, int R, int H, int dtype) {
-  if (!on_tensor_cores(dtype)) return kSimtCols;
-  const int slices = (H + 127) / 128, HS = (H + slices - 1) / slices;
+  const int most = on_tensor_cores(dtype) ? 128 : kSimtCols;
+  const int slices = (H + most - 1) / most, HS = (H + slices - 1) / slices;
   const int T = R > 0 ? (N + R - 1) / R : 1;
   const long long want = (long long)HS * T;
+  if (!on_tensor_cores(dtype)) return want <= 4 ? 4 : want <= 8 ? 8 : kSimtCols;
   return want <= 32 ? 32 : want <= 64 ? 64 : 128;
 }
 
@@ -582,11 +605,8 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
     const cudaError_t e = tc_cache_attn(p, st);
     if (e != cudaSuccess) return e;
   } else {
-    static tc::SmemAttrOnce attr;
-    const cudaError_t e = attr.ensure(reinterpret_cast<const void *>(hca_cache_simt_kernel), kTileKeys * (256 + 4));
+    const cudaError_t e = p.NQ == 4 ? simt<4>(p, st) : p.NQ == 8 ? simt<8>(p, st) : simt<kSimtCols>(p, st);
     if (e != cudaSuccess) return e;
-    ProfScope prof(kKCacheSimt, st);
-    hca_cache_simt_kernel<<<p.grid, kSimtThreads, kTileKeys * (a.D + 4), st>>>(p);
   }
   const int gmax = (int)std::min<size_t>(l.gmax, 1 << 20);
   const cudaError_t e = tcs ? combine<__nv_bfloat16>(p, gmax, sms, st) : combine<float>(p, gmax, sms, st);

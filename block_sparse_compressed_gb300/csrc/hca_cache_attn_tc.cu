@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       if (x.last()) p.border[blockIdx.x] = border_of(p, g, c0, c1, quota, blockIdx.x);
     }
   } else {
+    pdl_wait();  // for the schedule
     ntiles = p.hdr->ntiles;
     quota = cta_quota(ntiles, p.grid, p.min_tiles);
     busy = ntiles > 0 && blockIdx.x <= (ntiles - 1) / quota;
@@ -921,6 +922,7 @@ cudaError_t launch(const AttnParams &p, cudaStream_t st) {
   const cudaError_t e = attr.ensure(reinterpret_cast<const void *>(hca_cache_attn_kernel<NQ, D>), C::kSmem);
   if (e != cudaSuccess) return e;
   ProfScope prof(kKCacheAttn, st);
+  if (!p.in_cta) return launch_behind(hca_cache_attn_kernel<NQ, D>, dim3(p.grid), kThreads, C::kSmem, st, p);
   hca_cache_attn_kernel<NQ, D><<<p.grid, kThreads, C::kSmem, st>>>(p);
   return cudaGetLastError();
 }
