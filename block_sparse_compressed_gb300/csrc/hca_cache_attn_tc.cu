@@ -59,6 +59,7 @@ constexpr int kWG = 128;
 constexpr int kThreads = 3 * kWG;  // softmax | converter | page and MMA warp
 constexpr int kTmem = 256;      // S of keys 0 .. 63 | S of keys 64 .. 127 (P takes the first half of each) | O
 constexpr uint32_t kColO = 128;
+enum { kBarOut = 1, kBarQ = 2 };  // named barriers of the softmax's and the converter's warps
 
 template <int NQ, int D>
 struct Cfg {
@@ -91,7 +92,7 @@ struct Shared {
   uint4 join[kWG * 4];  // O on its way out: 64 bytes of each lane's row
   uint64_t meta_full[kMetaStages], meta_empty[kMetaStages];
   uint64_t raw_full[kHalfStages], kv_full[kHalfStages], kv_empty[kHalfStages];
-  uint64_t q_full, s_full[2], p_full[2], pv_done[2], drain, never;
+  uint64_t q_full, q_read, s_full[2], p_full[2], pv_done[2], drain, never;
   uint64_t scale_full[kMetaStages];
   PageMeta meta[kMetaStages][8];
   uint32_t nan_keys[kMetaStages][4];  // keys whose rows hold a NaN that not everybody sees
@@ -102,6 +103,7 @@ struct Shared {
   // workspace's groups
   Segment seg[kMaxSegs];
   int gbase[kThreads];
+  float q_factor[NQ];                            // log2(e) |scale| / (a row's factor)
   float2 ml[kWG];                                // copies: reference and sum of every lane
   int2 sums[2][kThreads / 32];                   // tiles and groups of each warp
   uint32_t tmem_base;
@@ -202,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       mbar_init(&sh.kv_empty[s], 1);
     }
     mbar_init(&sh.q_full, kWG);
+    mbar_init(&sh.q_read, kWG);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&sh.s_full[h], 1);
       mbar_init(&sh.p_full[h], kWG);
@@ -512,17 +515,81 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       const uint32_t to0 = smem_u32(smem) + (ch >> 2) * kHalfTile + row0 * 128;
       const uint32_t swz0 = (((2 * (ch & 3)) ^ (row0 & 7)) << 4);  // the other piece's differs in one bit
       static_assert(kRowStep % 8 == 0, "a thread's rows have one swizzle");
-      uint32_t n = 0;
-      bool ok = true;
+      const int q_row = ct % NQ, copy = ct / NQ;
+      // q of a group into shared memory: D / 8 neighbouring lanes copy a row's
+      // 16-byte pieces as they are, asynchronously; rows beyond the group's are
+      // zero.
+      constexpr int kLanes = D / 8, step = kWG / kLanes;  // rows at a time
+      const int q_ch = ct % kLanes, c0q = ct / kLanes;
+      const uint32_t dst = smem_u32(smem) + C::kOffQ + (q_ch >> 3) * kHalfTile;
+      auto copy_q = [&](const Segment &g) {
+        const int nq = real_columns(p, g.npos, g.slice());
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)g.row0 * p.H + g.slice() * p.HS) * D + q_ch * 8;
 #pragma unroll 1
-      for (int k = 0; ok; ++k) {
+        for (int c = c0q; c < NQ; c += step)
+          cp_async_16(dst + c * 128 + (((q_ch & 7) ^ (c & 7)) << 4), c < nq ? q + (size_t)c * D : q, c < nq ? 16 : 0);
+      };
+      copy_q(segment(0));
+      uint32_t n = 0;
+      // no way out when a wait has given up: the warps meet at barriers
+#pragma unroll 1
+      for (int k = 0;; ++k) {
         const Segment g = segment(k);
         const uint32_t end = n + 2 * (g.j1 - g.j0);
+        // q of the first group comes before its keys do; that of a later one has to
+        // wait for the last group's scores, its first tile has not
+        const uint32_t q_at = k == 0 ? 0 : n + 2;
 #pragma unroll 1
-        for (; n < end; ++n) {
+        for (;; ++n) {
+          if (n == q_at) {
+            // bf16 -> fp16 with a factor for each row, by the row's thread (its
+            // copies share the work): the largest |q| becomes 224 .. 448; a
+            // negative scale goes into q's sign (of a row with an infinity nothing
+            // but NaN comes, whatever the factor)
+            if (k > 0) {
+              // the last group's scores have been made and its factors read
+              (void)wait_bar(&sh.q_read, (k - 1) & 1);
+              (void)wait_bar(&sh.s_full[1], ((q_at >> 1) - 2) & 1);
+              copy_q(g);
+            }
+            cp_async_wait();
+            named_bar_sync(kBarQ, kWG);
+            const uint32_t q_at_row = smem_u32(smem) + C::kOffQ + q_row * 128;
+            auto piece_at = [&](int c) { return q_at_row + (c >> 3) * kHalfTile + (((c & 7) ^ (q_row & 7)) << 4); };
+            uint32_t amax = 0;
+#pragma unroll 4
+            for (int c = 0; c < kLanes; ++c) {
+              uint32_t w[4];
+              ld_shared(piece_at(c), w);
+              amax = bf16x2_max(amax, bf16x2_max(bf16x2_max(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                                 bf16x2_max(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu)));
+            }
+            const int ex = scale_exponent(__uint_as_float(max(amax & 0xffffu, amax >> 16) << 16));
+            const float inv = p.scale < 0.f ? -exp2_int(-ex) : p.scale > 0.f ? exp2_int(-ex) : 0.f;
+            if (copy == 0) sh.q_factor[q_row] = exp2_int(ex) * fabsf(p.scale) * 1.4426950408889634f;
+            if constexpr (C::kCopies > 1) named_bar_sync(kBarQ, kWG);
+            const uint64_t inv2 = f32x2(__float_as_uint(inv), __float_as_uint(inv));
+            constexpr int kOwn = kLanes / C::kCopies;  // pieces of each copy
+#pragma unroll(kOwn < 2 ? kOwn : 2)
+            for (int i = 0; i < kOwn; ++i) {
+              const uint32_t at = piece_at(copy * kOwn + i);
+              uint32_t w[4], f[4];
+              ld_shared(at, w);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float lo, hi;
+                f32x2_split(fmul2(f32x2(w[e] << 16, w[e] & 0xffff0000u), inv2), lo, hi);
+                f[e] = f16x2_rn(lo, hi);
+              }
+#pragma unroll
+              for (int y = 0; y < C::kCopies; ++y) st_shared(at + y * NQ * 128, f[0], f[1], f[2], f[3]);
+            }
+            fence_async_smem();
+            mbar_arrive(&sh.q_full);
+          }
+          if (n == end) break;
           const int ms = (n >> 1) % kMetaStages, st = n % kHalfStages, h = n & 1;
-          ok = wait_bar(&sh.raw_full[st], (n / kHalfStages) & 1);
-          if (!ok) break;
+          (void)wait_bar(&sh.raw_full[st], (n / kHalfStages) & 1);
           const uint32_t valid = sh.valid[ms];
           const bool look = !((sh.all_seen[ms] >> h) & 1);
           const uint32_t from = from0 + (st >> 1) * C::kRawStride + h * 64 * D, to = to0 + (st >> 1) * C::kStageBytes + h * 8192;
@@ -589,167 +656,18 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       constexpr int kSpan = C::kSpan;
       const int row = tid % NQ, copy = tid / NQ;  // row of the group
       const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
-      // q of a group into shared memory: D / 8 neighbouring lanes copy a row's
-      // 16-byte pieces as they are, asynchronously; rows beyond the group's are
-      // zero.
-      constexpr int kLanes = D / 8, step = kWG / kLanes;  // rows at a time
-      const int ch = tid % kLanes, c0q = tid / kLanes;
-      const uint32_t dst = smem_u32(smem) + C::kOffQ + (ch >> 3) * kHalfTile;
-      auto copy_q = [&](const Segment &g) {
-        const int nq = real_columns(p, g.npos, g.slice());
-        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)g.row0 * p.H + g.slice() * p.HS) * D + ch * 8;
-#pragma unroll 1
-        for (int c = c0q; c < NQ; c += step)
-          cp_async_16(dst + c * 128 + (((ch & 7) ^ (c & 7)) << 4), c < nq ? q + (size_t)c * D : q, c < nq ? 16 : 0);
-      };
-      Segment g = segment(0);
-      copy_q(g);
       uint32_t n = 0;
-      float m_run = 0.f, l_run = 0.f, cs = 0.f;
-      bool last = false;
-      // A pass makes a group's q ready, so that the tensor cores have its first
-      // scores to make, ends the group before and then goes through the tiles.
 #pragma unroll 1
       for (int k = 0;; ++k) {
-        if (!last) g = segment(k);
-        if (!last) {
-          // bf16 -> fp16 with a factor for each row, by the row's thread (its
-          // copies share the work): the largest |q| becomes 224 .. 448; a
-          // negative scale goes into q's sign (of a row with an infinity nothing
-          // but NaN comes, whatever the factor)
-          cp_async_wait();
-          named_bar_sync(1, kWG);
-          const uint32_t qrow = smem_u32(smem) + C::kOffQ + row * 128;
-          auto piece_at = [&](int c) { return qrow + (c >> 3) * kHalfTile + (((c & 7) ^ (row & 7)) << 4); };
-          uint32_t amax = 0;
-#pragma unroll 4
-          for (int c = 0; c < kLanes; ++c) {
-            uint32_t w[4];
-            ld_shared(piece_at(c), w);
-            amax = bf16x2_max(amax, bf16x2_max(bf16x2_max(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                                               bf16x2_max(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu)));
-          }
-          const int ex = scale_exponent(__uint_as_float(max(amax & 0xffffu, amax >> 16) << 16));
-          const float inv = p.scale < 0.f ? -exp2_int(-ex) : p.scale > 0.f ? exp2_int(-ex) : 0.f;
-          cs = exp2_int(ex) * fabsf(p.scale) * 1.4426950408889634f;
-          if constexpr (C::kCopies > 1) named_bar_sync(1, kWG);
-          const uint64_t inv2 = f32x2(__float_as_uint(inv), __float_as_uint(inv));
-          constexpr int kOwn = kLanes / C::kCopies;  // pieces of each copy
-#pragma unroll(kOwn < 4 ? kOwn : 4)
-          for (int i = 0; i < kOwn; ++i) {
-            const uint32_t at = piece_at(copy * kOwn + i);
-            uint32_t w[4], f[4];
-            ld_shared(at, w);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float lo, hi;
-              f32x2_split(fmul2(f32x2(w[e] << 16, w[e] & 0xffff0000u), inv2), lo, hi);
-              f[e] = f16x2_rn(lo, hi);
-            }
-#pragma unroll
-            for (int y = 0; y < C::kCopies; ++y) st_shared(at + y * NQ * 128, f[0], f[1], f[2], f[3]);
-          }
-          fence_async_smem();
-          mbar_arrive(&sh.q_full);
-        }
-        if (k > 0) {
-          const Segment e = segment(k - 1);  // the group that ends
-          const int nreal = real_columns(p, e.npos, e.slice());
-          if (*abort_flag) l_run = __int_as_float(0x7fc00000);
-          const bool whole = e.slot < 0;
-          const size_t orow = (size_t)e.row0 * p.H + e.slice() * p.HS;  // rows of the group are rows of q and out in order
-          float weight = 1.f;
-          if constexpr (C::kCopies > 1) {
-            // the copies' common reference and sum
-            sh.ml[tid] = make_float2(m_run, l_run);
-            named_bar_sync(1, kWG);
-            float M = -INFINITY, L = 0.f;
-#pragma unroll
-            for (int y = 0; y < C::kCopies; ++y) M = fmaxf(M, sh.ml[row + y * NQ].x);
-#pragma unroll
-            for (int y = 0; y < C::kCopies; ++y) {
-              const float2 v = sh.ml[row + y * NQ];
-              const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
-              L += v.y != 0.f ? f * v.y : 0.f;  // NaN stays
-              if (y == copy) weight = f;
-            }
-            if (l_run != l_run) L = l_run;
-            m_run = M;
-            l_run = L;
-          }
-          if (row < nreal && copy == 0) {
-            if (whole) p.lse[orow + row] = (m_run + log2f(l_run)) * 0.69314718055994531f;
-            else p.part_ml[(size_t)e.slot * NQ + row] = make_float2(m_run, l_run);
-          }
-          const float inv = weight * (whole ? 1.f / l_run : 1.f);
-          (void)wait_bar(&sh.pv_done[1], (n - 1) & 1);
-          tc_fence_after();
-          // O leaves through shared memory, 64 bytes of a row at a time, so that
-          // four lanes write a row's: a store to 32 rows takes 32 cycles.
-          uint8_t *to = whole ? static_cast<uint8_t *>(p.out) + orow * D * 2 : reinterpret_cast<uint8_t *>(p.part_o + (size_t)e.slot * NQ * D);
-          const int row_bytes = whole ? D * 2 : D * 4, piece = lane & 3;
-          const uint32_t join = smem_u32(sh.join);
-          const uint32_t mine = join + tid * 64, swz = (tid >> 1) & 3;
-          const bool packed = C::kCopies == 1 && whole;  // staged as bf16 already: 32 columns
-          const int rounds = packed ? D / 32 : D / 16;
-#pragma unroll 1
-          for (int c = 0; c < rounds; ++c) {
-            uint32_t o[16];
-            if (packed) {
-              uint32_t x[32];
-              tmem_ld32(lane_addr + kColO + c * 32, x);
-              tmem_wait_ld();
-#pragma unroll
-              for (int y = 0; y < 16; ++y) o[y] = pack_bf16x2(__uint_as_float(x[2 * y]) * inv, __uint_as_float(x[2 * y + 1]) * inv);
-            } else {
-              tmem_ld16(lane_addr + kColO + c * 16, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * inv);
-            }
-#pragma unroll
-            for (int y = 0; y < 4; ++y) st_shared(mine + ((y ^ swz) << 4), o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-            if constexpr (C::kCopies == 1) {
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int r = warp * 32 + i * 8 + (lane >> 2);
-                uint32_t v[4];
-                ld_shared(join + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4), v);
-                if (r < nreal) *reinterpret_cast<uint4 *>(to + (size_t)r * row_bytes + c * 64 + piece * 16) = make_uint4(v[0], v[1], v[2], v[3]);
-              }
-              __syncwarp();
-            } else {
-              named_bar_sync(1, kWG);
-#pragma unroll
-              for (int i = 0; i < NQ / 32; ++i) {
-                const int r = i * 32 + (tid >> 2);
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int x = 0; x < C::kCopies; ++x) {
-                  uint32_t v[4];
-                  ld_shared(join + (r + x * NQ) * 64 + ((piece ^ ((r >> 1) & 3)) << 4), v);
-#pragma unroll
-                  for (int y = 0; y < 4; ++y) sum[y] += __uint_as_float(v[y]);
-                }
-                uint8_t *at = to + (size_t)r * row_bytes;
-                if (r < nreal) {
-                  if (whole) *reinterpret_cast<uint2 *>(at + c * 32 + piece * 8) = make_uint2(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]));
-                  else *reinterpret_cast<float4 *>(at + c * 64 + piece * 16) = make_float4(sum[0], sum[1], sum[2], sum[3]);
-                }
-              }
-              named_bar_sync(1, kWG);
-            }
-          }
-          tc_fence_before();
-        }
-        if (last) break;
+        const Segment g = segment(k);
         const int nreal = real_columns(p, g.npos, g.slice());
         const int pos = g.pos0 + (row < nreal ? row / p.HS : 0);
         // what the row sees: raw keys [raw_lo, pos], entries [0, entries)
         const int raw_lo = pos - p.W + 1, entries = (pos + 1) / p.m;
-        m_run = -INFINITY;
-        l_run = 0.f;
+        float m_run = -INFINITY, l_run = 0.f;
+        (void)wait_bar(&sh.q_full, k & 1);
+        const float cs = sh.q_factor[row];
+        mbar_arrive(&sh.q_read);
 #pragma unroll 1
         for (int j = g.j0; j < g.j1; ++j, ++n) {
           const int ms = n % kMetaStages;
@@ -760,8 +678,6 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           for (int h = 0; h < 2; ++h) {
             (void)wait_bar(&sh.s_full[h], n & 1);
             tc_fence_after();
-            // the group's last scores are made: the next one's q may come
-            if (h == 1 && j == g.j1 - 1 && !g.last()) copy_q(segment(k + 1));
             const int k0 = h * 64 + copy * kSpan;  // first of the thread's keys, uniform in a warp
             uint32_t sv[kSpan];
             if constexpr (kSpan == 16) {
@@ -901,7 +817,94 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           }
           mbar_arrive(&sh.meta_empty[ms]);
         }
-        last = g.last();
+        if (*abort_flag) l_run = __int_as_float(0x7fc00000);
+        const bool whole = g.slot < 0;
+        const size_t orow = (size_t)g.row0 * p.H + g.slice() * p.HS;  // rows of the group are rows of q and out in order
+        float weight = 1.f;
+        if constexpr (C::kCopies > 1) {
+          // the copies' common reference and sum
+          sh.ml[tid] = make_float2(m_run, l_run);
+          named_bar_sync(kBarOut, kWG);
+          float M = -INFINITY, L = 0.f;
+#pragma unroll
+          for (int y = 0; y < C::kCopies; ++y) M = fmaxf(M, sh.ml[row + y * NQ].x);
+#pragma unroll
+          for (int y = 0; y < C::kCopies; ++y) {
+            const float2 v = sh.ml[row + y * NQ];
+            const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
+            L += v.y != 0.f ? f * v.y : 0.f;  // NaN stays
+            if (y == copy) weight = f;
+          }
+          if (l_run != l_run) L = l_run;
+          m_run = M;
+          l_run = L;
+        }
+        if (row < nreal && copy == 0) {
+          if (whole) p.lse[orow + row] = (m_run + log2f(l_run)) * 0.69314718055994531f;
+          else p.part_ml[(size_t)g.slot * NQ + row] = make_float2(m_run, l_run);
+        }
+        const float inv = weight * (whole ? 1.f / l_run : 1.f);
+        (void)wait_bar(&sh.pv_done[1], (n - 1) & 1);
+        tc_fence_after();
+        // O leaves through shared memory, 64 bytes of a row at a time, so that
+        // four lanes write a row's: a store to 32 rows takes 32 cycles.
+        uint8_t *to = whole ? static_cast<uint8_t *>(p.out) + orow * D * 2 : reinterpret_cast<uint8_t *>(p.part_o + (size_t)g.slot * NQ * D);
+        const int row_bytes = whole ? D * 2 : D * 4, piece = lane & 3;
+        const uint32_t join = smem_u32(sh.join);
+        const uint32_t mine = join + tid * 64, swz = (tid >> 1) & 3;
+        const bool packed = C::kCopies == 1 && whole;  // staged as bf16 already: 32 columns
+        const int rounds = packed ? D / 32 : D / 16;
+#pragma unroll 1
+        for (int c = 0; c < rounds; ++c) {
+          uint32_t o[16];
+          if (packed) {
+            uint32_t x[32];
+            tmem_ld32(lane_addr + kColO + c * 32, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] = pack_bf16x2(__uint_as_float(x[2 * y]) * inv, __uint_as_float(x[2 * y + 1]) * inv);
+          } else {
+            tmem_ld16(lane_addr + kColO + c * 16, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * inv);
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) st_shared(mine + ((y ^ swz) << 4), o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+          if constexpr (C::kCopies == 1) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = warp * 32 + i * 8 + (lane >> 2);
+              uint32_t v[4];
+              ld_shared(join + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4), v);
+              if (r < nreal) *reinterpret_cast<uint4 *>(to + (size_t)r * row_bytes + c * 64 + piece * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+            __syncwarp();
+          } else {
+            named_bar_sync(kBarOut, kWG);
+#pragma unroll
+            for (int i = 0; i < NQ / 32; ++i) {
+              const int r = i * 32 + (tid >> 2);
+              float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int x = 0; x < C::kCopies; ++x) {
+                uint32_t v[4];
+                ld_shared(join + (r + x * NQ) * 64 + ((piece ^ ((r >> 1) & 3)) << 4), v);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) sum[y] += __uint_as_float(v[y]);
+              }
+              uint8_t *at = to + (size_t)r * row_bytes;
+              if (r < nreal) {
+                if (whole) *reinterpret_cast<uint2 *>(at + c * 32 + piece * 8) = make_uint2(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]));
+                else *reinterpret_cast<float4 *>(at + c * 64 + piece * 16) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+              }
+            }
+            named_bar_sync(kBarOut, kWG);
+          }
+        }
+        tc_fence_before();
+        if (g.last()) break;
       }
     }
   }
