@@ -352,7 +352,6 @@ __global__ void __launch_bounds__(kChunkThreads) hca_cache_append_kernel(const C
     // the order of the list does not matter
     if (i < cnt && brk && s >= 0 && s < limit) lead[atomicAdd(&nlead, 1)] = i;
   }
-  tc::pdl_wait();  // for the owners
   __syncthreads();
   auto length = [&](int i) {
     int w = (i + 1) >> 5;
@@ -364,10 +363,6 @@ __global__ void __launch_bounds__(kChunkThreads) hca_cache_append_kernel(const C
     const int i = lead[j], n = length(i);
     if (n < kLongRun) continue;
     const int t = t0 + i, slot = slot_of[i + 1], blk = slot >> a.log_bs, off = slot & (a.bs - 1);
-    if (a.owner[blk] != t) {
-      err = HCA_ERR_CACHE;
-      continue;
-    }
     const T *x = static_cast<const T *>(a.x) + (size_t)t * a.D;
     uint8_t *dst = a.pool + (size_t)slot * a.D;
     const int units = n * a.D / 16;
@@ -383,6 +378,11 @@ __global__ void __launch_bounds__(kChunkThreads) hca_cache_append_kernel(const C
 #pragma unroll
       for (int k = 0; k < kHold; ++k)
         if (u0 + k * kChunkThreads + tid < units) amax = fmaxf(amax, finite_max(v[k]));
+    }
+    tc::pdl_wait();  // for the owners
+    if (a.owner[blk] != t) {
+      err = HCA_ERR_CACHE;
+      continue;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -405,6 +405,7 @@ __global__ void __launch_bounds__(kChunkThreads) hca_cache_append_kernel(const C
       }
     }
   }
+  tc::pdl_wait();
   for (int j = warp; j < nlead; j += kChunkThreads / 32)
     if (length(lead[j]) < kLongRun) err = max(err, append_run<T, true>(a, t0 + lead[j], lane));
   if (__any_sync(0xffffffffu, err != HCA_OK) && lane == 0) atomicExch(a.status, HCA_ERR_CACHE);
