@@ -19,14 +19,15 @@
 // (quarter) of a half's keys: P is zero for the others.  The copies are so many
 // independent streams of the online softmax, joined when the group ends.
 //
-// The cache's e4m3 values become fp16 on the way to shared memory, exactly, once
-// for both products and all rows: converter warps load pages of global memory
-// into registers as soon as they have stored a tile, behind L2 prefetches
-// that the page warp issues up to four tiles ahead.  A key's block scale s
-// multiplies one number, its score; P is p * s, and the row's sum divides by s
-// again.  A row of q is scaled by a power of two, so its 8 bits survive in fp16
-// (what is below 2^-32 of its largest value is lost); p * s is rounded to fp16
-// (11 bits; 2^-25 of the row's reference where tiny).
+// The cache's e4m3 values become fp16, exactly, once for both products and all
+// rows.  A page is contiguous, so one bulk copy brings it to shared memory, into
+// the half of its fp16 rows' bytes that the converter warps overwrite last; they
+// also make q ready (below) while the softmax warps end the group before.  A
+// key's block scale s multiplies its score, and its probability before that is
+// rounded to fp16.  q becomes fp16 with a power of two for each row that puts its
+// largest value at 224 .. 448: bf16's 8 bits fit, what falls below 2^-14 loses
+// bits (2^-33 of the row's largest value); p * s is rounded to fp16 (11 bits;
+// 2^-25 of the row's reference where tiny).
 //
 // The reference exponent of a row is its largest score so far, raised only when
 // beaten by 2^8 (fp16 has room for 2^15), so O is rarely rescaled.
@@ -35,6 +36,23 @@
 // 0 * NaN is not 0: of the pages that not every row sees whole, the converter
 // stores zeros for keys with a NaN and notes them in a bit mask, by which the
 // softmax gives a NaN to whoever sees them.
+//
+// Bounds.  A half's scores take the tensor cores 384 cycles (8 products of 128 x
+// 64 x 16 at 48, bound by their operands from shared memory) and its part of O
+// 254, so a tile 1,228 when products are queued; but the time from issue to the
+// softmax's first look is 805 and 590, and a half's softmax 1,100.  Two CTAs of an
+// SM fill part of each other's gaps: 64 tokens over 95,000 rows each (199 MB of
+// cache, 64 heads, D = 128) take 98 us, 2.0 TB/s and 514 TFLOP/s, with the tensor
+// cores busy half of the time.  One decode step of 64 requests at 128 keys an
+// entry takes 22.6 us, of which 2.6 are the schedule, 3 the way to the first
+// scores and 2 the way out; chunks of 2,571 prompt tokens 87 us, two thirds of it
+// beginnings and ends of their groups of 2 tokens.
+// Measured and left, each against the kernel of its time: scores of a whole tile
+// at once (128 x 128 x 16 at 64 cycles: the tensor cores do less, but the softmax
+// waits: 109 us for 102); two softmax warpgroups, a half each (99 us for 96: the
+// products' latency is the limit, not the softmax's); pages through the
+// converter's registers (the same time, 4 KB more code); the next tile's loads
+// between a tile's stores (135 us for 105).
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -56,7 +74,7 @@ constexpr int kStages = 2;      // fp16 tiles; filled and released by halves
 constexpr int kHalfStages = 2 * kStages;
 constexpr int kMaxSegs = 64;    // pieces of groups listed in shared memory
 constexpr int kWG = 128;
-constexpr int kThreads = 3 * kWG;  // softmax | converter | page and MMA warp
+constexpr int kThreads = 3 * kWG;  // softmax | converter | page, MMA and copy warps
 constexpr int kTmem = 256;      // S of keys 0 .. 63 | S of keys 64 .. 127 (P takes the first half of each) | O
 constexpr uint32_t kColO = 128;
 enum { kBarOut = 1, kBarQ = 2 };  // named barriers of the softmax's and the converter's warps
