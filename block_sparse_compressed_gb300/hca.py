@@ -537,7 +537,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _enqueue(dev: torch.device, f, *args) -> int:
     """f(*args, stream) on the device's current stream."""
-    if dev.type == "cuda" and _raw_stream is not None and dev.index == torch.cuda.current_device():
+    if dev.type != "cuda":
+        raise ValueError(f"the cache calls work on CUDA tensors, not on {dev}")
+    if _raw_stream is not None and dev.index == torch.cuda.current_device():
         return f(*args, _raw_stream(dev.index))
     with _on(dev):
         return f(*args, _stream(dev))
@@ -559,7 +561,19 @@ def _fits(t: torch.Tensor, name: str, shape, dtype, device) -> int:
     return t.data_ptr()
 
 
+def _scratch(ws: torch.Tensor, dev: torch.device) -> Tuple[int, int]:
+    """Pointer and bytes of a caller's workspace (what it holds is for the C function to check)."""
+    if ws.dtype is not torch.uint8:
+        raise TypeError(f"ws has dtype {ws.dtype}, expected {torch.uint8}")
+    if ws.device != dev:
+        raise ValueError(f"ws is on {ws.device}, expected {dev}")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel()
+
+
 _I32, _F32, _E4M3 = torch.int32, torch.float32, torch.float8_e4m3fn
+_I32_MAX = (1 << 31) - 1  # no window and no ratio reaches further than that
 
 
 @functools.lru_cache(maxsize=4096)
@@ -605,8 +619,8 @@ def hca_cache_plan(held: torch.Tensor, added: torch.Tensor, table: torch.Tensor,
     rc = _enqueue(dev, lib.hca_cache_plan, _fits(held, "held", (R,), _I32, dev), _fits(added, "added", (R,), _I32, dev),
                   _fits(table, "table", (R, cols), _I32, dev), _fits(free_blocks, "free_blocks", (nfree,), _I32, dev),
                   _fits(free_count, "free_count", (1,), _I32, dev), _fits(free_left, "free_left", (1,), _I32, dev),
-                  _fits(start, "start", (R + 1,), _I32, dev), _fits(slots, "slots", (nslots,), _I32, dev), R, cols, bs, m,
-                  nblocks, nfree, nslots, ws.data_ptr(), ws.numel())
+                  _fits(start, "start", (R + 1,), _I32, dev), _fits(slots, "slots", (nslots,), _I32, dev), R, cols, bs,
+                  min(m, _I32_MAX), nblocks, nfree, nslots, *_scratch(ws, dev))
     if rc != 0:
         _check(rc, "hca_cache_plan")
     if check:
@@ -633,7 +647,7 @@ def hca_cache_append(x: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor, s
     ws = torch.empty(_append_ws_bytes(nblocks), dtype=torch.uint8, device=dev) if ws is None else ws
     rc = _enqueue(dev, lib.hca_cache_append, _fits(x, "x", (N, D), x.dtype, dev), _fits(slots, "slots", (N,), _I32, dev),
                   _fits(pool, "pool", (nblocks, bs, D), _E4M3, dev), _fits(scale, "scale", (nblocks,), _F32, dev), N, D,
-                  bs, nblocks, dt, ws.data_ptr(), ws.numel())
+                  bs, nblocks, dt, *_scratch(ws, dev))
     if rc != 0:
         _check(rc, "hca_cache_append")
     if check:
@@ -675,8 +689,8 @@ def hca_cache_attn(q: torch.Tensor, start: torch.Tensor, held: torch.Tensor, raw
     ws = torch.empty(_attn_ws_bytes(N, R, H, D, dt), dtype=torch.uint8, device=dev) if ws is None else ws
     rc = _enqueue(dev, lib.hca_cache_attn, _fits(q, "q", (N, H, D), q.dtype, dev), _fits(start, "start", (R + 1,), _I32, dev),
                   _fits(held, "held", (R,), _I32, dev), *args, _fits(out, "out", (N, H, D), q.dtype, dev),
-                  _fits(lse, "lse", (N, H), _F32, dev), N, R, H, D, min(W, 1 << 30), m, bs, scale, dt, ws.data_ptr(),
-                  ws.numel())
+                  _fits(lse, "lse", (N, H), _F32, dev), N, R, H, D, min(W, _I32_MAX), min(m, _I32_MAX), bs, scale, dt,
+                  *_scratch(ws, dev))
     if rc != 0:
         _check(rc, "hca_cache_attn")
     if check:

@@ -299,6 +299,16 @@ def test_attention_matches_oracle(held, added, H, D, W, m, bs, dtype, comp):
     check_attn(got, q, start, h, raw, c, W, m, scale_of(D), dtype)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bs", [16, 32, 64, 128])
+@pytest.mark.parametrize("H,T", [(3, 1), (40, 1), (64, 1), (64, 2), (128, 1)])
+def test_attention_of_every_block_size_and_group(D, bs, H, T):
+    held = [5 * bs + 3, 0, 700]
+    q, start, h, raw, c = attn_case(held, [T, 1, T], H, D, 150, 2, bs, BF16, bs + H + T)
+    got = hca.hca_cache_attn(q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), 150, 2, scale_of(D), check=True)
+    check_attn(got, q, start, h, raw, c, 150, 2, scale_of(D), BF16)
+
+
 @pytest.mark.parametrize("D", [16, 48, 80, 256])
 def test_fp32_attention_of_other_head_dims(D):
     held, added, H, W, m, bs = [77, 300], [2, 1], 3, 40, 8, 16
@@ -727,6 +737,13 @@ def test_results_go_into_the_callers_tensors():
     assert got[0] is out and got[1] is lse and torch.equal(out, want[0]) and torch.equal(lse, want[1])
     with pytest.raises(hca.HCAError):
         hca.hca_cache_attn(*args, ws=ws[:-1])
+    with pytest.raises(ValueError):
+        hca.hca_cache_attn(*args, ws=ws.cpu())
+    with pytest.raises(TypeError):
+        hca.hca_cache_attn(*args, ws=ws.float())
+    none = hca.hca_cache_attn(*args[:6], 1 << 40, args[7], check=True)   # a ratio that no length reaches
+    bare = hca.hca_cache_attn(*args[:4], None, 40, 1, args[7], check=True)
+    assert torch.equal(none[0], bare[0]) and torch.equal(none[1], bare[1])
     with pytest.raises(ValueError):
         hca.hca_cache_attn(*args, out=out[:2])
     with pytest.raises(TypeError):

@@ -136,3 +136,23 @@ def test_the_short_way_declines_what_is_not_ordinary():
     for raw, comp in ((c, None), (c, c), (list(c), None), (c[:2], None), (None, c)):
         assert hca._py.cache_attn(torch.zeros(2, 4, 64), i32(3), i32(2), raw, comp, 8, 4, 0.1, None, None, None) is None
     assert hca._py.cache_attn(torch.zeros(2, 4, 64), i32(3), i32(2), c, None, 1 << 40, 4, 0.1, None, None, None) is None
+
+
+def test_the_binding_refuses_other_devices_and_workspaces():
+    # nothing of a CPU tensor or a foreign workspace reaches the device
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    pool, scale, x = torch.zeros(4, 16, 64).to(torch.float8_e4m3fn), torch.ones(4), torch.zeros(3, 64)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    c = (pool, scale, i32(2, 3))
+    calls = (lambda **k: hca.hca_cache_append(x, i32(3), pool, scale, **k),
+             lambda **k: hca.hca_cache_plan(i32(3), i32(3), i32(3, 2), i32(5), i32(1), 8, 16, 4, **k),
+             lambda **k: hca.hca_cache_attn(torch.zeros(2, 4, 64), i32(3), i32(2), c, None, 8, 4, 0.1, **k))
+    for call in calls:
+        with pytest.raises(ValueError, match="CUDA"):
+            call(ws=ws)
+        with pytest.raises(ValueError, match="ws is on"):
+            call(ws=torch.empty(1 << 20, dtype=torch.uint8, device="meta"))
+        with pytest.raises(TypeError):
+            call(ws=ws.float())
+        with pytest.raises(ValueError, match="contiguous"):
+            call(ws=ws[::2])
