@@ -145,7 +145,13 @@ struct SchedHeader {  // at the start of the workspace
   int32_t status;
   int32_t ngroups;
   int32_t ntiles;     // -1: refused, the attention fills its outputs with NaN
+  int32_t longest;    // tiles of the longest group
 };
+
+// Many short groups (long prompts): the line can be cut between groups, which
+// saves every CTA a partial group's beginning and end and the join.  A group then
+// counts for kGroupCost tiles more than it has, what its beginning and end take.
+constexpr int kGroupCost = 2;
 
 struct Pages {
   int rp0, nraw;  // first raw page, raw pages
@@ -169,13 +175,14 @@ __device__ __forceinline__ int cta_quota(int ntiles, int grid, int min_tiles) {
 
 // Index of the group that holds tile t (all lanes of a warp call it): a search
 // that narrows 32-fold a step, since each step is one dependent load.
-__device__ __forceinline__ int find_group(const Group *groups, int n, int t) {
+// With `cost`, the line has so many places more in front of each later group.
+__device__ __forceinline__ int find_group(const Group *groups, int n, int t, int cost = 0) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = n;  // groups[lo].tile0 <= t, hi is past the answer
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
     const int i = lo + lane * step;
-    const bool le = i < hi && groups[i].tile0 <= t;
+    const bool le = i < hi && groups[i].tile0 + cost * i <= t;
     const uint32_t b = __ballot_sync(0xffffffffu, le);
     const int k = 31 - __clz(b);  // lane 0 always holds
     hi = min(hi, lo + (k + 1) * step);

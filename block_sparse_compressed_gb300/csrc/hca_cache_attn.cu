@@ -31,7 +31,9 @@ constexpr int kSchedThreads = 1024;
 
 __global__ void __launch_bounds__(kSchedThreads) hca_cache_sched_kernel(const AttnParams p) {
   __shared__ long long tmp[33];
+  __shared__ int longest;
   const int tid = threadIdx.x;
+  if (tid == 0) longest = 0;
   tc::pdl_launch_dependents();  // the attention kernel waits for this one's end by itself
   bool ok = true;
   long long chunks = 0;
@@ -59,6 +61,7 @@ __global__ void __launch_bounds__(kSchedThreads) hca_cache_sched_kernel(const At
         if (p.gbase[mid] <= c) lo = mid; else hi = mid;
       }
       ok = chunk_group(p, lo, (int)c - p.gbase[lo], g) && ok;
+      atomicMax(&longest, g.ntiles);
     }
     long long all;
     const long long before = block_scan(g.ntiles, tmp, all);
@@ -75,6 +78,7 @@ __global__ void __launch_bounds__(kSchedThreads) hca_cache_sched_kernel(const At
   if (tid == 0) {
     p.hdr->ngroups = (int)(chunks * p.slices);
     p.hdr->ntiles = ok ? (int)(line * p.slices) : -1;
+    p.hdr->longest = longest;
   }
 }
 

@@ -125,7 +125,7 @@ struct Shared {
   float2 ml[kWG];                                // copies: reference and sum of every lane
   int2 sums[2][kThreads / 32];                   // tiles and groups of each warp
   uint32_t tmem_base;
-  int abort, first;
+  int abort, first, range[2];
 };
 
 __device__ __forceinline__ float lg2_approx(float x) {
@@ -297,16 +297,35 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
     ntiles = p.hdr->ntiles;
     quota = cta_quota(ntiles, p.grid, p.min_tiles);
     busy = ntiles > 0 && blockIdx.x <= (ntiles - 1) / quota;
-    if (busy) {
+    const int ng = p.hdr->ngroups;
+    // cut between groups where that leaves the CTAs about as even: 2 groups and more
+    // each, none of them more than half of a CTA's share
+    const long long line = ntiles + (long long)kGroupCost * ng;
+    const int share = (int)min((line + p.grid - 1) / p.grid, 0x7fffffffll);
+    if (ng >= 2 * p.grid && line < kMaxTiles && p.hdr->longest + kGroupCost <= share / 2 && ntiles > 0) {
+      if (warp < 2) {
+        // the first group that begins at or behind the share's beginning (end)
+        const long long at = (long long)share * (blockIdx.x + warp);
+        const int g = at == 0 ? 0 : at > line ? ng : find_group(p.groups, ng, (int)at - 1, kGroupCost) + 1;
+        if (lane == 0) sh.range[warp] = g < ng ? p.groups[g].tile0 : ntiles;
+        if (warp == 0 && lane == 0) sh.first = g;
+      }
+      if (tid == 0) p.border[blockIdx.x] = Border{0, 0, 0, 0};
+      __syncthreads();
+      c0 = sh.range[0];
+      c1 = sh.range[1];
+      busy = c0 < c1;
+    } else if (busy) {
       c0 = quota * blockIdx.x;
       c1 = min(c0 + quota, ntiles);
-      const int ng = p.hdr->ngroups;
       if (warp < 2) {
         const int g = find_group(p.groups, ng, warp ? c1 - 1 : c0);
         if (warp == 0 && lane == 0) sh.first = g;
         if (warp == 1 && lane == 0) p.border[blockIdx.x] = border_of(p, p.groups[g], c0, c1, quota, blockIdx.x);
       }
       __syncthreads();
+    }
+    if (busy) {
       const int gi = sh.first + tid;
       if (tid < kMaxSegs && gi < ng) {
         const Group g = p.groups[gi];

@@ -836,3 +836,20 @@ def test_two_graphs_share_a_workspace():
         graphs[k][0].replay()
         assert torch.equal(outs[k][0], wants[k][0]) and torch.equal(outs[k][1], wants[k][1])
     assert hca.hca_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("H,D,held,added", [(64, 64, [3, 0, 900], [700, 1, 640]), (200, 64, [50, 0], [333, 12]), (128, 128, [0], [620])])
+def test_prompts_of_more_groups_than_blocks(H, D, held, added):
+    # two groups and more for each block: the line is cut between them
+    q, start, h, raw, c = attn_case(held, added, H, D, 70, 4, 32, BF16, 9)
+    got = hca.hca_cache_attn(q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), 70, 4, scale_of(D), check=True)
+    check_attn(got, q, start, h, raw, c, 70, 4, scale_of(D), BF16)
+
+
+def test_prompts_beside_a_long_request():
+    # one group with far more tiles than a block's share: it has to be divided
+    H, D = 128, 64
+    held, added = [0, 30000], [640, 1]
+    q, start, h, raw, c = attn_case(held, added, H, D, 70, 1, 64, BF16, 9)
+    got = hca.hca_cache_attn(q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), 70, 1, scale_of(D), check=True)
+    check_attn(got, q, start, h, raw, c, 70, 1, scale_of(D), BF16)
