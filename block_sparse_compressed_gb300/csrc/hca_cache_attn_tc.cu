@@ -298,11 +298,11 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
     quota = cta_quota(ntiles, p.grid, p.min_tiles);
     busy = ntiles > 0 && blockIdx.x <= (ntiles - 1) / quota;
     const int ng = p.hdr->ngroups;
-    // cut between groups where that leaves the CTAs about as even: 2 groups and more
-    // each, none of them more than half of a CTA's share
+    // cut between groups: 2 and more for each CTA, short ones, and none of them more
+    // than half of a CTA's share
     const long long line = ntiles + (long long)kGroupCost * ng;
     const int share = (int)min((line + p.grid - 1) / p.grid, 0x7fffffffll);
-    if (ng >= 2 * p.grid && line < kMaxTiles && p.hdr->longest + kGroupCost <= share / 2 && ntiles > 0) {
+    if (ng >= 2 * p.grid && line < kMaxTiles && p.hdr->longest <= min(kShortGroup, share / 2 - kGroupCost) && ntiles > 0) {
       if (warp < 2) {
         // the first group that begins at or behind the share's beginning (end)
         const long long at = (long long)share * (blockIdx.x + warp);
