@@ -70,27 +70,49 @@ __device__ __forceinline__ int find_request(const int32_t *before, int lo, int h
   return lo;
 }
 
+// Up to kPlanThreads requests' sums and items in shared memory, where a slot's
+// request is searched and looked up.
+struct PlanNear {
+  int32_t start[kPlanThreads + 1], taken[kPlanThreads + 1];
+  int32_t e0[kPlanThreads], last[kPlanThreads], n0[kPlanThreads];  // first and last new entry, blocks held before
+  __device__ __forceinline__ void put(int r, const PlanItem &t) {
+    e0[r] = t.e0;
+    last[r] = t.e0 + (int)t.entries - 1;
+    n0[r] = t.n0;
+  }
+};
+
 // Part `part` of `parts` of the slots and of the new table entries, by the
 // threads of this block.  start, taken [R + 1]: entries and blocks in front of
-// each request; avail: free blocks before the plan.
-__device__ __forceinline__ void plan_fill(const CachePlanArgs &a, const int32_t *start, const int32_t *taken, int avail,
-                                          int part, int parts) {
+// each request (near's, if it is given); avail: free blocks before the plan.
+__device__ __forceinline__ void plan_fill(const CachePlanArgs &a, const int32_t *start, const int32_t *taken,
+                                          const PlanNear *near, int avail, int part, int parts) {
   const int total = start[a.R], blocks = taken[a.R];
   const int per = (a.nslots + parts - 1) / parts, i0 = part * per, i1 = min(i0 + per, a.nslots);
   if (i0 < i1) {
     // the requests of this part
     const int r0 = i0 < total ? find_request(start, 0, a.R, i0) : 0;
     const int r1 = i0 < total ? find_request(start, r0, a.R, min(i1, total) - 1) + 1 : 0;
+#pragma unroll 4
     for (int i = i0 + threadIdx.x; i < i1; i += blockDim.x) {
       int slot = -1;
       if (i < total) {
         const int r = find_request(start, r0, r1, i);
-        const PlanItem t = plan_item(a, r);
-        const int e = t.e0 + i - start[r], last = t.e0 + (int)t.entries - 1;
-        const int page = e >> a.log_bs;
+        int e0, last, n0;
+        if (near) {
+          e0 = near->e0[r];
+          last = near->last[r];
+          n0 = near->n0[r];
+        } else {
+          const PlanItem t = plan_item(a, r);
+          e0 = t.e0;
+          last = t.e0 + (int)t.entries - 1;
+          n0 = t.n0;
+        }
+        const int e = e0 + i - start[r], page = e >> a.log_bs;
         if ((last >> a.log_bs) - page < a.cols) {  // else a later new entry takes the row
           const int col = page < a.cols ? page : page % a.cols;
-          const int id = col < t.n0 ? a.table[(size_t)r * a.cols + col] : a.free_blocks[avail - 1 - taken[r] - (col - t.n0)];
+          const int id = col < n0 ? a.table[(size_t)r * a.cols + col] : a.free_blocks[avail - 1 - taken[r] - (col - n0)];
           if (id >= 0 && id < a.nblocks) slot = (id << a.log_bs) + (e & (a.bs - 1));
           else atomicExch(a.status, HCA_ERR_CACHE);
         }
@@ -100,14 +122,14 @@ __device__ __forceinline__ void plan_fill(const CachePlanArgs &a, const int32_t 
   }
   const int bper = (blocks + parts - 1) / parts, k1 = min((part + 1) * bper, blocks);
   for (int k = part * bper + threadIdx.x; k < k1; k += blockDim.x) {
-    const int r = find_request(taken, 0, a.R, k);
-    a.table[(size_t)r * a.cols + plan_item(a, r).n0 + k - taken[r]] = a.free_blocks[avail - 1 - k];
+    const int r = find_request(taken, 0, a.R, k), n0 = near ? near->n0[r] : plan_item(a, r).n0;
+    a.table[(size_t)r * a.cols + n0 + k - taken[r]] = a.free_blocks[avail - 1 - k];
   }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) hca_cache_plan_kernel(const CachePlanArgs a) {
   __shared__ long long tmp[33];
-  __shared__ int32_t near[2][kPlanThreads + 1];  // start and taken of up to 1024 requests
+  __shared__ PlanNear near;
   const int tid = threadIdx.x;
   tc::pdl_launch_dependents();  // the fill kernel waits for this one's end by itself
   const int avail = *a.free_in;
@@ -131,14 +153,15 @@ __global__ void __launch_bounds__(kPlanThreads) hca_cache_plan_kernel(const Cach
     *a.status = go ? HCA_OK : valid ? HCA_ERR_CAPACITY : HCA_ERR_CACHE;
     *a.free_out = go ? avail - (int)all_blocks : avail;
     *a.avail = avail;
-    a.start[a.R] = near[0][few ? a.R : 0] = go ? (int)all_entries : 0;
-    a.taken[a.R] = near[1][few ? a.R : 0] = go ? (int)all_blocks : 0;
+    a.start[a.R] = near.start[few ? a.R : 0] = go ? (int)all_entries : 0;
+    a.taken[a.R] = near.taken[few ? a.R : 0] = go ? (int)all_blocks : 0;
   }
   if (few) {
     // one request a thread: its sums are at hand
     if (tid < a.R) {
-      a.start[tid] = near[0][tid] = go ? (int)s : 0;
-      a.taken[tid] = near[1][tid] = go ? (int)k : 0;
+      a.start[tid] = near.start[tid] = go ? (int)s : 0;
+      a.taken[tid] = near.taken[tid] = go ? (int)k : 0;
+      near.put(tid, t);
     }
   } else {
     long long at = 0, took = 0;
@@ -158,14 +181,27 @@ __global__ void __launch_bounds__(kPlanThreads) hca_cache_plan_kernel(const Cach
     }
   }
   __syncthreads();
-  if (a.nslots <= kPlanOneCta) plan_fill(a, few ? near[0] : a.start, few ? near[1] : a.taken, avail, 0, 1);
+  if (a.nslots <= kPlanOneCta) plan_fill(a, few ? near.start : a.start, few ? near.taken : a.taken, few ? &near : nullptr, avail, 0, 1);
 }
 
 constexpr int kFillThreads = 256, kSlotsPerCta = 1024;
 
 __global__ void __launch_bounds__(kFillThreads) hca_cache_fill_kernel(const CachePlanArgs a) {
+  __shared__ PlanNear near;
+  const bool few = a.R <= kPlanThreads;
+  if (few)
+    for (int r = threadIdx.x; r < a.R; r += kFillThreads) near.put(r, plan_item(a, r));
   tc::pdl_wait();
-  plan_fill(a, a.start, a.taken, *a.avail, blockIdx.x, gridDim.x);
+  const int avail = *a.avail;
+  if (few) {
+#pragma unroll 4
+    for (int r = threadIdx.x; r <= a.R; r += kFillThreads) {
+      near.start[r] = a.start[r];
+      near.taken[r] = a.taken[r];
+    }
+    __syncthreads();
+  }
+  plan_fill(a, few ? near.start : a.start, few ? near.taken : a.taken, few ? &near : nullptr, avail, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------------------
