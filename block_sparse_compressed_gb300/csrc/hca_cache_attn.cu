@@ -403,7 +403,10 @@ __global__ void __launch_bounds__(kCombineThreads, 4) hca_cache_combine_kernel(c
   tc::pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l8 = lane & 7;
   const Border g = p.border[blockIdx.x];
-  if (settle_status<T>(p) || g.columns <= (int)blockIdx.y * 4 * kCombineWarps) return;
+  if (g.columns <= (int)blockIdx.y * 4 * kCombineWarps) {
+    settle_status<T>(p);
+    return;
+  }
   const int c = (blockIdx.y * kCombineWarps + warp) * 4 + (lane >> 3);
   const bool mine = c < g.columns;
   const int n = g.parts, v4 = p.D / 4;
@@ -443,7 +446,8 @@ __global__ void __launch_bounds__(kCombineThreads, 4) hca_cache_combine_kernel(c
   }
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  if (!mine) return;
+  // the statuses' latency passes behind the parts'
+  if (settle_status<T>(p) || !mine) return;
   const float inv = 1.f / L;
   const size_t row = (size_t)g.row + c;
 #pragma unroll
