@@ -646,6 +646,7 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
   if (sms <= 0) return cudaErrorNoDevice;
   const bool tcs = on_tensor_cores(a.dtype);
   p.grid = std::min((tcs ? tc_cache_ctas() : 4) * sms, l.ctas);
+  // a CTA of one tile costs a part to join (94 tokens of 37 requests: 20.8 us, 18.6 with 2, 20.7 with 4)
   p.min_tiles = tcs ? 2 : 1;
   const int threads = tcs ? tc_cache_threads() : kSimtThreads;
   p.in_cta = l.slices == 1 && a.R <= threads && l.gmax <= (size_t)threads;

@@ -853,3 +853,66 @@ def test_prompts_beside_a_long_request():
     q, start, h, raw, c = attn_case(held, added, H, D, 70, 1, 64, BF16, 9)
     got = hca.hca_cache_attn(q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), 70, 1, scale_of(D), check=True)
     check_attn(got, q, start, h, raw, c, 70, 1, scale_of(D), BF16)
+
+
+@pytest.mark.parametrize("fill", [0x00, 0x7F, 0xFF])
+def test_what_a_workspace_holds_does_not_matter(fill):
+    lib = hca.load()
+    for dtype, H, D, held, added in ((BF16, 64, 128, [3000, 5, 700], [1, 1, 1]), (BF16, 64, 64, [3, 0, 900], [700, 1, 640]),
+                                     (BF16, 200, 64, [20, 400], [3, 1]), (F32, 4, 64, [500, 20], [1, 2]),
+                                     (F32, 4, 64, [k % 70 for k in range(200)], [1] * 200)):
+        q, start, h, raw, c = attn_case(held, added, H, D, 70, 4, 32, dtype, 9)
+        args = (q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), 70, 4, scale_of(D))
+        want = hca.hca_cache_attn(*args, check=True)
+        n = lib.hca_cache_attn_workspace_size(q.shape[0], len(held), H, D, 0 if dtype == BF16 else 1)
+        ws = torch.full((n,), fill, dtype=torch.uint8, device=DEV)
+        got = hca.hca_cache_attn(*args, ws=ws, check=True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for N in (40, 2000):
+        x = torch.randn(N, 64, generator=torch.Generator().manual_seed(3)).to(BF16).to(DEV)
+        slots = torch.randperm(-(-N // 16), generator=torch.Generator().manual_seed(4))
+        slots = (slots[:, None] * 16 + torch.arange(16)).flatten()[:N].int().to(DEV)
+        pools = []
+        for ws in (None, torch.full((lib.hca_cache_append_workspace_size(200),), fill, dtype=torch.uint8, device=DEV)):
+            pool, scale = torch.zeros(200, 16, 64, device=DEV).to(E4M3), torch.ones(200, device=DEV)
+            hca.hca_cache_append(x, slots, pool, scale, ws=ws, check=True)
+            pools.append((pool.view(torch.uint8), scale))
+        assert torch.equal(pools[0][0], pools[1][0]) and torch.equal(pools[0][1], pools[1][1])
+    for add in (3, 9000):
+        plans = []
+        for ws in (None, torch.full((lib.hca_cache_plan_workspace_size(2),), fill, dtype=torch.uint8, device=DEV)):
+            table = torch.full((2, 700), -1, dtype=torch.int32, device=DEV)
+            got = hca.hca_cache_plan(i32([0, 0]), i32([add, add]), table, i32(list(range(1400))), i32([1400]), 1400, 16, 2 * add + 5,
+                                     ws=ws, check=True)
+            plans.append([*got, table])
+        for a, b in zip(*plans):
+            assert torch.equal(a, b)
+
+
+def test_threads_that_call_at_once():
+    # host threads on streams of their own: the calls share nothing but the library
+    import threading
+    cases = []
+    for seed, (H, D, dtype) in enumerate(((64, 128, BF16), (16, 64, BF16), (4, 64, F32))):
+        q, start, h, raw, c = attn_case([900, 3, 77], [1, 2, 1], H, D, 64, 4, 16, dtype, seed)
+        args = (q.to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), 64, 4, scale_of(D))
+        cases.append((args, hca.hca_cache_attn(*args, check=True)))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(args, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    out, lse = hca.hca_cache_attn(*args, check=True)
+                    if not (torch.equal(out, want[0]) and torch.equal(lse, want[1])):
+                        bad.append("differs")
+        except Exception as e:  # noqa: BLE001
+            bad.append(repr(e))
+
+    ts = [threading.Thread(target=work, args=c) for c in cases for _ in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join(60)
+    assert not bad, bad[:3]
