@@ -8,7 +8,7 @@
 // requests (entries, blocks) say everything: one CTA computes them, and every
 // slot and every new table entry follows from a search in them and the free list
 // alone, so they are written in any order, by that CTA for a decode step or by
-// one CTA for 1,024 of them for prompts (1,060,000 slots: 12.5 us on the GPU, 191
+// one CTA for 1,024 of them for prompts (1,060,000 slots: 10.5 us on the GPU, 191
 // with one CTA).  A few hundred integers in, one integer out for each entry:
 // bound by the latency of a launch and a few dependent loads (6.4 us for 64
 // requests' next tokens; the bytes are 0.6 us for the prompts).
