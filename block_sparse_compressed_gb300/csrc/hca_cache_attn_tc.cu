@@ -83,7 +83,7 @@ template <int NQ, int D>
 struct Cfg {
   static constexpr int kCopies = 128 / NQ;                 // of a row in the lanes
   // Registers: 2 CTAs of 384 threads leave 80 each; a softmax thread holds kSpan scores.
-  static constexpr int kRegsSoft = kCopies == 1 ? 128 : 112, kRegsConv = 64, kRegsIssue = kCopies == 1 ? 48 : 64;
+  static constexpr int kRegsSoft = 128, kRegsConv = 56, kRegsIssue = 56;
   static_assert(kRegsSoft + kRegsConv + kRegsIssue <= 3 * 80, "register split must fit the launch");
   static constexpr int kSpan = 64 / kCopies;               // keys of a half that a thread takes: 64, 32, 16
   static constexpr int kHalves = D / 64;                   // 128-byte column blocks of an fp16 row
@@ -543,7 +543,6 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       // columns 0 .. 63 of the one and 64 .. 127 of the other, so that what they
       // load and what they store falls into different banks.
       constexpr int kRowStep = kWG * 16 / D, kPer = 64 / kRowStep;  // of a half
-      constexpr int kBatch = 2;     // pieces under way at a time
       const int ct = tid - kWG;
       const int ch = D == 128 ? (ct & 3) | (((ct >> 2) ^ (ct >> 3)) & 1) << 2 : ct & 3;
       const int row0 = D == 128 ? ((ct >> 2) & 1) | ((ct >> 3) & ~1) : ct >> 2;
@@ -628,46 +627,44 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           const int ms = (n >> 1) % kMetaStages, st = n % kHalfStages, h = n & 1;
           (void)wait_bar(&sh.raw_full[st], (n / kHalfStages) & 1);
           const uint32_t valid = sh.valid[ms];
-          const bool look = !((sh.all_seen[ms] >> h) & 1);
+          const bool look = !((sh.all_seen[ms] >> h) & 1), full = valid == (1u << ppt) - 1u;
           const uint32_t from = from0 + (st >> 1) * C::kRawStride + h * 64 * D, to = to0 + (st >> 1) * C::kStageBytes + h * 8192;
-#pragma unroll 1
-          for (int i0 = 0; i0 < kPer; i0 += kBatch) {
-            uint32_t raw[kBatch][4];
+          uint32_t raw[kPer][4];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const int row = h * 64 + row0 + (i0 + i) * kRowStep;
-              ld_shared(from + (i0 + i) * kRowStep * D, raw[i]);
+          for (int i = 0; i < kPer; ++i) ld_shared(from + i * kRowStep * D, raw[i]);
+          if (!full) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+              const int row = h * 64 + row0 + i * kRowStep;
               if (!((valid >> (row >> p.log_bs)) & 1)) raw[i][0] = raw[i][1] = raw[i][2] = raw[i][3] = 0;
             }
-            if (look) {
-#pragma unroll 1
-              for (int i = 0; i < kBatch; ++i) {
-                const uint4 v = i ? make_uint4(raw[1][0], raw[1][1], raw[1][2], raw[1][3]) : make_uint4(raw[0][0], raw[0][1], raw[0][2], raw[0][3]);
-                const uint32_t nan = __ballot_sync(0xffffffffu, nan_bytes(v) != 0);
-                if (nan) {
-                  // NaN in a row that not every row of the group sees
-                  const int row = h * 64 + row0 + (i0 + i) * kRowStep;
-                  if ((nan & row_lanes) && sh.meta[ms][row >> p.log_bs].kind != kAllSeen) {
-                    if (i) raw[1][0] = raw[1][1] = raw[1][2] = raw[1][3] = 0;
-                    else raw[0][0] = raw[0][1] = raw[0][2] = raw[0][3] = 0;
-                    if (ch == 0) {
-                      atomicOr(&sh.nan_keys[ms][row >> 5], 1u << (row & 31));
-                      sh.nan_any[ms] = 1;
-                    }
+          }
+          if (look) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+              const uint32_t nan = __ballot_sync(0xffffffffu, nan_bytes(make_uint4(raw[i][0], raw[i][1], raw[i][2], raw[i][3])) != 0);
+              if (nan & row_lanes) {
+                // NaN in a row that not every row of the group sees
+                const int row = h * 64 + row0 + i * kRowStep;
+                if (sh.meta[ms][row >> p.log_bs].kind != kAllSeen) {
+                  raw[i][0] = raw[i][1] = raw[i][2] = raw[i][3] = 0;
+                  if (ch == 0) {
+                    atomicOr(&sh.nan_keys[ms][row >> 5], 1u << (row & 31));
+                    sh.nan_any[ms] = 1;
                   }
                 }
               }
             }
-            __syncwarp();  // rows of 128 bytes are overwritten; all their pieces are a warp's
+          }
+          __syncwarp();  // rows of 128 bytes are overwritten; all their pieces are a warp's
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              uint32_t f[8];
+          for (int i = 0; i < kPer; ++i) {
+            uint32_t f[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) e4m3x4_to_f16(raw[i][e], f[2 * e], f[2 * e + 1]);
-              const uint32_t at = to + (i0 + i) * kRowStep * 128;
-              st_shared(at + swz0, f[0], f[1], f[2], f[3]);
-              st_shared(at + (swz0 ^ 16), f[4], f[5], f[6], f[7]);
-            }
+            for (int e = 0; e < 4; ++e) e4m3x4_to_f16(raw[i][e], f[2 * e], f[2 * e + 1]);
+            const uint32_t at = to + i * kRowStep * 128;
+            st_shared(at + swz0, f[0], f[1], f[2], f[3]);
+            st_shared(at + (swz0 ^ 16), f[4], f[5], f[6], f[7]);
           }
           fence_async_smem();
           mbar_arrive(&sh.kv_full[st]);
@@ -770,12 +767,13 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             // 16 columns at a time have one block scale
             constexpr int kGroups = kSpan / 16;
             float ck[kGroups], lb[kGroups], mx = -INFINITY;
-            int pgi[kGroups];
+            float iv[kGroups];
 #pragma unroll
             for (int c4 = 0; c4 < kGroups; ++c4) {
-              pgi[c4] = (k0 + c4 * 16) >> p.log_bs;
-              ck[c4] = fmaxf(meta[pgi[c4]].scale * cs, FLT_MIN);  // positive: a masked score stays -inf
-              lb[c4] = meta[pgi[c4]].log2_scale;
+              const float4 pm = *reinterpret_cast<const float4 *>(&meta[(k0 + c4 * 16) >> p.log_bs].scale);
+              ck[c4] = fmaxf(pm.x * cs, FLT_MIN);  // positive: a masked score stays -inf
+              lb[c4] = pm.y;
+              iv[c4] = pm.z;
               float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
               for (int y = 0; y < 16; y += 4) {
@@ -831,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
               }
               float a, b;
               f32x2_split(fadd2(acc[0], acc[1]), a, b);
-              l_run = fmaf(a + b, meta[pgi[c4]].inv_scale, l_run);
+              l_run = fmaf(a + b, iv[c4], l_run);
               if (kSpan > 16 && (c4 & 1)) tmem_st16(pcol + copy * (kSpan / 2) + (c4 - 1) * 8, *reinterpret_cast<uint32_t(*)[16]>(&pk[(c4 - 1) * 8]));
             }
             if constexpr (kSpan == 16) tmem_st8(pcol + copy * 8, pk);
