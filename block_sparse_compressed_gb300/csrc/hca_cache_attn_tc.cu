@@ -30,7 +30,9 @@
 // 2^-25 of the row's reference where tiny).
 //
 // The reference exponent of a row is its largest score so far, raised only when
-// beaten by 2^8 (fp16 has room for 2^15), so O is rarely rescaled.
+// beaten by 2^15, for which fp16 has room (below 2^16), so O is rarely rescaled: a
+// row of a warp that needs it costs all 32 a trip through O (prompts: 76.0 us
+// when raised at 2^8, 74.1 at 2^15).
 //
 // A row of the cache that some query row does not see may hold anything, and
 // 0 * NaN is not 0: of the pages that not every row sees whole, the converter
@@ -68,7 +70,7 @@ using namespace cache;
 
 namespace {
 
-constexpr float kRaiseLog2 = 8.f;
+constexpr float kRaiseLog2 = 15.f;
 constexpr int kMetaStages = 4;  // tiles whose pages are looked up ahead
 constexpr int kStages = 2;      // fp16 tiles; filled and released by halves
 constexpr int kHalfStages = 2 * kStages;
@@ -698,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         const int pos = g.pos0 + (row < nreal ? row / p.HS : 0);
         // what the row sees: raw keys [raw_lo, pos], entries [0, entries)
         const int raw_lo = pos - p.W + 1, entries = (pos + 1) / p.m;
-        float m_run = -INFINITY, l_run = 0.f;
+        float m_run = -INFINITY, m_use = 0.f, l_run = 0.f;  // m_use: what is subtracted
         (void)wait_bar(&sh.q_full, k & 1);
         const float cs = sh.q_factor[row];
         mbar_arrive(&sh.q_read);
@@ -782,31 +784,30 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
               }
               mx = fmaxf(mx, fmaf(fmaxf(m0, m1), ck[c4], lb[c4]));
             }
-            // raise the reference; the sums made with the old one follow
-            float f = 1.f;
-            bool raise = mx > m_run + kRaiseLog2 || (m_run == -INFINITY && mx > -INFINITY);
-            if (raise) {
-              if (m_run > -INFINITY) {
-                f = ex2_approx(m_run - mx);
-                l_run *= f;
-              } else {
-                raise = false;  // O holds nothing of this row yet
-              }
-              m_run = mx;
-            }
-            const float m_use = m_run == -INFINITY ? 0.f : m_run;
+            // raise the reference (seldom); the sums made with the old one follow
+            const bool raise = mx > m_run + kRaiseLog2;  // at first: any key that is seen
             if (__any_sync(0xffffffffu, raise)) {
-              // O holds the sum up to the keys before these once that is done
-              (void)wait_bar(&sh.pv_done[h ^ 1], (h ? n : n - 1) & 1);
-              tc_fence_after();
+              const bool had = raise && m_run > -INFINITY;  // else O holds nothing of this row yet
+              const float f = had ? ex2_approx(m_run - mx) : 1.f;
+              l_run *= f;
+              if (raise) m_run = mx;
+              m_use = m_run == -INFINITY ? 0.f : m_run;
+              if (__any_sync(0xffffffffu, had)) {
+                // O holds the sum up to the keys before these once that is done
+                (void)wait_bar(&sh.pv_done[h ^ 1], (h ? n : n - 1) & 1);
+                tc_fence_after();
+                constexpr int kPart = kSpan == 64 ? 16 : 32;  // columns that fit the registers beside the scores
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                tmem_ld16(lane_addr + kColO + c, o);
-                tmem_wait_ld();
+                for (int c = 0; c < D; c += kPart) {
+                  uint32_t o[kPart];
+                  if constexpr (kPart == 16) tmem_ld16(lane_addr + kColO + c, o);
+                  else tmem_ld32(lane_addr + kColO + c, o);
+                  tmem_wait_ld();
 #pragma unroll
-                for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                tmem_st16(lane_addr + kColO + c, o);
+                  for (int y = 0; y < kPart; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                  if constexpr (kPart == 16) tmem_st16(lane_addr + kColO + c, o);
+                  else tmem_st32(lane_addr + kColO + c, o);
+                }
               }
             }
             // P over the first columns of the half's S, with zeros for the other
