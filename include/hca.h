@@ -340,13 +340,15 @@ HCA_API int hca_cache_append(const void *x, const int32_t *slots, void *pool, fl
  * sliding attention; full causal attention with W beyond the length).  Rows of
  * out and lse from start[R] on are left as they are.  Cache rows that no token
  * sees may hold anything.
- * bf16: D = 64 or 128 (HCA_ERR_UNSUPPORTED otherwise); fp32: D a multiple of 16
- * up to 256.  Lengths out of range, a raw table too narrow for a token's window
- * or a compressed table too narrow for the entries, or 2^31 - 2^16 tiles of 128
- * keys and more in all (groups of up to 128 rows of q have their own), make all
- * N rows of out and lse NaN; a block id out of range, or a scale that is not
- * positive and finite, makes the tokens that see the block NaN; both are
- * HCA_ERR_CACHE.  A given input gives the same bits every time.  Workspace:
+ * bf16: D = 64 or 128 (HCA_ERR_UNSUPPORTED otherwise), scores scale <q, k> below
+ * 2^24 in magnitude (their differences are lost beyond it, and from 2^27 on a
+ * result may be NaN); fp32: D a multiple of 16 up to 256.
+ * Lengths out of range, a raw table too narrow for a token's window, a
+ * compressed table too narrow for the entries, or 2^31 - 2^16 tiles of 128 keys
+ * and more in all (each group of up to 128 rows of q has its own) make all N rows
+ * of out and lse NaN; a block id out of range, or a scale that is not positive
+ * and finite, makes the tokens that see the block NaN; both are HCA_ERR_CACHE.
+ * A given input gives the same bits every time.  Workspace:
  * hca_cache_attn_workspace_size bytes (0: unsupported sizes). */
 HCA_API size_t hca_cache_attn_workspace_size(int N, int R, int H, int D, int dtype);
 HCA_API int hca_cache_attn(const void *q, const int32_t *start, const int32_t *held, const void *raw_pool,

@@ -916,3 +916,16 @@ def test_threads_that_call_at_once():
     for t in ts:
         t.join(60)
     assert not bad, bad[:3]
+
+
+def test_scores_of_great_magnitude():
+    # up to 2^24 the order of the scores decides, and nothing overflows on the way
+    H, D = 64, 128
+    q, start, h, raw, c = attn_case([500, 40], [1, 2], H, D, 64, 4, 16, BF16, 12)
+    for big in (2.0 ** 4, 2.0 ** 10, 2.0 ** 16):
+        out, lse = hca.hca_cache_attn((q.float() * big).to(BF16).to(DEV), start.to(DEV), h.to(DEV), dev(raw), dev(c), 64, 4,
+                                      scale_of(D), check=True)
+        assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+        assert float(lse.abs().max()) < 2.0 ** 24
+        # every output is a mean of cache rows, none of which is beyond 448 times the largest scale
+        assert float(out.float().abs().max()) <= 448 * float(max(raw[1].max(), c[1].max()))
