@@ -45,10 +45,11 @@
 // softmax's first look is 805 and 590, and a half's softmax 1,100.  Two CTAs of an
 // SM fill part of each other's gaps: 64 tokens over 95,000 rows each (199 MB of
 // cache, 64 heads, D = 128) take 91.5 us, 2.2 TB/s and 552 TFLOP/s, with the
-// tensor cores busy half of the time (82 us with the products all but left out).  One decode step of 64 requests at 128 keys an
-// entry takes 22.4 us, of which 2.6 are the schedule, 3 the way to the first
-// scores and 2 the way out; chunks of 2,571 prompt tokens 74 us, half of it
-// beginnings and ends of their groups of 2 tokens.
+// tensor cores busy half of the time (82 us with the products all but left out).
+// One decode step of 64 requests at 128 keys an entry takes 22.4 us, of which 2.6
+// are the schedule, 3 the way to the first scores and 2 the way out; chunks of
+// 2,571 prompt tokens 74 us, half of it beginnings and ends of their groups of 2
+// tokens.
 // Measured and left, each against the kernel of its time: scores of a whole tile
 // at once (128 x 128 x 16 at 64 cycles: the tensor cores do less, but the softmax
 // waits: 109 us for 102); two softmax warpgroups, a half each (99 us for 96: the
