@@ -2,8 +2,9 @@
 //
 // A decode step's kernels take 6 to 25 us; checking a dozen tensors, allocating
 // three and passing thirty arguments takes Python 18 to 22 us a call.  Here the
-// same takes a few.  A function takes hca.py's arguments and answers
-//   a tuple   the call was made: the results and the workspace
+// same takes 2, and 2 more for each tensor that is made; a workspace that nobody
+// asks for is not made a tensor.  A function takes hca.py's arguments and answers
+//   a tuple   the call was made: the results and the workspace (None: its own)
 //   an int    the C function's status, not HCA_OK
 //   None      something is not as in an ordinary call (a tensor that does not
 //             fit, a subclass, another device than the current one, no memory):
@@ -12,6 +13,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -76,12 +78,28 @@ struct Call {
     }
     return at::empty(at::IntArrayRef(shape), at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, dev)));
   }
-  // a workspace is any bytes: what there is of them is for the C function to check
-  at::Tensor workspace(PyObject *o, size_t bytes) const {
-    if (o == Py_None) return at::empty({(int64_t)bytes}, at::TensorOptions().dtype(kU8).device(at::Device(at::kCUDA, dev)));
-    const at::Tensor &t = tensor(o);
-    need(t.is_cuda() && t.get_device() == dev && t.scalar_type() == kU8 && t.is_contiguous());
-    return t;
+};
+
+// The caller's workspace (any bytes: what there is of them is for the C function
+// to check), a tensor if its status will be looked at, or plain memory that goes
+// back to the allocator behind the launch, in the order of the stream.
+struct Workspace {
+  at::Tensor tensor_;
+  c10::DataPtr own;
+  void *ptr;
+  size_t bytes;
+
+  Workspace(const Call &c, PyObject *o, bool keep, size_t need_bytes) : bytes(need_bytes) {
+    if (o != Py_None) {
+      tensor_ = tensor(o);
+      need(tensor_.is_cuda() && tensor_.get_device() == c.dev && tensor_.scalar_type() == kU8 && tensor_.is_contiguous());
+      bytes = tensor_.numel();
+    } else if (keep) {
+      tensor_ = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(kU8).device(at::Device(at::kCUDA, c.dev)));
+    } else {
+      own = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
+    }
+    ptr = tensor_.defined() ? tensor_.data_ptr() : own.get();
   }
 };
 
@@ -96,7 +114,7 @@ PyObject *results(const T &...t) {
   Py_ssize_t i = 0;
   bool ok = r != nullptr;
   ([&](const at::Tensor &x) {
-    PyObject *o = ok ? THPVariable_Wrap(x) : nullptr;
+    PyObject *o = ok ? THPVariable_Wrap(x) : nullptr;  // None for an undefined one
     if (o) PyTuple_SET_ITEM(r, i++, o);
     else ok = false;
   }(t), ...);
@@ -114,10 +132,10 @@ PyObject *guarded(F f) {
   }
 }
 
-// held, added, table, free_blocks, free_count, nblocks, bs, nslots, m, start, slots, free_left, ws
+// held, added, table, free_blocks, free_count, nblocks, bs, nslots, m, start, slots, free_left, ws, check
 PyObject *cache_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
-    need(n == 13);
+    need(n == 14);
     const at::Tensor &held = tensor(a[0]), &table = tensor(a[2]), &free_blocks = tensor(a[3]);
     need(held.dim() == 1 && table.dim() == 2 && free_blocks.dim() == 1);
     const int64_t R = table.size(0), cols = table.size(1), nfree = free_blocks.size(0);
@@ -127,19 +145,19 @@ PyObject *cache_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *h = c.fits(held, kI32, {R}), *ad = c.fits(a[1], kI32, {R}), *t = c.fits(table, kI32, {R, cols});
     void *fb = c.fits(free_blocks, kI32, {nfree}), *fc = c.fits(a[4], kI32, {1});
     const at::Tensor start = c.result(a[9], kI32, {R + 1}), slots = c.result(a[10], kI32, {nslots}), left = c.result(a[11], kI32, {1});
-    const at::Tensor ws = c.workspace(a[12], lib.plan_ws((int)R));
+    const Workspace ws(c, a[12], a[13] != Py_False, lib.plan_ws((int)R));
     const int rc = lib.plan(static_cast<int32_t *>(h), static_cast<int32_t *>(ad), static_cast<int32_t *>(t), static_cast<int32_t *>(fb),
                             static_cast<int32_t *>(fc), static_cast<int32_t *>(left.data_ptr()), static_cast<int32_t *>(start.data_ptr()),
                             static_cast<int32_t *>(slots.data_ptr()), (int)R, (int)cols, bs, m, nblocks, (int)nfree, nslots,
-                            ws.data_ptr(), ws.numel(), c.stream());
-    return rc ? PyLong_FromLong(rc) : results(start, slots, left, ws);
+                            ws.ptr, ws.bytes, c.stream());
+    return rc ? PyLong_FromLong(rc) : results(start, slots, left, ws.tensor_);
   });
 }
 
-// x, slots, pool, scale, ws
+// x, slots, pool, scale, ws, check
 PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
-    need(n == 5);
+    need(n == 6);
     const at::Tensor &x = tensor(a[0]), &pool = tensor(a[2]);
     need(x.dim() == 2 && pool.dim() == 3);
     const int64_t N = x.size(0), D = x.size(1), nblocks = pool.size(0), bs = pool.size(1);
@@ -148,10 +166,10 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Call c(x);
     void *px = c.fits(x, x.scalar_type(), {N, D}), *ps = c.fits(a[1], kI32, {N});
     void *pp = c.fits(pool, kE4m3, {nblocks, bs, D}), *pc = c.fits(a[3], kF32, {nblocks});
-    const at::Tensor ws = c.workspace(a[4], lib.append_ws((int)nblocks));
+    const Workspace ws(c, a[4], a[5] != Py_False, lib.append_ws((int)nblocks));
     const int rc = lib.append(px, static_cast<int32_t *>(ps), pp, static_cast<float *>(pc), (int)N, (int)D, (int)bs, (int)nblocks, dt,
-                              ws.data_ptr(), ws.numel(), c.stream());
-    return rc ? PyLong_FromLong(rc) : results(ws);
+                              ws.ptr, ws.bytes, c.stream());
+    return rc ? PyLong_FromLong(rc) : results(ws.tensor_);
   });
 }
 
@@ -176,10 +194,10 @@ Cache cache_of(const Call &c, PyObject *o, int64_t R, int64_t bs, int64_t D) {
   return r;
 }
 
-// q, start, held, raw, comp, W, m, scale, out, lse, ws
+// q, start, held, raw, comp, W, m, scale, out, lse, ws, check
 PyObject *cache_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
-    need(n == 11);
+    need(n == 12);
     const at::Tensor &q = tensor(a[0]), &held = tensor(a[2]);
     need(q.dim() == 3 && held.dim() == 1 && PyTuple_CheckExact(a[3]) && PyTuple_GET_SIZE(a[3]) == 3);
     const at::Tensor &raw_pool = tensor(PyTuple_GET_ITEM(a[3], 0));
@@ -195,13 +213,13 @@ PyObject *cache_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const size_t bytes = lib.attn_ws((int)N, (int)R, (int)H, (int)D, dt);
     need(bytes > 0);
     const at::Tensor out = c.result(a[8], q.scalar_type(), {N, H, D}), lse = c.result(a[9], kF32, {N, H});
-    const at::Tensor ws = c.workspace(a[10], bytes);
+    const Workspace ws(c, a[10], a[11] != Py_False, bytes);
     const int rc = lib.attn(pq, static_cast<int32_t *>(ps), static_cast<int32_t *>(ph), raw.pool, static_cast<float *>(raw.scale),
                             static_cast<int32_t *>(raw.table), raw.nblocks, raw.cols, comp.pool, static_cast<float *>(comp.scale),
                             static_cast<int32_t *>(comp.table), comp.nblocks, comp.cols, out.data_ptr(),
                             static_cast<float *>(lse.data_ptr()), (int)N, (int)R, (int)H, (int)D, W, m, (int)bs, scale, dt,
-                            ws.data_ptr(), ws.numel(), c.stream());
-    return rc ? PyLong_FromLong(rc) : results(out, lse, ws);
+                            ws.ptr, ws.bytes, c.stream());
+    return rc ? PyLong_FromLong(rc) : results(out, lse, ws.tensor_);
   });
 }
 

@@ -604,7 +604,7 @@ def hca_cache_plan(held: torch.Tensor, added: torch.Tensor, table: torch.Tensor,
     slots[nslots], free_left[1]); free_left may be free_count itself."""
     lib = _lib or load()
     r = _py and _py.cache_plan(held, added, table, free_blocks, free_count, nblocks, bs, nslots, m, start, slots,
-                               free_left, ws)
+                               free_left, ws, check)
     if r is not None:
         return _made(r, "hca_cache_plan", check)[:3]
     dev = held.device
@@ -634,7 +634,7 @@ def hca_cache_append(x: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor, s
     cache pool[nblocks,bs,D] (float8_e4m3fn) with scale[nblocks] (fp32), both
     updated in place (include/hca.h, hca_cache_append)."""
     lib = _lib or load()
-    r = _py and _py.cache_append(x, slots, pool, scale, ws)
+    r = _py and _py.cache_append(x, slots, pool, scale, ws, check)
     if r is not None:
         _made(r, "hca_cache_append", check)
         return
@@ -674,7 +674,7 @@ def hca_cache_attn(q: torch.Tensor, start: torch.Tensor, held: torch.Tensor, raw
     (pool, scale, table[R,cols]); comp may be None.  Returns (out[N,H,D],
     lse[N,H] fp32)."""
     lib = _lib or load()
-    r = _py and _py.cache_attn(q, start, held, raw, comp, W, m, scale, out, lse, ws)
+    r = _py and _py.cache_attn(q, start, held, raw, comp, W, m, scale, out, lse, ws, check)
     if r is not None:
         return _made(r, "hca_cache_attn", check)[:2]
     dev = q.device

@@ -127,15 +127,15 @@ def test_the_short_way_declines_what_is_not_ordinary():
         pytest.skip("built without the headers of Python or torch")
     i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     pool, scale, x = torch.zeros(4, 16, 64).to(torch.float8_e4m3fn), torch.ones(4), torch.zeros(3, 64)
-    for a in ((x, i32(3), pool, scale, None), (None, i32(3), pool, scale, None), (x, 3, pool, scale, None), (x,),
-              (x[0], i32(3), pool, scale, None), (x, i32(3), pool[0], scale, None), (x.half(), i32(3), pool, scale, None)):
+    for a in ((x, i32(3), pool, scale, None, False), (None, i32(3), pool, scale, None, False), (x, 3, pool, scale, None, False), (x,),
+              (x[0], i32(3), pool, scale, None, False), (x, i32(3), pool[0], scale, None, False), (x.half(), i32(3), pool, scale, None, False)):
         assert hca._py.cache_append(*a) is None
-    assert hca._py.cache_plan(i32(3), i32(3), i32(3, 2), i32(5), i32(1), 8, 16, 4, 1, None, None, None, None) is None
-    assert hca._py.cache_plan(i32(3), i32(3), i32(3, 2), i32(5), i32(1), 8.0, 16, 4, 1, None, None, None, None) is None
+    assert hca._py.cache_plan(i32(3), i32(3), i32(3, 2), i32(5), i32(1), 8, 16, 4, 1, None, None, None, None, False) is None
+    assert hca._py.cache_plan(i32(3), i32(3), i32(3, 2), i32(5), i32(1), 8.0, 16, 4, 1, None, None, None, None, False) is None
     c = (pool, scale, i32(2, 3))
     for raw, comp in ((c, None), (c, c), (list(c), None), (c[:2], None), (None, c)):
-        assert hca._py.cache_attn(torch.zeros(2, 4, 64), i32(3), i32(2), raw, comp, 8, 4, 0.1, None, None, None) is None
-    assert hca._py.cache_attn(torch.zeros(2, 4, 64), i32(3), i32(2), c, None, 1 << 40, 4, 0.1, None, None, None) is None
+        assert hca._py.cache_attn(torch.zeros(2, 4, 64), i32(3), i32(2), raw, comp, 8, 4, 0.1, None, None, None, False) is None
+    assert hca._py.cache_attn(torch.zeros(2, 4, 64), i32(3), i32(2), c, None, 1 << 40, 4, 0.1, None, None, None, False) is None
 
 
 def test_the_binding_refuses_other_devices_and_workspaces():
