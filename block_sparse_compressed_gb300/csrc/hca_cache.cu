@@ -18,9 +18,9 @@
 // when s is divided out and bringing a block's earlier rows to a larger scale
 // rounds only what falls below the smallest normal e4m3.  Rows of one run are
 // contiguous in x and in the pool, so a run is one flat conversion of n * D
-// values after one maximum over them.  64,258 rows of 128 bf16 values take 12.3
-// us, 2.0 TB/s: one wave of CTAs that each wait for slots, values and owners in
-// turn, behind a kernel of the owners; 64 single rows take 6.1 us, latency.
+// values after one maximum over them.  64,258 rows of 128 bf16 values take 10.3
+// us, 2.4 TB/s: one wave of CTAs that each wait for slots, values and owners in
+// turn, behind a kernel of the owners; 64 single rows take 5 us, latency.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -231,26 +231,40 @@ __global__ void hca_cache_claim_kernel(const CacheAppendArgs a) {
   if (t < a.N && begins_run(a, t)) a.owner[a.slots[t] >> a.log_bs] = t;
 }
 
+// 16 values as they lie in memory
 template <typename T>
-__device__ __forceinline__ void load16(const T *p, float (&v)[16]) {
-  if constexpr (sizeof(T) == 4) {
+struct Held {
+  uint4 w[sizeof(T)];
+};
+
+template <typename T>
+__device__ __forceinline__ void hold16(const T *p, Held<T> &h) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 f = reinterpret_cast<const float4 *>(p)[i];
-      v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
-    }
-  } else {
+  for (int i = 0; i < (int)sizeof(T); ++i) h.w[i] = reinterpret_cast<const uint4 *>(p)[i];
+}
+
+template <typename T>
+__device__ __forceinline__ void expand16(const Held<T> &h, float (&v)[16]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 u = reinterpret_cast<const uint4 *>(p)[i];
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  for (int i = 0; i < (int)sizeof(T); ++i) {
+    const uint32_t w[4] = {h.w[i].x, h.w[i].y, h.w[i].z, h.w[i].w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (sizeof(T) == 4) {
+        v[4 * i + k] = __uint_as_float(w[k]);
+      } else {
         v[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
         v[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
       }
     }
   }
+}
+
+template <typename T>
+__device__ __forceinline__ void load16(const T *p, float (&v)[16]) {
+  Held<T> h;
+  hold16(p, h);
+  expand16(h, v);
 }
 
 __device__ __forceinline__ uint4 pack16(const float (&v)[16]) {
@@ -363,12 +377,13 @@ __device__ __forceinline__ int append_run(const CacheAppendArgs &a, int t, int l
 
 // A CTA takes the runs that begin in `rows` consecutive rows: long ones all
 // threads together, so that a block's rows are in flight at once, short ones a
-// warp each.
+// warp each.  Values wait for their block's scale as they came: as fp32 they took
+// 96 registers, 5 CTAs an SM and 12.3 us where it is 8 and 10.3 now.
 constexpr int kChunkThreads = 128, kChunkRows = 64, kLongRun = 8;
 constexpr int kWindow = kChunkRows + 128;  // rows looked at: the last run may go on for a block
 
 template <typename T>
-__global__ void __launch_bounds__(kChunkThreads) hca_cache_append_kernel(const CacheAppendArgs a, int rows) {
+__global__ void __launch_bounds__(kChunkThreads, sizeof(T) == 2 ? 8 : 5) hca_cache_append_kernel(const CacheAppendArgs a, int rows) {
   __shared__ int slot_of[kWindow + 1];       // slots of rows t0 - 1, t0, ...
   __shared__ uint32_t breaks[kWindow / 32];  // rows that are not behind the one in front
   __shared__ int lead[kChunkRows], nlead;
@@ -406,17 +421,20 @@ __global__ void __launch_bounds__(kChunkThreads) hca_cache_append_kernel(const C
     uint8_t *dst = a.pool + (size_t)slot * a.D;
     const int units = n * a.D / 16;
     constexpr int kHold = 4;  // units of 16 values that a thread keeps
-    float v[kHold][16];
-    float amax = 0.f;
+    Held<T> held[kHold];
+    float v[16], amax = 0.f;
     for (int u0 = 0; u0 < units; u0 += kHold * kChunkThreads) {
 #pragma unroll
       for (int k = 0; k < kHold; ++k) {
         const int u = u0 + k * kChunkThreads + tid;
-        if (u < units) load16(x + (size_t)u * 16, v[k]);
+        if (u < units) hold16(x + (size_t)u * 16, held[k]);
       }
 #pragma unroll
       for (int k = 0; k < kHold; ++k)
-        if (u0 + k * kChunkThreads + tid < units) amax = fmaxf(amax, finite_max(v[k]));
+        if (u0 + k * kChunkThreads + tid < units) {
+          expand16(held[k], v);
+          amax = fmaxf(amax, finite_max(v));
+        }
     }
     tc::pdl_wait();  // for the owners
     if (a.owner[blk] != t) {
@@ -438,8 +456,9 @@ __global__ void __launch_bounds__(kChunkThreads) hca_cache_append_kernel(const C
       for (int k = 0; k < kHold; ++k) {
         const int u = u0 + k * kChunkThreads + tid;
         if (u < units) {
-          if (units > kHold * kChunkThreads) load16(x + (size_t)u * 16, v[k]);  // else it is still there
-          *reinterpret_cast<uint4 *>(dst + (size_t)u * 16) = quantise16(v[k], inv);
+          if (units > kHold * kChunkThreads) hold16(x + (size_t)u * 16, held[k]);  // else it is still there
+          expand16(held[k], v);
+          *reinterpret_cast<uint4 *>(dst + (size_t)u * 16) = quantise16(v, inv);
         }
       }
     }
