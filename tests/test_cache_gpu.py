@@ -929,3 +929,41 @@ def test_scores_of_great_magnitude():
         assert float(lse.abs().max()) < 2.0 ** 24
         # every output is a mean of cache rows, none of which is beyond 448 times the largest scale
         assert float(out.float().abs().max()) <= 448 * float(max(raw[1].max(), c[1].max()))
+
+
+def test_a_captured_prompt_step():
+    # the kernels of long prompts, each set up while the one in front of it runs, in a graph
+    R, H, D, W, m, bs, added = 2, 8, 64, 40, 8, 16, [2500, 2101]
+    g = torch.Generator().manual_seed(6)
+    n, e = sum(added), sum(a // m for a in added)
+    xs, es = torch.randn(2, n, D, generator=g).to(BF16).to(DEV), torch.randn(2, e, D, generator=g).to(BF16).to(DEV)
+    qs, add = torch.randn(2, n, H, D, generator=g).to(BF16).to(DEV), i32(added)
+
+    def fresh():
+        return Server(R, H, D, W, m, bs, BF16, max(added), max(added) + 1)
+
+    def state(sv):
+        return [sv.pool.view(torch.uint8), sv.scale, sv.raw_table, sv.comp_table, sv.count, sv.held]
+
+    eager = []
+    for k in range(2):
+        sv = fresh()
+        eager.append([t.clone() for t in (*sv.step(xs[k], es[k], qs[k], add), *state(sv))])
+    sv = fresh()
+    start = [t.clone() for t in state(sv)]
+    x, ent, q = xs[0].clone(), es[0].clone(), qs[0].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        sv.step(x, ent, q, add)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = sv.step(x, ent, q, add)
+    for k in (0, 1, 1, 0):
+        for t, s in zip(state(sv), start):
+            t.copy_(s)
+        x.copy_(xs[k]); ent.copy_(es[k]); q.copy_(qs[k])
+        graph.replay()
+        for a, b in zip((out, lse, *state(sv)), eager[k]):
+            assert torch.equal(a, b), k
