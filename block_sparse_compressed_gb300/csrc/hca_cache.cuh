@@ -59,10 +59,10 @@ __device__ __forceinline__ uint32_t nan_bytes(const uint4 &v) {
 
 // Exponent k of the smallest power of two with amax <= 448 * 2^k (448 = 1.75
 // * 2^8, the largest e4m3 value); amax is finite and not negative.
-__device__ __forceinline__ int scale_exponent(float amax) {
+__device__ __forceinline__ int scale_exponent(float amax, int least = kMinScaleExp) {
   const uint32_t u = __float_as_uint(amax);
   const int k = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return max(k, kMinScaleExp);
+  return max(k, least);
 }
 __device__ __forceinline__ float exp2_int(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
 

@@ -15,6 +15,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "hca_cache_attn.cuh"
 #include "tc_tiles.cuh"
@@ -366,6 +367,7 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
         else p.part_o[((size_t)seg.slot * kCols + c) * p.D + d] = o[x2][c];
       }
     }
+    if (seg.slot >= 0 && tid == 0) p.part_unit[seg.slot] = 0;
     if (tid < nreal) {
       if (seg.slot < 0) p.lse[row0 + tid] = (sh.m[tid] + log2f(sh.l[tid])) * 0.69314718055994531f;
       else p.part_ml[(size_t)seg.slot * kCols + tid] = make_float2(sh.m[tid], sh.l[tid]);
@@ -374,11 +376,14 @@ __global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const Attn
 }
 
 // ---------------------------------------------------------------------------
-// combine: out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i over a group's parts,
-// and the call's status from its CTAs'
+// combine: out = sum 2^(m_i - M + u_i) O_i / sum 2^(m_i - M) l_i over a group's
+// parts, whose O_i have units of 2^u_i, and the call's status from its CTAs'
 // ---------------------------------------------------------------------------
 constexpr int kCombineWarps = 8, kCombineThreads = 32 * kCombineWarps;
 constexpr int kMaxBorders = 640;
+
+// 2^(unit - largest), what a part's O counts beside one of the largest unit
+__device__ __forceinline__ float unit_weight(int unit, int largest) { return exp2_int(max(unit - largest, -126)); }
 
 // The call's status from its CTAs' ones, written by the grid's first block; true
 // if a wait gave up: the outputs become NaN.
@@ -410,11 +415,20 @@ __global__ void __launch_bounds__(kCombineThreads, 4) hca_cache_combine_kernel(c
   const int c = (blockIdx.y * kCombineWarps + warp) * 4 + (lane >> 3);
   const bool mine = c < g.columns;
   const int n = g.parts, v4 = p.D / 4;
-  auto slot = [&](int i) { return (size_t)(i == 0 ? g.slot : 2 * ((int)blockIdx.x + i)) * p.NQ + c; };
+  auto part = [&](int i) { return i == 0 ? g.slot : 2 * ((int)blockIdx.x + i); };
+  auto slot = [&](int i) { return (size_t)part(i) * p.NQ + c; };
   float M = -INFINITY, L = 0.f;
-  for (int i = l8; mine && i < n; i += 8) M = fmaxf(M, p.part_ml[slot(i)].x);
+  int U = INT_MIN;
+  for (int i = l8; mine && i < n; i += 8) {
+    const float2 ml = p.part_ml[slot(i)];
+    M = fmaxf(M, ml.x);
+    if (ml.y != 0.f) U = max(U, p.part_unit[part(i)]);  // 0: a part in which the column saw no key
+  }
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  for (int o = 4; o > 0; o >>= 1) {
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    U = max(U, __shfl_xor_sync(0xffffffffu, U, o));
+  }
   float4 acc[kX];
 #pragma unroll
   for (int x = 0; x < kX; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -422,9 +436,10 @@ __global__ void __launch_bounds__(kCombineThreads, 4) hca_cache_combine_kernel(c
     float w = 0.f;
     if (mine && b + l8 < n) {
       const float2 ml = p.part_ml[slot(b + l8)];
-      if (ml.y != 0.f) {  // 0: a part in which the column saw no key
+      if (ml.y != 0.f) {
         w = exp2f(ml.x - M);
         L += w * ml.y;
+        w *= unit_weight(p.part_unit[part(b + l8)], U);
       }
     }
     const int k1 = min(8, n - b);
@@ -448,7 +463,7 @@ __global__ void __launch_bounds__(kCombineThreads, 4) hca_cache_combine_kernel(c
   for (int o = 4; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   // the statuses' latency passes behind the parts'
   if (settle_status<T>(p) || !mine) return;
-  const float inv = 1.f / L;
+  const float inv = exp2_int(U) / L;
   const size_t row = (size_t)g.row + c;
 #pragma unroll
   for (int x = 0; x < kX; ++x)
@@ -493,9 +508,15 @@ __global__ void __launch_bounds__(kCombineThreads) hca_cache_combine_few_kernel(
     const int n = c < g.columns ? g.parts : 0;
     auto slot = [&](int i) { return (size_t)(i == 0 ? g.slot : 2 * (lo + i)); };
     float M = -INFINITY, L = 0.f;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_ml[slot(i) * p.NQ + c].x);
+    int U = INT_MIN;
+    for (int i = lane; i < n; i += 32) {
+      const float2 ml = p.part_ml[slot(i) * p.NQ + c];
+      M = fmaxf(M, ml.x);
+      if (ml.y != 0.f) U = max(U, p.part_unit[slot(i)]);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    U = __reduce_max_sync(0xffffffffu, U);
     float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     for (int b = 0; b < n; b += 32) {
       float w = 0.f;
@@ -504,6 +525,7 @@ __global__ void __launch_bounds__(kCombineThreads) hca_cache_combine_few_kernel(
         if (ml.y != 0.f) {
           w = exp2f(ml.x - M);
           L += w * ml.y;
+          w *= unit_weight(p.part_unit[slot(b + lane)], U);
         }
       }
       const int k1 = min(32, n - b);
@@ -535,7 +557,7 @@ __global__ void __launch_bounds__(kCombineThreads) hca_cache_combine_few_kernel(
       }
     }
     if (n > 0 && sub == 0) {
-      const float inv = 1.f / L;
+      const float inv = exp2_int(U) / L;
       const size_t row = (size_t)g.row + c;
 #pragma unroll
       for (int x = 0; x < 2; ++x)
@@ -585,7 +607,7 @@ int pick_columns(int N, int R, int H, int dtype) {
 struct Layout {
   int NQ, HS, slices, P;
   size_t gmax;
-  size_t off_gbase, off_groups, off_err, off_border, off_ml, off_o, bytes;
+  size_t off_gbase, off_groups, off_err, off_border, off_unit, off_ml, off_o, bytes;
   int ctas;  // at most
 };
 
@@ -609,6 +631,8 @@ Layout layout_of(int N, int R, int H, int D, int dtype) {
   at += align_up(l.ctas * sizeof(int32_t));
   l.off_border = at;
   at += align_up(l.ctas * sizeof(Border));
+  l.off_unit = at;
+  at += align_up(slots * sizeof(int32_t));
   l.off_ml = at;
   at += align_up(slots * l.NQ * sizeof(float2));
   l.off_o = at;
@@ -639,6 +663,7 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
   p.border = reinterpret_cast<Border *>(ws + l.off_border);
   p.part_ml = reinterpret_cast<float2 *>(ws + l.off_ml);
   p.part_o = reinterpret_cast<float *>(ws + l.off_o);
+  p.part_unit = reinterpret_cast<int32_t *>(ws + l.off_unit);
   p.N = a.N; p.R = a.R; p.H = a.H; p.D = a.D; p.W = a.W; p.m = a.m; p.log_bs = log2_int(a.bs);
   p.HS = l.HS; p.slices = l.slices; p.P = l.P; p.NQ = l.NQ;
   p.scale = a.scale; p.wait_ns = std::min<uint64_t>(a.wait_ns, 4000000000u); p.stall = a.stall;

@@ -22,7 +22,8 @@ struct AttnParams {
   int32_t *err;        // [grid] status of each CTA
   Border *border;      // [grid]
   float2 *part_ml;     // [2 * grid][NQ] reference exponent and sum of a partial result
-  float *part_o;       // [2 * grid][NQ][D]
+  float *part_o;       // [2 * grid][NQ][D], in units of 2^part_unit
+  int32_t *part_unit;  // [2 * grid]
   int N, R, H, D, W, m, log_bs;
   int HS, slices, P;   // heads per slice, slices, positions per group
   int NQ;              // columns of a group, P * HS <= NQ

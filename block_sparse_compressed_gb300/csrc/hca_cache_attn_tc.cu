@@ -19,15 +19,27 @@
 // (quarter) of a half's keys: P is zero for the others.  The copies are so many
 // independent streams of the online softmax, joined when the group ends.
 //
-// The cache's e4m3 values become fp16, exactly, once for both products and all
-// rows.  A page is contiguous, so one bulk copy brings it to shared memory, into
-// the half of its fp16 rows' bytes that the converter warps overwrite last; they
-// also make q ready (below) while the softmax warps end the group before.  A
-// key's block scale s multiplies its score, and its probability before that is
-// rounded to fp16.  q becomes fp16 with a power of two for each row that puts its
-// largest value at 224 .. 448: bf16's 8 bits fit, what falls below 2^-14 loses
-// bits (2^-33 of the row's largest value); p * s is rounded to fp16 (11 bits;
-// 2^-25 of the row's reference where tiny).
+// The cache's e4m3 values become fp16 once for both products and all rows.  A page
+// is contiguous, so one bulk copy brings it to shared memory, into the half of its
+// fp16 rows' bytes that the converter warps overwrite last; they also make q ready
+// (below) while the softmax warps end the group before.  q becomes fp16 with a
+// power of two for each row that puts its largest value at 224 .. 448: bf16's 8
+// bits fit, what falls below 2^-14 loses bits (2^-33 of the row's largest value).
+//
+// Block scales go into the keys: a page of scale s is stored as k8 * 2^e in units
+// of 2^u, with s = 2^(u + e) and u the same for all of a segment's tiles, which
+// fp16 holds exactly for e in -15 .. 7.  So scores need one factor for all keys,
+// and the probabilities, rounded to fp16 (11 bits; 2^-25 of the row's reference
+// where tiny), and their sum do not depend on scales.  (p * s rounded to fp16
+// loses every key but those of the blocks with the largest scales, whatever their
+// values are, and a sum of (p * s) / s leaves fp32's range with s.)  u is the
+// largest scale of the segment's first tile; a page more than 2^7 beyond it raises
+// u, and O follows.  What is left of a scale below 2^-15 of the unit, or of one that
+// is no power of two, multiplies its scores and probabilities in tensor memory, in
+// functions of their own that ordinary tiles only pass by.  The factors take the
+// converter 3 of 94 us at m = 4; a factor for every 16 keys in the softmax
+// instead 2 there and 3.5 of 75 for prompts; both loops, of which a tile without
+// factors takes the shorter, 2.5 more for prompts.
 //
 // The reference exponent of a row is its largest score so far, raised only when
 // beaten by 2^15, for which fp16 has room (below 2^16), so O is rarely rescaled: a
@@ -72,6 +84,9 @@ using namespace cache;
 namespace {
 
 constexpr float kRaiseLog2 = 15.f;
+constexpr int kLeastExp = -15, kMostExp = 7;      // e: 2^-9 .. 448 times 2^e is an fp16 value
+constexpr int kLeastUnit = -100, kMostUnit = 127;  // u: 2^u / l is a normal number (l below 2^26)
+constexpr int kLeastQExp = -118;                  // exponent of q's factor: so is its reciprocal
 constexpr int kMetaStages = 4;  // tiles whose pages are looked up ahead
 constexpr int kStages = 2;      // fp16 tiles; filled and released by halves
 constexpr int kHalfStages = 2 * kStages;
@@ -104,8 +119,9 @@ enum PageKind { kRaw = 0, kComp = 1, kNoPage = 2, kAllSeen = 3 };  // kAllSeen: 
 struct __align__(16) PageMeta {
   const uint8_t *rows;  // NULL: no page, or a bad block id
   int key0, kind;
-  float scale, log2_scale, inv_scale;
-  int pad;
+  float rest;           // the page's scale is 2^(unit + e) * rest
+  uint32_t factor;      // 2^e, for both values of a pair of fp16
+  int pad[2];
 };
 
 template <int NQ, int D>
@@ -114,12 +130,15 @@ struct Shared {
   uint64_t meta_full[kMetaStages], meta_empty[kMetaStages];
   uint64_t raw_full[kHalfStages], kv_full[kHalfStages], kv_empty[kHalfStages];
   uint64_t q_full, q_read, s_full[2], p_full[2], pv_done[2], drain, never;
-  uint64_t scale_full[kMetaStages];
   PageMeta meta[kMetaStages][8];
   uint32_t nan_keys[kMetaStages][4];  // keys whose rows hold a NaN that not everybody sees
   int nan_any[kMetaStages];
   int all_seen[kMetaStages];          // bit h: every row sees every key of half h
   uint32_t valid[kMetaStages];        // bit i: there is a page i
+  int unit[kMetaStages];              // exponent of the tile's keys in fp16
+  // hardly ever not 0: (the unit of the tile in front less this one's) * 2 + (a
+  // page's rest is not 1)
+  int odd[kMetaStages];
   // the CTA's pieces of groups, in order; what there is no room for is in the
   // workspace's groups
   Segment seg[kMaxSegs];
@@ -131,10 +150,19 @@ struct Shared {
   int abort, first, range[2];
 };
 
-__device__ __forceinline__ float lg2_approx(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+// s = 2^exponent * part with part in (0.5, 1], for positive finite s.
+__device__ __forceinline__ int split_scale(float s, float &part) {
+  const int sub = s < FLT_MIN ? 24 : 0;  // a subnormal one
+  const uint32_t u = __float_as_uint(sub ? s * 16777216.f : s), mant = u & 0x7fffffu;
+  part = mant ? __uint_as_float(mant | (126u << 23)) : 1.f;
+  return (int)(u >> 23) - (mant ? 126 : 127) - sub;
+}
+// 2^e in both halves, e in [kLeastExp, kMostExp]
+__device__ __forceinline__ uint32_t f16x2_exp2(int e) { return (e >= -14 ? (uint32_t)(e + 15) << 10 : 0x400u >> (-14 - e)) * 0x10001u; }
+__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 __device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
   uint32_t r;
@@ -201,6 +229,56 @@ static __device__ __noinline__ int scan_tiles(int v, bool counts, int2 *sums, lo
   return before;
 }
 
+// Scores of kSpan keys from column k0 of a tile on, times their pages' rests.
+template <int kSpan>
+static __device__ __noinline__ void scale_s(uint32_t addr, const PageMeta *meta, int k0, int log_bs) {
+#pragma unroll 1
+  for (int c = 0; c < kSpan; c += 16) {
+    const float rest = meta[(k0 + c) >> log_bs].rest;
+    uint32_t v[16];
+    tmem_ld16(addr + c, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int y = 0; y < 16; ++y) v[y] = __float_as_uint(__uint_as_float(v[y]) * rest);
+    tmem_st16(addr + c, v);
+  }
+  tmem_wait_st();
+}
+
+// The same for their probabilities, pairs of fp16.
+template <int kSpan>
+static __device__ __noinline__ void scale_p(uint32_t addr, const PageMeta *meta, int k0, int log_bs) {
+#pragma unroll 1
+  for (int c = 0; c < kSpan; c += 16) {
+    const float rest = meta[(k0 + c) >> log_bs].rest;
+    uint32_t v[8];
+    tmem_ld8(addr + c / 2, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      const float2 e = __half22float2(*reinterpret_cast<const __half2 *>(&v[y]));
+      v[y] = f16x2_rn(e.x * rest, e.y * rest);
+    }
+    tmem_st8(addr + c / 2, v);
+  }
+  tmem_wait_st();
+}
+
+// A warp's rows of O times f.
+template <int D>
+static __device__ __noinline__ void scale_o(uint32_t addr, float f) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    uint32_t o[16];
+    tmem_ld16(addr + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+    tmem_st16(addr + c, o);
+  }
+  tmem_wait_st();
+}
+
 template <int NQ, int D>
 __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnParams p) {
   using C = Cfg<NQ, D>;
@@ -215,7 +293,6 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
 #pragma unroll 1
     for (int s = 0; s < kMetaStages; ++s) {
       mbar_init(&sh.meta_full[s], 1);
-      mbar_init(&sh.scale_full[s], 1);
       mbar_init(&sh.meta_empty[s], kWG);  // the softmax is the last to read a tile's pages
     }
 #pragma unroll 1
@@ -361,12 +438,15 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       bool ok = true;
 #pragma unroll 1
       for (int k = 0; ok; ++k) {
+        int unit = 0;
+        bool set = false;  // by the segment's first pages
         const Segment g = segment(k);
         const Pages pg = group_pages(g.pos0, g.npos, p.W, p.m, p.log_bs, p.comp.table != nullptr);
 #pragma unroll 1
         for (int jb = g.j0; ok && jb < g.j1; jb += batch) {
           const int v = jb * ppt + lane;
-          PageMeta pm = {nullptr, 0, kNoPage, 1.f, 0.f, 1.f, 0};
+          PageMeta pm = {nullptr, 0, kNoPage, 1.f, f16x2_exp2(0), {0, 0}};
+          float scale = 1.f;
           bool bad = false;  // block id out of range
           if (v < pg.nraw + pg.ncomp && v < g.j1 * ppt) {
             const bool comp = v >= pg.nraw;
@@ -379,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             pm.kind = all ? kAllSeen : comp ? kComp : kRaw;
             if (id >= 0 && id < cs.nblocks) {
               pm.rows = cs.pool + (size_t)id * page_bytes;
-              pm.scale = cs.scale[id];
+              scale = cs.scale[id];
             } else {
               bad = true;  // every key of it is noted as NaN
             }
@@ -409,24 +489,38 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
               sh.all_seen[ms] = ((a & half) == half ? 1 : 0) | ((b & half) == half ? 2 : 0);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.meta_full[ms]);
-            // the scales are needed later than the rows
+            const bool fine = !bad && scale > 0.f && scale < INFINITY;
+            float part = 1.f;
+            const int ex = here && pm.rows && fine ? split_scale(scale, part) : INT_MIN;
+            const int top = __reduce_max_sync(0xffffffffu, ex), was = unit;
+            if (top != INT_MIN && (!set || top > unit + kMostExp)) {
+              unit = min(max(top, kLeastUnit), kMostUnit);
+              set = true;
+            }
+            const int shift = jb + t == g.j0 ? 0 : max(was - unit, -126);
             if (here) {
-              if (bad || !(pm.scale > 0.f && pm.scale < INFINITY)) {
-                pm.scale = 1.f;
+              if (!fine) {
                 atomicExch(status, HCA_ERR_CACHE);
 #pragma unroll 1
                 for (int r = (lane % ppt) << p.log_bs, i = 0; i < 1 << p.log_bs; ++i, ++r)
                   atomicOr(&sh.nan_keys[ms][r >> 5], 1u << (r & 31));
                 sh.nan_any[ms] = 1;
               }
-              to.scale = pm.scale;
-              // powers of two, for which both are exact
-              to.log2_scale = lg2_approx(pm.scale);
-              to.inv_scale = ex2_approx(-to.log2_scale);
+              if (ex != INT_MIN) {
+                const int e = min(max(ex - unit, kLeastExp), kMostExp);
+                pm.factor = f16x2_exp2(e);
+                pm.rest = part * exp2_int(max(ex - unit - e, -120));
+              }
+              to.factor = pm.factor;
+              to.rest = pm.rest;
+            }
+            const bool rests = __any_sync(0xffffffffu, here && pm.rest != 1.f);
+            if (lane == 0) {
+              sh.unit[ms] = unit;
+              sh.odd[ms] = 2 * shift + (rests ? 1 : 0);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.scale_full[ms]);
+            if (lane == 0) mbar_arrive(&sh.meta_full[ms]);
           }
         }
         if (!g.last() && lane == 0) {
@@ -603,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
               amax = bf16x2_max(amax, bf16x2_max(bf16x2_max(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
                                                  bf16x2_max(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu)));
             }
-            const int ex = scale_exponent(__uint_as_float(max(amax & 0xffffu, amax >> 16) << 16));
+            const int ex = scale_exponent(__uint_as_float(max(amax & 0xffffu, amax >> 16) << 16), kLeastQExp);
             const float inv = p.scale < 0.f ? -exp2_int(-ex) : p.scale > 0.f ? exp2_int(-ex) : 0.f;
             if (copy == 0) sh.q_factor[q_row] = exp2_int(ex) * fabsf(p.scale) * 1.4426950408889634f;
             if constexpr (C::kCopies > 1) named_bar_sync(kBarQ, kWG);
@@ -665,6 +759,9 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             uint32_t f[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) e4m3x4_to_f16(raw[i][e], f[2 * e], f[2 * e + 1]);
+            const uint32_t factor = sh.meta[ms][(h * 64 + row0 + i * kRowStep) >> p.log_bs].factor;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = f16x2_mul(f[e], factor);
             const uint32_t at = to + i * kRowStep * 128;
             st_shared(at + swz0, f[0], f[1], f[2], f[3]);
             st_shared(at + (swz0 ^ 16), f[4], f[5], f[6], f[7]);
@@ -702,6 +799,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         // what the row sees: raw keys [raw_lo, pos], entries [0, entries)
         const int raw_lo = pos - p.W + 1, entries = (pos + 1) / p.m;
         float m_run = -INFINITY, m_use = 0.f, l_run = 0.f;  // m_use: what is subtracted
+        int unit = 0;                                       // exponent of O
         (void)wait_bar(&sh.q_full, k & 1);
         const float cs = sh.q_factor[row];
         mbar_arrive(&sh.q_read);
@@ -709,13 +807,22 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         for (int j = g.j0; j < g.j1; ++j, ++n) {
           const int ms = n % kMetaStages;
           const PageMeta *meta = sh.meta[ms];
-          (void)wait_bar(&sh.scale_full[ms], (n / kMetaStages) & 1);
-          const int all_seen = sh.all_seen[ms];
+          (void)wait_bar(&sh.meta_full[ms], (n / kMetaStages) & 1);
+          const int all_seen = sh.all_seen[ms], odd = sh.odd[ms];
+          // positive and finite: a masked score stays -inf, that of a row of zeros 0
+          const float ck = fminf(fmaxf(cs * exp2_int(sh.unit[ms]), FLT_MIN), FLT_MAX);
+          if (odd >> 1) {
+            // O in the tile's unit, once it holds the last tile's keys
+            (void)wait_bar(&sh.pv_done[1], (n - 1) & 1);
+            tc_fence_after();
+            scale_o<D>(lane_addr + kColO, exp2_int(odd >> 1));
+          }
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             (void)wait_bar(&sh.s_full[h], n & 1);
             tc_fence_after();
             const int k0 = h * 64 + copy * kSpan;  // first of the thread's keys, uniform in a warp
+            if (odd & 1) scale_s<kSpan>(lane_addr + k0, meta, k0, p.log_bs);
             uint32_t sv[kSpan];
             if constexpr (kSpan == 16) {
               tmem_ld16(lane_addr + k0, sv);
@@ -767,24 +874,13 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
                 }
               }
             }
-            // 16 columns at a time have one block scale
-            constexpr int kGroups = kSpan / 16;
-            float ck[kGroups], lb[kGroups], mx = -INFINITY;
-            float iv[kGroups];
+            float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-            for (int c4 = 0; c4 < kGroups; ++c4) {
-              const float4 pm = *reinterpret_cast<const float4 *>(&meta[(k0 + c4 * 16) >> p.log_bs].scale);
-              ck[c4] = fmaxf(pm.x * cs, FLT_MIN);  // positive: a masked score stays -inf
-              lb[c4] = pm.y;
-              iv[c4] = pm.z;
-              float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-              for (int y = 0; y < 16; y += 4) {
-                m0 = fmax3(m0, __uint_as_float(sv[c4 * 16 + y]), __uint_as_float(sv[c4 * 16 + y + 1]));
-                m1 = fmax3(m1, __uint_as_float(sv[c4 * 16 + y + 2]), __uint_as_float(sv[c4 * 16 + y + 3]));
-              }
-              mx = fmaxf(mx, fmaf(fmaxf(m0, m1), ck[c4], lb[c4]));
+            for (int y = 0; y < kSpan; y += 4) {
+              m0 = fmax3(m0, __uint_as_float(sv[y]), __uint_as_float(sv[y + 1]));
+              m1 = fmax3(m1, __uint_as_float(sv[y + 2]), __uint_as_float(sv[y + 3]));
             }
+            const float mx = fmaxf(m0, m1) * ck;
             // raise the reference (seldom); the sums made with the old one follow
             const bool raise = mx > m_run + kRaiseLog2;  // at first: any key that is seen
             if (__any_sync(0xffffffffu, raise)) {
@@ -815,12 +911,11 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             // copies' keys
             const uint32_t pcol = lane_addr + h * 64;
             uint32_t pk[kSpan / 2];
+            const uint64_t ck2 = f32x2(__float_as_uint(ck), __float_as_uint(ck));
+            const uint64_t nm2 = f32x2(__float_as_uint(-m_use), __float_as_uint(-m_use));
+            uint64_t acc[2] = {0, 0};
 #pragma unroll
-            for (int c4 = 0; c4 < kGroups; ++c4) {
-              const float nm = lb[c4] - m_use;
-              const uint64_t ck2 = f32x2(__float_as_uint(ck[c4]), __float_as_uint(ck[c4]));
-              const uint64_t nm2 = f32x2(__float_as_uint(nm), __float_as_uint(nm));
-              uint64_t acc[2] = {0, 0};
+            for (int c4 = 0; c4 < kSpan / 16; ++c4) {
 #pragma unroll
               for (int y = 0; y < 16; y += 2) {
                 float t0, t1;
@@ -829,9 +924,6 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
                 acc[(y >> 1) & 1] = fadd2(acc[(y >> 1) & 1], f32x2(__float_as_uint(e0), __float_as_uint(e1)));
                 pk[c4 * 8 + (y >> 1)] = f16x2_rn(e0, e1);
               }
-              float a, b;
-              f32x2_split(fadd2(acc[0], acc[1]), a, b);
-              l_run = fmaf(a + b, iv[c4], l_run);
               if (kSpan > 16 && (c4 & 1)) tmem_st16(pcol + copy * (kSpan / 2) + (c4 - 1) * 8, *reinterpret_cast<uint32_t(*)[16]>(&pk[(c4 - 1) * 8]));
             }
             if constexpr (kSpan == 16) tmem_st8(pcol + copy * 8, pk);
@@ -848,10 +940,15 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
 #pragma unroll
               for (int y = 1; y < 4; ++y) tmem_st8(pcol + ((copy + y) & 3) * 8, zero);
             }
+            float a, b;
+            f32x2_split(fadd2(acc[0], acc[1]), a, b);
+            l_run += a + b;
             tmem_wait_st();
+            if (odd & 1) scale_p<kSpan>(pcol + copy * (kSpan / 2), meta, k0, p.log_bs);
             tc_fence_before();
             mbar_arrive(&sh.p_full[h]);
           }
+          unit = sh.unit[ms];
           mbar_arrive(&sh.meta_empty[ms]);
         }
         if (*abort_flag) l_run = __int_as_float(0x7fc00000);
@@ -880,7 +977,8 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           if (whole) p.lse[orow + row] = (m_run + log2f(l_run)) * 0.69314718055994531f;
           else p.part_ml[(size_t)g.slot * NQ + row] = make_float2(m_run, l_run);
         }
-        const float inv = weight * (whole ? 1.f / l_run : 1.f);
+        if (!whole && tid == 0) p.part_unit[g.slot] = unit;
+        const float inv = weight * (whole ? exp2_int(unit) / l_run : 1.f);
         (void)wait_bar(&sh.pv_done[1], (n - 1) & 1);
         tc_fence_after();
         // O leaves through shared memory, 64 bytes of a row at a time, so that

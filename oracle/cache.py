@@ -138,3 +138,28 @@ def attend(q, start, held, raw, comp, W, m, scale):
             lse[t] = (top + np.log(tot))[:, 0]
             spread[t] = (np.abs(q[t]) @ np.abs(kv).T).max(1)
     return out, lse, mass, spread
+
+
+def terms(q, start, held, raw, comp, W, m, scale):
+    """For each query token of the requests, in order: (values [n,D] of the n keys
+    that it sees, probabilities [H,n], lse [H], spread [H,n]), spread being
+    sum_d |q_d k_d|."""
+    q = np.asarray(q, dtype=np.float64)
+    for r in range(len(held)):
+        for t in range(int(start[r]), int(start[r + 1])):
+            i = int(held[r]) + t - int(start[r])
+            kv = _rows_at_once(raw, r, np.arange(max(0, i - W + 1), i + 1))
+            if comp is not None and (i + 1) // m:
+                kv = np.concatenate([kv, _rows_at_once(comp, r, np.arange((i + 1) // m))])
+            s = scale * (q[t] @ kv.T)
+            top = s.max(1, keepdims=True)
+            p = np.exp(s - top)
+            tot = p.sum(1, keepdims=True)
+            yield kv, p / tot, (top + np.log(tot))[:, 0], np.abs(q[t]) @ np.abs(kv).T
+
+
+def _rows_at_once(cache, r, entries):
+    pool, scale, table = cache
+    bs, cols = pool.shape[1], table.shape[1]
+    blk = table[r, (entries // bs) % cols]
+    return pool[blk, entries % bs] * scale[blk][:, None]
