@@ -41,10 +41,14 @@
 // instead 2 there and 3.5 of 75 for prompts; both loops, of which a tile without
 // factors takes the shorter, 2.5 more for prompts.
 //
-// The reference exponent of a row is its largest score so far, raised only when
-// beaten by 2^15, for which fp16 has room (below 2^16), so O is rarely rescaled: a
-// row of a warp that needs it costs all 32 a trip through O (prompts: 76.0 us
-// when raised at 2^8, 74.1 at 2^15).
+// The reference exponent of a row is 2 below its largest score so far, so that fp16
+// reaches down to 2^-27 of the largest probability, and raised only when that score
+// is beaten by 2^11, so that O is rarely rescaled: a row of a warp that needs it
+// costs all 32 a trip through O.  (64 tokens at m = 4 and prompts of 2,571 tokens,
+// 6 and 7 instead: 95.9 and 76.5 us; 4 and 9: 95.2 and 75.8; 2 and 11: 94.3 and 75.4;
+// 0 and 13: 93.6 and 75.2.)  fp16 ends at 2^16: scores of 2^24 are 1.44 * 2^24 in
+// base 2, where fp32 has steps of 2, and the roundings of the score, the threshold
+// and the reference add at most 2 to those 13.
 //
 // A row of the cache that some query row does not see may hold anything, and
 // 0 * NaN is not 0: of the pages that not every row sees whole, the converter
@@ -83,7 +87,7 @@ using namespace cache;
 
 namespace {
 
-constexpr float kRaiseLog2 = 15.f;
+constexpr float kRaiseLog2 = 11.f, kBias = 2.f;
 constexpr int kLeastExp = -15, kMostExp = 7;      // e: 2^-9 .. 448 times 2^e is an fp16 value
 constexpr int kLeastUnit = -100, kMostUnit = 127;  // u: 2^u / l is a normal number (l below 2^26)
 constexpr int kLeastQExp = -118;                  // exponent of q's factor: so is its reciprocal
@@ -888,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
               const float f = had ? ex2_approx(m_run - mx) : 1.f;
               l_run *= f;
               if (raise) m_run = mx;
-              m_use = m_run == -INFINITY ? 0.f : m_run;
+              m_use = m_run == -INFINITY ? 0.f : m_run - kBias;
               if (__any_sync(0xffffffffu, had)) {
                 // O holds the sum up to the keys before these once that is done
                 (void)wait_bar(&sh.pv_done[h ^ 1], (h ? n : n - 1) & 1);
@@ -951,6 +955,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           unit = sh.unit[ms];
           mbar_arrive(&sh.meta_empty[ms]);
         }
+        m_run -= kBias;  // what the sums are relative to
         if (*abort_flag) l_run = __int_as_float(0x7fc00000);
         const bool whole = g.slot < 0;
         const size_t orow = (size_t)g.row0 * p.H + g.slice() * p.HS;  // rows of the group are rows of q and out in order

@@ -342,9 +342,9 @@ HCA_API int hca_cache_append(const void *x, const int32_t *slots, void *pool, fl
  * sees may hold anything.
  * Block scales may be any positive finite numbers, however far apart.
  * bf16: D = 64 or 128 (HCA_ERR_UNSUPPORTED otherwise).  out's probabilities are
- * rounded to 11 bits or 2^-25 of the row's largest, whichever is more (lse's sum
+ * rounded to 11 bits or 2^-27 of the row's largest, whichever is more (lse's sum
  * is not); a key in a block of scale below 2^-15 of a larger one S of its request
- * adds to out to within 2^-31 S, which is 2^-22 of the smallest e4m3 step there.
+ * adds to out to within 2^-33 S, which is 2^-24 of the smallest e4m3 step there.
  * Scores scale <q, k> are below 2^24 in magnitude (their differences are lost
  * beyond it, and from 2^27 on a result may be NaN).
  * fp32: D a multiple of 16 up to 256.

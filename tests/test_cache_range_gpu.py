@@ -176,3 +176,36 @@ def test_ordinary_caches_within_the_bounds_of_each_token(dtype, H, D, T, held, W
     q, start, h, raw, c = attn_case(held, [T] * len(held), H, D, W, m, 32, dtype, 21, ring=W < 1000)
     a = (q, start, h, raw, c, W, m, scale_of(D))
     check(run(*a), *a)
+
+
+@pytest.mark.parametrize("H,D", [(16, 64), (64, 128), (128, 64)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_up_to_the_stated_limit(H, D, sign):
+    # scores of 0.1 to 0.995 of 2^24 that differ by 13 to 19 in base 2, where fp32 has
+    # steps of 1 and 2: whatever the order that is left, every output is a mean of rows
+    n, bs = 2000, 16
+    raw = make_cache([n], -(-n // bs), bs, D, 3)
+    raw[0].view(torch.uint8)[:] = 0
+    v = torch.zeros(n, D)
+    v[:, 0] = 448.0
+    steps = torch.tensor([192.0, 208.0, 224.0, 240.0, 256.0])    # of 448, which is 32 in base 2
+    k = torch.arange(n)
+    v[:, 1] = torch.where(k < 300, 0.0, steps[(k // 7) % 5])
+    v[:, 2:] = torch.randn(n, D - 2, generator=torch.Generator().manual_seed(1)).abs() * 100
+    v.clamp_(max=448)
+    for r in range(n):
+        raw[0][int(raw[2][0, r // bs]), r % bs] = v[r].to(E4M3)
+    raw[1].fill_(2.0 ** -7)
+    q = torch.zeros(1, H, D)
+    q[0, :, 0] = sign * torch.linspace(0.1, 0.995, H) * 2.0 ** 24 / scale_of(D) / 3.5
+    q[0, :, 1] = 32 * np.log(2.0) / scale_of(D) / 3.5
+    q = q.to(BF16)
+    start, held = torch.tensor([0, 1], dtype=torch.int32), torch.tensor([n - 1], dtype=torch.int32)
+    out, lse = run(q, start, held, raw, None, 1 << 30, 4, scale_of(D))
+    assert bool(torch.isfinite(lse).all()) and bool(torch.isfinite(out).all())
+    # a column of equal values is their mean, up to the sum's and the result's roundings
+    assert float((out[..., 0].float() - 3.5).abs().max()) <= 3.5 * (2.0 ** -8 + 2.0 ** -10)
+    assert float(out[..., 2:].float().max()) <= 3.5 * (1 + 2.0 ** -8 + 2.0 ** -10) and float(out[..., 2:].float().min()) >= 0
+    top = q[0, :, 0].double() * 3.5 * scale_of(D)
+    # the reference, the score and what follows: a few roundings of fp32 at 2^24 in base 2
+    assert float((lse[0].double().cpu() - top).abs().max()) <= 32 + 16
