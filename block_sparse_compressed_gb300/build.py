@@ -51,8 +51,16 @@ def _stale(target, inputs) -> bool:
     return any(os.path.getmtime(p) > t for p in inputs)
 
 
-def _py_command(target: str):
-    import torch
+def _torch():
+    """torch, or None: libhca.so needs nothing of it."""
+    try:
+        import torch
+        return torch
+    except ImportError:
+        return None
+
+
+def _py_command(torch, target: str):
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
@@ -78,29 +86,34 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             jobs.append(cmd)
 
     # the module belongs to the torch that it was compiled with
-    import torch
+    torch = _torch()
     stamp = os.path.join(BUILD, "hca_py.torch")
     known = open(stamp).read() if os.path.exists(stamp) else ""
     py_src = [os.path.join(CSRC, "hca_py.cpp"), os.path.join(os.path.dirname(HERE), "include", "hca.h")]
     py_tmp = PY_LIB + f".tmp{os.getpid()}"
-    py_stale = force or known != torch.__version__ or _stale(PY_LIB, py_src)
-    if py_stale:
-        jobs.insert(0, _py_command(py_tmp))
-    kernels = len(jobs) - py_stale
+    py_stale = force or torch is None or known != torch.__version__ or _stale(PY_LIB, py_src)
+    kernels = len(jobs)
+    py_cmd = _py_command(torch, py_tmp) if torch is not None and py_stale else None
+    if py_cmd:
+        jobs.insert(0, py_cmd)
 
     def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
+        try:
+            r = subprocess.run(cmd, capture_output=True, text=True)
+        except OSError as e:  # no such compiler
+            r = subprocess.CompletedProcess(cmd, 127, "", str(e))
         return cmd, r
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
         for cmd, r in ex.map(run, jobs):
             if verbose or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-            if r.returncode != 0 and "-o" in cmd and cmd[cmd.index("-o") + 1] == py_tmp:
-                # no headers of Python or torch: the calls work without it, through ctypes
-                sys.stderr.write("_hca_py.so was not built: the serving calls cost 10 to 20 us more each\n")
-            elif r.returncode != 0:
+            if r.returncode != 0 and cmd is not py_cmd:
                 raise RuntimeError(f"nvcc failed on {cmd[-3]}")
+    if py_stale and not os.path.exists(py_tmp):
+        # no torch, no headers of it or of Python, no host compiler: the calls work
+        # without the module, through ctypes
+        sys.stderr.write("_hca_py.so was not built: the serving calls cost 10 to 20 us more each\n")
     if py_stale and os.path.exists(py_tmp):
         os.replace(py_tmp, PY_LIB)
         with open(stamp, "w") as f:
