@@ -4,9 +4,11 @@ Each ``csrc/*.cu`` translation unit is compiled to an object in parallel,
 then linked into ``block_sparse_compressed_gb300/libhca.so`` with the CUDA
 runtime linked statically (the driver API is reached at run time through
 ``cudaGetDriverEntryPoint``, so the library loads on a machine without a
-GPU).  ``csrc/hca_py.cpp``, the serving calls without their Python, becomes
-``_hca_py.so`` with the host compiler and torch's headers.  Usage: ``python -m
-block_sparse_compressed_gb300.build [--force]``.
+GPU).  ``csrc/hca_py.cpp``, the serving calls without their Python, becomes an
+extension module with the host compiler and torch's headers; its file name says
+which Python it is for and the module itself which torch.  Usage: ``python -m
+block_sparse_compressed_gb300.build [--force]`` (without torch: ``python
+block_sparse_compressed_gb300/build.py``).
 """
 from __future__ import annotations
 
@@ -21,7 +23,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhca.so")
-PY_LIB = os.path.join(HERE, "_hca_py.so")
+PY_LIB = os.path.join(HERE, "_hca_py" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xcompiler", "-fvisibility=hidden"]
@@ -66,7 +68,7 @@ def _py_command(torch, target: str):
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(a for i in inc for a in ("-isystem", i)),
+            f'-DHCA_TORCH="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(a for i in inc for a in ("-isystem", i)),
             os.path.join(CSRC, "hca_py.cpp"), "-o", target, "-L" + os.path.join(root, "lib"), "-ltorch_python",
             "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
@@ -85,13 +87,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             cmd = [nvcc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", s, "-o", o]
             jobs.append(cmd)
 
-    # the module belongs to the torch that it was compiled with
+    # the module belongs to the Python, the torch and the command that it was compiled with
     torch = _torch()
-    stamp = os.path.join(BUILD, "hca_py.torch")
+    stamp = os.path.join(BUILD, "hca_py.command")
     known = open(stamp).read() if os.path.exists(stamp) else ""
+    made_with = "\n".join([sys.version, *_py_command(torch, PY_LIB)]) if torch is not None else ""
     py_src = [os.path.join(CSRC, "hca_py.cpp"), os.path.join(os.path.dirname(HERE), "include", "hca.h")]
     py_tmp = PY_LIB + f".tmp{os.getpid()}"
-    py_stale = force or torch is None or known != torch.__version__ or _stale(PY_LIB, py_src)
+    py_stale = force or torch is None or known != made_with or _stale(PY_LIB, py_src)
     kernels = len(jobs)
     py_cmd = _py_command(torch, py_tmp) if torch is not None and py_stale else None
     if py_cmd:
@@ -113,13 +116,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if py_stale and not os.path.exists(py_tmp):
         # no torch, no headers of it or of Python, no host compiler: the calls work
         # without the module, through ctypes
-        sys.stderr.write("_hca_py.so was not built: the serving calls cost 10 to 20 us more each\n")
+        sys.stderr.write(f"{os.path.basename(PY_LIB)} was not built: the serving calls cost 10 to 20 us more each\n")
     if py_stale and os.path.exists(py_tmp):
         os.replace(py_tmp, PY_LIB)
         with open(stamp, "w") as f:
-            f.write(torch.__version__)
+            f.write(made_with)
     elif py_stale and os.path.exists(PY_LIB):
-        os.remove(PY_LIB)  # of another torch or another source
+        os.remove(PY_LIB)  # of another Python, torch or source
+    plain = os.path.join(HERE, "_hca_py.so")  # any Python would take that one
+    if plain != PY_LIB and os.path.exists(plain):
+        os.remove(plain)
     if force or kernels or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"]

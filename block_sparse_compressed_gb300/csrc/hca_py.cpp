@@ -252,4 +252,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_hca_py", nullptr, -1, methods, nu
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__hca_py() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__hca_py() {
+  PyObject *m = PyModule_Create(&module);
+  // what torch's headers were: hca.py uses the module with that torch only
+  if (m && PyModule_AddStringConstant(m, "torch_version", HCA_TORCH) != 0) Py_CLEAR(m);
+  return m;
+}

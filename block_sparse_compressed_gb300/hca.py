@@ -47,6 +47,16 @@ class HCAError(RuntimeError):
         super().__init__(f"{where}: {hca_status_string(status)}")
 
 
+def _extension():
+    """The extension module, or None: not built (no host compiler, no headers of
+    Python or torch), or built with another torch."""
+    try:
+        from . import _hca_py as py
+    except ImportError:
+        return None
+    return py if getattr(py, "torch_version", None) == torch.__version__ else None
+
+
 def load(path: str = LIB_PATH):
     """Load libhca.so and declare the C signatures (no CUDA call is made)."""
     global _lib, _py
@@ -121,14 +131,12 @@ def load(path: str = LIB_PATH):
             lib.hca_cache_attn_workspace_size.restype = Z
             lib.hca_cache_attn.argtypes = [P, P, P, P, P, P, I, I, P, P, P, I, I, P, P, I, I, I, I, I, I, I, F, I, P, Z, P]
             lib.hca_cache_attn.restype = I
-            try:
-                from . import _hca_py as py
+            py = _extension()
+            if py is not None:
                 py.bind(*(ctypes.cast(getattr(lib, f), P).value for f in (
                     "hca_cache_plan_workspace_size", "hca_cache_plan", "hca_cache_append_workspace_size",
                     "hca_cache_append", "hca_cache_attn_workspace_size", "hca_cache_attn")))
                 _py = py
-            except ImportError:  # not built: no headers of Python or torch
-                pass
             _lib = lib
     return _lib
 

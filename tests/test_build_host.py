@@ -80,3 +80,37 @@ def test_a_kernel_that_does_not_compile_ends_the_build(place, monkeypatch):
     with pytest.raises(RuntimeError, match="nvcc failed"):
         B.build()
     assert not os.path.exists(B.LIB)
+
+
+def test_the_module_is_of_one_python_torch_and_command(place, monkeypatch):
+    import sysconfig
+    import torch
+    assert MODULE == "_hca_py" + sysconfig.get_config_var("EXT_SUFFIX") != "_hca_py.so"
+    old = os.path.join(B.HERE, "_hca_py.so")
+    place()
+    open(old, "w").close()                 # one that any Python would import
+    assert place() == [] and not os.path.exists(old)
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "2.0.0")
+        assert place() == [MODULE] and place() == []
+    assert place() == [MODULE]
+    with monkeypatch.context() as m:
+        m.setattr(sys, "version", "3.99")
+        assert place() == [MODULE]
+    place()
+    monkeypatch.setenv("CXX", "clang++")
+    assert place() == [MODULE] and place() == []
+
+
+def test_a_module_of_another_torch_is_not_used(monkeypatch):
+    import types
+    import block_sparse_compressed_gb300 as pkg
+    from block_sparse_compressed_gb300 import hca
+    import torch
+    for version, used in ((torch.__version__, True), ("1.0", False), (None, False)):
+        m = types.ModuleType("_hca_py")
+        if version:
+            m.torch_version = version
+        monkeypatch.setitem(sys.modules, pkg.__name__ + "._hca_py", m)
+        monkeypatch.setattr(pkg, "_hca_py", m, raising=False)
+        assert (hca._extension() is m) == used
