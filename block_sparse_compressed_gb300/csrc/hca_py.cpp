@@ -20,6 +20,7 @@
 
 #include <climits>
 #include <initializer_list>
+#include <memory>
 
 #include "../../include/hca.h"
 
@@ -108,19 +109,27 @@ int dtype_code(at::ScalarType t) {
   return t == at::kFloat ? HCA_F32 : HCA_BF16;
 }
 
+struct Release {
+  void operator()(PyObject *o) const { Py_DECREF(o); }
+};
+using Tuple = std::unique_ptr<PyObject, Release>;
+
+// The answer is made in front of the launch, so that nothing is left to fail behind
+// it: a call that has been made is never answered as one that has not.
 template <typename... T>
-PyObject *results(const T &...t) {
-  PyObject *r = PyTuple_New(sizeof...(t));
+Tuple results(const T &...t) {
+  Tuple r(PyTuple_New(sizeof...(t)));
+  need(r != nullptr);
   Py_ssize_t i = 0;
-  bool ok = r != nullptr;
   ([&](const at::Tensor &x) {
-    PyObject *o = ok ? THPVariable_Wrap(x) : nullptr;  // None for an undefined one
-    if (o) PyTuple_SET_ITEM(r, i++, o);
-    else ok = false;
+    PyObject *o = THPVariable_Wrap(x);  // None for an undefined one
+    need(o);
+    PyTuple_SET_ITEM(r.get(), i++, o);
   }(t), ...);
-  if (!ok) Py_CLEAR(r);
   return r;
 }
+
+PyObject *answer(int rc, Tuple &r) { return rc ? PyLong_FromLong(rc) : r.release(); }
 
 template <typename F>
 PyObject *guarded(F f) {
@@ -146,11 +155,13 @@ PyObject *cache_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *fb = c.fits(free_blocks, kI32, {nfree}), *fc = c.fits(a[4], kI32, {1});
     const at::Tensor start = c.result(a[9], kI32, {R + 1}), slots = c.result(a[10], kI32, {nslots}), left = c.result(a[11], kI32, {1});
     const Workspace ws(c, a[12], a[13] != Py_False, lib.plan_ws((int)R));
+    Tuple r = results(start, slots, left, ws.tensor_);
+    void *const stream = c.stream();
     const int rc = lib.plan(static_cast<int32_t *>(h), static_cast<int32_t *>(ad), static_cast<int32_t *>(t), static_cast<int32_t *>(fb),
                             static_cast<int32_t *>(fc), static_cast<int32_t *>(left.data_ptr()), static_cast<int32_t *>(start.data_ptr()),
                             static_cast<int32_t *>(slots.data_ptr()), (int)R, (int)cols, bs, m, nblocks, (int)nfree, nslots,
-                            ws.ptr, ws.bytes, c.stream());
-    return rc ? PyLong_FromLong(rc) : results(start, slots, left, ws.tensor_);
+                            ws.ptr, ws.bytes, stream);
+    return answer(rc, r);
   });
 }
 
@@ -167,9 +178,11 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *px = c.fits(x, x.scalar_type(), {N, D}), *ps = c.fits(a[1], kI32, {N});
     void *pp = c.fits(pool, kE4m3, {nblocks, bs, D}), *pc = c.fits(a[3], kF32, {nblocks});
     const Workspace ws(c, a[4], a[5] != Py_False, lib.append_ws((int)nblocks));
+    Tuple r = results(ws.tensor_);
+    void *const stream = c.stream();
     const int rc = lib.append(px, static_cast<int32_t *>(ps), pp, static_cast<float *>(pc), (int)N, (int)D, (int)bs, (int)nblocks, dt,
-                              ws.ptr, ws.bytes, c.stream());
-    return rc ? PyLong_FromLong(rc) : results(ws.tensor_);
+                              ws.ptr, ws.bytes, stream);
+    return answer(rc, r);
   });
 }
 
@@ -214,12 +227,14 @@ PyObject *cache_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
     need(bytes > 0);
     const at::Tensor out = c.result(a[8], q.scalar_type(), {N, H, D}), lse = c.result(a[9], kF32, {N, H});
     const Workspace ws(c, a[10], a[11] != Py_False, bytes);
+    Tuple r = results(out, lse, ws.tensor_);
+    void *const stream = c.stream();
     const int rc = lib.attn(pq, static_cast<int32_t *>(ps), static_cast<int32_t *>(ph), raw.pool, static_cast<float *>(raw.scale),
                             static_cast<int32_t *>(raw.table), raw.nblocks, raw.cols, comp.pool, static_cast<float *>(comp.scale),
                             static_cast<int32_t *>(comp.table), comp.nblocks, comp.cols, out.data_ptr(),
                             static_cast<float *>(lse.data_ptr()), (int)N, (int)R, (int)H, (int)D, W, m, (int)bs, scale, dt,
-                            ws.ptr, ws.bytes, c.stream());
-    return rc ? PyLong_FromLong(rc) : results(out, lse, ws.tensor_);
+                            ws.ptr, ws.bytes, stream);
+    return answer(rc, r);
   });
 }
 
