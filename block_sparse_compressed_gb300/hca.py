@@ -581,7 +581,13 @@ def _scratch(ws: torch.Tensor, dev: torch.device) -> Tuple[int, int]:
 
 
 _I32, _F32, _E4M3 = torch.int32, torch.float32, torch.float8_e4m3fn
-_I32_MAX = (1 << 31) - 1  # no window and no ratio reaches further than that
+
+
+def _int(v: int) -> int:
+    """v as an int32 (ctypes would drop its upper bits).  No window and no ratio
+    reaches beyond the largest; every other number out of range stays one that
+    the C function refuses."""
+    return max(min(v, (1 << 31) - 1), -(1 << 31))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -627,8 +633,8 @@ def hca_cache_plan(held: torch.Tensor, added: torch.Tensor, table: torch.Tensor,
     rc = _enqueue(dev, lib.hca_cache_plan, _fits(held, "held", (R,), _I32, dev), _fits(added, "added", (R,), _I32, dev),
                   _fits(table, "table", (R, cols), _I32, dev), _fits(free_blocks, "free_blocks", (nfree,), _I32, dev),
                   _fits(free_count, "free_count", (1,), _I32, dev), _fits(free_left, "free_left", (1,), _I32, dev),
-                  _fits(start, "start", (R + 1,), _I32, dev), _fits(slots, "slots", (nslots,), _I32, dev), R, cols, bs,
-                  min(m, _I32_MAX), nblocks, nfree, nslots, *_scratch(ws, dev))
+                  _fits(start, "start", (R + 1,), _I32, dev), _fits(slots, "slots", (nslots,), _I32, dev), R, cols, _int(bs),
+                  _int(m), _int(nblocks), nfree, _int(nslots), *_scratch(ws, dev))
     if rc != 0:
         _check(rc, "hca_cache_plan")
     if check:
@@ -697,7 +703,7 @@ def hca_cache_attn(q: torch.Tensor, start: torch.Tensor, held: torch.Tensor, raw
     ws = torch.empty(_attn_ws_bytes(N, R, H, D, dt), dtype=torch.uint8, device=dev) if ws is None else ws
     rc = _enqueue(dev, lib.hca_cache_attn, _fits(q, "q", (N, H, D), q.dtype, dev), _fits(start, "start", (R + 1,), _I32, dev),
                   _fits(held, "held", (R,), _I32, dev), *args, _fits(out, "out", (N, H, D), q.dtype, dev),
-                  _fits(lse, "lse", (N, H), _F32, dev), N, R, H, D, min(W, _I32_MAX), min(m, _I32_MAX), bs, scale, dt,
+                  _fits(lse, "lse", (N, H), _F32, dev), N, R, H, D, _int(W), _int(m), bs, scale, dt,
                   *_scratch(ws, dev))
     if rc != 0:
         _check(rc, "hca_cache_attn")

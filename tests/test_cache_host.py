@@ -156,3 +156,25 @@ def test_the_binding_refuses_other_devices_and_workspaces():
             call(ws=ws.float())
         with pytest.raises(ValueError, match="contiguous"):
             call(ws=ws[::2])
+
+
+@pytest.mark.parametrize("kw,status", [(dict(nblocks=(1 << 32) + 8), E_SHAPE), (dict(bs=(1 << 32) + 16), E_ARG), (dict(m=1 - (1 << 32)), E_ARG),
+                                       (dict(nblocks=8 - (1 << 32)), E_SHAPE)])
+def test_plan_refuses_numbers_beyond_32_bits(kw, status, monkeypatch):
+    # each is an ordinary number in its lower 32 bits
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    monkeypatch.setattr(hca, "_enqueue", lambda dev, f, *a: f(*a, None))   # refused in front of any CUDA call
+    a = dict(dict(nblocks=8, bs=16, m=1), **kw)
+    with pytest.raises(hca.HCAError) as e:
+        hca.hca_cache_plan(i32(3), i32(3), i32(3, 2), i32(5), i32(1), a["nblocks"], a["bs"], 4, m=a["m"])
+    assert e.value.status == status
+
+
+@pytest.mark.parametrize("W,m", [(5 - (1 << 32), 4), (5, 4 - (1 << 32)), (-(1 << 40), 4), (5, -(1 << 31) - 1)])
+def test_attention_refuses_numbers_beyond_32_bits(W, m, monkeypatch):
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    monkeypatch.setattr(hca, "_enqueue", lambda dev, f, *a: f(*a, None))
+    c = (torch.zeros(4, 16, 64).to(torch.float8_e4m3fn), torch.ones(4), i32(2, 3))
+    with pytest.raises(hca.HCAError) as e:
+        hca.hca_cache_attn(torch.zeros(2, 4, 64), i32(3), i32(2), c, c, W, m, 0.1)
+    assert e.value.status == E_ARG
