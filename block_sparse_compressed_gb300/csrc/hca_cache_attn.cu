@@ -16,6 +16,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "hca_cache_attn.cuh"
 #include "tc_tiles.cuh"
@@ -586,8 +587,10 @@ cudaError_t combine(const AttnParams &p, int gmax, int sms, cudaStream_t st) {
   ProfScope prof(kKCacheCombine, st);
   // its blocks are set up while the attention's last CTAs run
   if (few) return launch_behind(hca_cache_combine_few_kernel<T>, grid, kCombineThreads, 0, st, p);
-  return p.D <= 128 ? launch_behind(hca_cache_combine_kernel<T, 4>, grid, kCombineThreads, 0, st, p)
-                    : launch_behind(hca_cache_combine_kernel<T, 8>, grid, kCombineThreads, 0, st, p);
+  if constexpr (std::is_same_v<T, float>) {  // bf16: D is 64 or 128
+    if (p.D > 128) return launch_behind(hca_cache_combine_kernel<T, 8>, grid, kCombineThreads, 0, st, p);
+  }
+  return launch_behind(hca_cache_combine_kernel<T, 4>, grid, kCombineThreads, 0, st, p);
 }
 
 // Columns of a group for H heads: enough for one position's slice of heads, and

@@ -209,3 +209,12 @@ def test_scores_up_to_the_stated_limit(H, D, sign):
     top = q[0, :, 0].double() * 3.5 * scale_of(D)
     # the reference, the score and what follows: a few roundings of fp32 at 2^24 in base 2
     assert float((lse[0].double().cpu() - top).abs().max()) <= 32 + 16
+
+
+@pytest.mark.parametrize("D", [144, 256])
+def test_fp32_of_wide_heads_in_many_groups(D):
+    # so many requests, a few of them long, that the join of many groups takes rows of more than 128
+    held = [(k * 613) % 500 + (20000 if k % 31 == 0 else 0) for k in range(70)]
+    q, start, h, raw, c = attn_case(held, [1] * 70, 3, D, 64, 4, 16, F32, 5)
+    a = (q, start, h, raw, c, 64, 4, scale_of(D))
+    check(run(*a), *a)
