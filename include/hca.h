@@ -321,10 +321,12 @@ HCA_API int hca_cache_plan(const int32_t *held, const int32_t *added, int32_t *t
  * as its scale; otherwise its scale becomes the larger of its own and that one,
  * and its rows in front of the new ones are brought to it (rounded to nearest
  * even; only values that become subnormal in e4m3 can change).  New values are
- * x / s rounded to nearest even; infinities and NaN are stored as NaN.  Rows
- * behind the new ones keep their bytes.  A slot >= nblocks * bs is skipped, a
- * scale that is not positive and finite is replaced, and of several runs of
- * rows for one block only one is written; all three are HCA_ERR_CACHE.
+ * x / s rounded to nearest even; infinities and NaN are stored as NaN.  (A larger
+ * scale that is no power of two, which only a caller can have written, stays too:
+ * x is then multiplied by fp32's 1 / s.)  Rows behind the new ones keep their
+ * bytes.  A slot >= nblocks * bs is skipped, a scale that is not positive and
+ * finite is replaced, and of several runs of rows for one block only one is
+ * written; all three are HCA_ERR_CACHE.
  * Workspace: hca_cache_append_workspace_size(nblocks). */
 HCA_API size_t hca_cache_append_workspace_size(int nblocks);
 HCA_API int hca_cache_append(const void *x, const int32_t *slots, void *pool, float *scale, int N, int D, int bs,
@@ -340,14 +342,15 @@ HCA_API int hca_cache_append(const void *x, const int32_t *slots, void *pool, fl
  * sliding attention; full causal attention with W beyond the length).  Rows of
  * out and lse from start[R] on are left as they are.  Cache rows that no token
  * sees may hold anything.
- * Block scales may be any positive finite numbers, however far apart.
+ * Block scales are positive and finite, 2^-96 to 2^120 as hca_cache_append makes
+ * them (beyond that bits may be lost), powers of two or not, however far apart.
  * bf16: D = 64 or 128 (HCA_ERR_UNSUPPORTED otherwise).  out's probabilities are
  * rounded to 11 bits or 2^-27 of the row's largest, whichever is more (lse's sum
  * is not); a key in a block of scale below 2^-15 of a larger one S of its request
  * adds to out to within 2^-33 S, which is 2^-24 of the smallest e4m3 step there.
  * Scores scale <q, k> are below 2^24 in magnitude (their differences are lost
  * beyond it, and from 2^27 on a result may be NaN).
- * fp32: D a multiple of 16 up to 256.
+ * fp32: D a multiple of 16 up to 256, q below 2^100 in magnitude.
  * Lengths out of range, a raw table too narrow for a token's window, a
  * compressed table too narrow for the entries, or 2^31 - 2^16 tiles of 128 keys
  * and more in all (each group of up to 128 rows of q has its own) make all N rows

@@ -218,3 +218,24 @@ def test_fp32_of_wide_heads_in_many_groups(D):
     q, start, h, raw, c = attn_case(held, [1] * 70, 3, D, 64, 4, 16, F32, 5)
     a = (q, start, h, raw, c, 64, 4, scale_of(D))
     check(run(*a), *a)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N", [5, 700])
+def test_append_keeps_a_scale_that_is_no_power_of_two(dtype, N):
+    # rows behind others in blocks of scales 1 .. 2 and large enough: x times fp32's 1 / s
+    bs, D = 32, 64
+    nblocks = -(-N // 5)
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(N, D, generator=g).to(dtype)
+    slots = torch.tensor([k // 5 * bs + 11 + k % 5 for k in range(N)], dtype=torch.int32)
+    pool = (torch.randn(nblocks, bs, D, generator=g) * 100).clamp(-448, 448).to(E4M3)
+    scale = 1 + torch.rand(nblocks, generator=g)
+    p, s = pool.to(DEV), scale.to(DEV)
+    hca.hca_cache_append(x.to(DEV), slots.to(DEV), p, s, check=True)
+    want = pool.float().double().numpy()
+    inv = (1 / scale).double().numpy()[slots.numpy() // bs]
+    scaled = (x.float() * torch.from_numpy(inv).float()[:, None]).double().numpy()
+    want.reshape(-1, D)[slots.numpy()] = OC.e4m3_round(scaled)
+    assert torch.equal(s.cpu(), scale)
+    np.testing.assert_array_equal(p.float().cpu().double().numpy(), want)
