@@ -20,7 +20,8 @@
 // contiguous in x and in the pool, so a run is one flat conversion of n * D
 // values after one maximum over them.  64,258 rows of 128 bf16 values take 10.3
 // us, 2.4 TB/s: one wave of CTAs that each wait for slots, values and owners in
-// turn, behind a kernel of the owners; 64 single rows take 5 us, latency.
+// turn, behind a kernel of the owners (500,000 rows: 43 us, 4.5 TB/s); 64 single
+// rows take 5 us, latency.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -37,7 +38,9 @@ namespace {
 // plan
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanOneCta = 4096;  // slots that the planning CTA itself writes
+// Slots that the planning CTA itself writes: 3,000 and 5,000 take it 8.3 and 10.4 us,
+// a second kernel 8.3 for both (10,000: 12.5 and 8.3).
+constexpr int kPlanOneCta = 4096;
 
 struct PlanItem {
   long long entries;
@@ -184,6 +187,8 @@ __global__ void __launch_bounds__(kPlanThreads) hca_cache_plan_kernel(const Cach
   if (a.nslots <= kPlanOneCta) plan_fill(a, few ? near.start : a.start, few ? near.taken : a.taken, few ? &near : nullptr, avail, 0, 1);
 }
 
+// Slots of a CTA (198,600 and 1,059,918 slots: 10.4 and 10.3 us; 512 of them 8.4 and
+// 12.4, 2,048 12.5 and 10.3).
 constexpr int kFillThreads = 256, kSlotsPerCta = 1024;
 
 __global__ void __launch_bounds__(kFillThreads) hca_cache_fill_kernel(const CachePlanArgs a) {
@@ -378,7 +383,10 @@ __device__ __forceinline__ int append_run(const CacheAppendArgs &a, int t, int l
 // A CTA takes the runs that begin in `rows` consecutive rows: long ones all
 // threads together, so that a block's rows are in flight at once, short ones a
 // warp each.  Values wait for their block's scale as they came: as fp32 they took
-// 96 registers, 5 CTAs an SM and 12.3 us where it is 8 and 10.3 now.
+// 96 registers, 5 CTAs an SM and 12.3 us where it is 8 and 10.3 now.  Long is from
+// kLongRun rows on: 1,500 runs of 1 to 12 rows take 8.4 us, 10.3 from 4 on; 8 runs
+// of up to 300 rows 6.2, 7.4 from 16 on (which is better for blocks of 16: 64,258
+// rows 12.6 for 13.0).
 constexpr int kChunkThreads = 128, kChunkRows = 64, kLongRun = 8;
 constexpr int kWindow = kChunkRows + 128;  // rows looked at: the last run may go on for a block
 
@@ -521,6 +529,8 @@ cudaError_t cache_append(const CacheAppendArgs &args, cudaStream_t st) {
   }
   hca_cache_claim_kernel<<<(a.N + 255) / 256, 256, 0, st>>>(a);
   // enough CTAs for every SM, but no more than one for each block of a long prompt
+  // (64,258 rows in blocks of 64 and of 16, and 1,500 runs of 1 to 40 rows: 10.5, 13.0
+  // and 12.2 us; N / 512 10.5, 14.5 and 14.6; N / 2048 11.3, 12.9 and 12.4)
   const int rows = std::min(std::max(a.N / 1024, 4), kChunkRows);
   const int grid = (a.N + rows - 1) / rows;
   return f32 ? launch_behind(hca_cache_append_kernel<float>, dim3(grid), kChunkThreads, 0, st, a, rows)

@@ -150,10 +150,13 @@ struct SchedHeader {  // at the start of the workspace
 
 // Many short groups (prompts): the line is cut between groups, which saves every
 // CTA a partial group's beginning and end and the join (12 prompts of 200 to 500
-// tokens over up to 130,000 rows, groups of up to 11 tiles: 159 us, 188 when cut
+// tokens over up to 130,000 rows, groups of up to 11 tiles: 152 us, 188 when cut
 // anywhere); a group then counts for kGroupCost tiles more than it has, what its
-// beginning and end take (0 and 4: 179 and 166 us).  Longer groups leave the CTAs
-// less even than cuts cost (66 tiles: 585 us, 568 when cut anywhere).
+// beginning and end take (0 and 4: 174 and 162 us).  Longer groups leave the CTAs
+// less even than cuts cost (3 and 6 prompts of 447 tokens over 80,000 rows, groups
+// of 43 tiles: 226 and 425 us cut anywhere, 276 and 457 cut between groups),
+// unless a CTA has many of them (24 such prompts over up to 130,000 rows: 1,764 us,
+// 1,363 cut between groups, which the rule leaves).
 constexpr int kGroupCost = 2, kShortGroup = 32;
 
 struct Pages {

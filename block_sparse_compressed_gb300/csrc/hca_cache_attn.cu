@@ -114,8 +114,8 @@ __device__ __forceinline__ void poison(const AttnParams &p) {
 // fp32 kernel: one thread per key for the scores, one per dimension for the
 // output; D a multiple of 16 up to 256.  Rows of q share a key tile in groups of
 // kCols; of more columns than the requests' tokens fill the rest is wasted (8
-// requests of one or two tokens and 4 heads over up to 4,000 rows: 18.6 us with 8
-// columns, 20.7 with 16).  Bound by latency: the tile's table, scale and rows are
+// requests of one or two tokens and 4 heads over up to 4,000 rows: 17.2 us with 8
+// columns, 20.6 with 16).  Bound by latency: the tile's table, scale and rows are
 // three dependent loads.
 // ---------------------------------------------------------------------------
 constexpr int kSimtThreads = 128;
@@ -581,7 +581,10 @@ cudaError_t simt(const AttnParams &p, cudaStream_t st) {
 
 template <typename T>
 cudaError_t combine(const AttnParams &p, int gmax, int sms, cudaStream_t st) {
-  // few groups: fewer than leave each 16 CTAs
+  // Few groups: fewer than leave each 16 CTAs.  One, 8, 16 and 19 requests over 100,000
+  // rows at m = 4 take 26.7, 33.0, 41.8 and 47.2 us, with the kernel of many groups
+  // 62.2, 43.6, 46.6 and 48.7; 24 and 48 52.8 and 80.7, with the one of few 53.2 and
+  // 83.8.
   const bool few = (long long)gmax * 16 <= p.grid;
   const dim3 grid = few ? dim3(4 * sms) : dim3(p.grid, (p.P * p.HS + 4 * kCombineWarps - 1) / (4 * kCombineWarps));
   ProfScope prof(kKCacheCombine, st);
@@ -674,7 +677,7 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
   if (sms <= 0) return cudaErrorNoDevice;
   const bool tcs = on_tensor_cores(a.dtype);
   p.grid = std::min((tcs ? tc_cache_ctas() : 4) * sms, l.ctas);
-  // a CTA of one tile costs a part to join (94 tokens of 37 requests: 20.8 us, 18.6 with 2, 20.7 with 4)
+  // a CTA of one tile costs a part to join (94 tokens of 37 requests: 20.6 us, 18.6 with 2, 20.4 with 4)
   p.min_tiles = tcs ? 2 : 1;
   const int threads = tcs ? tc_cache_threads() : kSimtThreads;
   p.in_cta = l.slices == 1 && a.R <= threads && l.gmax <= (size_t)threads;

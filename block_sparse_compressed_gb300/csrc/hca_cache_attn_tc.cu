@@ -37,9 +37,10 @@
 // u, and O follows.  What is left of a scale below 2^-15 of the unit, or of one that
 // is no power of two, multiplies its scores and probabilities in tensor memory, in
 // functions of their own that ordinary tiles only pass by.  The factors take the
-// converter 3 of 94 us at m = 4; a factor for every 16 keys in the softmax
-// instead 2 there and 3.5 of 75 for prompts; both loops, of which a tile without
-// factors takes the shorter, 2.5 more for prompts.
+// converter 3 of 95 us at m = 4.  (Other ways, there and for prompts of 2,571 tokens,
+// where this one took 93.4 and 74.0: scales for every 16 keys in the softmax 96.5
+// and 78.0, the rest beside them 96.9 and 83.5; a unit for each half and a second
+// loop for those that need factors 93.8 and 79.2.)
 //
 // The reference exponent of a row is 2 below its largest score so far, so that fp16
 // reaches down to 2^-27 of the largest probability, and raised only when that score
@@ -58,14 +59,15 @@
 // Bounds.  A half's scores take the tensor cores 384 cycles (8 products of 128 x
 // 64 x 16 at 48, bound by their operands from shared memory) and its part of O
 // 254, so a tile 1,228 when products are queued; but the time from issue to the
-// softmax's first look is 805 and 590, and a half's softmax 1,100.  Two CTAs of an
-// SM fill part of each other's gaps: 64 tokens over 95,000 rows each (199 MB of
-// cache, 64 heads, D = 128) take 91.5 us, 2.2 TB/s and 552 TFLOP/s, with the
-// tensor cores busy half of the time (82 us with the products all but left out).
-// One decode step of 64 requests at 128 keys an entry takes 22.4 us, of which 2.6
-// are the schedule, 3 the way to the first scores and 2 the way out; chunks of
-// 2,571 prompt tokens 74 us, half of it beginnings and ends of their groups of 2
-// tokens.
+// softmax's first look is 805 and 590, and a half's softmax about 1,100.  Two CTAs
+// of an SM fill part of each other's gaps: 64 tokens over 95,000 rows each (199 MB
+// of cache, 64 heads, D = 128) take 94.8 us, 2.1 TB/s and 533 TFLOP/s, with the
+// tensor cores busy half of the time (81.6 us with one product of each half left, 87.3
+// with half of the score products, 93 with half of the output products or without
+// exponentials, 91.5 without the keys' factors).  One decode step of 64 requests at 128
+// keys an entry takes 22.5 us: the schedule, the way to the first scores and the way
+// out are most of it.  Chunks of 2,571 prompt tokens take 75.4 us, 67.9 with one
+// product left: beginnings and ends of their groups of 2 tokens.
 // Measured and left, each against the kernel of its time: scores of a whole tile
 // at once (128 x 128 x 16 at 64 cycles: the tensor cores do less, but the softmax
 // waits: 109 us for 102); two softmax warpgroups, a half each (99 us for 96: the
@@ -357,6 +359,10 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
     // Ranges that no group's border cuts give a CTA tiles of one group only and
     // save it a second one's beginning and end, about two tiles' time each;
     // ceil(tiles / quota) of them for each group fit the grid with a larger quota.
+    // Up to 2 tiles more they pay: 64 requests over up to 131,072 rows at m = 128 22.6
+    // us, 24.9 cut anywhere, 20 over up to 20,000 at m = 4 27.4 and 30.7; more do not:
+    // 140 over 3,000 rows 24.8 cut anywhere, 30.8 with 4 more, 64 over 60,000 to
+    // 131,072 rows 95 cut anywhere, 107 with as many as it takes.
     quota = cta_quota(ntiles, p.grid, p.min_tiles);
     const int own = cta_quota(ntiles, max(p.grid - ngroups, 1), p.min_tiles);
     const bool whole_groups = ngroups < p.grid && own <= quota + 2;
