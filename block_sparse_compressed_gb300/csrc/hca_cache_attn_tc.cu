@@ -251,23 +251,28 @@ static __device__ __noinline__ void scale_s(uint32_t addr, const PageMeta *meta,
   tmem_wait_st();
 }
 
-// The same for their probabilities, pairs of fp16.
+// Probabilities of kSpan keys whose scores lie at `s`, times their pages' rests, to
+// `to` (which a key's score has left by then); returns the sum of the
+// probabilities themselves.
 template <int kSpan>
-static __device__ __noinline__ void scale_p(uint32_t addr, const PageMeta *meta, int k0, int log_bs) {
+static __device__ __noinline__ float scaled_p(uint32_t s, uint32_t to, float ck, float m_use, const PageMeta *meta, int k0, int log_bs) {
+  float sum = 0.f;
 #pragma unroll 1
   for (int c = 0; c < kSpan; c += 16) {
     const float rest = meta[(k0 + c) >> log_bs].rest;
-    uint32_t v[8];
-    tmem_ld8(addr + c / 2, v);
+    uint32_t v[16], pk[8];
+    tmem_ld16(s + c, v);
     tmem_wait_ld();
 #pragma unroll
-    for (int y = 0; y < 8; ++y) {
-      const float2 e = __half22float2(*reinterpret_cast<const __half2 *>(&v[y]));
-      v[y] = f16x2_rn(e.x * rest, e.y * rest);
+    for (int y = 0; y < 16; y += 2) {
+      const float e0 = ex2_approx(fmaf(__uint_as_float(v[y]), ck, -m_use)), e1 = ex2_approx(fmaf(__uint_as_float(v[y + 1]), ck, -m_use));
+      sum += e0 + e1;
+      pk[y >> 1] = f16x2_rn(e0 * rest, e1 * rest);
     }
-    tmem_st8(addr + c / 2, v);
+    tmem_st8(to + c / 2, pk);
   }
   tmem_wait_st();
+  return sum;
 }
 
 // A warp's rows of O times f.
@@ -920,23 +925,38 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
             // P over the first columns of the half's S, with zeros for the other
             // copies' keys
             const uint32_t pcol = lane_addr + h * 64;
-            uint32_t pk[kSpan / 2];
-            const uint64_t ck2 = f32x2(__float_as_uint(ck), __float_as_uint(ck));
-            const uint64_t nm2 = f32x2(__float_as_uint(-m_use), __float_as_uint(-m_use));
-            uint64_t acc[2] = {0, 0};
+            if (odd & 1) {
+              // the masked scores go back to tensor memory
+              if constexpr (kSpan == 16) {
+                tmem_st16(lane_addr + k0, sv);
+              } else {
 #pragma unroll
-            for (int c4 = 0; c4 < kSpan / 16; ++c4) {
-#pragma unroll
-              for (int y = 0; y < 16; y += 2) {
-                float t0, t1;
-                f32x2_split(ffma2(f32x2(sv[c4 * 16 + y], sv[c4 * 16 + y + 1]), ck2, nm2), t0, t1);
-                const float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
-                acc[(y >> 1) & 1] = fadd2(acc[(y >> 1) & 1], f32x2(__float_as_uint(e0), __float_as_uint(e1)));
-                pk[c4 * 8 + (y >> 1)] = f16x2_rn(e0, e1);
+                for (int c = 0; c < kSpan; c += 32) tmem_st32(lane_addr + k0 + c, *reinterpret_cast<uint32_t(*)[32]>(sv + c));
               }
-              if (kSpan > 16 && (c4 & 1)) tmem_st16(pcol + copy * (kSpan / 2) + (c4 - 1) * 8, *reinterpret_cast<uint32_t(*)[16]>(&pk[(c4 - 1) * 8]));
+              tmem_wait_st();
+              l_run += scaled_p<kSpan>(lane_addr + k0, pcol + copy * (kSpan / 2), ck, m_use, meta, k0, p.log_bs);
+            } else {
+              uint32_t pk[kSpan / 2];
+              const uint64_t ck2 = f32x2(__float_as_uint(ck), __float_as_uint(ck));
+              const uint64_t nm2 = f32x2(__float_as_uint(-m_use), __float_as_uint(-m_use));
+              uint64_t acc[2] = {0, 0};
+#pragma unroll
+              for (int c4 = 0; c4 < kSpan / 16; ++c4) {
+#pragma unroll
+                for (int y = 0; y < 16; y += 2) {
+                  float t0, t1;
+                  f32x2_split(ffma2(f32x2(sv[c4 * 16 + y], sv[c4 * 16 + y + 1]), ck2, nm2), t0, t1);
+                  const float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
+                  acc[(y >> 1) & 1] = fadd2(acc[(y >> 1) & 1], f32x2(__float_as_uint(e0), __float_as_uint(e1)));
+                  pk[c4 * 8 + (y >> 1)] = f16x2_rn(e0, e1);
+                }
+                if (kSpan > 16 && (c4 & 1)) tmem_st16(pcol + copy * (kSpan / 2) + (c4 - 1) * 8, *reinterpret_cast<uint32_t(*)[16]>(&pk[(c4 - 1) * 8]));
+              }
+              if constexpr (kSpan == 16) tmem_st8(pcol + copy * 8, pk);
+              float a, b;
+              f32x2_split(fadd2(acc[0], acc[1]), a, b);
+              l_run += a + b;
             }
-            if constexpr (kSpan == 16) tmem_st8(pcol + copy * 8, pk);
             if constexpr (C::kCopies == 2) {
               uint32_t zero[16];
 #pragma unroll
@@ -950,11 +970,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
 #pragma unroll
               for (int y = 1; y < 4; ++y) tmem_st8(pcol + ((copy + y) & 3) * 8, zero);
             }
-            float a, b;
-            f32x2_split(fadd2(acc[0], acc[1]), a, b);
-            l_run += a + b;
             tmem_wait_st();
-            if (odd & 1) scale_p<kSpan>(pcol + copy * (kSpan / 2), meta, k0, p.log_bs);
             tc_fence_before();
             mbar_arrive(&sh.p_full[h]);
           }

@@ -239,3 +239,30 @@ def test_append_keeps_a_scale_that_is_no_power_of_two(dtype, N):
     want.reshape(-1, D)[slots.numpy()] = OC.e4m3_round(scaled)
     assert torch.equal(s.cpu(), scale)
     np.testing.assert_array_equal(p.float().cpu().double().numpy(), want)
+
+
+@pytest.mark.parametrize("H,D", [(16, 64), (64, 128), (128, 64)])
+def test_probabilities_beside_other_scales_are_rounded_once(H, D):
+    # blocks of scales 1 .. 2.  A token sees a key with the top score and values of 0 and
+    # two of nearly equal scores and opposite values, so that the result is the
+    # difference of two probabilities, and what their roundings leave of it shows
+    R, bs, W, half = 150, 16, 3, D // 2
+    g = torch.Generator().manual_seed(6)
+    raw = make_cache([3] * R, 1, bs, D, 6)
+    u = torch.randn(half, generator=g)
+    raw[1].copy_(2.0 ** -7 * (1 + torch.rand(raw[1].shape, generator=g)))
+    for r in range(R):
+        k = torch.zeros(3, D)
+        k[0, :half] = 100 * u + 10 * torch.randn(half, generator=g)
+        k[1, :half] = 40 * u + 10 * torch.randn(half, generator=g)
+        k[2, :half] = k[1, :half]
+        k[2, r % half] *= 1.15                      # one step of e4m3 or two
+        k[1, half:] = 300 * torch.randn(half, generator=g).sign()
+        k[2, half:] = -k[1, half:]
+        raw[0][int(raw[2][r, 0]), :3] = k.clamp(-448, 448).to(E4M3)
+    q = torch.zeros(R, H, D)
+    q[..., :half] = u / half ** 0.5 * (1 + torch.rand(R, H, 1, generator=g))
+    q = q.to(BF16)
+    start, held = torch.arange(R + 1, dtype=torch.int32), torch.full((R,), 2, dtype=torch.int32)
+    a = (q, start, held, raw, None, W, 4, scale_of(D))
+    check(run(*a), *a)
