@@ -61,12 +61,13 @@
 // 254, so a tile 1,228 when products are queued; but the time from issue to the
 // softmax's first look is 805 and 590, and a half's softmax about 1,100.  Two CTAs
 // of an SM fill part of each other's gaps: 64 tokens over 95,000 rows each (199 MB
-// of cache, 64 heads, D = 128) take 94.8 us, 2.1 TB/s and 533 TFLOP/s, with the
-// tensor cores busy half of the time (81.6 us with one product of each half left, 87.3
-// with half of the score products, 93 with half of the output products or without
-// exponentials, 91.5 without the keys' factors).  One decode step of 64 requests at 128
+// of cache, 64 heads, D = 128) take 95.5 us, 2.1 TB/s and 529 TFLOP/s, with the
+// tensor cores busy half of the time (timing copies of a build of 94.8 us: 81.6 with
+// one product of each half left, 87.3 with half of the score products, 93 with half
+// of the output products or without exponentials, 91.5 without the keys' factors).
+// One decode step of 64 requests at 128
 // keys an entry takes 22.5 us: the schedule, the way to the first scores and the way
-// out are most of it.  Chunks of 2,571 prompt tokens take 75.4 us, 67.9 with one
+// out are most of it.  Chunks of 2,571 prompt tokens take 75.0 us, 67.9 with one
 // product left: beginnings and ends of their groups of 2 tokens.
 // Measured and left, each against the kernel of its time: scores of a whole tile
 // at once (128 x 128 x 16 at 64 cycles: the tensor cores do less, but the softmax
