@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <utility>
 
 #include "hca_common.cuh"
 #include "hca_internal.h"
@@ -424,6 +425,160 @@ int hca_local_attn_bwd(const void *q, const void *kv, const int32_t *seg, const 
   void *dckv = static_cast<char *>(workspace) + need;  // [B, 1, D], discarded
   return hca_attn_bwd(q, kv, kv, seg, out, lse, dout, dq, dkv, dckv, B, H, S, D, W, m, scale, dtype, workspace,
                       need, stream);
+}
+
+// ---------------------------------------------------------------------------
+// norms and positions
+// ---------------------------------------------------------------------------
+constexpr int kMaxRowD = 512, kMaxRopeAxes = 4;
+
+static int norm_rope_shape(const NormRopeArgs &a, int H) {
+  if (a.dtype != HCA_BF16 && a.dtype != HCA_F32) return HCA_ERR_DTYPE;
+  if (a.B < 0 || a.S < 0 || H < 0 || H > (1 << 20) || a.D < 1 || a.D > kMaxRowD || a.S > (1 << 30) || a.R < 0 || a.R > (1 << 24) ||
+      (double)a.B * a.S * (H + 1.0) > 4.0e15)
+    return HCA_ERR_SHAPE;
+  if (a.D % 8 != 0) return HCA_ERR_ALIGN;
+  if (a.axes < 1 || a.axes > kMaxRopeAxes || a.rot < 0 || a.first < 0 || a.rot > a.D || a.first > a.D - a.rot) return HCA_ERR_ARG;
+  if (a.first % 8 != 0 || a.rot % (a.halves ? 16 : 8) != 0) return HCA_ERR_ARG;
+  if (!std::isfinite(a.eps) || a.eps < 0.f) return HCA_ERR_ARG;
+  if (a.start && a.B > 1) return HCA_ERR_SHAPE;
+  return HCA_OK;
+}
+
+// What rotates has its frequencies and coordinates.
+static int norm_rope_pointers(const NormRopeArgs &a) {
+  if (a.rot > 0 && (!a.freq || (a.axes > 1 && !a.pos))) return HCA_ERR_NULL;
+  if (a.start && a.R > 0 && !a.pos && !a.held && a.rot > 0) return HCA_ERR_NULL;
+  if (!a.start && a.held) return HCA_ERR_NULL;
+  return HCA_OK;
+}
+
+// Strides of batch rows, heads and positions; given ones lack the head's with H < 0 (kv).
+struct RowStrides {
+  int64_t b, h, s;
+};
+static int row_strides(const int64_t *given, int H, const NormRopeArgs &a, RowStrides &r) {
+  const int64_t heads = H < 0 ? 1 : H;
+  if (given) {
+    r = H < 0 ? RowStrides{given[0], 0, given[1]} : RowStrides{given[0], given[1], given[2]};
+  } else if (a.start) {
+    r = RowStrides{0, a.D, heads * a.D};
+  } else {
+    r = RowStrides{heads * a.S * a.D, (int64_t)a.S * a.D, a.D};
+  }
+  const int unit = 16 / elt_bytes(a.dtype);
+  const int64_t extent[3] = {a.B, heads, a.S}, stride[3] = {r.b, r.h, r.s};
+  double last = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (extent[i] > 1 && (stride[i] < 0 || stride[i] % unit != 0)) return HCA_ERR_ALIGN;
+    if (extent[i] > 1) last += (double)stride[i] * (double)(extent[i] - 1);
+  }
+  return last > 4.0e18 ? HCA_ERR_SHAPE : HCA_OK;
+}
+
+// Rows that are written lie apart from one another.
+static bool rows_apart(const RowStrides &r, int H, const NormRopeArgs &a) {
+  int64_t extent[3] = {a.B, H, a.S}, stride[3] = {r.b, r.h, r.s};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (stride[j] < stride[i]) {
+        std::swap(stride[i], stride[j]);
+        std::swap(extent[i], extent[j]);
+      }
+  int64_t end = a.D;  // of the rows of the smaller strides
+  for (int i = 0; i < 3; ++i) {
+    if (extent[i] <= 1) continue;
+    if (stride[i] < end) return false;
+    end += stride[i] * (extent[i] - 1);
+  }
+  return true;
+}
+
+static int norm_rope_tensor(NormRopeTensor &t, const NormRopeArgs &a, int H, const void *x, const int64_t *x_strides, const void *g,
+                            void *y, const int64_t *y_strides, const float *w, float *dw) {
+  const int heads = H < 0 ? 1 : H;
+  t = NormRopeTensor{};
+  t.x = x; t.g = g; t.y = y; t.w = w; t.dw = dw;
+  t.H = heads;
+  RowStrides sx, sg, sy;
+  int rc = row_strides(x_strides, H, a, sx);
+  if (rc == HCA_OK) rc = row_strides(nullptr, H, a, sg);
+  if (rc == HCA_OK) rc = row_strides(y_strides, H, a, sy);
+  if (rc != HCA_OK) return rc;
+  t.xb = sx.b; t.xh = sx.h; t.xs = sx.s;
+  t.gb = sg.b; t.gh = sg.h; t.gs = sg.s;
+  t.yb = sy.b; t.yh = sy.h; t.ys = sy.s;
+  if (a.B * (long long)a.S * heads == 0) {
+    t.H = 0;
+    return HCA_OK;
+  }
+  if (!rows_apart(sy, heads, a)) return HCA_ERR_ARG;
+  if (!x || !y || (a.mode == 2 && !g) || (dw && !w)) return HCA_ERR_NULL;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(g)) return HCA_ERR_ALIGN;
+  return HCA_OK;
+}
+
+int hca_norm_rope_fwd(const void *q, const int64_t *q_strides, const float *wq, void *qo, const void *kv, const int64_t *kv_strides,
+                      const float *wkv, void *kvo, const int32_t *pos, const float *freq, const int32_t *start,
+                      const int32_t *held, int B, int H, int S, int D, int R, int axes, int first, int rot, int halves,
+                      float eps, int dtype, void *stream) {
+  NormRopeArgs a = {};
+  a.pos = pos; a.start = start; a.held = held; a.freq = freq;
+  a.B = B; a.S = S; a.D = D; a.R = R; a.axes = axes; a.first = first; a.rot = rot; a.halves = halves; a.dtype = dtype;
+  a.mode = 1; a.eps = eps;
+  int rc = norm_rope_shape(a, H);
+  if (rc == HCA_OK) rc = norm_rope_pointers(a);
+  if (rc == HCA_OK && (q || qo)) rc = norm_rope_tensor(a.t[0], a, H, q, q_strides, nullptr, qo, nullptr, wq, nullptr);
+  if (rc == HCA_OK && (kv || kvo)) rc = norm_rope_tensor(a.t[1], a, -1, kv, kv_strides, nullptr, kvo, nullptr, wkv, nullptr);
+  if (rc != HCA_OK) return rc;
+  if (take_launch_failure()) return HCA_ERR_CUDA;
+  if (a.t[0].H + a.t[1].H == 0 || (start && R == 0)) return HCA_OK;
+  return cuda_status(norm_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t hca_norm_rope_workspace_size(int D) {
+  return D < 1 || D > kMaxRowD ? 0 : align_up((size_t)kNormRopeParts * 2 * D * sizeof(float));
+}
+
+int hca_norm_rope_bwd(const void *q, const int64_t *q_strides, const float *wq, const void *dqo, void *dq,
+                      const int64_t *dq_strides, float *dwq, const void *kv, const int64_t *kv_strides, const float *wkv,
+                      const void *dkvo, void *dkv, const int64_t *dkv_strides, float *dwkv, const int32_t *pos,
+                      const float *freq, int B, int H, int S, int D, int axes, int first, int rot, int halves, float eps,
+                      int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+  NormRopeArgs a = {};
+  a.pos = pos; a.freq = freq;
+  a.B = B; a.S = S; a.D = D; a.axes = axes; a.first = first; a.rot = rot; a.halves = halves; a.dtype = dtype;
+  a.mode = 2; a.eps = eps;
+  int rc = norm_rope_shape(a, H);
+  if (rc == HCA_OK) rc = norm_rope_pointers(a);
+  if (rc == HCA_OK && (q || dq)) rc = norm_rope_tensor(a.t[0], a, H, q, q_strides, dqo, dq, dq_strides, wq, dwq);
+  if (rc == HCA_OK && (kv || dkv)) rc = norm_rope_tensor(a.t[1], a, -1, kv, kv_strides, dkvo, dkv, dkv_strides, wkv, dwkv);
+  if (rc == HCA_OK) rc = check_ws(workspace, workspace_bytes, hca_norm_rope_workspace_size(D));
+  if (rc != HCA_OK) return rc;
+  if (take_launch_failure()) return HCA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  float *const dws[2] = {dwq, dwkv};
+  for (int i = 0; i < 2 && rc == HCA_OK; ++i)  // sums over no rows
+    if (dws[i] && a.t[i].H == 0) rc = cuda_status(cudaMemsetAsync(dws[i], 0, sizeof(float) * D, st)), a.t[i].dw = nullptr;
+  if (rc != HCA_OK || a.t[0].H + a.t[1].H == 0) return rc;
+  a.part = static_cast<float *>(workspace);
+  return cuda_status(norm_rope(a, st));
+}
+
+int hca_rope(const void *x, const int64_t *x_strides, void *y, const int64_t *y_strides, const int32_t *pos, const float *freq,
+             const int32_t *start, const int32_t *held, int B, int H, int S, int D, int R, int axes, int first, int rot,
+             int halves, int inverse, int dtype, void *stream) {
+  NormRopeArgs a = {};
+  a.pos = pos; a.start = start; a.held = held; a.freq = freq;
+  a.B = B; a.S = S; a.D = D; a.R = R; a.axes = axes; a.first = first; a.rot = rot; a.halves = halves; a.dtype = dtype;
+  a.inverse = inverse;
+  int rc = norm_rope_shape(a, H);
+  if (rc == HCA_OK) rc = norm_rope_pointers(a);
+  if (rc == HCA_OK) rc = norm_rope_tensor(a.t[0], a, H, x, x_strides, nullptr, y, y_strides, nullptr, nullptr);
+  if (rc != HCA_OK) return rc;
+  if (take_launch_failure()) return HCA_ERR_CUDA;
+  if (a.t[0].H == 0 || (start && R == 0)) return HCA_OK;
+  return cuda_status(norm_rope(a, static_cast<cudaStream_t>(stream)));
 }
 
 // ---------------------------------------------------------------------------

@@ -12,7 +12,7 @@ namespace hca {
 enum KernelId {
   kKPrep = 0, kKFwdTc, kKBwdDq, kKBwdDkv, kKBwdReduce, kKSimtFwd, kKSimtBwd, kKVisibility, kKCompress,
   kKIndexScore, kKIndexTopk, kKCsaUnion, kKCsaDckv, kKCachePlan, kKCacheAppend, kKCacheSched, kKCacheAttn,
-  kKCacheSimt, kKCacheCombine, kNumKernels
+  kKCacheSimt, kKCacheCombine, kKNormRope, kKNormRopeBwd, kNumKernels
 };
 
 // Brackets the launches issued during its lifetime with CUDA events on `st`
@@ -88,6 +88,28 @@ cudaError_t compress_fwd(const void *x, const float *g, const float *bias, const
 cudaError_t compress_bwd(const void *x, const float *g, const float *bias, const int32_t *seg, const void *dckv,
                          void *dx, float *dg, float *dbias, float *dz, int B, int S, int D, int m, int dtype,
                          cudaStream_t st);
+
+// Norms of queries and kv rows with positions, and the rotation alone (hca_norm_rope.cu)
+struct NormRopeTensor {
+  const void *x, *g;  // rows, cotangents of the outputs (backward)
+  void *y;            // outputs, or gradients of the rows
+  const float *w;     // [D] or NULL
+  float *dw;          // [D] or NULL (backward)
+  int H;              // 0: no such tensor
+  int64_t xb, xh, xs, gb, gh, gs, yb, yh, ys;  // strides of batch rows, heads and positions in elements
+};
+struct NormRopeArgs {
+  NormRopeTensor t[2];         // queries, kv
+  const int32_t *pos;          // [axes,B,S] or NULL
+  const int32_t *start, *held; // packed tokens of R requests (B = 1) or NULL
+  const float *freq;           // [axes,rot/2]
+  float *part;                 // workspace [kNormRopeParts][2][D] (backward)
+  int B, S, D, R, axes, first, rot, halves, inverse, dtype;
+  int mode;                    // 0 rotation alone (t[0]), 1 forward, 2 backward
+  float eps;
+};
+constexpr int kNormRopeParts = 1024;
+cudaError_t norm_rope(const NormRopeArgs &a, cudaStream_t st);
 
 // Lightning Indexer (hca_indexer.cu)
 struct IndexerArgs {

@@ -35,7 +35,8 @@ EXPORTS = ("hca_status_string", "hca_version", "hca_workspace_size", "hca_query_
            "hca_compress_fwd", "hca_compress_workspace_size", "hca_compress_bwd", "hca_indexer_workspace_size",
            "hca_indexer_topk", "hca_csa_workspace_size", "hca_csa_attn_fwd", "hca_csa_attn_bwd",
            "hca_cache_plan_workspace_size", "hca_cache_plan", "hca_cache_append_workspace_size", "hca_cache_append",
-           "hca_cache_attn_workspace_size", "hca_cache_attn")
+           "hca_cache_attn_workspace_size", "hca_cache_attn", "hca_norm_rope_fwd", "hca_norm_rope_workspace_size",
+           "hca_norm_rope_bwd", "hca_rope")
 
 # failure-path test hooks (hca_test_inject)
 INJECT_RESET, INJECT_LAUNCH_FAILURE, INJECT_STALL, INJECT_WAIT_LIMIT_NS, INJECT_CSA_UNION = 0, 1, 2, 3, 4
@@ -131,6 +132,14 @@ def load(path: str = LIB_PATH):
             lib.hca_cache_attn_workspace_size.restype = Z
             lib.hca_cache_attn.argtypes = [P, P, P, P, P, P, I, I, P, P, P, I, I, P, P, I, I, I, I, I, I, I, F, I, P, Z, P]
             lib.hca_cache_attn.restype = I
+            lib.hca_norm_rope_fwd.argtypes = [P] * 12 + [I] * 9 + [F, I, P]
+            lib.hca_norm_rope_fwd.restype = I
+            lib.hca_norm_rope_workspace_size.argtypes = [I]
+            lib.hca_norm_rope_workspace_size.restype = Z
+            lib.hca_norm_rope_bwd.argtypes = [P] * 16 + [I] * 8 + [F, I, P, Z, P]
+            lib.hca_norm_rope_bwd.restype = I
+            lib.hca_rope.argtypes = [P] * 8 + [I] * 11 + [P]
+            lib.hca_rope.restype = I
             py = _extension()
             if py is not None:
                 py.bind(*(ctypes.cast(getattr(lib, f), P).value for f in (
@@ -533,6 +542,154 @@ def hca_csa_attn_bwd(q, kv, ckv, seg, sel, out, lse, dout, W: int, m: int, scale
 
 
 # ---------------------------------------------------------------------------
+# norms and positions
+# ---------------------------------------------------------------------------
+def _rows(t: torch.Tensor, name: str, shape, dtype, device, written: bool = False):
+    """Pointer and strides (elements; NULL where contiguous) of a tensor whose
+    rows' columns are adjacent."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    st = t.stride()[:-1]
+    return t.data_ptr(), (ctypes.c_int64 * len(st))(*st)
+
+
+def _angles(pos, freq, lead, dev):
+    """(pos pointer, freq pointer, axes, rot) for tokens of shape `lead`: pos
+    [*lead] or [axes, *lead] int32 or None, freq [rot/2] or [axes, rot/2] fp32."""
+    if freq is None:
+        raise ValueError("freq is required")
+    if freq.dim() not in (1, 2):
+        raise ValueError("freq must be [rot/2] or [axes,rot/2]")
+    axes = freq.shape[0] if freq.dim() == 2 else 1
+    _need(freq, "freq", freq.shape, torch.float32, dev)
+    if pos is not None:
+        _need(pos, "pos", lead if axes == 1 and pos.dim() == len(lead) else (axes, *lead), torch.int32, dev)
+    elif axes > 1:
+        raise ValueError("pos is required for more than one axis")
+    return _pp(pos), freq.data_ptr(), axes, 2 * freq.shape[-1]
+
+
+def _pp(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _weight(w, name: str, D: int, dev):
+    if w is not None:
+        _need(w, name, (D,), torch.float32, dev)
+    return _pp(w)
+
+
+def _norm_rope_sizes(q, kv):
+    """(B, H, S, D, dtype, device) of q[B,H,S,D] and kv[B,S,D], either of which may be None."""
+    t = q if q is not None else kv
+    if t is None:
+        raise ValueError("q or kv is required")
+    if (q is not None and q.dim() != 4) or (kv is not None and kv.dim() != 3):
+        raise ValueError("q must be [B,H,S,D] and kv [B,S,D]")
+    B, S, D = t.shape[0], t.shape[-2], t.shape[-1]
+    if t.device.type != "cuda":
+        raise ValueError(f"the calls work on CUDA tensors, not on {t.device}")
+    return B, (q.shape[1] if q is not None else 0), S, D, t.dtype, t.device
+
+
+def hca_norm_rope_fwd(q: Optional[torch.Tensor], kv: Optional[torch.Tensor], wq: Optional[torch.Tensor],
+                      wkv: Optional[torch.Tensor], pos: Optional[torch.Tensor], freq: torch.Tensor, eps: float,
+                      first: Optional[int] = None, halves: bool = False, qo: Optional[torch.Tensor] = None,
+                      kvo: Optional[torch.Tensor] = None):
+    """Norms of each head of q[B,H,S,D] and of kv[B,S,D] (bf16 or fp32; any
+    strides with adjacent columns, such as a projection's [B,S,H,D] seen as
+    [B,H,S,D]) and the rotation of columns [first, first + rot) (the last ones
+    by default): (qo[B,H,S,D], kvo[B,S,D]), contiguous.  wq, wkv [D] fp32 or
+    None; pos [B,S] or [axes,B,S] int32 (None: 0 .. S - 1); freq [rot/2] or
+    [axes,rot/2] fp32 (include/hca.h, hca_norm_rope_fwd).  q or kv may be None."""
+    lib = load()
+    B, H, S, D, dt, dev = _norm_rope_sizes(q, kv)
+    pp, fp, axes, rot = _angles(pos, freq, (B, S), dev)
+    args = []
+    for x, w, y, name, shape in ((q, wq, qo, "q", (B, H, S, D)), (kv, wkv, kvo, "kv", (B, S, D))):
+        if x is None:
+            args += [None, None, None, None]
+            continue
+        y = torch.empty(shape, dtype=dt, device=dev) if y is None else y
+        _need(y, name + "o", shape, dt, dev)
+        args += [*_rows(x, name, shape, dt, dev), _weight(w, "w" + name, D, dev), y.data_ptr()]
+        if name == "q":
+            qo = y
+        else:
+            kvo = y
+    with _on(dev):
+        rc = lib.hca_norm_rope_fwd(*args, pp, fp, None, None, B, H, S, D, 0, axes, _int(D - rot if first is None else first), rot, int(halves),
+                                   eps, _dtype_code(q if q is not None else kv), _stream(dev))
+    _check(rc, "hca_norm_rope_fwd")
+    return (qo if q is not None else None), (kvo if kv is not None else None)
+
+
+def hca_norm_rope_bwd(q, kv, wq, wkv, pos, freq, eps: float, dqo, dkvo, first: Optional[int] = None, halves: bool = False, dq=None,
+                      dkv=None, dwq=None, dwkv=None, ws: Optional[torch.Tensor] = None):
+    """Backward of hca_norm_rope_fwd for the cotangents dqo[B,H,S,D] and
+    dkvo[B,S,D] (contiguous): (dq, dkv, dwq, dwkv), dq and dkv laid out as q and
+    kv are, None where there is no q, kv or weight."""
+    lib = load()
+    B, H, S, D, dt, dev = _norm_rope_sizes(q, kv)
+    pp, fp, axes, rot = _angles(pos, freq, (B, S), dev)
+    args, res = [], []
+    for x, w, g, dx, dw, name, shape in ((q, wq, dqo, dq, dwq, "q", (B, H, S, D)), (kv, wkv, dkvo, dkv, dwkv, "kv", (B, S, D))):
+        if x is None:
+            args += [None] * 7
+            res.append((None, None))
+            continue
+        _need(g, f"d{name}o", shape, dt, dev)
+        px = _rows(x, name, shape, dt, dev)
+        if dx is None:
+            dx = torch.empty_like(x) if 0 not in x.stride() else torch.empty(shape, dtype=dt, device=dev)
+        if w is None and dw is not None:
+            raise ValueError(f"dw{name} is the gradient of w{name}, which is None")
+        dw = torch.empty(D, dtype=torch.float32, device=dev) if dw is None and w is not None else dw
+        args += [*px, _weight(w, "w" + name, D, dev), g.data_ptr(), *_rows(dx, "d" + name, shape, dt, dev),
+                 _weight(dw, "dw" + name, D, dev)]
+        res.append((dx, dw))
+    if ws is None:
+        ws = torch.empty(lib.hca_norm_rope_workspace_size(D), dtype=torch.uint8, device=dev)
+    with _on(dev):
+        rc = lib.hca_norm_rope_bwd(*args, pp, fp, B, H, S, D, axes, _int(D - rot if first is None else first), rot, int(halves), eps,
+                                   _dtype_code(q if q is not None else kv), *_scratch(ws, dev), _stream(dev))
+    _check(rc, "hca_norm_rope_bwd")
+    return res[0][0], res[1][0], res[0][1], res[1][1]
+
+
+def hca_rope(x: torch.Tensor, pos: Optional[torch.Tensor], freq: torch.Tensor, inverse: bool = False,
+             first: Optional[int] = None, halves: bool = False, y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The rotation alone of x[B,H,S,D]: y[B,H,S,D] (any strides with adjacent
+    columns for both; y may be x).  ``inverse`` turns back, as the attention's
+    output has to be before the output projection; it is also the gradient of
+    the call without it, and the other way round."""
+    lib = load()
+    if x.dim() != 4:
+        raise ValueError("x must be [B,H,S,D]")
+    B, H, S, D = x.shape
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError(f"the calls work on CUDA tensors, not on {dev}")
+    pp, fp, axes, rot = _angles(pos, freq, (B, S), dev)
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if y is None else y
+    with _on(dev):
+        rc = lib.hca_rope(*_rows(x, "x", x.shape, x.dtype, dev), *_rows(y, "y", x.shape, x.dtype, dev), pp, fp, None, None, B, H, S, D,
+                          0, axes, _int(D - rot if first is None else first), rot, int(halves), int(inverse), _dtype_code(x), _stream(dev))
+    _check(rc, "hca_rope")
+    return y
+
+
+# ---------------------------------------------------------------------------
 # serving: plan, append and attend over a paged 8-bit cache
 #
 # A decode step's kernels take a few microseconds each, so what these calls do
@@ -710,3 +867,76 @@ def hca_cache_attn(q: torch.Tensor, start: torch.Tensor, held: torch.Tensor, raw
     if check:
         _check(hca_workspace_status(ws), "hca_cache_attn (device)")
     return out, lse
+
+
+def _packed(t: torch.Tensor, name: str, shape, dtype, dev):
+    """Pointer and strides of packed rows [N,H,D] or [N,D] as the C functions take them."""
+    p, st = _rows(t, name, shape, dtype, dev)
+    if st is None:
+        return p, None
+    return p, (ctypes.c_int64 * 3)(0, st[1], st[0]) if len(shape) == 3 else (ctypes.c_int64 * 2)(0, st[0])
+
+
+def _packed_requests(start, held, pos, dev):
+    if start.dim() != 1 or start.shape[0] < 1:
+        raise ValueError("start must be [R+1]")
+    R = start.shape[0] - 1
+    if held is None and pos is None:
+        raise ValueError("held or pos is required")
+    return _fits(start, "start", (R + 1,), _I32, dev), None if held is None else _fits(held, "held", (R,), _I32, dev), R
+
+
+def hca_cache_norm_rope(q: Optional[torch.Tensor], kv: Optional[torch.Tensor], start: torch.Tensor, held: Optional[torch.Tensor],
+                        wq: Optional[torch.Tensor], wkv: Optional[torch.Tensor], freq: torch.Tensor, eps: float,
+                        first: Optional[int] = None, halves: bool = False, pos: Optional[torch.Tensor] = None,
+                        qo: Optional[torch.Tensor] = None, kvo: Optional[torch.Tensor] = None):
+    """hca_norm_rope_fwd for a serving step's packed tokens: q[N,H,D] and kv[N,D]
+    of the requests that hca_cache_attn takes by start[R+1] and held[R]; pos
+    [N] or [axes,N] int32 replaces the positions held[r], held[r] + 1, ...  Rows
+    of the results from start[R] on are left as they are.  Returns (qo, kvo)."""
+    lib = _lib or load()
+    t = q if q is not None else kv
+    if t is None:
+        raise ValueError("q or kv is required")
+    if (q is not None and q.dim() != 3) or (kv is not None and kv.dim() != 2):
+        raise ValueError("q must be [N,H,D] and kv [N,D]")
+    N, D, dev, dt = t.shape[0], t.shape[-1], t.device, t.dtype
+    H = q.shape[1] if q is not None else 0
+    ps, ph, R = _packed_requests(start, held, pos, dev)
+    pp, fp, axes, rot = _angles(pos, freq, (N,), dev)
+    args = []
+    for x, w, y, name, shape in ((q, wq, qo, "q", (N, H, D)), (kv, wkv, kvo, "kv", (N, D))):
+        if x is None:
+            args += [None, None, None, None]
+            continue
+        y = torch.empty(shape, dtype=dt, device=dev) if y is None else y
+        args += [*_packed(x, name, shape, dt, dev), _weight(w, "w" + name, D, dev), _fits(y, name + "o", shape, dt, dev)]
+        if name == "q":
+            qo = y
+        else:
+            kvo = y
+    rc = _enqueue(dev, lib.hca_norm_rope_fwd, *args, pp, fp, ps, ph, 1, H, N, D, R, axes, _int(D - rot if first is None else first), rot,
+                  int(halves), eps, _dtype_code(t))
+    if rc != 0:
+        _check(rc, "hca_cache_norm_rope")
+    return (qo if q is not None else None), (kvo if kv is not None else None)
+
+
+def hca_cache_rope(x: torch.Tensor, start: torch.Tensor, held: Optional[torch.Tensor], freq: torch.Tensor, inverse: bool = False,
+                   first: Optional[int] = None, halves: bool = False, pos: Optional[torch.Tensor] = None,
+                   y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """hca_rope for a serving step's packed tokens x[N,H,D] (arguments as
+    hca_cache_norm_rope); y may be x."""
+    lib = _lib or load()
+    if x.dim() != 3:
+        raise ValueError("x must be [N,H,D]")
+    N, H, D = x.shape
+    dev = x.device
+    ps, ph, R = _packed_requests(start, held, pos, dev)
+    pp, fp, axes, rot = _angles(pos, freq, (N,), dev)
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if y is None else y
+    rc = _enqueue(dev, lib.hca_rope, *_packed(x, "x", x.shape, x.dtype, dev), *_packed(y, "y", x.shape, x.dtype, dev), pp, fp, ps, ph, 1, H,
+                  N, D, R, axes, _int(D - rot if first is None else first), rot, int(halves), int(inverse), _dtype_code(x))
+    if rc != 0:
+        _check(rc, "hca_cache_rope")
+    return y

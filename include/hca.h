@@ -238,6 +238,67 @@ HCA_API int hca_compress_bwd(const void *x, const float *g, const float *bias, c
                              int B, int S, int D, int m, int dtype,
                              void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Norms and positions --------------------------------------------------
+ *
+ * What stands between a layer's projections and its attention.  The pages take
+ * q and kv as they come; these calls are this library's own.  For a row x of D
+ * columns, a token's coordinates c_a and frequencies f[a][p] of the pairs p:
+ *   y = x (mean(x^2) + eps)^-1/2 w                       (w NULL: 1)
+ *   theta_p = sum_a c_a f[a][p]
+ *   (u, v) -> (u cos theta_p - v sin theta_p, u sin theta_p + v cos theta_p)
+ * for the two columns u, v of pair p of y; the columns outside [first, first +
+ * rot) stay as they are.  Pair p is columns first + 2p and first + 2p + 1, or
+ * with `halves` first + p and first + p + rot/2.
+ *   freq   [axes,rot/2] fp32 (device), radians per unit, below 2^32 in
+ *          magnitude; angles are right to 2^-24 for any coordinates
+ *   pos    [axes,B,S] int32 (device): the coordinates.  NULL (axes = 1): 0, 1,
+ *          ... S - 1 in every batch row, or those of start and held
+ *   start, held   NULL, or the packed form of a serving step: B = 1 and tensors
+ *          are [N,H,D] and [N,D] with N = S; token start[r] + t of request r
+ *          (device int32 [R+1], [R], ascending) is at position held[r] + t unless
+ *          pos says otherwise, and rows from start[R] on are left as they are.
+ *          held may be NULL where pos is given.  Values out of order give
+ *          positions that mean nothing; no row outside [0, N) is touched.
+ *   dtype  of x and of the results; w, freq and dw are fp32, and so is all
+ *          arithmetic, rounded once at the end.  Squares are summed in fp32:
+ *          |x| below 2^60, and above 2^-60 somewhere in a row where eps is 0.
+ * D, first and rot are multiples of 8 (rot of 16 with halves; 0: no rotation),
+ * D at most 512, axes 1 to 4, eps finite and not negative.  *_strides are host
+ * arrays with the elements from one batch row, head (not for kv) and position to
+ * the next, multiples of 16 bytes and not negative, NULL for contiguous tensors;
+ * a row's columns are adjacent.  Results may be the inputs themselves (same
+ * pointer and strides), but not overlap them otherwise. */
+
+/* qo[B,H,S,D] from q and kvo[B,S,D] from kv (contiguous), the norm of each row
+ * and its rotation; q or kv may be NULL (H is then not used for kv alone).
+ * H heads of q are normalised one by one with the same wq [D].  No workspace. */
+HCA_API int hca_norm_rope_fwd(const void *q, const int64_t *q_strides, const float *wq, void *qo, const void *kv,
+                              const int64_t *kv_strides, const float *wkv, void *kvo, const int32_t *pos,
+                              const float *freq, const int32_t *start, const int32_t *held, int B, int H, int S, int D,
+                              int R, int axes, int first, int rot, int halves, float eps, int dtype, void *stream);
+
+/* Backward of hca_norm_rope_fwd (without start) for the cotangents dqo[B,H,S,D]
+ * and dkvo[B,S,D] (contiguous): dq and dkv with strides of their own, and dwq,
+ * dwkv [D] fp32, summed over all rows in a fixed order (NULL: not wanted; with
+ * wq, wkv only).  Everything is fully overwritten.  Workspace:
+ * hca_norm_rope_workspace_size(D) bytes. */
+HCA_API size_t hca_norm_rope_workspace_size(int D);
+HCA_API int hca_norm_rope_bwd(const void *q, const int64_t *q_strides, const float *wq, const void *dqo, void *dq,
+                              const int64_t *dq_strides, float *dwq, const void *kv, const int64_t *kv_strides,
+                              const float *wkv, const void *dkvo, void *dkv, const int64_t *dkv_strides, float *dwkv,
+                              const int32_t *pos, const float *freq, int B, int H, int S, int D, int axes, int first,
+                              int rot, int halves, float eps, int dtype, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/* The rotation alone: y[B,H,S,D] from x[B,H,S,D], by minus the angles with
+ * `inverse`.  kv is key and value at once, so the attention's output is a sum of
+ * rows rotated by their positions; hca_rope with `inverse` turns each head's
+ * output by its query's own, which leaves the differences.  The gradient of the
+ * call is the call with `inverse` the other way. */
+HCA_API int hca_rope(const void *x, const int64_t *x_strides, void *y, const int64_t *y_strides, const int32_t *pos,
+                     const float *freq, const int32_t *start, const int32_t *held, int B, int H, int S, int D, int R,
+                     int axes, int first, int rot, int halves, int inverse, int dtype, void *stream);
+
 /* Lightning Indexer with top-k selection, the step that feeds CSA
  * ("[DeepSeek-V4] Implement Compressed Attention Layers": the indexer's
  * per-head scores are the matmul of its queries with the transposed
