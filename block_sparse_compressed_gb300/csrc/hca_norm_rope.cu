@@ -52,43 +52,61 @@ struct Args {
   int splits, per;      // head ranges of a tile, heads (of q, then kv) of a range
 };
 
+// 8 columns of a row as they are in memory, and as 4 packed pairs of fp32.  With
+// neighbours for pairs of a rotation the packed ones are (0, 2), (4, 6), (1, 3),
+// (5, 7), so that the two columns of a rotation lie in slots i and i ^ 2, which
+// costs bf16 nothing: its halves are taken apart in any case.
+template <bool HALVES>
+__device__ __forceinline__ constexpr int column(int slot, int e) {
+  return HALVES ? 2 * slot + e : (slot & 1) * 4 + 2 * e + (slot >> 1);
+}
+
 template <typename T>
-struct Vec {  // 8 columns
+struct Vec {
   static constexpr int kWords = sizeof(T) * 2;
   uint32_t w[kWords];
-  __device__ __forceinline__ void load(const T *p) {
-    const uint4 *v = reinterpret_cast<const uint4 *>(p);
-#pragma unroll
-    for (int i = 0; i < kWords / 4; ++i) {
-      const uint4 u = v[i];
-      w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
-    }
+  __device__ __forceinline__ void piece(int i, const uint4 &u) {
+    w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
   }
-  __device__ __forceinline__ void zero() {
+  __device__ __forceinline__ void store(T *p) const {
+    uint4 *v = reinterpret_cast<uint4 *>(p);
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = 0;
+    for (int i = 0; i < kWords / 4; ++i) v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    if constexpr (sizeof(T) == 4) {
+  // the same columns of the row's lane `from`
+  __device__ __forceinline__ Vec of(int from) const {
+    Vec r;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
-    } else {
+    for (int i = 0; i < kWords; ++i) r.w[i] = __shfl_sync(0xffffffffu, w[i], from);
+    return r;
+  }
+  __device__ __forceinline__ uint32_t at(int c) const {
+    if constexpr (sizeof(T) == 4) return w[c];
+    else return c & 1 ? w[c >> 1] & 0xffff0000u : w[c >> 1] << 16;
+  }
+  template <bool HALVES>
+  __device__ __forceinline__ void get(uint64_t (&f)[4]) const {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
+    for (int i = 0; i < 4; ++i) f[i] = tc::f32x2(at(column<HALVES>(i, 0)), at(column<HALVES>(i, 1)));
+  }
+  template <bool HALVES>
+  __device__ __forceinline__ void put(const uint64_t (&f)[4]) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tc::f32x2_split(f[i], v[column<HALVES>(i, 0)], v[column<HALVES>(i, 1)]);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
+      else w[i] = tc::pack_bf16x2(v[2 * i], v[2 * i + 1]);
     }
   }
 };
 
-__device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&f)[8]) {
-  *reinterpret_cast<uint4 *>(p) = make_uint4(tc::pack_bf16x2(f[0], f[1]), tc::pack_bf16x2(f[2], f[3]),
-                                             tc::pack_bf16x2(f[4], f[5]), tc::pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint64_t pair(float a, float b) { return tc::f32x2(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ float total(uint64_t v) {
+  float a, b;
+  tc::f32x2_split(v, a, b);
+  return a + b;
 }
 
 // f / 2pi of a turn per unit as a 64-bit fraction
@@ -119,10 +137,13 @@ __device__ __forceinline__ float2 cos_sin(unsigned long long phase, float sign) 
   return make_float2(c, s * sign);
 }
 
-// a^-1/2, correct to an ulp
+// a^-1/2: of fp32 rows correct to an ulp, of bf16 rows to 2^-22
+template <typename T>
 __device__ __forceinline__ float inv_sqrt(float a) {
-  const float y = rsqrtf(a);
-  return a < 1e38f && a > 1e-37f ? fmaf(0.5f * y, fmaf(-a * y, y, 1.f), y) : y;
+  float y;
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(a));
+  if constexpr (sizeof(T) == 4) return a < 1e38f && a > 1e-37f ? fmaf(0.5f * y, fmaf(-a * y, y, 1.f), y) : y;
+  return y;
 }
 
 // Request of token t: start[r] <= t < start[r + 1], r in [0, R) whatever they hold
@@ -135,19 +156,37 @@ __device__ __forceinline__ int request_of(const int32_t *start, int R, int t) {
   return lo;
 }
 
-template <int CH>
-struct Turn {
-  float c[CH][8], s[CH][8];  // halves: of each column; interleaved: of pair k in [k], k < 4
+// A thread's rows come through shared memory, its own 16-byte pieces in kStages
+// slots that only it writes (asynchronously) and reads, so nothing waits but the
+// thread itself.
+template <typename T, int CH, int MODE>
+struct Ring {
+  static constexpr int kPieces = CH * (int)(sizeof(T) / 2) * (MODE == kBwd ? 2 : 1);  // of a row
+  static constexpr int kStages = kPieces <= 4 ? 8 / kPieces : 2;
+  static constexpr int kBytes = kStages * kPieces * kThreads * 16;
 };
 
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *p, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <typename T, int L, int CH, int MODE, bool HALVES>
-__global__ void __launch_bounds__(kThreads) hca_norm_rope_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MODE == kBwd ? 3 : 4) hca_norm_rope_kernel(const Args a) {
+  using R = Ring<T, CH, MODE>;
   constexpr int kRows = kThreads / L;  // rows of a pass
-  constexpr int kBatch = CH > 1 || MODE == kBwd ? 2 : 4;  // rows of a lane in flight
+  constexpr int kVec = (int)(sizeof(T) / 2);  // pieces of 8 columns
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, l = tid % L, group = tid / L;
   const int np = a.rot / 2, row_lanes = lane & ~(L - 1);
-  unsigned long long *sh_freq = reinterpret_cast<unsigned long long *>(smem);   // [axes][np]
+  const uint32_t ring = tc::smem_u32(smem) + 16 * tid;
+  float4 *sh_dw = reinterpret_cast<float4 *>(smem + R::kBytes);                 // [2][CH * 2][kThreads] (backward)
+  unsigned long long *sh_freq =
+      reinterpret_cast<unsigned long long *>(smem + R::kBytes + (MODE == kBwd ? 2 * CH * 2 * kThreads * 16 : 0));  // [axes][np]
   float2 *sh_cs = reinterpret_cast<float2 *>(sh_freq + a.axes * np);            // [tile][np]
   long long *sh_pos = reinterpret_cast<long long *>(sh_cs + a.tile * np);       // [tile] positions from start and held
   int *sh_req = reinterpret_cast<int *>(sh_pos + a.tile);                       // [2][R + 1] starts and held
@@ -167,9 +206,8 @@ __global__ void __launch_bounds__(kThreads) hca_norm_rope_kernel(const Args a) {
   }
 
   // columns of the lane
-  bool mine[CH], turned[CH];
+  bool mine[CH], turned[CH], upper[CH];
   int partner[CH], pair0[CH];
-  bool upper[CH];
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     const int c = l + k * L, z = 8 * c - a.first;  // chunk, its first column among the rotated ones
@@ -179,14 +217,9 @@ __global__ void __launch_bounds__(kThreads) hca_norm_rope_kernel(const Args a) {
     pair0[k] = HALVES ? (upper[k] ? z - np : z) : z / 2;
     partner[k] = turned[k] && HALVES ? (upper[k] ? c - np / 8 : c + np / 8) : c;
   }
-  float dw[2][CH][8];
   if constexpr (MODE == kBwd) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int k = 0; k < CH; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dw[i][k][j] = 0.f;
+    for (int i = 0; i < 4 * CH; ++i) sh_dw[i * kThreads + tid] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   const float inv_d = 1.f / (float)a.D;
 
@@ -196,189 +229,236 @@ __global__ void __launch_bounds__(kThreads) hca_norm_rope_kernel(const Args a) {
     const int per_row = (a.S + a.tile - 1) >> a.log_tile;
     const int b = (int)(tile / per_row), s0 = (int)(tile % per_row) << a.log_tile;
     if (s0 >= live) continue;
+    const int s = s0 + token;
+    const bool alive = s < live;
+    // heads of the block's range: of queries, then of kv
+    const int lo0 = split * a.per, hi0 = min(lo0 + a.per, a.t[0].H);
+    const int lo1 = max(lo0 - a.t[0].H, 0), hi1 = min(lo0 + a.per - a.t[0].H, a.t[1].H);
+    const int n0 = max((hi0 - lo0 + head_step - 1) / head_step, 0);
+    const int steps = n0 + (MODE == kRope ? 0 : max((hi1 - lo1 + head_step - 1) / head_step, 0));
+
+    // row `n` of the thread's: its pieces on their way to slot n % kStages
+    auto issue = [&](int n) {
+      if (n < steps) {
+        const bool kv = MODE != kRope && n >= n0;
+        const NormRopeTensor &t = a.t[kv];
+        const int h = (kv ? lo1 + (n - n0) * head_step : lo0 + n * head_step) + head0;
+        const bool row = alive && h < (kv ? hi1 : hi0);
+        const T *x = static_cast<const T *>(t.x), *g = static_cast<const T *>(t.g);
+        if (row) {
+          x += b * t.xb + s * t.xs + h * t.xh + 8 * l;
+          if constexpr (MODE == kBwd) g += b * t.gb + s * t.gs + h * t.gh + 8 * l;
+        }
+        const uint32_t to = ring + (n % R::kStages) * (R::kPieces * kThreads * 16);
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+          const bool there = row && mine[k];
+#pragma unroll
+          for (int v = 0; v < kVec; ++v) {
+            const int at = there ? 8 * k * L + v * (16 / (int)sizeof(T)) : 0;
+            cp_async_16(to + (k * kVec + v) * (kThreads * 16), x + at, there ? 16 : 0);
+            if constexpr (MODE == kBwd) cp_async_16(to + ((CH + k) * kVec + v) * (kThreads * 16), g + at, there ? 16 : 0);
+          }
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll 1
+    for (int n = 0; n < R::kStages; ++n) issue(n);
+
     __syncthreads();  // sh_cs may still be read; sh_freq and sh_req are written
     if (a.start && !a.pos) {
       if (tid < a.tile) {
-        const int s = s0 + tid, r = request_of(listed ? sh_req : a.start, a.R, s);
-        sh_pos[tid] = listed ? (long long)sh_req[a.R + 1 + r] + s - sh_req[r] : (long long)a.held[r] + s - a.start[r];
+        const int t = s0 + tid, r = request_of(listed ? sh_req : a.start, a.R, t);
+        sh_pos[tid] = listed ? (long long)sh_req[a.R + 1 + r] + t - sh_req[r] : (long long)a.held[r] + t - a.start[r];
       }
       __syncthreads();
     }
     for (int i = tid; i < a.tile * np; i += kThreads) {
-      const int t = i / np, p = i - t * np, s = s0 + t;
+      const int t = i / np, p = i - t * np, at = s0 + t;
       unsigned long long phase = 0;
-      if (s < live) {
+      if (at < live) {
         if (a.pos) {
           for (int x = 0; x < a.axes; ++x)
-            phase += (unsigned long long)(long long)a.pos[((size_t)x * a.B + b) * a.S + s] * sh_freq[x * np + p];
+            phase += (unsigned long long)(long long)a.pos[((size_t)x * a.B + b) * a.S + at] * sh_freq[x * np + p];
         } else {
-          phase = (unsigned long long)(a.start ? sh_pos[t] : s) * sh_freq[p];
+          phase = (unsigned long long)(a.start ? sh_pos[t] : at) * sh_freq[p];
         }
       }
       sh_cs[i] = cos_sin(phase, a.sign);
     }
     __syncthreads();
-    Turn<CH> turn;
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-#pragma unroll
-      for (int j = 0; j < (HALVES ? 8 : 4); ++j) {
-        const float2 v = turned[k] ? sh_cs[token * np + pair0[k] + j] : make_float2(1.f, 0.f);
-        turn.c[k][j] = v.x;
-        turn.s[k][j] = HALVES && !upper[k] ? -v.y : v.y;
-      }
-    }
-    const int s = s0 + token;
-    const bool alive = s < live;
 
-    // in place: (u, v) of each pair turned by the angle (by minus it for back)
-    auto rotate = [&](float (&f)[CH][8], auto back) {
-      constexpr float kSign = decltype(back)::value ? -1.f : 1.f;
-      if constexpr (HALVES) {
-        float o[CH][8];
-#pragma unroll
-        for (int k = 0; k < CH; ++k) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float p;
-            if constexpr (CH == 1) {
-              p = __shfl_sync(0xffffffffu, f[0][j], row_lanes + partner[0]);
-            } else {
-              // the partner may be in the other chunk of its lane
-              const float p0 = __shfl_sync(0xffffffffu, f[0][j], partner[k] & 31), p1 = __shfl_sync(0xffffffffu, f[1][j], partner[k] & 31);
-              p = partner[k] >= 32 ? p1 : p0;
-            }
-            o[k][j] = turned[k] ? fmaf(f[k][j], turn.c[k][j], kSign * p * turn.s[k][j]) : f[k][j];
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < CH; ++k)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[k][j] = o[k][j];
-      } else {
-#pragma unroll
-        for (int k = 0; k < CH; ++k) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float u = f[k][2 * j], v = f[k][2 * j + 1], c = turn.c[k][j], sn = kSign * turn.s[k][j];
-            if (turned[k]) {
-              f[k][2 * j] = fmaf(u, c, -v * sn);
-              f[k][2 * j + 1] = fmaf(v, c, u * sn);
-            }
-          }
-        }
-      }
-    };
-
+    int n = 0;
 #pragma unroll
     for (int which = 0; which < (MODE == kRope ? 1 : 2); ++which) {
       const NormRopeTensor &t = a.t[which];
-      // heads of the block's range
-      const int base = which ? a.t[0].H : 0;
-      const int h_lo = max(split * a.per - base, 0), h_hi = min(min((split + 1) * a.per, base + t.H) - base, t.H);
-      if (h_lo >= h_hi) continue;
-      const T *x = static_cast<const T *>(t.x) + b * t.xb + s * t.xs + 8 * l;
-      const T *g = MODE == kBwd ? static_cast<const T *>(t.g) + b * t.gb + s * t.gs + 8 * l : nullptr;
+      const int end = which ? steps : n0;
+      if (n >= end) continue;
       T *y = static_cast<T *>(t.y) + b * t.yb + s * t.ys + 8 * l;
-      float w[CH][8];
-      if constexpr (MODE != kRope) {
+      // What a column and its partner count in a rotated column (backwards: turned
+      // back).  Forwards the weights are in them.
+      uint64_t own[CH][4], other[CH][4], w[CH][4], dw[CH][4];
 #pragma unroll
-        for (int k = 0; k < CH; ++k)
+      for (int k = 0; k < CH; ++k) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) w[k][j] = t.w && mine[k] ? t.w[8 * (l + k * L) + j] : 1.f;
-      }
-#pragma unroll 1
-      for (int h0 = h_lo; h0 < h_hi; h0 += kBatch * head_step) {
-        Vec<T> vx[kBatch][CH], vg[kBatch][CH];
+        for (int i = 0; i < 4; ++i) {
+          float o[2], p[2], wt[2];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int h = h0 + u * head_step + head0;
-#pragma unroll
-          for (int k = 0; k < CH; ++k) {
-            if (alive && h < h_hi && mine[k]) {
-              vx[u][k].load(x + h * t.xh + 8 * k * L);
-              if constexpr (MODE == kBwd) vg[u][k].load(g + h * t.gh + 8 * k * L);
-            } else {
-              vx[u][k].zero();
-              if constexpr (MODE == kBwd) vg[u][k].zero();
+          for (int e = 0; e < 2; ++e) {
+            const int c = column<HALVES>(i, e), z = 8 * (l + k * L) + c;
+            const float2 cs = turned[k] ? sh_cs[token * np + pair0[k] + (HALVES ? c : c >> 1)] : make_float2(1.f, 0.f);
+            const bool second = HALVES ? upper[k] : (c & 1) != 0;
+            o[e] = cs.x;
+            p[e] = (second == (MODE != kBwd)) ? cs.y : -cs.y;
+            wt[e] = 1.f;
+            if (MODE != kRope && t.w && mine[k]) {
+              wt[e] = t.w[z];
+              if (MODE == kFwd) {
+                o[e] *= wt[e];
+                p[e] *= turned[k] ? t.w[HALVES ? 8 * partner[k] + c : z ^ 1] : 0.f;
+              }
             }
           }
+          own[k][i] = pair(o[0], o[1]);
+          other[k][i] = pair(p[0], p[1]);
+          w[k][i] = pair(wt[0], wt[1]);
         }
+        if constexpr (MODE == kBwd) {
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int h = h0 + u * head_step + head0;
-          float f[CH][8];
+          for (int i = 0; i < 2; ++i) {
+            const float4 v = sh_dw[(which * 2 * CH + 2 * k + i) * kThreads + tid];
+            dw[k][2 * i] = pair(v.x, v.y);
+            dw[k][2 * i + 1] = pair(v.z, v.w);
+          }
+        }
+      }
+      // own f + other f of the partner, for a row's slots
+      auto rotate = [&](const Vec<T> (&v)[CH], const uint64_t (&f)[CH][4], uint64_t (&o)[CH][4]) {
 #pragma unroll
-          for (int k = 0; k < CH; ++k) vx[u][k].get(f[k]);
-          if constexpr (MODE == kRope) {
-            rotate(f, std::false_type());
-          } else {
-            float ss = 0.f, hx = 0.f;
-            float gr[CH][8];
-            if constexpr (MODE == kBwd) {
-#pragma unroll
-              for (int k = 0; k < CH; ++k) vg[u][k].get(gr[k]);
-              rotate(gr, std::true_type());
+        for (int k = 0; k < CH; ++k) {
+          uint64_t q[4];
+          if constexpr (HALVES) {
+            Vec<T> p = v[0].of(CH == 1 ? row_lanes + partner[k] : partner[k] & 31);
+            if constexpr (CH > 1) {  // the partner may be in the other chunk of its lane
+              const Vec<T> p1 = v[CH - 1].of(partner[k] & 31);
+              if (partner[k] >= 32) p = p1;
             }
+            p.template get<HALVES>(q);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[k][i] = tc::ffma2(f[k][i], own[k][i], tc::fmul2(HALVES ? q[i] : f[k][i ^ 2], other[k][i]));
+        }
+      };
+      const int lo = which ? lo1 : lo0, hi = which ? hi1 : hi0, first = which ? n0 : 0;
+#pragma unroll 1
+      for (; n < end; ++n) {
+        cp_async_wait<R::kStages - 1>();
+        Vec<T> vx[CH], vg[CH];
+        const uint32_t from = (n % R::kStages) * (R::kPieces * kThreads * 16) + 16 * tid;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+#pragma unroll
+          for (int v = 0; v < kVec; ++v) {
+            vx[k].piece(v, *reinterpret_cast<const uint4 *>(smem + from + (k * kVec + v) * (kThreads * 16)));
+            if constexpr (MODE == kBwd) vg[k].piece(v, *reinterpret_cast<const uint4 *>(smem + from + ((CH + k) * kVec + v) * (kThreads * 16)));
+          }
+        }
+        const int h = lo + (n - first) * head_step + head0;
+        const bool row = alive && h < hi;
+        uint64_t f[CH][4], o[CH][4];
+#pragma unroll
+        for (int k = 0; k < CH; ++k) vx[k].template get<HALVES>(f[k]);
+        if constexpr (MODE == kRope) {
+          rotate(vx, f, o);
+        } else {
+          uint64_t ss = 0, hx = 0, gx[CH][4];
+          if constexpr (MODE == kBwd) {
+            uint64_t g0[CH][4];
+#pragma unroll
+            for (int k = 0; k < CH; ++k) vg[k].template get<HALVES>(g0[k]);
+            rotate(vg, g0, o);
+          }
+#pragma unroll
+          for (int k = 0; k < CH; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              ss = tc::ffma2(f[k][i], f[k][i], ss);
+              if constexpr (MODE == kBwd) {
+                gx[k][i] = tc::fmul2(o[k][i], f[k][i]);
+                hx = tc::ffma2(gx[k][i], w[k][i], hx);
+              }
+            }
+          }
+          float s1 = total(ss), h1 = MODE == kBwd ? total(hx) : 0.f;
+#pragma unroll
+          for (int d = L / 2; d > 0; d >>= 1) {
+            s1 += __shfl_xor_sync(0xffffffffu, s1, d);
+            if constexpr (MODE == kBwd) h1 += __shfl_xor_sync(0xffffffffu, h1, d);
+          }
+          const float r = inv_sqrt<T>(fmaf(s1, inv_d, a.eps));
+          const uint64_t r2 = pair(r, r);
+          if constexpr (MODE == kFwd) {
+            rotate(vx, f, o);
+#pragma unroll
+            for (int k = 0; k < CH; ++k)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[k][i] = tc::fmul2(o[k][i], r2);
+          } else {
+            const float q = -(r * r) * (h1 * inv_d), rw = row ? r : 0.f;
+            const uint64_t q2 = pair(q, q), rw2 = pair(rw, rw);
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                ss = fmaf(f[k][j], f[k][j], ss);
-                if constexpr (MODE == kBwd) hx = fmaf(gr[k][j] * w[k][j], f[k][j], hx);
-              }
-            }
-#pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) {
-              ss += __shfl_xor_sync(0xffffffffu, ss, o);
-              if constexpr (MODE == kBwd) hx += __shfl_xor_sync(0xffffffffu, hx, o);
-            }
-            const float r = inv_sqrt(fmaf(ss, inv_d, a.eps));
-            if constexpr (MODE == kFwd) {
-#pragma unroll
-              for (int k = 0; k < CH; ++k)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[k][j] = f[k][j] * r * w[k][j];
-              rotate(f, std::false_type());
-            } else {
-              const float q = r * r * (hx * inv_d);
-              const bool row = alive && h < h_hi;
-#pragma unroll
-              for (int k = 0; k < CH; ++k) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const float xv = f[k][j], gv = gr[k][j];
-                  if (row) dw[which][k][j] = fmaf(gv * xv, r, dw[which][k][j]);
-                  f[k][j] = r * fmaf(-xv, q, gv * w[k][j]);
-                }
+              for (int i = 0; i < 4; ++i) {
+                dw[k][i] = tc::ffma2(gx[k][i], rw2, dw[k][i]);
+                o[k][i] = tc::fmul2(r2, tc::ffma2(f[k][i], q2, tc::fmul2(o[k][i], w[k][i])));
               }
             }
           }
+        }
 #pragma unroll
-          for (int k = 0; k < CH; ++k)
-            if (alive && h < h_hi && mine[k]) store8(y + h * t.yh + 8 * k * L, f[k]);
+        for (int k = 0; k < CH; ++k) {
+          if (row && mine[k]) {
+            Vec<T> out;
+            out.template put<HALVES>(o[k]);
+            if (MODE == kRope && !turned[k]) out = vx[k];  // as it was, infinities too
+            out.store(y + h * t.yh + 8 * k * L);
+          }
+        }
+        issue(n + R::kStages);
+      }
+      if constexpr (MODE == kBwd) {
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float4 v;
+            tc::f32x2_split(dw[k][2 * i], v.x, v.y);
+            tc::f32x2_split(dw[k][2 * i + 1], v.z, v.w);
+            sh_dw[(which * 2 * CH + 2 * k + i) * kThreads + tid] = v;
+          }
         }
       }
     }
+    cp_async_wait<0>();  // empty groups, but the next item's are counted anew
   }
 
   if constexpr (MODE == kBwd) {
-    // sums of the block's rows: over its row groups in shared memory, in their order
-    float *sum = reinterpret_cast<float *>(smem);  // [kRows][D]
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
+    // sums of the block's rows: over its row groups, in their order
+    __syncthreads();
+    for (int i = tid; i < 2 * a.D; i += kThreads) {
+      const int which = i / a.D, d = i - which * a.D, chunk = d >> 3, c = d & 7;
       if (!a.t[which].dw) continue;
-      __syncthreads();
+      int slot = 0;  // of the column among the lane's 8 floats
 #pragma unroll
-      for (int k = 0; k < CH; ++k)
-        if (mine[k]) store8(sum + (size_t)group * a.D + 8 * (l + k * L), dw[which][k]);
-      __syncthreads();
-      for (int d = tid; d < a.D; d += kThreads) {
-        float v = 0.f;
+      for (int j = 0; j < 8; ++j)
+        if (column<HALVES>(j >> 1, j & 1) == c) slot = j;
+      const float *from = reinterpret_cast<const float *>(sh_dw + (size_t)(which * 2 * CH + 2 * (chunk / L) + (slot >> 2)) * kThreads + chunk % L) + (slot & 3);
+      float v = 0.f;
 #pragma unroll 8
-        for (int i = 0; i < kRows; ++i) v += sum[(size_t)i * a.D + d];
-        a.part[((size_t)blockIdx.x * 2 + which) * a.D + d] = v;
-      }
+      for (int r = 0; r < kRows; ++r) v += from[4 * r * L];
+      a.part[((size_t)blockIdx.x * 2 + which) * a.D + d] = v;
     }
   }
 }
@@ -386,12 +466,12 @@ __global__ void __launch_bounds__(kThreads) hca_norm_rope_kernel(const Args a) {
 // dw from the blocks' sums, in a fixed order: 8 warps take every 8th block each,
 // a lane a column.
 __global__ void __launch_bounds__(kThreads) hca_norm_rope_dw_kernel(const float *part, int n, int D, float *dwq, float *dwkv) {
-  __shared__ float sum[8][32];
+  __shared__ double sum[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.y, d = blockIdx.x * 32 + lane;
   float *dw = which ? dwkv : dwq;
   tc::pdl_wait();
   if (!dw) return;
-  float v = 0.f;
+  double v = 0;
   if (d < D) {
 #pragma unroll 8
     for (int i = warp; i < n; i += 8) v += part[((size_t)i * 2 + which) * D + d];
@@ -400,7 +480,7 @@ __global__ void __launch_bounds__(kThreads) hca_norm_rope_dw_kernel(const float 
   __syncthreads();
   if (warp == 0 && d < D) {
     for (int i = 1; i < 8; ++i) v += sum[i][lane];
-    dw[d] = v;
+    dw[d] = (float)v;
   }
 }
 
@@ -417,14 +497,19 @@ cudaError_t launch(Args &a, cudaStream_t st) {
   const int want = (int)std::min<long long>((4ll * sms + a.tiles - 1) / a.tiles, heads);
   a.per = ((heads + want - 1) / want + pass - 1) / pass * pass;
   a.splits = (heads + a.per - 1) / a.per;
-  size_t smem = 8 * ((size_t)(a.axes + a.tile) * (a.rot / 2) + a.tile);  // 33 KB at most, with the requests
+  using R = Ring<T, CH, MODE>;
+  constexpr int kFixed = R::kBytes + (MODE == kBwd ? 2 * CH * 2 * kThreads * 16 : 0);
+  size_t smem = kFixed + 8 * ((size_t)(a.axes + a.tile) * (a.rot / 2) + a.tile);
   if (a.start && a.R <= kRequestsInSmem) smem += 2 * sizeof(int) * ((size_t)a.R + 1);
-  if (MODE == kBwd) smem = std::max(smem, (size_t)kRows * a.D * sizeof(float));
+  auto *kernel = hca_norm_rope_kernel<T, L, CH, MODE, HALVES>;
+  static tc::SmemAttrOnce attr;
+  cudaError_t e = attr.ensure(reinterpret_cast<const void *>(kernel), kFixed + 34 * 1024);  // the most that the rest takes
+  if (e != cudaSuccess) return e;
   long long grid = a.tiles * a.splits;
-  grid = std::min<long long>(grid, MODE == kBwd ? std::min(kNormRopeParts, 4 * sms) : 1 << 30);
+  grid = std::min<long long>(grid, MODE == kBwd ? std::min(kNormRopeParts, (CH > 1 ? 1 : 3) * sms) : 1 << 30);
   ProfScope prof(MODE == kBwd ? kKNormRopeBwd : kKNormRope, st);
-  hca_norm_rope_kernel<T, L, CH, MODE, HALVES><<<(unsigned)grid, kThreads, smem, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  kernel<<<(unsigned)grid, kThreads, smem, st>>>(a);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (MODE == kBwd && (a.t[0].dw || a.t[1].dw)) {
     e = cache::launch_behind(hca_norm_rope_dw_kernel, dim3((a.D + 31) / 32, 2), kThreads, 0, st, (const float *)a.part, (int)grid, a.D, a.t[0].dw,
