@@ -656,13 +656,11 @@ size_t hca_cache_attn_workspace_size(int N, int R, int H, int D, int dtype) {
   return cache_attn_ws_bytes(N, R, H, D, dtype);
 }
 
-int hca_cache_attn(const void *q, const int32_t *start, const int32_t *held, const void *raw_pool,
-                   const float *raw_scale, const int32_t *raw_table, int raw_blocks, int raw_cols,
-                   const void *comp_pool, const float *comp_scale, const int32_t *comp_table, int comp_blocks,
-                   int comp_cols, void *out, float *lse, int N, int R, int H, int D, int W, int m, int bs, float scale,
-                   int dtype, void *workspace, size_t workspace_bytes, void *stream) {
-  int rc = cache_attn_shape(N, R, H, D, dtype);
-  if (rc != HCA_OK) return rc;
+static int cache_attn_call(const void *q, const int32_t *start, const int32_t *held, const void *raw_pool, const float *raw_scale,
+                           const int32_t *raw_table, int raw_blocks, int raw_cols, const void *comp_pool,
+                           const float *comp_scale, const int32_t *comp_table, int comp_blocks, int comp_cols,
+                           const CacheShare &share, void *out, float *lse, int N, int R, int H, int D, int W, int m, int bs,
+                           float scale, int dtype, void *workspace, size_t workspace_bytes, size_t need, void *stream) {
   if (!std::isfinite(scale) || W < 1 || m < 1 || !block_size_ok(bs)) return HCA_ERR_ARG;
   if (raw_blocks < 0 || raw_cols < 1 || (long long)raw_blocks * bs > 0x7fffffffll) return HCA_ERR_SHAPE;
   if (comp_table && (comp_blocks < 0 || comp_cols < 1 || (long long)comp_blocks * bs > 0x7fffffffll)) return HCA_ERR_SHAPE;
@@ -671,10 +669,11 @@ int hca_cache_attn(const void *q, const int32_t *start, const int32_t *held, con
     if (!q || !start || !held || !out || !lse || !raw_table) return HCA_ERR_NULL;
     if (raw_blocks > 0 && (!raw_pool || !raw_scale)) return HCA_ERR_NULL;
     if (comp_table && comp_blocks > 0 && (!comp_pool || !comp_scale)) return HCA_ERR_NULL;
+    if (share.G > 0 && (!comp_table || !share.first || !share.cols)) return HCA_ERR_NULL;
     if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(raw_pool) || !aligned16(comp_pool))
       return HCA_ERR_ALIGN;
   }
-  rc = check_ws(workspace, workspace_bytes, cache_attn_ws_bytes(N, R, H, D, dtype));
+  int rc = check_ws(workspace, workspace_bytes, need);
   if (rc != HCA_OK) return rc;
   if (take_launch_failure()) return HCA_ERR_CUDA;
   if (empty) return empty_call(workspace, stream);
@@ -691,7 +690,45 @@ int hca_cache_attn(const void *q, const int32_t *start, const int32_t *held, con
   a.ws = workspace;
   a.wait_ns = wait_limit_ns();
   a.stall = dtype == HCA_BF16 ? take_stall_mask() & HCA_STALL_FWD : 0;
-  return cuda_status(cache_attn(a, static_cast<cudaStream_t>(stream)));
+  a.share = share;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(share.G > 0 ? cache_attn_shared(a, st) : cache_attn(a, st));
+}
+
+int hca_cache_attn(const void *q, const int32_t *start, const int32_t *held, const void *raw_pool,
+                   const float *raw_scale, const int32_t *raw_table, int raw_blocks, int raw_cols,
+                   const void *comp_pool, const float *comp_scale, const int32_t *comp_table, int comp_blocks,
+                   int comp_cols, void *out, float *lse, int N, int R, int H, int D, int W, int m, int bs, float scale,
+                   int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+  const int rc = cache_attn_shape(N, R, H, D, dtype);
+  if (rc != HCA_OK) return rc;
+  return cache_attn_call(q, start, held, raw_pool, raw_scale, raw_table, raw_blocks, raw_cols, comp_pool, comp_scale, comp_table,
+                         comp_blocks, comp_cols, CacheShare{}, out, lse, N, R, H, D, W, m, bs, scale, dtype, workspace,
+                         workspace_bytes, cache_attn_ws_bytes(N, R, H, D, dtype), stream);
+}
+
+static int cache_attn_shared_shape(int N, int R, int H, int D, int G, int dtype) {
+  const int rc = cache_attn_shape(N, R, H, D, dtype);
+  if (rc != HCA_OK) return rc;
+  return G < 0 || G > cache_shared_max_groups() ? HCA_ERR_SHAPE : HCA_OK;
+}
+
+size_t hca_cache_attn_shared_workspace_size(int N, int R, int H, int D, int G, int dtype) {
+  if (cache_attn_shared_shape(N, R, H, D, G, dtype) != HCA_OK) return 0;
+  return cache_attn_shared_ws_bytes(N, R, H, D, G, dtype);
+}
+
+int hca_cache_attn_shared(const void *q, const int32_t *start, const int32_t *held, const void *raw_pool,
+                          const float *raw_scale, const int32_t *raw_table, int raw_blocks, int raw_cols,
+                          const void *comp_pool, const float *comp_scale, const int32_t *comp_table, int comp_blocks,
+                          int comp_cols, const int32_t *first, const int32_t *shared_cols, void *out, float *lse, int N,
+                          int R, int H, int D, int G, int W, int m, int bs, float scale, int dtype, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+  const int rc = cache_attn_shared_shape(N, R, H, D, G, dtype);
+  if (rc != HCA_OK) return rc;
+  return cache_attn_call(q, start, held, raw_pool, raw_scale, raw_table, raw_blocks, raw_cols, comp_pool, comp_scale, comp_table,
+                         comp_blocks, comp_cols, CacheShare{first, shared_cols, G, 0}, out, lse, N, R, H, D, W, m, bs, scale, dtype,
+                         workspace, workspace_bytes, cache_attn_shared_ws_bytes(N, R, H, D, G, dtype), stream);
 }
 
 int hca_visible_pairs(const int32_t *seg, int B, int S, int W, int m, int64_t *raw_pairs, int64_t *comp_pairs,

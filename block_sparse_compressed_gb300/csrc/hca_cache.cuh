@@ -162,6 +162,7 @@ constexpr int kGroupCost = 2, kShortGroup = 32;
 struct Pages {
   int rp0, nraw;  // first raw page, raw pages
   int ncomp;      // compressed pages
+  int cp0;        // the first of them
 };
 
 __device__ __forceinline__ Pages group_pages(int pos0, int npos, int W, int m, int log_bs, bool comp) {
@@ -171,6 +172,7 @@ __device__ __forceinline__ Pages group_pages(int pos0, int npos, int W, int m, i
   g.nraw = (last >> log_bs) - g.rp0 + 1;
   const int ent = comp ? (last + 1) / m : 0;
   g.ncomp = (ent + (1 << log_bs) - 1) >> log_bs;
+  g.cp0 = 0;
   return g;
 }
 

@@ -31,13 +31,14 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr int kSchedThreads = 1024;
 
-__global__ void __launch_bounds__(kSchedThreads) hca_cache_sched_kernel(const AttnParams p) {
+template <typename P>
+__global__ void __launch_bounds__(kSchedThreads) hca_cache_sched_kernel(const P p) {
   __shared__ long long tmp[33];
   __shared__ int longest;
   const int tid = threadIdx.x;
   if (tid == 0) longest = 0;
   tc::pdl_launch_dependents();  // the attention kernel waits for this one's end by itself
-  bool ok = true;
+  bool ok = prefixes_ok(p);
   long long chunks = 0;
   for (int r0 = 0; r0 < p.R; r0 += kSchedThreads) {
     const int r = r0 + tid;
@@ -137,12 +138,12 @@ struct SimtShared {
 
 // The line's groups by the CTA's threads, one each, into sh.groups; returns its
 // tiles (-1: refused).
-template <int kCols>
-__device__ __forceinline__ int schedule(const AttnParams &p, SimtShared<kCols> &sh, int &ngroups) {
+template <typename P, int kCols>
+__device__ __forceinline__ int schedule(const P &p, SimtShared<kCols> &sh, int &ngroups) {
   const int tid = threadIdx.x;
   int n = 0;
-  bool ok = true;
-  if (tid < p.R) ok = request_chunks(p, tid, n);
+  bool ok = prefixes_ok(p);
+  if (tid < p.R) ok = request_chunks(p, tid, n) && ok;
   long long chunks, tiles;
   sh.gbase[tid] = (int)block_scan(n, sh.tmp, chunks);
   ok = __syncthreads_and(ok);
@@ -163,8 +164,8 @@ __device__ __forceinline__ int schedule(const AttnParams &p, SimtShared<kCols> &
   return __syncthreads_and(ok) && tiles < kMaxTiles ? (int)tiles : -1;
 }
 
-template <int kCols>
-__global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const AttnParams p) {
+template <int kCols, typename P>
+__global__ void __launch_bounds__(kSimtThreads) hca_cache_simt_kernel(const P p) {
   extern __shared__ uint8_t keys[];  // [128][D + 4] bytes: a row's words fall into different banks
   __shared__ SimtShared<kCols> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -568,14 +569,14 @@ __global__ void __launch_bounds__(kCombineThreads) hca_cache_combine_few_kernel(
   }
 }
 
-template <int kCols>
-cudaError_t simt(const AttnParams &p, cudaStream_t st) {
+template <int kCols, typename P>
+cudaError_t simt(const P &p, cudaStream_t st) {
   static tc::SmemAttrOnce attr;
-  const cudaError_t e = attr.ensure(reinterpret_cast<const void *>(hca_cache_simt_kernel<kCols>), kTileKeys * (256 + 4));
+  const cudaError_t e = attr.ensure(reinterpret_cast<const void *>(hca_cache_simt_kernel<kCols, P>), kTileKeys * (256 + 4));
   if (e != cudaSuccess) return e;
   ProfScope prof(kKCacheSimt, st);
-  if (!p.in_cta) return launch_behind(hca_cache_simt_kernel<kCols>, dim3(p.grid), kSimtThreads, kTileKeys * (p.D + 4), st, p);
-  hca_cache_simt_kernel<kCols><<<p.grid, kSimtThreads, kTileKeys * (p.D + 4), st>>>(p);
+  if (!p.in_cta) return launch_behind(hca_cache_simt_kernel<kCols, P>, dim3(p.grid), kSimtThreads, kTileKeys * (p.D + 4), st, p);
+  hca_cache_simt_kernel<kCols, P><<<p.grid, kSimtThreads, kTileKeys * (p.D + 4), st>>>(p);
   return cudaGetLastError();
 }
 
@@ -657,10 +658,12 @@ int log2_int(int v) {
 
 size_t cache_attn_ws_bytes(int N, int R, int H, int D, int dtype) { return layout_of(N, R, H, D, dtype).bytes; }
 
-cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
+namespace {
+
+template <typename P>
+cudaError_t attend(P &p, const CacheAttnArgs &a, cudaStream_t st) {
   const Layout l = layout_of(a.N, a.R, a.H, a.D, a.dtype);
   char *ws = static_cast<char *>(a.ws);
-  AttnParams p;
   p.q = a.q; p.start = a.start; p.held = a.held; p.raw = a.raw; p.comp = a.comp; p.out = a.out; p.lse = a.lse;
   p.hdr = reinterpret_cast<SchedHeader *>(ws);
   p.gbase = reinterpret_cast<int32_t *>(ws + l.off_gbase);
@@ -683,7 +686,7 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
   p.in_cta = l.slices == 1 && a.R <= threads && l.gmax <= (size_t)threads;
   if (!p.in_cta) {
     ProfScope prof(kKCacheSched, st);
-    hca_cache_sched_kernel<<<1, kSchedThreads, 0, st>>>(p);
+    hca_cache_sched_kernel<P><<<1, kSchedThreads, 0, st>>>(p);
   }
   if (tcs) {
     const cudaError_t e = tc_cache_attn(p, st);
@@ -693,9 +696,22 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   const int gmax = (int)std::min<size_t>(l.gmax, 1 << 20);
-  const cudaError_t e = tcs ? combine<__nv_bfloat16>(p, gmax, sms, st) : combine<float>(p, gmax, sms, st);
+  const bool bf16_rows = tcs && !(P::kShared && a.share.apart);
+  const cudaError_t e = bf16_rows ? combine<__nv_bfloat16>(p, gmax, sms, st) : combine<float>(p, gmax, sms, st);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
+  if (a.share.G == 0) {
+    AttnParams p;
+    return attend(p, a, st);
+  }
+  SharedAttnParams p;
+  p.first = a.share.first; p.cols = a.share.cols; p.G = a.share.G; p.apart = a.share.apart;
+  return attend(p, a, st);
 }
 
 }  // namespace hca

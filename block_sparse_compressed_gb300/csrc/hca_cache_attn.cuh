@@ -33,7 +33,52 @@ struct AttnParams {
   float scale;
   uint64_t wait_ns;
   int stall;
+  static constexpr bool kShared = false;
 };
+
+// The requests of prefix g are first[g] .. first[g + 1] - 1; the first cols[g]
+// columns of their compressed tables are the same blocks.
+struct SharedAttnParams : AttnParams {
+  const int32_t *first, *cols;
+  int G;
+  int apart;  // those columns are left out, and out is fp32 (the join adds them)
+  static constexpr bool kShared = true;
+};
+
+// Prefixes are in order and cover all requests (each thread of a block looks at its
+// own of them).
+__device__ __forceinline__ bool prefixes_ok(const AttnParams &) { return true; }
+__device__ __forceinline__ bool prefixes_ok(const SharedAttnParams &p) {
+  bool ok = true;
+  for (int g = threadIdx.x; g < p.G; g += blockDim.x)
+    ok = ok && p.first[g] <= p.first[g + 1] && p.cols[g] >= 0 && p.cols[g] <= p.comp.cols && (g > 0 || p.first[0] == 0) &&
+         (g < p.G - 1 || p.first[p.G] == p.R);
+  return ok;
+}
+
+// Common columns of request r's prefix
+__device__ __forceinline__ int prefix_pages(const AttnParams &, int) { return 0; }
+__device__ __forceinline__ int prefix_pages(const SharedAttnParams &p, int r) {
+  int lo = 0, hi = p.G;  // first[lo] <= r < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.first[mid] <= r) lo = mid; else hi = mid;
+  }
+  return p.cols[lo];
+}
+
+// What of a group's pages is not its prefix's
+__device__ __forceinline__ Pages own_pages(const AttnParams &, int, const Pages &pg) { return pg; }
+__device__ __forceinline__ Pages own_pages(const SharedAttnParams &p, int r, Pages pg) {
+  if (p.apart) {
+    pg.cp0 = prefix_pages(p, r);
+    pg.ncomp -= pg.cp0;
+  }
+  return pg;
+}
+
+__device__ __forceinline__ bool wide_rows(const AttnParams &) { return false; }
+__device__ __forceinline__ bool wide_rows(const SharedAttnParams &p) { return p.apart != 0; }
 
 // Columns of a group that stand for a (position, head).
 __device__ __forceinline__ int real_columns(const AttnParams &p, int npos, int slice) {
@@ -67,31 +112,39 @@ __device__ __forceinline__ Border border_of(const AttnParams &p, const Group &g,
 }
 
 // Chunks (groups before slicing) of request r; false: lengths out of range.
-__device__ __forceinline__ bool request_chunks(const AttnParams &p, int r, int &n) {
+template <typename P>
+__device__ __forceinline__ bool request_chunks(const P &p, int r, int &n) {
   const int s0 = p.start[r], s1 = p.start[r + 1], h = p.held[r];
-  const bool ok = s0 >= 0 && s1 >= s0 && s1 <= p.N && h >= 0 && h <= kMaxPos - (s1 - s0) && (r > 0 || s0 == 0);
+  bool ok = s0 >= 0 && s1 >= s0 && s1 <= p.N && h >= 0 && h <= kMaxPos - (s1 - s0) && (r > 0 || s0 == 0);
+  if constexpr (P::kShared) {
+    // every token sees the whole prefix
+    const long long c = prefix_pages(p, r);
+    ok = ok && c >= 0 && c <= p.comp.cols && (s1 == s0 || (c << p.log_bs) * p.m <= (long long)h + 1);
+  }
   n = ok ? (s1 - s0 + p.P - 1) / p.P : 0;
   return ok;
 }
 
 // Group of chunk c, the k-th of request r; false: the tables are too narrow.
-__device__ __forceinline__ bool chunk_group(const AttnParams &p, int r, int k, Group &g) {
+template <typename P>
+__device__ __forceinline__ bool chunk_group(const P &p, int r, int k, Group &g) {
   const int s0 = p.start[r], T = p.start[r + 1] - s0, h = p.held[r], first = k * p.P;
   g.r = r;
   g.row0 = s0 + first;
   g.pos0 = h + first;
   g.npos = min(p.P, T - first);
   g.slice = 0;
-  const Pages pg = group_pages(g.pos0, g.npos, p.W, p.m, p.log_bs, p.comp.table != nullptr);
+  const Pages pg = own_pages(p, r, group_pages(g.pos0, g.npos, p.W, p.m, p.log_bs, p.comp.table != nullptr));
   g.ntiles = (int)((((uint32_t)(pg.nraw + pg.ncomp) << p.log_bs) + kTileKeys - 1) / kTileKeys);
   // the raw table keeps the last cols pages of the request's tokens
-  return ((h + T - 1) >> p.log_bs) - pg.rp0 < p.raw.cols && pg.ncomp <= p.comp.cols;
+  return ((h + T - 1) >> p.log_bs) - pg.rp0 < p.raw.cols && pg.cp0 + pg.ncomp <= p.comp.cols;
 }
 
 // tensor-core kernel (hca_cache_attn_tc.cu)
 int tc_cache_ctas();     // CTAs per SM
 int tc_cache_threads();  // threads of a CTA
 cudaError_t tc_cache_attn(const AttnParams &p, cudaStream_t st);
+cudaError_t tc_cache_attn(const SharedAttnParams &p, cudaStream_t st);
 
 }  // namespace cache
 }  // namespace hca

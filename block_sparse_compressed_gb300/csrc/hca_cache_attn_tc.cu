@@ -82,7 +82,7 @@
 #include <type_traits>
 
 #include "hca_cache_attn.cuh"
-#include "tc_tiles.cuh"
+#include "hca_cache_tc.cuh"
 
 namespace hca {
 using namespace tc;
@@ -90,10 +90,6 @@ using namespace cache;
 
 namespace {
 
-constexpr float kRaiseLog2 = 11.f, kBias = 2.f;
-constexpr int kLeastExp = -15, kMostExp = 7;      // e: 2^-9 .. 448 times 2^e is an fp16 value
-constexpr int kLeastUnit = -100, kMostUnit = 127;  // u: 2^u / l is a normal number (l below 2^26)
-constexpr int kLeastQExp = -118;                  // exponent of q's factor: so is its reciprocal
 constexpr int kMetaStages = 4;  // tiles whose pages are looked up ahead
 constexpr int kStages = 2;      // fp16 tiles; filled and released by halves
 constexpr int kHalfStages = 2 * kStages;
@@ -156,56 +152,6 @@ struct Shared {
   uint32_t tmem_base;
   int abort, first, range[2];
 };
-
-// s = 2^exponent * part with part in (0.5, 1], for positive finite s.
-__device__ __forceinline__ int split_scale(float s, float &part) {
-  const int sub = s < FLT_MIN ? 24 : 0;  // a subnormal one
-  const uint32_t u = __float_as_uint(sub ? s * 16777216.f : s), mant = u & 0x7fffffu;
-  part = mant ? __uint_as_float(mant | (126u << 23)) : 1.f;
-  return (int)(u >> 23) - (mant ? 126 : 127) - sub;
-}
-// 2^e in both halves, e in [kLeastExp, kMostExp]
-__device__ __forceinline__ uint32_t f16x2_exp2(int e) { return (e >= -14 ? (uint32_t)(e + 15) << 10 : 0x400u >> (-14 - e)) * 0x10001u; }
-__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ void st_shared(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ void ld_shared(uint32_t addr, uint32_t (&v)[4]) {
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// 16 bytes of which the first n come from p and the others are 0
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *p, uint32_t n) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
-               "r"(smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-// 4 e4m3 values -> two fp16 pairs
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &a, uint32_t &b) {
-  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
-      : "=r"(a), "=r"(b)
-      : "r"(w));
-}
 
 // Sum of v over the threads in front of this one, total and number of those
 // that count; a warp's v sum up to less than 2^31 (a group has 2^25 tiles at
@@ -276,23 +222,8 @@ static __device__ __noinline__ float scaled_p(uint32_t s, uint32_t to, float ck,
   return sum;
 }
 
-// A warp's rows of O times f.
-template <int D>
-static __device__ __noinline__ void scale_o(uint32_t addr, float f) {
-#pragma unroll 1
-  for (int c = 0; c < D; c += 16) {
-    uint32_t o[16];
-    tmem_ld16(addr + c, o);
-    tmem_wait_ld();
-#pragma unroll
-    for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-    tmem_st16(addr + c, o);
-  }
-  tmem_wait_st();
-}
-
-template <int NQ, int D>
-__global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnParams p) {
+template <int NQ, int D, typename P>
+__global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const P p) {
   using C = Cfg<NQ, D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -335,8 +266,8 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
   if (p.in_cta) {
     // one thread per request; where some bring more than one group, one per group
     int n = 0, r = tid, k = 0;
-    bool ok = true;
-    if (tid < p.R) ok = request_chunks(p, tid, n);
+    bool ok = prefixes_ok(p);
+    if (tid < p.R) ok = request_chunks(p, tid, n) && ok;
     bool mine = n == 1;
     if (__syncthreads_or(n > 1)) {
       long long all;
@@ -429,6 +360,9 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       }
     }
   }
+  if constexpr (P::kShared) {
+    if (p.in_cta && tid == 0 && blockIdx.x == 0) p.hdr->ntiles = ntiles;  // the join looks whether all was refused
+  }
   if (tid == 0) {
     p.err[blockIdx.x] = ntiles < 0 ? HCA_ERR_CACHE : HCA_OK;
     if (!busy) p.border[blockIdx.x] = Border{0, 0, 0, 0};
@@ -457,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         int unit = 0;
         bool set = false;  // by the segment's first pages
         const Segment g = segment(k);
-        const Pages pg = group_pages(g.pos0, g.npos, p.W, p.m, p.log_bs, p.comp.table != nullptr);
+        const Pages pg = own_pages(p, g.r, group_pages(g.pos0, g.npos, p.W, p.m, p.log_bs, p.comp.table != nullptr));
 #pragma unroll 1
         for (int jb = g.j0; ok && jb < g.j1; jb += batch) {
           const int v = jb * ppt + lane;
@@ -467,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
           if (v < pg.nraw + pg.ncomp && v < g.j1 * ppt) {
             const bool comp = v >= pg.nraw;
             const CacheSet &cs = comp ? p.comp : p.raw;
-            const int page = comp ? v - pg.nraw : pg.rp0 + v;
+            const int page = comp ? v - pg.nraw + pg.cp0 : pg.rp0 + v;
             const int id = cs.table[(size_t)g.r * cs.cols + page % cs.cols];
             pm.key0 = page << p.log_bs;
             const long long end = (long long)pm.key0 + (1 << p.log_bs);
@@ -795,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
       const size_t rows = (size_t)p.N * p.H;
       const uint4 nan4 = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
 #pragma unroll 1
-      for (size_t i = (size_t)blockIdx.x * kWG + tid; i < rows * (D / 8); i += (size_t)gridDim.x * kWG)
+      for (size_t i = (size_t)blockIdx.x * kWG + tid; i < rows * (wide_rows(p) ? D / 4 : D / 8); i += (size_t)gridDim.x * kWG)
         reinterpret_cast<uint4 *>(p.out)[i] = nan4;
 #pragma unroll 1
       for (size_t i = (size_t)blockIdx.x * kWG + tid; i < rows; i += (size_t)gridDim.x * kWG)
@@ -980,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         }
         m_run -= kBias;  // what the sums are relative to
         if (*abort_flag) l_run = __int_as_float(0x7fc00000);
-        const bool whole = g.slot < 0;
+        const bool whole = g.slot < 0, bf16 = whole && !wide_rows(p);
         const size_t orow = (size_t)g.row0 * p.H + g.slice() * p.HS;  // rows of the group are rows of q and out in order
         float weight = 1.f;
         if constexpr (C::kCopies > 1) {
@@ -1011,11 +945,11 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
         tc_fence_after();
         // O leaves through shared memory, 64 bytes of a row at a time, so that
         // four lanes write a row's: a store to 32 rows takes 32 cycles.
-        uint8_t *to = whole ? static_cast<uint8_t *>(p.out) + orow * D * 2 : reinterpret_cast<uint8_t *>(p.part_o + (size_t)g.slot * NQ * D);
-        const int row_bytes = whole ? D * 2 : D * 4, piece = lane & 3;
+        uint8_t *to = whole ? static_cast<uint8_t *>(p.out) + orow * D * (bf16 ? 2 : 4) : reinterpret_cast<uint8_t *>(p.part_o + (size_t)g.slot * NQ * D);
+        const int row_bytes = bf16 ? D * 2 : D * 4, piece = lane & 3;
         const uint32_t join = smem_u32(sh.join);
         const uint32_t mine = join + tid * 64, swz = (tid >> 1) & 3;
-        const bool packed = C::kCopies == 1 && whole;  // staged as bf16 already: 32 columns
+        const bool packed = C::kCopies == 1 && bf16;  // staged as bf16 already: 32 columns
         const int rounds = packed ? D / 32 : D / 16;
 #pragma unroll 1
         for (int c = 0; c < rounds; ++c) {
@@ -1059,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
               }
               uint8_t *at = to + (size_t)r * row_bytes;
               if (r < nreal) {
-                if (whole) *reinterpret_cast<uint2 *>(at + c * 32 + piece * 8) = make_uint2(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]));
+                if (bf16) *reinterpret_cast<uint2 *>(at + c * 32 + piece * 8) = make_uint2(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]));
                 else *reinterpret_cast<float4 *>(at + c * 64 + piece * 16) = make_float4(sum[0], sum[1], sum[2], sum[3]);
               }
             }
@@ -1081,26 +1015,20 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const AttnP
   }
 }
 
-template <int NQ, int D>
-cudaError_t launch(const AttnParams &p, cudaStream_t st) {
+template <int NQ, int D, typename P>
+cudaError_t launch(const P &p, cudaStream_t st) {
   using C = Cfg<NQ, D>;
   static SmemAttrOnce attr;
-  const cudaError_t e = attr.ensure(reinterpret_cast<const void *>(hca_cache_attn_kernel<NQ, D>), C::kSmem);
+  const cudaError_t e = attr.ensure(reinterpret_cast<const void *>(hca_cache_attn_kernel<NQ, D, P>), C::kSmem);
   if (e != cudaSuccess) return e;
   ProfScope prof(kKCacheAttn, st);
-  if (!p.in_cta) return launch_behind(hca_cache_attn_kernel<NQ, D>, dim3(p.grid), kThreads, C::kSmem, st, p);
-  hca_cache_attn_kernel<NQ, D><<<p.grid, kThreads, C::kSmem, st>>>(p);
+  if (!p.in_cta) return launch_behind(hca_cache_attn_kernel<NQ, D, P>, dim3(p.grid), kThreads, C::kSmem, st, p);
+  hca_cache_attn_kernel<NQ, D, P><<<p.grid, kThreads, C::kSmem, st>>>(p);
   return cudaGetLastError();
 }
 
-}  // namespace
-
-namespace cache {
-
-int tc_cache_ctas() { return 2; }
-int tc_cache_threads() { return kThreads; }
-
-cudaError_t tc_cache_attn(const AttnParams &p, cudaStream_t st) {
+template <typename P>
+cudaError_t by_shape(const P &p, cudaStream_t st) {
   const int which = (p.NQ == 32 ? 0 : p.NQ == 64 ? 1 : 2) + (p.D == 64 ? 3 : 0);
   switch (which) {
     case 0: return launch<32, 128>(p, st);
@@ -1111,6 +1039,16 @@ cudaError_t tc_cache_attn(const AttnParams &p, cudaStream_t st) {
     default: return launch<128, 64>(p, st);
   }
 }
+
+}  // namespace
+
+namespace cache {
+
+int tc_cache_ctas() { return 2; }
+int tc_cache_threads() { return kThreads; }
+
+cudaError_t tc_cache_attn(const AttnParams &p, cudaStream_t st) { return by_shape(p, st); }
+cudaError_t tc_cache_attn(const SharedAttnParams &p, cudaStream_t st) { return by_shape(p, st); }
 
 }  // namespace cache
 }  // namespace hca

@@ -1,0 +1,829 @@
+// hca_cache_shared.cu -- attention over the 8-bit cache for requests that begin
+// with the same compressed entries: the common ones once for all of them.
+//
+// The rows of q of a prefix's requests are adjacent, and every one of them sees
+// every common entry, so that part is dense attention of one matrix of rows over
+// one list of pages, without masks:
+//   S [256 x 128 keys] = Q K^T,  O [256 x D] += P K     kind::f16 (tcgen05)
+// A request by itself fills 64 of the tensor cores' 128 rows with a token of 64
+// heads, and each request converts the entries to fp16 for itself.  Here tiles
+// are full, and an entry is converted once for 256 rows.
+//
+// The work.  A prefix of `rows` rows and `tiles` key tiles is ceil(rows / 256) row
+// tiles of `tiles` units; all units of all prefixes form one line, cut into equal
+// ranges, one for each CTA.  What a CTA has of a row tile (a segment) leaves a
+// partial result: O / l in fp32, the reference exponent and the sum l.  The
+// requests' own keys (window and entries behind the prefix) go through the kernels
+// of hca_cache_attn, which leave fp32 rows, and the join kernel adds up.
+//
+// A CTA has two tiles A and B of 128 rows and one stream of keys, 512 threads:
+//   warps 0 - 3, 4 - 7   softmax of A, of B: a thread has a row
+//   warps 8 - 11         converter: e4m3 -> fp16 key tiles, and q of a segment
+//   warp 12              pages: block ids and scales, looked up ahead
+//   warps 13, 14         MMA issuers of A and of B
+//   warp 15              copies of pages (bulk), tensor memory
+// S of a tile is 128 columns of tensor memory, softmaxed in two halves of 64 keys
+// whose P (fp16) takes the first half of their columns: the first half's product
+// with K runs while the second half is worked on, and one tile's products while
+// the other tile's softmax runs.  Numbers are as in hca_cache_attn_tc.cu: q as
+// fp16 with a power of two for each row, keys as k8 * 2^e in units of 2^u, u the
+// largest scale of the segment's pages; what is left of a scale (below 2^-15 of
+// the unit, or no power of two) multiplies scores and probabilities.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <climits>
+
+#include "hca_cache_tc.cuh"
+
+namespace hca {
+using namespace tc;
+using namespace cache;
+
+namespace {
+
+constexpr int kRowTile = 256, kSharedMaxGroups = 256, kMaxGrid = 256;
+constexpr int kWG = 128, kThreads = 4 * kWG;
+constexpr int kMetaStages = 4, kKvStages = 3, kRawStages = 2;
+constexpr int kRegsSoft = 168, kRegsConv = 88, kRegsIssue = 88;
+static_assert(2 * kRegsSoft + kRegsConv + kRegsIssue <= 4 * 128, "register split must fit the launch");
+constexpr uint32_t kTmem = 512;
+__device__ __forceinline__ constexpr uint32_t col_s(int x) { return 128u * x; }
+__device__ __forceinline__ constexpr uint32_t col_o(int x) { return 256u + 128u * x; }
+enum { kBarQ = 1, kBarOut = 2 };  // named barriers
+
+struct SharedParams {
+  const __nv_bfloat16 *q;
+  const int32_t *start, *first, *cols;
+  CacheSet comp;
+  int32_t *err;     // [grid]
+  float2 *part_ml;  // [slots][256] reference exponent and sum
+  float *part_o;    // [slots][256][D]
+  const float *own_out, *own_lse;
+  const SchedHeader *own;  // of the requests' own keys
+  int32_t *status;
+  __nv_bfloat16 *out;
+  float *lse;
+  int N, R, H, D, G, log_bs, grid;
+  float scale;
+  uint64_t wait_ns;
+  int stall;
+};
+
+// A prefix with its rows and its place in the line.
+struct Prefix {
+  int row0, rows;   // rows of q and out
+  int tiles, pages; // key tiles, pages
+  int line0, rt0;   // first unit, first row tile
+  int request;      // whose table is read
+};
+
+struct Table {
+  Prefix g[kSharedMaxGroups];
+  long long tmp[33];
+};
+
+// The line, by all threads of a block (at least kSharedMaxGroups): its units, -1 if
+// the prefixes are refused.
+__device__ __forceinline__ int make_table(const SharedParams &p, Table &t) {
+  const int i = threadIdx.x;
+  Prefix x = {0, 0, 0, 0, 0, 0, 0};
+  bool ok = true;
+  long long units = 0;
+  int rts = 0;
+  if (i < p.G) {
+    const int f0 = p.first[i], f1 = p.first[i + 1], c = p.cols[i];
+    ok = f0 >= 0 && f1 >= f0 && f1 <= p.R && (i > 0 || f0 == 0) && (i < p.G - 1 || f1 == p.R) && c >= 0 && c <= p.comp.cols;
+    if (ok) {
+      const int s0 = p.start[f0], s1 = p.start[f1];
+      ok = s0 >= 0 && s1 >= s0 && s1 <= p.N;
+      if (ok) {
+        x.row0 = s0 * p.H;
+        x.rows = (s1 - s0) * p.H;
+        x.pages = c;
+        x.request = f0;
+        ok = ((long long)c << p.log_bs) <= kMaxPos;
+        x.tiles = ok ? ((c << p.log_bs) + kTileKeys - 1) / kTileKeys : 0;
+        rts = x.tiles > 0 ? (x.rows + kRowTile - 1) / kRowTile : 0;
+        units = (long long)rts * x.tiles;
+      }
+    }
+  }
+  ok = __syncthreads_and(ok);
+  long long all, nrt;
+  const long long line0 = block_scan(units, t.tmp, all);
+  x.rt0 = (int)block_scan((long long)rts, t.tmp, nrt);
+  ok = ok && all < kMaxTiles;
+  x.line0 = ok ? (int)line0 : 0;
+  if (i < p.G) t.g[i] = x;
+  __syncthreads();
+  return ok ? (int)all : -1;
+}
+
+__device__ __forceinline__ int units_per_cta(int units, int grid) { return max((units + grid - 1) / grid, 1); }
+
+// What a CTA has of a row tile.
+struct Part {
+  int row0, rows;      // rows of q
+  int j0, j1;          // key tiles
+  int slot;
+  int pages, request;
+  bool last;           // of the CTA's
+};
+
+struct Walk {
+  int u, end, g;
+  __device__ __forceinline__ Part next(const Table &t, int cta) {
+    while (u >= t.g[g].line0 + (t.g[g].rows + kRowTile - 1) / kRowTile * t.g[g].tiles) ++g;
+    const Prefix &x = t.g[g];
+    const int rt = (u - x.line0) / x.tiles;
+    Part s;
+    s.j0 = u - x.line0 - rt * x.tiles;
+    s.j1 = min(x.tiles, s.j0 + (end - u));
+    s.row0 = x.row0 + rt * kRowTile;
+    s.rows = min(kRowTile, x.rows - rt * kRowTile);
+    s.slot = x.rt0 + rt + cta;
+    s.pages = x.pages;
+    s.request = x.request;
+    u += s.j1 - s.j0;
+    s.last = u >= end;
+    return s;
+  }
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kStageBytes = kHalves * kHalfTile;  // fp16 tile of 128 keys, or of 128 rows of q
+  static constexpr int kOffQ = kKvStages * kStageBytes;
+  static constexpr int kOffRaw = kOffQ + 2 * kStageBytes;
+  static constexpr int kRawBytes = kTileKeys * D;
+  static constexpr int kSmem = kOffRaw + kRawStages * kRawBytes + 1024;
+};
+
+struct TileMeta {
+  const uint8_t *rows[8];  // NULL: no page, or a bad one
+  uint32_t factor[8];      // 2^e of its keys, for both values of a pair of fp16
+  float rest[8];           // the page's scale is 2^(unit + e) * rest
+  uint32_t valid;          // pages that are there
+  int keys;                // keys of the tile
+  int unit;
+  int odd, bad;            // some rest is not 1; a bad block id or scale
+};
+
+struct Shared {
+  uint4 out[2 * kWG * 4];  // O on its way out: 64 bytes of each row
+  uint64_t meta_full[kMetaStages], meta_empty[kMetaStages];
+  uint64_t raw_full[kRawStages], raw_empty[kRawStages];
+  uint64_t kv_full[kKvStages], kv_empty[kKvStages];
+  uint64_t q_full, q_read, s_full[2], p_full[2][2], pv_done[2][2], drain[2], never;
+  TileMeta meta[kMetaStages];
+  float q_factor[kRowTile];
+  Table table;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const SharedParams p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int *abort_flag = &sh.abort;
+  int32_t *status = &p.err[blockIdx.x];
+
+  if (tid == 0) {
+    for (int s = 0; s < kMetaStages; ++s) {
+      mbar_init(&sh.meta_full[s], 1);
+      mbar_init(&sh.meta_empty[s], 2 * kWG);  // the softmax warps are the last to read a tile's pages
+    }
+    for (int s = 0; s < kRawStages; ++s) {
+      mbar_init(&sh.raw_full[s], 1);
+      mbar_init(&sh.raw_empty[s], kWG);
+    }
+    for (int s = 0; s < kKvStages; ++s) {
+      mbar_init(&sh.kv_full[s], kWG);
+      mbar_init(&sh.kv_empty[s], 2);
+    }
+    mbar_init(&sh.q_full, kWG);
+    mbar_init(&sh.q_read, 2 * kWG);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sh.s_full[x], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sh.p_full[x][h], kWG);
+        mbar_init(&sh.pv_done[x][h], 1);
+      }
+      mbar_init(&sh.drain[x], 1);
+    }
+    mbar_init(&sh.never, 1);
+    sh.abort = 0;
+    p.err[blockIdx.x] = HCA_OK;
+    fence_mbar_init();
+  }
+  if (warp == 15) {
+    tmem_alloc(&sh.tmem_base, kTmem);
+    tmem_relinquish();
+  }
+  const int units = make_table(p, sh.table);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  const int quota = units_per_cta(max(units, 0), p.grid);
+  const long long c0 = (long long)quota * blockIdx.x;
+  const bool busy = c0 < units;
+  const Walk from = {(int)c0, (int)min(c0 + quota, (long long)max(units, 0)), 0};
+
+  const uint32_t limit_ns = (uint32_t)p.wait_ns;
+  auto wait_bar = [&](uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_idle(bar, parity, abort_flag, limit_ns));
+  };
+  const int ppt = kTileKeys >> p.log_bs;  // pages of a tile: 1 .. 8
+  if (warp >= 12) {
+    setmaxnreg_dec<kRegsIssue>();
+    if (warp == 12 && busy) {
+      // ------------------------------------------------------------ pages
+      const int batch = 32 / ppt;  // tiles whose pages the warp's lanes look up at once
+      const uint32_t page_bytes = D << p.log_bs;
+      Walk walk = from;
+      uint32_t n = 0;
+      bool ok = true;
+      auto page_scale = [&](const Part &s, int page, int &id) {
+        id = p.comp.table[(size_t)s.request * p.comp.cols + page];
+        const bool in = id >= 0 && id < p.comp.nblocks;
+        if (!in) id = -1;
+        return in ? p.comp.scale[id] : 0.f;
+      };
+#pragma unroll 1
+      for (bool last = false; ok && !last;) {
+        const Part s = walk.next(sh.table, blockIdx.x);
+        last = s.last;
+        // the unit: the largest scale of the segment's pages
+        int unit = INT_MIN;
+        const int v0 = s.j0 * ppt, v1 = min(s.j1 * ppt, s.pages);
+#pragma unroll 4
+        for (int v = v0 + lane; v < v1; v += 32) {
+          int id;
+          const float scale = page_scale(s, v, id);
+          float part;
+          if (scale > 0.f && scale < INFINITY) unit = max(unit, split_scale(scale, part));
+        }
+        unit = __reduce_max_sync(0xffffffffu, unit);
+        unit = unit == INT_MIN ? 0 : min(max(unit, kLeastUnit), kMostUnit);
+#pragma unroll 1
+        for (int jb = s.j0; ok && jb < s.j1; jb += batch) {
+          const int v = jb * ppt + lane;
+          const uint8_t *rows = nullptr;
+          uint32_t factor = f16x2_exp2(0);
+          float rest = 1.f;
+          bool bad = false;
+          if (v < v1 && lane < batch * ppt) {
+            int id;
+            const float scale = page_scale(s, v, id);
+            bad = !(scale > 0.f && scale < INFINITY);
+            if (!bad) {
+              rows = p.comp.pool + (size_t)id * page_bytes;
+              float part;
+              const int ex = split_scale(scale, part), e = min(max(ex - unit, kLeastExp), kMostExp);
+              factor = f16x2_exp2(e);
+              rest = part * exp2_int(max(ex - unit - e, -120));
+            }
+          }
+          const int jn = min(batch, s.j1 - jb);
+#pragma unroll 1
+          for (int t = 0; t < jn; ++t, ++n) {
+            const int ms = n % kMetaStages;
+            if (n >= (uint32_t)kMetaStages) ok = wait_bar(&sh.meta_empty[ms], ((n / kMetaStages) - 1) & 1);
+            if (!ok) break;
+            TileMeta &to = sh.meta[ms];
+            const bool here = lane / ppt == t;
+            if (here) {
+              if (rows) prefetch_l2(rows, page_bytes);
+              to.rows[lane % ppt] = rows;
+              to.factor[lane % ppt] = factor;
+              to.rest[lane % ppt] = rest;
+            }
+            const uint32_t valid = __ballot_sync(0xffffffffu, here && rows) >> (t * ppt);
+            const bool odd = __any_sync(0xffffffffu, here && rest != 1.f), wrong = __any_sync(0xffffffffu, here && bad);
+            if (lane == 0) {
+              to.valid = valid;
+              to.keys = min(ppt, s.pages - (jb + t) * ppt) << p.log_bs;
+              to.unit = unit;
+              to.odd = odd;
+              to.bad = wrong;
+              if (wrong) *status = HCA_ERR_CACHE;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.meta_full[ms]);
+          }
+        }
+      }
+    } else if ((warp == 13 || warp == 14) && busy) {
+      // ------------------------------------------------------------ MMA of tile x
+      // One thread's products run in order: S of tile n + 1 is issued right behind
+      // the O product of tile n, whose P it overwrites.
+      const int x = warp - 13;
+      const uint32_t kv0 = smem_u32(smem), q0 = smem_u32(smem + C::kOffQ) + x * C::kStageBytes;
+      const uint64_t dk = smem_desc_sw128(kv0, 16, 1024);         // K view of stage 0
+      const uint64_t dv = smem_desc_sw128(kv0, kHalfTile, 1024);  // V view of stage 0
+      const uint64_t dq = smem_desc_sw128(q0, 16, 1024);
+      const uint32_t id_s = idesc_f16_f32(128, 128, false, false), id_o = idesc_f16_f32(128, D, false, true);
+      const uint32_t ts = tmem + col_s(x), to = tmem + col_o(x);
+      Walk walk = from;
+      uint32_t n = 0, nseg = 0;
+      bool ok = true, issued = false;
+      if (p.stall && x == 0) {
+        injected_stall(&sh.never, abort_flag, status, p.wait_ns);
+        ok = false;
+      }
+      auto scores = [&](uint32_t t) {
+        const uint32_t st = t % kKvStages;
+        ok = wait_bar(&sh.kv_full[st], (t / kKvStages) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t b = dk + desc_bytes(st * C::kStageBytes);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) mma_ss(ts, dq + kmaj_step(kk), b + kmaj_step(kk), id_s, kk > 0);
+          mma_commit(&sh.s_full[x]);
+        }
+        __syncwarp();
+        issued = true;
+      };
+#pragma unroll 1
+      for (bool last = false; ok && !last; ++nseg) {
+        const Part s = walk.next(sh.table, blockIdx.x);
+        last = s.last;
+        ok = wait_bar(&sh.q_full, nseg & 1);
+        if (ok) scores(n);
+#pragma unroll 1
+        for (int j = s.j0; ok && j < s.j1; ++j, ++n) {
+          const uint32_t st = n % kKvStages;
+#pragma unroll 1
+          for (int h = 0; ok && h < 2; ++h) {
+            ok = wait_bar(&sh.p_full[x][h], n & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t bv = dv + desc_bytes(st * C::kStageBytes + h * 8192);
+            const uint32_t more = j > s.j0 || h > 0;
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) mma_ts(to, ts + h * 64 + kk * 8, bv + mnmaj_step(kk), id_o, more || kk > 0);
+              mma_commit(&sh.pv_done[x][h]);
+              if (h == 1) mma_commit(&sh.kv_empty[st]);
+            }
+            __syncwarp();
+          }
+          if (ok && j + 1 < s.j1) scores(n + 1);
+        }
+      }
+      if (!ok && issued) {
+        volatile int never = 0;
+        if (elect_one()) mma_commit(&sh.drain[x]);
+        __syncwarp();
+        if (lane == 0) mbar_wait(&sh.drain[x], 0, &never, status, 100000000ull);
+        __syncwarp();
+      }
+    } else if (warp == 15 && busy) {
+      // ------------------------------------------------------------ copies
+      const uint32_t bytes = D << p.log_bs;
+      const uint32_t to = smem_u32(smem) + C::kOffRaw + lane * bytes;
+      Walk walk = from;
+      uint32_t n = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (bool last = false; ok && !last;) {
+        const Part s = walk.next(sh.table, blockIdx.x);
+        last = s.last;
+#pragma unroll 1
+        for (int j = s.j0; j < s.j1; ++j, ++n) {
+          const int ms = n % kMetaStages, st = n % kRawStages;
+          ok = wait_bar(&sh.meta_full[ms], (n / kMetaStages) & 1);
+          if (ok && n >= (uint32_t)kRawStages) ok = wait_bar(&sh.raw_empty[st], ((n / kRawStages) - 1) & 1);
+          if (!ok) break;
+          const uint32_t valid = sh.meta[ms].valid;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.raw_full[st], __popc(valid) * bytes);
+          __syncwarp();
+          if ((valid >> lane) & 1) bulk_load(to + st * C::kRawBytes, sh.meta[ms].rows[lane], bytes, &sh.raw_full[st]);
+          __syncwarp();
+        }
+      }
+      // copies in flight end in any case; none may outlive the CTA
+      volatile int never = 0;
+#pragma unroll 1
+      for (uint32_t t = n > (uint32_t)kRawStages ? n - kRawStages : 0; t < n; ++t)
+        if (lane == 0) mbar_wait(&sh.raw_full[t % kRawStages], (t / kRawStages) & 1, &never, status, 100000000ull);
+      __syncwarp();
+    }
+  } else if (warp >= 8) {
+    setmaxnreg_dec<kRegsConv>();
+    if (busy) {
+      // ------------------------------------------------------------ converter
+      // A thread takes 16-byte pieces (16 values) of rows kRowStep apart.  Of 8
+      // neighbouring lanes 4 have pieces of one row and 4 of the next, with
+      // columns 0 .. 63 of the one and 64 .. 127 of the other, so that what they
+      // load and what they store falls into different banks.
+      constexpr int kRowStep = kWG * 16 / D, kPer = kTileKeys / kRowStep;
+      const int ct = tid - 2 * kWG;
+      const int ch = D == 128 ? (ct & 3) | (((ct >> 2) ^ (ct >> 3)) & 1) << 2 : ct & 3;
+      const int row0 = D == 128 ? ((ct >> 2) & 1) | ((ct >> 3) & ~1) : ct >> 2;
+      const uint32_t from0 = smem_u32(smem) + C::kOffRaw + row0 * D + ch * 16;
+      const uint32_t to0 = smem_u32(smem) + (ch >> 2) * kHalfTile + row0 * 128;
+      const uint32_t swz0 = (((2 * (ch & 3)) ^ (row0 & 7)) << 4);  // the other piece's differs in one bit
+      static_assert(kRowStep % 8 == 0, "a thread's rows have one swizzle");
+      // q: D / 8 neighbouring lanes copy a row's 16-byte pieces
+      constexpr int kLanes = D / 8, kStep = kWG / kLanes;
+      const int q_ch = ct % kLanes, q_row = ct / kLanes;
+      const uint32_t q0 = smem_u32(smem) + C::kOffQ;
+      Walk walk = from;
+      uint32_t n = 0;
+      int nseg = 0;
+      // no way out when a wait has given up: the warps meet at barriers
+#pragma unroll 1
+      for (bool last = false; !last; ++nseg) {
+        const Part s = walk.next(sh.table, blockIdx.x);
+        last = s.last;
+        if (nseg > 0) {
+          // the last segment's scores have been made and its factors read
+          (void)wait_bar(&sh.q_read, (nseg - 1) & 1);
+          (void)wait_bar(&sh.s_full[0], (n - 1) & 1);
+          (void)wait_bar(&sh.s_full[1], (n - 1) & 1);
+        }
+        const __nv_bfloat16 *q = p.q + (size_t)s.row0 * D + q_ch * 8;
+#pragma unroll 4
+        for (int r = q_row; r < kRowTile; r += kStep) {
+          const uint32_t to = q0 + (r >> 7) * C::kStageBytes + (q_ch >> 3) * kHalfTile + (r & 127) * 128 + (((q_ch & 7) ^ (r & 7)) << 4);
+          cp_async_16(to, r < s.rows ? q + (size_t)r * D : p.q, r < s.rows ? 16 : 0);
+        }
+        cp_async_wait();
+        named_bar_sync(kBarQ, kWG);
+        // bf16 -> fp16 with a factor for each row: the largest |q| becomes 224 ..
+        // 448; a negative scale goes into q's sign
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t at_row = q0 + x * C::kStageBytes + ct * 128;
+          auto piece_at = [&](int c) { return at_row + (c >> 3) * kHalfTile + (((c & 7) ^ (ct & 7)) << 4); };
+          uint32_t amax = 0;
+#pragma unroll 4
+          for (int c = 0; c < kLanes; ++c) {
+            uint32_t w[4];
+            ld_shared(piece_at(c), w);
+            amax = bf16x2_max(amax, bf16x2_max(bf16x2_max(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                               bf16x2_max(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu)));
+          }
+          const int ex = scale_exponent(__uint_as_float(max(amax & 0xffffu, amax >> 16) << 16), kLeastQExp);
+          const float inv = p.scale < 0.f ? -exp2_int(-ex) : p.scale > 0.f ? exp2_int(-ex) : 0.f;
+          sh.q_factor[x * kWG + ct] = exp2_int(ex) * fabsf(p.scale) * 1.4426950408889634f;
+          const uint64_t inv2 = f32x2(__float_as_uint(inv), __float_as_uint(inv));
+#pragma unroll 2
+          for (int c = 0; c < kLanes; ++c) {
+            uint32_t w[4], f[4];
+            ld_shared(piece_at(c), w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float lo, hi;
+              f32x2_split(fmul2(f32x2(w[e] << 16, w[e] & 0xffff0000u), inv2), lo, hi);
+              f[e] = f16x2_rn(lo, hi);
+            }
+            st_shared(piece_at(c), f[0], f[1], f[2], f[3]);
+          }
+        }
+        fence_async_smem();
+        mbar_arrive(&sh.q_full);
+#pragma unroll 1
+        for (int j = s.j0; j < s.j1; ++j, ++n) {
+          const int ms = n % kMetaStages, rs = n % kRawStages, st = n % kKvStages;
+          (void)wait_bar(&sh.raw_full[rs], (n / kRawStages) & 1);
+          if (n >= (uint32_t)kKvStages) (void)wait_bar(&sh.kv_empty[st], ((n / kKvStages) - 1) & 1);
+          const uint32_t valid = sh.meta[ms].valid;
+          const bool full = valid == (1u << ppt) - 1u;
+          const uint32_t src = from0 + rs * C::kRawBytes, dst = to0 + st * C::kStageBytes;
+#pragma unroll 4
+          for (int i = 0; i < kPer; ++i) {
+            uint32_t raw[4], f[8];
+            ld_shared(src + i * kRowStep * D, raw);
+            const int page = (row0 + i * kRowStep) >> p.log_bs;
+            if (!full && !((valid >> page) & 1)) raw[0] = raw[1] = raw[2] = raw[3] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) e4m3x4_to_f16(raw[e], f[2 * e], f[2 * e + 1]);
+            const uint32_t factor = sh.meta[ms].factor[page];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = f16x2_mul(f[e], factor);
+            const uint32_t at = dst + i * kRowStep * 128;
+            st_shared(at + swz0, f[0], f[1], f[2], f[3]);
+            st_shared(at + (swz0 ^ 16), f[4], f[5], f[6], f[7]);
+          }
+          mbar_arrive(&sh.raw_empty[rs]);
+          fence_async_smem();
+          mbar_arrive(&sh.kv_full[st]);
+        }
+      }
+    }
+  } else {
+    setmaxnreg_inc<kRegsSoft>();
+    if (busy) {
+      // ------------------------------------------------------------ softmax
+      // Rows beyond the prefix's are zero in Q: their results are not written.
+      const int x = warp >> 2, row = tid & (kWG - 1);
+      const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16), scol = lane_addr + col_s(x), ocol = lane_addr + col_o(x);
+      Walk walk = from;
+      uint32_t n = 0;
+      int nseg = 0;
+#pragma unroll 1
+      for (bool last = false; !last; ++nseg) {
+        const Part s = walk.next(sh.table, blockIdx.x);
+        last = s.last;
+        float m_run = -INFINITY, m_use = 0.f, l_run = 0.f;  // m_use: what is subtracted
+        int unit = 0;
+        (void)wait_bar(&sh.q_full, nseg & 1);
+        const float cs = sh.q_factor[x * kWG + row];
+        mbar_arrive(&sh.q_read);
+#pragma unroll 1
+        for (int j = s.j0; j < s.j1; ++j, ++n) {
+          const int ms = n % kMetaStages;
+          const TileMeta &meta = sh.meta[ms];
+          (void)wait_bar(&sh.meta_full[ms], (n / kMetaStages) & 1);
+          unit = meta.unit;
+          const int odd = meta.odd, keys = meta.keys;
+          if (meta.bad) l_run = __int_as_float(0x7fc00000);
+          const float ck = fminf(fmaxf(cs * exp2_int(unit), FLT_MIN), FLT_MAX);
+          (void)wait_bar(&sh.s_full[x], n & 1);
+          tc_fence_after();
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t sv[64];
+            tmem_ld32(scol + h * 64, *reinterpret_cast<uint32_t(*)[32]>(sv));
+            tmem_ld32(scol + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
+            tmem_wait_ld();
+            if (keys < kTileKeys) {
+#pragma unroll
+              for (int y = 0; y < 64; ++y)
+                if (h * 64 + y >= keys) sv[y] = 0xff800000u;
+            }
+            if (odd) {
+#pragma unroll
+              for (int c = 0; c < 64; c += 16) {
+                const float rest = meta.rest[(h * 64 + c) >> p.log_bs];
+#pragma unroll
+                for (int y = 0; y < 16; ++y) sv[c + y] = __float_as_uint(__uint_as_float(sv[c + y]) * rest);
+              }
+            }
+            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+            for (int y = 0; y < 64; y += 4) {
+              m0 = fmax3(m0, __uint_as_float(sv[y]), __uint_as_float(sv[y + 1]));
+              m1 = fmax3(m1, __uint_as_float(sv[y + 2]), __uint_as_float(sv[y + 3]));
+            }
+            const float mx = fmaxf(m0, m1) * ck;
+            // raise the reference (seldom); the sums made with the old one follow
+            const bool raise = mx > m_run + kRaiseLog2;  // at first: any key
+            if (__any_sync(0xffffffffu, raise)) {
+              const bool had = raise && m_run > -INFINITY;  // else O holds nothing of this row yet
+              const float f = had ? ex2_approx(m_run - mx) : 1.f;
+              l_run *= f;
+              if (raise) m_run = mx;
+              m_use = m_run == -INFINITY ? 0.f : m_run - kBias;
+              if (__any_sync(0xffffffffu, had)) {
+                (void)wait_bar(&sh.pv_done[x][h ^ 1], (h ? n : n - 1) & 1);
+                tc_fence_after();
+                scale_o<D>(ocol, f);
+              }
+            }
+            const uint64_t ck2 = f32x2(__float_as_uint(ck), __float_as_uint(ck));
+            const uint64_t nm2 = f32x2(__float_as_uint(-m_use), __float_as_uint(-m_use));
+            uint64_t acc[2] = {0, 0};
+            const uint32_t pcol = scol + h * 64;
+            auto probabilities = [&](auto scaled) {
+#pragma unroll
+              for (int c = 0; c < 64; c += 32) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int y = 0; y < 32; y += 2) {
+                  float t0, t1;
+                  f32x2_split(ffma2(f32x2(sv[c + y], sv[c + y + 1]), ck2, nm2), t0, t1);
+                  float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
+                  acc[(y >> 1) & 1] = fadd2(acc[(y >> 1) & 1], f32x2(__float_as_uint(e0), __float_as_uint(e1)));
+                  if constexpr (decltype(scaled)::value) {
+                    const float rest = meta.rest[(h * 64 + c + y) >> p.log_bs];
+                    e0 *= rest;
+                    e1 *= rest;
+                  }
+                  pk[y >> 1] = f16x2_rn(e0, e1);
+                }
+                tmem_st16(pcol + c / 2, pk);
+              }
+            };
+            if (odd) probabilities(std::true_type());
+            else probabilities(std::false_type());
+            float a, b;
+            f32x2_split(fadd2(acc[0], acc[1]), a, b);
+            l_run += a + b;
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&sh.p_full[x][h]);
+          }
+          mbar_arrive(&sh.meta_empty[ms]);
+        }
+        if (*abort_flag) l_run = __int_as_float(0x7fc00000);
+        const bool mine = x * kWG + row < s.rows;
+        if (mine) p.part_ml[(size_t)s.slot * kRowTile + x * kWG + row] = make_float2(m_use, l_run);
+        const float inv = exp2_int(unit) / l_run;
+        (void)wait_bar(&sh.pv_done[x][1], (n - 1) & 1);
+        tc_fence_after();
+        // O leaves through shared memory, 64 bytes of a row at a time, so that four
+        // lanes write a row's: a store to 32 rows takes 32 cycles.
+        float *out = p.part_o + ((size_t)s.slot * kRowTile + x * kWG) * D;
+        const int nrows = s.rows - x * kWG;
+        const uint32_t buf = smem_u32(sh.out) + x * kWG * 64, at = buf + row * 64, swz = (row >> 1) & 3;
+        const int piece = lane & 3;
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t o[16];
+          tmem_ld16(ocol + c * 16, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * inv);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) st_shared(at + ((y ^ swz) << 4), o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = (warp & 3) * 32 + i * 8 + (lane >> 2);
+            uint32_t v[4];
+            ld_shared(buf + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4), v);
+            if (r < nrows) *reinterpret_cast<uint4 *>(out + (size_t)r * D + c * 16 + piece * 4) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && sh.abort) atomicExch(status, HCA_ERR_TIMEOUT);
+  if (warp == 15) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmem);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// join: out = (w_0 o_0 + sum 2^(m_i - M) l_i o_i) / (w_0 + sum 2^(m_i - M) l_i) of a
+// row's own keys (w_0 = 2^(lse - M)) and the parts of its prefix
+// ---------------------------------------------------------------------------
+constexpr int kJoinThreads = 256;
+static_assert(kJoinThreads >= kSharedMaxGroups, "a thread for each prefix");
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const SharedParams p) {
+  __shared__ Table table;
+  constexpr int kLanes = D / 4, kRows = kJoinThreads / kLanes;
+  constexpr float kLog2e = 1.4426950408889634f;
+  const int tid = threadIdx.x, l = tid % kLanes;
+  pdl_wait();
+  const int units = make_table(p, table);
+  int worst = p.own->status;
+  for (int i = tid; i < p.grid; i += kJoinThreads) worst = max(worst, p.err[i] == HCA_ERR_TIMEOUT ? 1000 : p.err[i]);
+  const bool late = __syncthreads_or(worst == 1000 || worst == HCA_ERR_TIMEOUT), wrong = __syncthreads_or(worst != HCA_OK);
+  if (blockIdx.x == 0 && tid == 0) *p.status = late ? HCA_ERR_TIMEOUT : wrong ? HCA_ERR_CACHE : HCA_OK;
+  const bool refused = units < 0 || p.own->ntiles < 0 || late;  // then all rows are NaN
+  const int live = refused ? p.N : min(max(p.start[p.R], 0), p.N);
+  const int quota = units_per_cta(max(units, 0), p.grid);
+  const long long rows = (long long)live * p.H;
+  for (long long row = (long long)blockIdx.x * kRows + tid / kLanes; row < rows; row += (long long)gridDim.x * kRows) {
+    float4 o = *reinterpret_cast<const float4 *>(p.own_out + row * D + 4 * l);
+    float lse = p.own_lse[row];
+    if (refused) {
+      lse = __int_as_float(0x7fc00000);
+      o = make_float4(lse, lse, lse, lse);
+    } else {
+      int lo = 0, hi = p.G;  // the row's prefix
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (table.g[mid].row0 <= row) lo = mid; else hi = mid;
+      }
+      const Prefix x = table.g[lo];
+      if (x.tiles > 0) {
+        const int r = (int)(row - x.row0), rt = r / kRowTile, u0 = x.line0 + rt * x.tiles;
+        const int first = u0 / quota, n = (u0 + x.tiles - 1) / quota - first + 1;
+        const size_t slot = (size_t)(x.rt0 + rt + first) * kRowTile + r % kRowTile;  // the next part's is 256 further
+        const float m0 = lse * kLog2e;
+        float M = m0;
+        for (int i = 0; i < n; ++i) M = fmaxf(M, p.part_ml[slot + (size_t)i * kRowTile].x);
+        float w = exp2f(m0 - M), sum = w;
+        o.x *= w; o.y *= w; o.z *= w; o.w *= w;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+          const size_t at = slot + (size_t)i * kRowTile;
+          const float2 ml = p.part_ml[at];
+          const float4 v = *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * l);
+          w = exp2f(ml.x - M) * ml.y;
+          sum += w;
+          o.x = fmaf(w, v.x, o.x); o.y = fmaf(w, v.y, o.y); o.z = fmaf(w, v.z, o.z); o.w = fmaf(w, v.w, o.w);
+        }
+        const float inv = 1.f / sum;
+        o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+        lse = (M + log2f(sum)) * 0.69314718055994531f;
+      }
+    }
+    *reinterpret_cast<uint2 *>(p.out + row * D + 4 * l) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+    if (l == 0) p.lse[row] = lse;
+  }
+}
+
+struct Layout {
+  size_t off_own, off_out, off_lse, off_err, off_ml, off_o, bytes;
+};
+
+Layout layout_of(int N, int R, int H, int D, int G) {
+  Layout l;
+  const size_t rows = (size_t)N * H, slots = rows / kRowTile + G + kMaxGrid;
+  size_t at = kHeaderBytes;
+  l.off_own = at;
+  at += align_up(cache_attn_ws_bytes(N, R, H, D, HCA_BF16));
+  l.off_out = at;
+  at += align_up(rows * D * sizeof(float));
+  l.off_lse = at;
+  at += align_up(rows * sizeof(float));
+  l.off_err = at;
+  at += align_up(kMaxGrid * sizeof(int32_t));
+  l.off_ml = at;
+  at += align_up(slots * kRowTile * sizeof(float2));
+  l.off_o = at;
+  at += align_up(slots * kRowTile * D * sizeof(float));
+  l.bytes = at;
+  return l;
+}
+
+template <int D>
+cudaError_t launch(const CacheAttnArgs &a, SharedParams &p, int sms, cudaStream_t st) {
+  using C = Cfg<D>;
+  static SmemAttrOnce attr;
+  cudaError_t e = attr.ensure(reinterpret_cast<const void *>(hca_cache_prefix_kernel<D>), C::kSmem);
+  if (e != cudaSuccess) return e;
+  {
+    ProfScope prof(kKCachePrefix, st);
+    hca_cache_prefix_kernel<D><<<p.grid, kThreads, C::kSmem, st>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  e = cache_attn(a, st);
+  if (e != cudaSuccess) return e;
+  ProfScope prof(kKCacheJoin, st);
+  const long long blocks = ((long long)p.N * p.H * (D / 4) + kJoinThreads - 1) / kJoinThreads;
+  return launch_behind(hca_cache_join_kernel<D>, dim3((unsigned)std::min<long long>(blocks, 8ll * sms)), kJoinThreads, 0, st, p);
+}
+
+}  // namespace
+
+int cache_shared_max_groups() { return kSharedMaxGroups; }
+
+size_t cache_attn_shared_ws_bytes(int N, int R, int H, int D, int G, int dtype) {
+  return dtype == HCA_F32 ? cache_attn_ws_bytes(N, R, H, D, dtype) : layout_of(N, R, H, D, G).bytes;
+}
+
+cudaError_t cache_attn_shared(const CacheAttnArgs &args, cudaStream_t st) {
+  CacheAttnArgs a = args;
+  if (a.dtype == HCA_F32) {
+    // its multiplications are what bounds fp32, and they are the same
+    a.share.apart = 0;
+    return cache_attn(a, st);
+  }
+  const Layout l = layout_of(a.N, a.R, a.H, a.D, a.share.G);
+  char *ws = static_cast<char *>(a.ws);
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorNoDevice;
+  SharedParams p;
+  p.q = static_cast<const __nv_bfloat16 *>(a.q);
+  p.start = a.start; p.first = a.share.first; p.cols = a.share.cols;
+  p.comp = a.comp;
+  p.err = reinterpret_cast<int32_t *>(ws + l.off_err);
+  p.part_ml = reinterpret_cast<float2 *>(ws + l.off_ml);
+  p.part_o = reinterpret_cast<float *>(ws + l.off_o);
+  p.own_out = reinterpret_cast<const float *>(ws + l.off_out);
+  p.own_lse = reinterpret_cast<const float *>(ws + l.off_lse);
+  p.own = reinterpret_cast<const SchedHeader *>(ws + l.off_own);
+  p.status = reinterpret_cast<int32_t *>(ws);
+  p.out = static_cast<__nv_bfloat16 *>(a.out);
+  p.lse = a.lse;
+  p.N = a.N; p.R = a.R; p.H = a.H; p.D = a.D; p.G = a.share.G;
+  p.log_bs = 0;
+  while ((1 << p.log_bs) < a.bs) ++p.log_bs;
+  p.grid = std::min(sms, kMaxGrid);
+  p.scale = a.scale;
+  p.wait_ns = std::min<uint64_t>(a.wait_ns, 4000000000u);
+  p.stall = a.stall;
+  a.stall = 0;
+  a.out = ws + l.off_out;
+  a.lse = reinterpret_cast<float *>(ws + l.off_lse);
+  a.ws = ws + l.off_own;
+  a.share.apart = 1;
+  return a.D == 64 ? launch<64>(a, p, sms, st) : launch<128>(a, p, sms, st);
+}
+
+}  // namespace hca

@@ -12,7 +12,7 @@ namespace hca {
 enum KernelId {
   kKPrep = 0, kKFwdTc, kKBwdDq, kKBwdDkv, kKBwdReduce, kKSimtFwd, kKSimtBwd, kKVisibility, kKCompress,
   kKIndexScore, kKIndexTopk, kKCsaUnion, kKCsaDckv, kKCachePlan, kKCacheAppend, kKCacheSched, kKCacheAttn,
-  kKCacheSimt, kKCacheCombine, kKNormRope, kKNormRopeBwd, kNumKernels
+  kKCacheSimt, kKCacheCombine, kKNormRope, kKNormRopeBwd, kKCachePrefix, kKCacheJoin, kNumKernels
 };
 
 // Brackets the launches issued during its lifetime with CUDA events on `st`
@@ -175,6 +175,11 @@ struct CacheSet {
   const int32_t *table;  // [R][cols]
   int nblocks, cols;
 };
+struct CacheShare {
+  const int32_t *first, *cols;  // [G+1] requests, [G] common columns of their compressed tables
+  int G;                        // 0: nothing is shared
+  int apart;                    // hca_cache_attn's kernels leave the common columns out and write fp32 rows
+};
 struct CacheAttnArgs {
   const void *q;
   const int32_t *start, *held;
@@ -187,9 +192,14 @@ struct CacheAttnArgs {
   void *ws;
   uint64_t wait_ns;
   int stall;
+  CacheShare share;
 };
 size_t cache_attn_ws_bytes(int N, int R, int H, int D, int dtype);
 cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st);
+// with prefixes that requests share (hca_cache_shared.cu)
+int cache_shared_max_groups();
+size_t cache_attn_shared_ws_bytes(int N, int R, int H, int D, int G, int dtype);
+cudaError_t cache_attn_shared(const CacheAttnArgs &a, cudaStream_t st);
 
 // tensor-core (tcgen05) path
 bool tc_fwd_supported(int H, int D, int dtype);

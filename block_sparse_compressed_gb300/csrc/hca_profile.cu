@@ -43,7 +43,7 @@ const char *kNames[kNumKernels] = {"hca_prep",       "hca_fwd_tc",   "hca_bwd_dq
                                    "hca_compress",   "hca_index_score", "hca_index_topk",   "hca_csa_union",
                                    "hca_csa_dckv",   "hca_cache_plan", "hca_cache_append", "hca_cache_sched",
                                    "hca_cache_attn", "hca_cache_simt", "hca_cache_combine", "hca_norm_rope",
-                                   "hca_norm_rope_bwd"};
+                                   "hca_norm_rope_bwd", "hca_cache_prefix", "hca_cache_join"};
 
 }  // namespace
 

@@ -36,7 +36,7 @@ EXPORTS = ("hca_status_string", "hca_version", "hca_workspace_size", "hca_query_
            "hca_indexer_topk", "hca_csa_workspace_size", "hca_csa_attn_fwd", "hca_csa_attn_bwd",
            "hca_cache_plan_workspace_size", "hca_cache_plan", "hca_cache_append_workspace_size", "hca_cache_append",
            "hca_cache_attn_workspace_size", "hca_cache_attn", "hca_norm_rope_fwd", "hca_norm_rope_workspace_size",
-           "hca_norm_rope_bwd", "hca_rope")
+           "hca_norm_rope_bwd", "hca_rope", "hca_cache_attn_shared_workspace_size", "hca_cache_attn_shared")
 
 # failure-path test hooks (hca_test_inject)
 INJECT_RESET, INJECT_LAUNCH_FAILURE, INJECT_STALL, INJECT_WAIT_LIMIT_NS, INJECT_CSA_UNION = 0, 1, 2, 3, 4
@@ -140,6 +140,10 @@ def load(path: str = LIB_PATH):
             lib.hca_norm_rope_bwd.restype = I
             lib.hca_rope.argtypes = [P] * 8 + [I] * 11 + [P]
             lib.hca_rope.restype = I
+            lib.hca_cache_attn_shared_workspace_size.argtypes = [I, I, I, I, I, I]
+            lib.hca_cache_attn_shared_workspace_size.restype = Z
+            lib.hca_cache_attn_shared.argtypes = [P, P, P, P, P, P, I, I, P, P, P, I, I, P, P, P, P, I, I, I, I, I, I, I, I, F, I, P, Z, P]
+            lib.hca_cache_attn_shared.restype = I
             py = _extension()
             if py is not None:
                 py.bind(*(ctypes.cast(getattr(lib, f), P).value for f in (
@@ -866,6 +870,47 @@ def hca_cache_attn(q: torch.Tensor, start: torch.Tensor, held: torch.Tensor, raw
         _check(rc, "hca_cache_attn")
     if check:
         _check(hca_workspace_status(ws), "hca_cache_attn (device)")
+    return out, lse
+
+
+@functools.lru_cache(maxsize=4096)
+def _attn_shared_ws_bytes(N: int, R: int, H: int, D: int, G: int, dt: int) -> int:
+    n = load().hca_cache_attn_shared_workspace_size(N, R, H, D, G, dt)
+    if n == 0:
+        raise HCAError(8, "hca_cache_attn_shared_workspace_size")
+    return n
+
+
+def hca_cache_attn_shared(q: torch.Tensor, start: torch.Tensor, held: torch.Tensor, raw, comp, first: torch.Tensor,
+                          shared_cols: torch.Tensor, W: int, m: int, scale: float, out: Optional[torch.Tensor] = None,
+                          lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                          check: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+    """hca_cache_attn for requests that begin with the same blocks of compressed
+    entries, which are attended once for all of them (include/hca.h,
+    hca_cache_attn_shared): requests first[g] .. first[g+1] - 1 have the first
+    shared_cols[g] columns of their compressed tables in common; first[G+1] and
+    shared_cols[G] are int32 tensors.  Results as hca_cache_attn's."""
+    lib = _lib or load()
+    dev = q.device
+    if q.dim() != 3 or held.dim() != 1 or raw[0].dim() != 3:
+        raise ValueError("q must be [N,H,D], held [R] and the raw pool [nblocks,bs,D]")
+    if comp is None or shared_cols.dim() != 1:
+        raise ValueError("comp is required, and shared_cols must be [G]")
+    N, H, D = q.shape
+    R, bs, G = held.shape[0], raw[0].shape[1], shared_cols.shape[0]
+    dt = _dtype_code(q)
+    args = (*_cache_args("raw", raw, R, bs, D, dev), *_cache_args("comp", comp, R, bs, D, dev),
+            _fits(first, "first", (G + 1,), _I32, dev), _fits(shared_cols, "shared_cols", (G,), _I32, dev))
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((N, H), dtype=_F32, device=dev) if lse is None else lse
+    ws = torch.empty(_attn_shared_ws_bytes(N, R, H, D, G, dt), dtype=torch.uint8, device=dev) if ws is None else ws
+    rc = _enqueue(dev, lib.hca_cache_attn_shared, _fits(q, "q", (N, H, D), q.dtype, dev), _fits(start, "start", (R + 1,), _I32, dev),
+                  _fits(held, "held", (R,), _I32, dev), *args, _fits(out, "out", (N, H, D), q.dtype, dev),
+                  _fits(lse, "lse", (N, H), _F32, dev), N, R, H, D, G, _int(W), _int(m), bs, scale, dt, *_scratch(ws, dev))
+    if rc != 0:
+        _check(rc, "hca_cache_attn_shared")
+    if check:
+        _check(hca_workspace_status(ws), "hca_cache_attn_shared (device)")
     return out, lse
 
 

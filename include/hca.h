@@ -426,6 +426,32 @@ HCA_API int hca_cache_attn(const void *q, const int32_t *start, const int32_t *h
                            int comp_cols, void *out, float *lse, int N, int R, int H, int D, int W, int m, int bs,
                            float scale, int dtype, void *workspace, size_t workspace_bytes, void *stream);
 
+/* hca_cache_attn for requests that begin with the same tokens (a system prompt,
+ * one long document): the entries that they have in common are attended once for
+ * all of them.  Arguments, results and errors are those of hca_cache_attn with a
+ * compressed set, and so is what is computed; besides
+ *   first [G+1]       request first[g] is the first of prefix g's, which are
+ *                     adjacent: first[0] = 0, first[G] = R (device int32, like all
+ *                     lengths)
+ *   shared_cols [G]   so many first columns of the compressed tables of prefix g's
+ *                     requests hold the same blocks, all of whose entries every
+ *                     token sees, shared_cols[g] * bs * m <= held[r] + 1; 0: none.
+ *                     (A prefix's last block is common if it is full; what is behind
+ *                     it belongs to the requests, and so do their raw rows.)
+ * G is at most 256 (HCA_ERR_SHAPE); with G = 0 nothing is shared.  The common
+ * columns are read in the table of the prefix's first request.  Values of first and
+ * shared_cols that do not fit make all N rows of out and lse NaN, as lengths out of
+ * range do (HCA_ERR_CACHE).  bf16: a prefix's part is rounded to fp32 and joined
+ * with the request's own; fp32 has the same arithmetic as hca_cache_attn.
+ * Workspace: hca_cache_attn_shared_workspace_size bytes (0: unsupported sizes). */
+HCA_API size_t hca_cache_attn_shared_workspace_size(int N, int R, int H, int D, int G, int dtype);
+HCA_API int hca_cache_attn_shared(const void *q, const int32_t *start, const int32_t *held, const void *raw_pool,
+                                  const float *raw_scale, const int32_t *raw_table, int raw_blocks, int raw_cols,
+                                  const void *comp_pool, const float *comp_scale, const int32_t *comp_table,
+                                  int comp_blocks, int comp_cols, const int32_t *first, const int32_t *shared_cols,
+                                  void *out, float *lse, int N, int R, int H, int D, int G, int W, int m, int bs,
+                                  float scale, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Failure-path test hooks.  "Add HCA Static Compilation for Splash Attention
  * [Deepseek v4]" (Description, validation-guard bullet) wants unsupported or
  * failing cases reported as errors rather than crashes; the tests that check
