@@ -18,10 +18,10 @@
 //
 // A CTA has two tiles A and B of 128 rows and one stream of keys, 512 threads:
 //   warps 0 - 3, 4 - 7   softmax of A, of B: a thread has a row
-//   warps 8 - 11         converter: e4m3 -> fp16 key tiles, and q of a segment
+//   warps 8 - 11         converter: e4m3 -> fp16 key tiles
 //   warp 12              pages: block ids and scales, looked up ahead
 //   warps 13, 14         MMA issuers of A and of B
-//   warp 15              copies of pages (bulk), tensor memory
+//   warp 15              tensor memory
 // S of a tile is 128 columns of tensor memory, softmaxed in two halves of 64 keys
 // whose P (fp16) takes the first half of their columns: the first half's product
 // with K runs while the second half is worked on, and one tile's products while
@@ -45,13 +45,13 @@ namespace {
 
 constexpr int kRowTile = 256, kSharedMaxGroups = 256, kMaxGrid = 256;
 constexpr int kWG = 128, kThreads = 4 * kWG;
-constexpr int kMetaStages = 4, kKvStages = 3, kRawStages = 2;
+constexpr int kMetaStages = 8, kKvStages = 4;
 constexpr int kRegsSoft = 168, kRegsConv = 88, kRegsIssue = 88;
 static_assert(2 * kRegsSoft + kRegsConv + kRegsIssue <= 4 * 128, "register split must fit the launch");
 constexpr uint32_t kTmem = 512;
-__device__ __forceinline__ constexpr uint32_t col_s(int x) { return 128u * x; }
+// S of tile x and half h (P takes the first half of its columns), O of tile x
+__device__ __forceinline__ constexpr uint32_t col_s(int x, int h) { return 128u * x + 64u * h; }
 __device__ __forceinline__ constexpr uint32_t col_o(int x) { return 256u + 128u * x; }
-enum { kBarQ = 1, kBarOut = 2 };  // named barriers
 
 struct SharedParams {
   const __nv_bfloat16 *q;
@@ -69,6 +69,7 @@ struct SharedParams {
   float scale;
   uint64_t wait_ns;
   int stall;
+  int merge;        // the requests' own keys are done: row tiles that are not cut are finished here
 };
 
 // A prefix with its rows and its place in the line.
@@ -82,6 +83,7 @@ struct Prefix {
 struct Table {
   Prefix g[kSharedMaxGroups];
   long long tmp[33];
+  int row_tiles;    // of all prefixes, those without common entries among them
 };
 
 // The line, by all threads of a block (at least kSharedMaxGroups): its units, -1 if
@@ -105,7 +107,7 @@ __device__ __forceinline__ int make_table(const SharedParams &p, Table &t) {
         x.request = f0;
         ok = ((long long)c << p.log_bs) <= kMaxPos;
         x.tiles = ok ? ((c << p.log_bs) + kTileKeys - 1) / kTileKeys : 0;
-        rts = x.tiles > 0 ? (x.rows + kRowTile - 1) / kRowTile : 0;
+        rts = (x.rows + kRowTile - 1) / kRowTile;
         units = (long long)rts * x.tiles;
       }
     }
@@ -117,6 +119,7 @@ __device__ __forceinline__ int make_table(const SharedParams &p, Table &t) {
   ok = ok && all < kMaxTiles;
   x.line0 = ok ? (int)line0 : 0;
   if (i < p.G) t.g[i] = x;
+  if (i == 0) t.row_tiles = (int)nrt;
   __syncthreads();
   return ok ? (int)all : -1;
 }
@@ -129,6 +132,7 @@ struct Part {
   int j0, j1;          // key tiles
   int slot;
   int pages, request;
+  bool whole;          // all key tiles of the row tile
   bool last;           // of the CTA's
 };
 
@@ -141,6 +145,7 @@ struct Walk {
     Part s;
     s.j0 = u - x.line0 - rt * x.tiles;
     s.j1 = min(x.tiles, s.j0 + (end - u));
+    s.whole = s.j0 == 0 && s.j1 == x.tiles;
     s.row0 = x.row0 + rt * kRowTile;
     s.rows = min(kRowTile, x.rows - rt * kRowTile);
     s.slot = x.rt0 + rt + cta;
@@ -152,14 +157,14 @@ struct Walk {
   }
 };
 
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kStageBytes = kHalves * kHalfTile;  // fp16 tile of 128 keys, or of 128 rows of q
   static constexpr int kOffQ = kKvStages * kStageBytes;
-  static constexpr int kOffRaw = kOffQ + 2 * kStageBytes;
-  static constexpr int kRawBytes = kTileKeys * D;
-  static constexpr int kSmem = kOffRaw + kRawStages * kRawBytes + 1024;
+  static constexpr int kSmem = kOffQ + 2 * kStageBytes + 1024;
 };
 
 struct TileMeta {
@@ -174,12 +179,11 @@ struct TileMeta {
 
 struct Shared {
   uint4 out[2 * kWG * 4];  // O on its way out: 64 bytes of each row
+  float own[kRowTile];     // what a row's own part counts
   uint64_t meta_full[kMetaStages], meta_empty[kMetaStages];
-  uint64_t raw_full[kRawStages], raw_empty[kRawStages];
   uint64_t kv_full[kKvStages], kv_empty[kKvStages];
-  uint64_t q_full, q_read, s_full[2], p_full[2][2], pv_done[2][2], drain[2], never;
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], drain[2], never;
   TileMeta meta[kMetaStages];
-  float q_factor[kRowTile];
   Table table;
   uint32_t tmem_base;
   int abort;
@@ -191,29 +195,24 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Shared sh;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   volatile int *abort_flag = &sh.abort;
   int32_t *status = &p.err[blockIdx.x];
 
   if (tid == 0) {
     for (int s = 0; s < kMetaStages; ++s) {
       mbar_init(&sh.meta_full[s], 1);
-      mbar_init(&sh.meta_empty[s], 2 * kWG);  // the softmax warps are the last to read a tile's pages
-    }
-    for (int s = 0; s < kRawStages; ++s) {
-      mbar_init(&sh.raw_full[s], 1);
-      mbar_init(&sh.raw_empty[s], kWG);
+      mbar_init(&sh.meta_empty[s], 8);  // the softmax warps are the last to read a tile's pages
     }
     for (int s = 0; s < kKvStages; ++s) {
-      mbar_init(&sh.kv_full[s], kWG);
+      mbar_init(&sh.kv_full[s], 4);
       mbar_init(&sh.kv_empty[s], 2);
     }
-    mbar_init(&sh.q_full, kWG);
-    mbar_init(&sh.q_read, 2 * kWG);
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&sh.s_full[x], 1);
+      mbar_init(&sh.q_full[x], 4);
       for (int h = 0; h < 2; ++h) {
-        mbar_init(&sh.p_full[x][h], kWG);
+        mbar_init(&sh.s_full[x][h], 1);
+        mbar_init(&sh.p_full[x][h], 4);
         mbar_init(&sh.pv_done[x][h], 1);
       }
       mbar_init(&sh.drain[x], 1);
@@ -231,15 +230,15 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem_base;
+  const uint32_t tmem = uniform(sh.tmem_base);
   const int quota = units_per_cta(max(units, 0), p.grid);
   const long long c0 = (long long)quota * blockIdx.x;
   const bool busy = c0 < units;
   const Walk from = {(int)c0, (int)min(c0 + quota, (long long)max(units, 0)), 0};
 
   const uint32_t limit_ns = (uint32_t)p.wait_ns;
-  auto wait_bar = [&](uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait_idle(bar, parity, abort_flag, limit_ns));
+  auto wait_bar = [&](uint64_t *bar, uint32_t parity) {  // mostly there already
+    return __all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity) || mbar_wait_idle(bar, parity, abort_flag, limit_ns));
   };
   const int ppt = kTileKeys >> p.log_bs;  // pages of a tile: 1 .. 8
   if (warp >= 12) {
@@ -323,99 +322,69 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
       }
     } else if ((warp == 13 || warp == 14) && busy) {
       // ------------------------------------------------------------ MMA of tile x
-      // One thread's products run in order: S of tile n + 1 is issued right behind
-      // the O product of tile n, whose P it overwrites.
+      // Its products run in order: S of half u + 2 is issued right behind the
+      // O product of half u, whose P it overwrites.
       const int x = warp - 13;
       const uint32_t kv0 = smem_u32(smem), q0 = smem_u32(smem + C::kOffQ) + x * C::kStageBytes;
       const uint64_t dk = smem_desc_sw128(kv0, 16, 1024);         // K view of stage 0
       const uint64_t dv = smem_desc_sw128(kv0, kHalfTile, 1024);  // V view of stage 0
       const uint64_t dq = smem_desc_sw128(q0, 16, 1024);
-      const uint32_t id_s = idesc_f16_f32(128, 128, false, false), id_o = idesc_f16_f32(128, D, false, true);
-      const uint32_t ts = tmem + col_s(x), to = tmem + col_o(x);
-      Walk walk = from;
-      uint32_t n = 0, nseg = 0;
-      bool ok = true, issued = false;
-      if (p.stall && x == 0) {
-        injected_stall(&sh.never, abort_flag, status, p.wait_ns);
-        ok = false;
-      }
-      auto scores = [&](uint32_t t) {
-        const uint32_t st = t % kKvStages;
-        ok = wait_bar(&sh.kv_full[st], (t / kKvStages) & 1);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t b = dk + desc_bytes(st * C::kStageBytes);
-        if (elect_one()) {
+      const uint32_t id_s = idesc_f16_f32(128, 64, false, false), id_o = idesc_f16_f32(128, D, false, true);
+      if (elect_one()) {
+        // by one thread from its waits to its products: a warp that looks at barriers
+        // together and elects a thread for each step takes longer than the products
+        Walk walk = from;
+        uint32_t n = 0, nseg = 0;  // tiles, segments
+        bool ok = true, issued = false;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+          return mbar_try_wait(smem_u32(bar), parity) || mbar_wait_idle(bar, parity, abort_flag, limit_ns);
+        };
+        if (p.stall && x == 0) ok = mbar_wait(&sh.never, 0, abort_flag, status, p.wait_ns);  // injected: nothing arrives
+#pragma unroll 1
+        for (bool last = false; ok && !last; ++nseg) {
+          const Part s = walk.next(sh.table, blockIdx.x);
+          last = s.last;
+          const int halves = 2 * (s.j1 - s.j0);
+          ok = wait(&sh.q_full[x], nseg & 1);
+#pragma unroll 1
+          for (int u = 0; ok && u < halves + 2; u += 2) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) mma_ss(ts, dq + kmaj_step(kk), b + kmaj_step(kk), id_s, kk > 0);
-          mma_commit(&sh.s_full[x]);
-        }
-        __syncwarp();
-        issued = true;
-      };
-#pragma unroll 1
-      for (bool last = false; ok && !last; ++nseg) {
-        const Part s = walk.next(sh.table, blockIdx.x);
-        last = s.last;
-        ok = wait_bar(&sh.q_full, nseg & 1);
-        if (ok) scores(n);
-#pragma unroll 1
-        for (int j = s.j0; ok && j < s.j1; ++j, ++n) {
-          const uint32_t st = n % kKvStages;
-#pragma unroll 1
-          for (int h = 0; ok && h < 2; ++h) {
-            ok = wait_bar(&sh.p_full[x][h], n & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t bv = dv + desc_bytes(st * C::kStageBytes + h * 8192);
-            const uint32_t more = j > s.j0 || h > 0;
-            if (elect_one()) {
+            for (int h = 0; h < 2; ++h) {
+              if (u >= 2) {
+                const uint32_t t = n + (u >> 1) - 1, st = t % kKvStages;
+                ok = ok && wait(&sh.p_full[x][h], t & 1);
+                if (ok) {
+                  tc_fence_after();
+                  const uint64_t bv = dv + desc_bytes(st * C::kStageBytes + h * 8192);
+                  const uint32_t more = u > 2 || h > 0;
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) mma_ts(to, ts + h * 64 + kk * 8, bv + mnmaj_step(kk), id_o, more || kk > 0);
-              mma_commit(&sh.pv_done[x][h]);
-              if (h == 1) mma_commit(&sh.kv_empty[st]);
+                  for (int kk = 0; kk < 4; ++kk) mma_ts(tmem + col_o(x), tmem + col_s(x, h) + kk * 8, bv + mnmaj_step(kk), id_o, more || kk > 0);
+                  mma_commit(&sh.pv_done[x][h]);
+                  if (h == 1) mma_commit(&sh.kv_empty[st]);
+                }
+              }
+              if (u < halves) {
+                const uint32_t t = n + (u >> 1), st = t % kKvStages;
+                if (h == 0) ok = ok && wait(&sh.kv_full[st], (t / kKvStages) & 1);
+                if (ok) {
+                  tc_fence_after();
+                  const uint64_t b = dk + desc_bytes(st * C::kStageBytes + h * 8192);
+#pragma unroll
+                  for (int kk = 0; kk < D / 16; ++kk) mma_ss(tmem + col_s(x, h), dq + kmaj_step(kk), b + kmaj_step(kk), id_s, kk > 0);
+                  mma_commit(&sh.s_full[x][h]);
+                  issued = true;
+                }
+              }
             }
-            __syncwarp();
           }
-          if (ok && j + 1 < s.j1) scores(n + 1);
+          n += halves / 2;
+        }
+        if (!ok && issued) {
+          volatile int never = 0;
+          mma_commit(&sh.drain[x]);
+          mbar_wait(&sh.drain[x], 0, &never, status, 100000000ull);
         }
       }
-      if (!ok && issued) {
-        volatile int never = 0;
-        if (elect_one()) mma_commit(&sh.drain[x]);
-        __syncwarp();
-        if (lane == 0) mbar_wait(&sh.drain[x], 0, &never, status, 100000000ull);
-        __syncwarp();
-      }
-    } else if (warp == 15 && busy) {
-      // ------------------------------------------------------------ copies
-      const uint32_t bytes = D << p.log_bs;
-      const uint32_t to = smem_u32(smem) + C::kOffRaw + lane * bytes;
-      Walk walk = from;
-      uint32_t n = 0;
-      bool ok = true;
-#pragma unroll 1
-      for (bool last = false; ok && !last;) {
-        const Part s = walk.next(sh.table, blockIdx.x);
-        last = s.last;
-#pragma unroll 1
-        for (int j = s.j0; j < s.j1; ++j, ++n) {
-          const int ms = n % kMetaStages, st = n % kRawStages;
-          ok = wait_bar(&sh.meta_full[ms], (n / kMetaStages) & 1);
-          if (ok && n >= (uint32_t)kRawStages) ok = wait_bar(&sh.raw_empty[st], ((n / kRawStages) - 1) & 1);
-          if (!ok) break;
-          const uint32_t valid = sh.meta[ms].valid;
-          if (lane == 0) mbar_arrive_expect_tx(&sh.raw_full[st], __popc(valid) * bytes);
-          __syncwarp();
-          if ((valid >> lane) & 1) bulk_load(to + st * C::kRawBytes, sh.meta[ms].rows[lane], bytes, &sh.raw_full[st]);
-          __syncwarp();
-        }
-      }
-      // copies in flight end in any case; none may outlive the CTA
-      volatile int never = 0;
-#pragma unroll 1
-      for (uint32_t t = n > (uint32_t)kRawStages ? n - kRawStages : 0; t < n; ++t)
-        if (lane == 0) mbar_wait(&sh.raw_full[t % kRawStages], (t / kRawStages) & 1, &never, status, 100000000ull);
       __syncwarp();
     }
   } else if (warp >= 8) {
@@ -430,117 +399,96 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
       const int ct = tid - 2 * kWG;
       const int ch = D == 128 ? (ct & 3) | (((ct >> 2) ^ (ct >> 3)) & 1) << 2 : ct & 3;
       const int row0 = D == 128 ? ((ct >> 2) & 1) | ((ct >> 3) & ~1) : ct >> 2;
-      const uint32_t from0 = smem_u32(smem) + C::kOffRaw + row0 * D + ch * 16;
       const uint32_t to0 = smem_u32(smem) + (ch >> 2) * kHalfTile + row0 * 128;
       const uint32_t swz0 = (((2 * (ch & 3)) ^ (row0 & 7)) << 4);  // the other piece's differs in one bit
       static_assert(kRowStep % 8 == 0, "a thread's rows have one swizzle");
-      // q: D / 8 neighbouring lanes copy a row's 16-byte pieces
-      constexpr int kLanes = D / 8, kStep = kWG / kLanes;
-      const int q_ch = ct % kLanes, q_row = ct / kLanes;
-      const uint32_t q0 = smem_u32(smem) + C::kOffQ;
-      Walk walk = from;
-      uint32_t n = 0;
-      int nseg = 0;
-      // no way out when a wait has given up: the warps meet at barriers
-#pragma unroll 1
-      for (bool last = false; !last; ++nseg) {
-        const Part s = walk.next(sh.table, blockIdx.x);
-        last = s.last;
-        if (nseg > 0) {
-          // the last segment's scores have been made and its factors read
-          (void)wait_bar(&sh.q_read, (nseg - 1) & 1);
-          (void)wait_bar(&sh.s_full[0], (n - 1) & 1);
-          (void)wait_bar(&sh.s_full[1], (n - 1) & 1);
-        }
-        const __nv_bfloat16 *q = p.q + (size_t)s.row0 * D + q_ch * 8;
-#pragma unroll 4
-        for (int r = q_row; r < kRowTile; r += kStep) {
-          const uint32_t to = q0 + (r >> 7) * C::kStageBytes + (q_ch >> 3) * kHalfTile + (r & 127) * 128 + (((q_ch & 7) ^ (r & 7)) << 4);
-          cp_async_16(to, r < s.rows ? q + (size_t)r * D : p.q, r < s.rows ? 16 : 0);
-        }
-        cp_async_wait();
-        named_bar_sync(kBarQ, kWG);
-        // bf16 -> fp16 with a factor for each row: the largest |q| becomes 224 ..
-        // 448; a negative scale goes into q's sign
-#pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t at_row = q0 + x * C::kStageBytes + ct * 128;
-          auto piece_at = [&](int c) { return at_row + (c >> 3) * kHalfTile + (((c & 7) ^ (ct & 7)) << 4); };
-          uint32_t amax = 0;
-#pragma unroll 4
-          for (int c = 0; c < kLanes; ++c) {
-            uint32_t w[4];
-            ld_shared(piece_at(c), w);
-            amax = bf16x2_max(amax, bf16x2_max(bf16x2_max(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                                               bf16x2_max(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu)));
-          }
-          const int ex = scale_exponent(__uint_as_float(max(amax & 0xffffu, amax >> 16) << 16), kLeastQExp);
-          const float inv = p.scale < 0.f ? -exp2_int(-ex) : p.scale > 0.f ? exp2_int(-ex) : 0.f;
-          sh.q_factor[x * kWG + ct] = exp2_int(ex) * fabsf(p.scale) * 1.4426950408889634f;
-          const uint64_t inv2 = f32x2(__float_as_uint(inv), __float_as_uint(inv));
-#pragma unroll 2
-          for (int c = 0; c < kLanes; ++c) {
-            uint32_t w[4], f[4];
-            ld_shared(piece_at(c), w);
+      const uint32_t tiles = from.end - from.u;
+      // Piece i of a tile, from memory (zero where there is no page).
+      auto piece = [&](const TileMeta &meta, int i, uint4 &w) {
+        const int row = row0 + i * kRowStep, page = row >> p.log_bs;
+        const uint8_t *rows = meta.rows[page];
+        w = make_uint4(0, 0, 0, 0);
+        if (rows) w = *reinterpret_cast<const uint4 *>(rows + (row - (page << p.log_bs)) * D + ch * 16);
+      };
+      uint4 raw[kPer];
+      (void)wait_bar(&sh.meta_full[0], 0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float lo, hi;
-              f32x2_split(fmul2(f32x2(w[e] << 16, w[e] & 0xffff0000u), inv2), lo, hi);
-              f[e] = f16x2_rn(lo, hi);
-            }
-            st_shared(piece_at(c), f[0], f[1], f[2], f[3]);
-          }
+      for (int i = 0; i < kPer; ++i) piece(sh.meta[0], i, raw[i]);
+      // no way out when a wait has given up: the softmax goes on too
+#pragma unroll 1
+      for (uint32_t n = 0; n < tiles; ++n) {
+        const TileMeta &meta = sh.meta[n % kMetaStages], &next = sh.meta[(n + 1) % kMetaStages];
+        const uint32_t st = n % kKvStages, dst = to0 + st * C::kStageBytes;
+        if (n + 1 < tiles) (void)wait_bar(&sh.meta_full[(n + 1) % kMetaStages], ((n + 1) / kMetaStages) & 1);
+        if (n >= (uint32_t)kKvStages) (void)wait_bar(&sh.kv_empty[st], ((n / kKvStages) - 1) & 1);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          uint32_t f[8];
+          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) e4m3x4_to_f16(w[e], f[2 * e], f[2 * e + 1]);
+          const uint32_t factor = meta.factor[(row0 + i * kRowStep) >> p.log_bs];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = f16x2_mul(f[e], factor);
+          const uint32_t at = dst + i * kRowStep * 128;
+          st_shared(at + swz0, f[0], f[1], f[2], f[3]);
+          st_shared(at + (swz0 ^ 16), f[4], f[5], f[6], f[7]);
+          if (n + 1 < tiles) piece(next, i, raw[i]);  // on its way while this tile is used
         }
         fence_async_smem();
-        mbar_arrive(&sh.q_full);
-#pragma unroll 1
-        for (int j = s.j0; j < s.j1; ++j, ++n) {
-          const int ms = n % kMetaStages, rs = n % kRawStages, st = n % kKvStages;
-          (void)wait_bar(&sh.raw_full[rs], (n / kRawStages) & 1);
-          if (n >= (uint32_t)kKvStages) (void)wait_bar(&sh.kv_empty[st], ((n / kKvStages) - 1) & 1);
-          const uint32_t valid = sh.meta[ms].valid;
-          const bool full = valid == (1u << ppt) - 1u;
-          const uint32_t src = from0 + rs * C::kRawBytes, dst = to0 + st * C::kStageBytes;
-#pragma unroll 4
-          for (int i = 0; i < kPer; ++i) {
-            uint32_t raw[4], f[8];
-            ld_shared(src + i * kRowStep * D, raw);
-            const int page = (row0 + i * kRowStep) >> p.log_bs;
-            if (!full && !((valid >> page) & 1)) raw[0] = raw[1] = raw[2] = raw[3] = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) e4m3x4_to_f16(raw[e], f[2 * e], f[2 * e + 1]);
-            const uint32_t factor = sh.meta[ms].factor[page];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = f16x2_mul(f[e], factor);
-            const uint32_t at = dst + i * kRowStep * 128;
-            st_shared(at + swz0, f[0], f[1], f[2], f[3]);
-            st_shared(at + (swz0 ^ 16), f[4], f[5], f[6], f[7]);
-          }
-          mbar_arrive(&sh.raw_empty[rs]);
-          fence_async_smem();
-          mbar_arrive(&sh.kv_full[st]);
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.kv_full[st]);
       }
     }
   } else {
     setmaxnreg_inc<kRegsSoft>();
     if (busy) {
       // ------------------------------------------------------------ softmax
-      // Rows beyond the prefix's are zero in Q: their results are not written.
+      // A thread has a row from its q to its O.  Rows beyond the prefix's are zero in
+      // Q: their results are not written.
       const int x = warp >> 2, row = tid & (kWG - 1);
-      const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16), scol = lane_addr + col_s(x), ocol = lane_addr + col_o(x);
+      const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16), ocol = lane_addr + col_o(x);
       Walk walk = from;
+      const uint32_t q_at = smem_u32(smem) + C::kOffQ + x * C::kStageBytes + row * 128;
       uint32_t n = 0;
-      int nseg = 0;
 #pragma unroll 1
-      for (bool last = false; !last; ++nseg) {
+      for (bool last = false; !last;) {
         const Part s = walk.next(sh.table, blockIdx.x);
         last = s.last;
         float m_run = -INFINITY, m_use = 0.f, l_run = 0.f;  // m_use: what is subtracted
         int unit = 0;
-        (void)wait_bar(&sh.q_full, nseg & 1);
-        const float cs = sh.q_factor[x * kWG + row];
-        mbar_arrive(&sh.q_read);
+        const bool mine = x * kWG + row < s.rows;
+        // bf16 -> fp16 with a factor for the row: the largest |q| becomes 224 .. 448;
+        // a negative scale goes into q's sign
+        float cs;
+        {
+          uint32_t w[D / 2];
+          const uint4 *q = reinterpret_cast<const uint4 *>(p.q + ((size_t)s.row0 + (mine ? x * kWG + row : 0)) * D);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = mine ? q[c] : make_uint4(0, 0, 0, 0);
+            w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
+          }
+          uint32_t amax = 0;
+#pragma unroll
+          for (int c = 0; c < D / 2; ++c) amax = bf16x2_max(amax, w[c] & 0x7fff7fffu);
+          const int ex = scale_exponent(__uint_as_float(max(amax & 0xffffu, amax >> 16) << 16), kLeastQExp);
+          const float inv = p.scale < 0.f ? -exp2_int(-ex) : p.scale > 0.f ? exp2_int(-ex) : 0.f;
+          cs = exp2_int(ex) * fabsf(p.scale) * 1.4426950408889634f;
+          const uint64_t inv2 = f32x2(__float_as_uint(inv), __float_as_uint(inv));
+#pragma unroll
+          for (int c = 0; c < D / 2; ++c) {
+            float lo, hi;
+            f32x2_split(fmul2(f32x2(w[c] << 16, w[c] & 0xffff0000u), inv2), lo, hi);
+            w[c] = f16x2_rn(lo, hi);
+          }
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c)
+            st_shared(q_at + (c >> 3) * kHalfTile + (((c & 7) ^ (row & 7)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.q_full[x]);
+        }
 #pragma unroll 1
         for (int j = s.j0; j < s.j1; ++j, ++n) {
           const int ms = n % kMetaStages;
@@ -550,13 +498,15 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
           const int odd = meta.odd, keys = meta.keys;
           if (meta.bad) l_run = __int_as_float(0x7fc00000);
           const float ck = fminf(fmaxf(cs * exp2_int(unit), FLT_MIN), FLT_MAX);
-          (void)wait_bar(&sh.s_full[x], n & 1);
-          tc_fence_after();
+          const uint64_t ck2 = f32x2(__float_as_uint(ck), __float_as_uint(ck));
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
+            (void)wait_bar(&sh.s_full[x][h], n & 1);
+            tc_fence_after();
+            const uint32_t scol = lane_addr + col_s(x, 0) + h * 64;
             uint32_t sv[64];
-            tmem_ld32(scol + h * 64, *reinterpret_cast<uint32_t(*)[32]>(sv));
-            tmem_ld32(scol + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
+            tmem_ld32(scol, *reinterpret_cast<uint32_t(*)[32]>(sv));
+            tmem_ld32(scol + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
             tmem_wait_ld();
             if (keys < kTileKeys) {
 #pragma unroll
@@ -592,28 +542,26 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
                 scale_o<D>(ocol, f);
               }
             }
-            const uint64_t ck2 = f32x2(__float_as_uint(ck), __float_as_uint(ck));
             const uint64_t nm2 = f32x2(__float_as_uint(-m_use), __float_as_uint(-m_use));
             uint64_t acc[2] = {0, 0};
-            const uint32_t pcol = scol + h * 64;
             auto probabilities = [&](auto scaled) {
 #pragma unroll
-              for (int c = 0; c < 64; c += 32) {
+              for (int c = 0; c < 2; ++c) {
                 uint32_t pk[16];
 #pragma unroll
                 for (int y = 0; y < 32; y += 2) {
                   float t0, t1;
-                  f32x2_split(ffma2(f32x2(sv[c + y], sv[c + y + 1]), ck2, nm2), t0, t1);
+                  f32x2_split(ffma2(f32x2(sv[32 * c + y], sv[32 * c + y + 1]), ck2, nm2), t0, t1);
                   float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
                   acc[(y >> 1) & 1] = fadd2(acc[(y >> 1) & 1], f32x2(__float_as_uint(e0), __float_as_uint(e1)));
                   if constexpr (decltype(scaled)::value) {
-                    const float rest = meta.rest[(h * 64 + c + y) >> p.log_bs];
+                    const float rest = meta.rest[(h * 64 + 32 * c + y) >> p.log_bs];
                     e0 *= rest;
                     e1 *= rest;
                   }
                   pk[y >> 1] = f16x2_rn(e0, e1);
                 }
-                tmem_st16(pcol + c / 2, pk);
+                tmem_st16(scol + 16 * c, pk);
               }
             };
             if (odd) probabilities(std::true_type());
@@ -623,24 +571,44 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
             l_run += a + b;
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&sh.p_full[x][h]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[x][h]);
           }
-          mbar_arrive(&sh.meta_empty[ms]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.meta_empty[ms]);
         }
         if (*abort_flag) l_run = __int_as_float(0x7fc00000);
-        const bool mine = x * kWG + row < s.rows;
-        if (mine) p.part_ml[(size_t)s.slot * kRowTile + x * kWG + row] = make_float2(m_use, l_run);
-        const float inv = exp2_int(unit) / l_run;
+        const bool merge = p.merge && s.whole;
+        const int nrows = s.rows - x * kWG;
+        const size_t at_row = merge ? (size_t)s.row0 + x * kWG : (size_t)s.slot * kRowTile + x * kWG;  // of the tile's first row
+        float inv = exp2_int(unit) / l_run;
+        if (merge) {
+          // with the row's own part: (2^(lse - M) own + 2^(m - M) O) / (2^(lse - M) + 2^(m - M) l)
+          const float m0 = mine ? p.own_lse[at_row + row] * 1.4426950408889634f : 0.f;
+          const float M = fmaxf(m0, m_use), w0 = exp2f(m0 - M), w1 = exp2f(m_use - M), sum = fmaf(w1, l_run, w0);
+          sh.own[x * kWG + row] = w0 / sum;
+          inv = w1 * exp2_int(unit) / sum;
+          if (mine) p.lse[at_row + row] = (M + log2f(sum)) * 0.69314718055994531f;
+        } else if (mine) {
+          p.part_ml[at_row + row] = make_float2(m_use, l_run);
+        }
         (void)wait_bar(&sh.pv_done[x][1], (n - 1) & 1);
         tc_fence_after();
         // O leaves through shared memory, 64 bytes of a row at a time, so that four
         // lanes write a row's: a store to 32 rows takes 32 cycles.
-        float *out = p.part_o + ((size_t)s.slot * kRowTile + x * kWG) * D;
-        const int nrows = s.rows - x * kWG;
         const uint32_t buf = smem_u32(sh.out) + x * kWG * 64, at = buf + row * 64, swz = (row >> 1) & 3;
         const int piece = lane & 3;
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
+          const size_t col = (size_t)(c * 16 + piece * 4);
+          float4 own[4];
+          if (merge) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = (warp & 3) * 32 + i * 8 + (lane >> 2);
+              if (r < nrows) own[i] = *reinterpret_cast<const float4 *>(p.own_out + (at_row + r) * D + col);
+            }
+          }
           uint32_t o[16];
           tmem_ld16(ocol + c * 16, o);
           tmem_wait_ld();
@@ -654,7 +622,16 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
             const int r = (warp & 3) * 32 + i * 8 + (lane >> 2);
             uint32_t v[4];
             ld_shared(buf + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4), v);
-            if (r < nrows) *reinterpret_cast<uint4 *>(out + (size_t)r * D + c * 16 + piece * 4) = make_uint4(v[0], v[1], v[2], v[3]);
+            if (r >= nrows) continue;
+            if (merge) {
+              const float w0 = sh.own[x * kWG + r];
+              const float4 u = own[i];
+              *reinterpret_cast<uint2 *>(p.out + (at_row + r) * D + col) =
+                  make_uint2(pack_bf16x2(fmaf(w0, u.x, __uint_as_float(v[0])), fmaf(w0, u.y, __uint_as_float(v[1]))),
+                             pack_bf16x2(fmaf(w0, u.z, __uint_as_float(v[2])), fmaf(w0, u.w, __uint_as_float(v[3]))));
+            } else {
+              *reinterpret_cast<uint4 *>(p.part_o + (at_row + r) * D + col) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
           }
           __syncwarp();
         }
@@ -679,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
 constexpr int kJoinThreads = 256;
 static_assert(kJoinThreads >= kSharedMaxGroups, "a thread for each prefix");
 
-template <int D>
+template <int D, int U>  // U rows of a lane at a time
 __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const SharedParams p) {
   __shared__ Table table;
   constexpr int kLanes = D / 4, kRows = kJoinThreads / kLanes;
@@ -692,47 +669,83 @@ __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const Shar
   const bool late = __syncthreads_or(worst == 1000 || worst == HCA_ERR_TIMEOUT), wrong = __syncthreads_or(worst != HCA_OK);
   if (blockIdx.x == 0 && tid == 0) *p.status = late ? HCA_ERR_TIMEOUT : wrong ? HCA_ERR_CACHE : HCA_OK;
   const bool refused = units < 0 || p.own->ntiles < 0 || late;  // then all rows are NaN
-  const int live = refused ? p.N : min(max(p.start[p.R], 0), p.N);
-  const int quota = units_per_cta(max(units, 0), p.grid);
-  const long long rows = (long long)live * p.H;
-  for (long long row = (long long)blockIdx.x * kRows + tid / kLanes; row < rows; row += (long long)gridDim.x * kRows) {
-    float4 o = *reinterpret_cast<const float4 *>(p.own_out + row * D + 4 * l);
-    float lse = p.own_lse[row];
-    if (refused) {
-      lse = __int_as_float(0x7fc00000);
-      o = make_float4(lse, lse, lse, lse);
-    } else {
-      int lo = 0, hi = p.G;  // the row's prefix
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (table.g[mid].row0 <= row) lo = mid; else hi = mid;
-      }
-      const Prefix x = table.g[lo];
-      if (x.tiles > 0) {
-        const int r = (int)(row - x.row0), rt = r / kRowTile, u0 = x.line0 + rt * x.tiles;
-        const int first = u0 / quota, n = (u0 + x.tiles - 1) / quota - first + 1;
-        const size_t slot = (size_t)(x.rt0 + rt + first) * kRowTile + r % kRowTile;  // the next part's is 256 further
-        const float m0 = lse * kLog2e;
-        float M = m0;
-        for (int i = 0; i < n; ++i) M = fmaxf(M, p.part_ml[slot + (size_t)i * kRowTile].x);
-        float w = exp2f(m0 - M), sum = w;
-        o.x *= w; o.y *= w; o.z *= w; o.w *= w;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-          const size_t at = slot + (size_t)i * kRowTile;
-          const float2 ml = p.part_ml[at];
-          const float4 v = *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * l);
-          w = exp2f(ml.x - M) * ml.y;
-          sum += w;
-          o.x = fmaf(w, v.x, o.x); o.y = fmaf(w, v.y, o.y); o.z = fmaf(w, v.z, o.z); o.w = fmaf(w, v.w, o.w);
-        }
-        const float inv = 1.f / sum;
-        o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
-        lse = (M + log2f(sum)) * 0.69314718055994531f;
+  if (refused) {
+    const size_t rows = (size_t)p.N * p.H;
+    for (size_t row = (size_t)blockIdx.x * kRows + tid / kLanes; row < rows; row += (size_t)gridDim.x * kRows) {
+      *reinterpret_cast<uint2 *>(p.out + row * D + 4 * l) = make_uint2(0x7fc07fc0u, 0x7fc07fc0u);
+      if (l == 0) p.lse[row] = __int_as_float(0x7fc00000);
+    }
+    return;
+  }
+  const int quota = units_per_cta(units, p.grid);
+  constexpr int kChunks = kRowTile / (kRows * U);  // of a row tile, a block's each
+  for (int item = blockIdx.x; item < table.row_tiles * kChunks; item += gridDim.x) {
+    int lo = 0, hi = p.G;  // the row tile's prefix
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (table.g[mid].rt0 <= item / kChunks) lo = mid; else hi = mid;
+    }
+    const Prefix &x = table.g[lo];
+    const int rt = item / kChunks - x.rt0, u0 = x.line0 + rt * x.tiles, first = u0 / quota;
+    const int parts = x.tiles > 0 ? (u0 + x.tiles - 1) / quota - first + 1 : 0;
+    if (p.merge && parts == 1) continue;  // finished by the CTA that had it
+    const int r0 = item % kChunks * (kRows * U) + tid / kLanes;  // the lane's first row; the others are kRows apart
+    float4 o[U];
+    float lse[U];
+    size_t slot[U];
+    int n[U];  // parts; -1: no such row
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = rt * kRowTile + r0 + u * kRows;
+      n[u] = r < x.rows ? parts : -1;
+      slot[u] = (size_t)(x.rt0 + rt + first) * kRowTile + r0 + u * kRows;  // the next part's is 256 further
+      o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      lse[u] = 0.f;
+      if (n[u] >= 0) {
+        o[u] = *reinterpret_cast<const float4 *>(p.own_out + (size_t)(x.row0 + r) * D + 4 * l);
+        lse[u] = p.own_lse[x.row0 + r];
       }
     }
-    *reinterpret_cast<uint2 *>(p.out + row * D + 4 * l) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-    if (l == 0) p.lse[row] = lse;
+    int most = 0;
+    float M[U], sum[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      most = max(most, n[u]);
+      M[u] = lse[u] * kLog2e;
+    }
+    for (int i = 0; i < most; ++i) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i < n[u]) M[u] = fmaxf(M[u], p.part_ml[slot[u] + (size_t)i * kRowTile].x);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      sum[u] = n[u] > 0 ? exp2f(lse[u] * kLog2e - M[u]) : 1.f;
+      o[u].x *= sum[u]; o[u].y *= sum[u]; o[u].z *= sum[u]; o[u].w *= sum[u];
+    }
+#pragma unroll(U > 1 ? 1 : 4)
+    for (int i = 0; i < most; ++i) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i < n[u]) {
+          const size_t at = slot[u] + (size_t)i * kRowTile;
+          const float2 ml = p.part_ml[at];
+          const float4 v = *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * l);
+          const float w = exp2f(ml.x - M[u]) * ml.y;
+          sum[u] += w;
+          o[u].x = fmaf(w, v.x, o[u].x); o[u].y = fmaf(w, v.y, o[u].y);
+          o[u].z = fmaf(w, v.z, o[u].z); o[u].w = fmaf(w, v.w, o[u].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (n[u] < 0) continue;
+      const size_t row = (size_t)x.row0 + rt * kRowTile + r0 + u * kRows;
+      const float inv = n[u] > 0 ? 1.f / sum[u] : 1.f;
+      *reinterpret_cast<uint2 *>(p.out + row * D + 4 * l) = make_uint2(pack_bf16x2(o[u].x * inv, o[u].y * inv), pack_bf16x2(o[u].z * inv, o[u].w * inv));
+      if (l == 0) p.lse[row] = n[u] > 0 ? (M[u] + log2f(sum[u])) * 0.69314718055994531f : lse[u];
+    }
   }
 }
 
@@ -766,17 +779,25 @@ cudaError_t launch(const CacheAttnArgs &a, SharedParams &p, int sms, cudaStream_
   static SmemAttrOnce attr;
   cudaError_t e = attr.ensure(reinterpret_cast<const void *>(hca_cache_prefix_kernel<D>), C::kSmem);
   if (e != cudaSuccess) return e;
-  {
+  auto prefix = [&] {
     ProfScope prof(kKCachePrefix, st);
     hca_cache_prefix_kernel<D><<<p.grid, kThreads, C::kSmem, st>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  e = cache_attn(a, st);
+    return cudaGetLastError();
+  };
+  // As many row tiles as CTAs: most are one CTA's, which adds the rows' own part
+  // where it has O.
+  p.merge = (long long)p.N * p.H >= (long long)kRowTile * p.grid;
+  if (!p.merge) e = prefix();
+  if (e == cudaSuccess) e = cache_attn(a, st);
+  if (e == cudaSuccess && p.merge) e = prefix();
   if (e != cudaSuccess) return e;
   ProfScope prof(kKCacheJoin, st);
-  const long long blocks = ((long long)p.N * p.H * (D / 4) + kJoinThreads - 1) / kJoinThreads;
-  return launch_behind(hca_cache_join_kernel<D>, dim3((unsigned)std::min<long long>(blocks, 8ll * sms)), kJoinThreads, 0, st, p);
+  // Many rows: 4 of them a lane, whose loads are in flight together.
+  const bool many = p.merge;
+  const long long per = (long long)kJoinThreads / (D / 4) * (many ? 4 : 1);
+  const dim3 grid((unsigned)std::min<long long>((long long)p.N * p.H / per + p.G * (kRowTile / per), (many ? 3ll : 5ll) * sms));
+  if (many) return launch_behind(hca_cache_join_kernel<D, 4>, grid, kJoinThreads, 0, st, p);
+  return launch_behind(hca_cache_join_kernel<D, 1>, grid, kJoinThreads, 0, st, p);
 }
 
 }  // namespace

@@ -1,4 +1,5 @@
-// hca_py.cpp -- the serving calls of hca.py without its Python
+// hca_py.cpp -- the serving calls of hca.py, and those of the norms with positions,
+// without their Python
 //
 // A decode step's kernels take 6 to 25 us; checking a dozen tensors, allocating
 // three and passing thirty arguments takes Python 18 to 22 us a call.  Here the
@@ -13,6 +14,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <ATen/ops/empty_like.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -33,6 +35,12 @@ struct {
   decltype(&hca_cache_append) append;
   decltype(&hca_cache_attn_workspace_size) attn_ws;
   decltype(&hca_cache_attn) attn;
+  decltype(&hca_cache_attn_shared_workspace_size) shared_ws;
+  decltype(&hca_cache_attn_shared) shared;
+  decltype(&hca_norm_rope_fwd) norm_rope_fwd;
+  decltype(&hca_norm_rope_workspace_size) norm_rope_ws;
+  decltype(&hca_norm_rope_bwd) norm_rope_bwd;
+  decltype(&hca_rope) rope;
 } lib;
 
 constexpr at::ScalarType kI32 = at::kInt, kF32 = at::kFloat, kU8 = at::kByte, kE4m3 = at::kFloat8_e4m3fn;
@@ -238,16 +246,287 @@ PyObject *cache_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// q, start, held, raw, comp, first, shared_cols, W, m, scale, out, lse, ws, check
+PyObject *cache_attn_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    need(n == 14);
+    const at::Tensor &q = tensor(a[0]), &held = tensor(a[2]), &cols = tensor(a[6]);
+    need(q.dim() == 3 && held.dim() == 1 && cols.dim() == 1 && PyTuple_CheckExact(a[3]) && PyTuple_GET_SIZE(a[3]) == 3 && a[4] != Py_None);
+    const at::Tensor &raw_pool = tensor(PyTuple_GET_ITEM(a[3], 0));
+    need(raw_pool.dim() == 3);
+    const int64_t N = q.size(0), H = q.size(1), D = q.size(2), R = held.size(0), bs = raw_pool.size(1), G = cols.size(0);
+    need(N <= INT_MAX && H <= INT_MAX && D <= INT_MAX && R < INT_MAX && bs <= INT_MAX && G < INT_MAX);
+    const int W = integer(a[7]), m = integer(a[8]), dt = dtype_code(q.scalar_type());
+    need(PyFloat_CheckExact(a[9]));
+    const float scale = (float)PyFloat_AS_DOUBLE(a[9]);
+    const Call c(q);
+    const Cache raw = cache_of(c, a[3], R, bs, D), comp = cache_of(c, a[4], R, bs, D);
+    void *pq = c.fits(q, q.scalar_type(), {N, H, D}), *ps = c.fits(a[1], kI32, {R + 1}), *ph = c.fits(held, kI32, {R});
+    void *pf = c.fits(a[5], kI32, {G + 1}), *pc = c.fits(cols, kI32, {G});
+    const size_t bytes = lib.shared_ws((int)N, (int)R, (int)H, (int)D, (int)G, dt);
+    need(bytes > 0);
+    const at::Tensor out = c.result(a[10], q.scalar_type(), {N, H, D}), lse = c.result(a[11], kF32, {N, H});
+    const Workspace ws(c, a[12], a[13] != Py_False, bytes);
+    Tuple r = results(out, lse, ws.tensor_);
+    void *const stream = c.stream();
+    const int rc = lib.shared(pq, static_cast<int32_t *>(ps), static_cast<int32_t *>(ph), raw.pool, static_cast<float *>(raw.scale),
+                              static_cast<int32_t *>(raw.table), raw.nblocks, raw.cols, comp.pool, static_cast<float *>(comp.scale),
+                              static_cast<int32_t *>(comp.table), comp.nblocks, comp.cols, static_cast<int32_t *>(pf),
+                              static_cast<int32_t *>(pc), out.data_ptr(), static_cast<float *>(lse.data_ptr()), (int)N, (int)R, (int)H,
+                              (int)D, (int)G, W, m, (int)bs, scale, dt, ws.ptr, ws.bytes, stream);
+    return answer(rc, r);
+  });
+}
+
+// Rows with adjacent columns: their pointer, and the strides of the other
+// dimensions where they are not contiguous.
+struct Rows {
+  void *ptr = nullptr;
+  int64_t v[3];
+  const int64_t *strides = nullptr;
+
+  Rows() = default;
+  // packed: [N,H,D] or [N,D] as batch rows of one, heads and positions
+  Rows(const Call &c, const at::Tensor &t, at::ScalarType type, at::IntArrayRef shape, bool packed) {
+    need(t.is_cuda() && t.get_device() == c.dev && t.scalar_type() == type && t.sizes() == shape);
+    ptr = t.data_ptr();
+    if (t.is_contiguous()) return;
+    const auto st = t.strides();
+    need(st.back() == 1);
+    if (packed) {
+      v[0] = 0;
+      if (shape.size() == 3) v[1] = st[1], v[2] = st[0];
+      else v[1] = st[0];
+    } else {
+      for (size_t i = 0; i + 1 < shape.size(); ++i) v[i] = st[i];
+    }
+    strides = v;
+  }
+  Rows(const Rows &) = delete;
+  Rows &operator=(const Rows &o) {
+    ptr = o.ptr;
+    for (int i = 0; i < 3; ++i) v[i] = o.v[i];
+    strides = o.strides ? v : nullptr;
+    return *this;
+  }
+};
+
+// Coordinates of tokens (a batch of them, or packed ones) and frequencies
+struct Angles {
+  int32_t *pos = nullptr;
+  float *freq;
+  int axes, rot, first;
+
+  Angles(const Call &c, PyObject *pos_, PyObject *freq_, PyObject *first_, at::IntArrayRef lead, int64_t D) {
+    const at::Tensor &f = tensor(freq_);
+    need(f.is_cuda() && f.get_device() == c.dev && f.scalar_type() == kF32 && f.is_contiguous() && (f.dim() == 1 || f.dim() == 2));
+    need(f.size(-1) <= INT_MAX / 2);
+    freq = static_cast<float *>(f.data_ptr());
+    axes = f.dim() == 2 ? (int)f.size(0) : 1;
+    rot = 2 * (int)f.size(-1);
+    first = first_ == Py_None ? (int)D - rot : integer(first_);
+    if (pos_ == Py_None) {
+      need(axes == 1);
+      return;
+    }
+    const at::Tensor &p = tensor(pos_);
+    need(p.is_cuda() && p.get_device() == c.dev && p.scalar_type() == kI32 && p.is_contiguous());
+    if (!(axes == 1 && p.sizes() == lead)) {
+      need(p.dim() == (int64_t)lead.size() + 1 && p.size(0) == axes && p.sizes().slice(1) == lead);
+    }
+    pos = static_cast<int32_t *>(p.data_ptr());
+  }
+};
+
+float number(PyObject *o) {
+  need(PyFloat_CheckExact(o));
+  return (float)PyFloat_AS_DOUBLE(o);
+}
+
+int flag(PyObject *o) {
+  need(PyBool_Check(o));
+  return o == Py_True;
+}
+
+const float *weight(const Call &c, PyObject *o, int64_t D) { return o == Py_None ? nullptr : static_cast<float *>(c.fits(o, kF32, {D})); }
+
+// Sizes of q [B,H,S,D] and kv [B,S,D], or packed q [N,H,D] and kv [N,D]; one may be None
+struct Pair {
+  const at::Tensor *q = nullptr, *kv = nullptr, *any;
+  int64_t B = 1, H = 0, S, D;
+  at::ScalarType type;
+  at::DimVector qshape, kvshape, lead;
+
+  Pair(PyObject *q_, PyObject *kv_, bool packed) {
+    if (q_ != Py_None) q = &tensor(q_);
+    if (kv_ != Py_None) kv = &tensor(kv_);
+    need(q || kv);
+    any = q ? q : kv;
+    const int64_t lead_dims = packed ? 1 : 2;
+    need((!q || q->dim() == lead_dims + 2) && (!kv || kv->dim() == lead_dims + 1));
+    D = any->size(-1);
+    S = packed ? any->size(0) : any->size(-2);
+    if (!packed) B = any->size(0);
+    if (q) H = q->size(1);
+    need(B <= INT_MAX && H <= INT_MAX && S <= INT_MAX && D <= INT_MAX);
+    type = any->scalar_type();
+    if (packed) {
+      qshape = {S, H, D};
+      kvshape = {S, D};
+      lead = {S};
+    } else {
+      qshape = {B, H, S, D};
+      kvshape = {B, S, D};
+      lead = {B, S};
+    }
+  }
+};
+
+at::Tensor result_like(const Call &c, PyObject *o, at::ScalarType type, at::IntArrayRef shape) {
+  if (o != Py_None) {
+    const at::Tensor &t = tensor(o);
+    need(t.is_cuda() && t.get_device() == c.dev && t.scalar_type() == type && t.sizes() == shape && t.is_contiguous());
+    return t;
+  }
+  return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, c.dev)));
+}
+
+// q, kv, start, held, wq, wkv, pos, freq, eps, first, halves, qo, kvo (start None: a batch; else packed)
+PyObject *norm_rope_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    need(n == 13);
+    const bool packed = a[2] != Py_None;
+    const Pair s(a[0], a[1], packed);
+    const int dt = dtype_code(s.type);
+    const Call c(*s.any);
+    const float eps = number(a[8]);
+    const Angles an(c, a[6], a[7], a[9], s.lead, s.D);
+    const int halves = flag(a[10]);
+    void *ps = nullptr, *ph = nullptr;
+    int64_t R = 0;
+    if (packed) {
+      const at::Tensor &start = tensor(a[2]);
+      need(start.dim() == 1 && start.size(0) >= 1 && start.size(0) <= INT_MAX && (a[3] != Py_None || an.pos));
+      R = start.size(0) - 1;
+      ps = c.fits(start, kI32, {R + 1});
+      if (a[3] != Py_None) ph = c.fits(a[3], kI32, {R});
+    }
+    const float *wq = nullptr, *wkv = nullptr;
+    Rows xq, xkv;
+    at::Tensor qo, kvo;
+    if (s.q) {
+      xq = Rows(c, *s.q, s.type, s.qshape, packed);
+      wq = weight(c, a[4], s.D);
+      qo = result_like(c, a[11], s.type, s.qshape);
+    }
+    if (s.kv) {
+      xkv = Rows(c, *s.kv, s.type, s.kvshape, packed);
+      wkv = weight(c, a[5], s.D);
+      kvo = result_like(c, a[12], s.type, s.kvshape);
+    }
+    Tuple r = results(qo, kvo);
+    void *const stream = c.stream();
+    const int rc = lib.norm_rope_fwd(xq.ptr, xq.strides, wq, s.q ? qo.data_ptr() : nullptr, xkv.ptr, xkv.strides, wkv,
+                                     s.kv ? kvo.data_ptr() : nullptr, an.pos, an.freq, static_cast<int32_t *>(ps),
+                                     static_cast<int32_t *>(ph), (int)s.B, (int)s.H, (int)s.S, (int)s.D, (int)R, an.axes, an.first, an.rot,
+                                     halves, eps, dt, stream);
+    return answer(rc, r);
+  });
+}
+
+// The gradient of x: the caller's, or one laid out as x is.
+at::Tensor gradient(const Call &c, PyObject *o, const at::Tensor &x) {
+  if (o != Py_None) return tensor(o);
+  for (const int64_t st : x.strides()) need(st != 0);
+  return at::empty_like(x);
+}
+
+// q, kv, wq, wkv, pos, freq, eps, dqo, dkvo, first, halves, dq, dkv, dwq, dwkv, ws
+PyObject *norm_rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    need(n == 16);
+    const Pair s(a[0], a[1], false);
+    const int dt = dtype_code(s.type);
+    const Call c(*s.any);
+    const float eps = number(a[6]);
+    const Angles an(c, a[4], a[5], a[9], s.lead, s.D);
+    const int halves = flag(a[10]);
+    const float *w[2] = {nullptr, nullptr};
+    void *g[2] = {nullptr, nullptr};
+    Rows x[2], dx[2];
+    at::Tensor gx[2], dw[2];
+    for (int i = 0; i < 2; ++i) {
+      const at::Tensor *t = i ? s.kv : s.q;
+      if (!t) continue;
+      const at::IntArrayRef shape = i ? s.kvshape : s.qshape;
+      x[i] = Rows(c, *t, s.type, shape, false);
+      const at::Tensor &cot = tensor(a[7 + i]);
+      need(cot.is_cuda() && cot.get_device() == c.dev && cot.scalar_type() == s.type && cot.sizes() == shape && cot.is_contiguous());
+      g[i] = cot.data_ptr();
+      gx[i] = gradient(c, a[11 + i], *t);
+      dx[i] = Rows(c, gx[i], s.type, shape, false);
+      w[i] = weight(c, a[2 + i], s.D);
+      need(w[i] || a[13 + i] == Py_None);
+      if (w[i]) dw[i] = result_like(c, a[13 + i], kF32, {s.D});
+    }
+    const Workspace ws(c, a[15], false, lib.norm_rope_ws((int)s.D));
+    Tuple r = results(gx[0], gx[1], dw[0], dw[1]);
+    void *const stream = c.stream();
+    auto ptr = [](const at::Tensor &t) { return t.defined() ? static_cast<float *>(t.data_ptr()) : nullptr; };
+    const int rc = lib.norm_rope_bwd(x[0].ptr, x[0].strides, w[0], g[0], dx[0].ptr, dx[0].strides, ptr(dw[0]), x[1].ptr, x[1].strides, w[1],
+                                     g[1], dx[1].ptr, dx[1].strides, ptr(dw[1]), an.pos, an.freq, (int)s.B, (int)s.H, (int)s.S, (int)s.D,
+                                     an.axes, an.first, an.rot, halves, eps, dt, ws.ptr, ws.bytes, stream);
+    return answer(rc, r);
+  });
+}
+
+// x, start, held, pos, freq, inverse, first, halves, y (start None: a batch; else packed)
+PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    need(n == 9);
+    const bool packed = a[1] != Py_None;
+    const Pair s(a[0], Py_None, packed);
+    const int dt = dtype_code(s.type);
+    const Call c(*s.any);
+    const Angles an(c, a[3], a[4], a[6], s.lead, s.D);
+    const int inverse = flag(a[5]), halves = flag(a[7]);
+    void *ps = nullptr, *ph = nullptr;
+    int64_t R = 0;
+    if (packed) {
+      const at::Tensor &start = tensor(a[1]);
+      need(start.dim() == 1 && start.size(0) >= 1 && start.size(0) <= INT_MAX && (a[2] != Py_None || an.pos));
+      R = start.size(0) - 1;
+      ps = c.fits(start, kI32, {R + 1});
+      if (a[2] != Py_None) ph = c.fits(a[2], kI32, {R});
+    }
+    const Rows x(c, *s.q, s.type, s.qshape, packed);
+    const at::Tensor out = a[8] != Py_None ? tensor(a[8]) : result_like(c, Py_None, s.type, s.qshape);
+    const Rows y(c, out, s.type, s.qshape, packed);
+    Tuple r = results(out);
+    void *const stream = c.stream();
+    const int rc = lib.rope(x.ptr, x.strides, y.ptr, y.strides, an.pos, an.freq, static_cast<int32_t *>(ps), static_cast<int32_t *>(ph),
+                            (int)s.B, (int)s.H, (int)s.S, (int)s.D, (int)R, an.axes, an.first, an.rot, halves, inverse, dt, stream);
+    return answer(rc, r);
+  });
+}
+
 // addresses of the C functions, in the order of `lib`
 PyObject *bind(PyObject *, PyObject *args) {
-  unsigned long long f[6];
-  if (!PyArg_ParseTuple(args, "KKKKKK", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5])) return nullptr;
+  unsigned long long f[12];
+  if (!PyArg_ParseTuple(args, "KKKKKKKKKKKK", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9], &f[10], &f[11]))
+    return nullptr;
   lib.plan_ws = reinterpret_cast<decltype(lib.plan_ws)>(f[0]);
   lib.plan = reinterpret_cast<decltype(lib.plan)>(f[1]);
   lib.append_ws = reinterpret_cast<decltype(lib.append_ws)>(f[2]);
   lib.append = reinterpret_cast<decltype(lib.append)>(f[3]);
   lib.attn_ws = reinterpret_cast<decltype(lib.attn_ws)>(f[4]);
   lib.attn = reinterpret_cast<decltype(lib.attn)>(f[5]);
+  lib.shared_ws = reinterpret_cast<decltype(lib.shared_ws)>(f[6]);
+  lib.shared = reinterpret_cast<decltype(lib.shared)>(f[7]);
+  lib.norm_rope_fwd = reinterpret_cast<decltype(lib.norm_rope_fwd)>(f[8]);
+  lib.norm_rope_ws = reinterpret_cast<decltype(lib.norm_rope_ws)>(f[9]);
+  lib.norm_rope_bwd = reinterpret_cast<decltype(lib.norm_rope_bwd)>(f[10]);
+  lib.rope = reinterpret_cast<decltype(lib.rope)>(f[11]);
   Py_RETURN_NONE;
 }
 
@@ -260,6 +539,10 @@ PyMethodDef methods[] = {
     {"cache_plan", fast(cache_plan), METH_FASTCALL, nullptr},
     {"cache_append", fast(cache_append), METH_FASTCALL, nullptr},
     {"cache_attn", fast(cache_attn), METH_FASTCALL, nullptr},
+    {"cache_attn_shared", fast(cache_attn_shared), METH_FASTCALL, nullptr},
+    {"norm_rope_fwd", fast(norm_rope_fwd), METH_FASTCALL, nullptr},
+    {"norm_rope_bwd", fast(norm_rope_bwd), METH_FASTCALL, nullptr},
+    {"rope", fast(rope), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

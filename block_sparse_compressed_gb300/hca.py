@@ -148,7 +148,8 @@ def load(path: str = LIB_PATH):
             if py is not None:
                 py.bind(*(ctypes.cast(getattr(lib, f), P).value for f in (
                     "hca_cache_plan_workspace_size", "hca_cache_plan", "hca_cache_append_workspace_size",
-                    "hca_cache_append", "hca_cache_attn_workspace_size", "hca_cache_attn")))
+                    "hca_cache_append", "hca_cache_attn_workspace_size", "hca_cache_attn", "hca_cache_attn_shared_workspace_size",
+                    "hca_cache_attn_shared", "hca_norm_rope_fwd", "hca_norm_rope_workspace_size", "hca_norm_rope_bwd", "hca_rope")))
                 _py = py
             _lib = lib
     return _lib
@@ -616,7 +617,10 @@ def hca_norm_rope_fwd(q: Optional[torch.Tensor], kv: Optional[torch.Tensor], wq:
     by default): (qo[B,H,S,D], kvo[B,S,D]), contiguous.  wq, wkv [D] fp32 or
     None; pos [B,S] or [axes,B,S] int32 (None: 0 .. S - 1); freq [rot/2] or
     [axes,rot/2] fp32 (include/hca.h, hca_norm_rope_fwd).  q or kv may be None."""
-    lib = load()
+    lib = _lib or load()
+    r = _py and _py.norm_rope_fwd(q, kv, None, None, wq, wkv, pos, freq, eps, first, halves, qo, kvo)
+    if r is not None:
+        return _made(r, "hca_norm_rope_fwd", False)
     B, H, S, D, dt, dev = _norm_rope_sizes(q, kv)
     pp, fp, axes, rot = _angles(pos, freq, (B, S), dev)
     args = []
@@ -643,7 +647,10 @@ def hca_norm_rope_bwd(q, kv, wq, wkv, pos, freq, eps: float, dqo, dkvo, first: O
     """Backward of hca_norm_rope_fwd for the cotangents dqo[B,H,S,D] and
     dkvo[B,S,D] (contiguous): (dq, dkv, dwq, dwkv), dq and dkv laid out as q and
     kv are, None where there is no q, kv or weight."""
-    lib = load()
+    lib = _lib or load()
+    r = _py and _py.norm_rope_bwd(q, kv, wq, wkv, pos, freq, eps, dqo, dkvo, first, halves, dq, dkv, dwq, dwkv, ws)
+    if r is not None:
+        return _made(r, "hca_norm_rope_bwd", False)
     B, H, S, D, dt, dev = _norm_rope_sizes(q, kv)
     pp, fp, axes, rot = _angles(pos, freq, (B, S), dev)
     args, res = [], []
@@ -677,7 +684,10 @@ def hca_rope(x: torch.Tensor, pos: Optional[torch.Tensor], freq: torch.Tensor, i
     columns for both; y may be x).  ``inverse`` turns back, as the attention's
     output has to be before the output projection; it is also the gradient of
     the call without it, and the other way round."""
-    lib = load()
+    lib = _lib or load()
+    r = _py and _py.rope(x, None, None, pos, freq, inverse, first, halves, y)
+    if r is not None:
+        return _made(r, "hca_rope", False)[0]
     if x.dim() != 4:
         raise ValueError("x must be [B,H,S,D]")
     B, H, S, D = x.shape
@@ -891,6 +901,9 @@ def hca_cache_attn_shared(q: torch.Tensor, start: torch.Tensor, held: torch.Tens
     shared_cols[g] columns of their compressed tables in common; first[G+1] and
     shared_cols[G] are int32 tensors.  Results as hca_cache_attn's."""
     lib = _lib or load()
+    r = _py and _py.cache_attn_shared(q, start, held, raw, comp, first, shared_cols, W, m, scale, out, lse, ws, check)
+    if r is not None:
+        return _made(r, "hca_cache_attn_shared", check)[:2]
     dev = q.device
     if q.dim() != 3 or held.dim() != 1 or raw[0].dim() != 3:
         raise ValueError("q must be [N,H,D], held [R] and the raw pool [nblocks,bs,D]")
@@ -940,6 +953,9 @@ def hca_cache_norm_rope(q: Optional[torch.Tensor], kv: Optional[torch.Tensor], s
     [N] or [axes,N] int32 replaces the positions held[r], held[r] + 1, ...  Rows
     of the results from start[R] on are left as they are.  Returns (qo, kvo)."""
     lib = _lib or load()
+    r = _py and _py.norm_rope_fwd(q, kv, start, held, wq, wkv, pos, freq, eps, first, halves, qo, kvo)
+    if r is not None:
+        return _made(r, "hca_cache_norm_rope", False)
     t = q if q is not None else kv
     if t is None:
         raise ValueError("q or kv is required")
@@ -973,6 +989,9 @@ def hca_cache_rope(x: torch.Tensor, start: torch.Tensor, held: Optional[torch.Te
     """hca_rope for a serving step's packed tokens x[N,H,D] (arguments as
     hca_cache_norm_rope); y may be x."""
     lib = _lib or load()
+    r = _py and _py.rope(x, start, held, pos, freq, inverse, first, halves, y)
+    if r is not None:
+        return _made(r, "hca_cache_rope", False)[0]
     if x.dim() != 3:
         raise ValueError("x must be [N,H,D]")
     N, H, D = x.shape

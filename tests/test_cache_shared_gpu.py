@@ -248,6 +248,26 @@ def test_long_prefix_of_many_rows():
     check_attn(call(case, first, cols, 16, 1), *case, 16, 1, scale_of(128), BF16)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_more_row_tiles_than_blocks(D):
+    """Most row tiles are finished by the block that has them, some are cut, one prefix
+    has no common entries."""
+    case, first, cols = shared_case([(2, 5), (1, 0), (1, 9)], [0, 30, 17, 5], [101, 97, 50, 73], 128, D, 16, 1, 32, BF16, 20, pad=3)
+    out, lse = torch.full((324, 128, D), 4.0, dtype=BF16, device=DEV), torch.full((324, 128), 4.0, device=DEV)
+    call(case, first, cols, 16, 1, out=out, lse=lse)
+    assert bool((out[321:] == 4).all()) and bool((lse[321:] == 4).all())
+    check_attn((out[:321], lse[:321]), case[0][:321], *case[1:], 16, 1, scale_of(D), BF16)
+    again = call(case, first, cols, 16, 1)
+    assert torch.equal(again[0][:321], out[:321]) and torch.equal(again[1][:321], lse[:321])
+    # refused: all rows
+    out, lse = call(case, first, cols + 1, 16, 1, check=False)
+    assert bool(out.isnan().all()) and bool(lse.isnan().all())
+    # a bad block reaches its prefix only
+    case[4][2][3, 4] = -7
+    bad, _ = call(case, first, cols, 16, 1, check=False)
+    assert bool(bad[248:321].isnan().all()) and torch.equal(bad[:248], again[0][:248])
+
+
 def test_a_stalled_wait_times_out():
     case, first, cols = shared_case([(3, 12)], [0, 1, 2], [1, 2, 1], 16, 128, 16, 1, 16, BF16, 19)
     ws = torch.empty(hca.load().hca_cache_attn_shared_workspace_size(4, 3, 16, 128, 1, 0), dtype=torch.uint8, device=DEV)
