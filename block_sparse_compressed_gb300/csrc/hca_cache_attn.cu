@@ -660,8 +660,8 @@ size_t cache_attn_ws_bytes(int N, int R, int H, int D, int dtype) { return layou
 
 namespace {
 
-template <typename P>
-cudaError_t attend(P &p, const CacheAttnArgs &a, cudaStream_t st) {
+// Parameters of a call's kernels; sms: SMs of the device.
+void fill(AttnParams &p, const CacheAttnArgs &a, int sms) {
   const Layout l = layout_of(a.N, a.R, a.H, a.D, a.dtype);
   char *ws = static_cast<char *>(a.ws);
   p.q = a.q; p.start = a.start; p.held = a.held; p.raw = a.raw; p.comp = a.comp; p.out = a.out; p.lse = a.lse;
@@ -676,14 +676,21 @@ cudaError_t attend(P &p, const CacheAttnArgs &a, cudaStream_t st) {
   p.N = a.N; p.R = a.R; p.H = a.H; p.D = a.D; p.W = a.W; p.m = a.m; p.log_bs = log2_int(a.bs);
   p.HS = l.HS; p.slices = l.slices; p.P = l.P; p.NQ = l.NQ;
   p.scale = a.scale; p.wait_ns = std::min<uint64_t>(a.wait_ns, 4000000000u); p.stall = a.stall;
-  const int sms = tc::sm_count();
-  if (sms <= 0) return cudaErrorNoDevice;
   const bool tcs = on_tensor_cores(a.dtype);
   p.grid = std::min((tcs ? tc_cache_ctas() : 4) * sms, l.ctas);
   // a CTA of one tile costs a part to join (94 tokens of 37 requests: 20.6 us, 18.6 with 2, 20.4 with 4)
   p.min_tiles = tcs ? 2 : 1;
   const int threads = tcs ? tc_cache_threads() : kSimtThreads;
   p.in_cta = l.slices == 1 && a.R <= threads && l.gmax <= (size_t)threads;
+}
+
+template <typename P>
+cudaError_t attend(P &p, const CacheAttnArgs &a, cudaStream_t st) {
+  const Layout l = layout_of(a.N, a.R, a.H, a.D, a.dtype);
+  const int sms = tc::sm_count();
+  if (sms <= 0) return cudaErrorNoDevice;
+  fill(p, a, sms);
+  const bool tcs = on_tensor_cores(a.dtype);
   if (!p.in_cta) {
     ProfScope prof(kKCacheSched, st);
     hca_cache_sched_kernel<P><<<1, kSchedThreads, 0, st>>>(p);
@@ -710,8 +717,15 @@ cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st) {
     return attend(p, a, st);
   }
   SharedAttnParams p;
-  p.first = a.share.first; p.cols = a.share.cols; p.G = a.share.G; p.apart = a.share.apart;
+  shared_params(a, p);
   return attend(p, a, st);
+}
+
+void cache::shared_params(const CacheAttnArgs &a, SharedAttnParams &p) {
+  p.sms = std::max(tc::sm_count(), 0);
+  fill(p, a, p.sms);
+  p.first = a.share.first; p.cols = a.share.cols; p.G = a.share.G; p.apart = a.share.apart;
+  p.beside = a.share.beside && p.in_cta;
 }
 
 }  // namespace hca

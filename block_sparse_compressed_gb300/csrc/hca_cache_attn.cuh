@@ -42,6 +42,8 @@ struct SharedAttnParams : AttnParams {
   const int32_t *first, *cols;
   int G;
   int apart;  // those columns are left out, and out is fp32 (the join adds them)
+  int beside; // the kernel of the prefixes runs at the same time, on other SMs
+  int sms;
   static constexpr bool kShared = true;
 };
 
@@ -139,6 +141,72 @@ __device__ __forceinline__ bool chunk_group(const P &p, int r, int k, Group &g) 
   // the raw table keeps the last cols pages of the request's tokens
   return ((h + T - 1) >> p.log_bs) - pg.rp0 < p.raw.cols && pg.cp0 + pg.ncomp <= p.comp.cols;
 }
+
+// Rows of a prefix that share the converted keys on an SM, and a step of theirs is 128
+// keys (hca_cache_shared.cu).
+constexpr int kRowTile = 256;
+
+// A prefix's rows and key tiles; false: it does not fit.
+struct PrefixSize {
+  int row0, rows, tiles;
+  __device__ __forceinline__ int row_tiles() const { return (rows + kRowTile - 1) / kRowTile; }
+};
+__device__ __forceinline__ bool prefix_size(const SharedAttnParams &p, int g, PrefixSize &x) {
+  x = PrefixSize{0, 0, 0};
+  const int f0 = p.first[g], f1 = p.first[g + 1], c = p.cols[g];
+  if (f0 < 0 || f1 < f0 || f1 > p.R || (g == 0 && f0 != 0) || (g == p.G - 1 && f1 != p.R) || c < 0 || c > p.comp.cols ||
+      ((long long)c << p.log_bs) > kMaxPos)
+    return false;
+  const int s0 = p.start[f0], s1 = p.start[f1];
+  if (s0 < 0 || s1 < s0 || s1 > p.N) return false;
+  x.row0 = s0 * p.H;
+  x.rows = (s1 - s0) * p.H;
+  x.tiles = ((c << p.log_bs) + kTileKeys - 1) / kTileKeys;
+  return true;
+}
+
+// SMs of the prefixes' kernel, when it has `units` steps in all and the requests'
+// own keys run beside it: so many that both end at about the same time.  By every
+// thread of a block, in both kernels, which come to the same answer: each request's
+// own tiles are estimated by its last chunk's.
+//   a step takes 1.7 us, an own tile 2.4 us with two CTAs on an SM (a group's
+//   beginning and end two more), and the kernels' beginnings and ends about 10 us
+__device__ __forceinline__ int prefix_sms(const SharedAttnParams &p, long long units, long long *tmp) {
+  long long own = 0;
+  for (int r = threadIdx.x; r < p.R; r += blockDim.x) {
+    int n;
+    Group g;
+    g.ntiles = 0;
+    if (request_chunks(p, r, n) && n > 0) (void)chunk_group(p, r, n - 1, g);
+    own += (long long)(g.ntiles + kGroupCost) * n * p.slices;
+  }
+  long long all;
+  (void)block_scan(own, tmp, all);
+  long long best = 0x7fffffffffffffffll;
+  const int lane = threadIdx.x & 31;
+  for (int s = 1 + lane; s < p.sms; s += 32) {  // SMs of the own keys
+    const long long a = 10000 + (units + p.sms - s - 1) / (p.sms - s) * 1700;
+    const long long b = 10000 + max((all + 2 * s - 1) / (2 * s), (long long)p.min_tiles) * 2400;
+    best = min(best, max(a, b) << 12 | s);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
+  return units == 0 ? 0 : p.sms - (int)(best & 0xfff);
+}
+
+// CTAs that the own keys' kernel works with
+__device__ __forceinline__ int own_grid(const AttnParams &p, long long *) { return p.grid; }
+__device__ __forceinline__ int own_grid(const SharedAttnParams &p, long long *tmp) {
+  if (!p.beside) return p.grid;
+  PrefixSize x = {0, 0, 0};
+  if ((int)threadIdx.x < p.G) (void)prefix_size(p, threadIdx.x, x);
+  long long units;
+  (void)block_scan((long long)x.row_tiles() * x.tiles, tmp, units);
+  return min(p.grid, 2 * (p.sms - prefix_sms(p, units, tmp)));
+}
+
+// what of a call the kernels get (hca_cache_attn.cu)
+void shared_params(const CacheAttnArgs &a, SharedAttnParams &p);
 
 // tensor-core kernel (hca_cache_attn_tc.cu)
 int tc_cache_ctas();     // CTAs per SM

@@ -127,7 +127,7 @@ struct __align__(16) PageMeta {
   int pad[2];
 };
 
-template <int NQ, int D>
+template <int NQ, int D, int Scan>
 struct Shared {
   uint4 join[kWG * 4];  // O on its way out: 64 bytes of each lane's row
   uint64_t meta_full[kMetaStages], meta_empty[kMetaStages];
@@ -149,6 +149,7 @@ struct Shared {
   float q_factor[NQ];                            // log2(e) |scale| / (a row's factor)
   float2 ml[kWG];                                // copies: reference and sum of every lane
   int2 sums[2][kThreads / 32];                   // tiles and groups of each warp
+  long long scan[Scan];
   uint32_t tmem_base;
   int abort, first, range[2];
 };
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const P p) 
   using C = Cfg<NQ, D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ Shared<NQ, D> sh;
+  __shared__ Shared<NQ, D, P::kShared ? 33 : 1> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int *abort_flag = &sh.abort;
   int32_t *status = &p.err[blockIdx.x];
@@ -266,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const P p) 
   if (p.in_cta) {
     // one thread per request; where some bring more than one group, one per group
     int n = 0, r = tid, k = 0;
+    const int grid = own_grid(p, sh.scan);
     bool ok = prefixes_ok(p);
     if (tid < p.R) ok = request_chunks(p, tid, n) && ok;
     bool mine = n == 1;
@@ -300,9 +302,9 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const P p) 
     // us, 24.9 cut anywhere, 20 over up to 20,000 at m = 4 27.4 and 30.7; more do not:
     // 140 over 3,000 rows 24.8 cut anywhere, 30.8 with 4 more, 64 over 60,000 to
     // 131,072 rows 95 cut anywhere, 107 with as many as it takes.
-    quota = cta_quota(ntiles, p.grid, p.min_tiles);
-    const int own = cta_quota(ntiles, max(p.grid - ngroups, 1), p.min_tiles);
-    const bool whole_groups = ngroups < p.grid && own <= quota + 2;
+    quota = cta_quota(ntiles, grid, p.min_tiles);
+    const int own = cta_quota(ntiles, max(grid - ngroups, 1), p.min_tiles);
+    const bool whole_groups = ngroups < grid && own <= quota + 2;
     if (whole_groups) {
       quota = own;
       g.tile0 = quota * scan_tiles(mine ? (g.ntiles + quota - 1) / quota : 0, mine, sh.sums[1], total, ngroups, index);
@@ -1008,6 +1010,9 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const P p) 
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (P::kShared) {
+    if (p.beside && blockIdx.x == 0) pdl_wait();  // who waits for this kernel waits for the prefixes' too
+  }
   if (tid == 0 && sh.abort) atomicExch(status, HCA_ERR_TIMEOUT);
   if (warp == 10) {
     tc_fence_after();
@@ -1022,7 +1027,9 @@ cudaError_t launch(const P &p, cudaStream_t st) {
   const cudaError_t e = attr.ensure(reinterpret_cast<const void *>(hca_cache_attn_kernel<NQ, D, P>), C::kSmem);
   if (e != cudaSuccess) return e;
   ProfScope prof(kKCacheAttn, st);
-  if (!p.in_cta) return launch_behind(hca_cache_attn_kernel<NQ, D, P>, dim3(p.grid), kThreads, C::kSmem, st, p);
+  bool behind = !p.in_cta;
+  if constexpr (P::kShared) behind = behind || p.beside;
+  if (behind) return launch_behind(hca_cache_attn_kernel<NQ, D, P>, dim3(p.grid), kThreads, C::kSmem, st, p);
   hca_cache_attn_kernel<NQ, D, P><<<p.grid, kThreads, C::kSmem, st>>>(p);
   return cudaGetLastError();
 }

@@ -35,6 +35,7 @@
 #include <cfloat>
 #include <climits>
 
+#include "hca_cache_attn.cuh"
 #include "hca_cache_tc.cuh"
 
 namespace hca {
@@ -43,7 +44,7 @@ using namespace cache;
 
 namespace {
 
-constexpr int kRowTile = 256, kSharedMaxGroups = 256, kMaxGrid = 256;
+constexpr int kSharedMaxGroups = 256, kMaxGrid = 256, kPadded = 6;
 constexpr int kWG = 128, kThreads = 4 * kWG;
 constexpr int kMetaStages = 8, kKvStages = 4;
 constexpr int kRegsSoft = 168, kRegsConv = 88, kRegsIssue = 88;
@@ -54,28 +55,24 @@ __device__ __forceinline__ constexpr uint32_t col_s(int x, int h) { return 128u 
 __device__ __forceinline__ constexpr uint32_t col_o(int x) { return 256u + 128u * x; }
 
 struct SharedParams {
-  const __nv_bfloat16 *q;
-  const int32_t *start, *first, *cols;
-  CacheSet comp;
-  int32_t *err;     // [grid]
-  float2 *part_ml;  // [slots][256] reference exponent and sum
-  float *part_o;    // [slots][256][D]
+  SharedAttnParams own;  // of the requests' own keys
+  int32_t *err;          // [grid]
+  float2 *part_ml;       // [slots][256] reference exponent and sum
+  float *part_o;         // [slots][256][D]
   const float *own_out, *own_lse;
-  const SchedHeader *own;  // of the requests' own keys
   int32_t *status;
   __nv_bfloat16 *out;
   float *lse;
-  int N, R, H, D, G, log_bs, grid;
-  float scale;
-  uint64_t wait_ns;
+  int grid;              // CTAs of the prefixes' kernel
   int stall;
-  int merge;        // the requests' own keys are done: row tiles that are not cut are finished here
+  int merge;             // the requests' own keys are done: row tiles that are not cut are finished here
 };
 
 // A prefix with its rows and its place in the line.
 struct Prefix {
   int row0, rows;   // rows of q and out
   int tiles, pages; // key tiles, pages
+  int span;         // units that a row tile takes of the line: its key tiles, or more (below)
   int line0, rt0;   // first unit, first row tile
   int request;      // whose table is read
 };
@@ -83,48 +80,67 @@ struct Prefix {
 struct Table {
   Prefix g[kSharedMaxGroups];
   long long tmp[33];
-  int row_tiles;    // of all prefixes, those without common entries among them
+  int pieces[kPadded];  // CTAs that row tiles of their own take with so many units more each
+  int row_tiles;        // of all prefixes, those without common entries among them
+  int quota;            // units of a CTA
 };
 
 // The line, by all threads of a block (at least kSharedMaxGroups): its units, -1 if
 // the prefixes are refused.
+//
+// A CTA that has the end of one row tile and the beginning of the next pays for an
+// epilogue, a q and a pipeline that fills again, about kPadded - 1 units' time.  So
+// where row tiles can be cut into pieces of up to that much more than an equal
+// share, each CTA gets one piece (the line has gaps then: `span`).
 __device__ __forceinline__ int make_table(const SharedParams &p, Table &t) {
   const int i = threadIdx.x;
-  Prefix x = {0, 0, 0, 0, 0, 0, 0};
+  Prefix x = {0, 0, 0, 0, 0, 0, 0, 0};
   bool ok = true;
-  long long units = 0;
-  int rts = 0;
-  if (i < p.G) {
-    const int f0 = p.first[i], f1 = p.first[i + 1], c = p.cols[i];
-    ok = f0 >= 0 && f1 >= f0 && f1 <= p.R && (i > 0 || f0 == 0) && (i < p.G - 1 || f1 == p.R) && c >= 0 && c <= p.comp.cols;
-    if (ok) {
-      const int s0 = p.start[f0], s1 = p.start[f1];
-      ok = s0 >= 0 && s1 >= s0 && s1 <= p.N;
-      if (ok) {
-        x.row0 = s0 * p.H;
-        x.rows = (s1 - s0) * p.H;
-        x.pages = c;
-        x.request = f0;
-        ok = ((long long)c << p.log_bs) <= kMaxPos;
-        x.tiles = ok ? ((c << p.log_bs) + kTileKeys - 1) / kTileKeys : 0;
-        rts = (x.rows + kRowTile - 1) / kRowTile;
-        units = (long long)rts * x.tiles;
+  if (i < kPadded) t.pieces[i] = 0;
+  if (i < p.own.G) {
+    PrefixSize z;
+    ok = prefix_size(p.own, i, z);
+    x.row0 = z.row0;
+    x.rows = z.rows;
+    x.tiles = z.tiles;
+    x.pages = ok ? p.own.cols[i] : 0;
+    x.request = ok ? p.own.first[i] : 0;
+  }
+  const int rts = (x.rows + kRowTile - 1) / kRowTile;
+  ok = __syncthreads_and(ok);
+  long long all, nrt;
+  (void)block_scan((long long)rts * x.tiles, t.tmp, all);
+  x.rt0 = (int)block_scan((long long)rts, t.tmp, nrt);
+  ok = ok && all < kMaxTiles;
+  if (!ok) all = 0;
+  const int ctas = p.own.beside ? max(prefix_sms(p.own, all, t.tmp), 1) : p.grid;
+  int quota = max((int)((all + ctas - 1) / ctas), 1);
+  const bool few = nrt <= ctas;  // else there are more row tiles than CTAs
+  if (ok && few && x.tiles > 0) {
+#pragma unroll
+    for (int k = 0; k < kPadded; ++k) atomicAdd(&t.pieces[k], rts * ((x.tiles + quota + k - 1) / (quota + k)));
+  }
+  __syncthreads();
+  bool pad = false;
+  if (ok && few) {
+    for (int k = 0; k < kPadded && !pad; ++k) {
+      if (t.pieces[k] <= ctas) {
+        pad = true;
+        quota += k;
       }
     }
   }
-  ok = __syncthreads_and(ok);
-  long long all, nrt;
-  const long long line0 = block_scan(units, t.tmp, all);
-  x.rt0 = (int)block_scan((long long)rts, t.tmp, nrt);
-  ok = ok && all < kMaxTiles;
+  x.span = pad ? (x.tiles + quota - 1) / quota * quota : x.tiles;
+  const long long line0 = block_scan((long long)rts * x.span, t.tmp, all);
   x.line0 = ok ? (int)line0 : 0;
-  if (i < p.G) t.g[i] = x;
-  if (i == 0) t.row_tiles = (int)nrt;
+  if (i < p.own.G) t.g[i] = x;
+  if (i == 0) {
+    t.row_tiles = (int)nrt;
+    t.quota = quota;
+  }
   __syncthreads();
   return ok ? (int)all : -1;
 }
-
-__device__ __forceinline__ int units_per_cta(int units, int grid) { return max((units + grid - 1) / grid, 1); }
 
 // What a CTA has of a row tile.
 struct Part {
@@ -139,25 +155,28 @@ struct Part {
 struct Walk {
   int u, end, g;
   __device__ __forceinline__ Part next(const Table &t, int cta) {
-    while (u >= t.g[g].line0 + (t.g[g].rows + kRowTile - 1) / kRowTile * t.g[g].tiles) ++g;
+    while (u >= t.g[g].line0 + (t.g[g].rows + kRowTile - 1) / kRowTile * t.g[g].span) ++g;
     const Prefix &x = t.g[g];
-    const int rt = (u - x.line0) / x.tiles;
+    const int rt = (u - x.line0) / x.span;
     Part s;
-    s.j0 = u - x.line0 - rt * x.tiles;
-    s.j1 = min(x.tiles, s.j0 + (end - u));
+    s.j0 = u - x.line0 - rt * x.span;
+    const int n = min(x.span - s.j0, end - u);
+    s.j1 = min(x.tiles, s.j0 + n);
     s.whole = s.j0 == 0 && s.j1 == x.tiles;
     s.row0 = x.row0 + rt * kRowTile;
     s.rows = min(kRowTile, x.rows - rt * kRowTile);
     s.slot = x.rt0 + rt + cta;
     s.pages = x.pages;
     s.request = x.request;
-    u += s.j1 - s.j0;
+    u += n;
     s.last = u >= end;
     return s;
   }
 };
 
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+__device__ __forceinline__ void prefetch_line(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); }
 
 template <int D>
 struct Cfg {
@@ -199,6 +218,17 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
   volatile int *abort_flag = &sh.abort;
   int32_t *status = &p.err[blockIdx.x];
 
+  // what the schedule looks at, and this CTA's share of q, on their way to L2
+  for (int r = tid * 32; r < p.own.R; r += kThreads * 32) {
+    prefetch_line(p.own.start + r);
+    prefetch_line(p.own.held + r);
+  }
+  if (tid == kThreads - 1) {
+    prefetch_line(p.own.first);
+    prefetch_line(p.own.cols);
+    const size_t bytes = (size_t)p.own.N * p.own.H * D * 2, share = (bytes / gridDim.x + 15) & ~(size_t)15, at = share * blockIdx.x;
+    if (!p.merge && at < bytes) prefetch_l2(static_cast<const uint8_t *>(p.own.q) + at, (uint32_t)min(share, bytes - at));
+  }
   if (tid == 0) {
     for (int s = 0; s < kMetaStages; ++s) {
       mbar_init(&sh.meta_full[s], 1);
@@ -226,35 +256,35 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
     tmem_alloc(&sh.tmem_base, kTmem);
     tmem_relinquish();
   }
-  const int units = make_table(p, sh.table);
+  pdl_launch_dependents();  // the requests' own keys, where they run beside this
+  const int units = make_table(p, sh.table), quota = sh.table.quota;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(sh.tmem_base);
-  const int quota = units_per_cta(max(units, 0), p.grid);
   const long long c0 = (long long)quota * blockIdx.x;
   const bool busy = c0 < units;
   const Walk from = {(int)c0, (int)min(c0 + quota, (long long)max(units, 0)), 0};
 
-  const uint32_t limit_ns = (uint32_t)p.wait_ns;
+  const uint32_t limit_ns = (uint32_t)p.own.wait_ns;
   auto wait_bar = [&](uint64_t *bar, uint32_t parity) {  // mostly there already
     return __all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity) || mbar_wait_idle(bar, parity, abort_flag, limit_ns));
   };
-  const int ppt = kTileKeys >> p.log_bs;  // pages of a tile: 1 .. 8
+  const int ppt = kTileKeys >> p.own.log_bs;  // pages of a tile: 1 .. 8
   if (warp >= 12) {
     setmaxnreg_dec<kRegsIssue>();
     if (warp == 12 && busy) {
       // ------------------------------------------------------------ pages
       const int batch = 32 / ppt;  // tiles whose pages the warp's lanes look up at once
-      const uint32_t page_bytes = D << p.log_bs;
+      const uint32_t page_bytes = D << p.own.log_bs;
       Walk walk = from;
       uint32_t n = 0;
       bool ok = true;
       auto page_scale = [&](const Part &s, int page, int &id) {
-        id = p.comp.table[(size_t)s.request * p.comp.cols + page];
-        const bool in = id >= 0 && id < p.comp.nblocks;
+        id = p.own.comp.table[(size_t)s.request * p.own.comp.cols + page];
+        const bool in = id >= 0 && id < p.own.comp.nblocks;
         if (!in) id = -1;
-        return in ? p.comp.scale[id] : 0.f;
+        return in ? p.own.comp.scale[id] : 0.f;
       };
 #pragma unroll 1
       for (bool last = false; ok && !last;) {
@@ -263,12 +293,15 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
         // the unit: the largest scale of the segment's pages
         int unit = INT_MIN;
         const int v0 = s.j0 * ppt, v1 = min(s.j1 * ppt, s.pages);
+        int id = -1;  // of the lane's page of the next tiles
+        float scale = 0.f;
+        if (v0 + lane < v1) scale = page_scale(s, v0 + lane, id);
 #pragma unroll 4
         for (int v = v0 + lane; v < v1; v += 32) {
-          int id;
-          const float scale = page_scale(s, v, id);
+          int other;
+          const float sc = v < v0 + 32 ? scale : page_scale(s, v, other);
           float part;
-          if (scale > 0.f && scale < INFINITY) unit = max(unit, split_scale(scale, part));
+          if (sc > 0.f && sc < INFINITY) unit = max(unit, split_scale(sc, part));
         }
         unit = __reduce_max_sync(0xffffffffu, unit);
         unit = unit == INT_MIN ? 0 : min(max(unit, kLeastUnit), kMostUnit);
@@ -279,12 +312,11 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
           uint32_t factor = f16x2_exp2(0);
           float rest = 1.f;
           bool bad = false;
-          if (v < v1 && lane < batch * ppt) {
-            int id;
-            const float scale = page_scale(s, v, id);
+          if (v < v1) {
+            if (jb > s.j0) scale = page_scale(s, v, id);
             bad = !(scale > 0.f && scale < INFINITY);
             if (!bad) {
-              rows = p.comp.pool + (size_t)id * page_bytes;
+              rows = p.own.comp.pool + (size_t)id * page_bytes;
               float part;
               const int ex = split_scale(scale, part), e = min(max(ex - unit, kLeastExp), kMostExp);
               factor = f16x2_exp2(e);
@@ -309,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
             const bool odd = __any_sync(0xffffffffu, here && rest != 1.f), wrong = __any_sync(0xffffffffu, here && bad);
             if (lane == 0) {
               to.valid = valid;
-              to.keys = min(ppt, s.pages - (jb + t) * ppt) << p.log_bs;
+              to.keys = min(ppt, s.pages - (jb + t) * ppt) << p.own.log_bs;
               to.unit = unit;
               to.odd = odd;
               to.bad = wrong;
@@ -339,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
         auto wait = [&](uint64_t *bar, uint32_t parity) {
           return mbar_try_wait(smem_u32(bar), parity) || mbar_wait_idle(bar, parity, abort_flag, limit_ns);
         };
-        if (p.stall && x == 0) ok = mbar_wait(&sh.never, 0, abort_flag, status, p.wait_ns);  // injected: nothing arrives
+        if (p.stall && x == 0) ok = mbar_wait(&sh.never, 0, abort_flag, status, p.own.wait_ns);  // injected: nothing arrives
 #pragma unroll 1
         for (bool last = false; ok && !last; ++nseg) {
           const Part s = walk.next(sh.table, blockIdx.x);
@@ -402,13 +434,19 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
       const uint32_t to0 = smem_u32(smem) + (ch >> 2) * kHalfTile + row0 * 128;
       const uint32_t swz0 = (((2 * (ch & 3)) ^ (row0 & 7)) << 4);  // the other piece's differs in one bit
       static_assert(kRowStep % 8 == 0, "a thread's rows have one swizzle");
-      const uint32_t tiles = from.end - from.u;
+      uint32_t tiles = 0;
+      Walk walk = from;
+      for (bool last = false; !last;) {
+        const Part s = walk.next(sh.table, blockIdx.x);
+        last = s.last;
+        tiles += s.j1 - s.j0;
+      }
       // Piece i of a tile, from memory (zero where there is no page).
       auto piece = [&](const TileMeta &meta, int i, uint4 &w) {
-        const int row = row0 + i * kRowStep, page = row >> p.log_bs;
+        const int row = row0 + i * kRowStep, page = row >> p.own.log_bs;
         const uint8_t *rows = meta.rows[page];
         w = make_uint4(0, 0, 0, 0);
-        if (rows) w = *reinterpret_cast<const uint4 *>(rows + (row - (page << p.log_bs)) * D + ch * 16);
+        if (rows) w = *reinterpret_cast<const uint4 *>(rows + (row - (page << p.own.log_bs)) * D + ch * 16);
       };
       uint4 raw[kPer];
       (void)wait_bar(&sh.meta_full[0], 0);
@@ -427,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
           const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) e4m3x4_to_f16(w[e], f[2 * e], f[2 * e + 1]);
-          const uint32_t factor = meta.factor[(row0 + i * kRowStep) >> p.log_bs];
+          const uint32_t factor = meta.factor[(row0 + i * kRowStep) >> p.own.log_bs];
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] = f16x2_mul(f[e], factor);
           const uint32_t at = dst + i * kRowStep * 128;
@@ -451,10 +489,23 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
       Walk walk = from;
       const uint32_t q_at = smem_u32(smem) + C::kOffQ + x * C::kStageBytes + row * 128;
       uint32_t n = 0;
+      // A warp's rows of q on their way to shared memory, as they are: D / 8 lanes copy a
+      // row's 16-byte pieces.
+      auto load_q = [&](const Part &s) {
+        constexpr int kLanes = D / 8;
+        const int c = lane % kLanes;
+#pragma unroll 4
+        for (int i = 0; i < kLanes; ++i) {
+          const int r = (warp & 3) * 32 + i * (32 / kLanes) + lane / kLanes;
+          const bool there = x * kWG + r < s.rows;
+          const uint32_t to = smem_u32(smem) + C::kOffQ + x * C::kStageBytes + (c >> 3) * kHalfTile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          cp_async_16(to, static_cast<const __nv_bfloat16 *>(p.own.q) + ((size_t)s.row0 + (there ? x * kWG + r : 0)) * D + c * 8, there ? 16 : 0);
+        }
+      };
+      Part s = walk.next(sh.table, blockIdx.x);
+      load_q(s);
 #pragma unroll 1
-      for (bool last = false; !last;) {
-        const Part s = walk.next(sh.table, blockIdx.x);
-        last = s.last;
+      for (;;) {
         float m_run = -INFINITY, m_use = 0.f, l_run = 0.f;  // m_use: what is subtracted
         int unit = 0;
         const bool mine = x * kWG + row < s.rows;
@@ -462,29 +513,33 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
         // a negative scale goes into q's sign
         float cs;
         {
-          uint32_t w[D / 2];
-          const uint4 *q = reinterpret_cast<const uint4 *>(p.q + ((size_t)s.row0 + (mine ? x * kWG + row : 0)) * D);
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = mine ? q[c] : make_uint4(0, 0, 0, 0);
-            w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
-          }
+          auto piece_at = [&](int c) { return q_at + (c >> 3) * kHalfTile + (((c & 7) ^ (row & 7)) << 4); };
+          cp_async_wait();
+          __syncwarp();
           uint32_t amax = 0;
-#pragma unroll
-          for (int c = 0; c < D / 2; ++c) amax = bf16x2_max(amax, w[c] & 0x7fff7fffu);
-          const int ex = scale_exponent(__uint_as_float(max(amax & 0xffffu, amax >> 16) << 16), kLeastQExp);
-          const float inv = p.scale < 0.f ? -exp2_int(-ex) : p.scale > 0.f ? exp2_int(-ex) : 0.f;
-          cs = exp2_int(ex) * fabsf(p.scale) * 1.4426950408889634f;
-          const uint64_t inv2 = f32x2(__float_as_uint(inv), __float_as_uint(inv));
-#pragma unroll
-          for (int c = 0; c < D / 2; ++c) {
-            float lo, hi;
-            f32x2_split(fmul2(f32x2(w[c] << 16, w[c] & 0xffff0000u), inv2), lo, hi);
-            w[c] = f16x2_rn(lo, hi);
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c) {
+            uint32_t w[4];
+            ld_shared(piece_at(c), w);
+            amax = bf16x2_max(amax, bf16x2_max(bf16x2_max(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                               bf16x2_max(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu)));
           }
+          const int ex = scale_exponent(__uint_as_float(max(amax & 0xffffu, amax >> 16) << 16), kLeastQExp);
+          const float inv = p.own.scale < 0.f ? -exp2_int(-ex) : p.own.scale > 0.f ? exp2_int(-ex) : 0.f;
+          cs = exp2_int(ex) * fabsf(p.own.scale) * 1.4426950408889634f;
+          const uint64_t inv2 = f32x2(__float_as_uint(inv), __float_as_uint(inv));
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c) {
+            uint32_t w[4];
+            ld_shared(piece_at(c), w);
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c)
-            st_shared(q_at + (c >> 3) * kHalfTile + (((c & 7) ^ (row & 7)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+            for (int e = 0; e < 4; ++e) {
+              float lo, hi;
+              f32x2_split(fmul2(f32x2(w[e] << 16, w[e] & 0xffff0000u), inv2), lo, hi);
+              w[e] = f16x2_rn(lo, hi);
+            }
+            st_shared(piece_at(c), w[0], w[1], w[2], w[3]);
+          }
           fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.q_full[x]);
@@ -516,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
             if (odd) {
 #pragma unroll
               for (int c = 0; c < 64; c += 16) {
-                const float rest = meta.rest[(h * 64 + c) >> p.log_bs];
+                const float rest = meta.rest[(h * 64 + c) >> p.own.log_bs];
 #pragma unroll
                 for (int y = 0; y < 16; ++y) sv[c + y] = __float_as_uint(__uint_as_float(sv[c + y]) * rest);
               }
@@ -555,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
                   float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
                   acc[(y >> 1) & 1] = fadd2(acc[(y >> 1) & 1], f32x2(__float_as_uint(e0), __float_as_uint(e1)));
                   if constexpr (decltype(scaled)::value) {
-                    const float rest = meta.rest[(h * 64 + 32 * c + y) >> p.log_bs];
+                    const float rest = meta.rest[(h * 64 + 32 * c + y) >> p.own.log_bs];
                     e0 *= rest;
                     e1 *= rest;
                   }
@@ -578,6 +633,10 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
           if (lane == 0) mbar_arrive(&sh.meta_empty[ms]);
         }
         if (*abort_flag) l_run = __int_as_float(0x7fc00000);
+        if (!s.last) {
+          Walk ahead = walk;
+          load_q(ahead.next(sh.table, blockIdx.x));  // arrives while O leaves
+        }
         const bool merge = p.merge && s.whole;
         const int nrows = s.rows - x * kWG;
         const size_t at_row = merge ? (size_t)s.row0 + x * kWG : (size_t)s.slot * kRowTile + x * kWG;  // of the tile's first row
@@ -636,6 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
           __syncwarp();
         }
         tc_fence_before();
+        if (s.last) break;
+        s = walk.next(sh.table, blockIdx.x);
       }
     }
   }
@@ -664,30 +725,31 @@ __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const Shar
   const int tid = threadIdx.x, l = tid % kLanes;
   pdl_wait();
   const int units = make_table(p, table);
-  int worst = p.own->status;
+  const SchedHeader *own = p.own.hdr;
+  int worst = own->status;
   for (int i = tid; i < p.grid; i += kJoinThreads) worst = max(worst, p.err[i] == HCA_ERR_TIMEOUT ? 1000 : p.err[i]);
   const bool late = __syncthreads_or(worst == 1000 || worst == HCA_ERR_TIMEOUT), wrong = __syncthreads_or(worst != HCA_OK);
   if (blockIdx.x == 0 && tid == 0) *p.status = late ? HCA_ERR_TIMEOUT : wrong ? HCA_ERR_CACHE : HCA_OK;
-  const bool refused = units < 0 || p.own->ntiles < 0 || late;  // then all rows are NaN
+  const bool refused = units < 0 || own->ntiles < 0 || late;  // then all rows are NaN
   if (refused) {
-    const size_t rows = (size_t)p.N * p.H;
+    const size_t rows = (size_t)p.own.N * p.own.H;
     for (size_t row = (size_t)blockIdx.x * kRows + tid / kLanes; row < rows; row += (size_t)gridDim.x * kRows) {
       *reinterpret_cast<uint2 *>(p.out + row * D + 4 * l) = make_uint2(0x7fc07fc0u, 0x7fc07fc0u);
       if (l == 0) p.lse[row] = __int_as_float(0x7fc00000);
     }
     return;
   }
-  const int quota = units_per_cta(units, p.grid);
+  const int quota = table.quota;
   constexpr int kChunks = kRowTile / (kRows * U);  // of a row tile, a block's each
   for (int item = blockIdx.x; item < table.row_tiles * kChunks; item += gridDim.x) {
-    int lo = 0, hi = p.G;  // the row tile's prefix
+    int lo = 0, hi = p.own.G;  // the row tile's prefix
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (table.g[mid].rt0 <= item / kChunks) lo = mid; else hi = mid;
     }
     const Prefix &x = table.g[lo];
-    const int rt = item / kChunks - x.rt0, u0 = x.line0 + rt * x.tiles, first = u0 / quota;
-    const int parts = x.tiles > 0 ? (u0 + x.tiles - 1) / quota - first + 1 : 0;
+    const int rt = item / kChunks - x.rt0, u0 = x.line0 + rt * x.span, first = u0 / quota;
+    const int parts = x.tiles > 0 ? (u0 + x.span - 1) / quota - first + 1 : 0;
     if (p.merge && parts == 1) continue;  // finished by the CTA that had it
     const int r0 = item % kChunks * (kRows * U) + tid / kLanes;  // the lane's first row; the others are kRows apart
     float4 o[U];
@@ -784,9 +846,6 @@ cudaError_t launch(const CacheAttnArgs &a, SharedParams &p, int sms, cudaStream_
     hca_cache_prefix_kernel<D><<<p.grid, kThreads, C::kSmem, st>>>(p);
     return cudaGetLastError();
   };
-  // As many row tiles as CTAs: most are one CTA's, which adds the rows' own part
-  // where it has O.
-  p.merge = (long long)p.N * p.H >= (long long)kRowTile * p.grid;
   if (!p.merge) e = prefix();
   if (e == cudaSuccess) e = cache_attn(a, st);
   if (e == cudaSuccess && p.merge) e = prefix();
@@ -795,7 +854,7 @@ cudaError_t launch(const CacheAttnArgs &a, SharedParams &p, int sms, cudaStream_
   // Many rows: 4 of them a lane, whose loads are in flight together.
   const bool many = p.merge;
   const long long per = (long long)kJoinThreads / (D / 4) * (many ? 4 : 1);
-  const dim3 grid((unsigned)std::min<long long>((long long)p.N * p.H / per + p.G * (kRowTile / per), (many ? 3ll : 5ll) * sms));
+  const dim3 grid((unsigned)std::min<long long>((long long)p.own.N * p.own.H / per + p.own.G * (kRowTile / per), (many ? 3ll : 5ll) * sms));
   if (many) return launch_behind(hca_cache_join_kernel<D, 4>, grid, kJoinThreads, 0, st, p);
   return launch_behind(hca_cache_join_kernel<D, 1>, grid, kJoinThreads, 0, st, p);
 }
@@ -820,30 +879,26 @@ cudaError_t cache_attn_shared(const CacheAttnArgs &args, cudaStream_t st) {
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorNoDevice;
   SharedParams p;
-  p.q = static_cast<const __nv_bfloat16 *>(a.q);
-  p.start = a.start; p.first = a.share.first; p.cols = a.share.cols;
-  p.comp = a.comp;
   p.err = reinterpret_cast<int32_t *>(ws + l.off_err);
   p.part_ml = reinterpret_cast<float2 *>(ws + l.off_ml);
   p.part_o = reinterpret_cast<float *>(ws + l.off_o);
   p.own_out = reinterpret_cast<const float *>(ws + l.off_out);
   p.own_lse = reinterpret_cast<const float *>(ws + l.off_lse);
-  p.own = reinterpret_cast<const SchedHeader *>(ws + l.off_own);
   p.status = reinterpret_cast<int32_t *>(ws);
   p.out = static_cast<__nv_bfloat16 *>(a.out);
   p.lse = a.lse;
-  p.N = a.N; p.R = a.R; p.H = a.H; p.D = a.D; p.G = a.share.G;
-  p.log_bs = 0;
-  while ((1 << p.log_bs) < a.bs) ++p.log_bs;
   p.grid = std::min(sms, kMaxGrid);
-  p.scale = a.scale;
-  p.wait_ns = std::min<uint64_t>(a.wait_ns, 4000000000u);
+  // As many row tiles as CTAs: most are one CTA's, which adds the rows' own part
+  // where it has O.  Otherwise both run at the same time.
+  p.merge = (long long)a.N * a.H >= (long long)kRowTile * p.grid;
   p.stall = a.stall;
   a.stall = 0;
   a.out = ws + l.off_out;
   a.lse = reinterpret_cast<float *>(ws + l.off_lse);
   a.ws = ws + l.off_own;
   a.share.apart = 1;
+  a.share.beside = !p.merge && sms <= kMaxGrid;
+  shared_params(a, p.own);
   return a.D == 64 ? launch<64>(a, p, sms, st) : launch<128>(a, p, sms, st);
 }
 

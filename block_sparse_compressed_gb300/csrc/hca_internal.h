@@ -179,6 +179,7 @@ struct CacheShare {
   const int32_t *first, *cols;  // [G+1] requests, [G] common columns of their compressed tables
   int G;                        // 0: nothing is shared
   int apart;                    // hca_cache_attn's kernels leave the common columns out and write fp32 rows
+  int beside;                   // and run while the prefixes' kernel does
 };
 struct CacheAttnArgs {
   const void *q;
