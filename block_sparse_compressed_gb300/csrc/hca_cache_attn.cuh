@@ -165,44 +165,69 @@ __device__ __forceinline__ bool prefix_size(const SharedAttnParams &p, int g, Pr
   return true;
 }
 
-// SMs of the prefixes' kernel, when it has `units` steps in all and the requests'
-// own keys run beside it: so many that both end at about the same time.  By every
-// thread of a block, in both kernels, which come to the same answer: each request's
-// own tiles are estimated by its last chunk's.
-//   a step takes 1.7 us, an own tile 2.4 us with two CTAs on an SM (a group's
-//   beginning and end two more), and the kernels' beginnings and ends about 10 us
-__device__ __forceinline__ int prefix_sms(const SharedAttnParams &p, long long units, long long *tmp) {
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Tiles of the requests' own keys, those of requests i, i + step, ...: each is
+// estimated by its last chunk's.
+__device__ __forceinline__ long long own_tiles(const SharedAttnParams &p, int i, int step) {
   long long own = 0;
-  for (int r = threadIdx.x; r < p.R; r += blockDim.x) {
+  for (int r = i; r < p.R; r += step) {
     int n;
     Group g;
     g.ntiles = 0;
     if (request_chunks(p, r, n) && n > 0) (void)chunk_group(p, r, n - 1, g);
     own += (long long)(g.ntiles + kGroupCost) * n * p.slices;
   }
-  long long all;
-  (void)block_scan(own, tmp, all);
-  long long best = 0x7fffffffffffffffll;
-  const int lane = threadIdx.x & 31;
-  for (int s = 1 + lane; s < p.sms; s += 32) {  // SMs of the own keys
-    const long long a = 10000 + (units + p.sms - s - 1) / (p.sms - s) * 1700;
-    const long long b = 10000 + max((all + 2 * s - 1) / (2 * s), (long long)p.min_tiles) * 2400;
-    best = min(best, max(a, b) << 12 | s);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
-  return units == 0 ? 0 : p.sms - (int)(best & 0xfff);
+  return own;
 }
 
-// CTAs that the own keys' kernel works with
+// SMs of the prefixes' kernel, when it has `units` steps in all and the requests'
+// own keys (`own` tiles) run beside it: so many that both end at about the same time
+// (all lanes of a warp call it).  A step takes 1.65 us, an own tile 2.8 us with two
+// CTAs on an SM (a group's beginning and end two more).  What the two kernels make
+// of it need not agree.
+__device__ __forceinline__ int prefix_sms(const SharedAttnParams &p, long long units, long long own) {
+  if (units == 0) return 0;
+  float best = INFINITY;
+  int at = 1;
+  for (int s = 1 + (threadIdx.x & 31); s < p.sms; s += 32) {  // SMs of the own keys
+    const float a = ceilf(__fdividef((float)units, (float)(p.sms - s))) * 1.65f;
+    const float b = fmaxf(ceilf(__fdividef((float)own, (float)(2 * s))), (float)p.min_tiles) * 2.8f;
+    const float t = fmaxf(a, b);
+    if (t < best) best = t, at = s;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float t = __shfl_xor_sync(0xffffffffu, best, o);
+    const int s = __shfl_xor_sync(0xffffffffu, at, o);
+    if (t < best || (t == best && s < at)) best = t, at = s;
+  }
+  return p.sms - at;
+}
+
+// CTAs that the own keys' kernel works with (`tmp` holds 33 values)
 __device__ __forceinline__ int own_grid(const AttnParams &p, long long *) { return p.grid; }
 __device__ __forceinline__ int own_grid(const SharedAttnParams &p, long long *tmp) {
   if (!p.beside) return p.grid;
+  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   PrefixSize x = {0, 0, 0};
   if ((int)threadIdx.x < p.G) (void)prefix_size(p, threadIdx.x, x);
-  long long units;
-  (void)block_scan((long long)x.row_tiles() * x.tiles, tmp, units);
-  return min(p.grid, 2 * (p.sms - prefix_sms(p, units, tmp)));
+  const long long u = warp_sum((long long)x.row_tiles() * x.tiles), o = warp_sum(own_tiles(p, threadIdx.x, blockDim.x));
+  if ((threadIdx.x & 31) == 0) {
+    tmp[warp] = u;
+    tmp[16 + warp] = o;
+  }
+  __syncthreads();
+  long long units = 0, own = 0;
+  for (int w = 0; w < warps; ++w) {
+    units += tmp[w];
+    own += tmp[16 + w];
+  }
+  return min(p.grid, 2 * (p.sms - prefix_sms(p, units, own)));
 }
 
 // what of a call the kernels get (hca_cache_attn.cu)

@@ -54,8 +54,11 @@ constexpr uint32_t kTmem = 512;
 __device__ __forceinline__ constexpr uint32_t col_s(int x, int h) { return 128u * x + 64u * h; }
 __device__ __forceinline__ constexpr uint32_t col_o(int x) { return 256u + 128u * x; }
 
+struct Table;
+
 struct SharedParams {
   SharedAttnParams own;  // of the requests' own keys
+  Table *table;          // what the prefixes' kernel went by
   int32_t *err;          // [grid]
   float2 *part_ml;       // [slots][256] reference exponent and sum
   float *part_o;         // [slots][256][D]
@@ -74,72 +77,98 @@ struct Prefix {
   int tiles, pages; // key tiles, pages
   int span;         // units that a row tile takes of the line: its key tiles, or more (below)
   int line0, rt0;   // first unit, first row tile
-  int request;      // whose table is read
+  int request;      // whose compressed table is read
 };
 
 struct Table {
-  Prefix g[kSharedMaxGroups];
-  long long tmp[33];
-  int pieces[kPadded];  // CTAs that row tiles of their own take with so many units more each
-  int row_tiles;        // of all prefixes, those without common entries among them
+  int units;            // of the line, -1: the prefixes are refused
   int quota;            // units of a CTA
+  int row_tiles;        // of all prefixes, those without common entries among them
+  int pad;
+  Prefix g[kSharedMaxGroups];
 };
 
-// The line, by all threads of a block (at least kSharedMaxGroups): its units, -1 if
-// the prefixes are refused.
+// The line, by all threads of a block.  `tmp` holds a value for each warp.
 //
 // A CTA that has the end of one row tile and the beginning of the next pays for an
 // epilogue, a q and a pipeline that fills again, about kPadded - 1 units' time.  So
 // where row tiles can be cut into pieces of up to that much more than an equal
 // share, each CTA gets one piece (the line has gaps then: `span`).
-__device__ __forceinline__ int make_table(const SharedParams &p, Table &t) {
-  const int i = threadIdx.x;
-  Prefix x = {0, 0, 0, 0, 0, 0, 0, 0};
+__device__ __forceinline__ void make_table(const SharedParams &p, Table &t, long long *tmp) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   bool ok = true;
-  if (i < kPadded) t.pieces[i] = 0;
-  if (i < p.own.G) {
-    PrefixSize z;
-    ok = prefix_size(p.own, i, z);
-    x.row0 = z.row0;
-    x.rows = z.rows;
-    x.tiles = z.tiles;
-    x.pages = ok ? p.own.cols[i] : 0;
-    x.request = ok ? p.own.first[i] : 0;
-  }
-  const int rts = (x.rows + kRowTile - 1) / kRowTile;
-  ok = __syncthreads_and(ok);
-  long long all, nrt;
-  (void)block_scan((long long)rts * x.tiles, t.tmp, all);
-  x.rt0 = (int)block_scan((long long)rts, t.tmp, nrt);
-  ok = ok && all < kMaxTiles;
-  if (!ok) all = 0;
-  const int ctas = p.own.beside ? max(prefix_sms(p.own, all, t.tmp), 1) : p.grid;
-  int quota = max((int)((all + ctas - 1) / ctas), 1);
-  const bool few = nrt <= ctas;  // else there are more row tiles than CTAs
-  if (ok && few && x.tiles > 0) {
-#pragma unroll
-    for (int k = 0; k < kPadded; ++k) atomicAdd(&t.pieces[k], rts * ((x.tiles + quota + k - 1) / (quota + k)));
+  long long units = 0, nrt = 0;
+  if (warp == 0) {
+    for (int g = lane; g < p.own.G; g += 32) {
+      PrefixSize z;
+      const bool fine = prefix_size(p.own, g, z);
+      ok = ok && fine;
+      t.g[g] = Prefix{z.row0, z.rows, z.tiles, fine ? p.own.cols[g] : 0, z.tiles, 0, 0, fine ? p.own.first[g] : 0};
+      units += (long long)z.row_tiles() * z.tiles;
+      nrt += z.row_tiles();
+    }
+    units = warp_sum(units);
+    nrt = warp_sum(nrt);
+    ok = __all_sync(0xffffffffu, ok) && units < kMaxTiles;
+  } else if (p.own.beside) {
+    const long long own = warp_sum(own_tiles(p.own, tid - 32, blockDim.x - 32));
+    if (lane == 0) tmp[warp] = own;
   }
   __syncthreads();
-  bool pad = false;
-  if (ok && few) {
-    for (int k = 0; k < kPadded && !pad; ++k) {
-      if (t.pieces[k] <= ctas) {
-        pad = true;
-        quota += k;
+  if (warp == 0) {
+    int ctas = p.grid;
+    if (p.own.beside) {
+      const long long own = warp_sum(lane > 0 && lane < warps ? tmp[lane] : 0);
+      ctas = max(prefix_sms(p.own, ok ? units : 0, own), 1);
+    }
+    int quota = max((int)(((ok ? units : 0) + ctas - 1) / ctas), 1);
+    bool pad = false;
+    if (ok && nrt <= ctas) {  // else there are more row tiles than CTAs
+      for (int k = 0; k < kPadded && !pad; ++k) {
+        long long pieces = 0;
+        for (int g = lane; g < p.own.G; g += 32) pieces += (t.g[g].rows + kRowTile - 1) / kRowTile * ((t.g[g].tiles + quota + k - 1) / (quota + k));
+        pad = warp_sum(pieces) <= ctas;
+        if (pad) quota += k;
       }
     }
-  }
-  x.span = pad ? (x.tiles + quota - 1) / quota * quota : x.tiles;
-  const long long line0 = block_scan((long long)rts * x.span, t.tmp, all);
-  x.line0 = ok ? (int)line0 : 0;
-  if (i < p.own.G) t.g[i] = x;
-  if (i == 0) {
-    t.row_tiles = (int)nrt;
-    t.quota = quota;
+    int line = 0, rt = 0;
+    for (int g0 = 0; ok && g0 < p.own.G; g0 += 32) {
+      const int g = g0 + lane;
+      int n = 0, span = 0;
+      if (g < p.own.G) {
+        n = (t.g[g].rows + kRowTile - 1) / kRowTile;
+        span = pad ? (t.g[g].tiles + quota - 1) / quota * quota : t.g[g].tiles;
+      }
+      int a = n, b = n * span;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+        if (lane >= o) a += x, b += y;
+      }
+      if (g < p.own.G) {
+        t.g[g].span = span;
+        t.g[g].rt0 = rt + a - n;
+        t.g[g].line0 = line + b - n * span;
+      }
+      rt += __shfl_sync(0xffffffffu, a, 31);
+      line += __shfl_sync(0xffffffffu, b, 31);
+    }
+    if (lane == 0) {
+      t.units = ok ? line : -1;
+      t.quota = quota;
+      t.row_tiles = rt;
+    }
+    __syncwarp();
+    if (blockIdx.x == 0) {  // for the join
+      if (lane == 0) {
+        p.table->units = t.units;
+        p.table->quota = quota;
+        p.table->row_tiles = rt;
+      }
+      for (int g = lane; g < p.own.G; g += 32) p.table->g[g] = t.g[g];
+    }
   }
   __syncthreads();
-  return ok ? (int)all : -1;
 }
 
 // What a CTA has of a row tile.
@@ -204,6 +233,7 @@ struct Shared {
   uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], drain[2], never;
   TileMeta meta[kMetaStages];
   Table table;
+  long long tmp[kThreads / 32];
   uint32_t tmem_base;
   int abort;
 };
@@ -257,7 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
     tmem_relinquish();
   }
   pdl_launch_dependents();  // the requests' own keys, where they run beside this
-  const int units = make_table(p, sh.table), quota = sh.table.quota;
+  make_table(p, sh.table, sh.tmp);
+  const int units = sh.table.units, quota = sh.table.quota;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -715,16 +746,15 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
 // row's own keys (w_0 = 2^(lse - M)) and the parts of its prefix
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
-static_assert(kJoinThreads >= kSharedMaxGroups, "a thread for each prefix");
 
 template <int D, int U>  // U rows of a lane at a time
 __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const SharedParams p) {
-  __shared__ Table table;
   constexpr int kLanes = D / 4, kRows = kJoinThreads / kLanes;
   constexpr float kLog2e = 1.4426950408889634f;
   const int tid = threadIdx.x, l = tid % kLanes;
   pdl_wait();
-  const int units = make_table(p, table);
+  const Table &table = *p.table;
+  const int units = table.units, quota = table.quota, row_tiles = table.row_tiles;
   const SchedHeader *own = p.own.hdr;
   int worst = own->status;
   for (int i = tid; i < p.grid; i += kJoinThreads) worst = max(worst, p.err[i] == HCA_ERR_TIMEOUT ? 1000 : p.err[i]);
@@ -739,15 +769,14 @@ __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const Shar
     }
     return;
   }
-  const int quota = table.quota;
   constexpr int kChunks = kRowTile / (kRows * U);  // of a row tile, a block's each
-  for (int item = blockIdx.x; item < table.row_tiles * kChunks; item += gridDim.x) {
+  for (int item = blockIdx.x; item < row_tiles * kChunks; item += gridDim.x) {
     int lo = 0, hi = p.own.G;  // the row tile's prefix
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (table.g[mid].rt0 <= item / kChunks) lo = mid; else hi = mid;
     }
-    const Prefix &x = table.g[lo];
+    const Prefix x = table.g[lo];
     const int rt = item / kChunks - x.rt0, u0 = x.line0 + rt * x.span, first = u0 / quota;
     const int parts = x.tiles > 0 ? (u0 + x.span - 1) / quota - first + 1 : 0;
     if (p.merge && parts == 1) continue;  // finished by the CTA that had it
@@ -812,13 +841,15 @@ __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const Shar
 }
 
 struct Layout {
-  size_t off_own, off_out, off_lse, off_err, off_ml, off_o, bytes;
+  size_t off_table, off_own, off_out, off_lse, off_err, off_ml, off_o, bytes;
 };
 
 Layout layout_of(int N, int R, int H, int D, int G) {
   Layout l;
   const size_t rows = (size_t)N * H, slots = rows / kRowTile + G + kMaxGrid;
   size_t at = kHeaderBytes;
+  l.off_table = at;
+  at += align_up(sizeof(Table));
   l.off_own = at;
   at += align_up(cache_attn_ws_bytes(N, R, H, D, HCA_BF16));
   l.off_out = at;
@@ -879,6 +910,7 @@ cudaError_t cache_attn_shared(const CacheAttnArgs &args, cudaStream_t st) {
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorNoDevice;
   SharedParams p;
+  p.table = reinterpret_cast<Table *>(ws + l.off_table);
   p.err = reinterpret_cast<int32_t *>(ws + l.off_err);
   p.part_ml = reinterpret_cast<float2 *>(ws + l.off_ml);
   p.part_o = reinterpret_cast<float *>(ws + l.off_o);
