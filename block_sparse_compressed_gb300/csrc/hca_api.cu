@@ -83,6 +83,7 @@ std::atomic<long long> g_inject_launch_failures{0};
 std::atomic<int> g_inject_stall_mask{0};
 std::atomic<unsigned long long> g_wait_ns{kDefaultWaitNs};
 std::atomic<int> g_csa_union{0};
+std::atomic<int> g_shared_path{0};
 
 bool take_counter(std::atomic<long long> &c) {
   long long v = c.load();
@@ -98,6 +99,7 @@ bool take_launch_failure() { return take_counter(g_inject_launch_failures); }
 int take_stall_mask() { return g_inject_stall_mask.exchange(0); }
 uint64_t wait_limit_ns() { return g_wait_ns.load(); }
 int csa_union_setting() { return g_csa_union.load(); }
+int shared_path_setting() { return g_shared_path.load(); }
 }  // namespace hca
 
 extern "C" {
@@ -136,6 +138,7 @@ int hca_test_inject(int what, long long value) {
       g_inject_stall_mask = 0;
       g_wait_ns = kDefaultWaitNs;
       g_csa_union = 0;
+      g_shared_path = 0;
       return HCA_OK;
     case HCA_INJECT_LAUNCH_FAILURE: g_inject_launch_failures = value; return HCA_OK;
     case HCA_INJECT_STALL:
@@ -146,6 +149,10 @@ int hca_test_inject(int what, long long value) {
     case HCA_INJECT_CSA_UNION:
       if (value > 16384 || (value > 1 && value % 64 != 0)) return HCA_ERR_ARG;
       g_csa_union = (int)value;
+      return HCA_OK;
+    case HCA_INJECT_SHARED_PATH:
+      if (value > 2) return HCA_ERR_ARG;
+      g_shared_path = (int)value;
       return HCA_OK;
     default: return HCA_ERR_ARG;
   }

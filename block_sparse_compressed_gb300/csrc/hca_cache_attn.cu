@@ -658,6 +658,8 @@ int log2_int(int v) {
 
 size_t cache_attn_ws_bytes(int N, int R, int H, int D, int dtype) { return layout_of(N, R, H, D, dtype).bytes; }
 
+long long cache_attn_groups(int N, int R, int H, int D, int dtype) { return (long long)layout_of(N, R, H, D, dtype).gmax; }
+
 namespace {
 
 // Parameters of a call's kernels; sms: SMs of the device.

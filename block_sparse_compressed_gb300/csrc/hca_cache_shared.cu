@@ -33,6 +33,7 @@
 
 #include <algorithm>
 #include <cfloat>
+#include <cmath>
 #include <climits>
 
 #include "hca_cache_attn.cuh"
@@ -122,6 +123,13 @@ __device__ __forceinline__ void make_table(const SharedParams &p, Table &t, long
       ctas = max(prefix_sms(p.own, ok ? units : 0, own), 1);
     }
     int quota = max((int)(((ok ? units : 0) + ctas - 1) / ctas), 1);
+    if (ok) {
+      // a part more costs the join about a sixteenth of a unit
+      int longest = 0;
+      for (int g = lane; g < p.own.G; g += 32) longest = max(longest, t.g[g].tiles);
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      quota = max(quota, (int)sqrtf((float)longest * (1.f / 16.f)));
+    }
     bool pad = false;
     if (ok && nrt <= ctas) {  // else there are more row tiles than CTAs
       for (int k = 0; k < kPadded && !pad; ++k) {
@@ -898,17 +906,41 @@ size_t cache_attn_shared_ws_bytes(int N, int R, int H, int D, int G, int dtype) 
   return dtype == HCA_F32 ? cache_attn_ws_bytes(N, R, H, D, dtype) : layout_of(N, R, H, D, G).bytes;
 }
 
+namespace {
+
+// Is it worth attending the common entries apart?  Of the lengths the host knows
+// how many rows there are and how many key tiles the compressed tables hold at most.
+// In us, with `groups` of rows that share key tiles where nothing else is shared, of
+// 128 rows or fewer, on 152 SMs:
+//   by itself  21 + groups (tiles + 6) / 304 * 1.7 (2.0 for groups of 128 rows)
+//   apart      30 + row tiles * tiles / 152 * 1.5 + groups * 8 / 152 * 1.2
+// Measured (64 heads, D = 128, by themselves | apart): 64 tokens over 8 tiles 21 | 28,
+// 64 tiles 47 | 40, 512 tiles 203 | 108; 16 tokens over 256 tiles 45 | 45, 512 tiles 69 |
+// 56; 4 tokens over 512 tiles 37 | 56; 200 tokens over 16 tiles 45 | 47, 256 tiles 305 |
+// 167; 8 heads, 64 tokens over 32 tiles 32 | 31, 512 tiles 201 | 49; 314 prompt tokens
+// over 32 tiles 66 | 74, 256 tiles 293 | 234.
+bool apart_pays(const CacheAttnArgs &a, int sms) {
+  const double groups = (double)cache_attn_groups(a.N, a.R, a.H, a.D, a.dtype), tiles = std::min((double)a.comp.cols * a.bs / kTileKeys, 8388608.0);
+  const double rows = (double)a.N * a.H, full = rows >= 100.0 * groups ? 2.0 : 1.7;
+  const double alone = 21 + groups * (tiles + 6) / (2.0 * sms) * full;
+  const double apart = 30 + std::ceil(rows / kRowTile) * tiles / sms * 1.5 + groups * 8 / sms * 1.2;
+  return apart < alone;
+}
+
+}  // namespace
+
 cudaError_t cache_attn_shared(const CacheAttnArgs &args, cudaStream_t st) {
   CacheAttnArgs a = args;
-  if (a.dtype == HCA_F32) {
-    // its multiplications are what bounds fp32, and they are the same
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorNoDevice;
+  const int path = shared_path_setting();
+  // fp32 is bound by its multiplications, which are the same
+  if (a.dtype == HCA_F32 || path == 2 || (path == 0 && !apart_pays(a, sms))) {
     a.share.apart = 0;
     return cache_attn(a, st);
   }
   const Layout l = layout_of(a.N, a.R, a.H, a.D, a.share.G);
   char *ws = static_cast<char *>(a.ws);
-  const int sms = sm_count();
-  if (sms <= 0) return cudaErrorNoDevice;
   SharedParams p;
   p.table = reinterpret_cast<Table *>(ws + l.off_table);
   p.err = reinterpret_cast<int32_t *>(ws + l.off_err);

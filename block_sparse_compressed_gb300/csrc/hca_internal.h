@@ -72,6 +72,8 @@ uint64_t wait_limit_ns();
 // How the CSA union is built (HCA_INJECT_CSA_UNION): 0 automatic, 1 the
 // sorting kernel, c >= 64 the byte-mask kernel with chunks of c entries.
 int csa_union_setting();
+// How the attention of shared prefixes goes (HCA_INJECT_SHARED_PATH)
+int shared_path_setting();
 
 cudaError_t launch_prep(const int32_t *seg, int B, int S, int32_t *sstart, int32_t *status, cudaStream_t st);
 cudaError_t launch_visible_pairs(const int32_t *sstart, int B, int S, int W, int m, int64_t *raw, int64_t *comp,
@@ -196,6 +198,7 @@ struct CacheAttnArgs {
   CacheShare share;
 };
 size_t cache_attn_ws_bytes(int N, int R, int H, int D, int dtype);
+long long cache_attn_groups(int N, int R, int H, int D, int dtype);  // of rows that share key tiles, at most
 cudaError_t cache_attn(const CacheAttnArgs &a, cudaStream_t st);
 // with prefixes that requests share (hca_cache_shared.cu)
 int cache_shared_max_groups();

@@ -39,7 +39,7 @@ EXPORTS = ("hca_status_string", "hca_version", "hca_workspace_size", "hca_query_
            "hca_norm_rope_bwd", "hca_rope", "hca_cache_attn_shared_workspace_size", "hca_cache_attn_shared")
 
 # failure-path test hooks (hca_test_inject)
-INJECT_RESET, INJECT_LAUNCH_FAILURE, INJECT_STALL, INJECT_WAIT_LIMIT_NS, INJECT_CSA_UNION = 0, 1, 2, 3, 4
+INJECT_RESET, INJECT_LAUNCH_FAILURE, INJECT_STALL, INJECT_WAIT_LIMIT_NS, INJECT_CSA_UNION, INJECT_SHARED_PATH = 0, 1, 2, 3, 4, 5
 
 
 class HCAError(RuntimeError):
@@ -936,7 +936,7 @@ def _packed(t: torch.Tensor, name: str, shape, dtype, dev):
 
 
 def _packed_requests(start, held, pos, dev):
-    if start.dim() != 1 or start.shape[0] < 1:
+    if start is None or start.dim() != 1 or start.shape[0] < 1:
         raise ValueError("start must be [R+1]")
     R = start.shape[0] - 1
     if held is None and pos is None:

@@ -443,6 +443,8 @@ HCA_API int hca_cache_attn(const void *q, const int32_t *start, const int32_t *h
  * shared_cols that do not fit make all N rows of out and lse NaN, as lengths out of
  * range do (HCA_ERR_CACHE).  bf16: a prefix's part is rounded to fp32 and joined
  * with the request's own; fp32 has the same arithmetic as hca_cache_attn.
+ * A call whose requests are few, or whose compressed tables are narrow, does what
+ * hca_cache_attn does, which is then faster.
  * Workspace: hca_cache_attn_shared_workspace_size bytes (0: unsupported sizes). */
 HCA_API size_t hca_cache_attn_shared_workspace_size(int N, int R, int H, int D, int G, int dtype);
 HCA_API int hca_cache_attn_shared(const void *q, const int32_t *start, const int32_t *held, const void *raw_pool,
@@ -480,6 +482,11 @@ HCA_API int hca_cache_attn_shared(const void *q, const int32_t *start, const int
  *                             forces the byte-mask kernel with chunks of that
  *                             many entries (so small cases reach its
  *                             several-chunk path).  Both give the same union.
+ *   HCA_INJECT_SHARED_PATH    how later bf16 calls of hca_cache_attn_shared go:
+ *                             0 picks the cheaper way by the sizes (the
+ *                             default), 1 attends the common entries apart,
+ *                             2 with each request's own (so small cases reach
+ *                             the kernels of the first way).
  * The settings are process-wide.  Returns HCA_OK, or HCA_ERR_ARG for an
  * unknown `what`, a negative value or a value out of its range. */
 #define HCA_INJECT_RESET 0
@@ -487,6 +494,7 @@ HCA_API int hca_cache_attn_shared(const void *q, const int32_t *start, const int
 #define HCA_INJECT_STALL 2
 #define HCA_INJECT_WAIT_LIMIT_NS 3
 #define HCA_INJECT_CSA_UNION 4
+#define HCA_INJECT_SHARED_PATH 5
 #define HCA_STALL_FWD 1
 #define HCA_STALL_DQ 2
 #define HCA_STALL_DKV 4

@@ -13,6 +13,15 @@ BF16, F32 = torch.bfloat16, torch.float32
 E_CACHE = 12
 
 
+@pytest.fixture(autouse=True)
+def apart():
+    """The common entries are attended apart however few they are; the argument of the
+    function is another HCA_INJECT_SHARED_PATH."""
+    hca.hca_test_inject(hca.INJECT_SHARED_PATH, 1)
+    yield lambda v: hca.hca_test_inject(hca.INJECT_SHARED_PATH, v)
+    hca.hca_test_inject(hca.INJECT_RESET)
+
+
 def i32(v):
     return torch.tensor(v, dtype=torch.int32, device=DEV)
 
@@ -61,6 +70,31 @@ CASES = [  # prefixes, tokens behind them, new tokens, H, D, W, m, bs
 def test_matches_oracle(prefixes, behind, added, H, D, W, m, bs, dtype):
     case, first, cols = shared_case(prefixes, behind, added, H, D, W, m, bs, dtype, 3)
     check_attn(call(case, first, cols, W, m), *case, W, m, scale_of(D), dtype)
+
+
+@pytest.mark.parametrize("path", [0, 2])
+@pytest.mark.parametrize("prefixes,behind,added,H,D,W,m,bs", CASES[2:5])
+def test_other_ways(prefixes, behind, added, H, D, W, m, bs, path, apart):
+    apart(path)
+    case, first, cols = shared_case(prefixes, behind, added, H, D, W, m, bs, BF16, 3)
+    check_attn(call(case, first, cols, W, m), *case, W, m, scale_of(D), BF16)
+    out, lse = call(case, first, cols + 1000, W, m, check=False)
+    assert bool(out.isnan().all()) and bool(lse.isnan().all())
+
+
+def test_the_way_is_picked_by_the_sizes(apart):
+    """Both ways of the default, told apart by what the calls launch."""
+    apart(0)
+    hca.hca_profile_enable(True)
+    try:
+        case, first, cols = shared_case([(40, 512)], [0] * 40, [1] * 40, 8, 64, 16, 1, 16, BF16, 21)
+        check_attn(call(case, first, cols, 16, 1), *case, 16, 1, scale_of(64), BF16)
+        assert hca.hca_profile_read()["hca_cache_prefix"][0] == 1
+        case, first, cols = shared_case([(2, 3)], [0, 1], [1, 1], 8, 64, 16, 1, 16, BF16, 22)
+        check_attn(call(case, first, cols, 16, 1), *case, 16, 1, scale_of(64), BF16)
+        assert hca.hca_profile_read()["hca_cache_prefix"][0] == 1
+    finally:
+        hca.hca_profile_enable(False)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -268,15 +302,38 @@ def test_more_row_tiles_than_blocks(D):
     assert bool(bad[248:321].isnan().all()) and torch.equal(bad[:248], again[0][:248])
 
 
+def test_few_rows_over_a_long_prefix():
+    """A row tile in as many parts as the join takes."""
+    case, first, cols = shared_case([(2, 300)], [5, 40], [1, 1], 8, 64, 16, 1, 64, BF16, 23)
+    check_attn(call(case, first, cols, 16, 1), *case, 16, 1, scale_of(64), BF16)
+
+
+def test_both_ways_of_the_binding_give_the_same(monkeypatch):
+    case, first, cols = shared_case([(2, 3), (1, 2)], [4, 7, 9], [1, 2, 1], 8, 64, 16, 4, 16, BF16, 24)
+    a = call(case, first, cols, 16, 4)
+    if hca._py is None:
+        pytest.skip("built without the headers of Python or torch")
+    monkeypatch.setattr(hca, "_py", None)
+    b = call(case, first, cols, 16, 4)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    with pytest.raises(ValueError):
+        hca.hca_cache_attn_shared(case[0].to(DEV), case[1].to(DEV), case[2].to(DEV), dev(case[3]), None, first, cols, 16, 4, 0.1)
+    with pytest.raises(ValueError):
+        call(case, first[:-1], cols, 16, 4)
+    with pytest.raises(TypeError):
+        call(case, first, cols.long(), 16, 4)
+
+
 def test_a_stalled_wait_times_out():
     case, first, cols = shared_case([(3, 12)], [0, 1, 2], [1, 2, 1], 16, 128, 16, 1, 16, BF16, 19)
     ws = torch.empty(hca.load().hca_cache_attn_shared_workspace_size(4, 3, 16, 128, 1, 0), dtype=torch.uint8, device=DEV)
     try:
-        hca.hca_test_inject(3, 2_000_000)
-        hca.hca_test_inject(2, 1)
+        hca.hca_test_inject(hca.INJECT_WAIT_LIMIT_NS, 2_000_000)
+        hca.hca_test_inject(hca.INJECT_STALL, 1)
         out, lse = call(case, first, cols, 16, 1, check=False, ws=ws)
         assert hca.hca_workspace_status(ws) == 10
         assert bool(out.isnan().all()) and bool(lse.isnan().all())
     finally:
-        hca.hca_test_inject(0)
+        hca.hca_test_inject(hca.INJECT_RESET)
+        hca.hca_test_inject(hca.INJECT_SHARED_PATH, 1)
     check_attn(call(case, first, cols, 16, 1, ws=ws), *case, 16, 1, scale_of(128), BF16)

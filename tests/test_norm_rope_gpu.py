@@ -310,3 +310,77 @@ def test_long_sequence_many_tiles():
     # roundings, each 2^-24 of a partial sum that stays below some sqrt(n) * 10
     for name, got, ref, n in (("dwq", back[2], sq, 540060), ("dwkv", back[3], skv, 27003)):
         assert float((got.double() - ref).abs().max()) <= n ** 0.5 * 10 * 2000 * 2.0 ** -24, name
+
+
+def test_both_ways_of_the_binding_give_the_same(monkeypatch):
+    if hca.load() and hca._py is None:
+        pytest.skip("built without the headers of Python or torch")
+    q, kv, wq, wkv, pos, freq, dq, dkv = make(2, 3, 21, 128, 64, BF16, 15, axes=2)
+    sq, skv, start, held, sfreq, _, w = serve_case([4, 9], [3, 8], 5, 64, 32, F32, 16, 2)
+    wide = torch.zeros(15, 6, 64, device="cuda")
+    wide[:, 1:] = sq
+    spos = torch.arange(15, dtype=torch.int32).cuda() * 7
+
+    def calls():
+        r = [*hca.hca_norm_rope_fwd(q, kv, wq, None, pos, freq, EPS, halves=True), *hca.hca_norm_rope_bwd(q, kv, wq, None, pos, freq, EPS, dq, dkv),
+             hca.hca_rope(q, pos, freq, inverse=True, first=0), hca.hca_rope(q, pos, freq, y=torch.empty_like(q)),
+             hca.hca_norm_rope_bwd(q[:, :1].expand(2, 3, 21, 128), None, None, None, pos, freq, EPS, dq, None)[0]]
+        out = torch.zeros_like(sq), torch.zeros_like(skv), torch.zeros_like(sq)
+        hca.hca_cache_norm_rope(wide[:, 1:], skv, start, held, w, w, sfreq, EPS, qo=out[0], kvo=out[1])
+        hca.hca_cache_rope(wide[:, 1:], start, None, sfreq[0], pos=spos, y=out[2])
+        return r + list(out)
+
+    a = calls()
+    monkeypatch.setattr(hca, "_py", None)
+    for x, y in zip(a, calls()):
+        assert (x is None and y is None) or (torch.equal(x, y) and x.stride() == y.stride())
+
+
+def test_the_binding_refuses():
+    q, kv, wq, wkv, pos, freq, dq, dkv = make(2, 3, 21, 128, 64, BF16, 17)
+    f = hca.hca_norm_rope_fwd
+    for bad, error in (((q, kv[:, :20], wq, wkv, pos, freq), ValueError), ((q, kv.float(), wq, wkv, pos, freq), TypeError),
+                       ((q, kv, wq.bfloat16(), wkv, pos, freq), TypeError), ((q, kv, wq[:64], wkv, pos, freq), ValueError),
+                       ((q, kv, wq, wkv, pos.long(), freq), TypeError), ((q, kv, wq, wkv, pos[:, :, :9], freq), ValueError),
+                       ((q, kv, wq, wkv, pos, freq.double()), TypeError), ((q, kv, wq, wkv, None, freq.expand(2, 32).contiguous()), ValueError),
+                       ((q, kv, wq, wkv, pos, freq.cpu()), ValueError), ((q.half(), kv.half(), wq, wkv, pos, freq), TypeError),
+                       ((q, kv, wq, wkv, pos, None), ValueError), ((q[..., ::2], kv, wq, wkv, pos, freq), ValueError)):
+        with pytest.raises(error):
+            f(*bad, EPS)
+    with pytest.raises(hca.HCAError):
+        f(q, kv, wq, wkv, pos, freq, -1.0)
+    with pytest.raises(hca.HCAError):
+        f(q, kv, wq, wkv, pos, freq, EPS, first=72)
+    with pytest.raises(ValueError):
+        hca.hca_norm_rope_bwd(q, kv, wq, None, pos, freq, EPS, dq, dkv, dwkv=torch.empty(128, device="cuda"))
+    with pytest.raises(ValueError):
+        hca.hca_norm_rope_bwd(q, kv, wq, wkv, pos, freq, EPS, dq[:, :2], dkv)
+    with pytest.raises(hca.HCAError) as e:
+        hca.hca_norm_rope_bwd(q, kv, wq, wkv, pos, freq, EPS, dq, dkv, ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 7
+    with pytest.raises(ValueError):
+        hca.hca_cache_rope(q[0].transpose(0, 1), None, None, freq)
+    with pytest.raises(ValueError):
+        hca.hca_cache_norm_rope(q[0].transpose(0, 1), None, torch.zeros(2, dtype=torch.int32, device="cuda"), None, None, None, freq, EPS)
+
+
+def test_threads_that_call_at_once():
+    import threading
+    q, kv, wq, wkv, pos, freq, dq, dkv = make(1, 4, 300, 64, 32, BF16, 18)
+    want = hca.hca_norm_rope_bwd(q, kv, wq, wkv, pos, freq, EPS, dq, dkv)
+    bad = []
+
+    def work():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got = hca.hca_norm_rope_bwd(q, kv, wq, wkv, pos, freq, EPS, dq, dkv)
+                torch.cuda.current_stream().synchronize()
+                bad.extend(1 for a, b in zip(got, want) if not torch.equal(a, b))
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
