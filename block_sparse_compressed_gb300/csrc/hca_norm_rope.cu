@@ -13,11 +13,11 @@
 //
 // Angles.  A position of 10^6 times a frequency of 1 is 10^6 radians, of which
 // fp32 keeps a sixteenth.  So a frequency becomes a 64-bit fraction of a turn
-// per unit, F = f / 2pi * 2^64 mod 2^64 (in two doubles, exact to 2^-64 turns),
+// per unit, F = f / 2pi * 2^64 mod 2^64 (exact to 2^-64 turns),
 // and a phase is sum_a c_a F[a] in integers, where the wrap-around of 64 bits is
 // the reduction to one turn: off by 2^-33 turns at most for any 32-bit
-// coordinates.  The two upper bits (rounded) are the quadrant, the rest, an eighth
-// of a turn at most, goes through sincospif.
+// coordinates.  The two upper bits (rounded) are the quadrant, the rest is an eighth
+// of a turn at most.
 //
 // A row belongs to L neighbouring lanes, 8 consecutive columns (one or two 16-byte
 // accesses) a lane and chunk, so a row is read once, stays in registers between
@@ -109,22 +109,41 @@ __device__ __forceinline__ float total(uint64_t v) {
   return a + b;
 }
 
-// f / 2pi of a turn per unit as a 64-bit fraction
+// f / 2pi of a turn per unit as a 64-bit fraction: f = m 2^e times 2^128 / 2pi,
+// whose bits from 64 - e on are the ones wanted.  (In doubles, which this GPU is slow
+// at, a block's table took 1 us.)
 __device__ __forceinline__ unsigned long long turns(float f) {
-  // 1 / 2pi in two doubles
-  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
-  const double p = (double)f * kHi;
-  const double e = fma((double)f, kHi, -p) + (double)f * kLo;
-  const double q = p - rint(p);  // exact
-  // the sum is taken mod 2^64, so half a turn is the same upwards and downwards
-  return (unsigned long long)__double2ll_rn(q * 18446744073709551616.0) + (unsigned long long)__double2ll_rn(e * 18446744073709551616.0);
+  constexpr uint32_t kInv2Pi[4] = {0x7d4d3770u, 0x7f09d5f4u, 0x9391054au, 0x28be60dbu};
+  const uint32_t u = __float_as_uint(f), ex = (u >> 23) & 255;
+  const uint32_t m = (u & 0x7fffffu) | (ex ? 0x800000u : 0u);
+  uint32_t w[7] = {0, 0, 0, 0, 0, 0, 0};
+  unsigned long long carry = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    carry += (unsigned long long)m * kInv2Pi[i];
+    w[i] = (uint32_t)carry;
+    carry >>= 32;
+  }
+  w[4] = (uint32_t)carry;
+  const int shift = 64 - (max((int)ex, 1) - 150);  // 55 and more for f below 2^32
+  uint32_t lo = 0, mid = 0, hi = 0;                // the three words that the 64 bits lie in
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    if (shift >> 5 == i) lo = w[i], mid = w[i + 1], hi = w[i + 2];
+  }
+  const unsigned long long t = (unsigned long long)__funnelshift_r(mid, hi, shift & 31) << 32 | __funnelshift_r(lo, mid, shift & 31);
+  return u >> 31 ? 0ull - t : t;
 }
 
+// The rest of a phase, an eighth of a turn at most, in radians: the Taylor series of
+// cos and sin there are within 2^-25 with the terms up to x^8 and x^9.
 __device__ __forceinline__ float2 cos_sin(unsigned long long phase, float sign) {
   const uint32_t quadrant = (uint32_t)((phase + (1ull << 61)) >> 62);
   const long long rest = (long long)(phase - ((unsigned long long)quadrant << 62));  // within 2^61
-  float s, c;
-  sincospif((float)(int)(rest >> 30) * 1.1641532182693481e-10f /* 2^-33 */, &s, &c);
+  const float x = (float)(int)(rest >> 30) * 3.6572952e-10f;                          // 2 pi 2^-34
+  const float z = x * x;
+  float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 40320.f, -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+  float s = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
   if (quadrant & 1) {
     const float t = c;
     c = -s;
@@ -178,7 +197,8 @@ __device__ __forceinline__ void cp_async_wait() {
 template <typename T, int L, int CH, int MODE, bool HALVES>
 __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MODE == kBwd ? 3 : 4) hca_norm_rope_kernel(const Args a) {
   using R = Ring<T, CH, MODE>;
-  constexpr int kRows = kThreads / L;  // rows of a pass
+  constexpr int kRows = kThreads / L, kRowsLog = L == 8 ? 5 : L == 16 ? 4 : 3;  // rows of a pass
+  static_assert(kRows == 1 << kRowsLog, "a power of two");
   constexpr int kVec = (int)(sizeof(T) / 2);  // pieces of 8 columns
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, l = tid % L, group = tid / L;
@@ -189,10 +209,17 @@ __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MO
       reinterpret_cast<unsigned long long *>(smem + R::kBytes + (MODE == kBwd ? 2 * CH * 2 * kThreads * 16 : 0));  // [axes][np]
   float2 *sh_cs = reinterpret_cast<float2 *>(sh_freq + a.axes * np);            // [tile][np]
   long long *sh_pos = reinterpret_cast<long long *>(sh_cs + a.tile * np);       // [tile] positions from start and held
-  int *sh_req = reinterpret_cast<int *>(sh_pos + a.tile);                       // [2][R + 1] starts and held
-  const int token = group & (a.tile - 1), head0 = group >> a.log_tile, head_step = kRows >> a.log_tile;
+  float *sh_w = reinterpret_cast<float *>(sh_pos + a.tile);                     // [2][D] weights
+  int *sh_req = reinterpret_cast<int *>(sh_w + (MODE == kRope ? 0 : 2 * a.D));  // [2][R + 1] starts and held
+  const int token = group & (a.tile - 1), head0 = group >> a.log_tile, head_step = kRows >> a.log_tile, step_log = kRowsLog - a.log_tile;
 
   for (int i = tid; i < a.axes * np; i += kThreads) sh_freq[i] = turns(a.freq[i]);
+  if constexpr (MODE != kRope) {
+    for (int i = tid; i < a.D; i += kThreads) {
+      sh_w[i] = a.t[0].w ? a.t[0].w[i] : 1.f;
+      sh_w[a.D + i] = a.t[1].w ? a.t[1].w[i] : 1.f;
+    }
+  }
   int live = a.S;
   const bool listed = a.start && a.R <= kRequestsInSmem;
   if (a.start) {
@@ -234,37 +261,55 @@ __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MO
     // heads of the block's range: of queries, then of kv
     const int lo0 = split * a.per, hi0 = min(lo0 + a.per, a.t[0].H);
     const int lo1 = max(lo0 - a.t[0].H, 0), hi1 = min(lo0 + a.per - a.t[0].H, a.t[1].H);
-    const int n0 = max((hi0 - lo0 + head_step - 1) / head_step, 0);
-    const int steps = n0 + (MODE == kRope ? 0 : max((hi1 - lo1 + head_step - 1) / head_step, 0));
+    const uint32_t n0 = max((hi0 - lo0 + head_step - 1) >> step_log, 0);
+    const uint32_t steps = n0 + (MODE == kRope ? 0 : max((hi1 - lo1 + head_step - 1) >> step_log, 0));
+    // rows that the thread has of each: heads lo + head0, + head_step, ...
+    const uint32_t own0 = alive ? max((hi0 - lo0 - head0 + head_step - 1) >> step_log, 0) : 0;
+    const uint32_t own1 = alive && MODE != kRope ? max((hi1 - lo1 - head0 + head_step - 1) >> step_log, 0) : 0;
 
-    // row `n` of the thread's: its pieces on their way to slot n % kStages
-    auto issue = [&](int n) {
-      if (n < steps) {
-        const bool kv = MODE != kRope && n >= n0;
-        const NormRopeTensor &t = a.t[kv];
-        const int h = (kv ? lo1 + (n - n0) * head_step : lo0 + n * head_step) + head0;
-        const bool row = alive && h < (kv ? hi1 : hi0);
-        const T *x = static_cast<const T *>(t.x), *g = static_cast<const T *>(t.g);
-        if (row) {
-          x += b * t.xb + s * t.xs + h * t.xh + 8 * l;
-          if constexpr (MODE == kBwd) g += b * t.gb + s * t.gs + h * t.gh + 8 * l;
+    // The thread's rows in order, their pieces on their way to slot n % kStages.
+    const T *next_x = static_cast<const T *>(a.t[0].x), *next_g = static_cast<const T *>(a.t[0].g);
+    if (own0 > 0) {
+      next_x += b * a.t[0].xb + s * a.t[0].xs + (lo0 + head0) * a.t[0].xh + 8 * l;
+      if constexpr (MODE == kBwd) next_g += b * a.t[0].gb + s * a.t[0].gs + (lo0 + head0) * a.t[0].gh + 8 * l;
+    }
+    int64_t step_x = head_step * a.t[0].xh, step_g = MODE == kBwd ? head_step * a.t[0].gh : 0;
+    uint32_t at = 0, left = own0;  // of the next row; rows of this tensor that are left
+    auto issue = [&] {
+      if (MODE != kRope && at == n0) {  // on to kv
+        left = own1;
+        next_x = static_cast<const T *>(a.t[1].x);
+        next_g = static_cast<const T *>(a.t[1].g);
+        if (own1 > 0) {
+          next_x += b * a.t[1].xb + s * a.t[1].xs + (lo1 + head0) * a.t[1].xh + 8 * l;
+          if constexpr (MODE == kBwd) next_g += b * a.t[1].gb + s * a.t[1].gs + (lo1 + head0) * a.t[1].gh + 8 * l;
         }
-        const uint32_t to = ring + (n % R::kStages) * (R::kPieces * kThreads * 16);
+        step_x = head_step * a.t[1].xh;
+        if constexpr (MODE == kBwd) step_g = head_step * a.t[1].gh;
+      }
+      if (at < steps) {
+        const uint32_t to = ring + (at % R::kStages) * (R::kPieces * kThreads * 16);
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-          const bool there = row && mine[k];
+          const bool there = left > 0 && mine[k];
 #pragma unroll
           for (int v = 0; v < kVec; ++v) {
-            const int at = there ? 8 * k * L + v * (16 / (int)sizeof(T)) : 0;
-            cp_async_16(to + (k * kVec + v) * (kThreads * 16), x + at, there ? 16 : 0);
-            if constexpr (MODE == kBwd) cp_async_16(to + ((CH + k) * kVec + v) * (kThreads * 16), g + at, there ? 16 : 0);
+            const int col = CH == 1 ? v * (16 / (int)sizeof(T)) : there ? 8 * k * L + v * (16 / (int)sizeof(T)) : 0;
+            cp_async_16(to + (k * kVec + v) * (kThreads * 16), next_x + col, there ? 16 : 0);
+            if constexpr (MODE == kBwd) cp_async_16(to + ((CH + k) * kVec + v) * (kThreads * 16), next_g + col, there ? 16 : 0);
           }
         }
+        if (left > 1) {
+          next_x += step_x;
+          if constexpr (MODE == kBwd) next_g += step_g;
+        }
+        left -= left > 0;
       }
+      ++at;
       cp_async_commit();
     };
 #pragma unroll 1
-    for (int n = 0; n < R::kStages; ++n) issue(n);
+    for (int n = 0; n < R::kStages; ++n) issue();
 
     __syncthreads();  // sh_cs may still be read; sh_freq and sh_req are written
     if (a.start && !a.pos) {
@@ -289,13 +334,15 @@ __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MO
     }
     __syncthreads();
 
-    int n = 0;
+    uint32_t n = 0;
 #pragma unroll
     for (int which = 0; which < (MODE == kRope ? 1 : 2); ++which) {
       const NormRopeTensor &t = a.t[which];
-      const int end = which ? steps : n0;
+      const uint32_t end = which ? steps : n0;
       if (n >= end) continue;
-      T *y = static_cast<T *>(t.y) + b * t.yb + s * t.ys + 8 * l;
+      T *y = static_cast<T *>(t.y) + b * t.yb + s * t.ys + ((which ? lo1 : lo0) + head0) * t.yh + 8 * l;
+      const int64_t step_y = head_step * t.yh;
+      uint32_t rows = which ? own1 : own0;  // that are left
       // What a column and its partner count in a rotated column (backwards: turned
       // back).  Forwards the weights are in them.
       uint64_t own[CH][4], other[CH][4], w[CH][4], dw[CH][4];
@@ -312,11 +359,12 @@ __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MO
             o[e] = cs.x;
             p[e] = (second == (MODE != kBwd)) ? cs.y : -cs.y;
             wt[e] = 1.f;
-            if (MODE != kRope && t.w && mine[k]) {
-              wt[e] = t.w[z];
+            if (MODE != kRope && mine[k]) {
+              const float *weight = sh_w + which * a.D;
+              wt[e] = weight[z];
               if (MODE == kFwd) {
                 o[e] *= wt[e];
-                p[e] *= turned[k] ? t.w[HALVES ? 8 * partner[k] + c : z ^ 1] : 0.f;
+                p[e] *= weight[HALVES ? 8 * partner[k] + c : z ^ 1];
               }
             }
           }
@@ -350,7 +398,6 @@ __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MO
           for (int i = 0; i < 4; ++i) o[k][i] = tc::ffma2(f[k][i], own[k][i], tc::fmul2(HALVES ? q[i] : f[k][i ^ 2], other[k][i]));
         }
       };
-      const int lo = which ? lo1 : lo0, hi = which ? hi1 : hi0, first = which ? n0 : 0;
 #pragma unroll 1
       for (; n < end; ++n) {
         cp_async_wait<R::kStages - 1>();
@@ -364,8 +411,7 @@ __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MO
             if constexpr (MODE == kBwd) vg[k].piece(v, *reinterpret_cast<const uint4 *>(smem + from + ((CH + k) * kVec + v) * (kThreads * 16)));
           }
         }
-        const int h = lo + (n - first) * head_step + head0;
-        const bool row = alive && h < hi;
+        const bool row = rows > 0;
         uint64_t f[CH][4], o[CH][4];
 #pragma unroll
         for (int k = 0; k < CH; ++k) vx[k].template get<HALVES>(f[k]);
@@ -423,10 +469,12 @@ __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MO
             Vec<T> out;
             out.template put<HALVES>(o[k]);
             if (MODE == kRope && !turned[k]) out = vx[k];  // as it was, infinities too
-            out.store(y + h * t.yh + 8 * k * L);
+            out.store(y + 8 * k * L);
           }
         }
-        issue(n + R::kStages);
+        y += step_y;
+        rows -= row;
+        issue();
       }
       if constexpr (MODE == kBwd) {
 #pragma unroll
@@ -499,11 +547,11 @@ cudaError_t launch(Args &a, cudaStream_t st) {
   a.splits = (heads + a.per - 1) / a.per;
   using R = Ring<T, CH, MODE>;
   constexpr int kFixed = R::kBytes + (MODE == kBwd ? 2 * CH * 2 * kThreads * 16 : 0);
-  size_t smem = kFixed + 8 * ((size_t)(a.axes + a.tile) * (a.rot / 2) + a.tile);
+  size_t smem = kFixed + 8 * ((size_t)(a.axes + a.tile) * (a.rot / 2) + a.tile) + (MODE == kRope ? 0 : 8 * (size_t)a.D);
   if (a.start && a.R <= kRequestsInSmem) smem += 2 * sizeof(int) * ((size_t)a.R + 1);
   auto *kernel = hca_norm_rope_kernel<T, L, CH, MODE, HALVES>;
   static tc::SmemAttrOnce attr;
-  cudaError_t e = attr.ensure(reinterpret_cast<const void *>(kernel), kFixed + 34 * 1024);  // the most that the rest takes
+  cudaError_t e = attr.ensure(reinterpret_cast<const void *>(kernel), kFixed + 38 * 1024);  // the most that the rest takes
   if (e != cudaSuccess) return e;
   long long grid = a.tiles * a.splits;
   grid = std::min<long long>(grid, MODE == kBwd ? std::min(kNormRopeParts, (CH > 1 ? 1 : 3) * sms) : 1 << 30);
