@@ -442,7 +442,7 @@ constexpr int kMaxRowD = 512, kMaxRopeAxes = 4;
 static int norm_rope_shape(const NormRopeArgs &a, int H) {
   if (a.dtype != HCA_BF16 && a.dtype != HCA_F32) return HCA_ERR_DTYPE;
   if (a.B < 0 || a.S < 0 || H < 0 || H > (1 << 20) || a.D < 1 || a.D > kMaxRowD || a.S > (1 << 30) || a.R < 0 || a.R > (1 << 24) ||
-      (double)a.B * a.S * (H + 1.0) > 4.0e15)
+      (double)a.B * a.S >= 2147483648.0)
     return HCA_ERR_SHAPE;
   if (a.D % 8 != 0) return HCA_ERR_ALIGN;
   if (a.axes < 1 || a.axes > kMaxRopeAxes || a.rot < 0 || a.first < 0 || a.rot > a.D || a.first > a.D - a.rot) return HCA_ERR_ARG;

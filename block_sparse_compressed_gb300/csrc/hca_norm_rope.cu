@@ -47,7 +47,9 @@ struct Args {
   float *part;          // [grid][2][D] sums of dw (backward)
   int B, S, D, R, axes, first, rot;
   float sign, eps;
-  long long tiles;      // token tiles of all batch rows
+  uint32_t tiles;       // token tiles of all batch rows
+  uint32_t per_row;     // of a batch row
+  uint32_t inv_np;      // 2^32 / (rot / 2), rounded up
   int tile, log_tile;   // tokens of a tile, a power of two
   int splits, per;      // head ranges of a tile, heads (of q, then kv) of a range
 };
@@ -175,6 +177,8 @@ __device__ __forceinline__ int request_of(const int32_t *start, int R, int t) {
   return lo;
 }
 
+constexpr int blocks_per_sm(int ch, int mode) { return ch > 1 ? (mode == kBwd ? 1 : 2) : mode == kBwd ? 3 : 4; }
+
 // A thread's rows come through shared memory, its own 16-byte pieces in kStages
 // slots that only it writes (asynchronously) and reads, so nothing waits but the
 // thread itself.
@@ -195,7 +199,7 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 template <typename T, int L, int CH, int MODE, bool HALVES>
-__global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MODE == kBwd ? 3 : 4) hca_norm_rope_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(CH, MODE)) hca_norm_rope_kernel(const Args a) {
   using R = Ring<T, CH, MODE>;
   constexpr int kRows = kThreads / L, kRowsLog = L == 8 ? 5 : L == 16 ? 4 : 3;  // rows of a pass
   static_assert(kRows == 1 << kRowsLog, "a power of two");
@@ -208,29 +212,50 @@ __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MO
   unsigned long long *sh_freq =
       reinterpret_cast<unsigned long long *>(smem + R::kBytes + (MODE == kBwd ? 2 * CH * 2 * kThreads * 16 : 0));  // [axes][np]
   float2 *sh_cs = reinterpret_cast<float2 *>(sh_freq + a.axes * np);            // [tile][np]
-  long long *sh_pos = reinterpret_cast<long long *>(sh_cs + a.tile * np);       // [tile] positions from start and held
-  float *sh_w = reinterpret_cast<float *>(sh_pos + a.tile);                     // [2][D] weights
+  long long *sh_pos = reinterpret_cast<long long *>(sh_cs + a.tile * np);       // [axes][tile] coordinates
+  float *sh_w = reinterpret_cast<float *>(sh_pos + a.axes * a.tile);            // [2][D] weights
   int *sh_req = reinterpret_cast<int *>(sh_w + (MODE == kRope ? 0 : 2 * a.D));  // [2][R + 1] starts and held
   const int token = group & (a.tile - 1), head0 = group >> a.log_tile, head_step = kRows >> a.log_tile, step_log = kRowsLog - a.log_tile;
 
-  for (int i = tid; i < a.axes * np; i += kThreads) sh_freq[i] = turns(a.freq[i]);
-  if constexpr (MODE != kRope) {
-    for (int i = tid; i < a.D; i += kThreads) {
-      sh_w[i] = a.t[0].w ? a.t[0].w[i] : 1.f;
-      sh_w[a.D + i] = a.t[1].w ? a.t[1].w[i] : 1.f;
-    }
-  }
-  int live = a.S;
+  if constexpr (MODE == kBwd) tc::pdl_launch_dependents();  // the sums of dw wait for this kernel's end by themselves
+  // What all items need, in registers first: the loads' latency passes while the
+  // first rows' copies are issued.
   const bool listed = a.start && a.R <= kRequestsInSmem;
+  const float freq = tid < a.axes * np ? a.freq[tid] : 0.f;
+  float weight[2] = {1.f, 1.f};
+  if constexpr (MODE != kRope) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (a.t[i].w && tid < a.D) weight[i] = a.t[i].w[tid];
+  }
+  int request[2] = {0, 0}, live = a.S;
   if (a.start) {
+    if (listed && tid <= a.R) request[0] = a.start[tid];
+    if (listed && tid < a.R && a.held) request[1] = a.held[tid];
+    live = a.start[a.R];  // rows behind the last request's are left
+  }
+  auto keep = [&] {
+    if (tid < a.axes * np) sh_freq[tid] = turns(freq);
+    for (int i = tid + kThreads; i < a.axes * np; i += kThreads) sh_freq[i] = turns(a.freq[i]);
+    if constexpr (MODE != kRope) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (tid < a.D) sh_w[i * a.D + tid] = weight[i];
+        for (int d = tid + kThreads; d < a.D; d += kThreads) sh_w[i * a.D + d] = a.t[i].w ? a.t[i].w[d] : 1.f;
+      }
+    }
     if (listed) {
-      for (int i = tid; i <= a.R; i += kThreads) {
+      if (tid <= a.R) {
+        sh_req[tid] = request[0];
+        sh_req[a.R + 1 + tid] = request[1];
+      }
+      for (int i = tid + kThreads; i <= a.R; i += kThreads) {
         sh_req[i] = a.start[i];
         sh_req[a.R + 1 + i] = a.held && i < a.R ? a.held[i] : 0;
       }
     }
-    live = min(a.S, a.start[a.R]);  // rows behind the last request's are left
-  }
+    live = min(a.S, live);
+  };
 
   // columns of the lane
   bool mine[CH], turned[CH], upper[CH];
@@ -250,22 +275,25 @@ __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MO
   }
   const float inv_d = 1.f / (float)a.D;
 
-  for (long long item = blockIdx.x; item < a.tiles * a.splits; item += gridDim.x) {
-    const int split = (int)(item % a.splits);
-    const long long tile = item / a.splits;
-    const int per_row = (a.S + a.tile - 1) >> a.log_tile;
-    const int b = (int)(tile / per_row), s0 = (int)(tile % per_row) << a.log_tile;
-    if (s0 >= live) continue;
+  const uint32_t items = a.tiles * a.splits;  // below 2^31
+  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const uint32_t tile = item / (uint32_t)a.splits, row = tile / a.per_row;
+    const int split = (int)(item - tile * a.splits), b = (int)row, s0 = (int)(tile - row * a.per_row) << a.log_tile;
     const int s = s0 + token;
-    const bool alive = s < live;
+    const bool there = s < a.S;  // rows behind the last request's are read like others
+    long long coordinate = 0;
+    if (tid < a.axes * a.tile) {
+      const int x = tid >> a.log_tile, at = s0 + (tid & (a.tile - 1));
+      if (at < a.S) coordinate = a.pos ? a.pos[((size_t)x * a.B + b) * a.S + at] : at;
+    }
     // heads of the block's range: of queries, then of kv
     const int lo0 = split * a.per, hi0 = min(lo0 + a.per, a.t[0].H);
     const int lo1 = max(lo0 - a.t[0].H, 0), hi1 = min(lo0 + a.per - a.t[0].H, a.t[1].H);
     const uint32_t n0 = max((hi0 - lo0 + head_step - 1) >> step_log, 0);
     const uint32_t steps = n0 + (MODE == kRope ? 0 : max((hi1 - lo1 + head_step - 1) >> step_log, 0));
     // rows that the thread has of each: heads lo + head0, + head_step, ...
-    const uint32_t own0 = alive ? max((hi0 - lo0 - head0 + head_step - 1) >> step_log, 0) : 0;
-    const uint32_t own1 = alive && MODE != kRope ? max((hi1 - lo1 - head0 + head_step - 1) >> step_log, 0) : 0;
+    const uint32_t own0 = there ? max((hi0 - lo0 - head0 + head_step - 1) >> step_log, 0) : 0;
+    const uint32_t own1 = there && MODE != kRope ? max((hi1 - lo1 - head0 + head_step - 1) >> step_log, 0) : 0;
 
     // The thread's rows in order, their pieces on their way to slot n % kStages.
     const T *next_x = static_cast<const T *>(a.t[0].x), *next_g = static_cast<const T *>(a.t[0].g);
@@ -291,12 +319,12 @@ __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MO
         const uint32_t to = ring + (at % R::kStages) * (R::kPieces * kThreads * 16);
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-          const bool there = left > 0 && mine[k];
+          const bool row = left > 0 && mine[k];
 #pragma unroll
           for (int v = 0; v < kVec; ++v) {
-            const int col = CH == 1 ? v * (16 / (int)sizeof(T)) : there ? 8 * k * L + v * (16 / (int)sizeof(T)) : 0;
-            cp_async_16(to + (k * kVec + v) * (kThreads * 16), next_x + col, there ? 16 : 0);
-            if constexpr (MODE == kBwd) cp_async_16(to + ((CH + k) * kVec + v) * (kThreads * 16), next_g + col, there ? 16 : 0);
+            const int col = CH == 1 ? v * (16 / (int)sizeof(T)) : row ? 8 * k * L + v * (16 / (int)sizeof(T)) : 0;
+            cp_async_16(to + (k * kVec + v) * (kThreads * 16), next_x + col, row ? 16 : 0);
+            if constexpr (MODE == kBwd) cp_async_16(to + ((CH + k) * kVec + v) * (kThreads * 16), next_g + col, row ? 16 : 0);
           }
         }
         if (left > 1) {
@@ -311,7 +339,14 @@ __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MO
 #pragma unroll 1
     for (int n = 0; n < R::kStages; ++n) issue();
 
-    __syncthreads();  // sh_cs may still be read; sh_freq and sh_req are written
+    if (item == blockIdx.x) keep();
+    if (s0 >= live) {
+      cp_async_wait<0>();
+      continue;
+    }
+    const bool alive = s < live;
+    if (tid < a.axes * a.tile) sh_pos[tid] = coordinate;
+    __syncthreads();  // and sh_cs is read no more
     if (a.start && !a.pos) {
       if (tid < a.tile) {
         const int t = s0 + tid, r = request_of(listed ? sh_req : a.start, a.R, t);
@@ -320,16 +355,9 @@ __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MO
       __syncthreads();
     }
     for (int i = tid; i < a.tile * np; i += kThreads) {
-      const int t = i / np, p = i - t * np, at = s0 + t;
-      unsigned long long phase = 0;
-      if (at < live) {
-        if (a.pos) {
-          for (int x = 0; x < a.axes; ++x)
-            phase += (unsigned long long)(long long)a.pos[((size_t)x * a.B + b) * a.S + at] * sh_freq[x * np + p];
-        } else {
-          phase = (unsigned long long)(a.start ? sh_pos[t] : at) * sh_freq[p];
-        }
-      }
+      const int t = (int)__umulhi(i, a.inv_np), p = i - t * np;
+      unsigned long long phase = (unsigned long long)sh_pos[t] * sh_freq[p];
+      for (int x = 1; x < a.axes; ++x) phase += (unsigned long long)sh_pos[x * a.tile + t] * sh_freq[x * np + p];
       sh_cs[i] = cos_sin(phase, a.sign);
     }
     __syncthreads();
@@ -411,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MO
             if constexpr (MODE == kBwd) vg[k].piece(v, *reinterpret_cast<const uint4 *>(smem + from + ((CH + k) * kVec + v) * (kThreads * 16)));
           }
         }
-        const bool row = rows > 0;
+        const bool row = alive && rows > 0;
         uint64_t f[CH][4], o[CH][4];
 #pragma unroll
         for (int k = 0; k < CH; ++k) vx[k].template get<HALVES>(f[k]);
@@ -473,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MO
           }
         }
         y += step_y;
-        rows -= row;
+        rows -= rows > 0;
         issue();
       }
       if constexpr (MODE == kBwd) {
@@ -511,10 +539,11 @@ __global__ void __launch_bounds__(kThreads, CH > 1 ? (MODE == kBwd ? 1 : 2) : MO
   }
 }
 
-// dw from the blocks' sums, in a fixed order: 8 warps take every 8th block each,
+// dw from the blocks' sums, in a fixed order: 32 warps take every 32nd block each,
 // a lane a column.
-__global__ void __launch_bounds__(kThreads) hca_norm_rope_dw_kernel(const float *part, int n, int D, float *dwq, float *dwkv) {
-  __shared__ double sum[8][32];
+constexpr int kDwThreads = 1024;
+__global__ void __launch_bounds__(kDwThreads) hca_norm_rope_dw_kernel(const float *part, int n, int D, float *dwq, float *dwkv) {
+  __shared__ double sum[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.y, d = blockIdx.x * 32 + lane;
   float *dw = which ? dwkv : dwq;
   tc::pdl_wait();
@@ -522,45 +551,57 @@ __global__ void __launch_bounds__(kThreads) hca_norm_rope_dw_kernel(const float 
   double v = 0;
   if (d < D) {
 #pragma unroll 8
-    for (int i = warp; i < n; i += 8) v += part[((size_t)i * 2 + which) * D + d];
+    for (int i = warp; i < n; i += 32) v += part[((size_t)i * 2 + which) * D + d];
   }
   sum[warp][lane] = v;
   __syncthreads();
-  if (warp == 0 && d < D) {
-    for (int i = 1; i < 8; ++i) v += sum[i][lane];
-    dw[d] = (float)v;
-  }
+  // the 32 sums of column `warp` by the warp's lanes
+  v = sum[lane][warp];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (lane == 0 && blockIdx.x * 32 + warp < D) dw[blockIdx.x * 32 + warp] = (float)v;
 }
 
 template <typename T, int L, int CH, int MODE, bool HALVES>
 cudaError_t launch(Args &a, cudaStream_t st) {
-  constexpr int kRows = kThreads / L;
+  constexpr int kRows = kThreads / L, kPerSm = blocks_per_sm(CH, MODE), kBegin = MODE == kRope ? 3 : 8;
   const int sms = tc::sm_count();
   if (sms <= 0) return cudaErrorNoDevice;
   // a tile's tokens: those of a pass, or as few as there are
   a.tile = 1, a.log_tile = 0;
   while (a.tile < kRows && a.tile < a.S) a.tile *= 2, ++a.log_tile;
-  a.tiles = (long long)a.B * ((a.S + a.tile - 1) >> a.log_tile);
-  const int heads = a.t[0].H + a.t[1].H, pass = kRows >> a.log_tile;
-  const int want = (int)std::min<long long>((4ll * sms + a.tiles - 1) / a.tiles, heads);
-  a.per = ((heads + want - 1) / want + pass - 1) / pass * pass;
+  a.per_row = (a.S + a.tile - 1) >> a.log_tile;
+  a.tiles = a.B * a.per_row;
+  a.inv_np = a.rot > 0 ? 0xffffffffu / (uint32_t)(a.rot / 2) + 1 : 0;
+  // Head ranges: all heads of a tile in one block, or more blocks where there would be
+  // too few.  A block costs its rows and a beginning of kBegin rows' time; the blocks
+  // that the SMs hold at once run together.
+  const int heads = a.t[0].H + a.t[1].H, pass = kRows >> a.log_tile, at_once = kPerSm * sms;
+  long long least = 0;
+  a.per = heads;
+  for (int splits = 1; splits <= heads; ++splits) {
+    const int per = ((heads + splits - 1) / splits + pass - 1) / pass * pass;
+    const long long blocks = (long long)a.tiles * ((heads + per - 1) / per), cost = (blocks + at_once - 1) / at_once * (kBegin + per / pass);
+    if (splits == 1 || cost < least) least = cost, a.per = per;
+    if (blocks > 8ll * at_once) break;
+  }
   a.splits = (heads + a.per - 1) / a.per;
   using R = Ring<T, CH, MODE>;
   constexpr int kFixed = R::kBytes + (MODE == kBwd ? 2 * CH * 2 * kThreads * 16 : 0);
-  size_t smem = kFixed + 8 * ((size_t)(a.axes + a.tile) * (a.rot / 2) + a.tile) + (MODE == kRope ? 0 : 8 * (size_t)a.D);
+  size_t smem = kFixed + 8 * ((size_t)(a.axes + a.tile) * (a.rot / 2) + a.axes * a.tile) + (MODE == kRope ? 0 : 8 * (size_t)a.D);
   if (a.start && a.R <= kRequestsInSmem) smem += 2 * sizeof(int) * ((size_t)a.R + 1);
   auto *kernel = hca_norm_rope_kernel<T, L, CH, MODE, HALVES>;
   static tc::SmemAttrOnce attr;
   cudaError_t e = attr.ensure(reinterpret_cast<const void *>(kernel), kFixed + 38 * 1024);  // the most that the rest takes
   if (e != cudaSuccess) return e;
-  long long grid = a.tiles * a.splits;
-  grid = std::min<long long>(grid, MODE == kBwd ? std::min(kNormRopeParts, (CH > 1 ? 1 : 3) * sms) : 1 << 30);
+  uint32_t grid = a.tiles * a.splits;
+  if (MODE == kBwd) grid = std::min<uint32_t>(grid, std::min(kNormRopeParts, kPerSm * sms));
   ProfScope prof(MODE == kBwd ? kKNormRopeBwd : kKNormRope, st);
-  kernel<<<(unsigned)grid, kThreads, smem, st>>>(a);
+  kernel<<<grid, kThreads, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (MODE == kBwd && (a.t[0].dw || a.t[1].dw)) {
-    e = cache::launch_behind(hca_norm_rope_dw_kernel, dim3((a.D + 31) / 32, 2), kThreads, 0, st, (const float *)a.part, (int)grid, a.D, a.t[0].dw,
+    e = cache::launch_behind(hca_norm_rope_dw_kernel, dim3((a.D + 31) / 32, 2), kDwThreads, 0, st, (const float *)a.part, (int)grid, a.D, a.t[0].dw,
                              a.t[1].dw);
     if (e != cudaSuccess) return e;
   }
