@@ -19,12 +19,19 @@
 // coordinates.  The two upper bits (rounded) are the quadrant, the rest is an eighth
 // of a turn at most.
 //
-// A row belongs to L neighbouring lanes, 8 consecutive columns (one or two 16-byte
-// accesses) a lane and chunk, so a row is read once, stays in registers between
-// the sum of its squares and its output, and is written once.  A block takes a
-// tile of tokens and a range of heads: the tile's cos and sin are made once in
-// shared memory, then each lane keeps those of its own columns and token in
-// registers for all of the block's heads.
+// A row belongs to L neighbouring lanes in chunks of 16 bytes, so it is read once,
+// stays in registers between the sum of its squares and its output, and is written
+// once.  A block takes a tile of tokens and a range of heads: the tile's cos and sin
+// are made once in shared memory, then each lane keeps those of its own columns and
+// token in registers, times the weights, for all of the block's heads.
+//
+// Bounds.  Long sequences are bound by memory: forward of B = 1, H = 64, S = 65,536,
+// D = 128 in bf16 (2.18 GB) 330 us, 98% of the measured copy bandwidth, backward
+// (3.27 GB) 530 us, 91%.  (With a row's loads in its registers: 422 and 671 us; fp32
+// one by one instead of in pairs, and addresses by multiplication: 354 and 631.)
+// Shorter ones are bound by the blocks' beginnings, 3 us from the first instruction
+// to the first row: 2,571 prompt tokens (86 MB) 20.5 us; one token of 64 requests 5 us
+// in a graph, of which 2 are the launch.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -54,50 +61,42 @@ struct Args {
   int splits, per;      // head ranges of a tile, heads (of q, then kv) of a range
 };
 
-// 8 columns of a row as they are in memory, and as 4 packed pairs of fp32.  With
-// neighbours for pairs of a rotation the packed ones are (0, 2), (4, 6), (1, 3),
-// (5, 7), so that the two columns of a rotation lie in slots i and i ^ 2, which
-// costs bf16 nothing: its halves are taken apart in any case.
-template <bool HALVES>
-__device__ __forceinline__ constexpr int column(int slot, int e) {
-  return HALVES ? 2 * slot + e : (slot & 1) * 4 + 2 * e + (slot >> 1);
-}
-
-template <typename T>
+// 16 bytes of a row (a chunk: 8 columns of bf16, 4 of fp32) as they are in memory, and
+// as packed pairs of fp32 in slots.  With neighbours for pairs of a rotation the slots
+// are columns (0, 2), (4, 6), (1, 3), (5, 7), or (0, 2), (1, 3), so that the two
+// columns of a rotation lie in slots i and i ^ kSlots / 2, which costs bf16 nothing:
+// its halves are taken apart in any case.
+template <typename T, bool HALVES>
 struct Vec {
-  static constexpr int kWords = sizeof(T) * 2;
-  uint32_t w[kWords];
-  __device__ __forceinline__ void piece(int i, const uint4 &u) {
-    w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+  static constexpr int kCols = 16 / (int)sizeof(T), kSlots = kCols / 2;
+  uint32_t w[4];
+
+  static __device__ __forceinline__ constexpr int column(int slot, int e) {
+    return HALVES ? 2 * slot + e : slot % (kSlots / 2) * 4 + 2 * e + slot / (kSlots / 2);
   }
-  __device__ __forceinline__ void store(T *p) const {
-    uint4 *v = reinterpret_cast<uint4 *>(p);
-#pragma unroll
-    for (int i = 0; i < kWords / 4; ++i) v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-  }
-  // the same columns of the row's lane `from`
+  __device__ __forceinline__ void load(const uint4 &u) { w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w; }
+  __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]); }
+  // the same chunk of lane `from`
   __device__ __forceinline__ Vec of(int from) const {
     Vec r;
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) r.w[i] = __shfl_sync(0xffffffffu, w[i], from);
+    for (int i = 0; i < 4; ++i) r.w[i] = __shfl_sync(0xffffffffu, w[i], from);
     return r;
   }
   __device__ __forceinline__ uint32_t at(int c) const {
     if constexpr (sizeof(T) == 4) return w[c];
     else return c & 1 ? w[c >> 1] & 0xffff0000u : w[c >> 1] << 16;
   }
-  template <bool HALVES>
-  __device__ __forceinline__ void get(uint64_t (&f)[4]) const {
+  __device__ __forceinline__ void get(uint64_t (&f)[kSlots]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = tc::f32x2(at(column<HALVES>(i, 0)), at(column<HALVES>(i, 1)));
+    for (int i = 0; i < kSlots; ++i) f[i] = tc::f32x2(at(column(i, 0)), at(column(i, 1)));
   }
-  template <bool HALVES>
-  __device__ __forceinline__ void put(const uint64_t (&f)[4]) {
-    float v[8];
+  __device__ __forceinline__ void put(const uint64_t (&f)[kSlots]) {
+    float v[kCols];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tc::f32x2_split(f[i], v[column<HALVES>(i, 0)], v[column<HALVES>(i, 1)]);
+    for (int i = 0; i < kSlots; ++i) tc::f32x2_split(f[i], v[column(i, 0)], v[column(i, 1)]);
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
+    for (int i = 0; i < 4; ++i) {
       if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
       else w[i] = tc::pack_bf16x2(v[2 * i], v[2 * i + 1]);
     }
@@ -177,14 +176,15 @@ __device__ __forceinline__ int request_of(const int32_t *start, int R, int t) {
   return lo;
 }
 
-constexpr int blocks_per_sm(int ch, int mode) { return ch > 1 ? (mode == kBwd ? 1 : 2) : mode == kBwd ? 3 : 4; }
+// of rows with so many columns a lane
+constexpr int blocks_per_sm(int cols, int mode) { return cols > 8 ? (mode == kBwd ? 1 : 2) : mode == kBwd ? 3 : 4; }
 
 // A thread's rows come through shared memory, its own 16-byte pieces in kStages
 // slots that only it writes (asynchronously) and reads, so nothing waits but the
 // thread itself.
-template <typename T, int CH, int MODE>
+template <int CH, int MODE>
 struct Ring {
-  static constexpr int kPieces = CH * (int)(sizeof(T) / 2) * (MODE == kBwd ? 2 : 1);  // of a row
+  static constexpr int kPieces = CH * (MODE == kBwd ? 2 : 1);  // of a row
   static constexpr int kStages = kPieces <= 4 ? 8 / kPieces : 2;
   static constexpr int kBytes = kStages * kPieces * kThreads * 16;
 };
@@ -198,19 +198,24 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// CH chunks of a row a lane, chunks l, l + L, ... for lane l of the row's L: the lanes
+// of an access are neighbours in memory (with 8 columns of fp32 side by side a lane
+// each 32-byte sector went over the way to L2 in two halves: backward of 2 x 8 x 4,093
+// rows of 64 columns 25 us, 19 this way).
 template <typename T, int L, int CH, int MODE, bool HALVES>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(CH, MODE)) hca_norm_rope_kernel(const Args a) {
-  using R = Ring<T, CH, MODE>;
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(CH * 16 / (int)sizeof(T), MODE)) hca_norm_rope_kernel(const Args a) {
+  using R = Ring<CH, MODE>;
+  using V = Vec<T, HALVES>;
+  constexpr int kCols = V::kCols, kSlots = V::kSlots, kF4 = kCols / 4;
   constexpr int kRows = kThreads / L, kRowsLog = L == 8 ? 5 : L == 16 ? 4 : 3;  // rows of a pass
   static_assert(kRows == 1 << kRowsLog, "a power of two");
-  constexpr int kVec = (int)(sizeof(T) / 2);  // pieces of 8 columns
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, l = tid % L, group = tid / L;
   const int np = a.rot / 2, row_lanes = lane & ~(L - 1);
   const uint32_t ring = tc::smem_u32(smem) + 16 * tid;
-  float4 *sh_dw = reinterpret_cast<float4 *>(smem + R::kBytes);                 // [2][CH * 2][kThreads] (backward)
+  float4 *sh_dw = reinterpret_cast<float4 *>(smem + R::kBytes);                 // [2][CH * kF4][kThreads] (backward)
   unsigned long long *sh_freq =
-      reinterpret_cast<unsigned long long *>(smem + R::kBytes + (MODE == kBwd ? 2 * CH * 2 * kThreads * 16 : 0));  // [axes][np]
+      reinterpret_cast<unsigned long long *>(smem + R::kBytes + (MODE == kBwd ? 2 * CH * kF4 * kThreads * 16 : 0));  // [axes][np]
   float2 *sh_cs = reinterpret_cast<float2 *>(sh_freq + a.axes * np);            // [tile][np]
   long long *sh_pos = reinterpret_cast<long long *>(sh_cs + a.tile * np);       // [axes][tile] coordinates
   float *sh_w = reinterpret_cast<float *>(sh_pos + a.axes * a.tile);            // [2][D] weights
@@ -262,16 +267,16 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH, MODE)) hca_norm_ro
   int partner[CH], pair0[CH];
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    const int c = l + k * L, z = 8 * c - a.first;  // chunk, its first column among the rotated ones
-    mine[k] = 8 * c < a.D;
+    const int c = l + k * L, z = kCols * c - a.first;  // chunk, its first column among the rotated ones
+    mine[k] = kCols * c < a.D;
     turned[k] = mine[k] && z >= 0 && z < a.rot;
     upper[k] = HALVES && z >= np;
     pair0[k] = HALVES ? (upper[k] ? z - np : z) : z / 2;
-    partner[k] = turned[k] && HALVES ? (upper[k] ? c - np / 8 : c + np / 8) : c;
+    partner[k] = turned[k] && HALVES ? (upper[k] ? c - np / kCols : c + np / kCols) : c;
   }
   if constexpr (MODE == kBwd) {
 #pragma unroll
-    for (int i = 0; i < 4 * CH; ++i) sh_dw[i * kThreads + tid] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < 2 * CH * kF4; ++i) sh_dw[i * kThreads + tid] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   const float inv_d = 1.f / (float)a.D;
 
@@ -298,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH, MODE)) hca_norm_ro
     // The thread's rows in order, their pieces on their way to slot n % kStages.
     const T *next_x = static_cast<const T *>(a.t[0].x), *next_g = static_cast<const T *>(a.t[0].g);
     if (own0 > 0) {
-      next_x += b * a.t[0].xb + s * a.t[0].xs + (lo0 + head0) * a.t[0].xh + 8 * l;
-      if constexpr (MODE == kBwd) next_g += b * a.t[0].gb + s * a.t[0].gs + (lo0 + head0) * a.t[0].gh + 8 * l;
+      next_x += b * a.t[0].xb + s * a.t[0].xs + (lo0 + head0) * a.t[0].xh + kCols * l;
+      if constexpr (MODE == kBwd) next_g += b * a.t[0].gb + s * a.t[0].gs + (lo0 + head0) * a.t[0].gh + kCols * l;
     }
     int64_t step_x = head_step * a.t[0].xh, step_g = MODE == kBwd ? head_step * a.t[0].gh : 0;
     uint32_t at = 0, left = own0;  // of the next row; rows of this tensor that are left
@@ -309,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH, MODE)) hca_norm_ro
         next_x = static_cast<const T *>(a.t[1].x);
         next_g = static_cast<const T *>(a.t[1].g);
         if (own1 > 0) {
-          next_x += b * a.t[1].xb + s * a.t[1].xs + (lo1 + head0) * a.t[1].xh + 8 * l;
-          if constexpr (MODE == kBwd) next_g += b * a.t[1].gb + s * a.t[1].gs + (lo1 + head0) * a.t[1].gh + 8 * l;
+          next_x += b * a.t[1].xb + s * a.t[1].xs + (lo1 + head0) * a.t[1].xh + kCols * l;
+          if constexpr (MODE == kBwd) next_g += b * a.t[1].gb + s * a.t[1].gs + (lo1 + head0) * a.t[1].gh + kCols * l;
         }
         step_x = head_step * a.t[1].xh;
         if constexpr (MODE == kBwd) step_g = head_step * a.t[1].gh;
@@ -320,12 +325,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH, MODE)) hca_norm_ro
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
           const bool row = left > 0 && mine[k];
-#pragma unroll
-          for (int v = 0; v < kVec; ++v) {
-            const int col = CH == 1 ? v * (16 / (int)sizeof(T)) : row ? 8 * k * L + v * (16 / (int)sizeof(T)) : 0;
-            cp_async_16(to + (k * kVec + v) * (kThreads * 16), next_x + col, row ? 16 : 0);
-            if constexpr (MODE == kBwd) cp_async_16(to + ((CH + k) * kVec + v) * (kThreads * 16), next_g + col, row ? 16 : 0);
-          }
+          const int col = k == 0 || row ? kCols * k * L : 0;
+          cp_async_16(to + k * (kThreads * 16), next_x + col, row ? 16 : 0);
+          if constexpr (MODE == kBwd) cp_async_16(to + (CH + k) * (kThreads * 16), next_g + col, row ? 16 : 0);
         }
         if (left > 1) {
           next_x += step_x;
@@ -368,20 +370,20 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH, MODE)) hca_norm_ro
       const NormRopeTensor &t = a.t[which];
       const uint32_t end = which ? steps : n0;
       if (n >= end) continue;
-      T *y = static_cast<T *>(t.y) + b * t.yb + s * t.ys + ((which ? lo1 : lo0) + head0) * t.yh + 8 * l;
+      T *y = static_cast<T *>(t.y) + b * t.yb + s * t.ys + ((which ? lo1 : lo0) + head0) * t.yh + kCols * l;
       const int64_t step_y = head_step * t.yh;
       uint32_t rows = which ? own1 : own0;  // that are left
       // What a column and its partner count in a rotated column (backwards: turned
       // back).  Forwards the weights are in them.
-      uint64_t own[CH][4], other[CH][4], w[CH][4], dw[CH][4];
+      uint64_t own[CH][kSlots], other[CH][kSlots], w[CH][kSlots], dw[CH][kSlots];
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
           float o[2], p[2], wt[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int c = column<HALVES>(i, e), z = 8 * (l + k * L) + c;
+            const int c = V::column(i, e), z = kCols * (l + k * L) + c;
             const float2 cs = turned[k] ? sh_cs[token * np + pair0[k] + (HALVES ? c : c >> 1)] : make_float2(1.f, 0.f);
             const bool second = HALVES ? upper[k] : (c & 1) != 0;
             o[e] = cs.x;
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH, MODE)) hca_norm_ro
               wt[e] = weight[z];
               if (MODE == kFwd) {
                 o[e] *= wt[e];
-                p[e] *= weight[HALVES ? 8 * partner[k] + c : z ^ 1];
+                p[e] *= weight[HALVES ? kCols * partner[k] + c : z ^ 1];
               }
             }
           }
@@ -402,61 +404,60 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH, MODE)) hca_norm_ro
         }
         if constexpr (MODE == kBwd) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float4 v = sh_dw[(which * 2 * CH + 2 * k + i) * kThreads + tid];
+          for (int i = 0; i < kF4; ++i) {
+            const float4 v = sh_dw[((which * CH + k) * kF4 + i) * kThreads + tid];
             dw[k][2 * i] = pair(v.x, v.y);
             dw[k][2 * i + 1] = pair(v.z, v.w);
           }
         }
       }
       // own f + other f of the partner, for a row's slots
-      auto rotate = [&](const Vec<T> (&v)[CH], const uint64_t (&f)[CH][4], uint64_t (&o)[CH][4]) {
+      auto rotate = [&](const V (&v)[CH], const uint64_t (&f)[CH][kSlots], uint64_t (&o)[CH][kSlots]) {
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-          uint64_t q[4];
+          uint64_t q[kSlots];
           if constexpr (HALVES) {
-            Vec<T> p = v[0].of(CH == 1 ? row_lanes + partner[k] : partner[k] & 31);
-            if constexpr (CH > 1) {  // the partner may be in the other chunk of its lane
-              const Vec<T> p1 = v[CH - 1].of(partner[k] & 31);
-              if (partner[k] >= 32) p = p1;
+            const int from = row_lanes + (partner[k] & (L - 1));
+            V p = v[0].of(from);
+#pragma unroll
+            for (int j = 1; j < CH; ++j) {  // the partner may be in another chunk of its lane
+              const V pj = v[j].of(from);
+              if (partner[k] >= j * L) p = pj;
             }
-            p.template get<HALVES>(q);
+            p.get(q);
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[k][i] = tc::ffma2(f[k][i], own[k][i], tc::fmul2(HALVES ? q[i] : f[k][i ^ 2], other[k][i]));
+          for (int i = 0; i < kSlots; ++i) o[k][i] = tc::ffma2(f[k][i], own[k][i], tc::fmul2(HALVES ? q[i] : f[k][i ^ (kSlots / 2)], other[k][i]));
         }
       };
 #pragma unroll 1
       for (; n < end; ++n) {
         cp_async_wait<R::kStages - 1>();
-        Vec<T> vx[CH], vg[CH];
-        const uint32_t from = (n % R::kStages) * (R::kPieces * kThreads * 16) + 16 * tid;
+        V vx[CH], vg[CH];
+        const uint8_t *from = smem + (n % R::kStages) * (R::kPieces * kThreads * 16) + 16 * tid;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-#pragma unroll
-          for (int v = 0; v < kVec; ++v) {
-            vx[k].piece(v, *reinterpret_cast<const uint4 *>(smem + from + (k * kVec + v) * (kThreads * 16)));
-            if constexpr (MODE == kBwd) vg[k].piece(v, *reinterpret_cast<const uint4 *>(smem + from + ((CH + k) * kVec + v) * (kThreads * 16)));
-          }
+          vx[k].load(*reinterpret_cast<const uint4 *>(from + k * (kThreads * 16)));
+          if constexpr (MODE == kBwd) vg[k].load(*reinterpret_cast<const uint4 *>(from + (CH + k) * (kThreads * 16)));
         }
         const bool row = alive && rows > 0;
-        uint64_t f[CH][4], o[CH][4];
+        uint64_t f[CH][kSlots], o[CH][kSlots];
 #pragma unroll
-        for (int k = 0; k < CH; ++k) vx[k].template get<HALVES>(f[k]);
+        for (int k = 0; k < CH; ++k) vx[k].get(f[k]);
         if constexpr (MODE == kRope) {
           rotate(vx, f, o);
         } else {
-          uint64_t ss = 0, hx = 0, gx[CH][4];
+          uint64_t ss = 0, hx = 0, gx[CH][kSlots];
           if constexpr (MODE == kBwd) {
-            uint64_t g0[CH][4];
+            uint64_t g0[CH][kSlots];
 #pragma unroll
-            for (int k = 0; k < CH; ++k) vg[k].template get<HALVES>(g0[k]);
+            for (int k = 0; k < CH; ++k) vg[k].get(g0[k]);
             rotate(vg, g0, o);
           }
 #pragma unroll
           for (int k = 0; k < CH; ++k) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kSlots; ++i) {
               ss = tc::ffma2(f[k][i], f[k][i], ss);
               if constexpr (MODE == kBwd) {
                 gx[k][i] = tc::fmul2(o[k][i], f[k][i]);
@@ -477,14 +478,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH, MODE)) hca_norm_ro
 #pragma unroll
             for (int k = 0; k < CH; ++k)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) o[k][i] = tc::fmul2(o[k][i], r2);
+              for (int i = 0; i < kSlots; ++i) o[k][i] = tc::fmul2(o[k][i], r2);
           } else {
             const float q = -(r * r) * (h1 * inv_d), rw = row ? r : 0.f;
             const uint64_t q2 = pair(q, q), rw2 = pair(rw, rw);
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
+              for (int i = 0; i < kSlots; ++i) {
                 dw[k][i] = tc::ffma2(gx[k][i], rw2, dw[k][i]);
                 o[k][i] = tc::fmul2(r2, tc::ffma2(f[k][i], q2, tc::fmul2(o[k][i], w[k][i])));
               }
@@ -494,10 +495,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH, MODE)) hca_norm_ro
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
           if (row && mine[k]) {
-            Vec<T> out;
-            out.template put<HALVES>(o[k]);
+            V out;
+            out.put(o[k]);
             if (MODE == kRope && !turned[k]) out = vx[k];  // as it was, infinities too
-            out.store(y + 8 * k * L);
+            out.store(y + kCols * k * L);
           }
         }
         y += step_y;
@@ -508,11 +509,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH, MODE)) hca_norm_ro
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < kF4; ++i) {
             float4 v;
             tc::f32x2_split(dw[k][2 * i], v.x, v.y);
             tc::f32x2_split(dw[k][2 * i + 1], v.z, v.w);
-            sh_dw[(which * 2 * CH + 2 * k + i) * kThreads + tid] = v;
+            sh_dw[((which * CH + k) * kF4 + i) * kThreads + tid] = v;
           }
         }
       }
@@ -524,13 +525,13 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH, MODE)) hca_norm_ro
     // sums of the block's rows: over its row groups, in their order
     __syncthreads();
     for (int i = tid; i < 2 * a.D; i += kThreads) {
-      const int which = i / a.D, d = i - which * a.D, chunk = d >> 3, c = d & 7;
+      const int which = i / a.D, d = i - which * a.D, chunk = d / kCols, c = d % kCols;
       if (!a.t[which].dw) continue;
-      int slot = 0;  // of the column among the lane's 8 floats
+      int slot = 0;  // of the column among the chunk's floats
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (column<HALVES>(j >> 1, j & 1) == c) slot = j;
-      const float *from = reinterpret_cast<const float *>(sh_dw + (size_t)(which * 2 * CH + 2 * (chunk / L) + (slot >> 2)) * kThreads + chunk % L) + (slot & 3);
+      for (int j = 0; j < kCols; ++j)
+        if (V::column(j >> 1, j & 1) == c) slot = j;
+      const float *from = reinterpret_cast<const float *>(sh_dw + (size_t)((which * CH + chunk / L) * kF4 + (slot >> 2)) * kThreads + chunk % L) + (slot & 3);
       float v = 0.f;
 #pragma unroll 8
       for (int r = 0; r < kRows; ++r) v += from[4 * r * L];
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(kDwThreads) hca_norm_rope_dw_kernel(const floa
 
 template <typename T, int L, int CH, int MODE, bool HALVES>
 cudaError_t launch(Args &a, cudaStream_t st) {
-  constexpr int kRows = kThreads / L, kPerSm = blocks_per_sm(CH, MODE), kBegin = MODE == kRope ? 3 : 8;
+  constexpr int kRows = kThreads / L, kPerSm = blocks_per_sm(CH * 16 / (int)sizeof(T), MODE), kBegin = MODE == kRope ? 3 : 8;
   const int sms = tc::sm_count();
   if (sms <= 0) return cudaErrorNoDevice;
   // a tile's tokens: those of a pass, or as few as there are
@@ -586,8 +587,8 @@ cudaError_t launch(Args &a, cudaStream_t st) {
     if (blocks > 8ll * at_once) break;
   }
   a.splits = (heads + a.per - 1) / a.per;
-  using R = Ring<T, CH, MODE>;
-  constexpr int kFixed = R::kBytes + (MODE == kBwd ? 2 * CH * 2 * kThreads * 16 : 0);
+  using R = Ring<CH, MODE>;
+  constexpr int kFixed = R::kBytes + (MODE == kBwd ? 2 * CH * (4 / (int)sizeof(T)) * kThreads * 16 : 0);
   size_t smem = kFixed + 8 * ((size_t)(a.axes + a.tile) * (a.rot / 2) + a.axes * a.tile) + (MODE == kRope ? 0 : 8 * (size_t)a.D);
   if (a.start && a.R <= kRequestsInSmem) smem += 2 * sizeof(int) * ((size_t)a.R + 1);
   auto *kernel = hca_norm_rope_kernel<T, L, CH, MODE, HALVES>;
@@ -610,10 +611,11 @@ cudaError_t launch(Args &a, cudaStream_t st) {
 
 template <typename T, int MODE, bool HALVES>
 cudaError_t by_width(Args &a, cudaStream_t st) {
-  if (a.D <= 64) return launch<T, 8, 1, MODE, HALVES>(a, st);
-  if (a.D <= 128) return launch<T, 16, 1, MODE, HALVES>(a, st);
-  if (a.D <= 256) return launch<T, 32, 1, MODE, HALVES>(a, st);
-  return launch<T, 32, 2, MODE, HALVES>(a, st);
+  constexpr int kCh = (int)sizeof(T) / 2;  // chunks of 8 columns
+  if (a.D <= 64) return launch<T, 8, kCh, MODE, HALVES>(a, st);
+  if (a.D <= 128) return launch<T, 16, kCh, MODE, HALVES>(a, st);
+  if (a.D <= 256) return launch<T, 32, kCh, MODE, HALVES>(a, st);
+  return launch<T, 32, 2 * kCh, MODE, HALVES>(a, st);
 }
 
 template <int MODE>
