@@ -704,6 +704,9 @@ cudaError_t attend(P &p, const CacheAttnArgs &a, cudaStream_t st) {
     const cudaError_t e = p.NQ == 4 ? simt<4>(p, st) : p.NQ == 8 ? simt<8>(p, st) : simt<kSimtCols>(p, st);
     if (e != cudaSuccess) return e;
   }
+  if constexpr (P::kShared) {
+    if (p.joined) return cudaSuccess;
+  }
   const int gmax = (int)std::min<size_t>(l.gmax, 1 << 20);
   const bool bf16_rows = tcs && !(P::kShared && a.share.apart);
   const cudaError_t e = bf16_rows ? combine<__nv_bfloat16>(p, gmax, sms, st) : combine<float>(p, gmax, sms, st);
@@ -728,6 +731,7 @@ void cache::shared_params(const CacheAttnArgs &a, SharedAttnParams &p) {
   fill(p, a, p.sms);
   p.first = a.share.first; p.cols = a.share.cols; p.G = a.share.G; p.apart = a.share.apart;
   p.beside = a.share.beside && p.in_cta;
+  p.joined = a.share.joined && p.beside;
 }
 
 }  // namespace hca

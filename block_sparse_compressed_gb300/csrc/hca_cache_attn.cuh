@@ -43,6 +43,7 @@ struct SharedAttnParams : AttnParams {
   int G;
   int apart;  // those columns are left out, and out is fp32 (the join adds them)
   int beside; // the kernel of the prefixes runs at the same time, on other SMs
+  int joined; // the join of the prefixes has the parts of these keys too
   int sms;
   static constexpr bool kShared = true;
 };

@@ -1010,13 +1010,13 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const P p) 
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (P::kShared) {
-    if (p.beside && blockIdx.x == 0) pdl_wait();  // who waits for this kernel waits for the prefixes' too
-  }
   if (tid == 0 && sh.abort) atomicExch(status, HCA_ERR_TIMEOUT);
   if (warp == 10) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmem);
+  }
+  if constexpr (P::kShared) {
+    if (p.beside && blockIdx.x == 0) pdl_wait();  // who waits for this kernel waits for the prefixes' too
   }
 }
 

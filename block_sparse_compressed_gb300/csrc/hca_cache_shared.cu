@@ -294,8 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
     tmem_alloc(&sh.tmem_base, kTmem);
     tmem_relinquish();
   }
-  pdl_launch_dependents();  // the requests' own keys, where they run beside this
   make_table(p, sh.table, sh.tmp);
+  // The requests' own keys, where they run beside this: when every CTA has its tensor
+  // memory, which those need too.
+  pdl_launch_dependents();
   const int units = sh.table.units, quota = sh.table.quota;
   tc_fence_before();
   __syncthreads();
@@ -755,8 +757,21 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
-template <int D, int U>  // U rows of a lane at a time
+// What a block's rows have of their own keys where a group's tiles were cut between
+// CTAs (the combine kernel's work in hca_cache_attn).
+struct OwnParts {
+  int row, columns;  // rows of the group
+  int slot0, cta;    // of the first part; the others have slots 2 (cta + i)
+  int parts;
+};
+
+// U rows of a lane at a time.  With `Own` the parts of the requests' own keys are joined
+// here too.
+template <int D, int U, bool Own>
 __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const SharedParams p) {
+  __shared__ OwnParts cut[kJoinThreads / (D / 4)];  // a block's rows have as many groups at most
+  __shared__ int ncut;
+  static_assert(!Own || U == 1, "a block's rows are adjacent");
   constexpr int kLanes = D / 4, kRows = kJoinThreads / kLanes;
   constexpr float kLog2e = 1.4426950408889634f;
   const int tid = threadIdx.x, l = tid % kLanes;
@@ -764,7 +779,10 @@ __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const Shar
   const Table &table = *p.table;
   const int units = table.units, quota = table.quota, row_tiles = table.row_tiles;
   const SchedHeader *own = p.own.hdr;
-  int worst = own->status;
+  int worst = Own ? HCA_OK : own->status;
+  if constexpr (Own) {
+    for (int i = tid; i < p.own.grid; i += kJoinThreads) worst = max(worst, p.own.err[i] == HCA_ERR_TIMEOUT ? 1000 : p.own.err[i]);
+  }
   for (int i = tid; i < p.grid; i += kJoinThreads) worst = max(worst, p.err[i] == HCA_ERR_TIMEOUT ? 1000 : p.err[i]);
   const bool late = __syncthreads_or(worst == 1000 || worst == HCA_ERR_TIMEOUT), wrong = __syncthreads_or(worst != HCA_OK);
   if (blockIdx.x == 0 && tid == 0) *p.status = late ? HCA_ERR_TIMEOUT : wrong ? HCA_ERR_CACHE : HCA_OK;
@@ -789,10 +807,23 @@ __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const Shar
     const int parts = x.tiles > 0 ? (u0 + x.span - 1) / quota - first + 1 : 0;
     if (p.merge && parts == 1) continue;  // finished by the CTA that had it
     const int r0 = item % kChunks * (kRows * U) + tid / kLanes;  // the lane's first row; the others are kRows apart
+    if constexpr (Own) {
+      // the groups among the block's rows that were cut
+      const int a = x.row0 + rt * kRowTile + item % kChunks * kRows, e = min(a + kRows, x.row0 + x.rows);
+      __syncthreads();
+      if (tid == 0) ncut = 0;
+      __syncthreads();
+      for (int c = tid; c < p.own.grid; c += kJoinThreads) {
+        const Border b = p.own.border[c];
+        if (b.columns > 0 && b.row < e && b.row + b.columns > a) cut[atomicAdd(&ncut, 1)] = OwnParts{b.row, b.columns, b.slot, c, b.parts};
+      }
+      __syncthreads();
+    }
     float4 o[U];
     float lse[U];
     size_t slot[U];
     int n[U];  // parts; -1: no such row
+    OwnParts mine = {0, 0, 0, 0, 0};
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = rt * kRowTile + r0 + u * kRows;
@@ -801,16 +832,30 @@ __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const Shar
       o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       lse[u] = 0.f;
       if (n[u] >= 0) {
-        o[u] = *reinterpret_cast<const float4 *>(p.own_out + (size_t)(x.row0 + r) * D + 4 * l);
-        lse[u] = p.own_lse[x.row0 + r];
+        if constexpr (Own) {
+          for (int i = 0; i < ncut; ++i)
+            if (x.row0 + r >= cut[i].row && x.row0 + r < cut[i].row + cut[i].columns) mine = cut[i];
+        }
+        if (mine.parts == 0) {
+          o[u] = *reinterpret_cast<const float4 *>(p.own_out + (size_t)(x.row0 + r) * D + 4 * l);
+          lse[u] = p.own_lse[x.row0 + r];
+        }
       }
     }
+    // part i of the row's own keys: its reference, its sum, and what its O counts beside
+    // a reference of M
+    auto own_slot = [&](int i) { return i == 0 ? mine.slot0 : 2 * (mine.cta + i); };
+    auto own_ml = [&](int i) { return p.own.part_ml[(size_t)own_slot(i) * p.own.NQ + (x.row0 + rt * kRowTile + r0 - mine.row)]; };
     int most = 0;
     float M[U], sum[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       most = max(most, n[u]);
       M[u] = lse[u] * kLog2e;
+    }
+    if constexpr (Own) {
+      if (mine.parts > 0) M[0] = -INFINITY;
+      for (int i = 0; i < mine.parts; ++i) M[0] = fmaxf(M[0], own_ml(i).x);
     }
     for (int i = 0; i < most; ++i) {
 #pragma unroll
@@ -819,8 +864,23 @@ __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const Shar
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      sum[u] = n[u] > 0 ? exp2f(lse[u] * kLog2e - M[u]) : 1.f;
+      sum[u] = mine.parts > 0 ? 0.f : n[u] > 0 ? exp2f(lse[u] * kLog2e - M[u]) : 1.f;
       o[u].x *= sum[u]; o[u].y *= sum[u]; o[u].z *= sum[u]; o[u].w *= sum[u];
+    }
+    if constexpr (Own) {
+#pragma unroll 4
+      for (int i = 0; i < mine.parts; ++i) {
+        const float2 ml = own_ml(i);
+        const size_t at = (size_t)own_slot(i) * p.own.NQ + (x.row0 + rt * kRowTile + r0 - mine.row);
+        const float4 v = *reinterpret_cast<const float4 *>(p.own.part_o + at * D + 4 * l);
+        // O / l as the prefixes' parts have it: 2^unit / l is a normal number
+        const float w = exp2f(ml.x - M[0]), f = ml.y != 0.f ? w * ml.y * (exp2_int(p.own.part_unit[own_slot(i)]) / ml.y) : 0.f;
+        sum[0] += ml.y != 0.f ? w * ml.y : 0.f;  // 0: a part in which the row saw no key
+        if (f != 0.f) {
+          o[0].x = fmaf(f, v.x, o[0].x); o[0].y = fmaf(f, v.y, o[0].y);
+          o[0].z = fmaf(f, v.z, o[0].z); o[0].w = fmaf(f, v.w, o[0].w);
+        }
+      }
     }
 #pragma unroll(U > 1 ? 1 : 4)
     for (int i = 0; i < most; ++i) {
@@ -841,9 +901,10 @@ __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const Shar
     for (int u = 0; u < U; ++u) {
       if (n[u] < 0) continue;
       const size_t row = (size_t)x.row0 + rt * kRowTile + r0 + u * kRows;
-      const float inv = n[u] > 0 ? 1.f / sum[u] : 1.f;
+      const bool joined = n[u] > 0 || mine.parts > 0;
+      const float inv = joined ? 1.f / sum[u] : 1.f;
       *reinterpret_cast<uint2 *>(p.out + row * D + 4 * l) = make_uint2(pack_bf16x2(o[u].x * inv, o[u].y * inv), pack_bf16x2(o[u].z * inv, o[u].w * inv));
-      if (l == 0) p.lse[row] = n[u] > 0 ? (M[u] + log2f(sum[u])) * 0.69314718055994531f : lse[u];
+      if (l == 0) p.lse[row] = joined ? (M[u] + log2f(sum[u])) * 0.69314718055994531f : lse[u];
     }
   }
 }
@@ -894,8 +955,9 @@ cudaError_t launch(const CacheAttnArgs &a, SharedParams &p, int sms, cudaStream_
   const bool many = p.merge;
   const long long per = (long long)kJoinThreads / (D / 4) * (many ? 4 : 1);
   const dim3 grid((unsigned)std::min<long long>((long long)p.own.N * p.own.H / per + p.own.G * (kRowTile / per), (many ? 3ll : 5ll) * sms));
-  if (many) return launch_behind(hca_cache_join_kernel<D, 4>, grid, kJoinThreads, 0, st, p);
-  return launch_behind(hca_cache_join_kernel<D, 1>, grid, kJoinThreads, 0, st, p);
+  if (many) return launch_behind(hca_cache_join_kernel<D, 4, false>, grid, kJoinThreads, 0, st, p);
+  if (p.own.joined) return launch_behind(hca_cache_join_kernel<D, 1, true>, grid, kJoinThreads, 0, st, p);
+  return launch_behind(hca_cache_join_kernel<D, 1, false>, grid, kJoinThreads, 0, st, p);
 }
 
 }  // namespace
@@ -962,6 +1024,10 @@ cudaError_t cache_attn_shared(const CacheAttnArgs &args, cudaStream_t st) {
   a.ws = ws + l.off_own;
   a.share.apart = 1;
   a.share.beside = !p.merge && sms <= kMaxGrid;
+  // The parts of the own keys in the same launch, where each block has one item (4,096
+  // rows over 24,960 entries 60 us, 69 with a launch of their own); with more items a
+  // block it is slower (12,800 rows over 4,096 entries 60 us, 57).
+  a.share.joined = (long long)a.N * a.H * (a.D / 4) <= 5ll * sms * kJoinThreads;
   shared_params(a, p.own);
   return a.D == 64 ? launch<64>(a, p, sms, st) : launch<128>(a, p, sms, st);
 }

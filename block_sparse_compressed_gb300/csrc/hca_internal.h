@@ -182,6 +182,7 @@ struct CacheShare {
   int G;                        // 0: nothing is shared
   int apart;                    // hca_cache_attn's kernels leave the common columns out and write fp32 rows
   int beside;                   // and run while the prefixes' kernel does
+  int joined;                   // and (beside) leave their parts to the join of the prefixes
 };
 struct CacheAttnArgs {
   const void *q;

@@ -152,12 +152,15 @@ def test_block_scales(what, D):
     check_attn(call(case, first, cols, 16, 1), *case, 16, 1, scale_of(D), BF16)
 
 
-def test_agrees_with_the_call_without_prefixes_where_nothing_is_shared():
+def test_where_nothing_is_shared(apart):
+    """Each request's own is then all there is; attended with it (2) it is the call without prefixes, bit for bit."""
     case, first, cols = shared_case([(6, 0)], [5, 900, 3, 77, 128, 4000], [1, 3, 1, 0, 2, 1], 64, 128, 64, 4, 32, BF16, 9)
     q, start, held, raw, comp = case
     want = hca.hca_cache_attn(q.to(DEV), start.to(DEV), held.to(DEV), dev(raw), dev(comp), 64, 4, scale_of(128))
+    check_attn(call(case, first, cols, 64, 4), *case, 64, 4, scale_of(128), BF16)
+    apart(2)
     got = call(case, first, cols, 64, 4)
-    assert torch.equal(want[0], got[0])
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
     none = call(case, i32([0]), i32([]), 64, 4)
     assert torch.equal(want[0], none[0]) and torch.equal(want[1], none[1])
 

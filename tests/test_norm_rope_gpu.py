@@ -364,6 +364,31 @@ def test_the_binding_refuses():
         hca.hca_cache_norm_rope(q[0].transpose(0, 1), None, torch.zeros(2, dtype=torch.int32, device="cuda"), None, None, None, freq, EPS)
 
 
+def test_offsets_beyond_32_bits():
+    """2.35e9 elements, turned in place; rows at both ends and around 2^31."""
+    B, H, S, D = 2, 70, 32768, 512
+    x = torch.empty(B, H, S, D, dtype=BF16, device="cuda")
+    assert x.numel() > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(19)
+    some = [(0, 0, 0), (0, 69, 32767), (1, 57, 32766), (1, 58, 32767), (1, 69, 32767), (1, 3, 5)]
+    x.zero_()
+    rows = torch.randn(len(some), D, generator=g, device="cuda").to(BF16)
+    for (b, h, s), r in zip(some, rows):
+        x[b, h, s] = r
+    freq = torch.rand(32, generator=g, device="cuda")
+    pos = torch.randint(0, 10 ** 6, (B, S), dtype=torch.int32, device="cuda", generator=g)
+    hca.hca_rope(x, pos, freq, y=x)
+    for (b, h, s), r in zip(some, rows):
+        th = ON.angles(pos[b, s].cpu().numpy()[None], freq.cpu().numpy()[None])
+        close("x", x[b, h, s], ON.rotate(f64(r), th, D - 64, False), ON.rotate_bound(f64(r), th, D - 64, False), BF16)
+    assert int((x != 0).any(-1).sum()) == len(some)
+    out = hca.hca_norm_rope_fwd(x, None, None, None, pos, freq, EPS)[0]
+    for b, h, s in some:
+        th = ON.angles(pos[b, s].cpu().numpy()[None], freq.cpu().numpy()[None])
+        check_fwd(x[b, h, s], None, th, D - 64, False, out[b, h, s], "q")
+    assert int((out != 0).any(-1).sum()) == len(some)
+
+
 def test_threads_that_call_at_once():
     import threading
     q, kv, wq, wkv, pos, freq, dq, dkv = make(1, 4, 300, 64, 32, BF16, 18)
