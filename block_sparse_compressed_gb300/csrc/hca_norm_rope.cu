@@ -206,7 +206,7 @@ template <typename T, int L, int CH, int MODE, bool HALVES>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH * 16 / (int)sizeof(T), MODE)) hca_norm_rope_kernel(const Args a) {
   using R = Ring<CH, MODE>;
   using V = Vec<T, HALVES>;
-  constexpr int kCols = V::kCols, kSlots = V::kSlots, kF4 = kCols / 4;
+  constexpr int kCols = V::kCols, kSlots = V::kSlots, kF4 = kCols / 4, kCs = HALVES ? kCols : kCols / 2;
   constexpr int kRows = kThreads / L, kRowsLog = L == 8 ? 5 : L == 16 ? 4 : 3;  // rows of a pass
   static_assert(kRows == 1 << kRowsLog, "a power of two");
   extern __shared__ __align__(16) uint8_t smem[];
@@ -217,9 +217,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH * 16 / (int)sizeof(
   unsigned long long *sh_freq =
       reinterpret_cast<unsigned long long *>(smem + R::kBytes + (MODE == kBwd ? 2 * CH * kF4 * kThreads * 16 : 0));  // [axes][np]
   float2 *sh_cs = reinterpret_cast<float2 *>(sh_freq + a.axes * np);            // [tile][np]
-  long long *sh_pos = reinterpret_cast<long long *>(sh_cs + a.tile * np);       // [axes][tile] coordinates
-  float *sh_w = reinterpret_cast<float *>(sh_pos + a.axes * a.tile);            // [2][D] weights
-  int *sh_req = reinterpret_cast<int *>(sh_w + (MODE == kRope ? 0 : 2 * a.D));  // [2][R + 1] starts and held
+  float *sh_w = reinterpret_cast<float *>(sh_cs + a.tile * np);                 // [2][D] weights
+  long long *sh_pos = reinterpret_cast<long long *>(sh_w + (MODE == kRope ? 0 : 2 * a.D));  // [axes][tile] coordinates
+  int *sh_req = reinterpret_cast<int *>(sh_pos + a.axes * a.tile);              // [2][R + 1] starts and held
   const int token = group & (a.tile - 1), head0 = group >> a.log_tile, head_step = kRows >> a.log_tile, step_log = kRowsLog - a.log_tile;
 
   if constexpr (MODE == kBwd) tc::pdl_launch_dependents();  // the sums of dw wait for this kernel's end by themselves
@@ -378,29 +378,46 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH * 16 / (int)sizeof(
       uint64_t own[CH][kSlots], other[CH][kSlots], w[CH][kSlots], dw[CH][kSlots];
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
+        float2 cs[kCs];
+        float wt[kCols], wp[kCols];  // weights of the columns, of their partners
+#pragma unroll
+        for (int c = 0; c < kCs; ++c) cs[c] = make_float2(1.f, 0.f);
+        if (turned[k]) {
+#pragma unroll
+          for (int c = 0; c < kCs; c += 2) {
+            const float4 v = *reinterpret_cast<const float4 *>(sh_cs + token * np + pair0[k] + c);
+            cs[c] = make_float2(v.x, v.y);
+            cs[c + 1] = make_float2(v.z, v.w);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) wt[c] = wp[c] = 1.f;
+        if (MODE != kRope && mine[k]) {
+          const float *weight = sh_w + which * a.D;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4) {
+            *reinterpret_cast<float4 *>(wt + c) = *reinterpret_cast<const float4 *>(weight + kCols * (l + k * L) + c);
+            if (HALVES && MODE == kFwd) *reinterpret_cast<float4 *>(wp + c) = *reinterpret_cast<const float4 *>(weight + kCols * partner[k] + c);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) {
-          float o[2], p[2], wt[2];
+          float o[2], p[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int c = V::column(i, e), z = kCols * (l + k * L) + c;
-            const float2 cs = turned[k] ? sh_cs[token * np + pair0[k] + (HALVES ? c : c >> 1)] : make_float2(1.f, 0.f);
+            const int c = V::column(i, e);
+            const float2 turn = cs[HALVES ? c : c >> 1];
             const bool second = HALVES ? upper[k] : (c & 1) != 0;
-            o[e] = cs.x;
-            p[e] = (second == (MODE != kBwd)) ? cs.y : -cs.y;
-            wt[e] = 1.f;
-            if (MODE != kRope && mine[k]) {
-              const float *weight = sh_w + which * a.D;
-              wt[e] = weight[z];
-              if (MODE == kFwd) {
-                o[e] *= wt[e];
-                p[e] *= weight[HALVES ? kCols * partner[k] + c : z ^ 1];
-              }
+            o[e] = turn.x;
+            p[e] = (second == (MODE != kBwd)) ? turn.y : -turn.y;
+            if (MODE == kFwd) {
+              o[e] *= wt[c];
+              p[e] *= HALVES ? wp[c] : wt[c ^ 1];
             }
           }
           own[k][i] = pair(o[0], o[1]);
           other[k][i] = pair(p[0], p[1]);
-          w[k][i] = pair(wt[0], wt[1]);
+          w[k][i] = pair(wt[V::column(i, 0)], wt[V::column(i, 1)]);
         }
         if constexpr (MODE == kBwd) {
 #pragma unroll
