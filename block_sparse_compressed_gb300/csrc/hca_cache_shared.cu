@@ -85,7 +85,6 @@ struct Table {
   int units;            // of the line, -1: the prefixes are refused
   int quota;            // units of a CTA
   int row_tiles;        // of all prefixes, those without common entries among them
-  int pad;
   Prefix g[kSharedMaxGroups];
 };
 
@@ -104,7 +103,12 @@ __device__ __forceinline__ void make_table(const SharedParams &p, Table &t, long
       PrefixSize z;
       const bool fine = prefix_size(p.own, g, z);
       ok = ok && fine;
-      t.g[g] = Prefix{z.row0, z.rows, z.tiles, fine ? p.own.cols[g] : 0, z.tiles, 0, 0, fine ? p.own.first[g] : 0};
+      int r = 0;
+      if (fine) {
+        r = p.own.first[g];
+        while (r + 1 < p.own.first[g + 1] && p.own.start[r + 1] <= p.own.start[r]) ++r;
+      }
+      t.g[g] = Prefix{z.row0, z.rows, z.tiles, fine ? p.own.cols[g] : 0, z.tiles, 0, 0, r};
       units += (long long)z.row_tiles() * z.tiles;
       nrt += z.row_tiles();
     }

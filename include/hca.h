@@ -261,7 +261,9 @@ HCA_API int hca_compress_bwd(const void *x, const float *g, const float *bias, c
  *          positions that mean nothing; no row outside [0, N) is touched.
  *   dtype  of x and of the results; w, freq and dw are fp32, and so is all
  *          arithmetic, rounded once at the end.  Squares are summed in fp32:
- *          |x| below 2^60, and above 2^-60 somewhere in a row where eps is 0.
+ *          |x| below 2^60, and above 2^-60 somewhere in a row where eps is 0.  A
+ *          row with a NaN or an infinity comes out as NaN and 0.  hca_rope hands the
+ *          columns that do not turn through as they are.
  * D, first and rot are multiples of 8 (rot of 16 with halves; 0: no rotation),
  * D at most 512, axes 1 to 4, eps finite and not negative.  *_strides are host
  * arrays with the elements from one batch row, head (not for kv) and position to
@@ -437,10 +439,11 @@ HCA_API int hca_cache_attn(const void *q, const int32_t *start, const int32_t *h
  *                     requests hold the same blocks, all of whose entries every
  *                     token sees, shared_cols[g] * bs * m <= held[r] + 1; 0: none.
  *                     (A prefix's last block is common if it is full; what is behind
- *                     it belongs to the requests, and so do their raw rows.)
+ *                     it belongs to the requests, and so do their raw rows.  Requests
+ *                     without tokens need no table.)
  * G is at most 256 (HCA_ERR_SHAPE); with G = 0 nothing is shared.  The common
- * columns are read in the table of the prefix's first request.  Values of first and
- * shared_cols that do not fit make all N rows of out and lse NaN, as lengths out of
+ * columns are read in the table of the prefix's first request that has tokens.  Values
+ * of first and shared_cols that do not fit make all N rows of out and lse NaN, as lengths out of
  * range do (HCA_ERR_CACHE).  bf16: a prefix's part is rounded to fp32 and joined
  * with the request's own; fp32 has the same arithmetic as hca_cache_attn.
  * A call whose requests are few, or whose compressed tables are narrow, does what

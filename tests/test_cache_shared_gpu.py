@@ -305,6 +305,20 @@ def test_more_row_tiles_than_blocks(D):
     assert bool(bad[248:321].isnan().all()) and torch.equal(bad[:248], again[0][:248])
 
 
+@pytest.mark.parametrize("path", [1, 2])
+def test_requests_without_tokens_need_no_table(path, apart):
+    """A batch of fixed size: places that are not taken, before, between and behind the others."""
+    apart(path)
+    case, first, cols = shared_case([(4, 5), (3, 9), (2, 2)], [3, 0, 6, 0, 0, 40, 0, 0, 0], [0, 1, 2, 0, 0, 1, 0, 0, 0], 16, 64, 16, 1, 16, BF16, 25)
+    want = call(case, first, cols, 16, 1)
+    check_attn(want, *case, 16, 1, scale_of(64), BF16)
+    q, start, held, raw, comp = case
+    for r in (0, 3, 4, 6, 7, 8):
+        raw[2][r], comp[2][r], held[r] = -1, -1, 0
+    got = call(case, first, cols, 16, 1)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_few_rows_over_a_long_prefix():
     """A row tile in as many parts as the join takes."""
     case, first, cols = shared_case([(2, 300)], [5, 40], [1, 1], 8, 64, 16, 1, 64, BF16, 23)
