@@ -26,12 +26,14 @@
 // token in registers, times the weights, for all of the block's heads.
 //
 // Bounds.  Long sequences are bound by memory: forward of B = 1, H = 64, S = 65,536,
-// D = 128 in bf16 (2.18 GB) 330 us, 98% of the measured copy bandwidth, backward
-// (3.27 GB) 530 us, 91%.  (With a row's loads in its registers: 422 and 671 us; fp32
+// D = 128 in bf16 (2.18 GB) 323 us, 99% of the measured copy bandwidth, backward
+// (3.27 GB) 490 us, 98%.  (With a row's loads in its registers: 422 and 671 us; fp32
 // one by one instead of in pairs, and addresses by multiplication: 354 and 631.)
-// Shorter ones are bound by the blocks' beginnings, 3 us from the first instruction
-// to the first row: 2,571 prompt tokens (86 MB) 20.5 us; one token of 64 requests 5 us
-// in a graph, of which 2 are the launch.
+// Shorter ones are bound by the blocks' beginnings, 2 us from the first instruction
+// to the first row: 2,571 prompt tokens (86 MB) 15.7 us; one token of 64 requests 4.5 us
+// in a graph, of which 2 are the launch.  Few heads are bound by instructions, since a
+// token's cos and sin and a lane's factors are for few rows: one head and kv of 524,288
+// tokens 251 us (540 MB, 80 us; 1,030 instructions of a warp for two rows of its lanes).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -177,15 +179,17 @@ __device__ __forceinline__ int request_of(const int32_t *start, int R, int t) {
 }
 
 // of rows with so many columns a lane
-constexpr int blocks_per_sm(int cols, int mode) { return cols > 8 ? (mode == kBwd ? 1 : 2) : mode == kBwd ? 3 : 4; }
+constexpr int blocks_per_sm(int cols, int mode) { return (mode == kBwd ? 2 : 4) / (cols > 8 ? 2 : 1); }
 
 // A thread's rows come through shared memory, its own 16-byte pieces in kStages
 // slots that only it writes (asynchronously) and reads, so nothing waits but the
-// thread itself.
-template <int CH, int MODE>
+// thread itself.  An SM has 128 KB of slots forwards and 64 KB backwards, where two rows
+// are read for one that is written: B = 1, H = 64, S = 65,536, D = 128 in bf16 backwards
+// 490 us, 519 with 48 KB, 559 with 128 KB, and 556 with three blocks of 32 KB.
+template <int CH, int MODE, int COLS>
 struct Ring {
   static constexpr int kPieces = CH * (MODE == kBwd ? 2 : 1);  // of a row
-  static constexpr int kStages = kPieces <= 4 ? 8 / kPieces : 2;
+  static constexpr int kStages = (MODE == kBwd ? 64 : 128) * 1024 / blocks_per_sm(CH * COLS, MODE) / (kPieces * kThreads * 16);
   static constexpr int kBytes = kStages * kPieces * kThreads * 16;
 };
 
@@ -204,8 +208,8 @@ __device__ __forceinline__ void cp_async_wait() {
 // rows of 64 columns 25 us, 19 this way).
 template <typename T, int L, int CH, int MODE, bool HALVES>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH * 16 / (int)sizeof(T), MODE)) hca_norm_rope_kernel(const Args a) {
-  using R = Ring<CH, MODE>;
   using V = Vec<T, HALVES>;
+  using R = Ring<CH, MODE, V::kCols>;
   constexpr int kCols = V::kCols, kSlots = V::kSlots, kF4 = kCols / 4, kCs = HALVES ? kCols : kCols / 2;
   constexpr int kRows = kThreads / L, kRowsLog = L == 8 ? 5 : L == 16 ? 4 : 3;  // rows of a pass
   static_assert(kRows == 1 << kRowsLog, "a power of two");
@@ -604,7 +608,7 @@ cudaError_t launch(Args &a, cudaStream_t st) {
     if (blocks > 8ll * at_once) break;
   }
   a.splits = (heads + a.per - 1) / a.per;
-  using R = Ring<CH, MODE>;
+  using R = Ring<CH, MODE, 16 / (int)sizeof(T)>;
   constexpr int kFixed = R::kBytes + (MODE == kBwd ? 2 * CH * (4 / (int)sizeof(T)) * kThreads * 16 : 0);
   size_t smem = kFixed + 8 * ((size_t)(a.axes + a.tile) * (a.rot / 2) + a.axes * a.tile) + (MODE == kRope ? 0 : 8 * (size_t)a.D);
   if (a.start && a.R <= kRequestsInSmem) smem += 2 * sizeof(int) * ((size_t)a.R + 1);
