@@ -27,7 +27,7 @@
 //
 // Bounds.  Long sequences are bound by memory: forward of B = 1, H = 64, S = 65,536,
 // D = 128 in bf16 (2.18 GB) 323 us, 99% of the measured copy bandwidth, backward
-// (3.27 GB) 490 us, 98%.  (With a row's loads in its registers: 422 and 671 us; fp32
+// (3.27 GB) 484 us, 99%.  (With a row's loads in its registers: 422 and 671 us; fp32
 // one by one instead of in pairs, and addresses by multiplication: 354 and 631.)
 // Shorter ones are bound by the blocks' beginnings, 2 us from the first instruction
 // to the first row: 2,571 prompt tokens (86 MB) 15.7 us; one token of 64 requests 4.5 us
@@ -185,7 +185,8 @@ constexpr int blocks_per_sm(int cols, int mode) { return (mode == kBwd ? 2 : 4) 
 // slots that only it writes (asynchronously) and reads, so nothing waits but the
 // thread itself.  An SM has 128 KB of slots forwards and 64 KB backwards, where two rows
 // are read for one that is written: B = 1, H = 64, S = 65,536, D = 128 in bf16 backwards
-// 490 us, 519 with 48 KB, 559 with 128 KB, and 556 with three blocks of 32 KB.
+// 490 us (6 of them a slower sum of dw at its end), 519 with 48 KB, 559 with 128 KB, and
+// 556 with three blocks of 32 KB.
 template <int CH, int MODE, int COLS>
 struct Ring {
   static constexpr int kPieces = CH * (MODE == kBwd ? 2 : 1);  // of a row
@@ -562,26 +563,41 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH * 16 / (int)sizeof(
 }
 
 // dw from the blocks' sums, in a fixed order: 32 warps take every 32nd block each,
-// a lane a column.
+// a lane a column.  What an addition rounds off is kept beside the sum; in doubles, which
+// this GPU is slow at, the kernel took 6 us longer (backward of 2 x 8 x 4,093 fp32 rows
+// of 64 columns 17.7 us, 12.1 this way).
+struct Sum {
+  float s, rest;
+  __device__ __forceinline__ void add(float x) {
+    const float t = s + x, z = t - s;
+    rest += (s - (t - z)) + (x - z);
+    s = t;
+  }
+};
+
 constexpr int kDwThreads = 1024;
 __global__ void __launch_bounds__(kDwThreads) hca_norm_rope_dw_kernel(const float *part, int n, int D, float *dwq, float *dwkv) {
-  __shared__ double sum[32][33];
+  __shared__ Sum sum[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.y, d = blockIdx.x * 32 + lane;
   float *dw = which ? dwkv : dwq;
   tc::pdl_wait();
   if (!dw) return;
-  double v = 0;
+  Sum v = {0.f, 0.f};
   if (d < D) {
 #pragma unroll 8
-    for (int i = warp; i < n; i += 32) v += part[((size_t)i * 2 + which) * D + d];
+    for (int i = warp; i < n; i += 32) v.add(part[((size_t)i * 2 + which) * D + d]);
   }
   sum[warp][lane] = v;
   __syncthreads();
   // the 32 sums of column `warp` by the warp's lanes
   v = sum[lane][warp];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (lane == 0 && blockIdx.x * 32 + warp < D) dw[blockIdx.x * 32 + warp] = (float)v;
+  for (int o = 16; o > 0; o >>= 1) {
+    const float s = __shfl_xor_sync(0xffffffffu, v.s, o), rest = __shfl_xor_sync(0xffffffffu, v.rest, o);
+    v.add(s);
+    v.rest += rest;
+  }
+  if (lane == 0 && blockIdx.x * 32 + warp < D) dw[blockIdx.x * 32 + warp] = v.rest == v.rest ? v.s + v.rest : v.s;  // not of infinite sums
 }
 
 template <typename T, int L, int CH, int MODE, bool HALVES>
