@@ -33,7 +33,7 @@
 // to the first row: 2,571 prompt tokens (86 MB) 15.7 us; one token of 64 requests 4.5 us
 // in a graph, of which 2 are the launch.  Few heads are bound by instructions, since a
 // token's cos and sin and a lane's factors are for few rows: one head and kv of 524,288
-// tokens 251 us (540 MB, 80 us; 1,030 instructions of a warp for two rows of its lanes).
+// tokens 229 us (540 MB, 80 us; a thousand instructions of a warp for two rows a lane).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -344,7 +344,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH * 16 / (int)sizeof(
       cp_async_commit();
     };
 #pragma unroll 1
-    for (int n = 0; n < R::kStages; ++n) issue();
+    for (uint32_t n = 0; n < R::kStages; ++n) {
+      if (n < steps) issue();
+      else cp_async_commit();  // an empty group
+    }
 
     if (item == blockIdx.x) keep();
     if (s0 >= live) {
@@ -633,7 +636,12 @@ cudaError_t launch(Args &a, cudaStream_t st) {
   cudaError_t e = attr.ensure(reinterpret_cast<const void *>(kernel), kFixed + 38 * 1024);  // the most that the rest takes
   if (e != cudaSuccess) return e;
   uint32_t grid = a.tiles * a.splits;
-  if (MODE == kBwd) grid = std::min<uint32_t>(grid, std::min(kNormRopeParts, kPerSm * sms));
+  // Blocks that take item after item: backwards, since each leaves a part of dw, and
+  // where two of them fill an SM and have few rows a thread (forward of 540 MB of rows of
+  // 512 columns: one head 153 us, 197 with a block an item; 8 heads 88 and 92; 16 heads
+  // 97 and 85.  With four an SM and 128 columns one head 218 and 229, 8 heads 95 and 94).
+  const bool stay = MODE == kBwd || (kPerSm <= 2 && a.per <= 12 * pass);
+  if (stay) grid = std::min<uint32_t>(grid, std::min(kNormRopeParts, kPerSm * sms));
   ProfScope prof(MODE == kBwd ? kKNormRopeBwd : kKNormRope, st);
   kernel<<<grid, kThreads, smem, st>>>(a);
   e = cudaGetLastError();

@@ -239,6 +239,26 @@ def test_packed_tokens(add, held, H, D, rot, halves, pad, dtype):
         assert bool((t[n:] == 5).all())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("halves", [False, True])
+def test_wide_rows_of_few_heads(halves, dtype):
+    """More tiles of 8 tokens than blocks, which take several each."""
+    add, held = [1200, 0, 1701, 3], [70, 5, 0, 900000]
+    q, kv, start, h, freq, pos, w = serve_case(add, held, 2, 512, 64, dtype, 17, 300)
+    n = sum(add)
+    th = ON.angles(pos[None], freq.cpu().numpy())
+    qo, kvo = torch.full_like(q, 5), torch.full_like(kv, 5)
+    hca.hca_cache_norm_rope(q, kv, start, h, w, w, freq, EPS, halves=halves, qo=qo, kvo=kvo)
+    check_fwd(q[:n], w, th[:n, None], 448, halves, qo[:n], "q")
+    check_fwd(kv[:n], w, th[:n], 448, halves, kvo[:n], "kv")
+    assert bool((qo[n:] == 5).all()) and bool((kvo[n:] == 5).all())
+    q, kv, wq, wkv, pos, freq, _, _ = make(3, 1, 1111, 320, 32, dtype, 18)
+    th = ON.angles(pos.cpu().numpy(), freq.cpu().numpy())
+    qo, kvo = hca.hca_norm_rope_fwd(q, kv, wq, wkv, pos, freq, EPS, halves=halves)
+    check_fwd(q, wq, th[:, None], 288, halves, qo, "q")
+    check_fwd(kv, wkv, th, 288, halves, kvo, "kv")
+
+
 def test_packed_coordinates_and_strides():
     q, kv, start, held, freq, _, w = serve_case([4, 9], [3, 8], 5, 64, 32, BF16, 11, 2, axes=3)
     pos = torch.randint(0, 999, (3, 15), dtype=torch.int32).cuda()
