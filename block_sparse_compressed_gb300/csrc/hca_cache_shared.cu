@@ -773,6 +773,7 @@ struct OwnParts {
 // here too.
 template <int D, int U, bool Own>
 __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const SharedParams p) {
+  __shared__ Prefix prefix[kSharedMaxGroups];
   __shared__ OwnParts cut[kJoinThreads / (D / 4)];  // a block's rows have as many groups at most
   __shared__ int ncut;
   static_assert(!Own || U == 1, "a block's rows are adjacent");
@@ -788,6 +789,13 @@ __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const Shar
     for (int i = tid; i < p.own.grid; i += kJoinThreads) worst = max(worst, p.own.err[i] == HCA_ERR_TIMEOUT ? 1000 : p.own.err[i]);
   }
   for (int i = tid; i < p.grid; i += kJoinThreads) worst = max(worst, p.err[i] == HCA_ERR_TIMEOUT ? 1000 : p.err[i]);
+  bool alone = false;  // a prefix without common entries
+  static_assert(kSharedMaxGroups <= kJoinThreads, "a thread a prefix");
+  if (tid < p.own.G) {
+    prefix[tid] = table.g[tid];
+    alone = prefix[tid].tiles == 0 && prefix[tid].rows > 0;
+  }
+  alone = __syncthreads_or(alone);
   const bool late = __syncthreads_or(worst == 1000 || worst == HCA_ERR_TIMEOUT), wrong = __syncthreads_or(worst != HCA_OK);
   if (blockIdx.x == 0 && tid == 0) *p.status = late ? HCA_ERR_TIMEOUT : wrong ? HCA_ERR_CACHE : HCA_OK;
   const bool refused = units < 0 || own->ntiles < 0 || late;  // then all rows are NaN
@@ -800,16 +808,24 @@ __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const Shar
     return;
   }
   constexpr int kChunks = kRowTile / (kRows * U);  // of a row tile, a block's each
-  for (int item = blockIdx.x; item < row_tiles * kChunks; item += gridDim.x) {
+  // All row tiles, or where whole ones were finished by the CTA that had them those in
+  // which a CTA's range begins (the first that does) and those without common entries.
+  const int begins = p.merge ? p.grid * kChunks : 0;
+  const int items = begins + (!p.merge || alone ? row_tiles * kChunks : 0);
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int tile = (item < begins ? item : item - begins) / kChunks;
+    const long long u = (long long)tile * quota;
+    if (item < begins && u >= units) continue;
     int lo = 0, hi = p.own.G;  // the row tile's prefix
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (table.g[mid].rt0 <= item / kChunks) lo = mid; else hi = mid;
+      if (item < begins ? prefix[mid].line0 <= u : prefix[mid].rt0 <= tile) lo = mid; else hi = mid;
     }
-    const Prefix x = table.g[lo];
-    const int rt = item / kChunks - x.rt0, u0 = x.line0 + rt * x.span, first = u0 / quota;
+    const Prefix x = prefix[lo];
+    if (p.merge && item >= begins && x.tiles > 0) continue;
+    const int rt = item < begins ? ((int)u - x.line0) / x.span : tile - x.rt0, u0 = x.line0 + rt * x.span, first = u0 / quota;
+    if (item < begins && (u0 == u || u - quota > u0)) continue;
     const int parts = x.tiles > 0 ? (u0 + x.span - 1) / quota - first + 1 : 0;
-    if (p.merge && parts == 1) continue;  // finished by the CTA that had it
     const int r0 = item % kChunks * (kRows * U) + tid / kLanes;  // the lane's first row; the others are kRows apart
     if constexpr (Own) {
       // the groups among the block's rows that were cut
