@@ -30,10 +30,10 @@
 // (3.27 GB) 484 us, 99%.  (With a row's loads in its registers: 422 and 671 us; fp32
 // one by one instead of in pairs, and addresses by multiplication: 354 and 631.)
 // Shorter ones are bound by the blocks' beginnings, 2 us from the first instruction
-// to the first row: 2,571 prompt tokens (86 MB) 15.7 us; one token of 64 requests 4.5 us
+// to the first row: 2,571 prompt tokens (86 MB) 16 us; one token of 64 requests 4 us
 // in a graph, of which 2 are the launch.  Few heads are bound by instructions, since a
 // token's cos and sin and a lane's factors are for few rows: one head and kv of 524,288
-// tokens 229 us (540 MB, 80 us; a thousand instructions of a warp for two rows a lane).
+// tokens 223 us (540 MB, 80 us; a thousand instructions of a warp for two rows a lane).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -344,10 +344,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH * 16 / (int)sizeof(
       cp_async_commit();
     };
 #pragma unroll 1
-    for (uint32_t n = 0; n < R::kStages; ++n) {
-      if (n < steps) issue();
-      else cp_async_commit();  // an empty group
-    }
+    for (int n = 0; n < min((int)steps, R::kStages); ++n) issue();
+#pragma unroll
+    for (uint32_t n = 0; n < R::kStages; ++n)
+      if (n >= steps) cp_async_commit();  // empty groups
 
     if (item == blockIdx.x) keep();
     if (s0 >= live) {
