@@ -549,7 +549,7 @@ def hca_csa_attn_bwd(q, kv, ckv, seg, sel, out, lse, dout, W: int, m: int, scale
 # ---------------------------------------------------------------------------
 # norms and positions
 # ---------------------------------------------------------------------------
-def _rows(t: torch.Tensor, name: str, shape, dtype, device, written: bool = False):
+def _rows(t: torch.Tensor, name: str, shape, dtype, device):
     """Pointer and strides (elements; NULL where contiguous) of a tensor whose
     rows' columns are adjacent."""
     if t is None:
@@ -953,8 +953,8 @@ def hca_cache_norm_rope(q: Optional[torch.Tensor], kv: Optional[torch.Tensor], s
     [N] or [axes,N] int32 replaces the positions held[r], held[r] + 1, ...  Rows
     of the results from start[R] on are left as they are.  Returns (qo, kvo)."""
     lib = _lib or load()
-    r = _py and _py.norm_rope_fwd(q, kv, start, held, wq, wkv, pos, freq, eps, first, halves, qo, kvo)
-    if r is not None:
+    r = _py and start is not None and _py.norm_rope_fwd(q, kv, start, held, wq, wkv, pos, freq, eps, first, halves, qo, kvo)
+    if r:
         return _made(r, "hca_cache_norm_rope", False)
     t = q if q is not None else kv
     if t is None:
@@ -989,8 +989,8 @@ def hca_cache_rope(x: torch.Tensor, start: torch.Tensor, held: Optional[torch.Te
     """hca_rope for a serving step's packed tokens x[N,H,D] (arguments as
     hca_cache_norm_rope); y may be x."""
     lib = _lib or load()
-    r = _py and _py.rope(x, start, held, pos, freq, inverse, first, halves, y)
-    if r is not None:
+    r = _py and start is not None and _py.rope(x, start, held, pos, freq, inverse, first, halves, y)
+    if r:
         return _made(r, "hca_cache_rope", False)[0]
     if x.dim() != 3:
         raise ValueError("x must be [N,H,D]")

@@ -380,6 +380,10 @@ def test_the_binding_refuses():
     assert e.value.status == 7
     with pytest.raises(ValueError):
         hca.hca_cache_rope(q[0].transpose(0, 1), None, None, freq)
+    with pytest.raises(ValueError):  # a batch is not packed tokens
+        hca.hca_cache_rope(q, None, None, freq)
+    with pytest.raises(ValueError):
+        hca.hca_cache_norm_rope(q, kv, None, None, None, None, freq, EPS)
     with pytest.raises(ValueError):
         hca.hca_cache_norm_rope(q[0].transpose(0, 1), None, torch.zeros(2, dtype=torch.int32, device="cuda"), None, None, None, freq, EPS)
 
