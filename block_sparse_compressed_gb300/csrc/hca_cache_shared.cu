@@ -784,64 +784,87 @@ struct OwnParts {
   int parts;
 };
 
-// U rows of a lane at a time.  With `Own` the parts of the requests' own keys are joined
-// here too.
-template <int D, int U, bool Own>
-__global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const SharedParams p) {
-  __shared__ Prefix prefix[kSharedMaxGroups];
-  __shared__ OwnParts cut[kJoinThreads / (D / 4)];  // a block's rows have as many groups at most
-  __shared__ int ncut;
-  static_assert(!Own || U == 1, "a block's rows are adjacent");
+// Status, and the prefixes to shared memory; false: all rows are NaN.  `alone`: some
+// prefix has no common entries.  The block's threads together.
+template <int D, bool Own>
+__device__ __forceinline__ bool join_begin(const SharedParams &p, Prefix *prefix, bool &alone) {
   constexpr int kLanes = D / 4, kRows = kJoinThreads / kLanes;
-  constexpr float kLog2e = 1.4426950408889634f;
-  const int tid = threadIdx.x, l = tid % kLanes;
-  pdl_wait();
-  const Table &table = *p.table;
-  const int units = table.units, quota = table.quota, row_tiles = table.row_tiles;
+  static_assert(kSharedMaxGroups <= kJoinThreads, "a thread a prefix");
+  const int tid = threadIdx.x;
   const SchedHeader *own = p.own.hdr;
   int worst = Own ? HCA_OK : own->status;
   if constexpr (Own) {
     for (int i = tid; i < p.own.grid; i += kJoinThreads) worst = max(worst, p.own.err[i] == HCA_ERR_TIMEOUT ? 1000 : p.own.err[i]);
   }
   for (int i = tid; i < p.grid; i += kJoinThreads) worst = max(worst, p.err[i] == HCA_ERR_TIMEOUT ? 1000 : p.err[i]);
-  bool alone = false;  // a prefix without common entries
-  static_assert(kSharedMaxGroups <= kJoinThreads, "a thread a prefix");
+  alone = false;
   if (tid < p.own.G) {
-    prefix[tid] = table.g[tid];
+    prefix[tid] = p.table->g[tid];
     alone = prefix[tid].tiles == 0 && prefix[tid].rows > 0;
   }
   alone = __syncthreads_or(alone);
   const bool late = __syncthreads_or(worst == 1000 || worst == HCA_ERR_TIMEOUT), wrong = __syncthreads_or(worst != HCA_OK);
   if (blockIdx.x == 0 && tid == 0) *p.status = late ? HCA_ERR_TIMEOUT : wrong ? HCA_ERR_CACHE : HCA_OK;
-  const bool refused = units < 0 || own->ntiles < 0 || late;  // then all rows are NaN
-  if (refused) {
-    const size_t rows = (size_t)p.own.N * p.own.H;
-    for (size_t row = (size_t)blockIdx.x * kRows + tid / kLanes; row < rows; row += (size_t)gridDim.x * kRows) {
-      *reinterpret_cast<uint2 *>(p.out + row * D + 4 * l) = make_uint2(0x7fc07fc0u, 0x7fc07fc0u);
-      if (l == 0) p.lse[row] = __int_as_float(0x7fc00000);
-    }
-    return;
+  if (p.table->units >= 0 && own->ntiles >= 0 && !late) return true;
+  const size_t rows = (size_t)p.own.N * p.own.H;
+  const int l = tid % kLanes;
+  for (size_t row = (size_t)blockIdx.x * kRows + tid / kLanes; row < rows; row += (size_t)gridDim.x * kRows) {
+    *reinterpret_cast<uint2 *>(p.out + row * D + 4 * l) = make_uint2(0x7fc07fc0u, 0x7fc07fc0u);
+    if (l == 0) p.lse[row] = __int_as_float(0x7fc00000);
   }
-  constexpr int kChunks = kRowTile / (kRows * U);  // of a row tile, a block's each
-  // All row tiles, or where whole ones were finished by the CTA that had them those in
-  // which a CTA's range begins (the first that does) and those without common entries.
-  const int begins = p.merge ? p.grid * kChunks : 0;
-  const int items = begins + (!p.merge || alone ? row_tiles * kChunks : 0);
+  return false;
+}
+
+__device__ __forceinline__ void add(float4 &o, float w, const float4 &v) {
+  o.x = fmaf(w, v.x, o.x);
+  o.y = fmaf(w, v.y, o.y);
+  o.z = fmaf(w, v.z, o.z);
+  o.w = fmaf(w, v.w, o.w);
+}
+
+// Few rows, many parts: D / 4 lanes have a row, each lane looks at a part's reference and
+// sum, and the first parts' O are on their way meanwhile.  With `Own` the parts of the
+// requests' own keys are joined here too.  kBatch parts at a time: 8 where three blocks an
+// SM are all there are, else 4 and more blocks (calls of 64
+// heads, columns of 64 entries: 4 tokens over 512 27.2 us and 28.5, 64 tokens over 390 62.5
+// and 60.0; with the parts' references one after the other 30.6 and 60.4).
+template <int D, bool Own, int kBatch>
+__global__ void __launch_bounds__(kJoinThreads, kBatch == 8 ? 3 : 4) hca_cache_join_kernel(const SharedParams p) {
+  constexpr int kLanes = D / 4, kRows = kJoinThreads / kLanes, kOwnBatch = 4;
+  constexpr int kChunks = kRowTile / kRows;  // of a row tile, a block's each
+  constexpr float kLog2e = 1.4426950408889634f;
+  __shared__ Prefix prefix[kSharedMaxGroups];
+  __shared__ OwnParts cut[kRows];  // a block's rows have as many groups at most
+  __shared__ int ncut;
+  const int tid = threadIdx.x, l = tid % kLanes, lane0 = (tid & 31) & ~(kLanes - 1);
+  pdl_wait();
+  bool alone;
+  if (!join_begin<D, Own>(p, prefix, alone)) return;
+  const int quota = p.table->quota, items = p.table->row_tiles * kChunks;
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int tile = (item < begins ? item : item - begins) / kChunks;
-    const long long u = (long long)tile * quota;
-    if (item < begins && u >= units) continue;
     int lo = 0, hi = p.own.G;  // the row tile's prefix
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (item < begins ? prefix[mid].line0 <= u : prefix[mid].rt0 <= tile) lo = mid; else hi = mid;
+      if (prefix[mid].rt0 <= item / kChunks) lo = mid; else hi = mid;
     }
     const Prefix x = prefix[lo];
-    if (p.merge && item >= begins && x.tiles > 0) continue;
-    const int rt = item < begins ? ((int)u - x.line0) / x.span : tile - x.rt0, u0 = x.line0 + rt * x.span, first = u0 / quota;
-    if (item < begins && (u0 == u || u - quota > u0)) continue;
-    const int parts = x.tiles > 0 ? (u0 + x.span - 1) / quota - first + 1 : 0;
-    const int r0 = item % kChunks * (kRows * U) + tid / kLanes;  // the lane's first row; the others are kRows apart
+    const int rt = item / kChunks - x.rt0, u0 = x.line0 + rt * x.span, first = u0 / quota;
+    const int r0 = item % kChunks * kRows + tid / kLanes, r = rt * kRowTile + r0;  // of the tile, of the prefix
+    const size_t row = (size_t)x.row0 + r;
+    const bool there = r < x.rows;
+    const int n = there && x.tiles > 0 ? (u0 + x.span - 1) / quota - first + 1 : 0;  // parts
+    const size_t slot = (size_t)(x.rt0 + rt + first) * kRowTile + r0;               // the next part's is 256 further
+    const float *part = p.part_o + slot * D + 4 * l;
+    float4 v[kBatch];
+    auto load = [&](int i) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        v[k] = i + k < n ? *reinterpret_cast<const float4 *>(part + (size_t)(i + k) * kRowTile * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(0);
+    auto ml_of = [&](int i) { return i < n ? p.part_ml[slot + (size_t)i * kRowTile] : make_float2(-INFINITY, 0.f); };
+    const float2 ml0 = ml_of(l);
+    OwnParts mine = {0, 0, 0, 0, 0};
     if constexpr (Own) {
       // the groups among the block's rows that were cut
       const int a = x.row0 + rt * kRowTile + item % kChunks * kRows, e = min(a + kRows, x.row0 + x.rows);
@@ -853,93 +876,144 @@ __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_kernel(const Shar
         if (b.columns > 0 && b.row < e && b.row + b.columns > a) cut[atomicAdd(&ncut, 1)] = OwnParts{b.row, b.columns, b.slot, c, b.parts};
       }
       __syncthreads();
+      for (int i = 0; there && i < ncut; ++i)
+        if ((int)row >= cut[i].row && (int)row < cut[i].row + cut[i].columns) mine = cut[i];
     }
-    float4 o[U];
-    float lse[U];
-    size_t slot[U];
-    int n[U];  // parts; -1: no such row
-    OwnParts mine = {0, 0, 0, 0, 0};
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = rt * kRowTile + r0 + u * kRows;
-      n[u] = r < x.rows ? parts : -1;
-      slot[u] = (size_t)(x.rt0 + rt + first) * kRowTile + r0 + u * kRows;  // the next part's is 256 further
-      o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      lse[u] = 0.f;
-      if (n[u] >= 0) {
-        if constexpr (Own) {
-          for (int i = 0; i < ncut; ++i)
-            if (x.row0 + r >= cut[i].row && x.row0 + r < cut[i].row + cut[i].columns) mine = cut[i];
-        }
-        if (mine.parts == 0) {
-          o[u] = *reinterpret_cast<const float4 *>(p.own_out + (size_t)(x.row0 + r) * D + 4 * l);
-          lse[u] = p.own_lse[x.row0 + r];
-        }
-      }
+    const int m = mine.parts;  // 0: the row's own keys are in own_out
+    const bool whole = there && m == 0;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float lse = 0.f;
+    if (whole) {
+      o = *reinterpret_cast<const float4 *>(p.own_out + row * D + 4 * l);
+      lse = p.own_lse[row];
     }
-    // part i of the row's own keys: its reference, its sum, and what its O counts beside
-    // a reference of M
+    // part i of the row's own keys
     auto own_slot = [&](int i) { return i == 0 ? mine.slot0 : 2 * (mine.cta + i); };
-    auto own_ml = [&](int i) { return p.own.part_ml[(size_t)own_slot(i) * p.own.NQ + (x.row0 + rt * kRowTile + r0 - mine.row)]; };
-    int most = 0;
-    float M[U], sum[U];
+    auto own_at = [&](int i) { return (size_t)own_slot(i) * p.own.NQ + ((int)row - mine.row); };
+    auto own_ml_of = [&](int i) { return i < m ? p.own.part_ml[own_at(i)] : make_float2(-INFINITY, 0.f); };
+    // the greatest reference
+    float M = whole ? lse * kLog2e : -INFINITY;
+    for (int i = l; i < n; i += kLanes) M = fmaxf(M, i == l ? ml0.x : ml_of(i).x);
+    for (int i = l; i < m; i += kLanes) M = fmaxf(M, own_ml_of(i).x);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      most = max(most, n[u]);
-      M[u] = lse[u] * kLog2e;
-    }
-    if constexpr (Own) {
-      if (mine.parts > 0) M[0] = -INFINITY;
-      for (int i = 0; i < mine.parts; ++i) M[0] = fmaxf(M[0], own_ml(i).x);
-    }
-    for (int i = 0; i < most; ++i) {
+    for (int d = kLanes / 2; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    const float w0 = whole ? n > 0 ? exp2f(lse * kLog2e - M) : 1.f : 0.f;
+    o.x *= w0; o.y *= w0; o.z *= w0; o.w *= w0;
+    float sum = l == 0 ? w0 : 0.f;  // a lane's parts
+    // The rows of a warp may have different numbers of parts: its loops are the longest's.
+    const int most = __reduce_max_sync(0xffffffffu, n), own_most = Own ? __reduce_max_sync(0xffffffffu, m) : 0;
+    for (int c = 0; c < own_most; c += kLanes) {
+      const float2 ml = own_ml_of(c + l);
+      // O / l as the prefixes' parts have it: 2^unit / l is a normal number; l = 0: a part in which the row saw no key
+      const float w = ml.y != 0.f ? exp2f(ml.x - M) * ml.y : 0.f;
+      const float f = w != 0.f ? w * (exp2_int(p.own.part_unit[own_slot(c + l)]) / ml.y) : 0.f;
+      sum += w;
+#pragma unroll 1
+      for (int i = 0; i < min(kLanes, own_most - c); i += kOwnBatch) {
+        float fs[kOwnBatch];
+        float4 u[kOwnBatch];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i < n[u]) M[u] = fmaxf(M[u], p.part_ml[slot[u] + (size_t)i * kRowTile].x);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      sum[u] = mine.parts > 0 ? 0.f : n[u] > 0 ? exp2f(lse[u] * kLog2e - M[u]) : 1.f;
-      o[u].x *= sum[u]; o[u].y *= sum[u]; o[u].z *= sum[u]; o[u].w *= sum[u];
-    }
-    if constexpr (Own) {
-#pragma unroll 4
-      for (int i = 0; i < mine.parts; ++i) {
-        const float2 ml = own_ml(i);
-        const size_t at = (size_t)own_slot(i) * p.own.NQ + (x.row0 + rt * kRowTile + r0 - mine.row);
-        const float4 v = *reinterpret_cast<const float4 *>(p.own.part_o + at * D + 4 * l);
-        // O / l as the prefixes' parts have it: 2^unit / l is a normal number
-        const float w = exp2f(ml.x - M[0]), f = ml.y != 0.f ? w * ml.y * (exp2_int(p.own.part_unit[own_slot(i)]) / ml.y) : 0.f;
-        sum[0] += ml.y != 0.f ? w * ml.y : 0.f;  // 0: a part in which the row saw no key
-        if (f != 0.f) {
-          o[0].x = fmaf(f, v.x, o[0].x); o[0].y = fmaf(f, v.y, o[0].y);
-          o[0].z = fmaf(f, v.z, o[0].z); o[0].w = fmaf(f, v.w, o[0].w);
+        for (int k = 0; k < kOwnBatch; ++k) {
+          fs[k] = __shfl_sync(0xffffffffu, f, lane0 + i + k);
+          u[k] = fs[k] != 0.f ? *reinterpret_cast<const float4 *>(p.own.part_o + own_at(c + i + k) * D + 4 * l) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+#pragma unroll
+        for (int k = 0; k < kOwnBatch; ++k) add(o, fs[k], u[k]);
       }
     }
-#pragma unroll(U > 1 ? 1 : 4)
-    for (int i = 0; i < most; ++i) {
+    for (int c = 0; c < most; c += kLanes) {
+      const float2 ml = c == 0 ? ml0 : ml_of(c + l);
+      const float w = c + l < n ? exp2f(ml.x - M) * ml.y : 0.f;
+      sum += w;
+#pragma unroll 1
+      for (int i = 0; i < min(kLanes, most - c); i += kBatch) {
+        if (c + i > 0) load(c + i);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i < n[u]) {
-          const size_t at = slot[u] + (size_t)i * kRowTile;
-          const float2 ml = p.part_ml[at];
-          const float4 v = *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * l);
-          const float w = exp2f(ml.x - M[u]) * ml.y;
-          sum[u] += w;
-          o[u].x = fmaf(w, v.x, o[u].x); o[u].y = fmaf(w, v.y, o[u].y);
-          o[u].z = fmaf(w, v.z, o[u].z); o[u].w = fmaf(w, v.w, o[u].w);
-        }
+        for (int k = 0; k < kBatch; ++k) add(o, __shfl_sync(0xffffffffu, w, lane0 + i + k), v[k]);
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (n[u] < 0) continue;
-      const size_t row = (size_t)x.row0 + rt * kRowTile + r0 + u * kRows;
-      const bool joined = n[u] > 0 || mine.parts > 0;
-      const float inv = joined ? 1.f / sum[u] : 1.f;
-      *reinterpret_cast<uint2 *>(p.out + row * D + 4 * l) = make_uint2(pack_bf16x2(o[u].x * inv, o[u].y * inv), pack_bf16x2(o[u].z * inv, o[u].w * inv));
-      if (l == 0) p.lse[row] = joined ? (M[u] + log2f(sum[u])) * 0.69314718055994531f : lse[u];
+    for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (!there) continue;
+    const bool joined = n > 0 || m > 0;
+    const float inv = joined ? 1.f / sum : 1.f;
+    *reinterpret_cast<uint2 *>(p.out + row * D + 4 * l) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (l == 0) p.lse[row] = joined ? (M + log2f(sum)) * 0.69314718055994531f : lse;
+  }
+}
+
+// Many rows, of which whole row tiles were finished by the CTA that had them: those in
+// which a CTA's range begins (the first that does) and those without common entries.
+// A lane has U rows at a time, whose loads are in flight together.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) hca_cache_join_many_kernel(const SharedParams p) {
+  constexpr int U = 4, kLanes = D / 4, kRows = kJoinThreads / kLanes;
+  constexpr int kChunks = kRowTile / (kRows * U);  // of a row tile, a block's each
+  constexpr float kLog2e = 1.4426950408889634f;
+  __shared__ Prefix prefix[kSharedMaxGroups];
+  const int tid = threadIdx.x, l = tid % kLanes;
+  pdl_wait();
+  bool alone;
+  if (!join_begin<D, false>(p, prefix, alone)) return;
+  const int units = p.table->units, quota = p.table->quota;
+  const int begins = p.grid * kChunks, items = begins + (alone ? p.table->row_tiles * kChunks : 0);
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int tile = (item < begins ? item : item - begins) / kChunks;
+    const long long u = (long long)tile * quota;
+    if (item < begins && u >= units) continue;
+    int lo = 0, hi = p.own.G;  // the row tile's prefix
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (item < begins ? prefix[mid].line0 <= u : prefix[mid].rt0 <= tile) lo = mid; else hi = mid;
+    }
+    const Prefix x = prefix[lo];
+    if (item >= begins && x.tiles > 0) continue;
+    const int rt = item < begins ? ((int)u - x.line0) / x.span : tile - x.rt0, u0 = x.line0 + rt * x.span, first = u0 / quota;
+    if (item < begins && (u0 == u || u - quota > u0)) continue;
+    const int parts = x.tiles > 0 ? (u0 + x.span - 1) / quota - first + 1 : 0;
+    const int r0 = item % kChunks * (kRows * U) + tid / kLanes;  // the lane's first row; the others are kRows apart
+    float4 o[U];
+    float lse[U], M[U], sum[U];
+    size_t slot[U];
+    bool there[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int r = rt * kRowTile + r0 + i * kRows;
+      there[i] = r < x.rows;
+      slot[i] = (size_t)(x.rt0 + rt + first) * kRowTile + r0 + i * kRows;  // the next part's is 256 further
+      o[i] = there[i] ? *reinterpret_cast<const float4 *>(p.own_out + (size_t)(x.row0 + r) * D + 4 * l) : make_float4(0.f, 0.f, 0.f, 0.f);
+      lse[i] = there[i] ? p.own_lse[x.row0 + r] : 0.f;
+      M[i] = lse[i] * kLog2e;
+    }
+    for (int k = 0; k < parts; ++k) {
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (there[i]) M[i] = fmaxf(M[i], p.part_ml[slot[i] + (size_t)k * kRowTile].x);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      sum[i] = parts > 0 ? exp2f(lse[i] * kLog2e - M[i]) : 1.f;
+      o[i].x *= sum[i]; o[i].y *= sum[i]; o[i].z *= sum[i]; o[i].w *= sum[i];
+    }
+#pragma unroll 1
+    for (int k = 0; k < parts; ++k) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (!there[i]) continue;
+        const size_t at = slot[i] + (size_t)k * kRowTile;
+        const float2 ml = p.part_ml[at];
+        const float w = exp2f(ml.x - M[i]) * ml.y;
+        sum[i] += w;
+        add(o[i], w, *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * l));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (!there[i]) continue;
+      const size_t row = (size_t)x.row0 + rt * kRowTile + r0 + i * kRows;
+      const float inv = parts > 0 ? 1.f / sum[i] : 1.f;
+      *reinterpret_cast<uint2 *>(p.out + row * D + 4 * l) = make_uint2(pack_bf16x2(o[i].x * inv, o[i].y * inv), pack_bf16x2(o[i].z * inv, o[i].w * inv));
+      if (l == 0) p.lse[row] = parts > 0 ? (M[i] + log2f(sum[i])) * 0.69314718055994531f : lse[i];
     }
   }
 }
@@ -986,13 +1060,13 @@ cudaError_t launch(const CacheAttnArgs &a, SharedParams &p, int sms, cudaStream_
   if (e == cudaSuccess && p.merge) e = prefix();
   if (e != cudaSuccess) return e;
   ProfScope prof(kKCacheJoin, st);
-  // Many rows: 4 of them a lane, whose loads are in flight together.
   const bool many = p.merge;
   const long long per = (long long)kJoinThreads / (D / 4) * (many ? 4 : 1);
   const dim3 grid((unsigned)std::min<long long>((long long)p.own.N * p.own.H / per + p.own.G * (kRowTile / per), (many ? 3ll : 5ll) * sms));
-  if (many) return launch_behind(hca_cache_join_kernel<D, 4, false>, grid, kJoinThreads, 0, st, p);
-  if (p.own.joined) return launch_behind(hca_cache_join_kernel<D, 1, true>, grid, kJoinThreads, 0, st, p);
-  return launch_behind(hca_cache_join_kernel<D, 1, false>, grid, kJoinThreads, 0, st, p);
+  if (many) return launch_behind(hca_cache_join_many_kernel<D>, grid, kJoinThreads, 0, st, p);
+  if (p.own.joined && (int)grid.x <= 3 * sms) return launch_behind(hca_cache_join_kernel<D, true, 8>, grid, kJoinThreads, 0, st, p);
+  if (p.own.joined) return launch_behind(hca_cache_join_kernel<D, true, 4>, grid, kJoinThreads, 0, st, p);
+  return launch_behind(hca_cache_join_kernel<D, false, 4>, grid, kJoinThreads, 0, st, p);
 }
 
 }  // namespace
