@@ -141,11 +141,11 @@ __device__ __forceinline__ void make_table(const SharedParams &p, Table &t, long
     }
     int quota = max((int)(((ok ? units : 0) + ctas - 1) / ctas), 1);
     if (ok) {
-      // a part more costs the join about a sixteenth of a unit
+      // a part more costs the join about an eighth of a unit
       int longest = 0;
       for (int g = lane; g < p.own.G; g += 32) longest = max(longest, t.g[g].tiles);
       longest = __reduce_max_sync(0xffffffffu, longest);
-      quota = max(quota, (int)sqrtf((float)longest * (1.f / 16.f)));
+      quota = max(quota, (int)sqrtf((float)longest * (1.f / 8.f)));
     }
     bool pad = false;
     if (ok && nrt <= ctas) {  // else there are more row tiles than CTAs
@@ -822,21 +822,25 @@ __device__ __forceinline__ void add(float4 &o, float w, const float4 &v) {
   o.w = fmaf(w, v.w, o.w);
 }
 
-// Few rows, many parts: D / 4 lanes have a row, each lane looks at a part's reference and
-// sum, and the first parts' O are on their way meanwhile.  With `Own` the parts of the
-// requests' own keys are joined here too.  kBatch parts at a time: 8 where three blocks an
-// SM are all there are, else 4 and more blocks (calls of 64
-// heads, columns of 64 entries: 4 tokens over 512 27.2 us and 28.5, 64 tokens over 390 62.5
-// and 60.0; with the parts' references one after the other 30.6 and 60.4).
-template <int D, bool Own, int kBatch>
+// Few rows, many parts: a row has S groups of D / 4 lanes, each of which has every S-th
+// part.  A lane looks at a part's reference and sum, and the first parts' O are on their way
+// meanwhile.  With `Own` the parts of the requests' own keys are joined here too.  kBatch
+// parts at a time: 8 where three blocks an SM are all there are, else 4 and more blocks
+// (calls of 64 heads, columns of 64 entries: 4 tokens over 512 27.2 us and 28.5, 64 tokens
+// over 390 62.5 and 60.0; with the parts' references one after the other 30.6 and 60.4).
+// S is 4 where that many blocks run at once: 8 tokens of 8 heads over 65,536 entries 28.9
+// us, 33.9 with 1 (25.6 since a CTA takes 8 steps at least).
+template <int D, bool Own, int kBatch, int S>
 __global__ void __launch_bounds__(kJoinThreads, kBatch == 8 ? 3 : 4) hca_cache_join_kernel(const SharedParams p) {
-  constexpr int kLanes = D / 4, kRows = kJoinThreads / kLanes, kOwnBatch = 4;
+  constexpr int kLanes = D / 4, kRows = kJoinThreads / kLanes / S, kOwnBatch = 4;
   constexpr int kChunks = kRowTile / kRows;  // of a row tile, a block's each
   constexpr float kLog2e = 1.4426950408889634f;
   __shared__ Prefix prefix[kSharedMaxGroups];
   __shared__ OwnParts cut[kRows];  // a block's rows have as many groups at most
   __shared__ int ncut;
-  const int tid = threadIdx.x, l = tid % kLanes, lane0 = (tid & 31) & ~(kLanes - 1);
+  __shared__ float4 group_o[S > 1 ? kJoinThreads : 1];
+  __shared__ float2 group_ml[S > 1 ? kJoinThreads / kLanes : 1];
+  const int tid = threadIdx.x, l = tid % kLanes, lane0 = (tid & 31) & ~(kLanes - 1), group = tid / kLanes, h = group / kRows;
   pdl_wait();
   bool alone;
   if (!join_begin<D, Own>(p, prefix, alone)) return;
@@ -849,20 +853,21 @@ __global__ void __launch_bounds__(kJoinThreads, kBatch == 8 ? 3 : 4) hca_cache_j
     }
     const Prefix x = prefix[lo];
     const int rt = item / kChunks - x.rt0, u0 = x.line0 + rt * x.span, first = u0 / quota;
-    const int r0 = item % kChunks * kRows + tid / kLanes, r = rt * kRowTile + r0;  // of the tile, of the prefix
+    const int r0 = item % kChunks * kRows + group % kRows, r = rt * kRowTile + r0;  // of the tile, of the prefix
     const size_t row = (size_t)x.row0 + r;
     const bool there = r < x.rows;
-    const int n = there && x.tiles > 0 ? (u0 + x.span - 1) / quota - first + 1 : 0;  // parts
-    const size_t slot = (size_t)(x.rt0 + rt + first) * kRowTile + r0;               // the next part's is 256 further
+    const int parts = there && x.tiles > 0 ? (u0 + x.span - 1) / quota - first + 1 : 0;
+    const int n = (parts - h + S - 1) / S;                                          // of the group: h, h + S, ...
+    const size_t slot = (size_t)(x.rt0 + rt + first + h) * kRowTile + r0, step = S * kRowTile;  // of them, from one to the next
     const float *part = p.part_o + slot * D + 4 * l;
     float4 v[kBatch];
     auto load = [&](int i) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
-        v[k] = i + k < n ? *reinterpret_cast<const float4 *>(part + (size_t)(i + k) * kRowTile * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[k] = i + k < n ? *reinterpret_cast<const float4 *>(part + (i + k) * step * D) : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     load(0);
-    auto ml_of = [&](int i) { return i < n ? p.part_ml[slot + (size_t)i * kRowTile] : make_float2(-INFINITY, 0.f); };
+    auto ml_of = [&](int i) { return i < n ? p.part_ml[slot + i * step] : make_float2(-INFINITY, 0.f); };
     const float2 ml0 = ml_of(l);
     OwnParts mine = {0, 0, 0, 0, 0};
     if constexpr (Own) {
@@ -879,25 +884,25 @@ __global__ void __launch_bounds__(kJoinThreads, kBatch == 8 ? 3 : 4) hca_cache_j
       for (int i = 0; there && i < ncut; ++i)
         if ((int)row >= cut[i].row && (int)row < cut[i].row + cut[i].columns) mine = cut[i];
     }
-    const int m = mine.parts;  // 0: the row's own keys are in own_out
-    const bool whole = there && m == 0;
+    const bool joined = parts > 0 || mine.parts > 0;
+    const int m = h == S - 1 ? mine.parts : 0;                      // parts of the row's own keys: the last group's
+    const bool whole = there && h == S - 1 && mine.parts == 0;  // these are in own_out
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float lse = 0.f;
     if (whole) {
       o = *reinterpret_cast<const float4 *>(p.own_out + row * D + 4 * l);
       lse = p.own_lse[row];
     }
-    // part i of the row's own keys
     auto own_slot = [&](int i) { return i == 0 ? mine.slot0 : 2 * (mine.cta + i); };
     auto own_at = [&](int i) { return (size_t)own_slot(i) * p.own.NQ + ((int)row - mine.row); };
     auto own_ml_of = [&](int i) { return i < m ? p.own.part_ml[own_at(i)] : make_float2(-INFINITY, 0.f); };
-    // the greatest reference
+    // the group's greatest reference
     float M = whole ? lse * kLog2e : -INFINITY;
     for (int i = l; i < n; i += kLanes) M = fmaxf(M, i == l ? ml0.x : ml_of(i).x);
     for (int i = l; i < m; i += kLanes) M = fmaxf(M, own_ml_of(i).x);
 #pragma unroll
     for (int d = kLanes / 2; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    const float w0 = whole ? n > 0 ? exp2f(lse * kLog2e - M) : 1.f : 0.f;
+    const float w0 = whole ? joined ? exp2f(lse * kLog2e - M) : 1.f : 0.f;
     o.x *= w0; o.y *= w0; o.z *= w0; o.w *= w0;
     float sum = l == 0 ? w0 : 0.f;  // a lane's parts
     // The rows of a warp may have different numbers of parts: its loops are the longest's.
@@ -934,8 +939,28 @@ __global__ void __launch_bounds__(kJoinThreads, kBatch == 8 ? 3 : 4) hca_cache_j
     }
 #pragma unroll
     for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (!there) continue;
-    const bool joined = n > 0 || m > 0;
+    if constexpr (S > 1) {
+      // the row's groups
+      group_o[tid] = o;
+      if (l == 0) group_ml[group] = make_float2(M, sum);
+      __syncthreads();
+      if (h == S - 1) {
+        const int of = group % kRows;
+        for (int i = 0; i < S - 1; ++i) M = fmaxf(M, group_ml[of + i * kRows].x);
+        float2 ml = group_ml[group];
+        const float f = joined ? exp2f(ml.x - M) : 1.f;
+        sum = f * ml.y;
+        o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+        for (int i = 0; i < S - 1; ++i) {
+          ml = group_ml[of + i * kRows];
+          const float w = ml.x > -INFINITY ? exp2f(ml.x - M) : 0.f;  // no part: not minus infinity less itself
+          sum = fmaf(w, ml.y, sum);
+          add(o, w, group_o[(of + i * kRows) * kLanes + l]);
+        }
+      }
+      __syncthreads();
+    }
+    if (!there || h != S - 1) continue;
     const float inv = joined ? 1.f / sum : 1.f;
     *reinterpret_cast<uint2 *>(p.out + row * D + 4 * l) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     if (l == 0) p.lse[row] = joined ? (M + log2f(sum)) * 0.69314718055994531f : lse;
@@ -1060,13 +1085,17 @@ cudaError_t launch(const CacheAttnArgs &a, SharedParams &p, int sms, cudaStream_
   if (e == cudaSuccess && p.merge) e = prefix();
   if (e != cudaSuccess) return e;
   ProfScope prof(kKCacheJoin, st);
-  const bool many = p.merge;
-  const long long per = (long long)kJoinThreads / (D / 4) * (many ? 4 : 1);
-  const dim3 grid((unsigned)std::min<long long>((long long)p.own.N * p.own.H / per + p.own.G * (kRowTile / per), (many ? 3ll : 5ll) * sms));
-  if (many) return launch_behind(hca_cache_join_many_kernel<D>, grid, kJoinThreads, 0, st, p);
-  if (p.own.joined && (int)grid.x <= 3 * sms) return launch_behind(hca_cache_join_kernel<D, true, 8>, grid, kJoinThreads, 0, st, p);
-  if (p.own.joined) return launch_behind(hca_cache_join_kernel<D, true, 4>, grid, kJoinThreads, 0, st, p);
-  return launch_behind(hca_cache_join_kernel<D, false, 4>, grid, kJoinThreads, 0, st, p);
+  auto join = [&](auto *kernel, long long rows, long long most) {  // of a block, blocks
+    const long long blocks = (long long)p.own.N * p.own.H / rows + p.own.G * (kRowTile / rows);
+    return launch_behind(kernel, dim3((unsigned)std::min(blocks, most)), kJoinThreads, 0, st, p);
+  };
+  constexpr int kRows = kJoinThreads / (D / 4);
+  if (p.merge) return join(hca_cache_join_many_kernel<D>, 4 * kRows, 3 * sms);
+  if (!p.own.joined) return join(hca_cache_join_kernel<D, false, 4, 1>, kRows, 5 * sms);
+  const long long blocks = (long long)p.own.N * p.own.H / kRows;
+  if (4 * blocks <= 3 * sms) return join(hca_cache_join_kernel<D, true, 8, 4>, kRows / 4, 3 * sms);
+  if (blocks <= 3 * sms) return join(hca_cache_join_kernel<D, true, 8, 1>, kRows, 3 * sms);
+  return join(hca_cache_join_kernel<D, true, 4, 1>, kRows, 5 * sms);
 }
 
 }  // namespace
@@ -1083,18 +1112,21 @@ namespace {
 // how many rows there are and how many key tiles the compressed tables hold at most.
 // In us, with `groups` of rows that share key tiles where nothing else is shared, of
 // 128 rows or fewer, on 152 SMs:
-//   by itself  21 + groups (tiles + 6) / 304 * 1.7 (2.0 for groups of 128 rows)
-//   apart      30 + row tiles * tiles / 152 * 1.5 + groups * 8 / 152 * 1.2
-// Measured (64 heads, D = 128, by themselves | apart): 64 tokens over 8 tiles 21 | 28,
-// 64 tiles 47 | 40, 512 tiles 203 | 108; 16 tokens over 256 tiles 45 | 45, 512 tiles 69 |
-// 56; 4 tokens over 512 tiles 37 | 56; 200 tokens over 16 tiles 45 | 47, 256 tiles 305 |
-// 167; 8 heads, 64 tokens over 32 tiles 32 | 31, 512 tiles 201 | 49; 314 prompt tokens
-// over 32 tiles 66 | 74, 256 tiles 293 | 234.
+//   by itself  19 + groups (tiles + 6) / 304 * 1.7 (2.0 for groups of 128 rows) + what the
+//              parts of a group take to join
+//   apart      22 + steps of a CTA * 1.5 + groups * 8 / 152 * 1.2 + rows to join
+// Measured (64 heads, D = 128, by themselves | apart): 64 tokens over 8 tiles 23 | 28,
+// 64 tiles 47 | 39, 512 tiles 202 | 106; 16 tokens over 128 tiles 34 | 33, 512 tiles 69 |
+// 48; 4 tokens over 64 tiles 22 | 26, 512 tiles 37 | 32; 1 token over 256 tiles 26 | 26, 512
+// 36 | 30; 200 tokens over 16 tiles 45 | 49, 256 tiles 305 | 173; 8 heads, 64 tokens over 16
+// tiles 26 | 27, 512 tiles 201 | 39; 314 prompt tokens over 32 tiles 66 | 76, 256 tiles
+// 292 | 238.
 bool apart_pays(const CacheAttnArgs &a, int sms) {
-  const double groups = (double)cache_attn_groups(a.N, a.R, a.H, a.D, a.dtype), tiles = std::min((double)a.comp.cols * a.bs / kTileKeys, 8388608.0);
-  const double rows = (double)a.N * a.H, full = rows >= 100.0 * groups ? 2.0 : 1.7;
-  const double alone = 21 + groups * (tiles + 6) / (2.0 * sms) * full;
-  const double apart = 30 + std::ceil(rows / kRowTile) * tiles / sms * 1.5 + groups * 8 / sms * 1.2;
+  const double groups = std::max(1.0, (double)cache_attn_groups(a.N, a.R, a.H, a.D, a.dtype));
+  const double rows = (double)a.N * a.H, full = rows >= 100.0 * groups ? 2.0 : 1.7, tiles = std::min((double)a.comp.cols * a.bs / kTileKeys, 8388608.0);
+  const double alone = 19 + groups * (tiles + 6) / (2.0 * sms) * full + 0.08 * std::min(tiles / 2, 2.0 * sms / groups);
+  const double steps = std::max(std::ceil(rows / kRowTile) * tiles / sms, std::sqrt(tiles / 8));
+  const double apart = 22 + steps * 1.5 + groups * 8 / sms * 1.2 + rows * 0.0007;
   return apart < alone;
 }
 

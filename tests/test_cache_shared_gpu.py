@@ -325,6 +325,20 @@ def test_few_rows_over_a_long_prefix():
     check_attn(call(case, first, cols, 16, 1), *case, 16, 1, scale_of(64), BF16)
 
 
+def test_more_parts_than_lanes():
+    """The prefix in 65 parts and a request's own keys in more than 16, which the join's lanes
+    take in turns."""
+    case, first, cols = shared_case([(2, 520)], [6000, 3], [1, 2], 8, 64, 16, 1, 128, BF16, 26)
+    check_attn(call(case, first, cols, 16, 1), *case, 16, 1, scale_of(64), BF16)
+
+
+@pytest.mark.parametrize("H,D,added", [(64, 128, [70, 61]), (96, 64, [70, 61]), (64, 128, [31, 20]), (20, 128, [31, 20])])
+def test_numbers_of_rows_between(H, D, added):
+    """Joins of their own launch, of some and of few rows."""
+    case, first, cols = shared_case([(2, 37)], [9, 500], added, H, D, 40, 1, 16, BF16, 27)
+    check_attn(call(case, first, cols, 40, 1), *case, 40, 1, scale_of(D), BF16)
+
+
 def test_both_ways_of_the_binding_give_the_same(monkeypatch):
     case, first, cols = shared_case([(2, 3), (1, 2)], [4, 7, 9], [1, 2, 1], 8, 64, 16, 4, 16, BF16, 24)
     a = call(case, first, cols, 16, 4)
