@@ -233,6 +233,32 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const P p) 
   volatile int *abort_flag = &sh.abort;
   int32_t *status = &p.err[blockIdx.x];
 
+  if (warp == 10) {
+    tmem_alloc(&sh.tmem_base, kTmem);
+    // early: an SM's next CTA begins when this one has let go (its schedule first: 64
+    // tokens of 8 heads over 16,384 common entries 33.5 us, 30.7 so)
+    tmem_relinquish();
+  }
+  int grid = p.grid;
+  if constexpr (P::kShared) {
+    if (p.beside) {
+      // Only some SMs are free: CTAs without a range make way, else the last of them begin
+      // their schedule when the prefixes' kernel has ended (16 tokens of 64 heads over
+      // 16,384 common entries 33.2 us, 29.3 so).
+      grid = own_grid(p, sh.scan);
+      if ((int)blockIdx.x >= grid) {
+        if (tid == 0) {
+          *status = HCA_OK;
+          p.border[blockIdx.x] = Border{0, 0, 0, 0};
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == 10) tmem_dealloc(sh.tmem_base, kTmem);
+        return;
+      }
+    }
+  }
   if (tid == 0) {
 #pragma unroll 1
     for (int s = 0; s < kMetaStages; ++s) {
@@ -257,17 +283,12 @@ __global__ void __launch_bounds__(kThreads, 2) hca_cache_attn_kernel(const P p) 
     sh.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 10) {
-    tmem_alloc(&sh.tmem_base, kTmem);
-    tmem_relinquish();
-  }
   // the CTA's range of the line, and its pieces of groups
   int ntiles, quota, c0 = 0, c1 = 0;
   bool busy = false;
   if (p.in_cta) {
     // one thread per request; where some bring more than one group, one per group
     int n = 0, r = tid, k = 0;
-    const int grid = own_grid(p, sh.scan);
     bool ok = prefixes_ok(p);
     if (tid < p.R) ok = request_chunks(p, tid, n) && ok;
     bool mine = n == 1;
