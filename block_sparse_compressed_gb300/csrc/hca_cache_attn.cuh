@@ -1,6 +1,8 @@
 // hca_cache_attn.cuh -- parameters of the attention-over-cache kernels.
 #pragma once
 
+#include <climits>
+
 #include "hca_cache.cuh"
 
 namespace hca {
@@ -201,12 +203,8 @@ __device__ __forceinline__ int prefix_sms(const SharedAttnParams &p, long long u
     const float t = fmaxf(a, b);
     if (t < best) best = t, at = s;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float t = __shfl_xor_sync(0xffffffffu, best, o);
-    const int s = __shfl_xor_sync(0xffffffffu, at, o);
-    if (t < best || (t == best && s < at)) best = t, at = s;
-  }
+  const uint32_t least = __reduce_min_sync(0xffffffffu, __float_as_uint(best));  // positive floats are in order
+  at = __reduce_min_sync(0xffffffffu, __float_as_uint(best) == least ? at : INT_MAX);
   return p.sms - at;
 }
 

@@ -149,12 +149,20 @@ __device__ __forceinline__ void make_table(const SharedParams &p, Table &t, long
     }
     bool pad = false;
     if (ok && nrt <= ctas) {  // else there are more row tiles than CTAs
-      for (int k = 0; k < kPadded && !pad; ++k) {
-        long long pieces = 0;
-        for (int g = lane; g < p.own.G; g += 32) pieces += (t.g[g].rows + kRowTile - 1) / kRowTile * ((t.g[g].tiles + quota + k - 1) / (quota + k));
-        pad = warp_sum(pieces) <= ctas;
-        if (pad) quota += k;
+      int pieces[kPadded] = {};
+      for (int g = lane; g < p.own.G; g += 32) {
+        const int n = (t.g[g].rows + kRowTile - 1) / kRowTile;  // at most kMaxGrid
+#pragma unroll
+        for (int k = 0; k < kPadded; ++k) pieces[k] += n * min((t.g[g].tiles + quota + k - 1) / (quota + k), kMaxGrid + 1);
       }
+#pragma unroll
+      for (int k = kPadded - 1; k >= 0; --k) pieces[k] = __reduce_add_sync(0xffffffffu, pieces[k]);
+      int more = kPadded;  // the least that fits
+#pragma unroll
+      for (int k = kPadded - 1; k >= 0; --k)
+        if (pieces[k] <= ctas) more = k;
+      pad = more < kPadded;
+      if (pad) quota += more;
     }
     int line = 0, rt = 0;
     for (int g0 = 0; ok && g0 < p.own.G; g0 += 32) {
