@@ -792,35 +792,51 @@ struct OwnParts {
   int parts;
 };
 
-// Status, and the prefixes to shared memory; false: all rows are NaN.  `alone`: some
-// prefix has no common entries.  The block's threads together.
+// What a join's block begins with.  All is loaded at once, and the block meets once.
+struct JoinBegin {
+  int units, quota, row_tiles;
+  bool alone;    // some prefix has no common entries
+  bool refused;  // then all rows are NaN, and written
+};
+
 template <int D, bool Own>
-__device__ __forceinline__ bool join_begin(const SharedParams &p, Prefix *prefix, bool &alone) {
+__device__ __forceinline__ JoinBegin join_begin(const SharedParams &p, Prefix *prefix) {
   constexpr int kLanes = D / 4, kRows = kJoinThreads / kLanes;
+  constexpr uint32_t kLate = 1, kWrong = 2, kAlone = 4;
   static_assert(kSharedMaxGroups <= kJoinThreads, "a thread a prefix");
+  __shared__ uint32_t seen[kJoinThreads / 32];
   const int tid = threadIdx.x;
-  const SchedHeader *own = p.own.hdr;
-  int worst = Own ? HCA_OK : own->status;
+  JoinBegin t = {p.table->units, p.table->quota, p.table->row_tiles, false, false};
+  const int own_tiles = p.own.hdr->ntiles;
+  uint32_t flags = 0;
+  auto look = [&](int status) { flags |= status == HCA_ERR_TIMEOUT ? kLate | kWrong : status != HCA_OK ? kWrong : 0; };
   if constexpr (Own) {
-    for (int i = tid; i < p.own.grid; i += kJoinThreads) worst = max(worst, p.own.err[i] == HCA_ERR_TIMEOUT ? 1000 : p.own.err[i]);
+    for (int i = tid; i < p.own.grid; i += kJoinThreads) look(p.own.err[i]);
+  } else {
+    look(p.own.hdr->status);
   }
-  for (int i = tid; i < p.grid; i += kJoinThreads) worst = max(worst, p.err[i] == HCA_ERR_TIMEOUT ? 1000 : p.err[i]);
-  alone = false;
+  for (int i = tid; i < p.grid; i += kJoinThreads) look(p.err[i]);
   if (tid < p.own.G) {
     prefix[tid] = p.table->g[tid];
-    alone = prefix[tid].tiles == 0 && prefix[tid].rows > 0;
+    if (prefix[tid].tiles == 0 && prefix[tid].rows > 0) flags |= kAlone;
   }
-  alone = __syncthreads_or(alone);
-  const bool late = __syncthreads_or(worst == 1000 || worst == HCA_ERR_TIMEOUT), wrong = __syncthreads_or(worst != HCA_OK);
-  if (blockIdx.x == 0 && tid == 0) *p.status = late ? HCA_ERR_TIMEOUT : wrong ? HCA_ERR_CACHE : HCA_OK;
-  if (p.table->units >= 0 && own->ntiles >= 0 && !late) return true;
-  const size_t rows = (size_t)p.own.N * p.own.H;
-  const int l = tid % kLanes;
-  for (size_t row = (size_t)blockIdx.x * kRows + tid / kLanes; row < rows; row += (size_t)gridDim.x * kRows) {
-    *reinterpret_cast<uint2 *>(p.out + row * D + 4 * l) = make_uint2(0x7fc07fc0u, 0x7fc07fc0u);
-    if (l == 0) p.lse[row] = __int_as_float(0x7fc00000);
+  flags = __reduce_or_sync(0xffffffffu, flags);
+  if ((tid & 31) == 0) seen[tid >> 5] = flags;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kJoinThreads / 32; ++i) flags |= seen[i];
+  if (blockIdx.x == 0 && tid == 0) *p.status = flags & kLate ? HCA_ERR_TIMEOUT : flags & kWrong ? HCA_ERR_CACHE : HCA_OK;
+  t.alone = flags & kAlone;
+  t.refused = t.units < 0 || own_tiles < 0 || (flags & kLate);
+  if (t.refused) {
+    const size_t rows = (size_t)p.own.N * p.own.H;
+    const int l = tid % kLanes;
+    for (size_t row = (size_t)blockIdx.x * kRows + tid / kLanes; row < rows; row += (size_t)gridDim.x * kRows) {
+      *reinterpret_cast<uint2 *>(p.out + row * D + 4 * l) = make_uint2(0x7fc07fc0u, 0x7fc07fc0u);
+      if (l == 0) p.lse[row] = __int_as_float(0x7fc00000);
+    }
   }
-  return false;
+  return t;
 }
 
 __device__ __forceinline__ void add(float4 &o, float w, const float4 &v) {
@@ -850,9 +866,9 @@ __global__ void __launch_bounds__(kJoinThreads, kBatch == 8 ? 3 : 4) hca_cache_j
   __shared__ float2 group_ml[S > 1 ? kJoinThreads / kLanes : 1];
   const int tid = threadIdx.x, l = tid % kLanes, lane0 = (tid & 31) & ~(kLanes - 1), group = tid / kLanes, h = group / kRows;
   pdl_wait();
-  bool alone;
-  if (!join_begin<D, Own>(p, prefix, alone)) return;
-  const int quota = p.table->quota, items = p.table->row_tiles * kChunks;
+  const JoinBegin t = join_begin<D, Own>(p, prefix);
+  if (t.refused) return;
+  const int quota = t.quota, items = t.row_tiles * kChunks;
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     int lo = 0, hi = p.own.G;  // the row tile's prefix
     while (hi - lo > 1) {
@@ -986,10 +1002,10 @@ __global__ void __launch_bounds__(kJoinThreads) hca_cache_join_many_kernel(const
   __shared__ Prefix prefix[kSharedMaxGroups];
   const int tid = threadIdx.x, l = tid % kLanes;
   pdl_wait();
-  bool alone;
-  if (!join_begin<D, false>(p, prefix, alone)) return;
-  const int units = p.table->units, quota = p.table->quota;
-  const int begins = p.grid * kChunks, items = begins + (alone ? p.table->row_tiles * kChunks : 0);
+  const JoinBegin t = join_begin<D, false>(p, prefix);
+  if (t.refused) return;
+  const int units = t.units, quota = t.quota;
+  const int begins = p.grid * kChunks, items = begins + (t.alone ? t.row_tiles * kChunks : 0);
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     const int tile = (item < begins ? item : item - begins) / kChunks;
     const long long u = (long long)tile * quota;
