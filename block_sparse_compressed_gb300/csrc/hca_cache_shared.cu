@@ -866,6 +866,16 @@ __global__ void __launch_bounds__(kJoinThreads, kBatch == 8 ? 3 : 4) hca_cache_j
   __shared__ float2 group_ml[S > 1 ? kJoinThreads / kLanes : 1];
   const int tid = threadIdx.x, l = tid % kLanes, lane0 = (tid & 31) & ~(kLanes - 1), group = tid / kLanes, h = group / kRows;
   pdl_wait();
+  Border border[2];  // of two of the own keys' CTAs, of which there are 2 kMaxGrid at most
+  if constexpr (Own) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      border[i] = Border{0, 0, 0, 0};
+      if (tid + i * kJoinThreads < p.own.grid) border[i] = p.own.border[tid + i * kJoinThreads];
+    }
+    if (tid == 0) ncut = 0;
+  }
+  static_assert(kMaxGrid <= kJoinThreads, "a thread has the borders of two CTAs");
   const JoinBegin t = join_begin<D, Own>(p, prefix);
   if (t.refused) return;
   const int quota = t.quota, items = t.row_tiles * kChunks;
@@ -897,16 +907,20 @@ __global__ void __launch_bounds__(kJoinThreads, kBatch == 8 ? 3 : 4) hca_cache_j
     if constexpr (Own) {
       // the groups among the block's rows that were cut
       const int a = x.row0 + rt * kRowTile + item % kChunks * kRows, e = min(a + kRows, x.row0 + x.rows);
-      __syncthreads();
-      if (tid == 0) ncut = 0;
-      __syncthreads();
-      for (int c = tid; c < p.own.grid; c += kJoinThreads) {
-        const Border b = p.own.border[c];
-        if (b.columns > 0 && b.row < e && b.row + b.columns > a) cut[atomicAdd(&ncut, 1)] = OwnParts{b.row, b.columns, b.slot, c, b.parts};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const Border b = border[i];
+        if (b.columns > 0 && b.row < e && b.row + b.columns > a)
+          cut[atomicAdd(&ncut, 1)] = OwnParts{b.row, b.columns, b.slot, tid + i * kJoinThreads, b.parts};
       }
       __syncthreads();
       for (int i = 0; there && i < ncut; ++i)
         if ((int)row >= cut[i].row && (int)row < cut[i].row + cut[i].columns) mine = cut[i];
+      if (item + (int)gridDim.x < items) {
+        __syncthreads();
+        if (tid == 0) ncut = 0;
+        __syncthreads();
+      }
     }
     const bool joined = parts > 0 || mine.parts > 0;
     const int m = h == S - 1 ? mine.parts : 0;                      // parts of the row's own keys: the last group's
