@@ -34,9 +34,10 @@
 // 1.62 PFLOP/s, 83% of the measured rate of a plain product; tensor pipe 70% active, 2.07
 // instructions a cycle.  A step of 256 rows x 128 keys takes 1.57 us: 64-key scores are
 // bound by shared memory (48 cycles a product where the pipe needs 32), and a half's
-// score -> softmax -> output has three hand-overs.  Beside it the requests' own keys 118 us and the
-// join 26: 659 us in all, 764 without sharing.  4,096 rows over 24,960 entries, 16 row tiles
-// in 152 ranges: 60 us, 94 without sharing; 35 are steps.
+// score -> softmax -> output has three hand-overs.  Beside it the requests' own keys 118 us
+// and the join 25: 657 us in all, 764 without sharing.  4,096 rows over 24,960 entries, 16
+// row tiles in 128 ranges: 58 us, 94 without sharing; 40 are steps, 8 the beginning (table,
+// scales, first keys), 3 the way out, 7 the join.
 //   Slower (each against the kernel of its time): S of 128 keys at once 646 to 686 us, 585
 // in halves; q in tensor memory 768 for 646; pages by bulk copies and converted from
 // shared memory 585 for 567; products issued by warps that wait together 562 for 555; the
@@ -780,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
 // join: out = (w_0 o_0 + sum 2^(m_i - M) l_i o_i) / (w_0 + sum 2^(m_i - M) l_i) of a
 // row's own keys (w_0 = 2^(lse - M)) and the parts of its prefix.  Bound by latency: table,
 // references, parts, one after the other.  Of 643 row tiles 151 were cut in the case above:
-// 26 us, 33 when the blocks looked at all tiles.
+// 25 us, 33 when the blocks looked at all tiles.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
@@ -1154,11 +1155,11 @@ namespace {
 //              parts of a group take to join
 //   apart      22 + steps of a CTA * 1.5 + groups * 8 / 152 * 1.2 + rows to join
 // Measured (64 heads, D = 128, by themselves | apart): 64 tokens over 8 tiles 23 | 28,
-// 64 tiles 47 | 39, 512 tiles 202 | 106; 16 tokens over 128 tiles 34 | 33, 512 tiles 69 |
-// 48; 4 tokens over 64 tiles 22 | 26, 512 tiles 37 | 32; 1 token over 256 tiles 26 | 26, 512
-// 36 | 30; 200 tokens over 16 tiles 45 | 49, 256 tiles 305 | 173; 8 heads, 64 tokens over 16
-// tiles 26 | 27, 512 tiles 201 | 39; 314 prompt tokens over 32 tiles 66 | 76, 256 tiles
-// 292 | 238.
+// 64 tiles 47 | 38, 512 tiles 203 | 105; 16 tokens over 64 tiles 26 | 27, 512 tiles 69 |
+// 44; 4 tokens over 64 tiles 22 | 25, 512 tiles 37 | 32; 1 token over 128 tiles 21 | 24, 512
+// 36 | 29; 200 tokens over 16 tiles 45 | 48, 256 tiles 305 | 167; 8 heads, 64 tokens over 16
+// tiles 25 | 27, 512 tiles 197 | 35; 314 prompt tokens over 32 tiles 66 | 73, 256 tiles
+// 293 | 237.
 bool apart_pays(const CacheAttnArgs &a, int sms) {
   const double groups = std::max(1.0, (double)cache_attn_groups(a.N, a.R, a.H, a.D, a.dtype));
   const double rows = (double)a.N * a.H, full = rows >= 100.0 * groups ? 2.0 : 1.7, tiles = std::min((double)a.comp.cols * a.bs / kTileKeys, 8388608.0);
