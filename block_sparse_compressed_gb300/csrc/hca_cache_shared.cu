@@ -508,15 +508,17 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
         last = s.last;
         tiles += s.j1 - s.j0;
       }
-      // Piece i of a tile, from memory (zero where there is no page).
+      // Piece i of a tile, from memory (zero where there is no page).  When a wait has
+      // given up the tile's pages may never have been looked up: nothing is read then.
+      bool ok = true;
       auto piece = [&](const TileMeta &meta, int i, uint4 &w) {
         const int row = row0 + i * kRowStep, page = row >> p.own.log_bs;
-        const uint8_t *rows = meta.rows[page];
+        const uint8_t *rows = ok ? meta.rows[page] : nullptr;
         w = make_uint4(0, 0, 0, 0);
         if (rows) w = *reinterpret_cast<const uint4 *>(rows + (row - (page << p.own.log_bs)) * D + ch * 16);
       };
       uint4 raw[kPer];
-      (void)wait_bar(&sh.meta_full[0], 0);
+      ok = wait_bar(&sh.meta_full[0], 0);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) piece(sh.meta[0], i, raw[i]);
       // no way out when a wait has given up: the softmax goes on too
@@ -524,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) hca_cache_prefix_kernel(const Sha
       for (uint32_t n = 0; n < tiles; ++n) {
         const TileMeta &meta = sh.meta[n % kMetaStages], &next = sh.meta[(n + 1) % kMetaStages];
         const uint32_t st = n % kKvStages, dst = to0 + st * C::kStageBytes;
-        if (n + 1 < tiles) (void)wait_bar(&sh.meta_full[(n + 1) % kMetaStages], ((n + 1) / kMetaStages) & 1);
+        if (n + 1 < tiles) ok = wait_bar(&sh.meta_full[(n + 1) % kMetaStages], ((n + 1) / kMetaStages) & 1) && ok;
         if (n >= (uint32_t)kKvStages) (void)wait_bar(&sh.kv_empty[st], ((n / kKvStages) - 1) & 1);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {

@@ -368,3 +368,25 @@ def test_a_stalled_wait_times_out():
         hca.hca_test_inject(hca.INJECT_RESET)
         hca.hca_test_inject(hca.INJECT_SHARED_PATH, 1)
     check_attn(call(case, first, cols, 16, 1, ws=ws), *case, 16, 1, scale_of(128), BF16)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("tokens", [100, 200])
+@pytest.mark.parametrize("limit", [1, 5000])
+def test_waits_that_give_up_before_the_first_pages(limit, tokens, D):
+    """A CTA's part of the prefix is some 2,700 pages, whose scales are all looked at before
+    the first page is handed on: the waits for it end first.  100 and 200 tokens of 2 requests:
+    beside the own keys, and behind them."""
+    case, first, cols = shared_case([(2, 4096)], [1, 2], [tokens, tokens], 128, D, 16, 1, 16, BF16, 28)
+    args = tuple(t.to(DEV) for t in case[:3]) + (dev(case[3]), dev(case[4]), first, cols, 16, 1, scale_of(D))
+    ws = torch.empty(hca.load().hca_cache_attn_shared_workspace_size(2 * tokens, 2, 128, D, 1, 0), dtype=torch.uint8, device=DEV)
+    want = hca.hca_cache_attn_shared(*args, ws=ws, check=True)
+    try:
+        hca.hca_test_inject(hca.INJECT_WAIT_LIMIT_NS, limit)
+        out, lse = hca.hca_cache_attn_shared(*args, ws=ws)
+        assert hca.hca_workspace_status(ws) == 10
+        assert bool(out.isnan().all()) and bool(lse.isnan().all())
+    finally:
+        hca.hca_test_inject(hca.INJECT_WAIT_LIMIT_NS, 0)
+    again = hca.hca_cache_attn_shared(*args, ws=ws, check=True)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
