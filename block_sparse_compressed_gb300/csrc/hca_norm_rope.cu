@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH * 16 / (int)sizeof(
     const bool alive = s < live;
     if (tid < a.axes * a.tile) sh_pos[tid] = coordinate;
     __syncthreads();  // and sh_cs is read no more
-    if (a.start && !a.pos) {
+    if (a.start && !a.pos && a.held) {  // without held nothing turns
       if (tid < a.tile) {
         const int t = s0 + tid, r = request_of(listed ? sh_req : a.start, a.R, t);
         sh_pos[tid] = listed ? (long long)sh_req[a.R + 1 + r] + t - sh_req[r] : (long long)a.held[r] + t - a.start[r];

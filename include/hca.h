@@ -257,8 +257,8 @@ HCA_API int hca_compress_bwd(const void *x, const float *g, const float *bias, c
  *          are [N,H,D] and [N,D] with N = S; token start[r] + t of request r
  *          (device int32 [R+1], [R], ascending) is at position held[r] + t unless
  *          pos says otherwise, and rows from start[R] on are left as they are.
- *          held may be NULL where pos is given.  Values out of order give
- *          positions that mean nothing; no row outside [0, N) is touched.
+ *          held may be NULL where pos is given or rot is 0.  Values out of order
+ *          give positions that mean nothing; no row outside [0, N) is touched.
  *   dtype  of x and of the results; w, freq and dw are fp32, and so is all
  *          arithmetic, rounded once at the end.  Squares are summed in fp32:
  *          |x| below 2^60, and above 2^-60 somewhere in a row where eps is 0.  A

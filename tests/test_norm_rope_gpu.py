@@ -1,4 +1,6 @@
 """Norms with positions and the rotation alone against the fp64 oracle."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -433,3 +435,22 @@ def test_threads_that_call_at_once():
     for t in threads:
         t.join()
     assert not bad
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("R", [1, 1024, 1025, 3000])
+def test_packed_norms_that_do_not_turn_need_no_lengths(R, dtype):
+    """The C call takes held = NULL where rot is 0, for any number of requests."""
+    q, kv, start, _, _, _, w = serve_case([1, 2, 0][:R] + [1] * (R - 3), [0] * R, 2, 64, 16, dtype, 20, pad=3)
+    n, N = int(start[-1]), q.shape[0]
+    qo, kvo, y = torch.full_like(q, 5), torch.full_like(kv, 5), torch.full_like(q, 5)
+    lib, code, st = hca.load(), 1 if dtype == F32 else 0, torch.cuda.current_stream().cuda_stream
+    assert lib.hca_norm_rope_fwd(q.data_ptr(), (ctypes.c_int64 * 3)(0, 64, 128), w.data_ptr(), qo.data_ptr(), kv.data_ptr(), None, None,
+                                 kvo.data_ptr(), None, None, start.data_ptr(), None, 1, 2, N, 64, R, 1, 0, 0, 0, EPS, code, st) == 0
+    assert lib.hca_rope(q.data_ptr(), None, y.data_ptr(), None, None, None, start.data_ptr(), None, 1, 2, N, 64, R, 1, 0, 0, 0, 0, code, st) == 0
+    th = np.zeros((n, 0))
+    check_fwd(q[:n], w, th[:, None], 0, False, qo[:n], "q")
+    check_fwd(kv[:n], None, th, 0, False, kvo[:n], "kv")
+    assert torch.equal(y[:n], q[:n])
+    for t in (qo, kvo, y):
+        assert bool((t[n:] == 5).all())
