@@ -1149,9 +1149,10 @@ size_t cache_attn_shared_ws_bytes(int N, int R, int H, int D, int G, int dtype) 
 
 namespace {
 
-// Is it worth attending the common entries apart?  Of the lengths the host knows
-// how many rows there are and how many key tiles the compressed tables hold at most.
-// In us, with `groups` of rows that share key tiles where nothing else is shared, of
+// Is it worth attending the common entries apart?  Of the lengths the host knows how many
+// rows and prefixes there are and how many key tiles the compressed tables hold at most:
+// it takes that for the common length, and the rows for shared out evenly among the
+// prefixes, whose row tiles are their own.  In us, with `groups` of rows that share key tiles where nothing else is shared, of
 // 128 rows or fewer, on 152 SMs:
 //   by itself  19 + groups (tiles + 6) / 304 * 1.7 (2.0 for groups of 128 rows) + what the
 //              parts of a group take to join
@@ -1161,12 +1162,17 @@ namespace {
 // 44; 4 tokens over 64 tiles 22 | 25, 512 tiles 37 | 32; 1 token over 128 tiles 21 | 24, 512
 // 36 | 29; 200 tokens over 16 tiles 45 | 48, 256 tiles 305 | 167; 8 heads, 64 tokens over 16
 // tiles 25 | 27, 512 tiles 197 | 35; 314 prompt tokens over 32 tiles 66 | 73, 256 tiles
-// 293 | 237.
+// 293 | 237.  As many prefixes, 64 heads, 64 tokens over 132 tiles: 16 prefixes 70 | 47, 64
+// prefixes 71 | 117; 64 over 516 tiles 209 | 347.  D = 64: 64 tokens over 28 tiles 26 | 29, 68
+// tiles 39 | 32; 64 prefixes over 68 tiles 39 | 65.  Of 264 calls (1 to 541 tokens of 1 to
+// 200 prefixes, 8 to 128 heads, both D, 12 to 516 tiles) the rule took the slower way in 7
+// by 5% or more, the worst by 21% (541 tokens of 6 prefixes over 132 tiles 267 | 323).
 bool apart_pays(const CacheAttnArgs &a, int sms) {
   const double groups = std::max(1.0, (double)cache_attn_groups(a.N, a.R, a.H, a.D, a.dtype));
   const double rows = (double)a.N * a.H, full = rows >= 100.0 * groups ? 2.0 : 1.7, tiles = std::min((double)a.comp.cols * a.bs / kTileKeys, 8388608.0);
   const double alone = 19 + groups * (tiles + 6) / (2.0 * sms) * full + 0.08 * std::min(tiles / 2, 2.0 * sms / groups);
-  const double steps = std::max(std::ceil(rows / kRowTile) * tiles / sms, std::sqrt(tiles / 8));
+  const double prefixes = std::max(1, std::min({a.share.G, a.R, a.N}));
+  const double steps = std::max(prefixes * std::ceil(rows / (kRowTile * prefixes)) * tiles / sms, std::sqrt(tiles / 8));
   const double apart = 22 + steps * 1.5 + groups * 8 / sms * 1.2 + rows * 0.0007;
   return apart < alone;
 }

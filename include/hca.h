@@ -446,8 +446,12 @@ HCA_API int hca_cache_attn(const void *q, const int32_t *start, const int32_t *h
  * of first and shared_cols that do not fit make all N rows of out and lse NaN, as lengths out of
  * range do (HCA_ERR_CACHE).  bf16: a prefix's part is rounded to fp32 and joined
  * with the request's own; fp32 has the same arithmetic as hca_cache_attn.
- * A call whose requests are few, or whose compressed tables are narrow, does what
- * hca_cache_attn does, which is then faster.
+ * A call whose requests are few, whose compressed tables are narrow, or whose
+ * prefixes have few rows each, does what hca_cache_attn does, which is then faster.
+ * The host picks by N, R, H, G and the tables' width, since the lengths are on the
+ * device: it takes the width for the common length.  Wide tables of requests that
+ * have little or nothing in common are better given to hca_cache_attn, and requests
+ * without common blocks to one prefix of 0 columns.
  * Workspace: hca_cache_attn_shared_workspace_size bytes (0: unsupported sizes). */
 HCA_API size_t hca_cache_attn_shared_workspace_size(int N, int R, int H, int D, int G, int dtype);
 HCA_API int hca_cache_attn_shared(const void *q, const int32_t *start, const int32_t *held, const void *raw_pool,

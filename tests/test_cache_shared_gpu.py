@@ -390,3 +390,17 @@ def test_waits_that_give_up_before_the_first_pages(limit, tokens, D):
         hca.hca_test_inject(hca.INJECT_WAIT_LIMIT_NS, 0)
     again = hca.hca_cache_attn_shared(*args, ws=ws, check=True)
     assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+@pytest.mark.parametrize("prefixes,launches", [([(1, 512)] * 40, 0), ([(10, 512)] * 4, 1)])
+def test_the_way_is_picked_by_the_prefixes(prefixes, launches, apart):
+    """40 tokens over 64 key tiles: one row tile each where every request has a prefix of its
+    own, which is slower apart (55 us for 30), and a row tile for every ten of them."""
+    apart(0)
+    hca.hca_profile_enable(True)
+    try:
+        case, first, cols = shared_case(prefixes, [0] * 40, [1] * 40, 8, 64, 16, 1, 16, BF16, 29)
+        check_attn(call(case, first, cols, 16, 1), *case, 16, 1, scale_of(64), BF16)
+        assert hca.hca_profile_read().get("hca_cache_prefix", (0,))[0] == launches
+    finally:
+        hca.hca_profile_enable(False)
