@@ -119,8 +119,13 @@ __device__ __forceinline__ void make_table(const SharedParams &p, Table &t, long
       ok = ok && fine;
       int r = 0;
       if (fine) {
+        // the first that has tokens: the last one that begins where the prefix does
         r = p.own.first[g];
-        while (r + 1 < p.own.first[g + 1] && p.own.start[r + 1] <= p.own.start[r]) ++r;
+        const int s0 = p.own.start[r];
+        for (int end = p.own.first[g + 1]; end - r > 1;) {
+          const int mid = (r + end) >> 1;
+          if (p.own.start[mid] <= s0) r = mid; else end = mid;
+        }
       }
       t.g[g] = Prefix{z.row0, z.rows, z.tiles, fine ? p.own.cols[g] : 0, z.tiles, 0, 0, r};
       units += (long long)z.row_tiles() * z.tiles;

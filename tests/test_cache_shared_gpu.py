@@ -404,3 +404,26 @@ def test_the_way_is_picked_by_the_prefixes(prefixes, launches, apart):
         assert hca.hca_profile_read().get("hca_cache_prefix", (0,))[0] == launches
     finally:
         hca.hca_profile_enable(False)
+
+
+def test_many_places_that_are_not_taken():
+    """20,000 requests without tokens in front of a prefix's others take no longer than behind
+    them (21 us): one after the other a load for each is 1.2 ms."""
+    case, first, cols = shared_case([(4, 40)], [0, 3, 40, 9], [1, 2, 1, 1], 16, 64, 16, 1, 16, BF16, 30)
+    q, start, held, raw, comp = case
+    n = 20000
+    none = torch.zeros(n, dtype=torch.int32)
+    times = []
+    for front in (False, True):
+        join = lambda a, b: torch.cat([b, a] if front else [a, b])  # noqa: E731
+        big = (q, join(start, none if front else none + start[-1]), join(held, none),
+               *((c[0], c[1], join(c[2], torch.full((n, c[2].shape[1]), -1, dtype=torch.int32))) for c in (raw, comp)))
+        for _ in range(2):
+            hca.hca_profile_enable(True)
+            try:
+                got = call(big, i32([0, n + 4]), cols, 16, 1)
+                times.append(hca.hca_profile_read()["hca_cache_prefix"][1])
+            finally:
+                hca.hca_profile_enable(False)
+        check_attn(got, *case, 16, 1, scale_of(64), BF16)
+    assert times[3] < 5 * times[1], times
