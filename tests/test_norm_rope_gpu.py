@@ -454,3 +454,23 @@ def test_packed_norms_that_do_not_turn_need_no_lengths(R, dtype):
     assert torch.equal(y[:n], q[:n])
     for t in (qo, kvo, y):
         assert bool((t[n:] == 5).all())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 2.0 ** 64, -3e38])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D,rot,halves,axes,at", [(64, 64, False, 1, 0), (64, 32, True, 2, 31), (512, 512, False, 4, 1023), (512, 256, True, 4, 300)])
+def test_frequencies_without_an_angle(D, rot, halves, axes, at, dtype, bad):
+    """All columns that turn are NaN then, at position 0 too; the others stay as they are."""
+    q, kv, wq, wkv, pos, freq, dq, dkv = make(2, 3, 37, D, rot, dtype, 21, axes=axes)
+    pos[:, 0, :5] = 0
+    calls = lambda: hca.hca_norm_rope_fwd(q, kv, wq, wkv, pos, freq, EPS, halves=halves) + (  # noqa: E731
+        hca.hca_rope(q, pos, freq, halves=halves, inverse=True),)
+    want, back = calls(), hca.hca_norm_rope_bwd(q, kv, wq, wkv, pos, freq, EPS, dq, dkv, halves=halves)
+    freq.view(-1)[at] = bad
+    first = D - rot
+    for a, b in zip(calls(), want):
+        assert bool(a[..., first:].isnan().all()) and torch.equal(a[..., :first], b[..., :first])
+    gq, gkv, gwq, gwkv = hca.hca_norm_rope_bwd(q, kv, wq, wkv, pos, freq, EPS, dq, dkv, halves=halves)
+    assert bool(gq.isnan().all()) and bool(gkv.isnan().all())  # a row's mean has them all
+    for a, b in ((gwq, back[2]), (gwkv, back[3])):
+        assert bool(a[first:].isnan().all()) and torch.equal(a[:first], b[:first])
