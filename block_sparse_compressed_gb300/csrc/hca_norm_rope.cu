@@ -209,6 +209,17 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// A sum in fp32 with what its additions round off beside it (this GPU is slow at doubles).
+struct Sum {
+  float s, rest;
+  __device__ __forceinline__ void add(float x) {
+    const float t = s + x, z = t - s;
+    rest += (s - (t - z)) + (x - z);
+    s = t;
+  }
+  __device__ __forceinline__ float value() const { return rest == rest ? s + rest : s; }  // rest: NaN of infinite sums
+};
+
 // CH chunks of a row a lane, chunks l, l + L, ... for lane l of the row's L: the lanes
 // of an access are neighbours in memory (with 8 columns of fp32 side by side a lane
 // each 32-byte sector went over the way to L2 in two halves: backward of 2 x 8 x 4,093
@@ -439,14 +450,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH * 16 / (int)sizeof(
           other[k][i] = pair(p[0], p[1]);
           w[k][i] = pair(wt[V::column(i, 0)], wt[V::column(i, 1)]);
         }
-        if constexpr (MODE == kBwd) {
 #pragma unroll
-          for (int i = 0; i < kF4; ++i) {
-            const float4 v = sh_dw[((which * CH + k) * kF4 + i) * kThreads + tid];
-            dw[k][2 * i] = pair(v.x, v.y);
-            dw[k][2 * i + 1] = pair(v.z, v.w);
-          }
-        }
+        for (int i = 0; i < kSlots; ++i) dw[k][i] = 0;
       }
       // own f + other f of the partner, for a row's slots
       auto rotate = [&](const V (&v)[CH], const uint64_t (&f)[CH][kSlots], uint64_t (&o)[CH][kSlots]) {
@@ -547,10 +552,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH * 16 / (int)sizeof(
         for (int k = 0; k < CH; ++k) {
 #pragma unroll
           for (int i = 0; i < kF4; ++i) {
-            float4 v;
+            float4 &to = sh_dw[((which * CH + k) * kF4 + i) * kThreads + tid], v;
             tc::f32x2_split(dw[k][2 * i], v.x, v.y);
             tc::f32x2_split(dw[k][2 * i + 1], v.z, v.w);
-            sh_dw[((which * CH + k) * kF4 + i) * kThreads + tid] = v;
+            to = make_float4(to.x + v.x, to.y + v.y, to.z + v.z, to.w + v.w);
           }
         }
       }
@@ -559,7 +564,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH * 16 / (int)sizeof(
   }
 
   if constexpr (MODE == kBwd) {
-    // sums of the block's rows: over its row groups, in their order
+    // sums of the block's rows: over its row groups, in their order.  (A thread adds up an
+    // item's rows, then the items': one long sum loses a bit for every doubling.)
     __syncthreads();
     for (int i = tid; i < 2 * a.D; i += kThreads) {
       const int which = i / a.D, d = i - which * a.D, chunk = d / kCols, c = d % kCols;
@@ -569,27 +575,17 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(CH * 16 / (int)sizeof(
       for (int j = 0; j < kCols; ++j)
         if (V::column(j >> 1, j & 1) == c) slot = j;
       const float *from = reinterpret_cast<const float *>(sh_dw + (size_t)((which * CH + chunk / L) * kF4 + (slot >> 2)) * kThreads + chunk % L) + (slot & 3);
-      float v = 0.f;
+      Sum v = {0.f, 0.f};
 #pragma unroll 8
-      for (int r = 0; r < kRows; ++r) v += from[4 * r * L];
-      a.part[((size_t)blockIdx.x * 2 + which) * a.D + d] = v;
+      for (int r = 0; r < kRows; ++r) v.add(from[4 * r * L]);
+      a.part[((size_t)blockIdx.x * 2 + which) * a.D + d] = v.value();
     }
   }
 }
 
 // dw from the blocks' sums, in a fixed order: 32 warps take every 32nd block each,
-// a lane a column.  What an addition rounds off is kept beside the sum; in doubles, which
-// this GPU is slow at, the kernel took 6 us longer (backward of 2 x 8 x 4,093 fp32 rows
-// of 64 columns 17.7 us, 12.1 this way).
-struct Sum {
-  float s, rest;
-  __device__ __forceinline__ void add(float x) {
-    const float t = s + x, z = t - s;
-    rest += (s - (t - z)) + (x - z);
-    s = t;
-  }
-};
-
+// a lane a column.  (In doubles 6 us longer: backward of 2 x 8 x 4,093 fp32 rows of 64
+// columns 17.7 us, 12.1 this way.)
 constexpr int kDwThreads = 1024;
 __global__ void __launch_bounds__(kDwThreads) hca_norm_rope_dw_kernel(const float *part, int n, int D, float *dwq, float *dwkv) {
   __shared__ Sum sum[32][33];
@@ -612,7 +608,7 @@ __global__ void __launch_bounds__(kDwThreads) hca_norm_rope_dw_kernel(const floa
     v.add(s);
     v.rest += rest;
   }
-  if (lane == 0 && blockIdx.x * 32 + warp < D) dw[blockIdx.x * 32 + warp] = v.rest == v.rest ? v.s + v.rest : v.s;  // not of infinite sums
+  if (lane == 0 && blockIdx.x * 32 + warp < D) dw[blockIdx.x * 32 + warp] = v.value();
 }
 
 template <typename T, int L, int CH, int MODE, bool HALVES>

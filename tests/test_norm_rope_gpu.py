@@ -474,3 +474,18 @@ def test_frequencies_without_an_angle(D, rot, halves, axes, at, dtype, bad):
     assert bool(gq.isnan().all()) and bool(gkv.isnan().all())  # a row's mean has them all
     for a, b in ((gwq, back[2]), (gwkv, back[3])):
         assert bool(a[first:].isnan().all()) and torch.equal(a[:first], b[:first])
+
+
+def test_dw_of_a_long_sequence_keeps_its_bits():
+    """8.4e6 equal terms in each column, c x r with x = r = 1.  A thread adds up its rows of a
+    tile of tokens (a head each), then its tiles, of which a block has S / 32 / SMs at most, as a
+    block has 32 rows of 8 columns at once: each of these additions is off by 2^-24 of a sum of
+    positive terms at most.  The sums over a block's rows and over blocks carry what they round
+    off: 2 each, and 2 for r.  (In one sum over all rows of a thread: 133 units in column 0.)"""
+    H, S, D = 32, 262144, 8
+    c = torch.tensor([1.1, 0.7654321, 1.7, 1.2345678, 1.3333334, 1.0000001, 0.9, 1.9])
+    x, g = torch.ones(1, H, S, D, device="cuda"), c.cuda().expand(1, H, S, D).contiguous()
+    dw = hca.hca_norm_rope_bwd(x, None, torch.ones(D, device="cuda"), None, None, torch.zeros(0, device="cuda"), 0.0, g, None)[2]
+    units = H + -(-S // 32 // torch.cuda.get_device_properties(0).multi_processor_count) + 6
+    ref = c.double() * H * S
+    assert bool(((dw.cpu().double() - ref).abs() <= units * 2.0 ** -24 * ref).all()), (dw.cpu().double() / ref - 1) * 2 ** 24
