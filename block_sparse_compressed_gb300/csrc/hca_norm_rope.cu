@@ -15,9 +15,9 @@
 // fp32 keeps a sixteenth.  So a frequency becomes a 64-bit fraction of a turn
 // per unit, F = f / 2pi * 2^64 mod 2^64 (exact to 2^-64 turns),
 // and a phase is sum_a c_a F[a] in integers, where the wrap-around of 64 bits is
-// the reduction to one turn: off by 2^-33 turns at most for any 32-bit
+// the reduction to one turn: off by 2^-33 turns an axis at most for any 32-bit
 // coordinates.  The two upper bits (rounded) are the quadrant, the rest is an eighth
-// of a turn at most.
+// of a turn at most; cos and sin are right to 3 2^-24.
 //
 // A row belongs to L neighbouring lanes in chunks of 16 bytes, so it is read once,
 // stays in registers between the sum of its squares and its output, and is written

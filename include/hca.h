@@ -250,7 +250,7 @@ HCA_API int hca_compress_bwd(const void *x, const float *g, const float *bias, c
  * rot) stay as they are.  Pair p is columns first + 2p and first + 2p + 1, or
  * with `halves` first + p and first + p + rot/2.
  *   freq   [axes,rot/2] fp32 (device), radians per unit, below 2^32 in
- *          magnitude; angles are right to 2^-24 for any coordinates.  With
+ *          magnitude; cos and sin are right to 3 2^-24 for any coordinates.  With
  *          one that is NaN, infinite or 2^64 and more all columns that turn are NaN.
  *   pos    [axes,B,S] int32 (device): the coordinates.  NULL (axes = 1): 0, 1,
  *          ... S - 1 in every batch row, or those of start and held

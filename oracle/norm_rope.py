@@ -56,8 +56,17 @@ def backward(x, w, eps, theta, first, halves, g):
 
 # ---------------------------------------------------------------------------
 # bounds of the fp32 arithmetic, elementwise.  A unit is 2^-24, the rounding of an
-# fp32 operation.  cos and sin: the angle as a fraction of a turn within an eighth
-# is rounded once (2^-25 of pi/4), sincospif is within 2 units of 1: 3 units.
+# fp32 operation.  cos and sin, 3 units:
+#   the phase, in turns: a frequency is cut off below 2^-64, so each of up to four axes
+#   is off by 2^-33, and what is left of a quarter turn is cut off below 2^-34: together
+#   0.06 units of radians;
+#   the rest in radians, pi/4 at most: rounded to fp32, times 2 pi 2^-34 as an fp32 number
+#   (off by 0.47 units) and rounded: 2.47 pi/4 = 1.94 units, 2 with the phase's.  Of that
+#   sin(pi/4) reaches cos, 1.42 units, and 2.47 x cos x + 0.06 sin, 1.43;
+#   the series end at x^8 and x^9: x^10/10! = 0.41 units, x^11/11! = 0.03;
+#   their evaluation: the last addition 0.5 (results from 0.5 to 1), and before it x^2,
+#   the inner sum and for sin x^3, 0.48 units for cos and 0.26 for sin:
+#   cos 2.81, sin 2.22.
 # r: the sum of D squares D units at most, halved by the root, and 3 for the root
 # itself.  A result u cos - v sin: r's and two roundings of u and v, 3 of cos and
 # sin and 2 of the sum: D/2 + 10 units of |u| + |v|.

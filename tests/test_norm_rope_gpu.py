@@ -489,3 +489,21 @@ def test_dw_of_a_long_sequence_keeps_its_bits():
     units = H + -(-S // 32 // torch.cuda.get_device_properties(0).multi_processor_count) + 6
     ref = c.double() * H * S
     assert bool(((dw.cpu().double() - ref).abs() <= units * 2.0 ** -24 * ref).all()), (dw.cpu().double() / ref - 1) * 2 ** 24
+
+
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("axes", [2, 3, 4])
+def test_far_coordinates_of_several_axes(axes, halves):
+    """Each axis at the ends of 32 bits, with frequencies up to the stated 2^32: what is cut off
+    adds up over the axes."""
+    g = torch.Generator().manual_seed(22)
+    ends = torch.tensor([2 ** 31 - 1, -2 ** 31, 2 ** 31 - 12345, -2 ** 31 + 777, 0, -1], dtype=torch.int64)
+    pos = ends[torch.randint(0, len(ends), (axes, 1, 400), generator=g)].to(torch.int32).cuda()
+    freq = torch.exp2(torch.rand(axes, 64, generator=g) * 62 - 30).cuda()  # 2^-30 .. 2^32
+    freq *= torch.where(torch.rand(axes, 64, generator=g) < 0.3, -1.0, 1.0).cuda()
+    x = torch.randn(1, 3, 400, 128, generator=g).cuda()
+    th = ON.angles(pos.cpu().numpy(), freq.cpu().numpy())[:, None]
+    for inverse in (False, True):
+        y = hca.hca_rope(x, pos, freq, halves=halves, inverse=inverse)
+        t = -th if inverse else th
+        close("y", y, ON.rotate(f64(x), t, 0, halves), ON.rotate_bound(f64(x), t, 0, halves), F32)
