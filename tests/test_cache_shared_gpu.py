@@ -418,12 +418,14 @@ def test_many_places_that_are_not_taken():
         join = lambda a, b: torch.cat([b, a] if front else [a, b])  # noqa: E731
         big = (q, join(start, none if front else none + start[-1]), join(held, none),
                *((c[0], c[1], join(c[2], torch.full((n, c[2].shape[1]), -1, dtype=torch.int32))) for c in (raw, comp)))
-        for _ in range(2):
+        took = []
+        for _ in range(6):
             hca.hca_profile_enable(True)
             try:
                 got = call(big, i32([0, n + 4]), cols, 16, 1)
-                times.append(hca.hca_profile_read()["hca_cache_prefix"][1])
+                took.append(hca.hca_profile_read()["hca_cache_prefix"][1])
             finally:
                 hca.hca_profile_enable(False)
+        times.append(min(took))
         check_attn(got, *case, 16, 1, scale_of(64), BF16)
-    assert times[3] < 5 * times[1], times
+    assert times[1] < 5 * times[0], times
