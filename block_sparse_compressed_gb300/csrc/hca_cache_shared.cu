@@ -36,7 +36,8 @@
 // bound by shared memory (48 cycles a product where the pipe needs 32), and a half's
 // score -> softmax -> output has three hand-overs.  Beside it the requests' own keys 118 us
 // and the join 25: 657 us in all, 764 without sharing.  4,096 rows over 24,960 entries, 16
-// row tiles in 128 ranges: 58 us, 94 without sharing; 40 are steps, 8 the beginning (table,
+// row tiles in 128 ranges: 58 us, 94 without sharing (calls in a graph, as all figures here
+// and below; between boxes they differ by 2%); 40 are steps, 8 the beginning (table,
 // scales, first keys), 3 the way out, 7 the join.
 //   Slower (each against the kernel of its time): S of 128 keys at once 646 to 686 us, 585
 // in halves; q in tensor memory 768 for 646; pages by bulk copies and converted from
@@ -1189,7 +1190,8 @@ cudaError_t cache_attn_shared(const CacheAttnArgs &args, cudaStream_t st) {
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorNoDevice;
   const int path = shared_path_setting();
-  // fp32 is bound by its multiplications, which are the same
+  // fp32: the kernel has no groups across requests, so each attends the common entries with
+  // its own (64 requests of 4 heads, D = 64, over 512 common tiles 300 us, one of them 37)
   if (a.dtype == HCA_F32 || path == 2 || (path == 0 && !apart_pays(a, sms))) {
     a.share.apart = 0;
     return cache_attn(a, st);

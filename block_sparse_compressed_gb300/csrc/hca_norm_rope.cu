@@ -27,13 +27,13 @@
 //
 // Bounds.  Long sequences are bound by memory: forward of B = 1, H = 64, S = 65,536,
 // D = 128 in bf16 (2.18 GB) 323 us, 99% of the measured copy bandwidth, backward
-// (3.27 GB) 484 us, 99%.  (With a row's loads in its registers: 422 and 671 us; fp32
+// (3.27 GB) 485 us, 99%; H = 16 in fp32 168 and 249 us, 100%.  (With a row's loads in its registers: 422 and 671 us; fp32
 // one by one instead of in pairs, and addresses by multiplication: 354 and 631.)
 // Shorter ones are bound by the blocks' beginnings, 2 us from the first instruction
-// to the first row: 2,571 prompt tokens (86 MB) 16 us; one token of 64 requests 4 us
-// in a graph, of which 2 are the launch.  Few heads are bound by instructions, since a
+// to the first row: 2,571 prompt tokens (86 MB) 16 us; one token of 64 requests 4 us, of
+// which 2 are the launch (calls in a graph, all of these).  Few heads are bound by instructions, since a
 // token's cos and sin and a lane's factors are for few rows: one head and kv of 524,288
-// tokens 223 us (540 MB, 80 us; a thousand instructions of a warp for two rows a lane).
+// tokens 225 us (540 MB, 80 us; a thousand instructions of a warp for two rows a lane).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -191,8 +191,8 @@ constexpr int blocks_per_sm(int cols, int mode) { return (mode == kBwd ? 2 : 4) 
 // slots that only it writes (asynchronously) and reads, so nothing waits but the
 // thread itself.  An SM has 128 KB of slots forwards and 64 KB backwards, where two rows
 // are read for one that is written: B = 1, H = 64, S = 65,536, D = 128 in bf16 backwards
-// 490 us (6 of them a slower sum of dw at its end), 519 with 48 KB, 559 with 128 KB, and
-// 556 with three blocks of 32 KB.
+// 519 us with 48 KB, 559 with 128 KB and 556 with three blocks of 32 KB, where this was
+// 490 (485 since: the sum of dw behind it).
 template <int CH, int MODE, int COLS>
 struct Ring {
   static constexpr int kPieces = CH * (MODE == kBwd ? 2 : 1);  // of a row
